@@ -393,6 +393,186 @@ mm_status mm_debug_fused_layout(const mm_plan* plan, const void* workspace, int3
  */
 mm_status mm_read_kernel_clock(const mm_plan* plan, const void* workspace, uint64_t* host_out, void* stream);
 
+/*
+ * ---------------------------------------------------------------- router
+ * mm_router -- the routes of a layer from its router: scores of every expert,
+ * the K largest per token and their weights, in the form that
+ * mm_dispatch_layout, mega_moe and mm_moe_few take.
+ *     z = x_t . Wr[e]
+ *     MM_ROUTER_SOFTMAX: z += bias[e]; score = softmax(z) over the E experts;
+ *                        experts are ranked by z
+ *     MM_ROUTER_SIGMOID: score = 1 / (1 + e^-z); experts are ranked by
+ *                        score + bias[e], or by z if bias is NULL
+ *     weight = score of the selected experts; with renormalize = 1 divided by
+ *     (their sum + 1e-20); then times route_scale
+ * The K experts of a token come in descending rank, ties to the lower id.
+ * Products and weights are float32; where float32 sums leave the order of
+ * two experts in doubt, it is decided by their sums in 64 bits.  A rank of
+ * -inf (a bias of -inf switches an expert off) is never selected: a slot
+ * with no expert left gets id -1 and weight 0, as does every slot of a token
+ * whose x_active_mask entry is 0.  A NaN ranks below every number and above
+ * -inf; its weight is NaN.  Results do not depend on the other tokens'
+ * values.
+ */
+typedef enum mm_router_scoring { MM_ROUTER_SOFTMAX = 0, MM_ROUTER_SIGMOID = 1 } mm_router_scoring;
+
+typedef struct mm_router_problem {
+  int64_t num_tokens;    /* T in [1, 2^24] */
+  int64_t hidden;        /* H, multiple of 256 up to 16384 */
+  int64_t num_experts;   /* E in [1, 1024] */
+  int64_t num_topk;      /* K in [1, min(E, 64)] */
+  int32_t scoring;       /* mm_router_scoring */
+  int32_t renormalize;   /* 0 or 1 */
+  float route_scale;     /* finite */
+  int32_t reserved0;     /* must be 0 */
+} mm_router_problem;
+
+typedef struct mm_router_plan {
+  mm_router_problem prob;
+  int64_t workspace_bytes;
+  uint64_t checksum;     /* guards against a modified plan */
+  int64_t reserved[4];   /* internal */
+} mm_router_plan;
+
+/* Host only.  Errors as mm_plan_create's (an unknown scoring:
+ * MM_ERR_UNSUPPORTED). */
+mm_status mm_router_plan_create(const mm_router_problem* problem, mm_router_plan* plan);
+
+/*
+ *   x              device bf16 [T][H]
+ *   weight         device bf16 [E][H]
+ *   bias           device f32 [E] or NULL
+ *   x_active_mask  device int8 [T] or NULL
+ *   topk_ids       device int32 [T][K] out
+ *   topk_weights   device f32 [T][K] out
+ *   workspace      device, plan.workspace_bytes
+ */
+mm_status mm_router(const mm_router_plan* plan, const void* x, const void* weight, const float* bias,
+                    const int8_t* x_active_mask, int32_t* topk_ids, float* topk_weights,
+                    void* workspace, uint64_t workspace_bytes, void* stream);
+
+/*
+ * -------------------------------------------------------- few-token layer
+ * mm_moe_few -- the whole layer for at most 64 tokens (a decode step):
+ *     y_t = sum_k G[t,k] * ( SwiGLU( x_t . W1[e] ) . W2[e] ),  e = E[t,k],
+ * plus the shared expert's FFN with weight 1 (num_shared_experts = 1, expert
+ * index E), from the routes of mm_router or of the caller.  Two kernels that
+ * stream the weights of the experts with a route once; no dispatch, no
+ * pool, no grid barrier.
+ * Weight formats: MM_FEW_BF16 and MM_FEW_FP8 (e4m3 with f32 scales per output
+ * channel) are the arrays that mm_prepare_weights writes for A16W16 and
+ * A8W8_FP8, so a layer holds one copy for both paths; MM_FEW_FP8_BLOCK is
+ * e4m3 in the same layout with one f32 scale per 128 x 128 block of the
+ * formula-order matrices.  Activations are not quantised in any format: W is
+ * widened exactly, products are exact, sums are float32.  A = SwiGLU(...) is
+ * rounded to bf16 when y is bf16 (as A16W16 does) and kept to 24 bits when y
+ * is f32.  The routes of a token are summed in order of their expert ids.
+ * Ids outside [0, E) are skipped (negative: masked) and contribute 0; an id
+ * that a token names twice counts once, with the sum of its weights.
+ */
+typedef enum mm_few_format { MM_FEW_BF16 = 0, MM_FEW_FP8 = 1, MM_FEW_FP8_BLOCK = 2 } mm_few_format;
+
+typedef struct mm_few_problem {
+  int64_t num_tokens;          /* T in [1, 64] */
+  int64_t hidden;              /* H, multiple of 256 up to 16384 */
+  int64_t intermediate_hidden; /* I, multiple of 128 up to 16384 */
+  int64_t num_experts;         /* E, E + S in [1, 1024] */
+  int64_t num_topk;            /* K in [1, min(E, 32)] */
+  int32_t weight_format;       /* mm_few_format */
+  int32_t y_dtype;             /* mm_out_dtype */
+  int32_t clamp_activation;    /* as in mm_problem */
+  float activation_clamp;
+  int32_t num_shared_experts;  /* S: 0 or 1 */
+  int32_t reserved0;           /* must be 0 */
+} mm_few_problem;
+
+typedef struct mm_few_plan {
+  mm_few_problem prob;
+  int64_t workspace_bytes;
+  uint64_t checksum;
+  int64_t reserved[4];
+} mm_few_plan;
+
+mm_status mm_few_plan_create(const mm_few_problem* problem, mm_few_plan* plan);
+
+/*
+ *   x              device bf16 [T][H]
+ *   topk_ids       device int32 [T][K]
+ *   topk_weights   device f32 [T][K]
+ *   x_active_mask  device int8 [T] or NULL: an inactive token's row of y is 0
+ *   w1             device [E+S][2I][H], rows interleaved as mm_prepare_weights
+ *                  writes them (groups of 32 gate rows, 32 up rows)
+ *   w1_scale       device f32, formula order (gate rows first): [E+S][2I]
+ *                  (FP8), [E+S][2I/128][H/128] (FP8_BLOCK), NULL (BF16)
+ *   w2             device [E+S][H][I]
+ *   w2_scale       device f32 [E+S][H], [E+S][H/128][I/128], or NULL
+ *   y              device [T][H] out, bf16 or f32
+ *   workspace      device, plan.workspace_bytes
+ */
+mm_status mm_moe_few(const mm_few_plan* plan, const void* x, const int32_t* topk_ids, const float* topk_weights,
+                     const int8_t* x_active_mask, const void* w1, const float* w1_scale, const void* w2,
+                     const float* w2_scale, void* y, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/*
+ * --------------------------------------------------- block-scaled product
+ * mm_block_quantize -- e4m3 codes of bf16 rows with one f32 scale per 128
+ * values: scale = max(max|group| / 448, 1e-8), code = x / scale rounded to
+ * nearest even and saturated, both decided in IEEE float32.  A group with a
+ * NaN has a NaN scale and NaN codes; one with an infinity an infinite scale,
+ * a NaN code for the infinity and 0 for the rest.
+ *   x       device bf16 [rows][cols], cols a multiple of 128
+ *   codes   device e4m3 [rows][cols] out
+ *   scales  device f32 [rows][cols/128] out
+ */
+mm_status mm_block_quantize(int64_t rows, int64_t cols, const void* x, void* codes, float* scales, void* stream);
+
+/*
+ * mm_block_gemm -- y[m][n] = sum over 128-blocks kb of
+ *     a_scale[m][kb] * b_scale[n/128][kb] * sum_{k in kb} a[m][k] * b[n][k],
+ * for one matrix (num_groups = 1, group arrays NULL) or for groups of rows
+ * with a matrix each (experts): group i covers the rows
+ * [group_offsets[i], group_offsets[i] + group_counts[i]), as
+ * mm_dispatch_layout's expert_offsets and expert_counts describe them.  Rows
+ * of y that no group covers are left as they are; the part of a group
+ * outside [0, rows) is ignored; groups must not overlap.  Each block's sum is
+ * an e4m3 MFMA result (float32, about 5e-5 of its RMS), blocks are summed in
+ * float32 and y is rounded once to bf16.
+ * mm_block_linear -- the same from bf16 rows: mm_block_quantize, then the
+ * product, with the same result bit for bit.
+ */
+typedef struct mm_block_problem {
+  int64_t rows;          /* M in [1, 2^24] */
+  int64_t out_features;  /* N, multiple of 16 up to 2^20 */
+  int64_t in_features;   /* K, multiple of 128 up to 2^20 */
+  int64_t num_groups;    /* G in [1, 1024] */
+} mm_block_problem;
+
+typedef struct mm_block_plan {
+  mm_block_problem prob;
+  int64_t workspace_bytes;   /* of mm_block_linear (codes and scales of the rows) */
+  uint64_t checksum;
+  int64_t reserved[4];
+} mm_block_plan;
+
+mm_status mm_block_plan_create(const mm_block_problem* problem, mm_block_plan* plan);
+
+/*
+ *   a              device e4m3 [M][K]
+ *   a_scale        device f32 [M][K/128]
+ *   b              device e4m3 [G][N][K]
+ *   b_scale        device f32 [G][ceil(N/128)][K/128]
+ *   group_offsets, group_counts  device int32 [G] each (group_offsets may be
+ *                  the [G+1] array of mm_dispatch_layout); both NULL if G = 1
+ *                  means all M rows
+ *   y              device bf16 [M][N] out
+ */
+mm_status mm_block_gemm(const mm_block_plan* plan, const void* a, const float* a_scale, const void* b,
+                        const float* b_scale, const int32_t* group_offsets, const int32_t* group_counts, void* y,
+                        void* stream);
+mm_status mm_block_linear(const mm_block_plan* plan, const void* x, const void* b, const float* b_scale,
+                          const int32_t* group_offsets, const int32_t* group_counts, void* y, void* workspace,
+                          uint64_t workspace_bytes, void* stream);
+
 /* Kernel timing (diagnostics).  While enabled, every kernel the library
  * launches is bracketed by two HIP events on its stream; mm_trace_collect
  * waits for them and returns, per kernel id, the number of launches and
@@ -401,7 +581,9 @@ typedef enum mm_kernel_id {
   MM_K_ZERO = 0, MM_K_COUNT = 1, MM_K_SCATTER = 2, MM_K_GATHER = 3,
   MM_K_L1 = 4, MM_K_REQUANT = 5, MM_K_L2 = 6, MM_K_COMBINE = 7, MM_K_PREPARE = 8,
   MM_K_MEGA = 9,                 /* the fused persistent kernel of mega_moe */
-  MM_K_COUNT_IDS = 10
+  MM_K_ROUTER = 10, MM_K_ROUTER_SELECT = 11, MM_K_FEW_L1 = 12, MM_K_FEW_L2 = 13,
+  MM_K_BLOCK_QUANTIZE = 14, MM_K_BLOCK_GEMM = 15,
+  MM_K_COUNT_IDS = 16
 } mm_kernel_id;
 
 mm_status mm_trace_enable(int on);

@@ -18,7 +18,11 @@ from . import _build
 MM_A16W16, MM_A8W8_FP8, MM_A8W8_INT8, MM_MXFP8, MM_MXFP4 = 0, 1, 2, 3, 4
 MM_OUT_BF16, MM_OUT_F32 = 0, 1
 USECASE = {"bf16": MM_A16W16, "fp8": MM_A8W8_FP8, "int8": MM_A8W8_INT8, "mxfp8": MM_MXFP8, "mxfp4": MM_MXFP4}
-KERNEL_IDS = 10
+KERNEL_IDS = 16
+MM_ROUTER_SOFTMAX, MM_ROUTER_SIGMOID = 0, 1
+SCORING = {"softmax": MM_ROUTER_SOFTMAX, "sigmoid": MM_ROUTER_SIGMOID}
+MM_FEW_BF16, MM_FEW_FP8, MM_FEW_FP8_BLOCK = 0, 1, 2
+FEW_FORMAT = {"bf16": MM_FEW_BF16, "fp8": MM_FEW_FP8, "fp8_block": MM_FEW_FP8_BLOCK}
 MM_DEVERR_BAD_EXPERT, MM_DEVERR_BARRIER_TIMEOUT, MM_DEVERR_BAD_OFFSETS = 1, 2, 4
 
 
@@ -59,10 +63,77 @@ class MMPlan(ctypes.Structure):
     ]
 
 
+class MMRouterProblem(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("hidden", ctypes.c_int64),
+        ("num_experts", ctypes.c_int64),
+        ("num_topk", ctypes.c_int64),
+        ("scoring", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("route_scale", ctypes.c_float),
+        ("reserved0", ctypes.c_int32),
+    ]
+
+
+class MMRouterPlan(ctypes.Structure):
+    _fields_ = [
+        ("prob", MMRouterProblem),
+        ("workspace_bytes", ctypes.c_int64),
+        ("checksum", ctypes.c_uint64),
+        ("reserved", ctypes.c_int64 * 4),
+    ]
+
+
+class MMFewProblem(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("hidden", ctypes.c_int64),
+        ("intermediate_hidden", ctypes.c_int64),
+        ("num_experts", ctypes.c_int64),
+        ("num_topk", ctypes.c_int64),
+        ("weight_format", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
+        ("clamp_activation", ctypes.c_int32),
+        ("activation_clamp", ctypes.c_float),
+        ("num_shared_experts", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32),
+    ]
+
+
+class MMFewPlan(ctypes.Structure):
+    _fields_ = [
+        ("prob", MMFewProblem),
+        ("workspace_bytes", ctypes.c_int64),
+        ("checksum", ctypes.c_uint64),
+        ("reserved", ctypes.c_int64 * 4),
+    ]
+
+
+class MMBlockProblem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("out_features", ctypes.c_int64),
+        ("in_features", ctypes.c_int64),
+        ("num_groups", ctypes.c_int64),
+    ]
+
+
+class MMBlockPlan(ctypes.Structure):
+    _fields_ = [
+        ("prob", MMBlockProblem),
+        ("workspace_bytes", ctypes.c_int64),
+        ("checksum", ctypes.c_uint64),
+        ("reserved", ctypes.c_int64 * 4),
+    ]
+
+
 EXPORTS = [
     "mm_plan_create", "mm_prepare_weights", "mm_dispatch_layout", "mm_grouped_l1_swiglu",
     "mm_grouped_l2_combine", "mega_moe", "mega_moe_noalloc", "mm_read_device_error", "mm_debug_raw_accumulators",
     "mm_debug_fused_layout", "mm_read_kernel_clock", "mm_trace_enable", "mm_trace_collect", "mm_kernel_name", "mm_status_string",
+    "mm_router_plan_create", "mm_router", "mm_few_plan_create", "mm_moe_few", "mm_block_quantize",
+    "mm_block_plan_create", "mm_block_gemm", "mm_block_linear",
 ]
 
 _lib = None
@@ -99,6 +170,16 @@ def load() -> ctypes.CDLL:
     lib.mm_debug_raw_accumulators.argtypes = [P, ctypes.c_int, i32p, i32p, vp, vp, i32p, vp, u64, vp]
     lib.mm_debug_fused_layout.argtypes = [P, vp, i32p, i32p, i32p, vp]
     lib.mm_read_kernel_clock.argtypes = [P, vp, ctypes.POINTER(ctypes.c_uint64), vp]
+    RP, FP, BP = ctypes.POINTER(MMRouterPlan), ctypes.POINTER(MMFewPlan), ctypes.POINTER(MMBlockPlan)
+    i64 = ctypes.c_int64
+    lib.mm_router_plan_create.argtypes = [ctypes.POINTER(MMRouterProblem), RP]
+    lib.mm_router.argtypes = [RP, vp, vp, f32p, vp, i32p, f32p, vp, u64, vp]
+    lib.mm_few_plan_create.argtypes = [ctypes.POINTER(MMFewProblem), FP]
+    lib.mm_moe_few.argtypes = [FP, vp, i32p, f32p, vp, vp, f32p, vp, f32p, vp, vp, u64, vp]
+    lib.mm_block_quantize.argtypes = [i64, i64, vp, vp, f32p, vp]
+    lib.mm_block_plan_create.argtypes = [ctypes.POINTER(MMBlockProblem), BP]
+    lib.mm_block_gemm.argtypes = [BP, vp, f32p, vp, f32p, i32p, i32p, vp, vp]
+    lib.mm_block_linear.argtypes = [BP, vp, vp, f32p, i32p, i32p, vp, vp, u64, vp]
     lib.mm_trace_enable.argtypes = [ctypes.c_int]
     lib.mm_trace_collect.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double)]
     lib.mm_kernel_name.argtypes = [ctypes.c_int]
@@ -194,6 +275,62 @@ def mega_moe_noalloc(plan, x, topk_ids, topk_weights, x_active_mask, w1, w1_scal
     _check("mega_moe_noalloc", load().mega_moe_noalloc(
         ctypes.byref(plan), _ptr(x), _ptr(topk_ids), _ptr(topk_weights), _ptr(x_active_mask), _ptr(w1),
         _ptr(w1_scale), _ptr(w2), _ptr(w2_scale), _ptr(y), _ptr(expert_token_nums), _stream(stream)))
+
+
+def mm_router_plan_create(T, H, E, K, scoring="softmax", renormalize=True, route_scale=1.0) -> MMRouterPlan:
+    sc = SCORING[scoring] if isinstance(scoring, str) else scoring
+    prob = MMRouterProblem(T, H, E, K, sc, int(renormalize), route_scale, 0)
+    plan = MMRouterPlan()
+    _check("mm_router_plan_create", load().mm_router_plan_create(ctypes.byref(prob), ctypes.byref(plan)))
+    return plan
+
+
+def mm_router(plan, x, weight, bias, x_active_mask, topk_ids, topk_weights, workspace, stream=None):
+    _check("mm_router", load().mm_router(
+        ctypes.byref(plan), _ptr(x), _ptr(weight), _ptr(bias), _ptr(x_active_mask), _ptr(topk_ids),
+        _ptr(topk_weights), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def mm_few_plan_create(T, H, I, E, K, weight_format="bf16", y_dtype="bf16", activation_clamp=None,
+                       num_shared_experts=0) -> MMFewPlan:
+    fmt = FEW_FORMAT[weight_format] if isinstance(weight_format, str) else weight_format
+    yd = (MM_OUT_F32 if y_dtype in ("f32", "fp32") else MM_OUT_BF16) if isinstance(y_dtype, str) else y_dtype
+    prob = MMFewProblem(T, H, I, E, K, fmt, yd, 0 if activation_clamp is None else 1,
+                        0.0 if activation_clamp is None else activation_clamp, num_shared_experts, 0)
+    plan = MMFewPlan()
+    _check("mm_few_plan_create", load().mm_few_plan_create(ctypes.byref(prob), ctypes.byref(plan)))
+    return plan
+
+
+def mm_moe_few(plan, x, topk_ids, topk_weights, x_active_mask, w1, w1_scale, w2, w2_scale, y, workspace, stream=None):
+    _check("mm_moe_few", load().mm_moe_few(
+        ctypes.byref(plan), _ptr(x), _ptr(topk_ids), _ptr(topk_weights), _ptr(x_active_mask), _ptr(w1),
+        _ptr(w1_scale), _ptr(w2), _ptr(w2_scale), _ptr(y), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def mm_block_quantize(rows, cols, x, codes, scales, stream=None):
+    _check("mm_block_quantize", load().mm_block_quantize(rows, cols, _ptr(x), _ptr(codes), _ptr(scales),
+                                                         _stream(stream)))
+
+
+def mm_block_plan_create(M, N, K, G=1) -> MMBlockPlan:
+    prob = MMBlockProblem(M, N, K, G)
+    plan = MMBlockPlan()
+    _check("mm_block_plan_create", load().mm_block_plan_create(ctypes.byref(prob), ctypes.byref(plan)))
+    return plan
+
+
+def mm_block_gemm(plan, a, a_scale, b, b_scale, group_offsets, group_counts, y, stream=None):
+    _check("mm_block_gemm", load().mm_block_gemm(
+        ctypes.byref(plan), _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(group_offsets), _ptr(group_counts),
+        _ptr(y), _stream(stream)))
+
+
+def mm_block_linear(plan, x, b, b_scale, group_offsets, group_counts, y, workspace, stream=None):
+    _check("mm_block_linear", load().mm_block_linear(
+        ctypes.byref(plan), _ptr(x), _ptr(b), _ptr(b_scale), _ptr(group_offsets), _ptr(group_counts), _ptr(y),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def mm_read_device_error(plan, workspace, stream=None) -> int:

@@ -1,0 +1,544 @@
+// The routed-expert layer for at most 64 tokens: two kernels that stream the
+// live experts' weights once from HBM into MFMA operands.
+//
+//   k_few_l1: A[r] = SwiGLU(x_t . W1[e]) for every route r = (t, k), e = id(r)
+//   k_few_l2: y[t] = sum over t's routes of g_r * (A[r] . W2[e])
+//
+// Weights are the A operand of the 16 x 16 x 32 MFMA (16 weight rows), up to
+// 16 * NT routes of one expert its B operand, so a weight byte is read once
+// whatever the number of tokens.  e4m3 weights are widened exactly to bf16
+// (activations are not quantised); float32 accumulators.  Bound: HBM.
+#include <type_traits>
+
+#include "mm_device.hpp"
+#include "mm_ops_internal.hpp"
+
+namespace mm {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / 64;
+constexpr int kMaxT = 64, kMaxE = 1025, kMaxRoutes = 64 * 33;
+constexpr int kStage = 128;            // K-values per stage of a wave
+
+__device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// 8 e4m3 -> 8 bf16, exact
+__device__ __forceinline__ u32x4 widen8(uint32_t w0, uint32_t w1) {
+#define CVT(x, hi_) __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((x), 1.0f, (hi_)))
+  return u32x4{CVT(w0, false), CVT(w0, true), CVT(w1, false), CVT(w1, true)};
+#undef CVT
+}
+
+// The routes of a batch grouped by expert, in LDS.
+struct Lists {
+  unsigned long long tokens[kMaxE];   // tokens of each expert, one bit each; then the place of its first entry
+  int32_t route[kMaxRoutes];   // list: route t * (K + S) + k, by expert and token
+  float gate[kMaxRoutes];
+  int16_t expert[kMaxE];       // live experts, ascending
+  int16_t start[kMaxE + 1];    // first list entry of each live expert
+  int16_t visit[kMaxE + 1];    // first visit of each live expert: a visit is a group of up to `group` of its routes
+  int16_t token[kMaxRoutes];
+  int16_t first[kMaxE];        // first list entry of expert e
+  int32_t live;
+};
+
+// Built by every workgroup for itself: a few thousand ids at most, which
+// cost less than a kernel of their own.  A route's place among its expert's
+// is the number of earlier tokens in the expert's bit mask, so the order
+// does not depend on how the atomics arrive.  An id that a token names twice
+// is one entry with the sum of the weights.
+__device__ void build_lists(const FewArgs& a, Lists& L, int group) {
+  const int tid = threadIdx.x, Et = a.E + a.S, n = a.T * a.K;
+  for (int e = tid; e < Et; e += kThreads) L.tokens[e] = 0;
+  for (int i = tid; i < n + a.T; i += kThreads) {
+    L.route[i] = 0x7fffffff;
+    L.gate[i] = 0.0f;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const int t = i / a.K, id = a.ids[i];
+    if (id >= 0 && id < a.E && (a.active == nullptr || a.active[t] != 0)) atomicOr(&L.tokens[id], 1ull << t);
+  }
+  if (a.S && tid < a.T && (a.active == nullptr || a.active[tid] != 0)) atomicOr(&L.tokens[a.E], 1ull << tid);
+  __syncthreads();
+  if (tid < 64) {
+    int live = 0, at = 0, vis = 0;
+    for (int e0 = 0; e0 < Et; e0 += 64) {
+      const int e = e0 + tid, c = e < Et ? __popcll(L.tokens[e]) : 0;
+      const uint64_t m = ballot(c > 0);
+      // routes and visits of the experts before this one, in one scan
+      const int mine = c | ((c + group - 1) / group) << 16;
+      int pre = mine;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(pre, o, 64);
+        if (tid >= o) pre += v;
+      }
+      const int all = __shfl(pre, 63, 64);
+      pre -= mine;
+      if (c > 0) {
+        const int p = live + __popcll((unsigned long long)(m & lanemask_lt()));
+        L.expert[p] = (int16_t)e;
+        L.start[p] = (int16_t)(at + (pre & 0xffff));
+        L.visit[p] = (int16_t)(vis + (pre >> 16));
+        L.first[e] = (int16_t)(at + (pre & 0xffff));
+      }
+      live += __popcll((unsigned long long)m);
+      at += all & 0xffff;
+      vis += all >> 16;
+    }
+    if (tid == 0) {
+      L.live = live;
+      L.start[live] = (int16_t)at;
+      L.visit[live] = (int16_t)vis;
+    }
+  }
+  __syncthreads();
+  auto place = [&](int e, int t, int k, float gate) {
+    const int p = L.first[e] + __popcll(L.tokens[e] & ((1ull << t) - 1));
+    atomicMin(&L.route[p], t * (a.K + a.S) + k);
+    atomicAdd(&L.gate[p], gate);
+    L.token[p] = (int16_t)t;
+  };
+  for (int i = tid; i < n; i += kThreads) {
+    const int t = i / a.K, id = a.ids[i];
+    if (id >= 0 && id < a.E && (a.active == nullptr || a.active[t] != 0)) place(id, t, i % a.K, a.weights[i]);
+  }
+  if (a.S && tid < a.T && (a.active == nullptr || a.active[tid] != 0)) place(a.E, tid, a.K, 1.0f);
+  __syncthreads();
+}
+
+// One stage of a wave: WT tiles of 16 weight rows and NT tiles of 16 routes
+// in P parts, 128 K-values.  A lane's 16-byte pieces of a weight row and of
+// a route's row cover the same K-values in the same order.
+template <int F, int WT, int NT, int P>
+struct Stage {
+  static constexpr int WL = F == MM_FEW_BF16 ? 4 : 2;
+  u32x4 w[WT][WL];
+  u32x4 b[P][NT][4];
+  float s[WT];
+};
+
+template <int F> constexpr int weight_bytes() { return F == MM_FEW_BF16 ? 2 : 1; }
+// byte offset of piece j of lane group g inside a stage
+template <int F> __device__ __forceinline__ int w_piece(int g, int j) {
+  return F == MM_FEW_BF16 ? 64 * j + 16 * g : 64 * j + 16 * g;
+}
+// bf16 operand piece j (of MFMA j) of lane group g: the K-values that
+// widened weight piece covers
+template <int F> __device__ __forceinline__ int b_piece(int g, int j) {
+  return F == MM_FEW_BF16 ? 64 * j + 16 * g : 128 * (j / 2) + 32 * g + 16 * (j % 2);
+}
+
+template <int F, int WT, int NT, int P>
+__device__ __forceinline__ void load_weights(Stage<F, WT, NT, P>& st, const uint8_t* const (&wp)[WT], int64_t off, int g) {
+#pragma unroll
+  for (int i = 0; i < WT; ++i)
+#pragma unroll
+    for (int j = 0; j < Stage<F, WT, NT, P>::WL; ++j)
+      st.w[i][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wp[i] + off + w_piece<F>(g, j)));
+}
+
+template <int F, int WT, int NT, int P>
+__device__ __forceinline__ void multiply(const Stage<F, WT, NT, P>& st, f32x4 (&acc)[WT][NT], int nt) {
+#pragma unroll
+  for (int i = 0; i < WT; ++i) {
+    f32x4 sum[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) sum[n] = F == MM_FEW_FP8_BLOCK ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][n];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u32x4 w = F == MM_FEW_BF16 ? st.w[i][F == MM_FEW_BF16 ? j : 0]
+                                       : widen8(st.w[i][F == MM_FEW_BF16 ? 0 : j / 2][2 * (j % 2)], st.w[i][F == MM_FEW_BF16 ? 0 : j / 2][2 * (j % 2) + 1]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (NT == 1 || n < nt) {
+#pragma unroll
+          for (int p = 0; p < P; ++p) sum[n] = mfma16(w, st.b[p][n][j], sum[n]);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[i][n] = F == MM_FEW_FP8_BLOCK ? acc[i][n] + sum[n] * st.s[i] : sum[n];
+  }
+}
+
+template <int WT, int NT>
+__device__ __forceinline__ void clear(f32x4 (&acc)[WT][NT]) {
+#pragma unroll
+  for (int i = 0; i < WT; ++i)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+// bf16 parts of a float whose sum is the float to P * 8 bits
+template <int P>
+__device__ __forceinline__ void split_bf16(float v, uint16_t (&o)[P]) {
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    o[p] = f32_to_bf16_bits(v);
+    const float h = bf16_bits_to_f32(o[p]);
+    v = p + 1 < P && h - h == 0.0f ? v - h : 0.0f;   // inf and NaN sit in the first part
+  }
+}
+
+}  // namespace
+
+// Linear1.  A unit is 16 columns of A of one live expert (16 gate and 16 up
+// rows of W1) for a group of up to 16 * NT of its routes; the 8 waves share
+// the hidden dimension, stage by stage, and their sums meet in LDS.  D
+// stages of a wave are in flight, across units.
+template <int F, int NT, int P, int D>
+__global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
+  __shared__ Lists L;
+  __shared__ f32x4 red[kWaves][2][NT][64];
+  build_lists(a, L, 16 * NT);
+  const int w = uniform(threadIdx.x / 64), l = threadIdx.x % 64, r = l % 16, g = l / 16;
+  constexpr int WB = weight_bytes<F>();
+  const int nst = a.H / kStage, nsw = (nst + kWaves - 1) / kWaves, cols = a.I / 16;
+  const int units = uniform(L.live) * cols;
+  const int64_t R = (int64_t)a.T * (a.K + a.S);
+
+  // the next stage to load: unit u, route group q of its expert, stage j
+  struct Cursor {
+    int u, q, j;
+    int e, c, n0, n;
+    const uint8_t* wp[2];
+    const uint8_t* bp[NT];
+    const float* sp[2];
+  };
+  auto aim = [&](Cursor& cu) {
+    if (cu.u >= units) return;
+    const int le = cu.u / cols;
+    cu.c = cu.u % cols;
+    cu.e = uniform(L.expert[le]);
+    cu.n0 = uniform(L.start[le]) + cu.q * 16 * NT;
+    cu.n = uniform(L.start[le + 1]) - cu.n0;
+    const int row = 64 * (cu.c / 2) + 16 * (cu.c % 2) + r;
+    const uint8_t* base = a.w1 + (int64_t)cu.e * 2 * a.I * a.H * WB;
+    cu.wp[0] = base + (int64_t)row * a.H * WB;
+    cu.wp[1] = base + (int64_t)(row + 32) * a.H * WB;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int i = 16 * n + r;
+      cu.bp[n] = static_cast<const uint8_t*>(a.x) + (int64_t)L.token[cu.n0 + (i < cu.n ? i : 0)] * a.H * 2;
+    }
+    if constexpr (F == MM_FEW_FP8_BLOCK) {
+      const float* s = a.s1 + (int64_t)cu.e * (2 * a.I / 128) * nst;
+      cu.sp[0] = s + (int64_t)(cu.c / 8) * nst;
+      cu.sp[1] = s + (int64_t)(a.I / 128 + cu.c / 8) * nst;
+    }
+  };
+  auto step = [&](Cursor& cu) {
+    if (++cu.j < nsw) return;
+    cu.j = 0;
+    if (cu.n > 16 * NT) {
+      ++cu.q;
+    } else {
+      cu.q = 0;
+      cu.u += gridDim.x;
+    }
+    aim(cu);
+  };
+  auto load = [&](const Cursor& cu, Stage<F, 2, NT, 1>& st) {
+    const int s = cu.j * kWaves + w;
+    if (cu.u >= units || s >= nst) return;
+    load_weights<F, 2, NT, 1>(st, cu.wp, (int64_t)s * (kStage * WB), g);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (NT == 1 || 16 * n < cu.n) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st.b[0][n][j] = *reinterpret_cast<const u32x4*>(cu.bp[n] + (int64_t)s * (kStage * 2) + b_piece<F>(g, j));
+      }
+    if constexpr (F == MM_FEW_FP8_BLOCK) st.s[0] = cu.sp[0][s], st.s[1] = cu.sp[1][s];
+  };
+
+  Cursor ld{}, cu{};
+  ld.u = cu.u = blockIdx.x;
+  aim(ld);
+  aim(cu);
+  Stage<F, 2, NT, 1> st[D];
+  f32x4 acc[2][NT];
+  clear(acc);
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    load(ld, st[d]);
+    if (ld.u < units) step(ld);
+  }
+  while (cu.u < units) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (cu.u < units) {
+        if (cu.j * kWaves + w < nst) multiply<F, 2, NT, 1>(st[d], acc, (cu.n + 15) / 16);
+        load(ld, st[d]);
+        if (ld.u < units) step(ld);
+        if (cu.j + 1 == nsw) {
+          // the unit's sums: 8 waves' parts, SwiGLU, A
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) red[w][i][n][l] = acc[i][n];
+          clear(acc);
+          __syncthreads();
+          const float* rf = reinterpret_cast<const float*>(red);
+          const int n16 = cu.n < 16 * NT ? cu.n : 16 * NT;
+          for (int i = threadIdx.x; i < 16 * n16; i += kThreads) {
+            // column c (of 16) of list entry m: accumulator c % 4 of lane 16 * (c / 4) + m % 16
+            const int c = i % 16, m = i / 16;
+            const int at = ((m / 16) * 64 + 16 * (c / 4) + m % 16) * 4 + c % 4;
+            float hg = 0.0f, hu = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kWaves; ++k) {
+              hg += rf[(k * 2 + 0) * NT * 256 + at];
+              hu += rf[(k * 2 + 1) * NT * 256 + at];
+            }
+            const int col = cu.c * 16 + c;
+            if constexpr (F == MM_FEW_FP8) {
+              hg *= a.s1[(int64_t)cu.e * 2 * a.I + col];
+              hu *= a.s1[(int64_t)cu.e * 2 * a.I + a.I + col];
+            }
+            // a NaN stays one (a clamp by min and max would replace it)
+            hg = hg > a.clamp ? a.clamp : hg < -a.clamp ? -a.clamp : hg;
+            hu = hu > a.clamp ? a.clamp : hu < -a.clamp ? -a.clamp : hu;
+            uint16_t o[P];
+            split_bf16<P>(hg / (1.0f + expf(-hg)) * hu, o);
+            const int64_t route = L.route[cu.n0 + m];
+#pragma unroll
+            for (int p = 0; p < P; ++p) a.a[(p * R + route) * a.I + col] = o[p];
+          }
+          __syncthreads();
+        }
+        step(cu);
+      }
+    }
+  }
+}
+
+// Linear2.  A unit is 16 * WT columns of y over every live expert; its
+// stages (expert, 128 values of I) are cut into 8 runs, one a wave.  A wave
+// adds gate * sum to its own copy of the unit's y in LDS at the end of an
+// expert, and the 8 copies are added in order.
+template <int F, int WT, int NT, int P, int D>
+__global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
+  __shared__ Lists L;
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  f32x4* ys = reinterpret_cast<f32x4*>(dyn);   // [kWaves][T][4 * WT]
+  build_lists(a, L, 16 * NT);
+  const int w = uniform(threadIdx.x / 64), l = threadIdx.x % 64, r = l % 16, g = l / 16;
+  constexpr int WB = weight_bytes<F>();
+  const int nst = a.I / kStage;
+  const int units = a.H / (16 * WT);
+  const int64_t R = (int64_t)a.T * (a.K + a.S);
+  const int live = uniform(L.live), visits = uniform(L.visit[live]);
+  const int total = visits * nst, nsw = total > kWaves ? (total + kWaves - 1) / kWaves : 1;
+  for (int i = threadIdx.x; i < kWaves * a.T * 4 * WT; i += kThreads) ys[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  __syncthreads();
+
+  // the live expert and its visit that hold this wave's first stage
+  int le0 = 0, q0 = 0;
+  {
+    const int v = w * nsw / nst;
+    int hi = live;             // the last expert whose first visit is at most v
+    while (hi - le0 > 1) {
+      const int mid = (le0 + hi) / 2;
+      if (uniform(L.visit[mid]) <= v) le0 = mid;
+      else hi = mid;
+    }
+    if (live > 0) q0 = v - uniform(L.visit[le0]);
+  }
+
+  struct Cursor {
+    int u, j;                  // unit, stage of this wave's run
+    int s, le, q;              // stage inside the visit, live expert, route group
+    int e, n0, n;
+    const uint8_t* wp[WT];
+    const uint8_t* bp[NT];
+    const float* sp[WT];
+  };
+  auto valid = [&](const Cursor& cu) { return w * nsw + cu.j < total; };
+  auto aim = [&](Cursor& cu) {
+    if (cu.u >= units || !valid(cu)) return;
+    cu.e = uniform(L.expert[cu.le]);
+    cu.n0 = uniform(L.start[cu.le]) + cu.q * 16 * NT;
+    cu.n = uniform(L.start[cu.le + 1]) - cu.n0;
+    const uint8_t* base = a.w2 + (int64_t)cu.e * a.H * a.I * WB;
+#pragma unroll
+    for (int i = 0; i < WT; ++i) {
+      cu.wp[i] = base + (int64_t)((cu.u * WT + i) * 16 + r) * a.I * WB;
+      if constexpr (F == MM_FEW_FP8_BLOCK)
+        cu.sp[i] = a.s2 + ((int64_t)cu.e * (a.H / 128) + (cu.u * WT + i) / 8) * nst;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int i = 16 * n + r;
+      cu.bp[n] = reinterpret_cast<const uint8_t*>(a.a) + (int64_t)L.route[cu.n0 + (i < cu.n ? i : 0)] * a.I * 2;
+    }
+  };
+  auto first = [&](Cursor& cu) {
+    cu.j = 0;
+    cu.s = (w * nsw) % nst;
+    cu.le = le0;
+    cu.q = q0;
+    aim(cu);
+  };
+  auto step = [&](Cursor& cu) {
+    if (++cu.j == nsw) {
+      cu.u += gridDim.x;
+      first(cu);
+    } else if (++cu.s == nst) {
+      cu.s = 0;
+      ++cu.q;
+      if (cu.le < live && uniform(L.start[cu.le]) + cu.q * 16 * NT >= uniform(L.start[cu.le + 1])) ++cu.le, cu.q = 0;
+      aim(cu);
+    }
+  };
+  auto load = [&](const Cursor& cu, Stage<F, WT, NT, P>& st) {
+    if (cu.u >= units || !valid(cu)) return;
+    load_weights<F, WT, NT, P>(st, cu.wp, (int64_t)cu.s * (kStage * WB), g);
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (NT == 1 || 16 * n < cu.n) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            st.b[p][n][j] = *reinterpret_cast<const u32x4*>(cu.bp[n] + (int64_t)p * R * a.I * 2 + (int64_t)cu.s * (kStage * 2) + b_piece<F>(g, j));
+        }
+    if constexpr (F == MM_FEW_FP8_BLOCK) {
+#pragma unroll
+      for (int i = 0; i < WT; ++i) st.s[i] = cu.sp[i][cu.s];
+    }
+  };
+
+  Cursor ld{}, cu{};
+  ld.u = cu.u = blockIdx.x;
+  first(ld);
+  first(cu);
+  Stage<F, WT, NT, P> st[D];
+  f32x4 acc[WT][NT];
+  clear(acc);
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    load(ld, st[d]);
+    if (ld.u < units) step(ld);
+  }
+  while (cu.u < units) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (cu.u < units) {
+        if (valid(cu)) multiply<F, WT, NT, P>(st[d], acc, (cu.n + 15) / 16);
+        load(ld, st[d]);
+        if (ld.u < units) step(ld);
+        const bool last = cu.j + 1 == nsw;
+        if (valid(cu) && (last || cu.s + 1 == nst || w * nsw + cu.j + 1 == total)) {
+          // end of this wave's part of a visit: gate * sum into its copy of y
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const int i = 16 * n + r;
+            if (i < cu.n) {
+              const float gate = L.gate[cu.n0 + i];
+              f32x4* y = ys + ((int64_t)w * a.T + L.token[cu.n0 + i]) * (4 * WT) + g;
+#pragma unroll
+              for (int k = 0; k < WT; ++k) {
+                f32x4 v = acc[k][n];
+                if constexpr (F == MM_FEW_FP8)
+                  v *= *reinterpret_cast<const f32x4*>(a.s2 + (int64_t)cu.e * a.H + (cu.u * WT + k) * 16 + 4 * g);
+                y[4 * k] += v * gate;
+              }
+            }
+          }
+          clear(acc);
+        }
+        if (last) {
+          __syncthreads();
+          // thread: 4 columns of a token
+          for (int i = threadIdx.x; i < a.T * 4 * WT; i += kThreads) {
+            f32x4 v = ys[i];
+            ys[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 1; k < kWaves; ++k) {
+              v += ys[(int64_t)k * a.T * 4 * WT + i];
+              ys[(int64_t)k * a.T * 4 * WT + i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+            const int64_t at = (int64_t)(i / (4 * WT)) * a.H + cu.u * 16 * WT + (i % (4 * WT)) * 4;
+            if (a.y_f32) {
+              *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = v;
+            } else {
+              *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            }
+          }
+          __syncthreads();
+        }
+        step(cu);
+      }
+    }
+  }
+}
+
+namespace {
+
+template <int F, int NT, int P, int D>
+hipError_t run_l1(const FewArgs& a, int num_cus, hipStream_t s) {
+  const int64_t routes = (int64_t)a.T * a.K + (a.S ? a.T : 0);
+  const int64_t live = routes < a.E + a.S ? routes : a.E + a.S;
+  const int64_t units = live * (a.I / 16);
+  const int grid = (int)(units < num_cus ? units : num_cus);
+  hipLaunchKernelGGL((k_few_l1<F, NT, P, D>), dim3(grid), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int F, int WT, int NT, int P, int D>
+hipError_t run_l2(const FewArgs& a, int num_cus, hipStream_t s) {
+  const int units = a.H / (16 * WT);
+  const size_t lds = (size_t)kWaves * a.T * 4 * WT * 16;
+  if (lds > 32768) {   // beside the lists, more than 64 KiB
+    const hipError_t err = hipFuncSetAttribute((const void*)k_few_l2<F, WT, NT, P, D>,
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, kWaves * kMaxT * 4 * WT * 16);
+    if (err != hipSuccess) return err;
+  }
+  hipLaunchKernelGGL((k_few_l2<F, WT, NT, P, D>), dim3(units < num_cus ? units : num_cus), dim3(kThreads), lds, s, a);
+  return hipGetLastError();
+}
+
+template <int F, int P>
+hipError_t run_l1_f(const FewArgs& a, int num_cus, hipStream_t s) {
+  if (a.T <= 16) return run_l1<F, 1, P, 3>(a, num_cus, s);
+  return run_l1<F, 2, P, 2>(a, num_cus, s);
+}
+template <int F, int P>
+hipError_t run_l2_f(const FewArgs& a, int num_cus, hipStream_t s) {
+  if (a.T <= 16) return run_l2<F, 1, 1, P, P == 1 ? 4 : 2>(a, num_cus, s);
+  return run_l2<F, 2, P == 1 ? 2 : 1, P, 2>(a, num_cus, s);
+}
+template <int P>
+hipError_t run_l1_p(const FewArgs& a, int num_cus, hipStream_t s) {
+  switch (a.format) {
+    case MM_FEW_BF16: return run_l1_f<MM_FEW_BF16, P>(a, num_cus, s);
+    case MM_FEW_FP8: return run_l1_f<MM_FEW_FP8, P>(a, num_cus, s);
+    default: return run_l1_f<MM_FEW_FP8_BLOCK, P>(a, num_cus, s);
+  }
+}
+template <int P>
+hipError_t run_l2_p(const FewArgs& a, int num_cus, hipStream_t s) {
+  switch (a.format) {
+    case MM_FEW_BF16: return run_l2_f<MM_FEW_BF16, P>(a, num_cus, s);
+    case MM_FEW_FP8: return run_l2_f<MM_FEW_FP8, P>(a, num_cus, s);
+    default: return run_l2_f<MM_FEW_FP8_BLOCK, P>(a, num_cus, s);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_few_l1(const FewArgs& a, int num_cus, hipStream_t s) {
+  return a.y_f32 ? run_l1_p<3>(a, num_cus, s) : run_l1_p<1>(a, num_cus, s);
+}
+hipError_t launch_few_l2(const FewArgs& a, int num_cus, hipStream_t s) {
+  return a.y_f32 ? run_l2_p<3>(a, num_cus, s) : run_l2_p<1>(a, num_cus, s);
+}
+
+}  // namespace mm

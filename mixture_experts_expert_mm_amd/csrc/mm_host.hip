@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "mm_internal.hpp"
+#include "mm_ops_internal.hpp"
 
 using namespace mm;
 
@@ -29,12 +30,13 @@ int64_t weight_bytes(int usecase, int64_t n) { return usecase == MM_MXFP4 ? n / 
 int64_t all_experts(const mm_problem& p) { return p.num_experts + p.num_shared_experts; }
 int64_t slots_per_token(const mm_problem& p) { return p.num_topk + p.num_shared_experts; }
 
-uint64_t plan_checksum(const mm_plan* p) {
+template <typename Plan>
+uint64_t plan_checksum(const Plan* p) {
   // FNV-1a over every byte of the plan except the checksum itself
   const uint8_t* b = reinterpret_cast<const uint8_t*>(p);
-  const size_t skip0 = offsetof(mm_plan, checksum), skip1 = skip0 + sizeof(p->checksum);
+  const size_t skip0 = offsetof(Plan, checksum), skip1 = skip0 + sizeof(p->checksum);
   uint64_t h = 1469598103934665603ull;
-  for (size_t i = 0; i < sizeof(mm_plan); ++i) {
+  for (size_t i = 0; i < sizeof(Plan); ++i) {
     if (i >= skip0 && i < skip1) continue;
     h ^= b[i];
     h *= 1099511628211ull;
@@ -167,7 +169,8 @@ mm_status run(int id, hipStream_t s, F&& f) {
     if (st__ != MM_OK) return st__; \
   } while (0)
 
-mm_status check_plan(const mm_plan* pl) {
+template <typename Plan>
+mm_status check_plan(const Plan* pl) {
   if (!pl) return MM_ERR_INVALID_ARG;
   if (pl->checksum != plan_checksum(pl)) return MM_ERR_INVALID_ARG;
   return MM_OK;
@@ -764,6 +767,191 @@ mm_status mm_debug_fused_layout(const mm_plan* plan, const void* workspace, int3
   return MM_OK;
 }
 
+// -------------------------------------------------------------- router
+mm_status mm_router_plan_create(const mm_router_problem* problem, mm_router_plan* plan) {
+  if (!problem || !plan) return MM_ERR_INVALID_ARG;
+  const mm_router_problem p = *problem;
+  if (p.scoring != MM_ROUTER_SOFTMAX && p.scoring != MM_ROUTER_SIGMOID) return MM_ERR_UNSUPPORTED;
+  if (p.num_tokens < 1 || p.num_tokens > (1 << 24)) return MM_ERR_INVALID_ARG;
+  if (p.hidden < 256 || p.hidden > 16384 || p.hidden % 256) return MM_ERR_INVALID_ARG;
+  if (p.num_experts < 1 || p.num_experts > 1024) return MM_ERR_INVALID_ARG;
+  if (p.num_topk < 1 || p.num_topk > 64 || p.num_topk > p.num_experts) return MM_ERR_INVALID_ARG;
+  if ((p.renormalize != 0 && p.renormalize != 1) || p.reserved0 != 0) return MM_ERR_INVALID_ARG;
+  if (!std::isfinite(p.route_scale)) return MM_ERR_INVALID_ARG;
+  mm_router_plan pl;
+  std::memset(&pl, 0, sizeof(pl));
+  pl.prob = p;
+  const RouterShape sh = router_shape(p.num_tokens, (int)p.hidden, (int)p.num_experts);
+  pl.reserved[0] = sh.ks;
+  pl.reserved[1] = sh.ep;
+  pl.workspace_bytes = align_up((int64_t)sh.ks * p.num_tokens * sh.ep * 4, kAlign) +
+                       align_up((int64_t)sh.ks * p.num_tokens * 4, kAlign) + align_up((int64_t)sh.ks * sh.ep * 4, kAlign);
+  pl.checksum = plan_checksum(&pl);
+  *plan = pl;
+  return MM_OK;
+}
+
+mm_status mm_router(const mm_router_plan* plan, const void* x, const void* weight, const float* bias,
+                    const int8_t* x_active_mask, int32_t* topk_ids, float* topk_weights, void* workspace,
+                    uint64_t workspace_bytes, void* stream) {
+  MM_TRY(check_plan(plan));
+  if (!ok16(x) || !ok16(weight) || !ok4(topk_ids) || !ok4(topk_weights) || !ok16(workspace) || !aligned(bias, 4))
+    return MM_ERR_INVALID_ARG;
+  if ((int64_t)workspace_bytes < plan->workspace_bytes) return MM_ERR_WORKSPACE;
+  const mm_router_problem& p = plan->prob;
+  RouterArgs a{};
+  a.x = x;
+  a.w = weight;
+  a.bias = bias;
+  a.active = x_active_mask;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.T = p.num_tokens;
+  a.H = (int)p.hidden;
+  a.E = (int)p.num_experts;
+  a.K = (int)p.num_topk;
+  a.KS = (int)plan->reserved[0];
+  a.Ep = (int)plan->reserved[1];
+  a.scoring = p.scoring;
+  a.renormalize = p.renormalize;
+  a.scale = p.route_scale;
+  const int64_t xnorm = align_up((int64_t)a.KS * a.T * a.Ep * 4, kAlign);
+  a.part = at<float>(workspace, 0);
+  a.xnorm = at<float>(workspace, xnorm);
+  a.wnorm = at<float>(workspace, xnorm + align_up((int64_t)a.KS * a.T * 4, kAlign));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  MM_TRY(run(MM_K_ROUTER, s, [&] { return launch_router_scores(a, s); }));
+  return run(MM_K_ROUTER_SELECT, s, [&] { return launch_router_select(a, s); });
+}
+
+// ------------------------------------------------------ few-token layer
+mm_status mm_few_plan_create(const mm_few_problem* problem, mm_few_plan* plan) {
+  if (!problem || !plan) return MM_ERR_INVALID_ARG;
+  const mm_few_problem p = *problem;
+  if (p.weight_format < MM_FEW_BF16 || p.weight_format > MM_FEW_FP8_BLOCK) return MM_ERR_UNSUPPORTED;
+  if (p.y_dtype != MM_OUT_BF16 && p.y_dtype != MM_OUT_F32) return MM_ERR_UNSUPPORTED;
+  if (p.clamp_activation != 0 && p.clamp_activation != 1) return MM_ERR_INVALID_ARG;
+  if (p.clamp_activation && !(p.activation_clamp >= 0.0f)) return MM_ERR_INVALID_ARG;
+  if (p.num_tokens < 1 || p.num_tokens > 64) return MM_ERR_INVALID_ARG;
+  if (p.hidden < 256 || p.hidden > 16384 || p.hidden % 256) return MM_ERR_INVALID_ARG;
+  if (p.intermediate_hidden < 128 || p.intermediate_hidden > 16384 || p.intermediate_hidden % 128)
+    return MM_ERR_INVALID_ARG;
+  if (p.num_shared_experts < 0 || p.num_shared_experts > 1 || p.reserved0 != 0) return MM_ERR_INVALID_ARG;
+  if (p.num_experts < 1 || p.num_experts + p.num_shared_experts > 1024) return MM_ERR_INVALID_ARG;
+  if (p.num_topk < 1 || p.num_topk > 32 || p.num_topk > p.num_experts) return MM_ERR_INVALID_ARG;
+  mm_few_plan pl;
+  std::memset(&pl, 0, sizeof(pl));
+  pl.prob = p;
+  const int64_t planes = p.y_dtype == MM_OUT_F32 ? 3 : 1;
+  pl.workspace_bytes =
+      align_up(planes * p.num_tokens * (p.num_topk + p.num_shared_experts) * p.intermediate_hidden * 2, kAlign);
+  pl.checksum = plan_checksum(&pl);
+  *plan = pl;
+  return MM_OK;
+}
+
+mm_status mm_moe_few(const mm_few_plan* plan, const void* x, const int32_t* topk_ids, const float* topk_weights,
+                     const int8_t* x_active_mask, const void* w1, const float* w1_scale, const void* w2,
+                     const float* w2_scale, void* y, void* workspace, uint64_t workspace_bytes, void* stream) {
+  MM_TRY(check_plan(plan));
+  const mm_few_problem& p = plan->prob;
+  if (!ok16(x) || !ok4(topk_ids) || !ok4(topk_weights) || !ok16(w1) || !ok16(w2) || !ok16(y) || !ok16(workspace))
+    return MM_ERR_INVALID_ARG;
+  if (p.weight_format != MM_FEW_BF16 && (!ok16(w1_scale) || !ok16(w2_scale))) return MM_ERR_INVALID_ARG;
+  if ((int64_t)workspace_bytes < plan->workspace_bytes) return MM_ERR_WORKSPACE;
+  FewArgs a{};
+  a.x = x;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.active = x_active_mask;
+  a.w1 = static_cast<const uint8_t*>(w1);
+  a.s1 = w1_scale;
+  a.w2 = static_cast<const uint8_t*>(w2);
+  a.s2 = w2_scale;
+  a.a = at<uint16_t>(workspace, 0);
+  a.y = y;
+  a.T = (int)p.num_tokens;
+  a.H = (int)p.hidden;
+  a.I = (int)p.intermediate_hidden;
+  a.E = (int)p.num_experts;
+  a.K = (int)p.num_topk;
+  a.S = p.num_shared_experts;
+  a.format = p.weight_format;
+  a.y_f32 = p.y_dtype == MM_OUT_F32;
+  a.clamp = p.clamp_activation ? p.activation_clamp : INFINITY;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  MM_TRY(run(MM_K_FEW_L1, s, [&] { return launch_few_l1(a, num_cus(), s); }));
+  return run(MM_K_FEW_L2, s, [&] { return launch_few_l2(a, num_cus(), s); });
+}
+
+// -------------------------------------------------- block-scaled product
+mm_status mm_block_quantize(int64_t rows, int64_t cols, const void* x, void* codes, float* scales, void* stream) {
+  if (rows < 1 || rows > (1 << 24) || cols < 128 || cols > (1 << 20) || cols % 128) return MM_ERR_INVALID_ARG;
+  if (!ok16(x) || !ok16(codes) || !ok4(scales)) return MM_ERR_INVALID_ARG;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return run(MM_K_BLOCK_QUANTIZE, s, [&] {
+    return launch_block_quantize(x, rows, (int)cols, static_cast<uint8_t*>(codes), scales, s);
+  });
+}
+
+mm_status mm_block_plan_create(const mm_block_problem* problem, mm_block_plan* plan) {
+  if (!problem || !plan) return MM_ERR_INVALID_ARG;
+  const mm_block_problem p = *problem;
+  if (p.rows < 1 || p.rows > (1 << 24)) return MM_ERR_INVALID_ARG;
+  if (p.out_features < 16 || p.out_features > (1 << 20) || p.out_features % 16) return MM_ERR_INVALID_ARG;
+  if (p.in_features < 128 || p.in_features > (1 << 20) || p.in_features % 128) return MM_ERR_INVALID_ARG;
+  if (p.num_groups < 1 || p.num_groups > 1024) return MM_ERR_INVALID_ARG;
+  mm_block_plan pl;
+  std::memset(&pl, 0, sizeof(pl));
+  pl.prob = p;
+  pl.workspace_bytes = align_up(p.rows * p.in_features, kAlign) + align_up(p.rows * (p.in_features / 128) * 4, kAlign);
+  pl.checksum = plan_checksum(&pl);
+  *plan = pl;
+  return MM_OK;
+}
+
+mm_status mm_block_gemm(const mm_block_plan* plan, const void* a, const float* a_scale, const void* b,
+                        const float* b_scale, const int32_t* group_offsets, const int32_t* group_counts, void* y,
+                        void* stream) {
+  MM_TRY(check_plan(plan));
+  const mm_block_problem& p = plan->prob;
+  if (!ok16(a) || !ok4(a_scale) || !ok16(b) || !ok4(b_scale) || !ok16(y)) return MM_ERR_INVALID_ARG;
+  // both group arrays or, for one group, neither
+  if (!aligned(group_offsets, 4) || !aligned(group_counts, 4) || !group_offsets != !group_counts ||
+      (!group_offsets && p.num_groups != 1))
+    return MM_ERR_INVALID_ARG;
+  BlockArgs g{};
+  g.a = static_cast<const uint8_t*>(a);
+  g.as = a_scale;
+  g.b = static_cast<const uint8_t*>(b);
+  g.bs = b_scale;
+  g.offsets = group_offsets;
+  g.counts = group_counts;
+  g.y = y;
+  g.M = p.rows;
+  g.N = (int)p.out_features;
+  g.K = (int)p.in_features;
+  g.G = (int)p.num_groups;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return run(MM_K_BLOCK_GEMM, s, [&] { return launch_block_gemm(g, num_cus(), s); });
+}
+
+mm_status mm_block_linear(const mm_block_plan* plan, const void* x, const void* b, const float* b_scale,
+                          const int32_t* group_offsets, const int32_t* group_counts, void* y, void* workspace,
+                          uint64_t workspace_bytes, void* stream) {
+  MM_TRY(check_plan(plan));
+  const mm_block_problem& p = plan->prob;
+  if (!ok16(x) || !ok16(b) || !ok4(b_scale) || !ok16(y) || !ok16(workspace)) return MM_ERR_INVALID_ARG;
+  if (!aligned(group_offsets, 4) || !aligned(group_counts, 4) || !group_offsets != !group_counts ||
+      (!group_offsets && p.num_groups != 1))
+    return MM_ERR_INVALID_ARG;
+  if ((int64_t)workspace_bytes < plan->workspace_bytes) return MM_ERR_WORKSPACE;
+  uint8_t* codes = at<uint8_t>(workspace, 0);
+  float* scales = at<float>(workspace, align_up(p.rows * p.in_features, kAlign));
+  MM_TRY(mm_block_quantize(p.rows, p.in_features, x, codes, scales, stream));
+  return mm_block_gemm(plan, codes, scales, b, b_scale, group_offsets, group_counts, y, stream);
+}
+
 mm_status mm_trace_enable(int on) {
   std::lock_guard<std::mutex> g(g_trace_mu);
   g_trace_on = on != 0;
@@ -801,7 +989,9 @@ mm_status mm_trace_collect(int32_t* launches, double* total_ms) {
 
 const char* mm_kernel_name(int id) {
   static const char* names[] = {"zero",    "count",   "scatter", "gather", "l1_swiglu",
-                                "requant", "l2_gate", "combine", "prepare", "mega"};
+                                "requant", "l2_gate", "combine", "prepare", "mega",
+                                "router", "router_select", "few_l1", "few_l2",
+                                "block_quantize", "block_gemm"};
   if (id < 0 || id >= MM_K_COUNT_IDS) return "unknown";
   return names[id];
 }

@@ -1,13 +1,18 @@
 """Device-memory plumbing around the C ABI (torch allocates, the library computes).
 
 ``ExpertLayer`` holds one plan, the prepared expert weights and a
-workspace, and calls the C-ABI entry points through ``binding``.  Nothing
+workspace, and calls the C-ABI entry points through ``binding``.  The
+functions ``route``, ``moe_few``, ``block_quantize``, ``block_matmul`` and
+``block_linear`` hold nothing: each checks its tensors, allocates the
+outputs and a workspace on the calling stream and makes one call.  Nothing
 here computes any part of the expert path.
 """
 
 from __future__ import annotations
 
+import contextlib
 import dataclasses
+import functools
 
 import torch
 
@@ -148,3 +153,208 @@ class ExpertLayer:
         self.linear1(im, stream)
         self.linear2_combine(im, topk_weights, y, stream)
         return y, im
+
+    def forward_few(self, x, topk_ids, topk_weights, y=None, stream=None, active=None):
+        """mm_moe_few on this layer's weights (bf16 or fp8): y [T,H] of at most 64 tokens, however many the
+        layer's plan was made for.  Activations are not quantised."""
+        if self.usecase not in ("bf16", "fp8"):
+            raise ValueError(f"forward_few takes bf16 or fp8 weights, not {self.usecase}")
+        clamp = self.plan.prob.activation_clamp if self.plan.prob.clamp_activation else None
+        return moe_few(x, self.w1, self.w2, self.s1, self.s2, topk_ids=topk_ids, topk_weights=topk_weights,
+                       num_shared_experts=self.S, activation_clamp=clamp, y_dtype=self.y_dtype, active=active, y=y,
+                       stream=stream)[0]
+
+
+# ------------------------------------------------- operators without a layer
+
+_router_plan = functools.lru_cache(maxsize=256)(B.mm_router_plan_create)
+_few_plan = functools.lru_cache(maxsize=256)(B.mm_few_plan_create)
+_block_plan = functools.lru_cache(maxsize=256)(B.mm_block_plan_create)
+
+FEW_MAX_TOKENS = 64
+_F32 = ("f32", "fp32")
+
+
+def _need(name, t, dtype, shape, device):
+    """The one check of a tensor argument: a message that says what it has to be."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor {list(shape)} on {device} is needed, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: requires a gradient, which this operator does not compute (call it under no_grad)")
+
+
+def _rows(name, x):
+    """(rows, columns, device) of a bf16 or e4m3 matrix on a GPU."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"{name}: a matrix is needed")
+    if x.device.type != "cuda":
+        raise ValueError(f"{name}: a tensor on a GPU is needed, got one on {x.device}")
+    return x.shape[0], x.shape[1], x.device
+
+
+def _stream_of(device, stream):
+    """Context in which outputs are allocated and kernels launched: the device of the inputs and, if one is given,
+    the stream, so that the allocator knows who uses the buffers."""
+    if stream is not None:
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+    if device.index is not None and device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _workspace(n, device):
+    # a fresh buffer for every call: two streams, or two captured graphs, never share one
+    return torch.empty(max(int(n), 16), dtype=torch.uint8, device=device)
+
+
+def route(x, weight, bias=None, *, topk, scoring="softmax", renormalize=True, scale=1.0, active=None, stream=None):
+    """mm_router: (topk_ids int32 [T,K], topk_weights float32 [T,K]) of the tokens x (bf16 [T,H]).
+
+    weight: bf16 [E,H]; bias: float32 [E] or None (softmax: added to the scores; sigmoid: to their ranking);
+    active: int8 [T] or None.  Ids are in descending rank, -1 where no expert is left or the token is inactive."""
+    T, H, dev = _rows("x", x)
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight: a matrix [experts, hidden] is needed")
+    E = weight.shape[0]
+    _need("x", x, torch.bfloat16, (T, H), dev)
+    _need("weight", weight, torch.bfloat16, (E, H), dev)
+    if bias is not None:
+        _need("bias", bias, torch.float32, (E,), dev)
+    if active is not None:
+        _need("active", active, torch.int8, (T,), dev)
+    if scoring not in B.SCORING:
+        raise ValueError(f"scoring: one of {sorted(B.SCORING)}, got {scoring!r}")
+    plan = _router_plan(max(T, 1), H, E, int(topk), scoring, bool(renormalize), float(scale))
+    with _stream_of(dev, stream):
+        ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
+        wts = torch.empty((T, topk), dtype=torch.float32, device=dev)
+        if T:
+            B.mm_router(plan, x, weight, bias, active, ids, wts, _workspace(plan.workspace_bytes, dev))
+    return ids, wts
+
+
+def moe_few(x, w1, w2, s1=None, s2=None, *, topk_ids=None, topk_weights=None, router_weight=None, router_bias=None,
+            topk=None, scoring="softmax", renormalize=True, route_scale=1.0, num_shared_experts=0,
+            activation_clamp=None, y_dtype="bf16", active=None, y=None, stream=None):
+    """The whole layer for at most 64 tokens: (y, topk_ids, topk_weights).
+
+    x: bf16 [T,H].  w1 [E+S,2I,H] and w2 [E+S,H,I] are prepared weights (``ExpertLayer.w1``, ``.w2``), bf16, or
+    e4m3 with float32 scales in formula order: per output channel (s1 [E+S,2I], s2 [E+S,H]) or per block of 128 x 128
+    (s1 [E+S,2I/128,H/128], s2 [E+S,H/128,I/128]).  Routes: topk_ids and topk_weights, or router_weight (with
+    router_bias, topk, scoring, renormalize and route_scale as in ``route``).  A shared expert is the last of w1, w2."""
+    T, H, dev = _rows("x", x)
+    if T > FEW_MAX_TOKENS:
+        raise ValueError(f"x: at most {FEW_MAX_TOKENS} tokens, got {T} (ExpertLayer.forward takes more)")
+    S = int(num_shared_experts)
+    if not isinstance(w1, torch.Tensor) or w1.dim() != 3 or w1.shape[1] % 2:
+        raise ValueError("w1: prepared weights [experts, 2 * intermediate, hidden] are needed")
+    Et, I = w1.shape[0], w1.shape[1] // 2
+    E = Et - S
+    if w1.dtype == torch.bfloat16:
+        fmt = "bf16"
+    elif w1.dtype == torch.float8_e4m3fn:
+        fmt = "fp8_block" if isinstance(s1, torch.Tensor) and s1.dim() == 3 else "fp8"
+    else:
+        raise ValueError(f"w1: bf16 or float8_e4m3fn weights are needed, got {w1.dtype}")
+    _need("x", x, torch.bfloat16, (T, H), dev)
+    _need("w1", w1, w1.dtype, (Et, 2 * I, H), dev)
+    _need("w2", w2, w1.dtype, (Et, H, I), dev)
+    if fmt == "bf16":
+        if s1 is not None or s2 is not None:
+            raise ValueError("s1, s2: bf16 weights have no scales")
+    else:
+        _need("s1", s1, torch.float32, (Et, 2 * I) if fmt == "fp8" else (Et, 2 * I // 128, H // 128), dev)
+        _need("s2", s2, torch.float32, (Et, H) if fmt == "fp8" else (Et, H // 128, I // 128), dev)
+    if active is not None:
+        _need("active", active, torch.int8, (T,), dev)
+    routed = router_weight is not None
+    if routed == (topk_ids is not None) or (topk_ids is None) != (topk_weights is None):
+        raise ValueError("routes: either topk_ids and topk_weights, or router_weight")
+    if routed:
+        if topk is None:
+            raise ValueError("topk: needed with router_weight")
+        if not isinstance(router_weight, torch.Tensor) or tuple(router_weight.shape) != (E, H):
+            raise ValueError(f"router_weight: [{E}, {H}] is needed")
+        K = int(topk)
+    else:
+        K = int(topk_ids.shape[1]) if topk_ids.dim() == 2 else 0
+        _need("topk_ids", topk_ids, torch.int32, (T, K), dev)
+        _need("topk_weights", topk_weights, torch.float32, (T, K), dev)
+    plan = _few_plan(max(T, 1), H, I, E, K, fmt, y_dtype, activation_clamp, S)
+    ydt = torch.float32 if y_dtype in _F32 else torch.bfloat16
+    if y is not None:
+        _need("y", y, ydt, (T, H), dev)
+    with _stream_of(dev, stream):
+        if y is None:
+            y = torch.empty((T, H), dtype=ydt, device=dev)
+        if routed:
+            topk_ids, topk_weights = route(x, router_weight, router_bias, topk=K, scoring=scoring,
+                                           renormalize=renormalize, scale=route_scale, active=active)
+        if T:
+            B.mm_moe_few(plan, x, topk_ids, topk_weights, active, w1, s1, w2, s2, y,
+                         _workspace(plan.workspace_bytes, dev))
+    return y, topk_ids, topk_weights
+
+
+def block_quantize(x, stream=None):
+    """mm_block_quantize: (codes float8_e4m3fn [M,K], scales float32 [M,K/128]) of bf16 rows."""
+    M, K, dev = _rows("x", x)
+    _need("x", x, torch.bfloat16, (M, K), dev)
+    if K % 128 or K == 0:
+        raise ValueError(f"x: the columns have to be a multiple of 128, got {K}")
+    with _stream_of(dev, stream):
+        q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+        s = torch.empty((M, K // 128), dtype=torch.float32, device=dev)
+        if M:
+            B.mm_block_quantize(M, K, x, q, s)
+    return q, s
+
+
+def _block_args(M, K, dev, w, ws, offsets, counts, y):
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
+        raise ValueError("w: [out, in] or [groups, out, in] is needed")
+    G, N = (1, w.shape[0]) if w.dim() == 2 else (w.shape[0], w.shape[1])
+    lead = () if w.dim() == 2 else (G,)
+    _need("w", w, torch.float8_e4m3fn, lead + (N, K), dev)
+    _need("ws", ws, torch.float32, lead + (-(-N // 128), K // 128), dev)
+    if (offsets is None) != (counts is None) or (offsets is None and G > 1):
+        raise ValueError("offsets, counts: both are needed, or neither with one matrix")
+    if offsets is not None:
+        n = offsets.shape[0] if isinstance(offsets, torch.Tensor) and offsets.dim() == 1 else -1
+        _need("offsets", offsets, torch.int32, (n if n == G + 1 else G,), dev)
+        _need("counts", counts, torch.int32, (G,), dev)
+    if y is not None:
+        _need("y", y, torch.bfloat16, (M, N), dev)
+    return N, _block_plan(max(M, 1), N, K, G)
+
+
+def block_matmul(q, s, w, ws, offsets=None, counts=None, y=None, stream=None):
+    """mm_block_gemm: y bf16 [M,N] of e4m3 rows (q [M,K], s [M,K/128]) and weights (w [N,K], ws [ceil(N/128),K/128]),
+    or, with w [G,N,K] and ws [G,...], of groups of rows: group g covers rows offsets[g] .. offsets[g] + counts[g]
+    (int32; offsets may have G + 1 entries).  Rows that no group covers are left as they are (in a new y: unset)."""
+    M, K, dev = _rows("q", q)
+    _need("q", q, torch.float8_e4m3fn, (M, K), dev)
+    _need("s", s, torch.float32, (M, K // 128), dev)
+    N, plan = _block_args(M, K, dev, w, ws, offsets, counts, y)
+    with _stream_of(dev, stream):
+        if y is None:
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        if M:
+            B.mm_block_gemm(plan, q, s, w, ws, offsets, counts, y)
+    return y
+
+
+def block_linear(x, w, ws, offsets=None, counts=None, y=None, stream=None):
+    """mm_block_linear: block_matmul of x's (bf16 [M,K]) codes and scales, in one call."""
+    M, K, dev = _rows("x", x)
+    _need("x", x, torch.bfloat16, (M, K), dev)
+    N, plan = _block_args(M, K, dev, w, ws, offsets, counts, y)
+    with _stream_of(dev, stream):
+        if y is None:
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        if M:
+            B.mm_block_linear(plan, x, w, ws, offsets, counts, y, _workspace(plan.workspace_bytes, dev))
+    return y

@@ -1,0 +1,515 @@
+"""Router, few-token layer and block-scaled product on the GPU against plain
+64-bit implementations, at the sizes and masks where they can go wrong.
+Tolerances are the error bounds that tests/ops_reference.py derives."""
+
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import ops_reference as ref
+from gpu_helpers import log
+from mixture_experts_expert_mm_amd import binding as B
+from mixture_experts_expert_mm_amd import moe
+from mixture_experts_expert_mm_amd import workloads as wl
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, F64, E4M3 = torch.bfloat16, torch.float32, torch.float64, torch.float8_e4m3fn
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def within(y, want, err, what=""):
+    y = y.detach().cpu().to(F64)
+    assert y.shape == want.shape
+    over = (y - want).abs() - err
+    assert bool((over <= 0).all()), (what, float(over.max()), float((y - want).abs().max()), float(want.abs().max()))
+
+
+# ------------------------------------------------------------------ router
+
+def router_case(T, H, E, K, scoring, bias, seed, **kw):
+    g = gen(seed)
+    x = torch.randn(T, H, generator=g).to(BF16)
+    w = (torch.randn(E, H, generator=g) * H ** -0.5).to(BF16)
+    b = torch.randn(E, generator=g) * (0.5 if scoring == "softmax" else 0.1) if bias else None
+    return x, w, b
+
+
+def check_router(x, w, b, K, scoring, renormalize=True, scale=1.0, active=None):
+    ids, wts = moe.route(x.cuda(), w.cuda(), None if b is None else b.cuda(), topk=K, scoring=scoring,
+                         renormalize=renormalize, scale=scale, active=None if active is None else active.cuda())
+    want, v, err = ref.route(x, w, b, K, scoring, renormalize, scale, active)
+    assert torch.equal(ids.cpu(), want), (ids.cpu() != want).nonzero()[:4]
+    within(wts, v, err, "weights")
+    return ids, wts
+
+
+@pytest.mark.parametrize("T,H,E,K", [(1, 256, 1, 1), (1, 7168, 32, 8), (3, 512, 5, 5), (17, 768, 33, 4), (64, 1024, 64, 64),
+                                     (65, 512, 65, 3), (130, 256, 130, 8), (200, 1280, 256, 8), (70, 512, 300, 10),
+                                     (5, 512, 1024, 16), (129, 256, 1000, 33)])
+@pytest.mark.parametrize("scoring,bias", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+def test_router(T, H, E, K, scoring, bias):
+    log(f"[router] T={T} H={H} E={E} K={K} {scoring} bias={bias}")
+    x, w, b = router_case(T, H, E, K, scoring, bias, 7 * T + E)
+    check_router(x, w, b, K, scoring, renormalize=E % 2 == 0, scale=2.5 if bias else 1.0)
+
+
+def test_router_inactive_and_switched_off():
+    x, w, b = router_case(100, 512, 12, 4, "softmax", True, 3)
+    active = (torch.rand(100, generator=gen(4)) > 0.3).to(torch.int8)
+    b[[0, 5]] = -math.inf
+    check_router(x, w, b, 4, "softmax", active=active)
+    b[2:] = -math.inf                      # one expert left: three slots stay empty
+    for scoring in ("softmax", "sigmoid"):
+        ids, wts = check_router(x, w, b, 4, scoring, active=active)
+        on = active.cuda() != 0
+        assert bool((ids[on][:, 0] == 1).all()) and bool((ids[:, 1:] == -1).all()) and bool((wts[:, 1:] == 0).all())
+    b[:] = -math.inf                       # none left
+    for scoring in ("softmax", "sigmoid"):
+        ids, wts = moe.route(x.cuda(), w.cuda(), b.cuda(), topk=4, scoring=scoring)
+        assert bool((ids == -1).all()) and bool((wts == 0).all())
+
+
+@pytest.mark.parametrize("T", [9, 300])
+@pytest.mark.parametrize("scoring,bias", [("softmax", False), ("sigmoid", True)])
+def test_router_ties_and_near_ties(T, scoring, bias):
+    """Equal experts go to the lower id; experts that differ in the last bit of one weight are ordered by their
+    64-bit scores, which float32 sums cannot tell apart."""
+    g = gen(11)
+    x = torch.randn(T, 2048, generator=g).to(BF16)
+    base = (torch.randn(6, 2048, generator=g) * 2048 ** -0.5).to(BF16)
+    w = base.repeat_interleave(4, 0).contiguous()          # experts 4i .. 4i + 3 alike
+    bits = w.view(torch.int16)
+    for i in range(6):
+        bits[4 * i + 2, 37 * i] ^= 1                        # and one of them off by the last bit of one weight
+    b = (torch.randn(6, generator=g) * 0.1).repeat_interleave(4) if bias else None
+    check_router(x, w, b, 9, scoring)
+
+
+def test_router_extreme_values():
+    x, w, _ = router_case(80, 512, 40, 6, "softmax", False, 21)
+    x[3] = 0.0                                              # every score equal: ids 0 .. 5
+    x[4, 7] = math.nan
+    x[6] *= 1e30
+    w[9] *= 2.0 ** 100                                      # sums past float32's range for token 6, huge ones elsewhere
+    w[11] *= 2.0 ** -100
+    for scoring in ("softmax", "sigmoid"):
+        ids, wts = moe.route(x.cuda(), w.cuda(), topk=6, scoring=scoring)
+        want, v, _ = ref.route(x, w, None, 6, scoring)
+        assert torch.equal(ids.cpu(), want)
+        assert bool(torch.isnan(wts[4]).all())
+        assert torch.equal(ids[3].cpu(), torch.arange(6, dtype=torch.int32))
+        ok = [t for t in range(80) if t not in (4, 6)]
+        assert bool((wts.cpu().double()[ok] - v[ok]).abs().max() < 1e-5)
+    w[2, 5] = math.nan                                      # one NaN expert ranks last
+    ids, _ = moe.route(x[:3].contiguous().cuda(), w.cuda(), topk=40, scoring="softmax")
+    assert bool((ids[:, -1] == 2).all())
+
+
+def test_router_empty_batch_and_refusals():
+    w = torch.zeros(8, 256, dtype=BF16, device="cuda")
+    ids, wts = moe.route(torch.zeros(0, 256, dtype=BF16, device="cuda"), w, topk=2)
+    assert ids.shape == (0, 2) and wts.shape == (0, 2)
+    x = torch.zeros(4, 256, dtype=BF16, device="cuda")
+    for bad in (dict(topk=9), dict(topk=2, scoring="top"), dict(topk=2, bias=torch.zeros(7, device="cuda")),
+                dict(topk=2, active=torch.ones(4, device="cuda")), dict(topk=0)):
+        with pytest.raises((ValueError, B.MMError)):
+            moe.route(x, w, **bad)
+    with pytest.raises(ValueError):
+        moe.route(x.float(), w, topk=2)
+    with pytest.raises(ValueError):
+        moe.route(x, w.t().contiguous().t(), topk=2)
+
+
+# ---------------------------------------------------------- few-token layer
+
+def few_weights(fmt, E, H, I, seed):
+    """Device arrays (w1, w2, s1, s2) in the prepared layout and 64-bit formula-order values."""
+    g = gen(seed)
+    w1 = torch.randn(E, 2 * I, H, generator=g) * H ** -0.5
+    w2 = torch.randn(E, H, I, generator=g) * I ** -0.5
+    s1 = s2 = None
+    if fmt == "bf16":
+        q1, q2 = w1.to(BF16), w2.to(BF16)
+        v1, v2 = list(q1.to(F64)), list(q2.to(F64))
+    elif fmt == "fp8":
+        s1, s2 = w1.abs().amax(2) / 448, w2.abs().amax(2) / 448
+        q1, q2 = (w1 / s1[..., None]).to(E4M3), (w2 / s2[..., None]).to(E4M3)
+        v1 = list(q1.float().to(F64) * s1.to(F64)[..., None])
+        v2 = list(q2.float().to(F64) * s2.to(F64)[..., None])
+    else:
+        p1, p2 = [ref.quantize_blocks(w) for w in w1], [ref.quantize_blocks(w) for w in w2]
+        q1, s1 = torch.stack([p[0] for p in p1]), torch.stack([p[1] for p in p1])
+        q2, s2 = torch.stack([p[0] for p in p2]), torch.stack([p[1] for p in p2])
+        v1, v2 = [ref.expand_blocks(*p) for p in p1], [ref.expand_blocks(*p) for p in p2]
+    q1 = torch.stack([ref.interleave(w.view(torch.int16 if fmt == "bf16" else torch.uint8), I) for w in q1]).view(q1.dtype)
+    dev = [None if t is None else t.contiguous().cuda() for t in (q1, q2, s1, s2)]
+    return dev, v1, v2
+
+
+def few_routes(T, E, K, seed, masked=0.0):
+    g = gen(seed)
+    ids = torch.stack([torch.randperm(E, generator=g)[:K] for _ in range(T)]).to(torch.int32)
+    wts = torch.softmax(torch.randn(T, K, generator=g), 1)
+    if masked:
+        m = torch.rand(T, K, generator=g) < masked
+        ids = torch.where(m, torch.full_like(ids, -1), ids)
+    return ids, wts
+
+
+def check_few(T, H, I, E, K, fmt, y_dtype, seed, S=0, clamp=None, masked=0.0, active=None, ids=None):
+    dev, v1, v2 = few_weights(fmt, E + S, H, I, seed)
+    x = torch.randn(T, H, generator=gen(seed + 1)).to(BF16)
+    i, wts = few_routes(T, E, K, seed + 2, masked)
+    ids = i if ids is None else ids
+    y, _, _ = moe.moe_few(x.cuda(), *dev, topk_ids=ids.cuda(), topk_weights=wts.cuda(), num_shared_experts=S,
+                          activation_clamp=clamp, y_dtype=y_dtype, active=None if active is None else active.cuda())
+    want, err = ref.moe(x, v1, v2, ids, wts, bool(S), clamp, active, y_dtype == "bf16")
+    within(y, want, err, "y")
+    return y
+
+
+FEW = [(1, 256, 128, 4, 2), (1, 512, 256, 8, 8), (2, 768, 384, 3, 1), (7, 512, 128, 16, 4), (16, 256, 384, 5, 3),
+       (17, 512, 256, 4, 2), (33, 256, 128, 2, 2), (64, 512, 256, 6, 3), (64, 256, 128, 1, 1)]
+
+
+@pytest.mark.parametrize("T,H,I,E,K", FEW)
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp8_block"])
+@pytest.mark.parametrize("y_dtype", ["bf16", "f32"])
+def test_few(T, H, I, E, K, fmt, y_dtype):
+    log(f"[few] T={T} H={H} I={I} E={E} K={K} {fmt} {y_dtype}")
+    check_few(T, H, I, E, K, fmt, y_dtype, 100 * T + E)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp8_block"])
+@pytest.mark.parametrize("T", [1, 5, 40])
+def test_few_shared_masked_inactive_clamped(fmt, T):
+    active = (torch.rand(T, generator=gen(T)) > 0.25).to(torch.int8)
+    active[0] = 1
+    log(f"[few shared] {fmt} T={T}")
+    check_few(T, 512, 256, 6, 3, fmt, "f32", 31, S=1, clamp=0.7, masked=0.3, active=active)
+
+
+def test_few_many_experts_and_routes():
+    check_few(64, 256, 128, 40, 32, "fp8", "f32", 5, S=1)          # 2112 routes, 41 experts of up to 64 rows
+    check_few(3, 256, 128, 1023, 32, "fp8", "bf16", 6, S=1)
+
+
+def test_few_nothing_to_do():
+    T, E = 6, 4
+    none = torch.full((T, 2), -1, dtype=torch.int32)
+    y = check_few(T, 512, 256, E, 2, "bf16", "f32", 9, ids=none)
+    assert bool((y == 0).all())
+    y = check_few(T, 512, 256, E, 2, "bf16", "f32", 9, S=1, active=torch.zeros(T, dtype=torch.int8))
+    assert bool((y == 0).all())
+    out = torch.tensor([[-1, 1], [E, 0], [2147483647, 2], [-2147483648, 3], [0, 1], [2, 3]], dtype=torch.int32)
+    check_few(T, 512, 256, E, 2, "fp8_block", "bf16", 10, ids=out)  # ids out of range are skipped
+    w, _, _ = few_weights("bf16", E, 512, 256, 1)
+    y, i, g = moe.moe_few(torch.zeros(0, 512, dtype=BF16, device="cuda"), *w, topk_ids=torch.zeros(0, 2, dtype=torch.int32, device="cuda"),
+                          topk_weights=torch.zeros(0, 2, device="cuda"))
+    assert y.shape == (0, 512)
+
+
+def test_few_same_expert_twice():
+    """An id that a token names twice counts with the sum of its weights."""
+    T, E = 20, 3
+    ids, wts = few_routes(T, E, 2, 3)
+    dev, v1, v2 = few_weights("bf16", E, 256, 128, 4)
+    x = torch.randn(T, 256, generator=gen(5)).to(BF16)
+    ids[4] = ids[4, 0]
+    y, _, _ = moe.moe_few(x.cuda(), *dev, topk_ids=ids.cuda(), topk_weights=wts.cuda(), y_dtype="f32")
+    want, err = ref.moe(x, v1, v2, ids, wts, y_bf16=False)
+    within(y, want, err)
+
+
+def test_few_nonfinite_stays_in_its_token():
+    T, E = 18, 4
+    dev, v1, v2 = few_weights("fp8_block", E, 512, 256, 8)
+    ids, wts = few_routes(T, E, 2, 9)
+    x = torch.randn(T, 512, generator=gen(10)).to(BF16)
+    x[3, 5], x[11, 7] = math.nan, math.inf
+    y, _, _ = moe.moe_few(x.cuda(), *dev, topk_ids=ids.cuda(), topk_weights=wts.cuda(), y_dtype="f32", activation_clamp=3.0)
+    assert bool(torch.isnan(y[3]).all())
+    keep = [t for t in range(T) if t not in (3, 11)]
+    x[3], x[11] = 0, 0
+    want, err = ref.moe(x, v1, v2, ids, wts, clamp=3.0, y_bf16=False)
+    within(y[keep], want[keep], err[keep])
+
+
+def test_few_refusals():
+    dev, _, _ = few_weights("fp8", 4, 256, 128, 1)
+    x = torch.zeros(3, 256, dtype=BF16, device="cuda")
+    ids = torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    wts = torch.zeros(3, 2, device="cuda")
+    ok = dict(topk_ids=ids, topk_weights=wts)
+    w1, w2, s1, s2 = dev
+    for args, kw in [((x, w1, w2), ok), ((x, w1, w2, s1, s2[:, :8]), ok), ((x, w1, w2, s1, s2), {}),
+                     ((x, w1, w2, s1, s2), dict(topk_ids=ids)), ((x, w1, w2, s1, s2), dict(ok, num_shared_experts=2)),
+                     ((x, w1, w2[:, :, :64], s1, s2), ok), ((x.float(), w1, w2, s1, s2), ok),
+                     ((x, w1.float(), w2, s1, s2), ok), ((x, w1, w2, s1, s2), dict(topk_ids=ids.long(), topk_weights=wts)),
+                     ((torch.zeros(65, 256, dtype=BF16, device="cuda"), w1, w2, s1, s2), ok),
+                     ((x, w1, w2, s1, s2), dict(router_weight=torch.zeros(4, 256, dtype=BF16, device="cuda"))),
+                     ((x, w1, w2, s1, s2), dict(router_weight=torch.zeros(5, 256, dtype=BF16, device="cuda"), topk=2)),
+                     ((x, w1, w2, s1, s2), dict(ok, y=torch.zeros(3, 256, device="cuda"))),
+                     ((x, w1, w2, s1, s2), dict(ok, activation_clamp=-1.0))]:
+        with pytest.raises((ValueError, B.MMError)):
+            moe.moe_few(*args, **kw)
+
+
+# --------------------------------------------------- block-scaled product
+
+def test_block_quantize_every_bf16_pattern():
+    """Codes and scales bit for bit, over every finite bf16 value and rows of one magnitude each."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    v = bits.view(BF16)
+    v = v[torch.isfinite(v.float())]
+    g = gen(2)
+    v = v[torch.randperm(v.numel(), generator=g)]
+    x = torch.cat([v, v[: -v.numel() % 384]]).view(-1, 384)
+    x = torch.cat([x, (torch.randn(300, 384, generator=g) * torch.exp(torch.randn(300, 1, generator=g) * 8)).to(BF16)])
+    x[5] = 0
+    q, s = moe.block_quantize(x.cuda())
+    want, ws = ref.quantize(x)
+    assert torch.equal(s.cpu(), ws)
+    assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("M,K", [(1, 128), (1, 7168), (3, 384), (257, 1152), (5000, 256)])
+def test_block_quantize_sizes(M, K):
+    x = torch.randn(M, K, generator=gen(M)).to(BF16)
+    q, s = moe.block_quantize(x.cuda())
+    want, ws = ref.quantize(x)
+    assert torch.equal(s.cpu(), ws) and torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8))
+    assert moe.block_quantize(torch.zeros(0, K, dtype=BF16, device="cuda"))[0].shape == (0, K)
+
+
+def test_block_quantize_nonfinite():
+    x = torch.randn(4, 384, generator=gen(1)).to(BF16)
+    x[0, 3], x[1, 200], x[2, 380] = math.nan, math.inf, -math.inf
+    q, s = (t.float().cpu() for t in moe.block_quantize(x.cuda()))
+    assert bool(torch.isnan(s[0, 0])) and bool(torch.isnan(q[0, :128]).all()) and bool(torch.isfinite(q[0, 128:]).all())
+    assert math.isinf(s[1, 1]) and bool(torch.isnan(q[1, 200])) and float(q[1, 128:200].abs().max()) == 0
+    assert math.isinf(s[2, 2]) and bool(torch.isnan(q[2, 380]))
+    want, ws = ref.quantize(x[3:])
+    assert torch.equal(s[3:], ws) and torch.equal(q[3:], want.float())
+
+
+def block_operands(M, N, K, G, seed):
+    g = gen(seed)
+    x = (torch.randn(M, K, generator=g) * torch.exp(0.5 * torch.randn(M, 1, generator=g))).to(BF16)
+    p = [ref.quantize_blocks(torch.randn(N, K, generator=g) * K ** -0.5 * (1 + i)) for i in range(G)]
+    return x, torch.stack([a for a, _ in p]), torch.stack([b for _, b in p])
+
+
+GEMM = [(1, 16, 128), (1, 7168, 256), (2, 144, 384), (15, 256, 1152), (16, 128, 128), (17, 272, 256), (33, 400, 640),
+        (64, 512, 512), (65, 112, 896), (127, 384, 256), (128, 128, 1024), (129, 656, 384), (257, 272, 512),
+        (300, 528, 128), (1030, 1040, 256)]
+
+
+@pytest.mark.parametrize("M,N,K", GEMM)
+def test_block_matmul(M, N, K):
+    log(f"[block] M={M} N={N} K={K}")
+    x, w, ws = block_operands(M, N, K, 1, M + N)
+    q, s = ref.quantize(x)
+    want, err = ref.block_matmul(q, s, w[0], ws[0])
+    y = moe.block_matmul(q.cuda(), s.cuda(), w[0].cuda(), ws[0].cuda())
+    within(y, want, err)
+    # from bf16 rows: the same product, bit for bit
+    assert torch.equal(moe.block_linear(x.cuda(), w[0].cuda(), ws[0].cuda()).view(torch.int16), y.view(torch.int16))
+
+
+@pytest.mark.parametrize("counts,gap", [([5, 0, 1, 130], 0), ([0, 0, 0], 3), ([300, 2, 257, 0, 64, 16], 7), ([1] * 70, 1),
+                                        ([128, 128], 0)])
+def test_block_matmul_groups(counts, gap):
+    """Ragged groups, empty ones, rows between groups: those of y stay as they were."""
+    G, N, K = len(counts), 272, 384
+    offs, at = [], gap
+    for c in counts:
+        offs.append(at)
+        at += c + gap
+    M = at + 2
+    x, w, ws = block_operands(M, N, K, G, G)
+    q, s = ref.quantize(x)
+    y = torch.full((M, N), 7.0, dtype=BF16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    o, c = torch.tensor(offs, **i32), torch.tensor(counts, **i32)
+    out = moe.block_matmul(q.cuda(), s.cuda(), w.cuda(), ws.cuda(), o, c, y=y)
+    assert out is y
+    free = torch.ones(M, dtype=torch.bool)
+    for i, (a, n) in enumerate(zip(offs, counts)):
+        if n:
+            want, err = ref.block_matmul(q[a:a + n], s[a:a + n], w[i], ws[i])
+            within(y[a:a + n], want, err, f"group {i}")
+            free[a:a + n] = False
+    assert bool((y.cpu()[free] == 7.0).all())
+    y2 = torch.full_like(y, 7.0)
+    moe.block_linear(x.cuda(), w.cuda(), ws.cuda(), o, c, y=y2)
+    assert torch.equal(y2.view(torch.int16), y.view(torch.int16))
+
+
+def test_block_matmul_groups_outside_the_rows():
+    """The part of a group outside the matrix is ignored."""
+    G, M, N, K = 5, 40, 128, 256
+    x, w, ws = block_operands(M, N, K, G, 8)
+    q, s = ref.quantize(x)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    offs, cnts = [-10, 30, 2147483647, 50, 12], [15, 100, 2147483647, -3, 4]
+    y = torch.full((M, N), 7.0, dtype=BF16, device="cuda")
+    moe.block_matmul(q.cuda(), s.cuda(), w.cuda(), ws.cuda(), torch.tensor(offs, **i32), torch.tensor(cnts, **i32), y=y)
+    for i, a, b in ((0, 0, 5), (1, 30, 40), (4, 12, 16)):
+        want, err = ref.block_matmul(q[a:b], s[a:b], w[i], ws[i])
+        within(y[a:b], want, err, f"group {i}")
+    assert bool((y[5:12] == 7.0).all()) and bool((y[16:30] == 7.0).all())
+
+
+def test_block_matmul_past_32_bit_offsets():
+    M, N, K = (1 << 18) + 5, 8208, 128          # y: 2^31 values and more
+    x, w, ws = block_operands(300, N, K, 1, 3)
+    xd = x.cuda().repeat(-(-M // 300), 1)[:M].contiguous()
+    y = moe.block_linear(xd, w[0].cuda(), ws[0].cuda())
+    q, s = ref.quantize(x)
+    want, err = ref.block_matmul(q, s, w[0], ws[0])
+    for r0 in (0, 261600, M - 300):      # value 2^31 lies in row 261633
+        rows = torch.arange(r0, r0 + 300)
+        within(y[r0:r0 + 300], want[rows % 300], err[rows % 300])
+
+
+def test_block_refusals():
+    x, w, ws = (t.cuda() for t in block_operands(4, 32, 256, 1, 1))
+    q, s = moe.block_quantize(x)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    o = torch.zeros(1, **i32)
+    for fn, args in [(moe.block_quantize, (x[:, :100].contiguous(),)), (moe.block_quantize, (x.float(),)),
+                     (moe.block_linear, (x, w[0], ws[0][:, :1])), (moe.block_linear, (x, w[0][:, :128], ws[0])),
+                     (moe.block_linear, (x, w[0], ws[0], o)), (moe.block_linear, (x, w[0], ws[0], o.long(), o.long())),
+                     (moe.block_linear, (x, w.repeat(2, 1, 1), ws.repeat(2, 1, 1))),
+                     (moe.block_matmul, (q, s[:, :1], w[0], ws[0])), (moe.block_matmul, (x, s, w[0], ws[0])),
+                     (moe.block_linear, (x, w[0][:24].contiguous(), ws[0]))]:
+        with pytest.raises((ValueError, B.MMError)):
+            fn(*args)
+
+
+# --------------------------------------------------------------- together
+
+def layer_of(T, usecase, S=0):
+    cfg = wl.Config("ops", usecase, T, 512, 256, 8, 2, 0.5, 77, shared=S)
+    inp = wl.make_inputs(cfg)
+    layer = moe.ExpertLayer(T, 512, 256, 8, 2, usecase, "f32", num_shared_experts=S)
+    layer.load_weights(inp.weights.w1, inp.weights.w2, inp.weights.s1, inp.weights.s2)
+    return inp, layer
+
+
+@pytest.mark.parametrize("usecase", ["bf16", "fp8"])
+@pytest.mark.parametrize("T,S", [(1, 0), (24, 1), (64, 0)])
+def test_router_then_layer_on_both_paths(usecase, T, S):
+    """The router's routes through mega_moe and through mm_moe_few, on the same weights."""
+    inp, layer = layer_of(T, usecase, S)
+    x = inp.x.cuda()
+    wr = (torch.randn(8, 512, generator=gen(1)) * 512 ** -0.5).to(BF16).cuda()
+    ids, wts = moe.route(x, wr, topk=2)
+    big, _ = layer.forward(x, ids, wts)
+    few = layer.forward_few(x, ids, wts)
+    # one call from the router's weights on: the same routes and bits
+    one, ids1, wts1 = moe.moe_few(x, layer.w1, layer.w2, layer.s1, layer.s2, router_weight=wr, topk=2,
+                                  num_shared_experts=S, y_dtype="f32")
+    assert torch.equal(ids1, ids) and torch.equal(wts1, wts) and torch.equal(one, few)
+    rms = float(big.square().mean().sqrt())
+    # mega_moe rounds A to bf16, or x and A to e4m3 (half a step 2^-4 each): its own bar against the formula
+    assert float((big - few).abs().max()) / rms <= (1e-2 if usecase == "bf16" else 0.25)
+
+
+def test_dispatch_then_grouped_block_product():
+    """mm_dispatch_layout's pool through the block quantiser and the grouped product: every pool row of every expert."""
+    T, H, N, E = 150, 512, 272, 8
+    inp, layer = layer_of(T, "bf16")
+    x = inp.x.cuda()
+    ids, _ = moe.route(x, (torch.randn(E, H, generator=gen(2)) * H ** -0.5).to(BF16).cuda(), topk=2)
+    im = layer.new_intermediates()
+    im.x_pool.zero_()
+    layer.dispatch(x, ids, im)
+    pool = im.x_pool.view(BF16).view(-1, H)
+    _, w, ws = block_operands(1, N, H, E, 5)
+    y = moe.block_linear(pool, w.cuda(), ws.cuda(), im.expert_offsets, im.expert_counts)
+    q, s = ref.quantize(inp.x)
+    src, off, cnt = im.pool_src.cpu(), im.expert_offsets.cpu(), im.expert_counts.cpu()
+    assert int(cnt.sum()) == 2 * T
+    for e in range(E):
+        a, n = int(off[e]), int(cnt[e])
+        tok = (src[a:a + n] // 2).long()
+        want, err = ref.block_matmul(q[tok], s[tok], w[e], ws[e])
+        within(y[a:a + n], want, err, f"expert {e}")
+
+
+def test_repeated_calls_are_bitwise_equal():
+    inp, layer = layer_of(40, "fp8", 1)
+    x = inp.x.cuda()
+    wr = torch.randn(8, 512, generator=gen(3)).mul_(0.05).to(BF16).cuda()
+    _, w, ws = block_operands(1, 400, 512, 1, 6)
+    w, ws = w[0].cuda(), ws[0].cuda()
+
+    def once():
+        y, i, g = moe.moe_few(x, layer.w1, layer.w2, layer.s1, layer.s2, router_weight=wr, topk=2, num_shared_experts=1)
+        return y, i, g, moe.block_linear(x, w, ws)
+
+    a = once()
+    for _ in range(5):
+        for p, q in zip(a, once()):
+            assert torch.equal(p, q)
+
+
+def test_streams_and_graphs():
+    """Captured and replayed with eager work between, two graphs replayed on two streams at once, and a call on a
+    stream other than the current one: all equal the eager results."""
+    inp, layer = layer_of(20, "bf16", 1)
+    wr = torch.randn(8, 512, generator=gen(3)).mul_(0.05).to(BF16).cuda()
+    _, w, ws = block_operands(1, 400, 512, 1, 6)
+    w, ws = w[0].cuda(), ws[0].cuda()
+    xs = [torch.randn(20, 512, generator=gen(50 + i)).to(BF16).cuda() for i in range(4)]
+
+    def work(x, stream=None):
+        y, i, g = moe.moe_few(x, layer.w1, layer.w2, router_weight=wr, topk=2, num_shared_experts=1, stream=stream)
+        return y, i, g, moe.block_linear(x, w, ws, stream=stream), *moe.block_quantize(x, stream=stream)
+
+    def same(a, b):
+        return all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(a, b))
+
+    want = [work(x) for x in xs]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = work(xs[0], side)
+    side.synchronize()
+    assert same(got, want[0])
+
+    graphs = []
+    for k in range(2):
+        buf = xs[k].clone()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            work(buf)
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = work(buf)
+        graphs.append((g, buf, out))
+    for n in range(4):
+        for k, (g, buf, out) in enumerate(graphs):
+            buf.copy_(xs[(n + k) % 4])
+            g.replay()
+            eager = work(xs[(n + 2) % 4])
+            torch.cuda.synchronize()
+            assert same(out, want[(n + k) % 4]) and same(eager, want[(n + 2) % 4])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for n in range(4):
+        for k, (g, buf, out) in enumerate(graphs):
+            with torch.cuda.stream(streams[k]):
+                buf.copy_(xs[(n + 3 * k) % 4])
+                g.replay()
+        torch.cuda.synchronize()
+        for k, (g, buf, out) in enumerate(graphs):
+            assert same(out, want[(n + 3 * k) % 4])
