@@ -88,6 +88,15 @@ hipError_t launch_block_quantize(const void* x, int64_t rows, int cols, uint8_t*
 
 namespace {
 
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+constexpr int kThreads = 512, kWaves = 8;
+constexpr int kBM = 256, kBN = 256;       // the large tile
+constexpr int kFewRows = 64;              // most rows of a streaming unit
+constexpr int kFewCols = 16;
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // rows of group gi, clipped to the matrix
 __device__ __forceinline__ void group_rows(const BlockArgs& a, int gi, int64_t& lo, int64_t& n) {
   if (a.offsets == nullptr) {
@@ -101,22 +110,54 @@ __device__ __forceinline__ void group_rows(const BlockArgs& a, int gi, int64_t& 
   n = hi > lo ? hi - lo : 0;
 }
 
+// How the rows of a group are cut: into blocks of 256 rows, a rest of up to
+// 128 rows being a half block (half the products), listed after the full
+// ones.  kFew: every row in streaming units of up to 64 rows (small groups).
+enum Class : int { kFull = 0, kHalf = 1, kFew = 2 };
+
+// M-blocks of class c in a group of n rows
+__device__ __forceinline__ int64_t blocks_of(int c, int64_t n) {
+  const int rest = (int)(n % kBM);
+  if (c == kFew) return (n + kFewRows - 1) / kFewRows;
+  if (c == kHalf) return rest > 0 && rest <= kBM / 2 ? 1 : 0;
+  return n / kBM + (rest > kBM / 2 ? 1 : 0);
+}
+__device__ __forceinline__ int64_t first_block_row(int c, int64_t n, int64_t mb) {
+  return c == kFull ? mb * kBM : c == kFew ? mb * kFewRows : n / kBM * kBM;
+}
+__device__ __forceinline__ int cols_of(int c) { return c == kFew ? kFewCols : kBN; }
+
+// M-blocks of class c over all groups (every lane of the wave takes part)
+__device__ int64_t count_blocks(const BlockArgs& a, int c) {
+  if (a.offsets == nullptr) return blocks_of(c, a.M);
+  int64_t sum = 0;
+  for (int g = lane_id(); g < a.G; g += 64) {
+    int64_t lo, n;
+    group_rows(a, g, lo, n);
+    sum += blocks_of(c, n);
+  }
+  return wave_sum(sum);
+}
+
 struct TileAt {
-  int64_t m0, rows;    // first row of the tile, rows of its group from there
-  int group, n0;
+  int64_t m0;          // first row
+  int rows, group, n0;
 };
 
-// Finds tile `at` of the list (group, N-block, M-block: M fastest) among the
-// groups, 64 at a time; every lane of the wave takes part.  Returns false
-// past the end.
-template <int BM, int BN>
-__device__ bool find_tile(const BlockArgs& a, int64_t at, TileAt& o) {
-  const int nb = (a.N + BN - 1) / BN;
-  const int l = lane_id();
+// in scalar registers, where the copies' descriptors need it (rows are below 2^24)
+__device__ __forceinline__ TileAt uniform_tile(const TileAt& t) {
+  return TileAt{(int64_t)(uint32_t)uniform((int)t.m0), uniform(t.rows), uniform(t.group), uniform(t.n0)};
+}
+
+// Tile `at` of class c in the order (group, N-block, M-block: M fastest).
+__device__ bool find_tile(const BlockArgs& a, int c, int64_t at, TileAt& o) {
+  const int bn = cols_of(c), nb = (a.N + bn - 1) / bn;
+  int l = lane_id();
+  asm volatile("" : "+v"(l));
   for (int g0 = 0; g0 < a.G; g0 += 64) {
     int64_t lo = 0, n = 0;
     if (g0 + l < a.G) group_rows(a, g0 + l, lo, n);
-    const int64_t mine = (n + BM - 1) / BM * nb;
+    const int64_t mine = blocks_of(c, n) * nb;
     int64_t pre = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -125,14 +166,15 @@ __device__ bool find_tile(const BlockArgs& a, int64_t at, TileAt& o) {
     }
     const int64_t all = __shfl(pre, 63, 64);
     if (at < all) {
-      const uint64_t m = ballot(at < pre);
-      const int src = __ffsll((unsigned long long)m) - 1;
+      const int src = __ffsll((unsigned long long)ballot(at < pre)) - 1;
       const int64_t first = __shfl(pre - mine, src, 64), rows = __shfl(n, src, 64), row0 = __shfl(lo, src, 64);
-      const int64_t mb = (rows + BM - 1) / BM, k = at - first;
+      const int64_t mb = blocks_of(c, rows), k = at - first;
+      const int64_t m = first_block_row(c, rows, k % mb);
+      const int64_t most = c == kFew ? kFewRows : kBM;
       o.group = g0 + src;
-      o.n0 = (int)(k / mb) * BN;
-      o.m0 = row0 + (k % mb) * BM;
-      o.rows = rows - (k % mb) * BM;
+      o.n0 = (int)(k / mb) * bn;
+      o.m0 = row0 + m;
+      o.rows = (int)(rows - m < most ? rows - m : most);
       return true;
     }
     at -= all;
@@ -140,100 +182,343 @@ __device__ bool find_tile(const BlockArgs& a, int64_t at, TileAt& o) {
   return false;
 }
 
+// Large tile: 64 * MT rows x 256 columns, 8 waves (2 along N, 4 along M) of
+// 16 * MT rows x 128 columns, one group of 128 K-values per stage, two LDS
+// stages filled by LDS-DMA.  Weights are the MFMA's A operand, so a lane's
+// four accumulators are four columns of one row: its scale is one number per
+// row tile, and its result one 8-byte store.
+// Bound: the MFMA at the clock the chip holds under it.  A stage of the full
+// tile takes 1.65 us against 1.61 us at the rate that a large e4m3 library
+// product reaches here (2.67 PFLOP/s); without the products the copies and
+// LDS reads alone take 90% of it.
+template <int MT>
+__device__ __forceinline__ void mma_tile(const BlockArgs& a, const TileAt& at, uint8_t* sa0, uint8_t* sa1, uint8_t* sb0,
+                                         uint8_t* sb1, float (*ssc)[2][kBM]) {
+  constexpr int WM = 4, NT = 8;
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));   // nothing derived from it is kept across tiles: the registers are full
+  const TileAt t = uniform_tile(at);
+  const int w = uniform(tid / 64), l = tid % 64, r = l % 16, g = l / 16;
+  const int wm = w % WM, wn = w / WM, KB = a.K / kBlock;
+  const int rows = t.rows, cols = a.N - t.n0 < kBN ? a.N - t.n0 : kBN;
+  // one instruction moves 8 rows of 128 bytes, lane i to byte 16 * i; the
+  // chunk at place p of row x is p ^ (x / 2 % 8), so that 16 rows read at one
+  // chunk hit 16 different bank groups.  Rows past the last one are beyond the
+  // descriptor and arrive as zeros without a memory access.
+  const uint32_t voff = (uint32_t)(l / 8) * a.K + (((l % 8) ^ ((4 * (w % 2) + l / 16) % 8)) * 16);
+  const uint8_t *ab = a.a + t.m0 * a.K, *bb = a.b + ((int64_t)t.group * a.N + t.n0) * a.K;
+  auto copy = [&](int kb, uint8_t* sa, uint8_t* sb) {
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)ab, (short)0, rows * a.K, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)bb, (short)0, cols * a.K, 0x00020000);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(sa + (w + 8 * i) * 1024), 16, voff, (w + 8 * i) * 8 * a.K + kb * kBlock, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kBN / 64; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(sb + (w + 8 * i) * 1024), 16, voff, (w + 8 * i) * 8 * a.K + kb * kBlock, 0, 0);
+  };
+  const int nb = (t.n0 + wn * NT * 16) / kBlock, nblocks = (a.N + kBlock - 1) / kBlock;
+  const float* bsp = a.bs + ((int64_t)t.group * nblocks + (nb < nblocks ? nb : nblocks - 1)) * KB;
+  const int sw = (r / 2) % 8;
+  const int c0 = ((2 * g) ^ sw) * 16 + r * kBlock, c1 = ((2 * g + 1) ^ sw) * 16 + r * kBlock;
+  // Row scales of two stages at a time through LDS, one a thread: a wave's own
+  // gather of its 64 rows' scales, each in a line of its own, cost a fifth of
+  // the time (780 against 612 us without them at 16384 x 4096 x 7168).
+  // Beyond the rows the descriptor gives 0, beyond a row's end its neighbour's
+  // scale, which no product takes.
+  const float* asb = a.as + t.m0 * KB;
+  const int srow = tid / 2;
+  auto ask = [&](int kb) {
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)asb, (short)0, rows * KB * 4, 0x00020000);
+    return __builtin_amdgcn_raw_buffer_load_b32(rs, (srow * KB + tid % 2) * 4, kb * 4, 0);
+  };
+  auto keep = [&](int pair, uint32_t v) { ssc[pair % 2][tid % 2][srow] = __uint_as_float(v); };
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto compute = [&](const uint8_t* sa, const uint8_t* sb, const float* ss, float scb) {
+    u32x4 af[MT][2], b[2][2];
+    float sc[MT];
+    f32x4 sum[2][MT];
+    auto weights = [&](int j) {
+      b[j % 2][0] = *reinterpret_cast<const u32x4*>(sb + (wn * NT + j) * 16 * kBlock + c0);
+      b[j % 2][1] = *reinterpret_cast<const u32x4*>(sb + (wn * NT + j) * 16 * kBlock + c1);
+    };
+    weights(0);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      af[i][0] = *reinterpret_cast<const u32x4*>(sa + (wm * MT + i) * 16 * kBlock + c0);
+      af[i][1] = *reinterpret_cast<const u32x4*>(sa + (wm * MT + i) * 16 * kBlock + c1);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sc[i] = ss[(wm * MT + i) * 16 + r] * scb;
+    // products of tile j while tile j - 1 is scaled and tile j + 1 is read;
+    // issue order: the reads, then a product and four scalings in turn
+#pragma unroll
+    for (int j = 0; j <= NT; ++j) {
+      if (j + 1 < NT) weights(j + 1);
+      if (j < NT) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sum[j % 2][i] = mfma128(b[j % 2][0], b[j % 2][1], af[i][0], af[i][1]);
+      }
+      if (j > 0) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[j - 1][i] += sum[(j - 1) % 2][i] * sc[i];
+      }
+      if (j > 0 && j < NT) {
+        if (j + 1 < NT) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto turn = [&]() {
+    // the stage's products stay before the wait: nothing else ties them to it
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) asm volatile("" : "+v"(acc[j][i]));
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's copies have landed
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  {
+    const uint32_t v = ask(0);
+    copy(0, sa0, sb0);
+    keep(0, v);
+  }
+  float scb = bsp[0];
+  turn();
+  int kb = 0, pair = 0;
+  for (; kb + 1 < KB; kb += 2, ++pair) {
+    // loads that the next stages need go out before the copies: a wait for
+    // them leaves the copies in flight
+    const uint32_t v = ask(kb + 2);
+    const float scb1 = bsp[kb + 1];
+    __builtin_amdgcn_sched_barrier(0);
+    copy(kb + 1, sa1, sb1);
+    compute(sa0, sb0, ssc[pair % 2][0], scb);
+    turn();
+    const int nx = kb + 2 < KB ? kb + 2 : KB - 1;   // past the end: the last stage again, unused
+    scb = bsp[nx];
+    __builtin_amdgcn_sched_barrier(0);
+    copy(nx, sa0, sb0);
+    keep(pair + 1, v);
+    compute(sa1, sb1, ssc[pair % 2][1], scb1);
+    turn();
+  }
+  if (kb < KB) compute(sa0, sb0, ssc[pair % 2][0], scb);
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int n = t.n0 + (wn * NT + j) * 16 + 4 * g;
+      const int row = (wm * MT + i) * 16 + r;
+      if (row < rows && n < a.N)
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + (t.m0 + row) * a.N + n) =
+            u32x2{pack_bf16x2(acc[j][i][0], acc[j][i][1]), pack_bf16x2(acc[j][i][2], acc[j][i][3])};
+    }
+  __syncthreads();      // the next tile of this workgroup writes the stages again
+}
+
+// 32 bf16 of a group of 128 (a quarter of it, the other quarters in the
+// lanes 16, 32, 48 away) -> their codes and the group's scale, the same
+// numbers as k_block_quantize.  The quotient is x * (1/s) with the exact
+// remainder folded back (two fused steps), which rounds like the division.
+__device__ __forceinline__ float quant_group(const u32x4 (&v)[4], u32x4 (&q)[2]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = amax_bits(v[i], m);
+#pragma unroll
+  for (int o = 16; o < 64; o <<= 1) {
+    const uint32_t x = (uint32_t)__shfl_xor((int)m, o, 64);
+    m = x > m ? x : m;
+  }
+  const float s = block_scale(m);
+  if (ballot(!(s < 1e36f)) != 0) {           // an infinity or a NaN somewhere: the plain division
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32x2 c = quant8(v[i], s);
+      q[i / 2][2 * (i % 2)] = c[0];
+      q[i / 2][2 * (i % 2) + 1] = c[1];
+    }
+    return s;
+  }
+  const float r = 1.0f / s;
+  auto div = [&](float x) {
+    const float p = x * r;
+    return sat448(__builtin_fmaf(__builtin_fmaf(-s, p, x), r, p));
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t x = v[i][2 * h], y = v[i][2 * h + 1];
+      int c = __builtin_amdgcn_cvt_pk_fp8_f32(div(__uint_as_float(x << 16)), div(__uint_as_float(x & 0xffff0000u)), 0, false);
+      c = __builtin_amdgcn_cvt_pk_fp8_f32(div(__uint_as_float(y << 16)), div(__uint_as_float(y & 0xffff0000u)), c, true);
+      q[i / 2][2 * (i % 2) + h] = (uint32_t)c;
+    }
+  return s;
+}
+
+// Streaming unit: up to 16 * NT rows x 16 columns.  Each weight byte goes
+// straight from memory into an operand; the 8 waves share the K-blocks, D of
+// them in flight a wave, and meet in LDS.  FROM_X: the rows are bf16 and are
+// quantised in registers.  Bound: HBM (latency for a single short product).
+template <int NT, int D, bool FROM_X>
+__device__ __forceinline__ void few_unit(const BlockArgs& a, const TileAt& at, f32x4 (*red)[NT][64]) {
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const TileAt t = uniform_tile(at);
+  const int w = uniform(tid / 64), l = tid % 64, r = l % 16, g = l / 16;
+  const int KB = a.K / kBlock, nblocks = (a.N + kBlock - 1) / kBlock;
+  const uint8_t* bp = a.b + ((int64_t)t.group * a.N + t.n0 + r) * a.K + g * 32;
+  const float* bsp = a.bs + ((int64_t)t.group * nblocks + t.n0 / kBlock) * KB;
+  const uint8_t* ap[NT];
+  const float* asp[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int64_t row = t.m0 + (16 * i + r < t.rows ? 16 * i + r : 0);
+    ap[i] = FROM_X ? static_cast<const uint8_t*>(a.x) + row * a.K * 2 + g * 64 : a.a + row * a.K + g * 32;
+    asp[i] = a.as + row * KB;
+  }
+  constexpr int XL = FROM_X ? 4 : 2;
+  struct Stage {
+    u32x4 b[2], x[NT][XL];
+    float sa[NT], sb;
+  } st[D];
+  auto load = [&](Stage& s, int kb) {
+    if (kb >= KB) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      s.b[h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(bp + (int64_t)kb * kBlock + h * 16));
+    s.sb = bsp[kb];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      if (NT == 1 || 16 * i < t.rows) {
+#pragma unroll
+        for (int h = 0; h < XL; ++h)
+          s.x[i][h] = *reinterpret_cast<const u32x4*>(ap[i] + (int64_t)kb * (kBlock * (FROM_X ? 2 : 1)) + h * 16);
+        if constexpr (!FROM_X) s.sa[i] = asp[i][kb];
+      }
+  };
+  f32x4 acc[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(st[d], w + d * kWaves);
+  for (int kb = w; kb < KB; kb += D * kWaves) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int k = kb + d * kWaves;
+      if (k < KB) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          if (NT == 1 || 16 * i < t.rows) {
+            if constexpr (FROM_X) {
+              u32x4 q[2];
+              const float s = quant_group(st[d].x[i], q);
+              acc[i] += mfma128(st[d].b[0], st[d].b[1], q[0], q[1]) * (s * st[d].sb);
+            } else {
+              acc[i] += mfma128(st[d].b[0], st[d].b[1], st[d].x[i][0], st[d].x[i][1]) * (st[d].sa[i] * st[d].sb);
+            }
+          }
+        load(st[d], k + D * kWaves);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) red[w][i][l] = acc[i];
+  __syncthreads();
+  for (int i = tid; i < NT * 64; i += kThreads) {
+    f32x4 v = red[0][i / 64][i % 64];
+#pragma unroll
+    for (int k = 1; k < kWaves; ++k) v += red[k][i / 64][i % 64];
+    const int row = i / 64 * 16 + i % 16;
+    if (row < t.rows)
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + (t.m0 + row) * a.N + t.n0 + i % 64 / 16 * 4) =
+          u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  }
+  __syncthreads();
+}
+
 }  // namespace
 
-// 128 rows x 128 columns, 4 waves of 64 x 64, one group of 128 K-values per
-// stage, two LDS stages.
-__global__ __launch_bounds__(256) void k_block_tile(BlockArgs a) {
-  constexpr int BM = 128, BN = 128;
-  __shared__ __attribute__((aligned(16))) u32x4 sa[2][BM * 8], sb[2][BN * 8];
-  const int tid = threadIdx.x, w = tid / 64, l = tid % 64, r = l % 16, g = l / 16;
-  const int wm = w % 2, wn = w / 2, KB = a.K / kBlock;
-  for (int64_t at = blockIdx.x;; at += gridDim.x) {
+// Products with many rows.  One workgroup a CU; XCD x takes an eighth of
+// each class's list (neighbours share an L2), and its workgroups take
+// every n-th tile of it in turn.
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_block_mma(BlockArgs a) {
+  // five separate arrays: the compiler then sees that a stage's reads and the
+  // other stage's copies do not meet, and does not wait for the copies
+  __shared__ __attribute__((aligned(1024))) uint8_t sa0[kBM * kBlock], sa1[kBM * kBlock], sb0[kBN * kBlock], sb1[kBN * kBlock];
+  __shared__ float ssc[2][2][kBM];
+  const int x = blockIdx.x % 8, step = gridDim.x / 8;
+  int64_t n[2], first[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int64_t total = count_blocks(a, c) * ((a.N + kBN - 1) / kBN);
+    first[c] = total * x / 8;
+    n[c] = total * (x + 1) / 8 - first[c];
+  }
+  for (int64_t k = blockIdx.x / 8; k < n[0] + n[1]; k += step) {
     TileAt t;
-    if (!find_tile<BM, BN>(a, at, t)) break;
-    const uint8_t *ap[4], *bp[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = i * 32 + tid / 8;
-      ap[i] = a.a + (t.m0 + (row < t.rows ? row : 0)) * a.K + (tid % 8) * 16;
-      const int n = t.n0 + row;
-      bp[i] = a.b + ((int64_t)t.group * a.N + (n < a.N ? n : a.N - 1)) * a.K + (tid % 8) * 16;
+    if (k < n[0]) {
+      if (!find_tile(a, kFull, first[0] + k, t)) break;
+      mma_tile<4>(a, t, sa0, sa1, sb0, sb1, ssc);
+    } else {
+      if (!find_tile(a, kHalf, first[1] + k - n[0], t)) break;
+      mma_tile<2>(a, t, sa0, sa1, sb0, sb1, ssc);
     }
-    const float* asp[4];
-    int64_t tok[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = wm * 64 + i * 16 + r;
-      tok[i] = row < t.rows ? t.m0 + row : -1;
-      asp[i] = a.as + (t.m0 + (row < t.rows ? row : 0)) * KB;
-    }
-    const int nb = (t.n0 + wn * 64) / kBlock, nblocks = (a.N + kBlock - 1) / kBlock;
-    const float* bsp = a.bs + ((int64_t)t.group * nblocks + (nb < nblocks ? nb : nblocks - 1)) * KB;
-    f32x4 acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    u32x4 ra[4], rb[4];
-    auto fetch = [&](int kb) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ra[i] = *reinterpret_cast<const u32x4*>(ap[i] + (int64_t)kb * kBlock);
-        rb[i] = *reinterpret_cast<const u32x4*>(bp[i] + (int64_t)kb * kBlock);
-      }
-    };
-    auto put = [&](int st) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = i * 32 + tid / 8, c = (tid % 8) ^ (row % 8);
-        sa[st][row * 8 + c] = ra[i];
-        sb[st][row * 8 + c] = rb[i];
-      }
-    };
-    fetch(0);
-    put(0);
-    __syncthreads();
-    for (int kb = 0; kb < KB; ++kb) {
-      if (kb + 1 < KB) fetch(kb + 1);
-      float sc[4];
-      const float bscale = bsp[kb];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sc[i] = asp[i][kb] * bscale;
-      const u32x4 *A = sa[kb & 1], *B = sb[kb & 1];
-      u32x4 bf[4][2];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = wn * 64 + j * 16 + r;
-        bf[j][0] = B[row * 8 + ((2 * g) ^ (row % 8))];
-        bf[j][1] = B[row * 8 + ((2 * g + 1) ^ (row % 8))];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = wm * 64 + i * 16 + r;
-        const u32x4 a0 = A[row * 8 + ((2 * g) ^ (row % 8))], a1 = A[row * 8 + ((2 * g + 1) ^ (row % 8))];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += mfma128(bf[j][0], bf[j][1], a0, a1) * sc[i];
-      }
-      if (kb + 1 < KB) put((kb + 1) & 1);
-      __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = t.n0 + wn * 64 + j * 16 + 4 * g;
-        if (tok[i] >= 0 && n < a.N)
-          *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + tok[i] * a.N + n) =
-              u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
-      }
   }
 }
 
-hipError_t launch_block_gemm(const BlockArgs& a, int num_cus, hipStream_t s) {
-  const int64_t tiles = ((a.M + 127) / 128 + (a.offsets ? a.G : 0)) * ((a.N + 127) / 128);
-  const int64_t most = 2 * (int64_t)num_cus;
-  hipLaunchKernelGGL(k_block_tile, dim3((unsigned)(tiles < most ? tiles : most)), dim3(256), 0, s, a);
+// Products with few rows, or few in each group.
+template <int NT, int D, bool FROM_X>
+__global__ __launch_bounds__(kThreads) void k_block_few(BlockArgs a) {
+  __shared__ f32x4 red[kWaves][NT][64];
+  if (a.offsets == nullptr) {          // one unit of all rows a workgroup
+    const TileAt t{a.m_first, (int)(a.M - a.m_first), 0, (int)blockIdx.x * kFewCols};
+    few_unit<NT, D, FROM_X>(a, t, red);
+    return;
+  }
+  const int64_t total = count_blocks(a, kFew) * (a.N / kFewCols);
+  for (int64_t k = blockIdx.x; k < total; k += gridDim.x) {
+    TileAt t;
+    if (!find_tile(a, kFew, k, t)) break;
+    few_unit<NT, D, FROM_X>(a, t, red);
+  }
+}
+
+bool block_from_x(const BlockArgs& a) { return a.offsets == nullptr && a.M <= 16; }
+
+hipError_t launch_block_gemm(const BlockArgs& args, int num_cus, hipStream_t s) {
+  BlockArgs a = args;
+  const int64_t units = a.N / kFewCols;
+  if (a.offsets != nullptr && a.M <= (int64_t)kFewRows * a.G) {
+    const int64_t most = 2 * (int64_t)num_cus, all = units * a.G;
+    hipLaunchKernelGGL((k_block_few<4, 2, false>), dim3((unsigned)(all < most ? all : most)), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+  }
+  // one matrix: up to 64 rows beyond the blocks of 256 go through the streaming units
+  const int64_t rest = a.offsets == nullptr ? a.M % kBM : 0;
+  if (rest == 0 || rest > kFewRows || a.M > rest) {
+    if (rest > 0 && rest <= kFewRows) a.M -= rest;
+    hipLaunchKernelGGL(k_block_mma, dim3((unsigned)((num_cus + 7) / 8 * 8)), dim3(kThreads), 0, s, a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess || a.M == args.M) return err;
+    a.m_first = a.M;
+    a.M = args.M;
+  }
+  if (a.x != nullptr) hipLaunchKernelGGL((k_block_few<1, 2, true>), dim3((unsigned)units), dim3(kThreads), 0, s, a);
+  else if (rest <= 16) hipLaunchKernelGGL((k_block_few<1, 4, false>), dim3((unsigned)units), dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_block_few<4, 2, false>), dim3((unsigned)units), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

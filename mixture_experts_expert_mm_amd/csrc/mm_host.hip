@@ -445,6 +445,26 @@ mm_status do_l2(const mm_plan& pl, const int32_t* offsets, const int32_t* counts
 bool ok16(const void* p) { return p && aligned(p, 16); }
 bool ok4(const void* p) { return p && aligned(p, 4); }
 
+// both group arrays or, for one group, neither
+bool block_groups_ok(const mm_block_problem& p, const int32_t* offsets, const int32_t* counts) {
+  return aligned(offsets, 4) && aligned(counts, 4) && !offsets == !counts && (offsets || p.num_groups == 1);
+}
+
+BlockArgs block_args(const mm_block_problem& p, const void* b, const float* b_scale, const int32_t* offsets,
+                     const int32_t* counts, void* y) {
+  BlockArgs g{};
+  g.b = static_cast<const uint8_t*>(b);
+  g.bs = b_scale;
+  g.offsets = offsets;
+  g.counts = counts;
+  g.y = y;
+  g.M = p.rows;
+  g.N = (int)p.out_features;
+  g.K = (int)p.in_features;
+  g.G = (int)p.num_groups;
+  return g;
+}
+
 // ---------------------------------------------------------------- static scratch
 // The workspace of mega_moe_noalloc: a device array of the library itself,
 // one copy per GPU, held until the process ends.  Host code never passes
@@ -914,24 +934,11 @@ mm_status mm_block_gemm(const mm_block_plan* plan, const void* a, const float* a
                         const float* b_scale, const int32_t* group_offsets, const int32_t* group_counts, void* y,
                         void* stream) {
   MM_TRY(check_plan(plan));
-  const mm_block_problem& p = plan->prob;
   if (!ok16(a) || !ok4(a_scale) || !ok16(b) || !ok4(b_scale) || !ok16(y)) return MM_ERR_INVALID_ARG;
-  // both group arrays or, for one group, neither
-  if (!aligned(group_offsets, 4) || !aligned(group_counts, 4) || !group_offsets != !group_counts ||
-      (!group_offsets && p.num_groups != 1))
-    return MM_ERR_INVALID_ARG;
-  BlockArgs g{};
+  if (!block_groups_ok(plan->prob, group_offsets, group_counts)) return MM_ERR_INVALID_ARG;
+  BlockArgs g = block_args(plan->prob, b, b_scale, group_offsets, group_counts, y);
   g.a = static_cast<const uint8_t*>(a);
   g.as = a_scale;
-  g.b = static_cast<const uint8_t*>(b);
-  g.bs = b_scale;
-  g.offsets = group_offsets;
-  g.counts = group_counts;
-  g.y = y;
-  g.M = p.rows;
-  g.N = (int)p.out_features;
-  g.K = (int)p.in_features;
-  g.G = (int)p.num_groups;
   hipStream_t s = static_cast<hipStream_t>(stream);
   return run(MM_K_BLOCK_GEMM, s, [&] { return launch_block_gemm(g, num_cus(), s); });
 }
@@ -942,14 +949,20 @@ mm_status mm_block_linear(const mm_block_plan* plan, const void* x, const void* 
   MM_TRY(check_plan(plan));
   const mm_block_problem& p = plan->prob;
   if (!ok16(x) || !ok16(b) || !ok4(b_scale) || !ok16(y) || !ok16(workspace)) return MM_ERR_INVALID_ARG;
-  if (!aligned(group_offsets, 4) || !aligned(group_counts, 4) || !group_offsets != !group_counts ||
-      (!group_offsets && p.num_groups != 1))
-    return MM_ERR_INVALID_ARG;
+  if (!block_groups_ok(p, group_offsets, group_counts)) return MM_ERR_INVALID_ARG;
   if ((int64_t)workspace_bytes < plan->workspace_bytes) return MM_ERR_WORKSPACE;
-  uint8_t* codes = at<uint8_t>(workspace, 0);
-  float* scales = at<float>(workspace, align_up(p.rows * p.in_features, kAlign));
-  MM_TRY(mm_block_quantize(p.rows, p.in_features, x, codes, scales, stream));
-  return mm_block_gemm(plan, codes, scales, b, b_scale, group_offsets, group_counts, y, stream);
+  BlockArgs g = block_args(p, b, b_scale, group_offsets, group_counts, y);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (block_from_x(g)) {
+    g.x = x;
+  } else {
+    uint8_t* codes = at<uint8_t>(workspace, 0);
+    float* scales = at<float>(workspace, align_up(p.rows * p.in_features, kAlign));
+    MM_TRY(mm_block_quantize(p.rows, p.in_features, x, codes, scales, stream));
+    g.a = codes;
+    g.as = scales;
+  }
+  return run(MM_K_BLOCK_GEMM, s, [&] { return launch_block_gemm(g, num_cus(), s); });
 }
 
 mm_status mm_trace_enable(int on) {

@@ -64,9 +64,12 @@ struct BlockArgs {
   const int32_t* counts;     // [G] rows of each group
   void* y;                   // bf16 [M][N]
   int64_t M;
+  int64_t m_first;           // first row of the streaming units (rows before it: the large tiles)
   int N, K, G;
 };
 hipError_t launch_block_quantize(const void* x, int64_t rows, int cols, uint8_t* q, float* s, hipStream_t st);
+// whether launch_block_gemm quantises a.x on the way (a.a and a.as unused)
+bool block_from_x(const BlockArgs& a);
 hipError_t launch_block_gemm(const BlockArgs& a, int num_cus, hipStream_t s);
 
 }  // namespace mm
