@@ -8,6 +8,8 @@
 //
 // Each group of 128 K-values is one 16 x 16 x 128 MFMA per 16 x 16 outputs,
 // started from zero; its float32 result is scaled into float32 accumulators.
+#include <type_traits>
+
 #include "mm_device.hpp"
 #include "mm_ops_internal.hpp"
 
@@ -92,8 +94,10 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr int kThreads = 512, kWaves = 8;
 constexpr int kBM = 256, kBN = 256;       // the large tile
+constexpr int kMidBM = 128, kMidBN = 64;  // the small tile
 constexpr int kFewRows = 64;              // most rows of a streaming unit
 constexpr int kFewCols = 16;
+constexpr int kGroupM = 6;                // M-blocks that a run of tiles goes through before the next N-block
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -113,19 +117,22 @@ __device__ __forceinline__ void group_rows(const BlockArgs& a, int gi, int64_t& 
 // How the rows of a group are cut: into blocks of 256 rows, a rest of up to
 // 128 rows being a half block (half the products), listed after the full
 // ones.  kFew: every row in streaming units of up to 64 rows (small groups).
-enum Class : int { kFull = 0, kHalf = 1, kFew = 2 };
+// kMid: blocks of 128 rows and 64 columns.
+enum Class : int { kFull = 0, kHalf = 1, kFew = 2, kMid = 3 };
 
 // M-blocks of class c in a group of n rows
 __device__ __forceinline__ int64_t blocks_of(int c, int64_t n) {
   const int rest = (int)(n % kBM);
   if (c == kFew) return (n + kFewRows - 1) / kFewRows;
+  if (c == kMid) return (n + kMidBM - 1) / kMidBM;
   if (c == kHalf) return rest > 0 && rest <= kBM / 2 ? 1 : 0;
   return n / kBM + (rest > kBM / 2 ? 1 : 0);
 }
 __device__ __forceinline__ int64_t first_block_row(int c, int64_t n, int64_t mb) {
-  return c == kFull ? mb * kBM : c == kFew ? mb * kFewRows : n / kBM * kBM;
+  return c == kFull ? mb * kBM : c == kFew ? mb * kFewRows : c == kMid ? mb * kMidBM : n / kBM * kBM;
 }
-__device__ __forceinline__ int cols_of(int c) { return c == kFew ? kFewCols : kBN; }
+__device__ __forceinline__ int cols_of(int c) { return c == kFew ? kFewCols : c == kMid ? kMidBN : kBN; }
+__device__ __forceinline__ int most_rows(int c) { return c == kFew ? kFewRows : c == kMid ? kMidBM : kBM; }
 
 // M-blocks of class c over all groups (every lane of the wave takes part)
 __device__ int64_t count_blocks(const BlockArgs& a, int c) {
@@ -149,7 +156,10 @@ __device__ __forceinline__ TileAt uniform_tile(const TileAt& t) {
   return TileAt{(int64_t)(uint32_t)uniform((int)t.m0), uniform(t.rows), uniform(t.group), uniform(t.n0)};
 }
 
-// Tile `at` of class c in the order (group, N-block, M-block: M fastest).
+// Tile `at` of class c in the order (group, 6 M-blocks, N-block, M-block): the
+// 32 tiles of an XCD then read 6 row panels and 5 or 6 weight panels.  A CU's
+// requests wait 500 cycles on average, and how many find L2 decides the rate:
+// 16384 x 4096 x 7168 takes 424 us (504 with all M-blocks first, 437 with 4).
 __device__ bool find_tile(const BlockArgs& a, int c, int64_t at, TileAt& o) {
   const int bn = cols_of(c), nb = (a.N + bn - 1) / bn;
   int l = lane_id();
@@ -169,10 +179,12 @@ __device__ bool find_tile(const BlockArgs& a, int c, int64_t at, TileAt& o) {
       const int src = __ffsll((unsigned long long)ballot(at < pre)) - 1;
       const int64_t first = __shfl(pre - mine, src, 64), rows = __shfl(n, src, 64), row0 = __shfl(lo, src, 64);
       const int64_t mb = blocks_of(c, rows), k = at - first;
-      const int64_t m = first_block_row(c, rows, k % mb);
-      const int64_t most = c == kFew ? kFewRows : kBM;
+      const int64_t chunk = k / (kGroupM * nb), m0 = chunk * kGroupM, in = k - m0 * nb;
+      const int64_t gm = mb - m0 < kGroupM ? mb - m0 : kGroupM;
+      const int64_t m = first_block_row(c, rows, m0 + in % gm);
+      const int64_t most = most_rows(c);
       o.group = g0 + src;
-      o.n0 = (int)(k / mb) * bn;
+      o.n0 = (int)(in / gm) * bn;
       o.m0 = row0 + m;
       o.rows = (int)(rows - m < most ? rows - m : most);
       return true;
@@ -187,40 +199,41 @@ __device__ bool find_tile(const BlockArgs& a, int c, int64_t at, TileAt& o) {
 // stages filled by LDS-DMA.  Weights are the MFMA's A operand, so a lane's
 // four accumulators are four columns of one row: its scale is one number per
 // row tile, and its result one 8-byte store.
-// Bound: the MFMA at the clock the chip holds under it.  A stage of the full
-// tile takes 1.65 us against 1.61 us at the rate that a large e4m3 library
-// product reaches here (2.67 PFLOP/s); without the products the copies and
-// LDS reads alone take 90% of it.
-template <int MT>
+// Bound: the copies.  Products alone take 1.03 us a stage, copies that always
+// hit the same lines 1.0 us, the real ones 1.65 us: 64 KiB a stage with a
+// mean latency of 500 cycles.  16384 x 4096 x 7168 runs at 2.27 PFLOP/s; a
+// large e4m3 library product reaches 2.67 here.
+template <int WN, int NT, int MT, int SR>
 __device__ __forceinline__ void mma_tile(const BlockArgs& a, const TileAt& at, uint8_t* sa0, uint8_t* sa1, uint8_t* sb0,
-                                         uint8_t* sb1, float (*ssc)[2][kBM]) {
-  constexpr int WM = 4, NT = 8;
+                                         uint8_t* sb1, float (*ssc)[2][SR]) {
+  constexpr int WM = kWaves / WN, BM = 16 * MT * WM, BN = 16 * NT * WN;
+  static_assert(BM <= SR && BM % 64 == 0 && BN % 64 == 0 && (kBlock % (16 * NT) == 0), "whole copies, one weight scale a wave");
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));   // nothing derived from it is kept across tiles: the registers are full
   const TileAt t = uniform_tile(at);
   const int w = uniform(tid / 64), l = tid % 64, r = l % 16, g = l / 16;
   const int wm = w % WM, wn = w / WM, KB = a.K / kBlock;
-  const int rows = t.rows, cols = a.N - t.n0 < kBN ? a.N - t.n0 : kBN;
+  const int rows = t.rows, cols = a.N - t.n0 < BN ? a.N - t.n0 : BN;
   // one instruction moves 8 rows of 128 bytes, lane i to byte 16 * i; the
   // chunk at place p of row x is p ^ (x / 2 % 8), so that 16 rows read at one
   // chunk hit 16 different bank groups.  Rows past the last one are beyond the
   // descriptor and arrive as zeros without a memory access.
   const uint32_t voff = (uint32_t)(l / 8) * a.K + (((l % 8) ^ ((4 * (w % 2) + l / 16) % 8)) * 16);
   const uint8_t *ab = a.a + t.m0 * a.K, *bb = a.b + ((int64_t)t.group * a.N + t.n0) * a.K;
-  auto copy = [&](int kb, uint8_t* sa, uint8_t* sb) {
-    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)ab, (short)0, rows * a.K, 0x00020000);
-    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)bb, (short)0, cols * a.K, 0x00020000);
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(sa + (w + 8 * i) * 1024), 16, voff, (w + 8 * i) * 8 * a.K + kb * kBlock, 0, 0);
-#pragma unroll
-    for (int i = 0; i < kBN / 64; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(sb + (w + 8 * i) * 1024), 16, voff, (w + 8 * i) * 8 * a.K + kb * kBlock, 0, 0);
+  constexpr int kCopies = (BM + BN) / 64;   // instructions of a wave and stage
+  auto copy = [&](int i, int kb, uint8_t* sa, uint8_t* sb) {
+    const bool of_a = i < BM / 64;
+    const int grp = w + 8 * (of_a ? i : i - BM / 64);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)(of_a ? ab : bb), (short)0, (of_a ? rows : cols) * a.K, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)((of_a ? sa : sb) + grp * 1024), 16, voff, grp * 8 * a.K + kb * kBlock, 0, 0);
   };
   const int nb = (t.n0 + wn * NT * 16) / kBlock, nblocks = (a.N + kBlock - 1) / kBlock;
   const float* bsp = a.bs + ((int64_t)t.group * nblocks + (nb < nblocks ? nb : nblocks - 1)) * KB;
   const int sw = (r / 2) % 8;
-  const int c0 = ((2 * g) ^ sw) * 16 + r * kBlock, c1 = ((2 * g + 1) ^ sw) * 16 + r * kBlock;
+  // a lane group takes chunks g and g + 4 of both operands: each read then
+  // covers four neighbouring chunks (2g and 2g + 1 met in the same banks:
+  // half of the LDS cycles were conflicts)
+  const int c0 = (g ^ sw) * 16 + r * kBlock, c1 = ((g + 4) ^ sw) * 16 + r * kBlock;
   // Row scales of two stages at a time through LDS, one a thread: a wave's own
   // gather of its 64 rows' scales, each in a line of its own, cost a fifth of
   // the time (780 against 612 us without them at 16384 x 4096 x 7168).
@@ -232,13 +245,19 @@ __device__ __forceinline__ void mma_tile(const BlockArgs& a, const TileAt& at, u
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)asb, (short)0, rows * KB * 4, 0x00020000);
     return __builtin_amdgcn_raw_buffer_load_b32(rs, (srow * KB + tid % 2) * 4, kb * 4, 0);
   };
-  auto keep = [&](int pair, uint32_t v) { ssc[pair % 2][tid % 2][srow] = __uint_as_float(v); };
+  auto keep = [&](int pair, uint32_t v) {
+    if (srow < SR) ssc[pair % 2][tid % 2][srow] = __uint_as_float(v);
+  };
   f32x4 acc[NT][MT];
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  auto compute = [&](const uint8_t* sa, const uint8_t* sb, const float* ss, float scb) {
+  // The copies of stage kn go out a few at a time between the products: all
+  // at once they hold up each wave's issue until the address unit has taken
+  // them, and copies and products add up.
+  auto compute = [&](auto more, const uint8_t* sa, const uint8_t* sb, const float* ss, float scb, int kn, uint8_t* na, uint8_t* nbuf) {
+    constexpr int per = decltype(more)::value ? (kCopies + NT - 1) / NT : 0;
     u32x4 af[MT][2], b[2][2];
     float sc[MT];
     f32x4 sum[2][MT];
@@ -261,6 +280,9 @@ __device__ __forceinline__ void mma_tile(const BlockArgs& a, const TileAt& at, u
       if (j + 1 < NT) weights(j + 1);
       if (j < NT) {
 #pragma unroll
+        for (int q = 0; q < per; ++q)
+          if (j * per + q < kCopies) copy(j * per + q, kn, na, nbuf);
+#pragma unroll
         for (int i = 0; i < MT; ++i) sum[j % 2][i] = mfma128(b[j % 2][0], b[j % 2][1], af[i][0], af[i][1]);
       }
       if (j > 0) {
@@ -269,6 +291,7 @@ __device__ __forceinline__ void mma_tile(const BlockArgs& a, const TileAt& at, u
       }
       if (j > 0 && j < NT) {
         if (j + 1 < NT) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        if (j * per < kCopies && per > 0) __builtin_amdgcn_sched_group_barrier(0x010, per, 0);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
@@ -291,7 +314,8 @@ __device__ __forceinline__ void mma_tile(const BlockArgs& a, const TileAt& at, u
   };
   {
     const uint32_t v = ask(0);
-    copy(0, sa0, sb0);
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) copy(i, 0, sa0, sb0);
     keep(0, v);
   }
   float scb = bsp[0];
@@ -303,18 +327,16 @@ __device__ __forceinline__ void mma_tile(const BlockArgs& a, const TileAt& at, u
     const uint32_t v = ask(kb + 2);
     const float scb1 = bsp[kb + 1];
     __builtin_amdgcn_sched_barrier(0);
-    copy(kb + 1, sa1, sb1);
-    compute(sa0, sb0, ssc[pair % 2][0], scb);
+    compute(std::true_type{}, sa0, sb0, ssc[pair % 2][0], scb, kb + 1, sa1, sb1);
     turn();
     const int nx = kb + 2 < KB ? kb + 2 : KB - 1;   // past the end: the last stage again, unused
     scb = bsp[nx];
     __builtin_amdgcn_sched_barrier(0);
-    copy(nx, sa0, sb0);
     keep(pair + 1, v);
-    compute(sa1, sb1, ssc[pair % 2][1], scb1);
+    compute(std::true_type{}, sa1, sb1, ssc[pair % 2][1], scb1, nx, sa0, sb0);
     turn();
   }
-  if (kb < KB) compute(sa0, sb0, ssc[pair % 2][0], scb);
+  if (kb < KB) compute(std::false_type{}, sa0, sb0, ssc[pair % 2][0], scb, 0, sa1, sb1);
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -471,11 +493,26 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     TileAt t;
     if (k < n[0]) {
       if (!find_tile(a, kFull, first[0] + k, t)) break;
-      mma_tile<4>(a, t, sa0, sa1, sb0, sb1, ssc);
+      mma_tile<2, 8, 4>(a, t, sa0, sa1, sb0, sb1, ssc);
     } else {
       if (!find_tile(a, kHalf, first[1] + k - n[0], t)) break;
-      mma_tile<2>(a, t, sa0, sa1, sb0, sb1, ssc);
+      mma_tile<2, 8, 2>(a, t, sa0, sa1, sb0, sb1, ssc);
     }
+  }
+}
+
+// Products whose large tiles would leave most CUs without one: small tiles,
+// three workgroups a CU.
+__global__ __launch_bounds__(kThreads) void k_block_mid(BlockArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t sa0[kMidBM * kBlock], sa1[kMidBM * kBlock], sb0[kMidBN * kBlock], sb1[kMidBN * kBlock];
+  __shared__ float ssc[2][2][kMidBM];
+  const int x = blockIdx.x % 8, step = gridDim.x / 8;
+  const int64_t total = count_blocks(a, kMid) * ((a.N + kMidBN - 1) / kMidBN);
+  const int64_t first = total * x / 8, n = total * (x + 1) / 8 - first;
+  for (int64_t k = blockIdx.x / 8; k < n; k += step) {
+    TileAt t;
+    if (!find_tile(a, kMid, first + k, t)) break;
+    mma_tile<2, 2, 2>(a, t, sa0, sa1, sb0, sb1, ssc);
   }
 }
 
@@ -510,7 +547,13 @@ hipError_t launch_block_gemm(const BlockArgs& args, int num_cus, hipStream_t s) 
   const int64_t rest = a.offsets == nullptr ? a.M % kBM : 0;
   if (rest == 0 || rest > kFewRows || a.M > rest) {
     if (rest > 0 && rest <= kFewRows) a.M -= rest;
-    hipLaunchKernelGGL(k_block_mma, dim3((unsigned)((num_cus + 7) / 8 * 8)), dim3(kThreads), 0, s, a);
+    // Measured at 4096 x 7168, us with large / small tiles: 128 rows 60 / 36,
+    // 512 rows 96 / 39, 1024 rows (64 large tiles) 97 / 51, 2048 rows (128
+    // tiles) 97 / 104; 32 groups of 128 rows (512 half tiles) 299 / 428.
+    const int64_t tiles = ((a.M / a.G + kBM - 1) / kBM) * a.G * ((a.N + kBN - 1) / kBN);
+    const unsigned cus = (unsigned)((num_cus + 7) / 8 * 8);
+    if (tiles < 112) hipLaunchKernelGGL(k_block_mid, dim3(3 * cus), dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL(k_block_mma, dim3(cus), dim3(kThreads), 0, s, a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || a.M == args.M) return err;
     a.m_first = a.M;

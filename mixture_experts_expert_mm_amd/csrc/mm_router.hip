@@ -15,8 +15,7 @@
 // expert, and where the best and another expert are closer than their
 // bounds, both are summed again in 64 bits.  A few in a hundred tokens need
 // it, for two experts each.
-#include "mm_device.hpp"
-#include "mm_ops_internal.hpp"
+#include "mm_router_dev.hpp"
 
 namespace mm {
 
@@ -34,8 +33,10 @@ __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, f32x4 c)
 
 __device__ __forceinline__ float sumsq(const u32x4& v, float acc) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    acc = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, v[i]), __builtin_bit_cast(bf16x2, v[i]), acc, false);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = v[i];     // a value: the cast of a vector's element takes the vector's first
+    acc = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, u), __builtin_bit_cast(bf16x2, u), acc, false);
+  }
   return acc;
 }
 
@@ -78,7 +79,7 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
     for (int j = 0; j < ET; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const bool do_x = blockIdx.y == 0 && ew == 0, do_w = blockIdx.x == 0;
   const int steps = a.H / kRouterStep, q = (int)blockIdx.z * KW + kw, Q = KW * a.KS;
-#pragma unroll 2
+#pragma unroll TT == 1 ? 4 : 2
   for (int s = q; s < steps; s += Q) {
     u32x4 xv[TT][2], wv[ET][2];
 #pragma unroll
@@ -164,222 +165,208 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
   }
 }
 
-// x_t . w_e in 64 bits by one wave (every lane gets the sum)
-__device__ double router_dot64(const RouterArgs& a, int64_t t, int e) {
-  const uint8_t* x = static_cast<const uint8_t*>(a.x) + t * a.H * 2;
-  const uint8_t* w = static_cast<const uint8_t*>(a.w) + (int64_t)e * a.H * 2;
-  double s = 0.0;
-  for (int k = lane_id() * 8; k < a.H; k += 512) {
-    const u32x4 xv = *reinterpret_cast<const u32x4*>(x + k * 2), wv = *reinterpret_cast<const u32x4*>(w + k * 2);
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+constexpr int kTileT = 128, kTileE = 256;
+
+// The same for many tokens and experts: 128 tokens x 256 experts a workgroup
+// (8 waves of 64 x 64), stages of 64 hidden values in three LDS slots filled
+// by LDS-DMA two stages ahead.  Bound: reading the tokens from HBM; at 16384
+// tokens and 256 experts two slices of the hidden dimension give every CU
+// one workgroup, and Wr is read from L2 128 times instead of 256.
+__global__ __launch_bounds__(kThreads) void k_router_tile(RouterArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t x0[kTileT * 128], x1[kTileT * 128], x2[kTileT * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t w0[kTileE * 128], w1[kTileE * 128], w2[kTileE * 128];
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid / 64), l = tid % 64, r = l % 16, g = l / 16;
+  const int wt = w % 2, we = w / 2;              // wave's 64 tokens and 64 experts
+  // workgroup b runs on XCD b % 8: an XCD keeps to one slice of the hidden
+  // dimension, so that slice of Wr stays in its L2
+  const int per = 8 / a.KS, z = (int)(blockIdx.x % 8) / per;
+  const int64_t tile = (int64_t)(blockIdx.x / 8) * per + blockIdx.x % per;
+  const int64_t t0 = tile * kTileT;
+  if (t0 >= a.T) return;
+  const int e0 = (int)blockIdx.y * kTileE;
+  const int rows = (int)(a.T - t0 < kTileT ? a.T - t0 : kTileT), cols = a.E - e0 < kTileE ? a.E - e0 : kTileE;
+  const int steps = a.H / 64, s0 = steps * z / a.KS, s1 = steps * (z + 1) / a.KS;
+  const int pitch = a.H * 2;
+  // one instruction moves 8 rows of 128 bytes; the chunk at place p of row y is p ^ (y / 2 % 8)
+  const uint32_t voff = (uint32_t)(l / 8) * pitch + (((l % 8) ^ ((4 * (w % 2) + l / 16) % 8)) * 16);
+  const uint8_t *xb = static_cast<const uint8_t*>(a.x) + t0 * pitch, *wb = static_cast<const uint8_t*>(a.w) + (int64_t)e0 * pitch;
+  auto copy = [&](int s, uint8_t* xs, uint8_t* ws) {
+    const int at = (s < s1 ? s : s1 - 1) * 128;  // past the end: the last stage again, unused
+    const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc((void*)xb, (short)0, rows * pitch, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc((void*)wb, (short)0, cols * pitch, 0x00020000);
+#pragma unroll
+    for (int i = 0; i < kTileT / 64; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr_t)(xs + (w + 8 * i) * 1024), 16, voff, (w + 8 * i) * 8 * pitch + at, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kTileE / 64; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr_t)(ws + (w + 8 * i) * 1024), 16, voff, (w + 8 * i) * 8 * pitch + at, 0, 0);
+  };
+  constexpr int kCopies = (kTileT + kTileE) / 64;
+  static_assert(kCopies == 6, "the wait below leaves one stage of copies in flight");
+  f32x4 acc[4][4];                               // [expert tile][token tile]
+  float xs2[4], ws2[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    xs2[i] = ws2[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const bool do_x = blockIdx.y == 0 && we == 0, do_w = tile == 0 && wt == 0;
+  const int sw = (r / 2) % 8;
+  auto compute = [&](const uint8_t* xs, const uint8_t* ws) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = ((4 * h + g) ^ sw) * 16 + r * 128;
+      u32x4 xf[4], wf[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xf[i] = *reinterpret_cast<const u32x4*>(xs + (wt * 4 + i) * 2048 + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wf[i] = *reinterpret_cast<const u32x4*>(ws + (we * 4 + i) * 2048 + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = mfma16(wf[i], xf[j], acc[i][j]);
+      if (do_x) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xs2[j] = sumsq(xf[j], xs2[j]);
+      }
+      if (do_w) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ws2[i] = sumsq(wf[i], ws2[i]);
+      }
+    }
+  };
+  auto turn = [&]() {
+    // the stage's products stay before the wait: nothing else ties them to it
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[i][j]));
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0x0F76);          // vmcnt(6): all copies but the newest stage's
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  copy(s0, x0, w0);
+  copy(s0 + 1, x1, w1);
+  turn();
+  for (int s = s0; s < s1; s += 3) {
+    copy(s + 2, x2, w2);
+    compute(x0, w0);
+    turn();
+    if (s + 1 >= s1) break;
+    copy(s + 3, x0, w0);
+    compute(x1, w1);
+    turn();
+    if (s + 2 >= s1) break;
+    copy(s + 4, x1, w1);
+    compute(x2, w2);
+    turn();
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);            // no copy outlives the workgroup
+  float* part = a.part + (int64_t)z * a.T * a.Ep;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int t = (wt * 4 + j) * 16 + r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // bf16 x bf16 is exact in float32's exponent range or beyond it: multiply in 64 bits
-      s += (double)bf16_bits_to_f32(xv[i] & 0xffffu) * (double)bf16_bits_to_f32(wv[i] & 0xffffu);
-      s += (double)__uint_as_float(xv[i] & 0xffff0000u) * (double)__uint_as_float(wv[i] & 0xffff0000u);
+      const int e = e0 + (we * 4 + i) * 16 + 4 * g;
+      if (t < rows && e < a.Ep) *reinterpret_cast<f32x4*>(part + (t0 + t) * a.Ep + e) = acc[i][j];
     }
   }
+  if (do_x) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
-  return s;
+    for (int j = 0; j < 4; ++j) {
+      float v = xs2[j];
+      v += __shfl_xor(v, 16, 64);
+      v += __shfl_xor(v, 32, 64);
+      const int t = (wt * 4 + j) * 16 + r;
+      if (g == 0 && t < rows) a.xnorm[(int64_t)z * a.T + t0 + t] = v;
+    }
+  }
+  if (do_w) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v = ws2[i];
+      v += __shfl_xor(v, 16, 64);
+      v += __shfl_xor(v, 32, 64);
+      const int e = e0 + (we * 4 + i) * 16 + r;
+      if (g == 0 && e < a.Ep) a.wnorm[(int64_t)z * a.Ep + e] = v;
+    }
+  }
 }
 
-// One wave per token; lane l holds experts l, l + 64, ...  Keys are doubles:
-// the selection value of each expert, NaN below every number, -inf taken out.
+// One wave per token.
 template <int NV>
-__global__ __launch_bounds__(256) void k_router_select(RouterArgs a) {
+__global__ __launch_bounds__(256, NV <= 4 ? 4 : 1) void k_router_select(RouterArgs a) {
   const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
   if (t >= a.T) return;
-  const int l = threadIdx.x % 64;
-  int my_id = -1;
-  double my_z = 0.0;          // lane k: score argument z of the k-th selection
-  double zmax = -__builtin_huge_val();
-  float zsum = 0.0f;
-  if (a.active == nullptr || a.active[t] != 0) {
-    const bool sig = a.scoring == MM_ROUTER_SIGMOID;
-    float xx = 0.0f;
-    for (int z = 0; z < a.KS; ++z) xx += a.xnorm[(int64_t)z * a.T + t];
-    const int steps = a.H / 32 + a.KS + kWaves;
-    const float unit = 1.1920929e-7f * sqrtf((float)steps) * sqrtf(xx);
-    double z[NV], key[NV];
-    float err[NV];
-    uint32_t live = 0;
-    auto key_of = [&](double zz, float b) -> double {
-      if (!sig || a.bias == nullptr) return zz;
-      return 1.0 / (1.0 + exp(-zz)) + (double)b;
-    };
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int e = l + 64 * v;
-      z[v] = 0.0, key[v] = 0.0, err[v] = 0.0f;
-      if (e < a.E) {
-        float s = 0.0f, ww = 0.0f;
-        for (int k = 0; k < a.KS; ++k) {
-          s += a.part[((int64_t)k * a.T + t) * a.Ep + e];
-          ww += a.wnorm[(int64_t)k * a.Ep + e];
-        }
-        const float b = a.bias ? a.bias[e] : 0.0f;
-        float d = unit * sqrtf(ww) + 1e-36f;
-        z[v] = sig ? (double)s : (double)s + (double)b;
-        if (sig && a.bias) {
-          // float32 sigmoid: its own rounding, and the slope of at most 1/4
-          key[v] = (double)(1.0f / (1.0f + expf(-s))) + (double)b;
-          d = 0.25f * d + 2.4e-7f;
-        } else {
-          key[v] = z[v];
-        }
-        if (!(fabs(key[v]) <= 3.0e38) && d < __builtin_huge_valf()) {
-          // +-inf or NaN: exact unless the float32 sum overflowed
-          if (xx < 1e36f && ww < 1e36f) d = 0.0f;
-        }
-        err[v] = d != d ? 0.0f : d;
-        if (key[v] != -__builtin_huge_val() || err[v] > 0.0f) live |= 1u << v;
-        if (b == -__builtin_huge_valf()) live &= ~(1u << v), err[v] = 0.0f;
-      }
-      if (key[v] != key[v]) key[v] = -1.7976931348623157e308;
-    }
-    for (int k = 0; k < a.K; ++k) {
-      double best = 0.0;
-      int be = -1;
-      for (;;) {
-        // the largest key, ties to the lowest expert
-        best = -__builtin_huge_val();
-        be = 1 << 30;
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-          if ((live >> v & 1u) && (key[v] > best || be == 1 << 30)) best = key[v], be = l + 64 * v;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-          const double ob = __shfl_xor(best, o, 64);
-          const int oe = __shfl_xor(be, o, 64);
-          if (oe < (1 << 30) && (be == 1 << 30 || ob > best || (ob == best && oe < be))) best = ob, be = oe;
-        }
-        if (be == 1 << 30) break;
-        float bd = 0.0f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-          if (be == l + 64 * v) bd = err[v];
-        bd = __shfl(bd, be % 64, 64);
-        bool again = false;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int e = l + 64 * v;
-          // contested: not surely below the best (inf - inf compares false)
-          const bool c = (live >> v & 1u) && e != be && (err[v] > 0.0f || bd > 0.0f) &&
-                         !(key[v] + (double)err[v] < best - (double)bd);
-          const uint64_t any = ballot(c);
-          if (any != 0) again = true;
-          uint64_t todo = ballot(c && err[v] > 0.0f);
-          while (todo != 0) {
-            const int src = __ffsll((unsigned long long)todo) - 1;
-            todo &= todo - 1;
-            const int ce = src + 64 * v;
-            const double dz = router_dot64(a, t, ce);
-            if (l == src) {
-              const float b = a.bias ? a.bias[ce] : 0.0f;
-              z[v] = sig ? dz : dz + (double)b;
-              key[v] = key_of(z[v], b);
-              if (key[v] == -__builtin_huge_val()) live &= ~(1u << v);
-              if (key[v] != key[v]) key[v] = -1.7976931348623157e308;
-              err[v] = 0.0f;
-            }
-          }
-        }
-        if (!again) {
-          if (bd > 0.0f && !(fabs(best) <= 3.0e38)) again = true;   // overflowed in float32, alone at the top
-          else break;
-        }
-        if (bd > 0.0f) {
-          const double dz = router_dot64(a, t, be);
-#pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            if (be == l + 64 * v) {
-              const float b = a.bias ? a.bias[be] : 0.0f;
-              z[v] = sig ? dz : dz + (double)b;
-              key[v] = key_of(z[v], b);
-              if (key[v] == -__builtin_huge_val()) live &= ~(1u << v);
-              if (key[v] != key[v]) key[v] = -1.7976931348623157e308;
-              err[v] = 0.0f;
-            }
-          }
-        }
-      }
-      if (be == 1 << 30) break;
-      double zb = 0.0;
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (be == l + 64 * v) zb = z[v], live &= ~(1u << v);
-      zb = __shfl(zb, be % 64, 64);
-      if (l == k) my_id = be, my_z = zb;
-    }
-    if (!sig) {
-      // softmax over every expert
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (l + 64 * v < a.E) zmax = z[v] > zmax || z[v] != z[v] ? z[v] : zmax;
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) {
-        const double w = __shfl_xor(zmax, o, 64);
-        zmax = w > zmax || w != w ? w : zmax;
-      }
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (l + 64 * v < a.E) zsum += expf((float)(z[v] - zmax));
-      zsum = wave_sum(zsum);
-    }
-  }
-  float wgt = 0.0f;
-  if (my_id >= 0)
-    wgt = a.scoring == MM_ROUTER_SIGMOID ? (float)(1.0 / (1.0 + exp(-my_z))) : expf((float)(my_z - zmax)) / zsum;
-  if (a.renormalize) {
-    float s = l < a.K ? wgt : 0.0f;
-    s = wave_sum(s);
-    wgt = wgt / (s + 1e-20f);
-  }
+  int id;
+  float w;
+  router_select_token<NV>(a, t, id, w);
+  const int l = lane_id();
   if (l < a.K) {
-    a.ids[t * a.K + l] = my_id;
-    a.weights[t * a.K + l] = wgt * a.scale;
+    a.ids[t * a.K + l] = id;
+    a.weights[t * a.K + l] = w;
   }
 }
 
-// Measured rules.  Up to 64 tokens the scores are a stream of Wr: 16 x 16
-// tiles over as many workgroups as the hidden dimension gives.  Beyond, a
-// wave holds 64 x 64 so that a token row is read once per 256 experts.
+// Up to 64 tokens the scores are a stream of Wr: 16 x 16 tiles over as many
+// workgroups as the hidden dimension gives.  Beyond, with up to 128 experts,
+// a wave holds 64 x 64 and the waves share the hidden dimension; with more, or
+// when ... the LDS tiles.
 RouterShape router_shape(int64_t T, int H, int E) {
   RouterShape s{};
   const int steps = H / kRouterStep;
   s.ep = (E + 15) / 16 * 16;
-  s.wide = T > 64;
-  if (!s.wide) {
+  s.wide = T <= 64 ? 0 : E <= 128 ? 1 : 2;
+  int64_t tiles = 1, most = steps / (kWaves * 4);
+  if (s.wide == 0) {
     s.ew = 1;
-    s.ks = steps / (kWaves * 4);
+    s.ks = (int)most;
   } else {
-    s.ew = E <= 64 ? 1 : E <= 128 ? 2 : 4;
-    const int64_t tiles = (T + 63) / 64 * ((E + 64 * s.ew - 1) / (64 * s.ew));
-    const int64_t want = 256 / tiles, most = steps / (2 * (kWaves / s.ew));
+    if (s.wide == 1) {
+      s.ew = E <= 64 ? 1 : 2;
+      tiles = (T + 63) / 64 * ((E + 64 * s.ew - 1) / (64 * s.ew));
+      most = steps / (2 * (kWaves / s.ew));
+    } else {
+      tiles = (T + kTileT - 1) / kTileT * ((E + kTileE - 1) / kTileE);
+      most = steps / 8;
+    }
+    const int64_t want = 256 / tiles;
     s.ks = (int)(want < most ? want : most);
   }
   s.ks = s.ks < 1 ? 1 : s.ks > 8 ? 8 : s.ks;
+  if (s.wide == 2) s.ks = s.ks >= 8 ? 8 : s.ks >= 4 ? 4 : s.ks >= 2 ? 2 : 1;   // whole XCDs to a slice
   return s;
 }
 
 hipError_t launch_router_scores(const RouterArgs& a, hipStream_t s) {
   const RouterShape sh = router_shape(a.T, a.H, a.E);
-  if (!sh.wide) {
+  if (sh.wide == 0) {
     const dim3 grid((unsigned)((a.T + 15) / 16), (unsigned)(a.Ep / 16), (unsigned)a.KS);
     hipLaunchKernelGGL((k_router_scores<1, 1, 1>), grid, dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+  }
+  if (sh.wide == 2) {
+    const int64_t tiles = (a.T + kTileT - 1) / kTileT, per = 8 / a.KS;
+    const dim3 grid((unsigned)((tiles + per - 1) / per * 8), (unsigned)((a.E + kTileE - 1) / kTileE));
+    hipLaunchKernelGGL(k_router_tile, grid, dim3(kThreads), 0, s, a);
     return hipGetLastError();
   }
   const int per = 64 * sh.ew;
   const dim3 grid((unsigned)((a.T + 63) / 64), (unsigned)((a.E + per - 1) / per), (unsigned)a.KS);
   if (sh.ew == 1) hipLaunchKernelGGL((k_router_scores<4, 4, 1>), grid, dim3(kThreads), 0, s, a);
-  else if (sh.ew == 2) hipLaunchKernelGGL((k_router_scores<4, 4, 2>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((k_router_scores<4, 4, 4>), grid, dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_router_scores<4, 4, 2>), grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_router_select(const RouterArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((a.T + 3) / 4));
   if (a.E <= 64) hipLaunchKernelGGL(k_router_select<1>, grid, dim3(256), 0, s, a);
+  else if (a.E <= 128) hipLaunchKernelGGL(k_router_select<2>, grid, dim3(256), 0, s, a);
   else if (a.E <= 256) hipLaunchKernelGGL(k_router_select<4>, grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL(k_router_select<16>, grid, dim3(256), 0, s, a);
   return hipGetLastError();

@@ -1,0 +1,315 @@
+// Selection of one token's experts from its partial scores, by one wave
+// (shared by the router's second kernel and the few-token layer).
+#pragma once
+#include "mm_device.hpp"
+#include "mm_ops_internal.hpp"
+
+namespace mm {
+
+// x_t . w_e in 64 bits by one wave (every lane gets the sum)
+__device__ __forceinline__ double router_dot64(const RouterArgs& a, int64_t t, int e) {
+  const uint8_t* x = static_cast<const uint8_t*>(a.x) + t * a.H * 2;
+  const uint8_t* w = static_cast<const uint8_t*>(a.w) + (int64_t)e * a.H * 2;
+  double s = 0.0;
+  constexpr int kAhead = 4;    // pieces of 512 values asked for at once: one wait of memory, not one each
+  for (int k0 = lane_id() * 8; k0 < a.H; k0 += 512 * kAhead) {
+    u32x4 xv[kAhead], wv[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = k0 + 512 * u < a.H ? k0 + 512 * u : k0;
+      xv[u] = *reinterpret_cast<const u32x4*>(x + k * 2);
+      wv[u] = *reinterpret_cast<const u32x4*>(w + k * 2);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (k0 + 512 * u < a.H) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s += (double)bf16_bits_to_f32(xv[u][i] & 0xffffu) * (double)bf16_bits_to_f32(wv[u][i] & 0xffffu);
+          s += (double)__uint_as_float(xv[u][i] & 0xffff0000u) * (double)__uint_as_float(wv[u][i] & 0xffff0000u);
+        }
+      }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+  return s;
+}
+
+// largest value of the wave: four shifts inside the rows of 16 lanes, two
+// broadcasts across them; lane 63 ends with it
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+#define MM_STEP(ctrl, rows)                                                                          \
+  {                                                                                                  \
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false);      \
+    v = o > v ? o : v;                                                                               \
+  }
+  MM_STEP(0x111, 0xf) MM_STEP(0x112, 0xf) MM_STEP(0x114, 0xf) MM_STEP(0x118, 0xf) MM_STEP(0x142, 0xa) MM_STEP(0x143, 0xc)
+#undef MM_STEP
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// floats as integers of the same order; NaN is 1, below every number, and 0
+// is an expert that cannot be taken
+__device__ __forceinline__ uint32_t rank_key(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return f != f ? 1u : u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float rank_value(uint32_t k) {
+  return k == 1u ? __builtin_nanf("") : __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// Lane l holds experts l, l + 64, ...; lane k returns the k-th expert and its
+// weight (-1 and 0 where none is left).  First the K + 1 largest float32
+// ranks are taken in turn; if each is above the next by more than both may be
+// off, their order is that of the 64-bit ranks.  If not (a few tokens in a
+// hundred), the token is selected again with a bound for each expert: where
+// another expert's reaches the best one's, both get their 64-bit sums, and
+// the set is compared in 64 bits.
+template <int NV>
+__device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t t, int& id, float& weight) {
+  const int l = lane_id();
+  id = -1;
+  weight = 0.0f;
+  if (a.active != nullptr && a.active[t] == 0) return;
+  const bool sig = a.scoring == MM_ROUTER_SIGMOID, biased = a.bias != nullptr;
+  constexpr int kMost = 8;     // most slices of the hidden dimension; all are asked for at once
+  float xp[kMost], sp[NV][kMost], wp[NV][kMost], bp[NV];
+#pragma unroll
+  for (int k = 0; k < kMost; ++k)
+    if (k == 0 || k < a.KS) xp[k] = a.xnorm[(int64_t)k * a.T + t];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int e = l + 64 * v < a.E ? l + 64 * v : 0;
+    bp[v] = biased ? a.bias[e] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k)
+      if (k == 0 || k < a.KS) {
+        sp[v][k] = a.part[((int64_t)k * a.T + t) * a.Ep + e];
+        wp[v][k] = a.wnorm[(int64_t)k * a.Ep + e];
+      }
+  }
+  float xx = xp[0];
+#pragma unroll
+  for (int k = 1; k < kMost; ++k)
+    if (k < a.KS) xx += xp[k];
+  float z[NV], err[NV];        // score argument; bound on the rank's error
+  uint32_t key[NV];
+  // Every step of a score's float32 sum rounds a partial sum, and the
+  // roundings are independent: sqrt(steps) * 2^-23 * the partial sums' size,
+  // which is |z| when the products add up and at most |x| |w| (taken at an
+  // eighth: only a sum that cancels down from there comes near it).  The
+  // errors seen are two hundred times smaller.
+  const float unit = 1.1920929e-7f * __builtin_amdgcn_sqrtf((float)(a.H / 32 + a.KS + 8)), xnorm = __builtin_amdgcn_sqrtf(xx);
+  float most = 0.0f;           // the largest bound of this lane
+  bool lost = false;           // some float32 sum left its range
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    z[v] = 0.0f, err[v] = 0.0f, key[v] = 0;
+    if (l + 64 * v >= a.E) continue;
+    float s = sp[v][0], ww = wp[v][0];
+#pragma unroll
+    for (int k = 1; k < kMost; ++k)
+      if (k < a.KS) s += sp[v][k], ww += wp[v][k];
+    const float b = bp[v];
+    float d = unit * (0.125f * __builtin_amdgcn_sqrtf(ww) * xnorm + fabsf(s)) + 1e-36f, rank;
+    if (sig) {
+      z[v] = s;
+      rank = s;
+      if (biased) {
+        // float32 sigmoid: a slope of at most 1/4, and its own rounding
+        rank = __builtin_amdgcn_rcpf(1.0f + __expf(-s)) + b;
+        d = 0.25f * d + 1e-6f;
+      }
+    } else {
+      z[v] = rank = s + b;
+    }
+    d += 2.4e-7f * fabsf(rank);
+    if (b == -__builtin_huge_valf()) continue;             // switched off
+    key[v] = rank_key(rank);
+    if (!(fabsf(rank) <= 3.0e38f) && !(xx < 1e36f && ww < 1e36f) && xx == xx && ww == ww) {
+      lost = true;
+      err[v] = __builtin_huge_valf();
+    } else {
+      err[v] = fabsf(rank) <= 3.0e38f ? d : 0.0f;
+      if (rank == -__builtin_huge_valf()) key[v] = 0;      // -inf: never taken
+    }
+    most = err[v] > most ? err[v] : most;
+  }
+  // bounds are not negative: their bits are in order
+  const float gap = 2.0f * __uint_as_float(wave_max_u32(__float_as_uint(most)));
+  // the expert at (bl, bv) leaves the ranking and becomes the k-th
+  uint32_t left[NV];
+  auto take = [&](int k, int bl, int bv) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (v == bv && l == bl) left[v] = 0;
+    if (l == k) id = bl + 64 * bv;
+  };
+  // the largest key left, 0 if none; (bl, bv): the lowest expert that has it
+  auto largest = [&](int& bl, int& bv) {
+    uint32_t m = left[0];
+#pragma unroll
+    for (int v = 1; v < NV; ++v) m = left[v] > m ? left[v] : m;
+    const uint32_t best = wave_max_u32(m);
+#pragma unroll
+    for (int v = NV - 1; v >= 0; --v) {
+      const uint64_t at = ballot(left[v] == best);
+      if (at != 0) bv = v, bl = __ffsll((unsigned long long)at) - 1;
+    }
+    return best;
+  };
+  bool sure = ballot(lost) == 0;
+  // the finite rank `best` after `before` is not surely below it
+  auto doubt = [&](uint32_t before, uint32_t best) {
+    return best > 1u && !(rank_value(before) - rank_value(best) > gap) && rank_value(best) - rank_value(best) == 0.0f;
+  };
+  uint32_t before = 0;
+  if constexpr (NV <= 4) {
+    // each lane's keys in descending order, equal ones by expert: a turn looks
+    // at the first one only (256 experts: 33 against 60 instructions a turn)
+    uint32_t at[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) left[v] = key[v], at[v] = (uint32_t)(l + 64 * v);
+#pragma unroll
+    for (int n = NV - 1; n > 0; --n)
+#pragma unroll
+      for (int v = 0; v < n; ++v) {
+        const bool swap = left[v + 1] > left[v];
+        const uint32_t hk = swap ? left[v + 1] : left[v], lk = swap ? left[v] : left[v + 1];
+        const uint32_t ha = swap ? at[v + 1] : at[v], la = swap ? at[v] : at[v + 1];
+        left[v] = hk, left[v + 1] = lk, at[v] = ha, at[v + 1] = la;
+      }
+    for (int k = 0; sure && k <= a.K; ++k) {
+      const uint32_t best = wave_max_u32(left[0]);
+      if (k > 0 && doubt(before, best)) sure = false;
+      if (best == 0 || k == a.K) break;
+      const uint64_t who = ballot(left[0] == best);
+      // equal infinite or NaN ranks of several lanes: by expert, below
+      if ((who & (who - 1)) != 0) sure = false;
+      const int bl = __ffsll((unsigned long long)who) - 1;
+      const int e = __builtin_amdgcn_readlane((int)at[0], bl);
+      if (l == k) id = e;
+      if (l == bl) {
+#pragma unroll
+        for (int v = 0; v + 1 < NV; ++v) left[v] = left[v + 1], at[v] = at[v + 1];
+        left[NV - 1] = 0;
+      }
+      before = best;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) left[v] = key[v];
+    for (int k = 0; sure && k <= a.K; ++k) {
+      int bl = 0, bv = 0;
+      const uint32_t best = largest(bl, bv);
+      if (k > 0 && doubt(before, best)) sure = false;
+      if (best == 0 || k == a.K) break;
+      take(k, bl, bv);
+      before = best;
+    }
+  }
+  if (!sure) {
+    double exact[NV];          // the 64-bit rank of an expert in `known`
+    uint32_t known = 0;
+    id = -1;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) left[v] = key[v], exact[v] = 0.0;
+    for (int k = 0; k < a.K; ++k) {
+      int bl = 0, bv = 0;
+      bool none = false;
+      for (;;) {
+        const uint32_t best = largest(bl, bv);
+        none = best == 0;
+        if (none) break;
+        float be = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (v == bv) be = err[v];
+        be = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(be), bl));
+        const float floor = rank_value(best) - be;
+        // experts whose bound reaches the best one's (the best one among them)
+        uint32_t near = 0;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (left[v] != 0 && (!(err[v] <= 3.0e38f) || (left[v] > 1u && rank_value(left[v]) + err[v] >= floor))) near |= 1u << v;
+        uint64_t others = 0;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const uint64_t n = ballot(near >> v & 1u);
+          others |= v == bv && err[v] <= 3.0e38f ? n & ~(1ull << bl) : n;
+        }
+        if (ballot(others != 0) == 0) break;
+        // their 64-bit ranks, each kept by its lane
+        bool grew = false;
+        for (int v = 0; v < NV; ++v)
+          for (uint64_t todo = ballot((near & ~known) >> v & 1u); todo != 0; todo &= todo - 1) {
+            const int src = __ffsll((unsigned long long)todo) - 1;
+            const double dz = router_dot64(a, t, src + 64 * v);
+            grew = true;
+            if (l == src) {
+              const double b = biased ? (double)a.bias[src + 64 * v] : 0.0;
+              const double zz = sig ? dz : dz + b, rank = sig && biased ? 1.0 / (1.0 + exp(-zz)) + b : zz;
+              float e = 2.4e-7f * fabsf((float)rank);
+              if (!(e <= 3.0e38f)) e = 0.0f;
+              const uint32_t kk = rank == -__builtin_huge_val() ? 0u : rank_key((float)rank);
+#pragma unroll
+              for (int u = 0; u < NV; ++u)
+                if (u == v) z[u] = (float)zz, exact[u] = rank, left[u] = kk, err[u] = e;
+              known |= 1u << v;
+            }
+          }
+        if (grew) continue;
+        // all known: the largest 64-bit rank, ties to the lowest expert
+        double top = -__builtin_huge_val();
+        int te = 1 << 30;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if ((near >> v & 1u) && (te == 1 << 30 || exact[v] > top)) top = exact[v], te = l + 64 * v;
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+          const double ot = __shfl_xor(top, o, 64);
+          const int oe = __shfl_xor(te, o, 64);
+          if (oe < (1 << 30) && (te == 1 << 30 || ot > top || (ot == top && oe < te))) top = ot, te = oe;
+        }
+        te = __builtin_amdgcn_readfirstlane(te);
+        bl = te % 64, bv = te / 64;
+        break;
+      }
+      if (none) break;
+      take(k, bl, bv);
+    }
+  }
+  // the selected experts' score arguments, from their lanes
+  float my_z = 0.0f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const float zz = __shfl(z[v], id & 63, 64);
+    if (id / 64 == v) my_z = zz;
+  }
+  if (sig) {
+    weight = id >= 0 ? 1.0f / (1.0f + expf(-my_z)) : 0.0f;
+  } else {
+    // softmax over every expert
+    float zmax = -__builtin_huge_valf(), zsum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (l + 64 * v < a.E) zmax = z[v] > zmax || z[v] != z[v] ? z[v] : zmax;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      const float w = __shfl_xor(zmax, o, 64);
+      zmax = w > zmax || w != w ? w : zmax;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (l + 64 * v < a.E) zsum += expf(z[v] - zmax);
+    zsum = wave_sum(zsum);
+    weight = id >= 0 ? expf(my_z - zmax) / zsum : 0.0f;
+  }
+  if (a.renormalize) {
+    const float s = wave_sum(weight);
+    weight = weight / (s + 1e-20f);
+  }
+  weight *= a.scale;
+}
+
+}  // namespace mm

@@ -92,6 +92,23 @@ def test_router_ties_and_near_ties(T, scoring, bias):
     check_router(x, w, b, 9, scoring)
 
 
+@pytest.mark.parametrize("T,E4", [(9, 6), (100, 6), (100, 40)])
+def test_router_near_ties_in_sparse_tokens(T, E4):
+    """The same where only every eighth value of a token is not zero: the bound on a score's error has to see all
+    of them, whichever place of a lane's eight they have."""
+    for place in range(8):
+        g = gen(60 + place)
+        x = torch.zeros(T, 2048)
+        x[:, place::8] = torch.randn(T, 256, generator=g)
+        x = x.to(BF16)
+        w = (torch.randn(E4, 2048, generator=g) * 2048 ** -0.5).to(BF16).repeat_interleave(4, 0).contiguous()
+        bits = w.view(torch.int16)
+        for i in range(E4):
+            bits[4 * i + 2, 8 * (i + 3) + place] ^= 1
+            bits[4 * i + 1, 8 * (i + 9) + place] ^= 1
+        check_router(x, w, None, 9, "softmax")
+
+
 def test_router_extreme_values():
     x, w, _ = router_case(80, 512, 40, 6, "softmax", False, 21)
     x[3] = 0.0                                              # every score equal: ids 0 .. 5
