@@ -95,7 +95,7 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 constexpr int kThreads = 512, kWaves = 8;
 constexpr int kBM = 256, kBN = 256;       // the large tile
 constexpr int kMidBM = 128, kMidBN = 64;  // the small tile
-constexpr int kFewRows = 64;              // most rows of a streaming unit
+constexpr int kFewRows = 16;              // most rows of a streaming unit
 constexpr int kFewCols = 16;
 constexpr int kGroupM = 6;                // M-blocks that a run of tiles goes through before the next N-block
 
@@ -116,23 +116,21 @@ __device__ __forceinline__ void group_rows(const BlockArgs& a, int gi, int64_t& 
 
 // How the rows of a group are cut: into blocks of 256 rows, a rest of up to
 // 128 rows being a half block (half the products), listed after the full
-// ones.  kFew: every row in streaming units of up to 64 rows (small groups).
-// kMid: blocks of 128 rows and 64 columns.
-enum Class : int { kFull = 0, kHalf = 1, kFew = 2, kMid = 3 };
+// ones.  kMid: blocks of 128 rows and 64 columns.
+enum Class : int { kFull = 0, kHalf = 1, kMid = 2 };
 
 // M-blocks of class c in a group of n rows
 __device__ __forceinline__ int64_t blocks_of(int c, int64_t n) {
   const int rest = (int)(n % kBM);
-  if (c == kFew) return (n + kFewRows - 1) / kFewRows;
   if (c == kMid) return (n + kMidBM - 1) / kMidBM;
   if (c == kHalf) return rest > 0 && rest <= kBM / 2 ? 1 : 0;
   return n / kBM + (rest > kBM / 2 ? 1 : 0);
 }
 __device__ __forceinline__ int64_t first_block_row(int c, int64_t n, int64_t mb) {
-  return c == kFull ? mb * kBM : c == kFew ? mb * kFewRows : c == kMid ? mb * kMidBM : n / kBM * kBM;
+  return c == kFull ? mb * kBM : c == kMid ? mb * kMidBM : n / kBM * kBM;
 }
-__device__ __forceinline__ int cols_of(int c) { return c == kFew ? kFewCols : c == kMid ? kMidBN : kBN; }
-__device__ __forceinline__ int most_rows(int c) { return c == kFew ? kFewRows : c == kMid ? kMidBM : kBM; }
+__device__ __forceinline__ int cols_of(int c) { return c == kMid ? kMidBN : kBN; }
+__device__ __forceinline__ int most_rows(int c) { return c == kMid ? kMidBM : kBM; }
 
 // M-blocks of class c over all groups (every lane of the wave takes part)
 __device__ int64_t count_blocks(const BlockArgs& a, int c) {
@@ -203,9 +201,12 @@ __device__ bool find_tile(const BlockArgs& a, int c, int64_t at, TileAt& o) {
 // hit the same lines 1.0 us, the real ones 1.65 us: 64 KiB a stage with a
 // mean latency of 500 cycles.  16384 x 4096 x 7168 runs at 2.27 PFLOP/s; a
 // large e4m3 library product reaches 2.67 here.
-template <int WN, int NT, int MT, int SR>
+// PAIR (small tiles): two groups of 128 a stage, in four slots of LDS, for
+// half as many waits.
+template <int WN, int NT, int MT, bool PAIR, int SR>
 __device__ __forceinline__ void mma_tile(const BlockArgs& a, const TileAt& at, uint8_t* sa0, uint8_t* sa1, uint8_t* sb0,
-                                         uint8_t* sb1, float (*ssc)[2][SR]) {
+                                         uint8_t* sb1, uint8_t* sa2, uint8_t* sa3, uint8_t* sb2, uint8_t* sb3,
+                                         float (*ssc)[2][SR]) {
   constexpr int WM = kWaves / WN, BM = 16 * MT * WM, BN = 16 * NT * WN;
   static_assert(BM <= SR && BM % 64 == 0 && BN % 64 == 0 && (kBlock % (16 * NT) == 0), "whole copies, one weight scale a wave");
   int tid = threadIdx.x;
@@ -312,31 +313,61 @@ __device__ __forceinline__ void mma_tile(const BlockArgs& a, const TileAt& at, u
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
   };
-  {
-    const uint32_t v = ask(0);
+  if constexpr (PAIR) {
+    auto last = [&](int kb) { return kb < KB ? kb : KB - 1; };   // past the end: the last group again, unused
+    float sc0 = bsp[0], sc1 = bsp[last(1)];
+    {
+      const uint32_t v = ask(0);
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) copy(i, 0, sa0, sb0);
-    keep(0, v);
-  }
-  float scb = bsp[0];
-  turn();
-  int kb = 0, pair = 0;
-  for (; kb + 1 < KB; kb += 2, ++pair) {
-    // loads that the next stages need go out before the copies: a wait for
-    // them leaves the copies in flight
-    const uint32_t v = ask(kb + 2);
-    const float scb1 = bsp[kb + 1];
-    __builtin_amdgcn_sched_barrier(0);
-    compute(std::true_type{}, sa0, sb0, ssc[pair % 2][0], scb, kb + 1, sa1, sb1);
+      for (int i = 0; i < kCopies; ++i) copy(i, 0, sa0, sb0);
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) copy(i, last(1), sa1, sb1);
+      keep(0, v);
+    }
     turn();
-    const int nx = kb + 2 < KB ? kb + 2 : KB - 1;   // past the end: the last stage again, unused
-    scb = bsp[nx];
-    __builtin_amdgcn_sched_barrier(0);
-    keep(pair + 1, v);
-    compute(std::true_type{}, sa1, sb1, ssc[pair % 2][1], scb1, nx, sa0, sb0);
+    auto stage = [&](int kb, int pair, uint8_t* a0, uint8_t* a1, uint8_t* b0, uint8_t* b1, uint8_t* na0, uint8_t* na1,
+                     uint8_t* nb0, uint8_t* nb1) {
+      const uint32_t v = ask(kb + 2);
+      const float n0 = bsp[last(kb + 2)], n1 = bsp[last(kb + 3)];
+      __builtin_amdgcn_sched_barrier(0);
+      compute(std::true_type{}, a0, b0, ssc[pair % 2][0], sc0, last(kb + 2), na0, nb0);
+      if (kb + 1 < KB) compute(std::true_type{}, a1, b1, ssc[pair % 2][1], sc1, last(kb + 3), na1, nb1);
+      keep(pair + 1, v);
+      turn();
+      sc0 = n0, sc1 = n1;
+    };
+    for (int kb = 0, pair = 0; kb < KB; kb += 4, pair += 2) {
+      stage(kb, pair, sa0, sa1, sb0, sb1, sa2, sa3, sb2, sb3);
+      if (kb + 2 >= KB) break;
+      stage(kb + 2, pair + 1, sa2, sa3, sb2, sb3, sa0, sa1, sb0, sb1);
+    }
+  } else {
+    {
+      const uint32_t v = ask(0);
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) copy(i, 0, sa0, sb0);
+      keep(0, v);
+    }
+    float scb = bsp[0];
     turn();
+    int kb = 0, pair = 0;
+    for (; kb + 1 < KB; kb += 2, ++pair) {
+      // loads that the next stages need go out before the copies: a wait for
+      // them leaves the copies in flight
+      const uint32_t v = ask(kb + 2);
+      const float scb1 = bsp[kb + 1];
+      __builtin_amdgcn_sched_barrier(0);
+      compute(std::true_type{}, sa0, sb0, ssc[pair % 2][0], scb, kb + 1, sa1, sb1);
+      turn();
+      const int nx = kb + 2 < KB ? kb + 2 : KB - 1;   // past the end: the last stage again, unused
+      scb = bsp[nx];
+      __builtin_amdgcn_sched_barrier(0);
+      keep(pair + 1, v);
+      compute(std::true_type{}, sa1, sb1, ssc[pair % 2][1], scb1, nx, sa0, sb0);
+      turn();
+    }
+    if (kb < KB) compute(std::false_type{}, sa0, sb0, ssc[pair % 2][0], scb, 0, sa1, sb1);
   }
-  if (kb < KB) compute(std::false_type{}, sa0, sb0, ssc[pair % 2][0], scb, 0, sa1, sb1);
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -348,127 +379,6 @@ __device__ __forceinline__ void mma_tile(const BlockArgs& a, const TileAt& at, u
             u32x2{pack_bf16x2(acc[j][i][0], acc[j][i][1]), pack_bf16x2(acc[j][i][2], acc[j][i][3])};
     }
   __syncthreads();      // the next tile of this workgroup writes the stages again
-}
-
-// 32 bf16 of a group of 128 (a quarter of it, the other quarters in the
-// lanes 16, 32, 48 away) -> their codes and the group's scale, the same
-// numbers as k_block_quantize.  The quotient is x * (1/s) with the exact
-// remainder folded back (two fused steps), which rounds like the division.
-__device__ __forceinline__ float quant_group(const u32x4 (&v)[4], u32x4 (&q)[2]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = amax_bits(v[i], m);
-#pragma unroll
-  for (int o = 16; o < 64; o <<= 1) {
-    const uint32_t x = (uint32_t)__shfl_xor((int)m, o, 64);
-    m = x > m ? x : m;
-  }
-  const float s = block_scale(m);
-  if (ballot(!(s < 1e36f)) != 0) {           // an infinity or a NaN somewhere: the plain division
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const u32x2 c = quant8(v[i], s);
-      q[i / 2][2 * (i % 2)] = c[0];
-      q[i / 2][2 * (i % 2) + 1] = c[1];
-    }
-    return s;
-  }
-  const float r = 1.0f / s;
-  auto div = [&](float x) {
-    const float p = x * r;
-    return sat448(__builtin_fmaf(__builtin_fmaf(-s, p, x), r, p));
-  };
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t x = v[i][2 * h], y = v[i][2 * h + 1];
-      int c = __builtin_amdgcn_cvt_pk_fp8_f32(div(__uint_as_float(x << 16)), div(__uint_as_float(x & 0xffff0000u)), 0, false);
-      c = __builtin_amdgcn_cvt_pk_fp8_f32(div(__uint_as_float(y << 16)), div(__uint_as_float(y & 0xffff0000u)), c, true);
-      q[i / 2][2 * (i % 2) + h] = (uint32_t)c;
-    }
-  return s;
-}
-
-// Streaming unit: up to 16 * NT rows x 16 columns.  Each weight byte goes
-// straight from memory into an operand; the 8 waves share the K-blocks, D of
-// them in flight a wave, and meet in LDS.  FROM_X: the rows are bf16 and are
-// quantised in registers.  Bound: HBM (latency for a single short product).
-template <int NT, int D, bool FROM_X>
-__device__ __forceinline__ void few_unit(const BlockArgs& a, const TileAt& at, f32x4 (*red)[NT][64]) {
-  int tid = threadIdx.x;
-  asm volatile("" : "+v"(tid));
-  const TileAt t = uniform_tile(at);
-  const int w = uniform(tid / 64), l = tid % 64, r = l % 16, g = l / 16;
-  const int KB = a.K / kBlock, nblocks = (a.N + kBlock - 1) / kBlock;
-  const uint8_t* bp = a.b + ((int64_t)t.group * a.N + t.n0 + r) * a.K + g * 32;
-  const float* bsp = a.bs + ((int64_t)t.group * nblocks + t.n0 / kBlock) * KB;
-  const uint8_t* ap[NT];
-  const float* asp[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int64_t row = t.m0 + (16 * i + r < t.rows ? 16 * i + r : 0);
-    ap[i] = FROM_X ? static_cast<const uint8_t*>(a.x) + row * a.K * 2 + g * 64 : a.a + row * a.K + g * 32;
-    asp[i] = a.as + row * KB;
-  }
-  constexpr int XL = FROM_X ? 4 : 2;
-  struct Stage {
-    u32x4 b[2], x[NT][XL];
-    float sa[NT], sb;
-  } st[D];
-  auto load = [&](Stage& s, int kb) {
-    if (kb >= KB) return;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      s.b[h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(bp + (int64_t)kb * kBlock + h * 16));
-    s.sb = bsp[kb];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-      if (NT == 1 || 16 * i < t.rows) {
-#pragma unroll
-        for (int h = 0; h < XL; ++h)
-          s.x[i][h] = *reinterpret_cast<const u32x4*>(ap[i] + (int64_t)kb * (kBlock * (FROM_X ? 2 : 1)) + h * 16);
-        if constexpr (!FROM_X) s.sa[i] = asp[i][kb];
-      }
-  };
-  f32x4 acc[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int d = 0; d < D; ++d) load(st[d], w + d * kWaves);
-  for (int kb = w; kb < KB; kb += D * kWaves) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      const int k = kb + d * kWaves;
-      if (k < KB) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          if (NT == 1 || 16 * i < t.rows) {
-            if constexpr (FROM_X) {
-              u32x4 q[2];
-              const float s = quant_group(st[d].x[i], q);
-              acc[i] += mfma128(st[d].b[0], st[d].b[1], q[0], q[1]) * (s * st[d].sb);
-            } else {
-              acc[i] += mfma128(st[d].b[0], st[d].b[1], st[d].x[i][0], st[d].x[i][1]) * (st[d].sa[i] * st[d].sb);
-            }
-          }
-        load(st[d], k + D * kWaves);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NT; ++i) red[w][i][l] = acc[i];
-  __syncthreads();
-  for (int i = tid; i < NT * 64; i += kThreads) {
-    f32x4 v = red[0][i / 64][i % 64];
-#pragma unroll
-    for (int k = 1; k < kWaves; ++k) v += red[k][i / 64][i % 64];
-    const int row = i / 64 * 16 + i % 16;
-    if (row < t.rows)
-      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + (t.m0 + row) * a.N + t.n0 + i % 64 / 16 * 4) =
-          u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-  }
-  __syncthreads();
 }
 
 }  // namespace
@@ -493,18 +403,21 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
     TileAt t;
     if (k < n[0]) {
       if (!find_tile(a, kFull, first[0] + k, t)) break;
-      mma_tile<2, 8, 4>(a, t, sa0, sa1, sb0, sb1, ssc);
+      mma_tile<2, 8, 4, false>(a, t, sa0, sa1, sb0, sb1, nullptr, nullptr, nullptr, nullptr, ssc);
     } else {
       if (!find_tile(a, kHalf, first[1] + k - n[0], t)) break;
-      mma_tile<2, 8, 2>(a, t, sa0, sa1, sb0, sb1, ssc);
+      mma_tile<2, 8, 2, false>(a, t, sa0, sa1, sb0, sb1, nullptr, nullptr, nullptr, nullptr, ssc);
     }
   }
 }
 
 // Products whose large tiles would leave most CUs without one: small tiles,
-// three workgroups a CU.
+// one workgroup a CU with two groups of 128 a stage, or (PAIR false) three
+// with one.
+template <bool PAIR>
 __global__ __launch_bounds__(kThreads) void k_block_mid(BlockArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t sa0[kMidBM * kBlock], sa1[kMidBM * kBlock], sb0[kMidBN * kBlock], sb1[kMidBN * kBlock];
+  __shared__ __attribute__((aligned(1024))) uint8_t sa0[kMidBM * kBlock], sa1[kMidBM * kBlock];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb0[kMidBN * kBlock], sb1[kMidBN * kBlock];
   __shared__ float ssc[2][2][kMidBM];
   const int x = blockIdx.x % 8, step = gridDim.x / 8;
   const int64_t total = count_blocks(a, kMid) * ((a.N + kMidBN - 1) / kMidBN);
@@ -512,56 +425,171 @@ __global__ __launch_bounds__(kThreads) void k_block_mid(BlockArgs a) {
   for (int64_t k = blockIdx.x / 8; k < n; k += step) {
     TileAt t;
     if (!find_tile(a, kMid, first + k, t)) break;
-    mma_tile<2, 2, 2>(a, t, sa0, sa1, sb0, sb1, ssc);
+    if constexpr (PAIR) {
+      __shared__ __attribute__((aligned(1024))) uint8_t sa2[kMidBM * kBlock], sa3[kMidBM * kBlock];
+      __shared__ __attribute__((aligned(1024))) uint8_t sb2[kMidBN * kBlock], sb3[kMidBN * kBlock];
+      mma_tile<2, 2, 2, true>(a, t, sa0, sa1, sb0, sb1, sa2, sa3, sb2, sb3, ssc);
+    } else {
+      mma_tile<2, 2, 2, false>(a, t, sa0, sa1, sb0, sb1, nullptr, nullptr, nullptr, nullptr, ssc);
+    }
   }
 }
 
-// Products with few rows, or few in each group.
-template <int NT, int D, bool FROM_X>
+// Up to 16 rows of one matrix (a.m_first and on): 16 columns a workgroup.
+// Each weight byte goes straight from memory into an operand; the 8 waves
+// share the K-blocks, D of them in flight a wave, and meet in LDS.
 __global__ __launch_bounds__(kThreads) void k_block_few(BlockArgs a) {
-  __shared__ f32x4 red[kWaves][NT][64];
-  if (a.offsets == nullptr) {          // one unit of all rows a workgroup
-    const TileAt t{a.m_first, (int)(a.M - a.m_first), 0, (int)blockIdx.x * kFewCols};
-    few_unit<NT, D, FROM_X>(a, t, red);
-    return;
+  constexpr int D = 4;
+  __shared__ f32x4 red[kWaves][64];
+  const int tid = threadIdx.x, w = uniform(tid / 64), l = tid % 64, r = l % 16, g = l / 16;
+  const int KB = a.K / kBlock, n0 = (int)blockIdx.x * kFewCols, rows = (int)(a.M - a.m_first);
+  const uint8_t* bp = a.b + (int64_t)(n0 + r) * a.K + g * 32;
+  const float* bsp = a.bs + (int64_t)(n0 / kBlock) * KB;
+  const int64_t row = a.m_first + (r < rows ? r : 0);
+  const uint8_t* ap = a.a + row * a.K + g * 32;
+  const float* asp = a.as + row * KB;
+  struct Stage {
+    u32x4 b[2], x[2];
+    float sa, sb;
+  } st[D];
+  // Past the end the last block again, unused: a load under a condition would
+  // make the compiler wait for every load in flight before each product.
+  auto load = [&](Stage& s, int kb) {
+    kb = kb < KB ? kb : KB - 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s.b[h] = *reinterpret_cast<const u32x4*>(bp + (int64_t)kb * kBlock + h * 16);
+    s.sb = bsp[kb];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s.x[h] = *reinterpret_cast<const u32x4*>(ap + (int64_t)kb * kBlock + h * 16);
+    s.sa = asp[kb];
+  };
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(st[d], w + d * kWaves);
+  for (int kb = w; kb < KB; kb += D * kWaves) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int k = kb + d * kWaves;
+      if (k < KB) acc += mfma128(st[d].b[0], st[d].b[1], st[d].x[0], st[d].x[1]) * (st[d].sa * st[d].sb);
+      load(st[d], k + D * kWaves);
+    }
   }
-  const int64_t total = count_blocks(a, kFew) * (a.N / kFewCols);
-  for (int64_t k = blockIdx.x; k < total; k += gridDim.x) {
-    TileAt t;
-    if (!find_tile(a, kFew, k, t)) break;
-    few_unit<NT, D, FROM_X>(a, t, red);
+  red[w][l] = acc;
+  __syncthreads();
+  if (tid < 64 && r < rows) {
+    f32x4 v = red[0][l];
+#pragma unroll
+    for (int k = 1; k < kWaves; ++k) v += red[k][l];
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + row * a.N + n0 + 4 * g) =
+        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
   }
 }
 
-bool block_from_x(const BlockArgs& a) { return a.offsets == nullptr && a.M <= 16; }
+// A few bf16 rows (a decoded token's projection): 16 columns a workgroup of 4
+// waves.  The first weights are asked for, the rows are quantised into LDS
+// meanwhile (the same codes and scales as k_block_quantize, by the same
+// code), then the waves stream their K-blocks.  Bound: latency: one row x
+// 7168 x 2048 takes 5.x us for 14.7 MB of weights (3 us at the copy rate);
+// a quantising kernel before it added 2 us and a launch.
+constexpr int kRowThreads = 256, kRowWaves = 4;
+constexpr int64_t kRowBytes = 64 * 1024;        // most codes in LDS
+
+__global__ __launch_bounds__(kRowThreads) void k_block_rows(BlockArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  __shared__ f32x4 red[kRowWaves][64];
+  const int tid = threadIdx.x, w = uniform(tid / 64), l = tid % 64, r = l % 16, g = l / 16;
+  const int KB = a.K / kBlock, M = (int)a.M, n0 = (int)blockIdx.x * kFewCols;
+  const int pitch = a.K + 16;                   // rows of one column of chunks in different banks
+  uint8_t* codes = dyn;                         // [M][pitch]
+  float* scales = reinterpret_cast<float*>(dyn + M * pitch);   // [M][KB]
+  constexpr int D = 4;
+  const uint8_t* bp = a.b + (int64_t)(n0 + r) * a.K + g * 32;
+  const float* bsp = a.bs + (int64_t)(n0 / kBlock) * KB;
+  u32x4 b[D][2];
+  float sb[D];
+  // past the end: the last block again, unused (a load under a condition would
+  // make the compiler wait for all of them)
+  auto load = [&](int d, int kb) {
+    kb = kb < KB ? kb : KB - 1;
+    b[d][0] = *reinterpret_cast<const u32x4*>(bp + (int64_t)kb * kBlock);
+    b[d][1] = *reinterpret_cast<const u32x4*>(bp + (int64_t)kb * kBlock + 16);
+    sb[d] = bsp[kb];
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, w + d * kRowWaves);
+  const int per = a.K / 8;
+  for (int i = tid; i < M * per; i += kRowThreads) {   // 16 lanes a group; a whole number of groups a round
+    const int row = i / per, c = i % per;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.x) + (int64_t)i * 16);
+    uint32_t m = amax_bits(v, 0);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      const uint32_t x = (uint32_t)__shfl_xor((int)m, o, 64);
+      m = x > m ? x : m;
+    }
+    const float s = block_scale(m);
+    *reinterpret_cast<u32x2*>(codes + row * pitch + c * 8) = quant8(v, s);
+    if (c % 16 == 0) scales[row * KB + c / 16] = s;
+  }
+  __syncthreads();
+  const int row = r < M ? r : 0;
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k0 = w; k0 < KB; k0 += D * kRowWaves) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int kb = k0 + d * kRowWaves;
+      if (kb < KB) {
+        const uint8_t* q = codes + row * pitch + kb * kBlock + g * 32;
+        acc += mfma128(b[d][0], b[d][1], *reinterpret_cast<const u32x4*>(q), *reinterpret_cast<const u32x4*>(q + 16)) *
+               (scales[row * KB + kb] * sb[d]);
+      }
+      load(d, kb + D * kRowWaves);
+    }
+  }
+  red[w][l] = acc;
+  __syncthreads();
+  if (tid < 64 && r < M) {
+    const f32x4 v = red[0][l] + red[1][l] + red[2][l] + red[3][l];
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + (int64_t)r * a.N + n0 + 4 * g) =
+        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  }
+}
+
+bool block_from_x(const BlockArgs& a) { return a.offsets == nullptr && a.M <= 16 && a.M * a.K <= kRowBytes; }
 
 hipError_t launch_block_gemm(const BlockArgs& args, int num_cus, hipStream_t s) {
   BlockArgs a = args;
   const int64_t units = a.N / kFewCols;
-  if (a.offsets != nullptr && a.M <= (int64_t)kFewRows * a.G) {
-    const int64_t most = 2 * (int64_t)num_cus, all = units * a.G;
-    hipLaunchKernelGGL((k_block_few<4, 2, false>), dim3((unsigned)(all < most ? all : most)), dim3(kThreads), 0, s, a);
+  if (a.x != nullptr) {
+    const size_t lds = (size_t)(a.M * (a.K + 16 + a.K / kBlock * 4));
+    if (lds > 60 * 1024) {   // with the static array, more than 64 KiB
+      const hipError_t err = hipFuncSetAttribute((const void*)k_block_rows, hipFuncAttributeMaxDynamicSharedMemorySize, 72 * 1024);
+      if (err != hipSuccess) return err;
+    }
+    hipLaunchKernelGGL(k_block_rows, dim3((unsigned)units), dim3(kRowThreads), lds, s, a);
     return hipGetLastError();
   }
-  // one matrix: up to 64 rows beyond the blocks of 256 go through the streaming units
+  // one matrix: up to 16 rows beyond the blocks of 256 are streamed
   const int64_t rest = a.offsets == nullptr ? a.M % kBM : 0;
   if (rest == 0 || rest > kFewRows || a.M > rest) {
     if (rest > 0 && rest <= kFewRows) a.M -= rest;
-    // Measured at 4096 x 7168, us with large / small tiles: 128 rows 60 / 36,
-    // 512 rows 96 / 39, 1024 rows (64 large tiles) 97 / 51, 2048 rows (128
-    // tiles) 97 / 104; 32 groups of 128 rows (512 half tiles) 299 / 428.
-    const int64_t tiles = ((a.M / a.G + kBM - 1) / kBM) * a.G * ((a.N + kBN - 1) / kBN);
+    // Measured at 4096 x 7168, us with large tiles / small ones / small ones
+    // two groups a stage: 128 rows 60 / 36 / 30, 512 rows 96 / 39 / 32, 1024 rows
+    // (64 large tiles, 512 small ones) 97 / 51 / 60, 2048 rows (128 large tiles)
+    // 97 / 104 / 90; 32 groups of 16 rows (512 half tiles) 184 / 276 / -.
+    const int64_t even = a.M / a.G > 0 ? a.M / a.G : 1;
+    const int64_t tiles = (even + kBM - 1) / kBM * a.G * ((a.N + kBN - 1) / kBN);
     const unsigned cus = (unsigned)((num_cus + 7) / 8 * 8);
-    if (tiles < 112) hipLaunchKernelGGL(k_block_mid, dim3(3 * cus), dim3(kThreads), 0, s, a);
+    const int64_t small = (even + kMidBM - 1) / kMidBM * a.G * ((a.N + kMidBN - 1) / kMidBN);
+    if (tiles < 112 && small <= num_cus) hipLaunchKernelGGL(k_block_mid<true>, dim3(cus), dim3(kThreads), 0, s, a);
+    else if (tiles < 112) hipLaunchKernelGGL(k_block_mid<false>, dim3(3 * cus), dim3(kThreads), 0, s, a);
     else hipLaunchKernelGGL(k_block_mma, dim3(cus), dim3(kThreads), 0, s, a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || a.M == args.M) return err;
     a.m_first = a.M;
     a.M = args.M;
   }
-  if (a.x != nullptr) hipLaunchKernelGGL((k_block_few<1, 2, true>), dim3((unsigned)units), dim3(kThreads), 0, s, a);
-  else if (rest <= 16) hipLaunchKernelGGL((k_block_few<1, 4, false>), dim3((unsigned)units), dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((k_block_few<4, 2, false>), dim3((unsigned)units), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL(k_block_few, dim3((unsigned)units), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

@@ -19,6 +19,13 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
+#ifndef CTA
+#define CTA 1
+#define CTB 2
+#define KWB 8
+#define WTA 2
+#define DA 3
+#endif
 constexpr int kMaxT = 64, kMaxE = 1025, kMaxRoutes = 64 * 33;
 constexpr int kStage = 128;            // K-values per stage of a wave
 
@@ -142,7 +149,7 @@ __device__ __forceinline__ void load_weights(Stage<F, WT, NT, P>& st, const uint
   for (int i = 0; i < WT; ++i)
 #pragma unroll
     for (int j = 0; j < Stage<F, WT, NT, P>::WL; ++j)
-      st.w[i][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wp[i] + off + w_piece<F>(g, j)));
+      st.w[i][j] = *reinterpret_cast<const u32x4*>(wp[i] + off + w_piece<F>(g, j));
 }
 
 template <int F, int WT, int NT, int P>
@@ -176,6 +183,13 @@ __device__ __forceinline__ void clear(f32x4 (&acc)[WT][NT]) {
     for (int n = 0; n < NT; ++n) acc[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 }
 
+__device__ __forceinline__ float swiglu(float g, float u, float clamp) {
+  // a NaN stays one (a clamp by min and max would replace it)
+  g = g > clamp ? clamp : g < -clamp ? -clamp : g;
+  u = u > clamp ? clamp : u < -clamp ? -clamp : u;
+  return g / (1.0f + expf(-g)) * u;
+}
+
 // bf16 parts of a float whose sum is the float to P * 8 bits
 template <int P>
 __device__ __forceinline__ void split_bf16(float v, uint16_t (&o)[P]) {
@@ -189,18 +203,20 @@ __device__ __forceinline__ void split_bf16(float v, uint16_t (&o)[P]) {
 
 }  // namespace
 
-// Linear1.  A unit is 16 columns of A of one live expert (16 gate and 16 up
-// rows of W1) for a group of up to 16 * NT of its routes; the 8 waves share
+// Linear1.  A unit is 16 * CT columns of A of one live expert (16 gate and 16
+// up rows of W1 for each CT) for a group of up to 16 * NT of its routes; the 8 waves share
 // the hidden dimension, stage by stage, and their sums meet in LDS.  D
 // stages of a wave are in flight, across units.
-template <int F, int NT, int P, int D>
+template <int F, int KW, int CT, int NT, int P, int D>
 __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
   __shared__ Lists L;
-  __shared__ f32x4 red[kWaves][2][NT][64];
+  constexpr int WT = 2 * CT;
+  constexpr bool kShared = KW > 1;      // waves that share a unit
+  __shared__ f32x4 red[kShared ? kWaves : 1][WT][NT][64];
   build_lists(a, L, 16 * NT);
   const int w = uniform(threadIdx.x / 64), l = threadIdx.x % 64, r = l % 16, g = l / 16;
   constexpr int WB = weight_bytes<F>();
-  const int nst = a.H / kStage, nsw = (nst + kWaves - 1) / kWaves, cols = a.I / 16;
+  const int nst = a.H / kStage, nsw = (nst + KW - 1) / KW, kw = w % KW, cols = a.I / (16 * CT);
   const int units = uniform(L.live) * cols;
   const int64_t R = (int64_t)a.T * (a.K + a.S);
 
@@ -208,10 +224,15 @@ __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
   struct Cursor {
     int u, q, j;
     int e, c, n0, n;
-    const uint8_t* wp[2];
+    const uint8_t* wp[WT];
     const uint8_t* bp[NT];
     const float* sp[2];
   };
+  const int first = (int)blockIdx.x * (kWaves / KW) + w / KW, stride = gridDim.x * (kWaves / KW);
+  if (first >= units) return;
+  // Past the last unit a cursor keeps its pointers: its loads go on, into
+  // stages that nothing multiplies.  A load under a condition would make the
+  // compiler wait for every load in flight before each product.
   auto aim = [&](Cursor& cu) {
     if (cu.u >= units) return;
     const int le = cu.u / cols;
@@ -219,10 +240,13 @@ __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
     cu.e = uniform(L.expert[le]);
     cu.n0 = uniform(L.start[le]) + cu.q * 16 * NT;
     cu.n = uniform(L.start[le + 1]) - cu.n0;
-    const int row = 64 * (cu.c / 2) + 16 * (cu.c % 2) + r;
     const uint8_t* base = a.w1 + (int64_t)cu.e * 2 * a.I * a.H * WB;
-    cu.wp[0] = base + (int64_t)row * a.H * WB;
-    cu.wp[1] = base + (int64_t)(row + 32) * a.H * WB;
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      const int col = cu.c * CT + c, row = 64 * (col / 2) + 16 * (col % 2) + r;
+      cu.wp[2 * c] = base + (int64_t)row * a.H * WB;
+      cu.wp[2 * c + 1] = base + (int64_t)(row + 32) * a.H * WB;
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int i = 16 * n + r;
@@ -230,8 +254,8 @@ __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
     }
     if constexpr (F == MM_FEW_FP8_BLOCK) {
       const float* s = a.s1 + (int64_t)cu.e * (2 * a.I / 128) * nst;
-      cu.sp[0] = s + (int64_t)(cu.c / 8) * nst;
-      cu.sp[1] = s + (int64_t)(a.I / 128 + cu.c / 8) * nst;
+      cu.sp[0] = s + (int64_t)(cu.c * CT / 8) * nst;
+      cu.sp[1] = s + (int64_t)(a.I / 128 + cu.c * CT / 8) * nst;
     }
   };
   auto step = [&](Cursor& cu) {
@@ -241,29 +265,30 @@ __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
       ++cu.q;
     } else {
       cu.q = 0;
-      cu.u += gridDim.x;
+      cu.u += stride;
     }
     aim(cu);
   };
-  auto load = [&](const Cursor& cu, Stage<F, 2, NT, 1>& st) {
-    const int s = cu.j * kWaves + w;
-    if (cu.u >= units || s >= nst) return;
-    load_weights<F, 2, NT, 1>(st, cu.wp, (int64_t)s * (kStage * WB), g);
+  auto load = [&](const Cursor& cu, Stage<F, WT, NT, 1>& st) {
+    const int js = cu.j * KW + kw, s = js < nst ? js : nst - 1;
+    load_weights<F, WT, NT, 1>(st, cu.wp, (int64_t)s * (kStage * WB), g);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      if (NT == 1 || 16 * n < cu.n) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) st.b[0][n][j] = *reinterpret_cast<const u32x4*>(cu.bp[n] + (int64_t)s * (kStage * 2) + b_piece<F>(g, j));
-      }
-    if constexpr (F == MM_FEW_FP8_BLOCK) st.s[0] = cu.sp[0][s], st.s[1] = cu.sp[1][s];
+      for (int j = 0; j < 4; ++j) st.b[0][n][j] = *reinterpret_cast<const u32x4*>(cu.bp[n] + (int64_t)s * (kStage * 2) + b_piece<F>(g, j));
+    if constexpr (F == MM_FEW_FP8_BLOCK) {
+      const float sg = cu.sp[0][s], su = cu.sp[1][s];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) st.s[2 * c] = sg, st.s[2 * c + 1] = su;
+    }
   };
 
   Cursor ld{}, cu{};
-  ld.u = cu.u = blockIdx.x;
+  ld.u = cu.u = first;
   aim(ld);
   aim(cu);
-  Stage<F, 2, NT, 1> st[D];
-  f32x4 acc[2][NT];
+  Stage<F, WT, NT, 1> st[D];
+  f32x4 acc[WT][NT];
   clear(acc);
 #pragma unroll
   for (int d = 0; d < D; ++d) {
@@ -273,40 +298,67 @@ __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
   while (cu.u < units) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
+      if (cu.u < units && cu.j * KW + kw < nst) multiply<F, WT, NT, 1>(st[d], acc, (cu.n + 15) / 16);
+      load(ld, st[d]);
+      if (ld.u < units) step(ld);
       if (cu.u < units) {
-        if (cu.j * kWaves + w < nst) multiply<F, 2, NT, 1>(st[d], acc, (cu.n + 15) / 16);
-        load(ld, st[d]);
-        if (ld.u < units) step(ld);
         if (cu.j + 1 == nsw) {
+          if constexpr (!kShared) {
+            // a lane has gate and up of four columns of one route
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+              const int col = (cu.c * CT + c) * 16 + 4 * g;
+              f32x4 sg, su;
+              if constexpr (F == MM_FEW_FP8) {
+                sg = *reinterpret_cast<const f32x4*>(a.s1 + (int64_t)cu.e * 2 * a.I + col);
+                su = *reinterpret_cast<const f32x4*>(a.s1 + (int64_t)cu.e * 2 * a.I + a.I + col);
+              }
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                f32x4 hg = acc[2 * c][n], hu = acc[2 * c + 1][n];
+                if constexpr (F == MM_FEW_FP8) hg *= sg, hu *= su;
+                uint16_t o[4][P];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split_bf16<P>(swiglu(hg[i], hu[i], a.clamp), o[i]);
+                if (16 * n + r < cu.n) {
+                  const int64_t route = L.route[cu.n0 + 16 * n + r];
+#pragma unroll
+                  for (int p = 0; p < P; ++p)
+                    *reinterpret_cast<u32x2*>(a.a + (p * R + route) * a.I + col) =
+                        u32x2{o[0][p] | (uint32_t)o[1][p] << 16, o[2][p] | (uint32_t)o[3][p] << 16};
+                }
+              }
+            }
+            clear(acc);
+            step(cu);
+            continue;
+          }
           // the unit's sums: 8 waves' parts, SwiGLU, A
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < WT; ++i)
 #pragma unroll
             for (int n = 0; n < NT; ++n) red[w][i][n][l] = acc[i][n];
           clear(acc);
           __syncthreads();
           const float* rf = reinterpret_cast<const float*>(red);
           const int n16 = cu.n < 16 * NT ? cu.n : 16 * NT;
-          for (int i = threadIdx.x; i < 16 * n16; i += kThreads) {
-            // column c (of 16) of list entry m: accumulator c % 4 of lane 16 * (c / 4) + m % 16
-            const int c = i % 16, m = i / 16;
+          for (int i = threadIdx.x; i < 16 * CT * n16; i += kThreads) {
+            // column c (of 16, in tile ct) of list entry m: accumulator c % 4 of lane 16 * (c / 4) + m % 16
+            const int c = i % 16, ct = i / 16 % CT, m = i / (16 * CT);
             const int at = ((m / 16) * 64 + 16 * (c / 4) + m % 16) * 4 + c % 4;
             float hg = 0.0f, hu = 0.0f;
 #pragma unroll
             for (int k = 0; k < kWaves; ++k) {
-              hg += rf[(k * 2 + 0) * NT * 256 + at];
-              hu += rf[(k * 2 + 1) * NT * 256 + at];
+              hg += rf[(k * WT + 2 * ct) * NT * 256 + at];
+              hu += rf[(k * WT + 2 * ct + 1) * NT * 256 + at];
             }
-            const int col = cu.c * 16 + c;
+            const int col = (cu.c * CT + ct) * 16 + c;
             if constexpr (F == MM_FEW_FP8) {
               hg *= a.s1[(int64_t)cu.e * 2 * a.I + col];
               hu *= a.s1[(int64_t)cu.e * 2 * a.I + a.I + col];
             }
-            // a NaN stays one (a clamp by min and max would replace it)
-            hg = hg > a.clamp ? a.clamp : hg < -a.clamp ? -a.clamp : hg;
-            hu = hu > a.clamp ? a.clamp : hu < -a.clamp ? -a.clamp : hu;
             uint16_t o[P];
-            split_bf16<P>(hg / (1.0f + expf(-hg)) * hu, o);
+            split_bf16<P>(swiglu(hg, hu, a.clamp), o);
             const int64_t route = L.route[cu.n0 + m];
 #pragma unroll
             for (int p = 0; p < P; ++p) a.a[(p * R + route) * a.I + col] = o[p];
@@ -339,17 +391,26 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
   for (int i = threadIdx.x; i < kWaves * a.T * 4 * WT; i += kThreads) ys[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
 
-  // the live expert and its visit that hold this wave's first stage
+  if (total == 0) {          // no route at all
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.T * a.H; i += gridDim.x * kThreads) {
+      if (a.y_f32) static_cast<float*>(a.y)[i] = 0.0f;
+      else static_cast<uint16_t*>(a.y)[i] = 0;
+    }
+    return;
+  }
+  // the live expert and its visit that hold this wave's first stage (the last
+  // stage for a wave without any: its loads have to go somewhere)
+  const int f0 = w * nsw < total ? w * nsw : total - 1;
   int le0 = 0, q0 = 0;
   {
-    const int v = w * nsw / nst;
+    const int v = f0 / nst;
     int hi = live;             // the last expert whose first visit is at most v
     while (hi - le0 > 1) {
       const int mid = (le0 + hi) / 2;
       if (uniform(L.visit[mid]) <= v) le0 = mid;
       else hi = mid;
     }
-    if (live > 0) q0 = v - uniform(L.visit[le0]);
+    q0 = v - uniform(L.visit[le0]);
   }
 
   struct Cursor {
@@ -362,7 +423,7 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
   };
   auto valid = [&](const Cursor& cu) { return w * nsw + cu.j < total; };
   auto aim = [&](Cursor& cu) {
-    if (cu.u >= units || !valid(cu)) return;
+    if (cu.u >= units) return;
     cu.e = uniform(L.expert[cu.le]);
     cu.n0 = uniform(L.start[cu.le]) + cu.q * 16 * NT;
     cu.n = uniform(L.start[cu.le + 1]) - cu.n0;
@@ -381,7 +442,7 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
   };
   auto first = [&](Cursor& cu) {
     cu.j = 0;
-    cu.s = (w * nsw) % nst;
+    cu.s = f0 % nst;
     cu.le = le0;
     cu.q = q0;
     aim(cu);
@@ -390,25 +451,22 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
     if (++cu.j == nsw) {
       cu.u += gridDim.x;
       first(cu);
-    } else if (++cu.s == nst) {
+    } else if (valid(cu) && ++cu.s == nst) {
       cu.s = 0;
       ++cu.q;
-      if (cu.le < live && uniform(L.start[cu.le]) + cu.q * 16 * NT >= uniform(L.start[cu.le + 1])) ++cu.le, cu.q = 0;
+      if (uniform(L.start[cu.le]) + cu.q * 16 * NT >= uniform(L.start[cu.le + 1])) ++cu.le, cu.q = 0;
       aim(cu);
     }
   };
   auto load = [&](const Cursor& cu, Stage<F, WT, NT, P>& st) {
-    if (cu.u >= units || !valid(cu)) return;
     load_weights<F, WT, NT, P>(st, cu.wp, (int64_t)cu.s * (kStage * WB), g);
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        if (NT == 1 || 16 * n < cu.n) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j)
             st.b[p][n][j] = *reinterpret_cast<const u32x4*>(cu.bp[n] + (int64_t)p * R * a.I * 2 + (int64_t)cu.s * (kStage * 2) + b_piece<F>(g, j));
-        }
     if constexpr (F == MM_FEW_FP8_BLOCK) {
 #pragma unroll
       for (int i = 0; i < WT; ++i) st.s[i] = cu.sp[i][cu.s];
@@ -430,10 +488,10 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
   while (cu.u < units) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
+      if (cu.u < units && valid(cu)) multiply<F, WT, NT, P>(st[d], acc, (cu.n + 15) / 16);
+      load(ld, st[d]);
+      if (ld.u < units) step(ld);
       if (cu.u < units) {
-        if (valid(cu)) multiply<F, WT, NT, P>(st[d], acc, (cu.n + 15) / 16);
-        load(ld, st[d]);
-        if (ld.u < units) step(ld);
         const bool last = cu.j + 1 == nsw;
         if (valid(cu) && (last || cu.s + 1 == nst || w * nsw + cu.j + 1 == total)) {
           // end of this wave's part of a visit: gate * sum into its copy of y
@@ -482,13 +540,14 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
 
 namespace {
 
-template <int F, int NT, int P, int D>
+template <int F, int KW, int CT, int NT, int P, int D>
 hipError_t run_l1(const FewArgs& a, int num_cus, hipStream_t s) {
   const int64_t routes = (int64_t)a.T * a.K + (a.S ? a.T : 0);
   const int64_t live = routes < a.E + a.S ? routes : a.E + a.S;
-  const int64_t units = live * (a.I / 16);
-  const int grid = (int)(units < num_cus ? units : num_cus);
-  hipLaunchKernelGGL((k_few_l1<F, NT, P, D>), dim3(grid), dim3(kThreads), 0, s, a);
+  const int64_t units = live * (a.I / (16 * CT));
+  const int64_t blocks = (units * KW + kWaves - 1) / kWaves;
+  const int grid = (int)(blocks < num_cus ? blocks : num_cus);
+  hipLaunchKernelGGL((k_few_l1<F, KW, CT, NT, P, D>), dim3(grid), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -507,12 +566,12 @@ hipError_t run_l2(const FewArgs& a, int num_cus, hipStream_t s) {
 
 template <int F, int P>
 hipError_t run_l1_f(const FewArgs& a, int num_cus, hipStream_t s) {
-  if (a.T <= 16) return run_l1<F, 1, P, 3>(a, num_cus, s);
-  return run_l1<F, 2, P, 2>(a, num_cus, s);
+  if (a.T <= 16) return run_l1<F, 8, CTA, 1, P, 3>(a, num_cus, s);
+  return run_l1<F, KWB, CTB, 2, P, 2>(a, num_cus, s);
 }
 template <int F, int P>
 hipError_t run_l2_f(const FewArgs& a, int num_cus, hipStream_t s) {
-  if (a.T <= 16) return run_l2<F, 1, 1, P, P == 1 ? 4 : 2>(a, num_cus, s);
+  if (a.T <= 16) return run_l2<F, WTA, 1, P, P == 1 ? DA : 2>(a, num_cus, s);
   return run_l2<F, 2, P == 1 ? 2 : 1, P, 2>(a, num_cus, s);
 }
 template <int P>

@@ -313,15 +313,18 @@ __global__ __launch_bounds__(256, NV <= 4 ? 4 : 1) void k_router_select(RouterAr
   }
 }
 
-// Up to 64 tokens the scores are a stream of Wr: 16 x 16 tiles over as many
-// workgroups as the hidden dimension gives.  Beyond, with up to 128 experts,
-// a wave holds 64 x 64 and the waves share the hidden dimension; with more, or
-// when ... the LDS tiles.
+// With few tokens or few scores in all, the scores are a stream of Wr: 16 x 16
+// tiles over as many workgroups as the hidden dimension gives (us for both
+// kernels, 16 x 16 / 64 x 64 a wave, hidden 7168: 333 tokens x 32 experts
+// 17 / 20, 1000 x 32 22 / 23, 1000 x 64 30 / 27, 4000 x 32 44 / 34).  Beyond, with
+// up to 128 experts, a wave holds 64 x 64 and the waves share the hidden
+// dimension; with more experts the LDS tiles (16384 x 256: 210 and 92 us for
+// the scores alone).
 RouterShape router_shape(int64_t T, int H, int E) {
   RouterShape s{};
   const int steps = H / kRouterStep;
   s.ep = (E + 15) / 16 * 16;
-  s.wide = T <= 64 ? 0 : E <= 128 ? 1 : 2;
+  s.wide = T <= 64 || T * E <= 32768 ? 0 : E <= 128 ? 1 : 2;
   int64_t tiles = 1, most = steps / (kWaves * 4);
   if (s.wide == 0) {
     s.ew = 1;

@@ -179,7 +179,7 @@ def _need(name, t, dtype, shape, device):
     """The one check of a tensor argument: a message that says what it has to be."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor {list(shape)} on {device} is needed, got {t.dtype} "
                          f"{list(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
     if t.requires_grad and torch.is_grad_enabled():
@@ -190,9 +190,9 @@ def _rows(name, x):
     """(rows, columns, device) of a bf16 or e4m3 matrix on a GPU."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError(f"{name}: a matrix is needed")
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"{name}: a tensor on a GPU is needed, got one on {x.device}")
-    return x.shape[0], x.shape[1], x.device
+    return *x.shape, x.device
 
 
 def _stream_of(device, stream):
@@ -200,9 +200,17 @@ def _stream_of(device, stream):
     the stream, so that the allocator knows who uses the buffers."""
     if stream is not None:
         return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
-    if device.index is not None and device.index != torch.cuda.current_device():
+    if device.index != torch.cuda.current_device():
         return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    return _HERE
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _raw_stream(device):
+    """The device's current stream as the C ABI takes it (a Stream object costs more than the launches)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _workspace(n, device):
@@ -232,7 +240,7 @@ def route(x, weight, bias=None, *, topk, scoring="softmax", renormalize=True, sc
         ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
         wts = torch.empty((T, topk), dtype=torch.float32, device=dev)
         if T:
-            B.mm_router(plan, x, weight, bias, active, ids, wts, _workspace(plan.workspace_bytes, dev))
+            B.mm_router(plan, x, weight, bias, active, ids, wts, _workspace(plan.workspace_bytes, dev), _raw_stream(dev))
     return ids, wts
 
 
@@ -295,7 +303,7 @@ def moe_few(x, w1, w2, s1=None, s2=None, *, topk_ids=None, topk_weights=None, ro
                                            renormalize=renormalize, scale=route_scale, active=active)
         if T:
             B.mm_moe_few(plan, x, topk_ids, topk_weights, active, w1, s1, w2, s2, y,
-                         _workspace(plan.workspace_bytes, dev))
+                         _workspace(plan.workspace_bytes, dev), _raw_stream(dev))
     return y, topk_ids, topk_weights
 
 
@@ -309,7 +317,7 @@ def block_quantize(x, stream=None):
         q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
         s = torch.empty((M, K // 128), dtype=torch.float32, device=dev)
         if M:
-            B.mm_block_quantize(M, K, x, q, s)
+            B.mm_block_quantize(M, K, x, q, s, _raw_stream(dev))
     return q, s
 
 
@@ -343,7 +351,7 @@ def block_matmul(q, s, w, ws, offsets=None, counts=None, y=None, stream=None):
         if y is None:
             y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
         if M:
-            B.mm_block_gemm(plan, q, s, w, ws, offsets, counts, y)
+            B.mm_block_gemm(plan, q, s, w, ws, offsets, counts, y, _raw_stream(dev))
     return y
 
 
@@ -356,5 +364,5 @@ def block_linear(x, w, ws, offsets=None, counts=None, y=None, stream=None):
         if y is None:
             y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
         if M:
-            B.mm_block_linear(plan, x, w, ws, offsets, counts, y, _workspace(plan.workspace_bytes, dev))
+            B.mm_block_linear(plan, x, w, ws, offsets, counts, y, _workspace(plan.workspace_bytes, dev), _raw_stream(dev))
     return y
