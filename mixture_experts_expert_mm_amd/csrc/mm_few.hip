@@ -19,13 +19,6 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
-#ifndef CTA
-#define CTA 1
-#define CTB 2
-#define KWB 8
-#define WTA 2
-#define DA 3
-#endif
 constexpr int kMaxT = 64, kMaxE = 1025, kMaxRoutes = 64 * 33;
 constexpr int kStage = 128;            // K-values per stage of a wave
 
@@ -538,6 +531,305 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// More tokens: tiles through LDS.  With several routes an expert, the kernels
+// above read a route's row again for every 16 columns, and those reads, not
+// the weights, fill the vector memory path (64 tokens, e4m3, 32 experts:
+// Linear1 264 us for 0.94 GB of weights).  Here a workgroup takes 256 weight
+// rows of one expert, 32 a wave, and all of the expert's routes; both come by
+// LDS-DMA, 128 bytes of a weight row a stage, two stages ahead.
+// Bound: HBM.
+// ---------------------------------------------------------------------------
+namespace {
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+constexpr int kTileRows = 256;         // weight rows of a workgroup
+
+// One live expert of the batch and its routes.
+struct ExpertRoutes {
+  unsigned long long tokens[kMaxE];
+  int32_t route[kMaxT];
+  int32_t token[kMaxT];
+  float gate[kMaxT];
+  int32_t expert, n;
+};
+
+// The `index`-th live expert (n = 0 if there are fewer); as build_lists.
+__device__ void find_expert(const FewArgs& a, ExpertRoutes& X, int index) {
+  const int tid = threadIdx.x, Et = a.E + a.S, n = a.T * a.K;
+  for (int e = tid; e < Et; e += kThreads) X.tokens[e] = 0;
+  if (tid < kMaxT) X.route[tid] = 0x7fffffff, X.token[tid] = 0, X.gate[tid] = 0.0f;
+  if (tid == 0) X.n = 0, X.expert = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const int t = i / a.K, id = a.ids[i];
+    if (id >= 0 && id < a.E && (a.active == nullptr || a.active[t] != 0)) atomicOr(&X.tokens[id], 1ull << t);
+  }
+  if (a.S && tid < a.T && (a.active == nullptr || a.active[tid] != 0)) atomicOr(&X.tokens[a.E], 1ull << tid);
+  __syncthreads();
+  if (tid < 64) {
+    int before = 0;
+    for (int e0 = 0; e0 < Et; e0 += 64) {
+      const bool on = e0 + tid < Et && X.tokens[e0 + tid] != 0;
+      const uint64_t m = ballot(on);
+      if (on && before + __popcll((unsigned long long)(m & lanemask_lt())) == index) {
+        X.expert = e0 + tid;
+        X.n = __popcll(X.tokens[e0 + tid]);
+      }
+      before += __popcll((unsigned long long)m);
+    }
+  }
+  __syncthreads();
+  if (X.n == 0) return;
+  const int e = X.expert;
+  const unsigned long long mine = X.tokens[e];
+  auto place = [&](int t, int k, float gate) {
+    const int p = __popcll(mine & ((1ull << t) - 1));
+    atomicMin(&X.route[p], t * (a.K + a.S) + k);
+    atomicAdd(&X.gate[p], gate);
+    X.token[p] = t;
+  };
+  if (e < a.E) {
+    for (int i = tid; i < n; i += kThreads)
+      if (a.ids[i] == e && (mine >> (i / a.K) & 1)) place(i / a.K, i % a.K, a.weights[i]);
+  } else if (tid < a.T && (mine >> tid & 1)) {
+    place(tid, a.K, 1.0f);
+  }
+  __syncthreads();
+}
+
+// MODE 1: Linear1, A = SwiGLU(x . W1) in P parts; MODE 2: Linear2, gate * (A .
+// W2) of every route into its slot, A in P parts.  NT: route tiles of 16 held
+// at once (an expert with more goes round again).
+template <int F, int MODE, int P, int NT>
+__device__ __forceinline__ void few_tile(const FewArgs& a) {
+  constexpr int WB = weight_bytes<F>();
+  constexpr int VK = 128 / WB;                 // K-values a stage
+  constexpr int PB = MODE == 1 ? 1 : P;        // parts of the routes' operand
+  constexpr int RB = VK * 2;                   // bytes of a route's row a stage: 256 (e4m3), 128 (bf16)
+  constexpr int S = PB * NT <= 4 ? 3 : 2;      // stages in LDS
+  constexpr int XB = PB * NT * 16 * RB;        // bytes of the routes' operand a stage
+  __shared__ __attribute__((aligned(1024))) uint8_t w0[kTileRows * 128], w1[kTileRows * 128], w2[S == 3 ? kTileRows * 128 : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t x0[XB], x1[XB], x2[S == 3 ? XB : 16];
+  __shared__ ExpertRoutes X;
+  find_expert(a, X, blockIdx.y);
+  const int total = uniform(X.n);
+  if (total == 0) return;
+  const int tid = threadIdx.x, w = uniform(tid / 64), l = tid % 64, r = l % 16, g = l / 16;
+  const int e = uniform(X.expert), Kd = MODE == 1 ? a.H : a.I, N = MODE == 1 ? 2 * a.I : a.H;
+  const int row0 = (int)blockIdx.x * kTileRows, steps = Kd / VK;
+  const int64_t R = (int64_t)a.T * (a.K + a.S);
+  const uint8_t* wb = (MODE == 1 ? a.w1 : a.w2) + ((int64_t)e * N + row0) * Kd * WB;
+  const int wpitch = Kd * WB;                  // N is a multiple of 256: every tile is whole
+  // weight rows: the chunk at place p of row y is p ^ (y / 2 % 8)
+  const uint32_t wvo = (uint32_t)(l / 8) * wpitch + (((l % 8) ^ ((4 * (w % 2) + l / 16) % 8)) * 16);
+  // the wave's two tiles: gate and up of 16 columns (groups of 32 rows), or 32 columns
+  const int t0 = MODE == 1 ? 64 * (w / 2) + 16 * (w % 2) : 32 * w, t1 = t0 + (MODE == 1 ? 32 : 16);
+  const int sw = (r / 2) % 8;
+  const int wc0 = (g ^ sw) * 16 + r * 128, wc1 = ((g + 4) ^ sw) * 16 + r * 128;
+  const int sx = RB == 256 ? 8 * (r & 1) + (r >> 1) : sw;
+  const float *sp0 = nullptr, *sp1 = nullptr;  // block scales of the two tiles
+  if constexpr (F == MM_FEW_FP8_BLOCK) {
+    const int nb = Kd / 128;
+    if constexpr (MODE == 1) {
+      const int c = (row0 / 2 + 16 * w) / 128;
+      sp0 = a.s1 + ((int64_t)e * (N / 128) + c) * nb;
+      sp1 = sp0 + (int64_t)(a.I / 128) * nb;
+    } else {
+      sp0 = sp1 = a.s2 + ((int64_t)e * (N / 128) + (row0 + t0) / 128) * nb;
+    }
+  }
+
+  for (int q0 = 0; q0 < total; q0 += 16 * NT) {
+    const int n = total - q0 < 16 * NT ? total - q0 : 16 * NT, nt = (n + 15) / 16;
+    // A route's row in LDS: e4m3 weights take 16 K-values a lane and piece, two
+    // chunks of it; chunk c = 8j + 2g + h sits at place (8j + 4h + g) ^ sx(row),
+    // so that a read covers neighbouring places over g.  One instruction
+    // moves 1024 / RB rows.
+    constexpr int RPI = 1024 / RB, XI = NT * 16 / RPI;   // rows an instruction; instructions a part
+    constexpr int XW = (PB * XI + kWaves - 1) / kWaves;  // a wave (those past the last repeat one)
+    uint32_t xvo[XW];
+#pragma unroll
+    for (int i = 0; i < XW; ++i) {
+      const int at = (w + kWaves * i) % (PB * XI), part = at / XI, y = at % XI * RPI + l / (RB / 16), pos = l % (RB / 16);
+      int c;
+      if constexpr (RB == 256) {
+        const int v = pos ^ (8 * (y & 1) + (y % 16 >> 1));
+        c = (v & 8) | (v & 3) << 1 | (v >> 2 & 1);
+      } else {
+        c = pos ^ (y / 2 % 8);
+      }
+      const int64_t line = MODE == 1 ? X.token[q0 + y < total ? q0 + y : 0] : part * R + X.route[q0 + y < total ? q0 + y : 0];
+      xvo[i] = q0 + y < total ? (uint32_t)(line * Kd * 2 + c * 16) : 0x7fffff00u;   // beyond the descriptor: zeros, no access
+    }
+    const uint8_t* xb = MODE == 1 ? static_cast<const uint8_t*>(a.x) : reinterpret_cast<const uint8_t*>(a.a);
+    const int xbytes = (int)((MODE == 1 ? (int64_t)a.T : PB * R) * Kd * 2);
+    auto copy = [&](int s, uint8_t* ws, uint8_t* xs) {
+      s = s < steps ? s : steps - 1;           // past the end: the last stage again, unused
+      const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc((void*)wb, (short)0, kTileRows * wpitch, 0x00020000);
+      const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc((void*)xb, (short)0, xbytes, 0x00020000);
+#pragma unroll
+      for (int i = 0; i < kTileRows / 64; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr_t)(ws + (w + 8 * i) * 1024), 16, wvo, (w + 8 * i) * 8 * wpitch + s * 128, 0, 0);
+#pragma unroll
+      for (int i = 0; i < XW; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr_t)(xs + (w + kWaves * i) % (PB * XI) * 1024), 16, xvo[i], s * RB, 0, 0);
+    };
+    constexpr int kCopies = kTileRows / 64 + XW;
+    f32x4 acc[2][NT];
+    clear(acc);
+    auto compute = [&](const uint8_t* ws, const uint8_t* xs, float s0, float s1) {
+      f32x4 sum[2][NT];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int m = 0; m < NT; ++m) sum[i][m] = F == MM_FEW_FP8_BLOCK ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][m];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const u32x4 wa = *reinterpret_cast<const u32x4*>(ws + t0 * 128 + (j ? wc1 : wc0));
+        const u32x4 wc = *reinterpret_cast<const u32x4*>(ws + t1 * 128 + (j ? wc1 : wc0));
+#pragma unroll
+        for (int h = 0; h < 3 - WB; ++h) {     // e4m3: two operands of 8 values
+          const u32x4 oa = WB == 2 ? wa : widen8(wa[2 * h], wa[2 * h + 1]);
+          const u32x4 ob = WB == 2 ? wc : widen8(wc[2 * h], wc[2 * h + 1]);
+#pragma unroll
+          for (int m = 0; m < NT; ++m)
+            if (m == 0 || m < nt) {
+#pragma unroll
+              for (int p = 0; p < PB; ++p) {
+                const int place = (RB == 256 ? 8 * j + 4 * h + g : 4 * j + g) ^ sx;
+                const u32x4 b = *reinterpret_cast<const u32x4*>(xs + ((p * NT + m) * 16 + r) * RB + place * 16);
+                sum[0][m] = mfma16(oa, b, sum[0][m]);
+                sum[1][m] = mfma16(ob, b, sum[1][m]);
+              }
+            }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < NT; ++m) {
+        acc[0][m] = F == MM_FEW_FP8_BLOCK ? acc[0][m] + sum[0][m] * s0 : sum[0][m];
+        acc[1][m] = F == MM_FEW_FP8_BLOCK ? acc[1][m] + sum[1][m] * s1 : sum[1][m];
+      }
+    };
+    auto turn = [&]() {
+      // the stage's products stay before the wait: nothing else ties them to it
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int m = 0; m < NT; ++m) asm volatile("" : "+v"(acc[i][m]));
+      __builtin_amdgcn_sched_barrier(0);
+      // all copies but the newest stage's (S == 3) have landed
+      __builtin_amdgcn_s_waitcnt(0x0F70 | (S == 3 ? kCopies : 0));
+      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    static_assert(kCopies < 16, "the wait's field");
+    auto scales = [&](int s, float& s0, float& s1) {
+      if constexpr (F == MM_FEW_FP8_BLOCK) s0 = sp0[s < steps ? s : steps - 1], s1 = sp1[s < steps ? s : steps - 1];
+    };
+    float sa[2] = {1.0f, 1.0f}, sn[2] = {1.0f, 1.0f};
+    auto stage = [&](int s, const uint8_t* ws, const uint8_t* xs, uint8_t* nw, uint8_t* nx) {
+      scales(s + 1, sn[0], sn[1]);
+      __builtin_amdgcn_sched_barrier(0);
+      copy(s + S - 1, nw, nx);
+      compute(ws, xs, sa[0], sa[1]);
+      turn();
+      sa[0] = sn[0], sa[1] = sn[1];
+    };
+    scales(0, sa[0], sa[1]);
+    copy(0, w0, x0);
+    if constexpr (S == 3) copy(1, w1, x1);
+    turn();
+    if constexpr (S == 3) {
+      for (int s = 0; s < steps; s += 3) {
+        stage(s, w0, x0, w2, x2);
+        if (s + 1 >= steps) break;
+        stage(s + 1, w1, x1, w0, x0);
+        if (s + 2 >= steps) break;
+        stage(s + 2, w2, x2, w1, x1);
+      }
+    } else {
+      for (int s = 0; s < steps; s += 2) {
+        stage(s, w0, x0, w1, x1);
+        if (s + 1 >= steps) break;
+        stage(s + 1, w1, x1, w0, x0);
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);        // no copy outlives the round
+    __syncthreads();
+    if constexpr (MODE == 1) {
+      const int col = row0 / 2 + 16 * w + 4 * g;
+      f32x4 sg, su;
+      if constexpr (F == MM_FEW_FP8) {
+        sg = *reinterpret_cast<const f32x4*>(a.s1 + (int64_t)e * 2 * a.I + col);
+        su = *reinterpret_cast<const f32x4*>(a.s1 + (int64_t)e * 2 * a.I + a.I + col);
+      }
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+        if (16 * m + r < n) {
+          f32x4 hg = acc[0][m], hu = acc[1][m];
+          if constexpr (F == MM_FEW_FP8) hg *= sg, hu *= su;
+          uint16_t o[4][P];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) split_bf16<P>(swiglu(hg[i], hu[i], a.clamp), o[i]);
+          const int64_t route = X.route[q0 + 16 * m + r];
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+            *reinterpret_cast<u32x2*>(a.a + (p * R + route) * a.I + col) =
+                u32x2{o[0][p] | (uint32_t)o[1][p] << 16, o[2][p] | (uint32_t)o[3][p] << 16};
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int col = row0 + t0 + 16 * i + 4 * g;
+        f32x4 sc;
+        if constexpr (F == MM_FEW_FP8) sc = *reinterpret_cast<const f32x4*>(a.s2 + (int64_t)e * a.H + col);
+#pragma unroll
+        for (int m = 0; m < NT; ++m)
+          if (16 * m + r < n) {
+            f32x4 v = acc[i][m];
+            if constexpr (F == MM_FEW_FP8) v *= sc;
+            *reinterpret_cast<f32x4*>(a.slot + (int64_t)X.route[q0 + 16 * m + r] * a.H + col) = v * X.gate[q0 + 16 * m + r];
+          }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+template <int F, int MODE, int P, int NT>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_few_tile(FewArgs a) {
+  few_tile<F, MODE, P, NT>(a);
+}
+
+// y[t]: the slots of t's routes in the order of k.  A slot is one that Linear2
+// wrote: a valid id that no earlier k of the token names.
+__global__ __launch_bounds__(256) void k_few_combine(FewArgs a) {
+  const int t = blockIdx.y, c = ((int)blockIdx.x * 256 + threadIdx.x) * 4, Ks = a.K + a.S;
+  __shared__ int32_t ids[32];
+  const bool on = a.active == nullptr || a.active[t] != 0;
+  if (threadIdx.x < a.K) ids[threadIdx.x] = a.ids[t * a.K + threadIdx.x];
+  __syncthreads();
+  if (c >= a.H) return;
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (on) {
+    for (int k = 0; k < Ks; ++k) {
+      if (k < a.K) {
+        const int id = ids[k];
+        bool first = id >= 0 && id < a.E;
+        for (int j = 0; j < k; ++j) first = first && ids[j] != id;
+        if (!first) continue;
+      }
+      v += *reinterpret_cast<const f32x4*>(a.slot + ((int64_t)t * Ks + k) * a.H + c);
+    }
+  }
+  const int64_t at = (int64_t)t * a.H + c;
+  if (a.y_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = v;
+  else *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
 namespace {
 
 template <int F, int KW, int CT, int NT, int P, int D>
@@ -564,15 +856,33 @@ hipError_t run_l2(const FewArgs& a, int num_cus, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int F, int MODE, int P>
+hipError_t run_tile(const FewArgs& a, hipStream_t s) {
+  const int64_t routes = (int64_t)a.T * a.K, most = routes < a.E ? routes : a.E;   // live routed experts at most
+  const int N = MODE == 1 ? 2 * a.I : a.H;
+  const dim3 grid((unsigned)((N + kTileRows - 1) / kTileRows), (unsigned)(most + a.S));
+  hipLaunchKernelGGL((k_few_tile<F, MODE, P, MODE == 2 && P == 3 ? 2 : 4>), grid, dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
 template <int F, int P>
 hipError_t run_l1_f(const FewArgs& a, int num_cus, hipStream_t s) {
-  if (a.T <= 16) return run_l1<F, 8, CTA, 1, P, 3>(a, num_cus, s);
-  return run_l1<F, KWB, CTB, 2, P, 2>(a, num_cus, s);
+  if (few_tiles(a.T, a.y_f32)) return run_tile<F, 1, P>(a, s);
+  return run_l1<F, 8, 1, 1, P, 3>(a, num_cus, s);
 }
 template <int F, int P>
 hipError_t run_l2_f(const FewArgs& a, int num_cus, hipStream_t s) {
-  if (a.T <= 16) return run_l2<F, WTA, 1, P, P == 1 ? DA : 2>(a, num_cus, s);
-  return run_l2<F, 2, P == 1 ? 2 : 1, P, 2>(a, num_cus, s);
+  if (few_tiles(a.T, a.y_f32)) {
+    const hipError_t err = run_tile<F, 2, P>(a, s);
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL(k_few_combine, dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.T), dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  // 32 columns a unit where that still gives most CUs one: half the control per weight byte
+  if constexpr (P == 1 && F != MM_FEW_BF16) {
+    if (a.H / 32 >= num_cus * 3 / 4) return run_l2<F, 2, 1, P, 3>(a, num_cus, s);
+  }
+  return run_l2<F, 1, 1, P, P == 1 ? 4 : 2>(a, num_cus, s);
 }
 template <int P>
 hipError_t run_l1_p(const FewArgs& a, int num_cus, hipStream_t s) {
@@ -592,6 +902,9 @@ hipError_t run_l2_p(const FewArgs& a, int num_cus, hipStream_t s) {
 }
 
 }  // namespace
+
+// the tile kernels, or the streaming ones
+bool few_tiles(int64_t T, int y_f32) { return T > (y_f32 ? 8 : 16); }
 
 hipError_t launch_few_l1(const FewArgs& a, int num_cus, hipStream_t s) {
   return a.y_f32 ? run_l1_p<3>(a, num_cus, s) : run_l1_p<1>(a, num_cus, s);
