@@ -200,16 +200,16 @@ __device__ __forceinline__ void split_bf16(float v, uint16_t (&o)[P]) {
 // up rows of W1 for each CT) for a group of up to 16 * NT of its routes; the 8 waves share
 // the hidden dimension, stage by stage, and their sums meet in LDS.  D
 // stages of a wave are in flight, across units.
-template <int F, int KW, int CT, int NT, int P, int D>
+template <int F, int CT, int NT, int P, int D>
 __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
   __shared__ Lists L;
   constexpr int WT = 2 * CT;
-  constexpr bool kShared = KW > 1;      // waves that share a unit
-  __shared__ f32x4 red[kShared ? kWaves : 1][WT][NT][64];
+  // two buffers: a unit's sums are read while the next unit's are written
+  __shared__ f32x4 red[2][kWaves][WT][NT][64];
   build_lists(a, L, 16 * NT);
   const int w = uniform(threadIdx.x / 64), l = threadIdx.x % 64, r = l % 16, g = l / 16;
   constexpr int WB = weight_bytes<F>();
-  const int nst = a.H / kStage, nsw = (nst + KW - 1) / KW, kw = w % KW, cols = a.I / (16 * CT);
+  const int nst = a.H / kStage, nsw = (nst + kWaves - 1) / kWaves, cols = a.I / (16 * CT);
   const int units = uniform(L.live) * cols;
   const int64_t R = (int64_t)a.T * (a.K + a.S);
 
@@ -221,8 +221,7 @@ __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
     const uint8_t* bp[NT];
     const float* sp[2];
   };
-  const int first = (int)blockIdx.x * (kWaves / KW) + w / KW, stride = gridDim.x * (kWaves / KW);
-  if (first >= units) return;
+  if ((int)blockIdx.x >= units) return;
   // Past the last unit a cursor keeps its pointers: its loads go on, into
   // stages that nothing multiplies.  A load under a condition would make the
   // compiler wait for every load in flight before each product.
@@ -258,12 +257,12 @@ __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
       ++cu.q;
     } else {
       cu.q = 0;
-      cu.u += stride;
+      cu.u += gridDim.x;
     }
     aim(cu);
   };
   auto load = [&](const Cursor& cu, Stage<F, WT, NT, 1>& st) {
-    const int js = cu.j * KW + kw, s = js < nst ? js : nst - 1;
+    const int js = cu.j * kWaves + w, s = js < nst ? js : nst - 1;
     load_weights<F, WT, NT, 1>(st, cu.wp, (int64_t)s * (kStage * WB), g);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -277,12 +276,13 @@ __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
   };
 
   Cursor ld{}, cu{};
-  ld.u = cu.u = first;
+  ld.u = cu.u = blockIdx.x;
   aim(ld);
   aim(cu);
   Stage<F, WT, NT, 1> st[D];
   f32x4 acc[WT][NT];
   clear(acc);
+  int side = 0;
 #pragma unroll
   for (int d = 0; d < D; ++d) {
     load(ld, st[d]);
@@ -291,49 +291,20 @@ __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
   while (cu.u < units) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      if (cu.u < units && cu.j * KW + kw < nst) multiply<F, WT, NT, 1>(st[d], acc, (cu.n + 15) / 16);
+      if (cu.u < units && cu.j * kWaves + w < nst) multiply<F, WT, NT, 1>(st[d], acc, (cu.n + 15) / 16);
       load(ld, st[d]);
       if (ld.u < units) step(ld);
       if (cu.u < units) {
         if (cu.j + 1 == nsw) {
-          if constexpr (!kShared) {
-            // a lane has gate and up of four columns of one route
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-              const int col = (cu.c * CT + c) * 16 + 4 * g;
-              f32x4 sg, su;
-              if constexpr (F == MM_FEW_FP8) {
-                sg = *reinterpret_cast<const f32x4*>(a.s1 + (int64_t)cu.e * 2 * a.I + col);
-                su = *reinterpret_cast<const f32x4*>(a.s1 + (int64_t)cu.e * 2 * a.I + a.I + col);
-              }
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                f32x4 hg = acc[2 * c][n], hu = acc[2 * c + 1][n];
-                if constexpr (F == MM_FEW_FP8) hg *= sg, hu *= su;
-                uint16_t o[4][P];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) split_bf16<P>(swiglu(hg[i], hu[i], a.clamp), o[i]);
-                if (16 * n + r < cu.n) {
-                  const int64_t route = L.route[cu.n0 + 16 * n + r];
-#pragma unroll
-                  for (int p = 0; p < P; ++p)
-                    *reinterpret_cast<u32x2*>(a.a + (p * R + route) * a.I + col) =
-                        u32x2{o[0][p] | (uint32_t)o[1][p] << 16, o[2][p] | (uint32_t)o[3][p] << 16};
-                }
-              }
-            }
-            clear(acc);
-            step(cu);
-            continue;
-          }
           // the unit's sums: 8 waves' parts, SwiGLU, A
 #pragma unroll
           for (int i = 0; i < WT; ++i)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) red[w][i][n][l] = acc[i][n];
+            for (int n = 0; n < NT; ++n) red[side][w][i][n][l] = acc[i][n];
           clear(acc);
           __syncthreads();
-          const float* rf = reinterpret_cast<const float*>(red);
+          const float* rf = reinterpret_cast<const float*>(red[side]);
+          side ^= 1;
           const int n16 = cu.n < 16 * NT ? cu.n : 16 * NT;
           for (int i = threadIdx.x; i < 16 * CT * n16; i += kThreads) {
             // column c (of 16, in tile ct) of list entry m: accumulator c % 4 of lane 16 * (c / 4) + m % 16
@@ -356,7 +327,6 @@ __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
 #pragma unroll
             for (int p = 0; p < P; ++p) a.a[(p * R + route) * a.I + col] = o[p];
           }
-          __syncthreads();
         }
         step(cu);
       }
@@ -372,7 +342,8 @@ template <int F, int WT, int NT, int P, int D>
 __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
   __shared__ Lists L;
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
-  f32x4* ys = reinterpret_cast<f32x4*>(dyn);   // [kWaves][T][4 * WT]
+  f32x4* ys = reinterpret_cast<f32x4*>(dyn);   // [2][kWaves][T][4 * WT]: one of the two is added and cleared while the other fills
+  const int ylen = kWaves * a.T * 4 * WT;
   build_lists(a, L, 16 * NT);
   const int w = uniform(threadIdx.x / 64), l = threadIdx.x % 64, r = l % 16, g = l / 16;
   constexpr int WB = weight_bytes<F>();
@@ -381,7 +352,7 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
   const int64_t R = (int64_t)a.T * (a.K + a.S);
   const int live = uniform(L.live), visits = uniform(L.visit[live]);
   const int total = visits * nst, nsw = total > kWaves ? (total + kWaves - 1) / kWaves : 1;
-  for (int i = threadIdx.x; i < kWaves * a.T * 4 * WT; i += kThreads) ys[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = threadIdx.x; i < 2 * ylen; i += kThreads) ys[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
 
   if (total == 0) {          // no route at all
@@ -473,6 +444,7 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
   Stage<F, WT, NT, P> st[D];
   f32x4 acc[WT][NT];
   clear(acc);
+  int side = 0;
 #pragma unroll
   for (int d = 0; d < D; ++d) {
     load(ld, st[d]);
@@ -493,7 +465,7 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
             const int i = 16 * n + r;
             if (i < cu.n) {
               const float gate = L.gate[cu.n0 + i];
-              f32x4* y = ys + ((int64_t)w * a.T + L.token[cu.n0 + i]) * (4 * WT) + g;
+              f32x4* y = ys + side * ylen + ((int64_t)w * a.T + L.token[cu.n0 + i]) * (4 * WT) + g;
 #pragma unroll
               for (int k = 0; k < WT; ++k) {
                 f32x4 v = acc[k][n];
@@ -508,13 +480,15 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
         if (last) {
           __syncthreads();
           // thread: 4 columns of a token
+          f32x4* yu = ys + side * ylen;
+          side ^= 1;
           for (int i = threadIdx.x; i < a.T * 4 * WT; i += kThreads) {
-            f32x4 v = ys[i];
-            ys[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            f32x4 v = yu[i];
+            yu[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int k = 1; k < kWaves; ++k) {
-              v += ys[(int64_t)k * a.T * 4 * WT + i];
-              ys[(int64_t)k * a.T * 4 * WT + i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+              v += yu[(int64_t)k * a.T * 4 * WT + i];
+              yu[(int64_t)k * a.T * 4 * WT + i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             }
             const int64_t at = (int64_t)(i / (4 * WT)) * a.H + cu.u * 16 * WT + (i % (4 * WT)) * 4;
             if (a.y_f32) {
@@ -523,7 +497,6 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
               *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
             }
           }
-          __syncthreads();
         }
         step(cu);
       }
@@ -832,24 +805,23 @@ __global__ __launch_bounds__(256) void k_few_combine(FewArgs a) {
 
 namespace {
 
-template <int F, int KW, int CT, int NT, int P, int D>
+template <int F, int CT, int NT, int P, int D>
 hipError_t run_l1(const FewArgs& a, int num_cus, hipStream_t s) {
   const int64_t routes = (int64_t)a.T * a.K + (a.S ? a.T : 0);
   const int64_t live = routes < a.E + a.S ? routes : a.E + a.S;
   const int64_t units = live * (a.I / (16 * CT));
-  const int64_t blocks = (units * KW + kWaves - 1) / kWaves;
-  const int grid = (int)(blocks < num_cus ? blocks : num_cus);
-  hipLaunchKernelGGL((k_few_l1<F, KW, CT, NT, P, D>), dim3(grid), dim3(kThreads), 0, s, a);
+  const int grid = (int)(units < num_cus ? units : num_cus);
+  hipLaunchKernelGGL((k_few_l1<F, CT, NT, P, D>), dim3(grid), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
 template <int F, int WT, int NT, int P, int D>
 hipError_t run_l2(const FewArgs& a, int num_cus, hipStream_t s) {
   const int units = a.H / (16 * WT);
-  const size_t lds = (size_t)kWaves * a.T * 4 * WT * 16;
+  const size_t lds = (size_t)2 * kWaves * a.T * 4 * WT * 16;
   if (lds > 32768) {   // beside the lists, more than 64 KiB
     const hipError_t err = hipFuncSetAttribute((const void*)k_few_l2<F, WT, NT, P, D>,
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, kWaves * kMaxT * 4 * WT * 16);
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (err != hipSuccess) return err;
   }
   hipLaunchKernelGGL((k_few_l2<F, WT, NT, P, D>), dim3(units < num_cus ? units : num_cus), dim3(kThreads), lds, s, a);
@@ -868,7 +840,7 @@ hipError_t run_tile(const FewArgs& a, hipStream_t s) {
 template <int F, int P>
 hipError_t run_l1_f(const FewArgs& a, int num_cus, hipStream_t s) {
   if (few_tiles(a.T, a.y_f32)) return run_tile<F, 1, P>(a, s);
-  return run_l1<F, 8, 1, 1, P, 3>(a, num_cus, s);
+  return run_l1<F, 1, 1, P, 3>(a, num_cus, s);
 }
 template <int F, int P>
 hipError_t run_l2_f(const FewArgs& a, int num_cus, hipStream_t s) {
