@@ -839,22 +839,28 @@ hipError_t run_tile(const FewArgs& a, hipStream_t s) {
 
 template <int F, int P>
 hipError_t run_l1_f(const FewArgs& a, int num_cus, hipStream_t s) {
-  if (few_tiles(a.T, a.y_f32)) return run_tile<F, 1, P>(a, s);
+  // 16 tokens, 32 experts of 7168 x 2048, top-8, us for the whole layer with
+  // streaming / tile Linear1: bf16 468 / 519, e4m3 253 / 269; 64 tokens e4m3: 420 / 305
+  if (a.T > 16) return run_tile<F, 1, P>(a, s);
   return run_l1<F, 1, 1, P, 3>(a, num_cus, s);
 }
 template <int F, int P>
 hipError_t run_l2_f(const FewArgs& a, int num_cus, hipStream_t s) {
-  if (few_tiles(a.T, a.y_f32)) {
+  if (few_slots(a.T, a.y_f32)) {
     const hipError_t err = run_tile<F, 2, P>(a, s);
     if (err != hipSuccess) return err;
     hipLaunchKernelGGL(k_few_combine, dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.T), dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  // 32 columns a unit where that still gives most CUs one: half the control per weight byte
-  if constexpr (P == 1 && F != MM_FEW_BF16) {
-    if (a.H / 32 >= num_cus * 3 / 4) return run_l2<F, 2, 1, P, 3>(a, num_cus, s);
+  if constexpr (P == 1) {
+    // 32 columns a unit where that still gives most CUs one: half the control
+    // per weight byte (e4m3, one token: 30 against 37 us; bf16, at 5.9 TB/s
+    // within a unit, loses by the missing units: 56 against 51 us)
+    if (F != MM_FEW_BF16 && a.H / 32 >= num_cus * 3 / 4) return run_l2<F, 2, 1, P, 3>(a, num_cus, s);
+    return run_l2<F, 1, 1, P, 4>(a, num_cus, s);
+  } else {
+    return hipErrorInvalidValue;               // float32 y always takes the tiles
   }
-  return run_l2<F, 1, 1, P, P == 1 ? 4 : 2>(a, num_cus, s);
 }
 template <int P>
 hipError_t run_l1_p(const FewArgs& a, int num_cus, hipStream_t s) {
@@ -875,8 +881,12 @@ hipError_t run_l2_p(const FewArgs& a, int num_cus, hipStream_t s) {
 
 }  // namespace
 
-// the tile kernels, or the streaming ones
-bool few_tiles(int64_t T, int y_f32) { return T > (y_f32 ? 8 : 16); }
+// Linear2 through slots (tiles and a combine), or streaming.  The three parts
+// of A that a float32 y takes cost the streaming kernel a read each per 16
+// columns.  us for the whole layer, streaming / tiles, e4m3: float32 y 1 token
+// 99 / 82, 4 tokens 214 / 176, 16 tokens 360 / 253; bf16 y 77 / 81, 156 / 172,
+// 231 / 243, 64 tokens 440 / 305.
+bool few_slots(int64_t T, int y_f32) { return y_f32 || T > 16; }
 
 hipError_t launch_few_l1(const FewArgs& a, int num_cus, hipStream_t s) {
   return a.y_f32 ? run_l1_p<3>(a, num_cus, s) : run_l1_p<1>(a, num_cus, s);

@@ -865,7 +865,7 @@ mm_status mm_few_plan_create(const mm_few_problem* problem, mm_few_plan* plan) {
   const int64_t planes = p.y_dtype == MM_OUT_F32 ? 3 : 1;
   const int64_t routes = p.num_tokens * (p.num_topk + p.num_shared_experts);
   pl.reserved[0] = align_up(planes * routes * p.intermediate_hidden * 2, kAlign);   // bytes of A's parts
-  pl.workspace_bytes = pl.reserved[0] + (few_tiles(p.num_tokens, p.y_dtype == MM_OUT_F32) ? align_up(routes * p.hidden * 4, kAlign) : 0);
+  pl.workspace_bytes = pl.reserved[0] + (few_slots(p.num_tokens, p.y_dtype == MM_OUT_F32) ? align_up(routes * p.hidden * 4, kAlign) : 0);
   pl.checksum = plan_checksum(&pl);
   *plan = pl;
   return MM_OK;
@@ -890,7 +890,7 @@ mm_status mm_moe_few(const mm_few_plan* plan, const void* x, const int32_t* topk
   a.w2 = static_cast<const uint8_t*>(w2);
   a.s2 = w2_scale;
   a.a = at<uint16_t>(workspace, 0);
-  a.slot = at<float>(workspace, plan->reserved[0]);   // (few_tiles)
+  a.slot = at<float>(workspace, plan->reserved[0]);   // (few_slots)
   a.y = y;
   a.T = (int)p.num_tokens;
   a.H = (int)p.hidden;

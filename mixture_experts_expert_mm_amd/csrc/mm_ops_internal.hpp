@@ -45,13 +45,14 @@ struct FewArgs {
   const uint8_t* w2;         // [E+S][H][I]
   const float* s2;           // [E+S][H], or [E+S][H/128][I/128]
   uint16_t* a;               // ws: [planes][T*(K+S)][I] bf16 parts of A
-  float* slot;               // ws: [T*(K+S)][H] gate-weighted contributions (few_tiles)
+  float* slot;               // ws: [T*(K+S)][H] gate-weighted contributions (few_slots)
   void* y;                   // [T][H]
   int T, H, I, E, K, S;
   int format, y_f32;
   float clamp;               // +inf: none
 };
-bool few_tiles(int64_t T, int y_f32);
+// whether Linear2 takes slots of the workspace
+bool few_slots(int64_t T, int y_f32);
 hipError_t launch_few_l1(const FewArgs& a, int num_cus, hipStream_t s);
 hipError_t launch_few_l2(const FewArgs& a, int num_cus, hipStream_t s);
 
