@@ -26,7 +26,6 @@ struct RouterArgs {
 };
 struct RouterShape {
   int wide;                  // 0: 16 x 16 a wave; 1: 64 tokens x 64 experts a wave; 2: LDS tiles
-  int ew;                    // waves of a workgroup side by side along the experts (wide)
   int ks;                    // slices of the hidden dimension over workgroups
   int ep;                    // padded experts of a row of partial scores
 };

@@ -13,8 +13,8 @@
 // step rounds a partial sum that Cauchy-Schwarz bounds by |x| |w|; the
 // roundings are independent), so the selection carries that bound per
 // expert, and where the best and another expert are closer than their
-// bounds, both are summed again in 64 bits.  A few in a hundred tokens need
-// it, for two experts each.
+// bounds, both are summed again in 64 bits.  About one token in a hundred needs
+// it, for two experts.
 #include "mm_router_dev.hpp"
 
 namespace mm {
@@ -42,20 +42,18 @@ __device__ __forceinline__ float sumsq(const u32x4& v, float acc) {
 
 }  // namespace
 
-// TT x ET tiles of 16 tokens x 16 experts a wave; EW waves along the experts,
-// KW = 8 / EW along the hidden dimension, added in LDS in a fixed order.
+// TT x ET tiles of 16 tokens x 16 experts a wave; the 8 waves share the hidden
+// dimension and are added in LDS in a fixed order.
 // Lane l of a tile holds 8 consecutive hidden values of expert (A) and token
 // (B) l % 16; accumulator i is expert 4 * (l / 16) + i of token l % 16.
-template <int TT, int ET, int EW>
+template <int TT, int ET>
 __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
-  constexpr int KW = kWaves / EW;
-  constexpr int kSlots = KW > 1 ? KW / 2 * EW : 1;
+  constexpr int KW = kWaves, kSlots = KW / 2;
   __shared__ f32x4 red[kSlots][TT * ET][64];
-  __shared__ float xn[KW][TT * 16], wn[KW][EW * ET * 16];
-  const int w = threadIdx.x / 64, l = threadIdx.x % 64, r = l % 16, g = l / 16;
-  const int ew = w % EW, kw = w / EW;
+  __shared__ float xn[KW][TT * 16], wn[KW][ET * 16];
+  const int kw = threadIdx.x / 64, l = threadIdx.x % 64, r = l % 16, g = l / 16;
   const int64_t t0 = (int64_t)blockIdx.x * (16 * TT);
-  const int e0 = (int)blockIdx.y * (16 * ET * EW) + ew * (16 * ET);
+  const int e0 = (int)blockIdx.y * (16 * ET);
   const uint8_t *xp[TT], *wp[ET];
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
@@ -77,7 +75,7 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
   for (int i = 0; i < TT; ++i)
 #pragma unroll
     for (int j = 0; j < ET; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const bool do_x = blockIdx.y == 0 && ew == 0, do_w = blockIdx.x == 0;
+  const bool do_x = blockIdx.y == 0, do_w = blockIdx.x == 0;
   const int steps = a.H / kRouterStep, q = (int)blockIdx.z * KW + kw, Q = KW * a.KS;
 #pragma unroll TT == 1 ? 4 : 2
   for (int s = q; s < steps; s += Q) {
@@ -111,14 +109,14 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
     float v = xs[i];
     v += __shfl_xor(v, 16, 64);
     v += __shfl_xor(v, 32, 64);
-    if (ew == 0 && g == 0) xn[kw][16 * i + r] = v;
+    if (g == 0) xn[kw][16 * i + r] = v;
   }
 #pragma unroll
   for (int j = 0; j < ET; ++j) {
     float v = ws[j];
     v += __shfl_xor(v, 16, 64);
     v += __shfl_xor(v, 32, 64);
-    if (g == 0) wn[kw][(ew * ET + j) * 16 + r] = v;
+    if (g == 0) wn[kw][j * 16 + r] = v;
   }
 #pragma unroll
   for (int h = KW / 2; h >= 1; h /= 2) {
@@ -126,18 +124,17 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
 #pragma unroll
       for (int i = 0; i < TT; ++i)
 #pragma unroll
-        for (int j = 0; j < ET; ++j) red[(kw - h) * EW + ew][i * ET + j][l] = acc[i][j];
+        for (int j = 0; j < ET; ++j) red[kw - h][i * ET + j][l] = acc[i][j];
     }
     __syncthreads();
     if (kw < h) {
 #pragma unroll
       for (int i = 0; i < TT; ++i)
 #pragma unroll
-        for (int j = 0; j < ET; ++j) acc[i][j] += red[kw * EW + ew][i * ET + j][l];
+        for (int j = 0; j < ET; ++j) acc[i][j] += red[kw][i * ET + j][l];
     }
     __syncthreads();
   }
-  if constexpr (KW == 1) __syncthreads();
   float* part = a.part + (int64_t)blockIdx.z * a.T * a.Ep;
   if (kw == 0) {
 #pragma unroll
@@ -156,8 +153,8 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
     for (int k = 0; k < KW; ++k) v += xn[k][threadIdx.x];
     a.xnorm[(int64_t)blockIdx.z * a.T + t0 + threadIdx.x] = v;
   }
-  if (do_w && (int)threadIdx.x < EW * ET * 16) {
-    const int e = (int)blockIdx.y * (16 * ET * EW) + threadIdx.x;
+  if (do_w && (int)threadIdx.x < ET * 16) {
+    const int e = (int)blockIdx.y * (16 * ET) + threadIdx.x;
     float v = 0.0f;
 #pragma unroll
     for (int k = 0; k < KW; ++k) v += wn[k][threadIdx.x];
@@ -298,14 +295,21 @@ __global__ __launch_bounds__(kThreads) void k_router_tile(RouterArgs a) {
   }
 }
 
-// One wave per token.
-template <int NV>
+// One wave per token.  (Four tokens a wave in turn, the next one's scores
+// asked for meanwhile, took 58 against 42 us at 16384 x 256: a token that needs
+// 64-bit sums then holds up three others.)  Bound: issue, about 500
+// instructions a token, and the latency of the scores.
+template <int NV, int KM>
 __global__ __launch_bounds__(256, NV <= 4 ? 4 : 1) void k_router_select(RouterArgs a) {
   const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
   if (t >= a.T) return;
+  RouterExperts<NV> ex;
+  RouterToken<NV, KM> tok;
+  router_load_token<NV, KM>(a, t, tok);
+  router_load_experts<NV, KM>(a, ex);
   int id;
   float w;
-  router_select_token<NV>(a, t, id, w);
+  router_select_token<NV, KM>(a, t, ex, tok, id, w);
   const int l = lane_id();
   if (l < a.K) {
     a.ids[t * a.K + l] = id;
@@ -317,23 +321,22 @@ __global__ __launch_bounds__(256, NV <= 4 ? 4 : 1) void k_router_select(RouterAr
 // tiles over as many workgroups as the hidden dimension gives (us for both
 // kernels, 16 x 16 / 64 x 64 a wave, hidden 7168: 333 tokens x 32 experts
 // 17 / 20, 1000 x 32 22 / 23, 1000 x 64 30 / 27, 4000 x 32 44 / 34).  Beyond, with
-// up to 128 experts, a wave holds 64 x 64 and the waves share the hidden
-// dimension; with more experts the LDS tiles (16384 x 256: 210 and 92 us for
-// the scores alone).
+// up to 64 experts, a wave holds 64 x 64 and the waves share the hidden
+// dimension; with more experts the LDS tiles (64 x 64 a wave / tiles: 16384 x
+// 32 81 / 94, 16384 x 64 91 / 95, 2000 x 128 40 / 38, 16384 x 128 144 / 110, 16384 x
+// 256 210 / 92 for the scores alone).
 RouterShape router_shape(int64_t T, int H, int E) {
   RouterShape s{};
   const int steps = H / kRouterStep;
   s.ep = (E + 15) / 16 * 16;
-  s.wide = T <= 64 || T * E <= 32768 ? 0 : E <= 128 ? 1 : 2;
+  s.wide = T <= 64 || T * E <= 32768 ? 0 : E <= 64 ? 1 : 2;
   int64_t tiles = 1, most = steps / (kWaves * 4);
   if (s.wide == 0) {
-    s.ew = 1;
     s.ks = (int)most;
   } else {
     if (s.wide == 1) {
-      s.ew = E <= 64 ? 1 : 2;
-      tiles = (T + 63) / 64 * ((E + 64 * s.ew - 1) / (64 * s.ew));
-      most = steps / (2 * (kWaves / s.ew));
+      tiles = (T + 63) / 64;
+      most = steps / (2 * kWaves);
     } else {
       tiles = (T + kTileT - 1) / kTileT * ((E + kTileE - 1) / kTileE);
       most = steps / 8;
@@ -350,7 +353,7 @@ hipError_t launch_router_scores(const RouterArgs& a, hipStream_t s) {
   const RouterShape sh = router_shape(a.T, a.H, a.E);
   if (sh.wide == 0) {
     const dim3 grid((unsigned)((a.T + 15) / 16), (unsigned)(a.Ep / 16), (unsigned)a.KS);
-    hipLaunchKernelGGL((k_router_scores<1, 1, 1>), grid, dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((k_router_scores<1, 1>), grid, dim3(kThreads), 0, s, a);
     return hipGetLastError();
   }
   if (sh.wide == 2) {
@@ -359,20 +362,27 @@ hipError_t launch_router_scores(const RouterArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(k_router_tile, grid, dim3(kThreads), 0, s, a);
     return hipGetLastError();
   }
-  const int per = 64 * sh.ew;
-  const dim3 grid((unsigned)((a.T + 63) / 64), (unsigned)((a.E + per - 1) / per), (unsigned)a.KS);
-  if (sh.ew == 1) hipLaunchKernelGGL((k_router_scores<4, 4, 1>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((k_router_scores<4, 4, 2>), grid, dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((k_router_scores<4, 4>), dim3((unsigned)((a.T + 63) / 64), 1, (unsigned)a.KS), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
-hipError_t launch_router_select(const RouterArgs& a, hipStream_t s) {
+namespace {
+
+template <int NV>
+hipError_t run_select(const RouterArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)((a.T + 3) / 4));
-  if (a.E <= 64) hipLaunchKernelGGL(k_router_select<1>, grid, dim3(256), 0, s, a);
-  else if (a.E <= 128) hipLaunchKernelGGL(k_router_select<2>, grid, dim3(256), 0, s, a);
-  else if (a.E <= 256) hipLaunchKernelGGL(k_router_select<4>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(k_router_select<16>, grid, dim3(256), 0, s, a);
+  if (a.KS <= 2) hipLaunchKernelGGL((k_router_select<NV, 2>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_router_select<NV, 8>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_router_select(const RouterArgs& a, hipStream_t s) {
+  if (a.E <= 64) return run_select<1>(a, s);
+  if (a.E <= 128) return run_select<2>(a, s);
+  if (a.E <= 256) return run_select<4>(a, s);
+  return run_select<16>(a, s);
 }
 
 }  // namespace mm

@@ -58,40 +58,69 @@ __device__ __forceinline__ float rank_value(uint32_t k) {
   return k == 1u ? __builtin_nanf("") : __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// Lane l holds experts l, l + 64, ...; lane k returns the k-th expert and its
-// weight (-1 and 0 where none is left).  First the K + 1 largest float32
-// ranks are taken in turn; if each is above the next by more than both may be
-// off, their order is that of the 64-bit ranks.  If not (a few tokens in a
-// hundred), the token is selected again with a bound for each expert: where
-// another expert's reaches the best one's, both get their 64-bit sums, and
-// the set is compared in 64 bits.
+// KM: most slices of the hidden dimension (2 or 8), all asked for at once.
+
+// What does not change from token to token: lane l holds experts l, l + 64, ...
 template <int NV>
-__device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t t, int& id, float& weight) {
+struct RouterExperts {
+  float norm[NV], bias[NV];      // |w|; bias
+};
+// One token's partial scores, all asked for at once.
+template <int NV, int KM>
+struct RouterToken {
+  float xx[KM], part[NV][KM];
+  int active;
+};
+
+template <int NV, int KM>
+__device__ __forceinline__ void router_load_experts(const RouterArgs& a, RouterExperts<NV>& x) {
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int e = lane_id() + 64 * v < a.E ? lane_id() + 64 * v : 0;
+    x.bias[v] = a.bias != nullptr ? a.bias[e] : 0.0f;
+    float p[KM], s;
+#pragma unroll
+    for (int k = 0; k < KM; ++k)
+      if (k == 0 || k < a.KS) p[k] = a.wnorm[(int64_t)k * a.Ep + e];
+    s = p[0];
+#pragma unroll
+    for (int k = 1; k < KM; ++k)
+      if (k < a.KS) s += p[k];
+    x.norm[v] = __builtin_amdgcn_sqrtf(s);
+  }
+}
+
+template <int NV, int KM>
+__device__ __forceinline__ void router_load_token(const RouterArgs& a, int64_t t, RouterToken<NV, KM>& x) {
+  x.active = a.active == nullptr ? 1 : a.active[t];
+#pragma unroll
+  for (int k = 0; k < KM; ++k)
+    if (k == 0 || k < a.KS) {
+      x.xx[k] = a.xnorm[(int64_t)k * a.T + t];
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        x.part[v][k] = a.part[((int64_t)k * a.T + t) * a.Ep + (lane_id() + 64 * v < a.E ? lane_id() + 64 * v : 0)];
+    }
+}
+
+// Lane k returns the k-th expert of token t and its weight (-1 and 0 where
+// none is left).  First the K + 1 largest float32 ranks are taken in turn; if
+// each is above the next by more than both may be off, their order is that of
+// the 64-bit ranks.  If not (a token in a hundred), the token is selected
+// again with a bound for each expert: where another expert's reaches the best
+// one's, both get their 64-bit sums, and the set is compared in 64 bits.
+template <int NV, int KM>
+__device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t t, const RouterExperts<NV>& ex,
+                                                    const RouterToken<NV, KM>& tok, int& id, float& weight) {
   const int l = lane_id();
   id = -1;
   weight = 0.0f;
-  if (a.active != nullptr && a.active[t] == 0) return;
+  if (tok.active == 0) return;
   const bool sig = a.scoring == MM_ROUTER_SIGMOID, biased = a.bias != nullptr;
-  constexpr int kMost = 8;     // most slices of the hidden dimension; all are asked for at once
-  float xp[kMost], sp[NV][kMost], wp[NV][kMost], bp[NV];
+  float xx = tok.xx[0];
 #pragma unroll
-  for (int k = 0; k < kMost; ++k)
-    if (k == 0 || k < a.KS) xp[k] = a.xnorm[(int64_t)k * a.T + t];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int e = l + 64 * v < a.E ? l + 64 * v : 0;
-    bp[v] = biased ? a.bias[e] : 0.0f;
-#pragma unroll
-    for (int k = 0; k < kMost; ++k)
-      if (k == 0 || k < a.KS) {
-        sp[v][k] = a.part[((int64_t)k * a.T + t) * a.Ep + e];
-        wp[v][k] = a.wnorm[(int64_t)k * a.Ep + e];
-      }
-  }
-  float xx = xp[0];
-#pragma unroll
-  for (int k = 1; k < kMost; ++k)
-    if (k < a.KS) xx += xp[k];
+  for (int k = 1; k < KM; ++k)
+    if (k < a.KS) xx += tok.xx[k];
   float z[NV], err[NV];        // score argument; bound on the rank's error
   uint32_t key[NV];
   // Every step of a score's float32 sum rounds a partial sum, and the
@@ -106,12 +135,12 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
   for (int v = 0; v < NV; ++v) {
     z[v] = 0.0f, err[v] = 0.0f, key[v] = 0;
     if (l + 64 * v >= a.E) continue;
-    float s = sp[v][0], ww = wp[v][0];
+    float s = tok.part[v][0];
 #pragma unroll
-    for (int k = 1; k < kMost; ++k)
-      if (k < a.KS) s += sp[v][k], ww += wp[v][k];
-    const float b = bp[v];
-    float d = unit * (0.125f * __builtin_amdgcn_sqrtf(ww) * xnorm + fabsf(s)) + 1e-36f, rank;
+    for (int k = 1; k < KM; ++k)
+      if (k < a.KS) s += tok.part[v][k];
+    const float b = ex.bias[v], wn = ex.norm[v];
+    float d = unit * (0.125f * wn * xnorm + fabsf(s)) + 1e-36f, rank;
     if (sig) {
       z[v] = s;
       rank = s;
@@ -126,7 +155,7 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
     d += 2.4e-7f * fabsf(rank);
     if (b == -__builtin_huge_valf()) continue;             // switched off
     key[v] = rank_key(rank);
-    if (!(fabsf(rank) <= 3.0e38f) && !(xx < 1e36f && ww < 1e36f) && xx == xx && ww == ww) {
+    if (!(fabsf(rank) <= 3.0e38f) && !(xx < 1e36f && wn < 1e18f) && xx == xx && wn == wn) {
       lost = true;
       err[v] = __builtin_huge_valf();
     } else {
