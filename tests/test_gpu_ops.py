@@ -60,6 +60,17 @@ def test_router(T, H, E, K, scoring, bias):
     check_router(x, w, b, K, scoring, renormalize=E % 2 == 0, scale=2.5 if bias else 1.0)
 
 
+@pytest.mark.parametrize("T,H,E,K", [(600, 512, 64, 8), (1100, 256, 33, 4), (2500, 2048, 48, 6), (530, 1280, 65, 8),
+                                     (1000, 1024, 300, 10), (2049, 2304, 128, 8), (300, 7168, 256, 8), (33000, 256, 66, 2)])
+@pytest.mark.parametrize("scoring,bias", [("softmax", False), ("sigmoid", True)])
+def test_router_many_tokens(T, H, E, K, scoring, bias):
+    """The kernels that share a tile among tokens: 64 x 64 up to 64 experts, 128 x 256 beyond, one to eight slices."""
+    log(f"[router many] T={T} H={H} E={E} K={K} {scoring} bias={bias}")
+    x, w, b = router_case(T, H, E, K, scoring, bias, 7 * T + E)
+    active = (torch.rand(T, generator=gen(E)) > 0.1).to(torch.int8)
+    check_router(x, w, b, K, scoring, active=active)
+
+
 def test_router_inactive_and_switched_off():
     x, w, b = router_case(100, 512, 12, 4, "softmax", True, 3)
     active = (torch.rand(100, generator=gen(4)) > 0.3).to(torch.int8)
@@ -204,6 +215,16 @@ def test_few(T, H, I, E, K, fmt, y_dtype):
     check_few(T, H, I, E, K, fmt, y_dtype, 100 * T + E)
 
 
+@pytest.mark.parametrize("T,H,I,E,K", [(1, 6144, 128, 3, 2), (5, 7168, 256, 2, 2), (16, 6144, 384, 2, 1), (3, 2048, 1408, 4, 3),
+                                       (17, 2048, 1408, 3, 2), (64, 1280, 640, 2, 2)])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp8_block"])
+@pytest.mark.parametrize("y_dtype", ["bf16", "f32"])
+def test_few_long_rows(T, H, I, E, K, fmt, y_dtype):
+    """Many steps along both contracted dimensions, and output wide enough for two tiles a wave."""
+    log(f"[few long] T={T} H={H} I={I} E={E} K={K} {fmt} {y_dtype}")
+    check_few(T, H, I, E, K, fmt, y_dtype, 100 * T + E, masked=0.2)
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp8_block"])
 @pytest.mark.parametrize("T", [1, 5, 40])
 def test_few_shared_masked_inactive_clamped(fmt, T):
@@ -341,11 +362,26 @@ def test_block_matmul(M, N, K):
     assert torch.equal(moe.block_linear(x.cuda(), w[0].cuda(), ws[0].cuda()).view(torch.int16), y.view(torch.int16))
 
 
+@pytest.mark.parametrize("M,N,K", [(1000, 5120, 384), (900, 6160, 640), (1792, 4096, 128), (1800, 4096, 640), (1900, 4112, 384),
+                                   (2048, 3616, 256), (1700, 4224, 896), (4097, 2064, 512)])
+def test_block_matmul_many_tiles(M, N, K):
+    """More tiles than compute units, small and large ones, odd and even runs of K-blocks, halves and remainders of rows."""
+    test_block_matmul(M, N, K)
+
+
+def test_block_matmul_many_groups():
+    """Large tiles over groups: every kind of remainder in one call."""
+    g = gen(12)
+    counts = torch.randint(0, 400, (32,), generator=g).tolist()
+    counts[:10] = [0, 1, 16, 17, 127, 128, 129, 256, 257, 272]
+    test_block_matmul_groups(counts, 3, N=1040, K=640)
+
+
 @pytest.mark.parametrize("counts,gap", [([5, 0, 1, 130], 0), ([0, 0, 0], 3), ([300, 2, 257, 0, 64, 16], 7), ([1] * 70, 1),
                                         ([128, 128], 0)])
-def test_block_matmul_groups(counts, gap):
+def test_block_matmul_groups(counts, gap, N=272, K=384):
     """Ragged groups, empty ones, rows between groups: those of y stay as they were."""
-    G, N, K = len(counts), 272, 384
+    G = len(counts)
     offs, at = [], gap
     for c in counts:
         offs.append(at)
