@@ -254,11 +254,13 @@ __device__ __forceinline__ void mma_tile(const BlockArgs& a, const TileAt& at, u
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  // The copies of stage kn go out a few at a time between the products: all
-  // at once they hold up each wave's issue until the address unit has taken
-  // them, and copies and products add up.
+  // The copies of stage kn go out two at a time between the first products:
+  // all at once they hold up each wave's issue until the address unit has taken
+  // them, and copies and products add up; one at a time, over the whole stage,
+  // the last ones are waited for (32 groups of 512 rows, 4096 x 7168: two 602 us,
+  // three 604, one 630; 4097 x 7168 x 4096 109, 112, 117).
   auto compute = [&](auto more, const uint8_t* sa, const uint8_t* sb, const float* ss, float scb, int kn, uint8_t* na, uint8_t* nbuf) {
-    constexpr int per = decltype(more)::value ? (kCopies + NT - 1) / NT : 0;
+    constexpr int need = (kCopies + NT - 1) / NT, per = decltype(more)::value ? (need > 2 ? need : 2) : 0;
     u32x4 af[MT][2], b[2][2];
     float sc[MT];
     f32x4 sum[2][MT];
