@@ -164,18 +164,19 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
-constexpr int kTileT = 128, kTileE = 256;
+constexpr int kTileE = 256;
 
-// The same for many tokens and experts: 128 tokens x 256 experts a workgroup
-// (8 waves of 64 x 64), stages of 64 hidden values in three LDS slots filled
-// by LDS-DMA two stages ahead.  Bound: reading the tokens from HBM; at 16384
-// tokens and 256 experts two slices of the hidden dimension give every CU
-// one workgroup, and Wr is read from L2 128 times instead of 256.
-__global__ __launch_bounds__(kThreads) void k_router_tile(RouterArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t x0[kTileT * 128], x1[kTileT * 128], x2[kTileT * 128];
-  __shared__ __attribute__((aligned(1024))) uint8_t w0[kTileE * 128], w1[kTileE * 128], w2[kTileE * 128];
+// The same for many tokens and experts: 32 * TT tokens x 256 experts a
+// workgroup (8 waves of 16 * TT x 64), stages of 64 hidden values filled by
+// LDS-DMA: three slots for TT = 4, two stages ahead; two slots for TT = 8.
+// Bound: the copies, of which a CU takes 36 to 40 bytes a ns: 2.8 MB a CU with
+// TT = 4 at 16384 x 256 x 7168, 1.9 MB with 8.
+template <int TT>
+__device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, uint8_t* w0, uint8_t* x1, uint8_t* w1,
+                                            uint8_t* x2, uint8_t* w2) {
+  constexpr int kTileT = 32 * TT;
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid / 64), l = tid % 64, r = l % 16, g = l / 16;
-  const int wt = w % 2, we = w / 2;              // wave's 64 tokens and 64 experts
+  const int wt = w % 2, we = w / 2;              // wave's 16 * TT tokens and 64 experts
   // workgroup b runs on XCD b % 8: an XCD keeps to one slice of the hidden
   // dimension, so that slice of Wr stays in its L2
   const int per = 8 / a.KS, z = (int)(blockIdx.x % 8) / per;
@@ -189,45 +190,46 @@ __global__ __launch_bounds__(kThreads) void k_router_tile(RouterArgs a) {
   // one instruction moves 8 rows of 128 bytes; the chunk at place p of row y is p ^ (y / 2 % 8)
   const uint32_t voff = (uint32_t)(l / 8) * pitch + (((l % 8) ^ ((4 * (w % 2) + l / 16) % 8)) * 16);
   const uint8_t *xb = static_cast<const uint8_t*>(a.x) + t0 * pitch, *wb = static_cast<const uint8_t*>(a.w) + (int64_t)e0 * pitch;
-  auto copy = [&](int s, uint8_t* xs, uint8_t* ws) {
-    const int at = (s < s1 ? s : s1 - 1) * 128;  // past the end: the last stage again, unused
-    const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc((void*)xb, (short)0, rows * pitch, 0x00020000);
-    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc((void*)wb, (short)0, cols * pitch, 0x00020000);
-#pragma unroll
-    for (int i = 0; i < kTileT / 64; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr_t)(xs + (w + 8 * i) * 1024), 16, voff, (w + 8 * i) * 8 * pitch + at, 0, 0);
-#pragma unroll
-    for (int i = 0; i < kTileE / 64; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr_t)(ws + (w + 8 * i) * 1024), 16, voff, (w + 8 * i) * 8 * pitch + at, 0, 0);
-  };
   constexpr int kCopies = (kTileT + kTileE) / 64;
-  static_assert(kCopies == 6, "the wait below leaves one stage of copies in flight");
-  f32x4 acc[4][4];                               // [expert tile][token tile]
-  float xs2[4], ws2[4];
+  auto copy = [&](int i, int s, uint8_t* xs, uint8_t* ws) {
+    const int at = (s < s1 ? s : s1 - 1) * 128;  // past the end: the last stage again, unused
+    const bool of_x = i < kTileT / 64;
+    const int grp = w + 8 * (of_x ? i : i - kTileT / 64);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)(of_x ? xb : wb), (short)0, (of_x ? rows : cols) * pitch, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)((of_x ? xs : ws) + grp * 1024), 16, voff, grp * 8 * pitch + at, 0, 0);
+  };
+  f32x4 acc[4][TT];                              // [expert tile][token tile]
+  float xs2[TT / 4], ws2[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    xs2[i] = ws2[i] = 0.0f;
+    ws2[i] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < TT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const bool do_x = blockIdx.y == 0 && we == 0, do_w = tile == 0 && wt == 0;
+#pragma unroll
+  for (int j = 0; j < TT / 4; ++j) xs2[j] = 0.0f;
+  // squared norms: of the tokens a quarter by each of the four waves that hold them
+  const bool do_x = blockIdx.y == 0, do_w = tile == 0 && wt == 0;
   const int sw = (r / 2) % 8;
-  auto compute = [&](const uint8_t* xs, const uint8_t* ws) {
+  // the copies of stage `next` go out two at a time among the first products
+  auto compute = [&](const uint8_t* xs, const uint8_t* ws, int next, uint8_t* nx, uint8_t* nw) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int c = ((4 * h + g) ^ sw) * 16 + r * 128;
-      u32x4 xf[4], wf[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) xf[i] = *reinterpret_cast<const u32x4*>(xs + (wt * 4 + i) * 2048 + c);
+      u32x4 xf[TT], wf[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) wf[i] = *reinterpret_cast<const u32x4*>(ws + (we * 4 + i) * 2048 + c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < TT; ++i) xf[i] = *reinterpret_cast<const u32x4*>(xs + (wt * TT + i) * 2048 + c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma16(wf[i], xf[j], acc[i][j]);
-      if (do_x) {
+      for (int j = 0; j < TT; ++j) {
+        if (h == 0 && 2 * j < kCopies) {
+          copy(2 * j, next, nx, nw);
+          if (2 * j + 1 < kCopies) copy(2 * j + 1, next, nx, nw);
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) xs2[j] = sumsq(xf[j], xs2[j]);
+        for (int i = 0; i < 4; ++i) acc[i][j] = mfma16(wf[i], xf[j], acc[i][j]);
+        if (do_x && j / (TT / 4) == we) xs2[j % (TT / 4)] = sumsq(xf[j], xs2[j % (TT / 4)]);
       }
       if (do_w) {
 #pragma unroll
@@ -240,33 +242,45 @@ __global__ __launch_bounds__(kThreads) void k_router_tile(RouterArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(acc[i][j]));
+      for (int j = 0; j < TT; ++j) asm volatile("" : "+v"(acc[i][j]));
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0x0F76);          // vmcnt(6): all copies but the newest stage's
+    // all copies but, with three slots, the newest stage's
+    static_assert(TT != 4 || kCopies == 6, "vmcnt(6)");
+    __builtin_amdgcn_s_waitcnt(TT == 4 ? 0x0F76 : 0x0F70);
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
   };
-  copy(s0, x0, w0);
-  copy(s0 + 1, x1, w1);
-  turn();
-  for (int s = s0; s < s1; s += 3) {
-    copy(s + 2, x2, w2);
-    compute(x0, w0);
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) copy(i, s0, x0, w0);
+  if constexpr (TT == 4) {
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) copy(i, s0 + 1, x1, w1);
     turn();
-    if (s + 1 >= s1) break;
-    copy(s + 3, x0, w0);
-    compute(x1, w1);
+    for (int s = s0; s < s1; s += 3) {
+      compute(x0, w0, s + 2, x2, w2);
+      turn();
+      if (s + 1 >= s1) break;
+      compute(x1, w1, s + 3, x0, w0);
+      turn();
+      if (s + 2 >= s1) break;
+      compute(x2, w2, s + 4, x1, w1);
+      turn();
+    }
+  } else {
     turn();
-    if (s + 2 >= s1) break;
-    copy(s + 4, x1, w1);
-    compute(x2, w2);
-    turn();
+    for (int s = s0; s < s1; s += 2) {
+      compute(x0, w0, s + 1, x1, w1);
+      turn();
+      if (s + 1 >= s1) break;
+      compute(x1, w1, s + 2, x0, w0);
+      turn();
+    }
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);            // no copy outlives the workgroup
   float* part = a.part + (int64_t)z * a.T * a.Ep;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int t = (wt * 4 + j) * 16 + r;
+  for (int j = 0; j < TT; ++j) {
+    const int t = (wt * TT + j) * 16 + r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = e0 + (we * 4 + i) * 16 + 4 * g;
@@ -275,11 +289,11 @@ __global__ __launch_bounds__(kThreads) void k_router_tile(RouterArgs a) {
   }
   if (do_x) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < TT / 4; ++j) {
       float v = xs2[j];
       v += __shfl_xor(v, 16, 64);
       v += __shfl_xor(v, 32, 64);
-      const int t = (wt * 4 + j) * 16 + r;
+      const int t = (wt * TT + we * (TT / 4) + j) * 16 + r;
       if (g == 0 && t < rows) a.xnorm[(int64_t)z * a.T + t0 + t] = v;
     }
   }
@@ -293,6 +307,18 @@ __global__ __launch_bounds__(kThreads) void k_router_tile(RouterArgs a) {
       if (g == 0 && e < a.Ep) a.wnorm[(int64_t)z * a.Ep + e] = v;
     }
   }
+}
+
+// separate arrays: the compiler then sees that a stage's reads and the next
+// stages' copies do not meet, and does not wait for the copies
+__global__ __launch_bounds__(kThreads) void k_router_tile128(RouterArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t x0[128 * 128], x1[128 * 128], x2[128 * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t w0[kTileE * 128], w1[kTileE * 128], w2[kTileE * 128];
+  router_tile<4>(a, x0, w0, x1, w1, x2, w2);
+}
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_router_tile256(RouterArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t x0[256 * 128], x1[256 * 128], w0[kTileE * 128], w1[kTileE * 128];
+  router_tile<8>(a, x0, w0, x1, w1, nullptr, nullptr);
 }
 
 // One wave per token.  (Four tokens a wave in turn, the next one's scores
@@ -329,7 +355,7 @@ RouterShape router_shape(int64_t T, int H, int E) {
   RouterShape s{};
   const int steps = H / kRouterStep;
   s.ep = (E + 15) / 16 * 16;
-  s.wide = T <= 64 || T * E <= 32768 ? 0 : E <= 64 ? 1 : 2;
+  s.wide = T <= 64 || T * E <= 32768 ? 0 : E <= 64 ? 1 : E > 128 && T >= 16384 ? 3 : 2;
   int64_t tiles = 1, most = steps / (kWaves * 4);
   if (s.wide == 0) {
     s.ks = (int)most;
@@ -338,14 +364,15 @@ RouterShape router_shape(int64_t T, int H, int E) {
       tiles = (T + 63) / 64;
       most = steps / (2 * kWaves);
     } else {
-      tiles = (T + kTileT - 1) / kTileT * ((E + kTileE - 1) / kTileE);
+      const int rows = s.wide == 3 ? 256 : 128;
+      tiles = (T + rows - 1) / rows * ((E + kTileE - 1) / kTileE);
       most = steps / 8;
     }
     const int64_t want = 256 / tiles;
     s.ks = (int)(want < most ? want : most);
   }
   s.ks = s.ks < 1 ? 1 : s.ks > 8 ? 8 : s.ks;
-  if (s.wide == 2) s.ks = s.ks >= 8 ? 8 : s.ks >= 4 ? 4 : s.ks >= 2 ? 2 : 1;   // whole XCDs to a slice
+  if (s.wide >= 2) s.ks = s.ks >= 8 ? 8 : s.ks >= 4 ? 4 : s.ks >= 2 ? 2 : 1;   // whole XCDs to a slice
   return s;
 }
 
@@ -356,10 +383,12 @@ hipError_t launch_router_scores(const RouterArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_router_scores<1, 1>), grid, dim3(kThreads), 0, s, a);
     return hipGetLastError();
   }
-  if (sh.wide == 2) {
-    const int64_t tiles = (a.T + kTileT - 1) / kTileT, per = 8 / a.KS;
+  if (sh.wide >= 2) {
+    const int rows = sh.wide == 3 ? 256 : 128;
+    const int64_t tiles = (a.T + rows - 1) / rows, per = 8 / a.KS;
     const dim3 grid((unsigned)((tiles + per - 1) / per * 8), (unsigned)((a.E + kTileE - 1) / kTileE));
-    hipLaunchKernelGGL(k_router_tile, grid, dim3(kThreads), 0, s, a);
+    if (sh.wide == 3) hipLaunchKernelGGL(k_router_tile256, grid, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL(k_router_tile128, grid, dim3(kThreads), 0, s, a);
     return hipGetLastError();
   }
   hipLaunchKernelGGL((k_router_scores<4, 4>), dim3((unsigned)((a.T + 63) / 64), 1, (unsigned)a.KS), dim3(kThreads), 0, s, a);
