@@ -6,33 +6,48 @@
 
 namespace mm {
 
-// x_t . w_e in 64 bits by one wave (every lane gets the sum)
-__device__ __forceinline__ double router_dot64(const RouterArgs& a, int64_t t, int e) {
+// x_t . w_e in 64 bits for two experts by one wave (every lane gets the sums)
+__device__ __forceinline__ void router_dot64(const RouterArgs& a, int64_t t, int e0, int e1, double& d0, double& d1) {
   const uint8_t* x = static_cast<const uint8_t*>(a.x) + t * a.H * 2;
-  const uint8_t* w = static_cast<const uint8_t*>(a.w) + (int64_t)e * a.H * 2;
-  double s = 0.0;
+  const uint8_t *w0 = static_cast<const uint8_t*>(a.w) + (int64_t)e0 * a.H * 2, *w1 = static_cast<const uint8_t*>(a.w) + (int64_t)e1 * a.H * 2;
+  double s0 = 0.0, s1 = 0.0;
   constexpr int kAhead = 4;    // pieces of 512 values asked for at once: one wait of memory, not one each
   for (int k0 = lane_id() * 8; k0 < a.H; k0 += 512 * kAhead) {
-    u32x4 xv[kAhead], wv[kAhead];
+    u32x4 xv[kAhead], wv[kAhead], vv[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int k = k0 + 512 * u < a.H ? k0 + 512 * u : k0;
       xv[u] = *reinterpret_cast<const u32x4*>(x + k * 2);
-      wv[u] = *reinterpret_cast<const u32x4*>(w + k * 2);
+      wv[u] = *reinterpret_cast<const u32x4*>(w0 + k * 2);
+      vv[u] = *reinterpret_cast<const u32x4*>(w1 + k * 2);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
       if (k0 + 512 * u < a.H) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s += (double)bf16_bits_to_f32(xv[u][i] & 0xffffu) * (double)bf16_bits_to_f32(wv[u][i] & 0xffffu);
-          s += (double)__uint_as_float(xv[u][i] & 0xffff0000u) * (double)__uint_as_float(wv[u][i] & 0xffff0000u);
+          const double lo = bf16_bits_to_f32(xv[u][i] & 0xffffu), hi = __uint_as_float(xv[u][i] & 0xffff0000u);
+          s0 += lo * (double)bf16_bits_to_f32(wv[u][i] & 0xffffu);
+          s0 += hi * (double)__uint_as_float(wv[u][i] & 0xffff0000u);
+          s1 += lo * (double)bf16_bits_to_f32(vv[u][i] & 0xffffu);
+          s1 += hi * (double)__uint_as_float(vv[u][i] & 0xffff0000u);
         }
       }
   }
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
-  return s;
+  for (int o = 32; o > 0; o >>= 1) s0 += __shfl_xor(s0, o, 64), s1 += __shfl_xor(s1, o, 64);
+  d0 = s0, d1 = s1;
+}
+
+// whether every value of token t is zero
+__device__ __forceinline__ bool router_zero_row(const RouterArgs& a, int64_t t) {
+  const uint8_t* x = static_cast<const uint8_t*>(a.x) + t * a.H * 2;
+  uint32_t any = 0;
+  for (int k = lane_id() * 8; k < a.H; k += 512) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(x + k * 2);
+    any |= v[0] | v[1] | v[2] | v[3];
+  }
+  return ballot((any & 0x7fff7fffu) != 0) == 0;
 }
 
 // largest value of the wave: four shifts inside the rows of 16 lanes, two
@@ -104,11 +119,12 @@ __device__ __forceinline__ void router_load_token(const RouterArgs& a, int64_t t
 }
 
 // Lane k returns the k-th expert of token t and its weight (-1 and 0 where
-// none is left).  First the K + 1 largest float32 ranks are taken in turn; if
-// each is above the next by more than both may be off, their order is that of
-// the 64-bit ranks.  If not (a token in a hundred), the token is selected
-// again with a bound for each expert: where another expert's reaches the best
-// one's, both get their 64-bit sums, and the set is compared in 64 bits.
+// none is left).  The largest float32 ranks are taken in turn; where one is
+// above the next by more than both may be off, their order is that of the
+// 64-bit ranks.  The others form runs of neighbours (one token in a hundred has
+// one, mostly of two): the members of a run get their 64-bit ranks and are put
+// in order among themselves.  Tokens whose float32 sums left their range, and
+// runs past 64 positions, are selected again one expert at a time.
 template <int NV, int KM>
 __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t t, const RouterExperts<NV>& ex,
                                                     const RouterToken<NV, KM>& tok, int& id, float& weight) {
@@ -187,12 +203,27 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
     }
     return best;
   };
-  bool sure = ballot(lost) == 0;
-  // the finite rank `best` after `before` is not surely below it
-  auto doubt = [&](uint32_t before, uint32_t best) {
-    return best > 1u && !(rank_value(before) - rank_value(best) > gap) && rank_value(best) - rank_value(best) == 0.0f;
+  // the 64-bit rank of a 64-bit score argument
+  auto rank_of = [&](double z, int e) {
+    const double b = biased ? (double)a.bias[e] : 0.0;
+    return !sig ? z + b : biased ? 1.0 / (1.0 + exp(-z)) + b : z;
   };
+  bool sure = ballot(lost) == 0;
+  uint64_t chained = 0;        // position k is not surely below position k - 1
+  // whether position k with key `best` after `before` ends the list; 2: too long
   uint32_t before = 0;
+  auto ends = [&](int k, uint32_t best) {
+    const float r = rank_value(best);
+    const bool doubt = k > 0 && best > 1u && r - r == 0.0f && !(rank_value(before) - r > gap);
+    if (best == 0 || (k >= a.K && !doubt)) return true;
+    if (k == 64) {
+      sure = false;
+      return true;
+    }
+    chained |= (uint64_t)doubt << k;
+    before = best;
+    return false;
+  };
   if constexpr (NV <= 4) {
     // each lane's keys in descending order, equal ones by expert: a turn looks
     // at the first one only (256 experts: 33 against 60 instructions a turn)
@@ -208,41 +239,84 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
         const uint32_t ha = swap ? at[v + 1] : at[v], la = swap ? at[v] : at[v + 1];
         left[v] = hk, left[v + 1] = lk, at[v] = ha, at[v + 1] = la;
       }
-    for (int k = 0; sure && k <= a.K; ++k) {
+    for (int k = 0; sure; ++k) {
       const uint32_t best = wave_max_u32(left[0]);
-      if (k > 0 && doubt(before, best)) sure = false;
-      if (best == 0 || k == a.K) break;
+      if (ends(k, best)) break;
       const uint64_t who = ballot(left[0] == best);
-      // equal infinite or NaN ranks of several lanes: by expert, below
-      if ((who & (who - 1)) != 0) sure = false;
-      const int bl = __ffsll((unsigned long long)who) - 1;
-      const int e = __builtin_amdgcn_readlane((int)at[0], bl);
+      int e = __builtin_amdgcn_readlane((int)at[0], __ffsll((unsigned long long)who) - 1);
+      if ((who & (who - 1)) != 0) e = (int)~wave_max_u32(left[0] == best ? ~at[0] : 0u);   // equal ones: the lowest
       if (l == k) id = e;
-      if (l == bl) {
+      if (l == e % 64) {
 #pragma unroll
         for (int v = 0; v + 1 < NV; ++v) left[v] = left[v + 1], at[v] = at[v + 1];
         left[NV - 1] = 0;
       }
-      before = best;
     }
   } else {
 #pragma unroll
     for (int v = 0; v < NV; ++v) left[v] = key[v];
-    for (int k = 0; sure && k <= a.K; ++k) {
+    for (int k = 0; sure; ++k) {
       int bl = 0, bv = 0;
       const uint32_t best = largest(bl, bv);
-      if (k > 0 && doubt(before, best)) sure = false;
-      if (best == 0 || k == a.K) break;
+      if (ends(k, best)) break;
       take(k, bl, bv);
-      before = best;
     }
   }
-  if (!sure) {
+  // a token of zeros: every float32 score is exact, and a long run of equal ones likely
+  const bool zero = (chained != 0 || !sure) && xx == 0.0f && router_zero_row(a, t);
+  if (sure && !zero && chained != 0) {
+    // 64-bit ranks of the positions in runs, two at a time: memory is waited for
+    const uint64_t runs = chained | chained >> 1;
+    double mine = 0.0;
+    for (uint64_t todo = runs; todo != 0;) {
+      const int p0 = __ffsll((unsigned long long)todo) - 1;
+      todo &= todo - 1;
+      const int p1 = todo != 0 ? __ffsll((unsigned long long)todo) - 1 : p0;
+      todo &= todo - 1;
+      double d0, d1;
+      router_dot64(a, t, __builtin_amdgcn_readlane(id, p0), __builtin_amdgcn_readlane(id, p1), d0, d1);
+      if (l == p0 || l == p1) mine = rank_of(l == p0 ? d0 : d1, id);
+    }
+    // each moves within its run by those that it was wrongly before or behind
+    const int run = __popcll((unsigned long long)(~chained & ((2ull << l) - 1)));
+    int place = l;
+    for (uint64_t todo = runs; todo != 0; todo &= todo - 1) {
+      const int q = __ffsll((unsigned long long)todo) - 1;
+      const double other = __shfl(mine, q, 64);
+      const int e = __builtin_amdgcn_readlane(id, q);
+      const bool above = other > mine || (other == mine && e < id);
+      if (__builtin_amdgcn_readlane(run, q) == run && q != l) place += q > l ? (above ? 1 : 0) : (above ? 0 : -1);
+    }
+    id = __builtin_amdgcn_ds_permute(4 * place, id);
+  }
+  if (!sure || zero) {
+    // one expert at a time, each with a bound of its own
     double exact[NV];          // the 64-bit rank of an expert in `known`
     uint32_t known = 0;
     id = -1;
 #pragma unroll
     for (int v = 0; v < NV; ++v) left[v] = key[v], exact[v] = 0.0;
+    auto learn = [&](int v, double zz) {
+      const double rank = rank_of(zz, l + 64 * v);
+      float e = 2.4e-7f * fabsf((float)rank);
+      if (!(e <= 3.0e38f)) e = 0.0f;
+      const uint32_t kk = rank == -__builtin_huge_val() ? 0u : rank_key((float)rank);
+#pragma unroll
+      for (int u = 0; u < NV; ++u)
+        if (u == v) z[u] = (float)(sig || !biased ? zz : rank), exact[u] = rank, left[u] = kk, err[u] = e;
+      known |= 1u << v;
+    };
+    if (zero) {
+      for (int v = 0; v < NV; ++v) {
+        float zv = 0.0f;
+        uint32_t kv = 0;
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+          if (u == v) zv = z[u], kv = key[u];
+        // a weight that is not finite has made its score NaN, which stays last
+        if (kv > 1u && zv - zv == 0.0f) learn(v, 0.0);
+      }
+    }
     for (int k = 0; k < a.K; ++k) {
       int bl = 0, bv = 0;
       bool none = false;
@@ -273,19 +347,10 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
         for (int v = 0; v < NV; ++v)
           for (uint64_t todo = ballot((near & ~known) >> v & 1u); todo != 0; todo &= todo - 1) {
             const int src = __ffsll((unsigned long long)todo) - 1;
-            const double dz = router_dot64(a, t, src + 64 * v);
+            double d0, d1;
+            router_dot64(a, t, src + 64 * v, src + 64 * v, d0, d1);
             grew = true;
-            if (l == src) {
-              const double b = biased ? (double)a.bias[src + 64 * v] : 0.0;
-              const double zz = sig ? dz : dz + b, rank = sig && biased ? 1.0 / (1.0 + exp(-zz)) + b : zz;
-              float e = 2.4e-7f * fabsf((float)rank);
-              if (!(e <= 3.0e38f)) e = 0.0f;
-              const uint32_t kk = rank == -__builtin_huge_val() ? 0u : rank_key((float)rank);
-#pragma unroll
-              for (int u = 0; u < NV; ++u)
-                if (u == v) z[u] = (float)zz, exact[u] = rank, left[u] = kk, err[u] = e;
-              known |= 1u << v;
-            }
+            if (l == src) learn(v, d0);
           }
         if (grew) continue;
         // all known: the largest 64-bit rank, ties to the lowest expert
@@ -308,6 +373,7 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
       take(k, bl, bv);
     }
   }
+  if (l >= a.K) id = -1;
   // the selected experts' score arguments, from their lanes
   float my_z = 0.0f;
 #pragma unroll

@@ -120,6 +120,26 @@ def test_router_near_ties_in_sparse_tokens(T, E4):
         check_router(x, w, None, 9, "softmax")
 
 
+@pytest.mark.parametrize("T,E", [(9, 40), (100, 130), (300, 300)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_router_equal_scores(T, E, scoring):
+    """Rows of zeros, with biases of which some are equal, and runs of equal experts longer than a wave."""
+    x, w, b = router_case(T, 512, E, 7, scoring, True, 70)
+    x[::3] = 0
+    x[6] = -0.0
+    b[3::4] = b[1]
+    check_router(x, w, None, 7, scoring)
+    check_router(x, w, b, 7, scoring)
+    w[: E - 10] = w[1]
+    w.view(torch.int16)[5, 9] ^= 1
+    check_router(x, w, None, 7, scoring)
+    check_router(x, w, b, 7, scoring)
+    w[4, 3] = math.nan                                      # NaN for the zero rows too
+    w[8, 3] = math.inf
+    ids, _ = moe.route(x.cuda(), w.cuda(), b.cuda(), topk=7, scoring=scoring)
+    assert torch.equal(ids.cpu(), ref.route(x, w, b, 7, scoring)[0])
+
+
 def test_router_extreme_values():
     x, w, _ = router_case(80, 512, 40, 6, "softmax", False, 21)
     x[3] = 0.0                                              # every score equal: ids 0 .. 5
