@@ -1,13 +1,18 @@
-// The routed-expert layer for at most 64 tokens: two kernels that stream the
-// live experts' weights once from HBM into MFMA operands.
+// The routed-expert layer for at most 64 tokens: kernels that read the live
+// experts' weights once from HBM into MFMA operands.
 //
-//   k_few_l1: A[r] = SwiGLU(x_t . W1[e]) for every route r = (t, k), e = id(r)
-//   k_few_l2: y[t] = sum over t's routes of g_r * (A[r] . W2[e])
+//   Linear1: A[r] = SwiGLU(x_t . W1[e]) for every route r = (t, k), e = id(r)
+//   Linear2: y[t] = sum over t's routes of g_r * (A[r] . W2[e])
 //
 // Weights are the A operand of the 16 x 16 x 32 MFMA (16 weight rows), up to
-// 16 * NT routes of one expert its B operand, so a weight byte is read once
+// 16 routes of one expert its B operand, so a weight byte is read once
 // whatever the number of tokens.  e4m3 weights are widened exactly to bf16
-// (activations are not quantised); float32 accumulators.  Bound: HBM.
+// (activations are not quantised); float32 accumulators.  A is held in bf16
+// parts: one when y is bf16, whose own rounding is as large; three, the whole
+// float, when y is float32.
+// Up to 16 tokens k_few_l1 and k_few_l2 stream the weights into registers;
+// with more, or (Linear2) a float32 y, k_few_tile brings them through LDS and
+// k_few_combine adds a token's contributions.  Bound: HBM.
 #include <type_traits>
 
 #include "mm_device.hpp"
@@ -19,7 +24,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
-constexpr int kMaxT = 64, kMaxE = 1025, kMaxRoutes = 64 * 33;
+constexpr int kMaxT = 64, kMaxE = 1024, kMaxK = 32;
+constexpr int kStreamT = 16;           // most tokens of the streaming kernels: one MFMA of routes an expert
 constexpr int kStage = 128;            // K-values per stage of a wave
 
 __device__ __forceinline__ f32x4 mfma16(const u32x4& a, const u32x4& b, f32x4 c) {
@@ -35,145 +41,145 @@ __device__ __forceinline__ u32x4 widen8(uint32_t w0, uint32_t w1) {
 #undef CVT
 }
 
-// The routes of a batch grouped by expert, in LDS.
-struct Lists {
-  unsigned long long tokens[kMaxE];   // tokens of each expert, one bit each; then the place of its first entry
-  int32_t route[kMaxRoutes];   // list: route t * (K + S) + k, by expert and token
-  float gate[kMaxRoutes];
-  int16_t expert[kMaxE];       // live experts, ascending
-  int16_t start[kMaxE + 1];    // first list entry of each live expert
-  int16_t visit[kMaxE + 1];    // first visit of each live expert: a visit is a group of up to `group` of its routes
-  int16_t token[kMaxRoutes];
-  int16_t first[kMaxE];        // first list entry of expert e
-  int32_t live;
-};
-
-// Built by every workgroup for itself: a few thousand ids at most, which
-// cost less than a kernel of their own.  A route's place among its expert's
-// is the number of earlier tokens in the expert's bit mask, so the order
-// does not depend on how the atomics arrive.  An id that a token names twice
-// is one entry with the sum of the weights.
-__device__ void build_lists(const FewArgs& a, Lists& L, int group) {
+// The tokens of each expert as bit masks, by every workgroup for itself: a
+// few thousand ids at most, which cost less than a kernel of their own.
+// Returns whether some token names an expert twice.
+__device__ __forceinline__ bool mark_tokens(const FewArgs& a, unsigned long long* tokens, int32_t& twice) {
   const int tid = threadIdx.x, Et = a.E + a.S, n = a.T * a.K;
-  for (int e = tid; e < Et; e += kThreads) L.tokens[e] = 0;
-  for (int i = tid; i < n + a.T; i += kThreads) {
-    L.route[i] = 0x7fffffff;
-    L.gate[i] = 0.0f;
-  }
+  for (int e = tid; e < Et; e += kThreads) tokens[e] = 0;
+  if (tid == 0) twice = 0;
   __syncthreads();
   for (int i = tid; i < n; i += kThreads) {
     const int t = i / a.K, id = a.ids[i];
-    if (id >= 0 && id < a.E && (a.active == nullptr || a.active[t] != 0)) atomicOr(&L.tokens[id], 1ull << t);
+    if (id >= 0 && id < a.E && (a.active == nullptr || a.active[t] != 0) &&
+        (atomicOr(&tokens[id], 1ull << t) >> t & 1))
+      twice = 1;
   }
-  if (a.S && tid < a.T && (a.active == nullptr || a.active[tid] != 0)) atomicOr(&L.tokens[a.E], 1ull << tid);
+  if (a.S && tid < a.T && (a.active == nullptr || a.active[tid] != 0)) atomicOr(&tokens[a.E], 1ull << tid);
   __syncthreads();
+  return twice != 0;
+}
+
+// Whether (t, k) is the route of its expert: the first k of t that names it.
+// Its weight is then the sum over all k that do, in their order.
+__device__ __forceinline__ bool first_route(const FewArgs& a, bool twice, int t, int k, int id, float& gate) {
+  gate = a.weights[t * a.K + k];
+  if (!twice) return true;
+  for (int j = 0; j < a.K; ++j)
+    if (j != k && a.ids[t * a.K + j] == id) {
+      if (j < k) return false;
+      gate += a.weights[t * a.K + j];
+    }
+  return true;
+}
+
+// The routes of a batch grouped by expert, in LDS.
+struct Lists {
+  unsigned long long tokens[kMaxE];            // tokens of each expert, one bit each
+  int32_t route[kStreamT * (kMaxK + 1)];       // list: route t * (K + S) + k, by expert and token
+  float gate[kStreamT * (kMaxK + 1)];
+  int16_t token[kStreamT * (kMaxK + 1)];
+  int16_t expert[kMaxE];       // live experts, ascending
+  int16_t start[kMaxE + 1];    // first list entry of each live expert
+  int16_t first[kMaxE];        // first list entry of expert e
+  int32_t live, twice;
+};
+
+// A route's place among its expert's is the number of earlier tokens in the
+// expert's mask: the order does not depend on how the atomics arrive.
+__device__ void build_lists(const FewArgs& a, Lists& L) {
+  const int tid = threadIdx.x, Et = a.E + a.S, n = a.T * a.K;
+  const bool twice = mark_tokens(a, L.tokens, L.twice);
   if (tid < 64) {
-    int live = 0, at = 0, vis = 0;
+    int live = 0, at = 0;
     for (int e0 = 0; e0 < Et; e0 += 64) {
       const int e = e0 + tid, c = e < Et ? __popcll(L.tokens[e]) : 0;
       const uint64_t m = ballot(c > 0);
-      // routes and visits of the experts before this one, in one scan
-      const int mine = c | ((c + group - 1) / group) << 16;
-      int pre = mine;
+      int pre = c;             // routes of the experts up to this one
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const int v = __shfl_up(pre, o, 64);
         if (tid >= o) pre += v;
       }
-      const int all = __shfl(pre, 63, 64);
-      pre -= mine;
       if (c > 0) {
         const int p = live + __popcll((unsigned long long)(m & lanemask_lt()));
         L.expert[p] = (int16_t)e;
-        L.start[p] = (int16_t)(at + (pre & 0xffff));
-        L.visit[p] = (int16_t)(vis + (pre >> 16));
-        L.first[e] = (int16_t)(at + (pre & 0xffff));
+        L.start[p] = L.first[e] = (int16_t)(at + pre - c);
       }
       live += __popcll((unsigned long long)m);
-      at += all & 0xffff;
-      vis += all >> 16;
+      at += __shfl(pre, 63, 64);
     }
     if (tid == 0) {
       L.live = live;
       L.start[live] = (int16_t)at;
-      L.visit[live] = (int16_t)vis;
     }
   }
   __syncthreads();
   auto place = [&](int e, int t, int k, float gate) {
     const int p = L.first[e] + __popcll(L.tokens[e] & ((1ull << t) - 1));
-    atomicMin(&L.route[p], t * (a.K + a.S) + k);
-    atomicAdd(&L.gate[p], gate);
+    L.route[p] = t * (a.K + a.S) + k;
+    L.gate[p] = gate;
     L.token[p] = (int16_t)t;
   };
   for (int i = tid; i < n; i += kThreads) {
     const int t = i / a.K, id = a.ids[i];
-    if (id >= 0 && id < a.E && (a.active == nullptr || a.active[t] != 0)) place(id, t, i % a.K, a.weights[i]);
+    float gate;
+    if (id >= 0 && id < a.E && (a.active == nullptr || a.active[t] != 0) && first_route(a, twice, t, i % a.K, id, gate))
+      place(id, t, i % a.K, gate);
   }
   if (a.S && tid < a.T && (a.active == nullptr || a.active[tid] != 0)) place(a.E, tid, a.K, 1.0f);
   __syncthreads();
 }
 
-// One stage of a wave: WT tiles of 16 weight rows and NT tiles of 16 routes
-// in P parts, 128 K-values.  A lane's 16-byte pieces of a weight row and of
-// a route's row cover the same K-values in the same order.
-template <int F, int WT, int NT, int P>
+// One stage of a wave: WT tiles of 16 weight rows and 16 routes in P parts,
+// 128 K-values.  A lane's 16-byte pieces of a weight row and of a route's row
+// cover the same K-values in the same order.
+template <int F, int WT, int P>
 struct Stage {
   static constexpr int WL = F == MM_FEW_BF16 ? 4 : 2;
   u32x4 w[WT][WL];
-  u32x4 b[P][NT][4];
+  u32x4 b[P][4];
   float s[WT];
 };
 
 template <int F> constexpr int weight_bytes() { return F == MM_FEW_BF16 ? 2 : 1; }
-// byte offset of piece j of lane group g inside a stage
-template <int F> __device__ __forceinline__ int w_piece(int g, int j) {
-  return F == MM_FEW_BF16 ? 64 * j + 16 * g : 64 * j + 16 * g;
-}
-// bf16 operand piece j (of MFMA j) of lane group g: the K-values that
-// widened weight piece covers
+// byte offset of a weight row's piece j of lane group g inside a stage
+__device__ __forceinline__ int w_piece(int g, int j) { return 64 * j + 16 * g; }
+// bf16 operand piece j (of MFMA j) of lane group g: the K-values that the
+// weight piece covers
 template <int F> __device__ __forceinline__ int b_piece(int g, int j) {
   return F == MM_FEW_BF16 ? 64 * j + 16 * g : 128 * (j / 2) + 32 * g + 16 * (j % 2);
 }
 
-template <int F, int WT, int NT, int P>
-__device__ __forceinline__ void load_weights(Stage<F, WT, NT, P>& st, const uint8_t* const (&wp)[WT], int64_t off, int g) {
+template <int F, int WT, int P>
+__device__ __forceinline__ void load_weights(Stage<F, WT, P>& st, const uint8_t* const (&wp)[WT], int64_t off, int g) {
 #pragma unroll
   for (int i = 0; i < WT; ++i)
 #pragma unroll
-    for (int j = 0; j < Stage<F, WT, NT, P>::WL; ++j)
-      st.w[i][j] = *reinterpret_cast<const u32x4*>(wp[i] + off + w_piece<F>(g, j));
+    for (int j = 0; j < Stage<F, WT, P>::WL; ++j)
+      st.w[i][j] = *reinterpret_cast<const u32x4*>(wp[i] + off + w_piece(g, j));
 }
 
-template <int F, int WT, int NT, int P>
-__device__ __forceinline__ void multiply(const Stage<F, WT, NT, P>& st, f32x4 (&acc)[WT][NT], int nt) {
+template <int F, int WT, int P>
+__device__ __forceinline__ void multiply(const Stage<F, WT, P>& st, f32x4 (&acc)[WT]) {
 #pragma unroll
   for (int i = 0; i < WT; ++i) {
-    f32x4 sum[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) sum[n] = F == MM_FEW_FP8_BLOCK ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][n];
+    f32x4 sum = F == MM_FEW_FP8_BLOCK ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const u32x4 w = F == MM_FEW_BF16 ? st.w[i][F == MM_FEW_BF16 ? j : 0]
                                        : widen8(st.w[i][F == MM_FEW_BF16 ? 0 : j / 2][2 * (j % 2)], st.w[i][F == MM_FEW_BF16 ? 0 : j / 2][2 * (j % 2) + 1]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (NT == 1 || n < nt) {
-#pragma unroll
-          for (int p = 0; p < P; ++p) sum[n] = mfma16(w, st.b[p][n][j], sum[n]);
-        }
+      for (int p = 0; p < P; ++p) sum = mfma16(w, st.b[p][j], sum);
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[i][n] = F == MM_FEW_FP8_BLOCK ? acc[i][n] + sum[n] * st.s[i] : sum[n];
+    acc[i] = F == MM_FEW_FP8_BLOCK ? acc[i] + sum * st.s[i] : sum;
   }
 }
 
-template <int WT, int NT>
-__device__ __forceinline__ void clear(f32x4 (&acc)[WT][NT]) {
+template <int WT>
+__device__ __forceinline__ void clear(f32x4 (&acc)[WT]) {
 #pragma unroll
-  for (int i = 0; i < WT; ++i)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[i][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < WT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 }
 
 __device__ __forceinline__ float swiglu(float g, float u, float clamp) {
@@ -196,29 +202,30 @@ __device__ __forceinline__ void split_bf16(float v, uint16_t (&o)[P]) {
 
 }  // namespace
 
-// Linear1.  A unit is 16 * CT columns of A of one live expert (16 gate and 16
-// up rows of W1 for each CT) for a group of up to 16 * NT of its routes; the 8 waves share
-// the hidden dimension, stage by stage, and their sums meet in LDS.  D
-// stages of a wave are in flight, across units.
-template <int F, int CT, int NT, int P, int D>
+// Linear1.  A unit is 16 columns of A of one live expert (16 gate and 16 up
+// rows of W1) for all of its routes; the 8 waves share the hidden dimension,
+// stage by stage, and their sums meet in LDS.  D stages of a wave are in
+// flight, across units.  One token, 7168 x 2048, 8 + 1 experts: 53 us for the
+// 264 MB of e4m3 weights (5.0 TB/s), 88 us for bf16 (5.3 TB/s with 8 experts); a
+// large copy moves 4.9 TB/s in both directions together.
+template <int F, int P, int D>
 __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
   __shared__ Lists L;
-  constexpr int WT = 2 * CT;
   // two buffers: a unit's sums are read while the next unit's are written
-  __shared__ f32x4 red[2][kWaves][WT][NT][64];
-  build_lists(a, L, 16 * NT);
+  __shared__ f32x4 red[2][kWaves][2][64];
+  build_lists(a, L);
   const int w = uniform(threadIdx.x / 64), l = threadIdx.x % 64, r = l % 16, g = l / 16;
   constexpr int WB = weight_bytes<F>();
-  const int nst = a.H / kStage, nsw = (nst + kWaves - 1) / kWaves, cols = a.I / (16 * CT);
+  const int nst = a.H / kStage, nsw = (nst + kWaves - 1) / kWaves, cols = a.I / 16;
   const int units = uniform(L.live) * cols;
   const int64_t R = (int64_t)a.T * (a.K + a.S);
 
-  // the next stage to load: unit u, route group q of its expert, stage j
+  // the next stage to load: stage j of unit u
   struct Cursor {
-    int u, q, j;
+    int u, j;
     int e, c, n0, n;
-    const uint8_t* wp[WT];
-    const uint8_t* bp[NT];
+    const uint8_t* wp[2];
+    const uint8_t* bp;
     const float* sp[2];
   };
   if ((int)blockIdx.x >= units) return;
@@ -230,57 +237,37 @@ __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
     const int le = cu.u / cols;
     cu.c = cu.u % cols;
     cu.e = uniform(L.expert[le]);
-    cu.n0 = uniform(L.start[le]) + cu.q * 16 * NT;
+    cu.n0 = uniform(L.start[le]);
     cu.n = uniform(L.start[le + 1]) - cu.n0;
-    const uint8_t* base = a.w1 + (int64_t)cu.e * 2 * a.I * a.H * WB;
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      const int col = cu.c * CT + c, row = 64 * (col / 2) + 16 * (col % 2) + r;
-      cu.wp[2 * c] = base + (int64_t)row * a.H * WB;
-      cu.wp[2 * c + 1] = base + (int64_t)(row + 32) * a.H * WB;
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int i = 16 * n + r;
-      cu.bp[n] = static_cast<const uint8_t*>(a.x) + (int64_t)L.token[cu.n0 + (i < cu.n ? i : 0)] * a.H * 2;
-    }
+    const int row = 64 * (cu.c / 2) + 16 * (cu.c % 2) + r;
+    cu.wp[0] = a.w1 + ((int64_t)cu.e * 2 * a.I + row) * a.H * WB;
+    cu.wp[1] = cu.wp[0] + (int64_t)32 * a.H * WB;
+    cu.bp = static_cast<const uint8_t*>(a.x) + (int64_t)L.token[cu.n0 + (r < cu.n ? r : 0)] * a.H * 2;
     if constexpr (F == MM_FEW_FP8_BLOCK) {
-      const float* s = a.s1 + (int64_t)cu.e * (2 * a.I / 128) * nst;
-      cu.sp[0] = s + (int64_t)(cu.c * CT / 8) * nst;
-      cu.sp[1] = s + (int64_t)(a.I / 128 + cu.c * CT / 8) * nst;
+      cu.sp[0] = a.s1 + ((int64_t)cu.e * (2 * a.I / 128) + cu.c / 8) * nst;
+      cu.sp[1] = cu.sp[0] + (int64_t)(a.I / 128) * nst;
     }
   };
   auto step = [&](Cursor& cu) {
     if (++cu.j < nsw) return;
     cu.j = 0;
-    if (cu.n > 16 * NT) {
-      ++cu.q;
-    } else {
-      cu.q = 0;
-      cu.u += gridDim.x;
-    }
+    cu.u += gridDim.x;
     aim(cu);
   };
-  auto load = [&](const Cursor& cu, Stage<F, WT, NT, 1>& st) {
+  auto load = [&](const Cursor& cu, Stage<F, 2, 1>& st) {
     const int js = cu.j * kWaves + w, s = js < nst ? js : nst - 1;
-    load_weights<F, WT, NT, 1>(st, cu.wp, (int64_t)s * (kStage * WB), g);
+    load_weights<F, 2, 1>(st, cu.wp, (int64_t)s * (kStage * WB), g);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) st.b[0][n][j] = *reinterpret_cast<const u32x4*>(cu.bp[n] + (int64_t)s * (kStage * 2) + b_piece<F>(g, j));
-    if constexpr (F == MM_FEW_FP8_BLOCK) {
-      const float sg = cu.sp[0][s], su = cu.sp[1][s];
-#pragma unroll
-      for (int c = 0; c < CT; ++c) st.s[2 * c] = sg, st.s[2 * c + 1] = su;
-    }
+    for (int j = 0; j < 4; ++j) st.b[0][j] = *reinterpret_cast<const u32x4*>(cu.bp + (int64_t)s * (kStage * 2) + b_piece<F>(g, j));
+    if constexpr (F == MM_FEW_FP8_BLOCK) st.s[0] = cu.sp[0][s], st.s[1] = cu.sp[1][s];
   };
 
   Cursor ld{}, cu{};
   ld.u = cu.u = blockIdx.x;
   aim(ld);
   aim(cu);
-  Stage<F, WT, NT, 1> st[D];
-  f32x4 acc[WT][NT];
+  Stage<F, 2, 1> st[D];
+  f32x4 acc[2];
   clear(acc);
   int side = 0;
 #pragma unroll
@@ -291,32 +278,28 @@ __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
   while (cu.u < units) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      if (cu.u < units && cu.j * kWaves + w < nst) multiply<F, WT, NT, 1>(st[d], acc, (cu.n + 15) / 16);
+      if (cu.u < units && cu.j * kWaves + w < nst) multiply<F, 2, 1>(st[d], acc);
       load(ld, st[d]);
       if (ld.u < units) step(ld);
       if (cu.u < units) {
         if (cu.j + 1 == nsw) {
           // the unit's sums: 8 waves' parts, SwiGLU, A
-#pragma unroll
-          for (int i = 0; i < WT; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) red[side][w][i][n][l] = acc[i][n];
+          red[side][w][0][l] = acc[0];
+          red[side][w][1][l] = acc[1];
           clear(acc);
           __syncthreads();
           const float* rf = reinterpret_cast<const float*>(red[side]);
           side ^= 1;
-          const int n16 = cu.n < 16 * NT ? cu.n : 16 * NT;
-          for (int i = threadIdx.x; i < 16 * CT * n16; i += kThreads) {
-            // column c (of 16, in tile ct) of list entry m: accumulator c % 4 of lane 16 * (c / 4) + m % 16
-            const int c = i % 16, ct = i / 16 % CT, m = i / (16 * CT);
-            const int at = ((m / 16) * 64 + 16 * (c / 4) + m % 16) * 4 + c % 4;
+          for (int i = threadIdx.x; i < 16 * cu.n; i += kThreads) {
+            // column c of list entry m: accumulator c % 4 of lane 16 * (c / 4) + m
+            const int c = i % 16, m = i / 16, at = (16 * (c / 4) + m) * 4 + c % 4;
             float hg = 0.0f, hu = 0.0f;
 #pragma unroll
             for (int k = 0; k < kWaves; ++k) {
-              hg += rf[(k * WT + 2 * ct) * NT * 256 + at];
-              hu += rf[(k * WT + 2 * ct + 1) * NT * 256 + at];
+              hg += rf[k * 512 + at];
+              hu += rf[k * 512 + 256 + at];
             }
-            const int col = (cu.c * CT + ct) * 16 + c;
+            const int col = cu.c * 16 + c;
             if constexpr (F == MM_FEW_FP8) {
               hg *= a.s1[(int64_t)cu.e * 2 * a.I + col];
               hu *= a.s1[(int64_t)cu.e * 2 * a.I + a.I + col];
@@ -337,59 +320,44 @@ __global__ __launch_bounds__(kThreads) void k_few_l1(FewArgs a) {
 // Linear2.  A unit is 16 * WT columns of y over every live expert; its
 // stages (expert, 128 values of I) are cut into 8 runs, one a wave.  A wave
 // adds gate * sum to its own copy of the unit's y in LDS at the end of an
-// expert, and the 8 copies are added in order.
-template <int F, int WT, int NT, int P, int D>
+// expert, and the 8 copies are added in order.  One token, 7168 x 2048, 8 + 1
+// experts: 29 us for the 132 MB of e4m3 weights, 53 us for bf16 with 8 experts.
+template <int F, int WT, int D>
 __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
   __shared__ Lists L;
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   f32x4* ys = reinterpret_cast<f32x4*>(dyn);   // [2][kWaves][T][4 * WT]: one of the two is added and cleared while the other fills
   const int ylen = kWaves * a.T * 4 * WT;
-  build_lists(a, L, 16 * NT);
+  build_lists(a, L);
   const int w = uniform(threadIdx.x / 64), l = threadIdx.x % 64, r = l % 16, g = l / 16;
   constexpr int WB = weight_bytes<F>();
   const int nst = a.I / kStage;
   const int units = a.H / (16 * WT);
-  const int64_t R = (int64_t)a.T * (a.K + a.S);
-  const int live = uniform(L.live), visits = uniform(L.visit[live]);
-  const int total = visits * nst, nsw = total > kWaves ? (total + kWaves - 1) / kWaves : 1;
+  const int total = uniform(L.live) * nst, nsw = total > kWaves ? (total + kWaves - 1) / kWaves : 1;
   for (int i = threadIdx.x; i < 2 * ylen; i += kThreads) ys[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
 
   if (total == 0) {          // no route at all
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.T * a.H; i += gridDim.x * kThreads) {
-      if (a.y_f32) static_cast<float*>(a.y)[i] = 0.0f;
-      else static_cast<uint16_t*>(a.y)[i] = 0;
-    }
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.T * a.H; i += gridDim.x * kThreads)
+      static_cast<uint16_t*>(a.y)[i] = 0;
     return;
   }
-  // the live expert and its visit that hold this wave's first stage (the last
-  // stage for a wave without any: its loads have to go somewhere)
+  // this wave's first stage (the last stage for a wave without any: its loads have to go somewhere)
   const int f0 = w * nsw < total ? w * nsw : total - 1;
-  int le0 = 0, q0 = 0;
-  {
-    const int v = f0 / nst;
-    int hi = live;             // the last expert whose first visit is at most v
-    while (hi - le0 > 1) {
-      const int mid = (le0 + hi) / 2;
-      if (uniform(L.visit[mid]) <= v) le0 = mid;
-      else hi = mid;
-    }
-    q0 = v - uniform(L.visit[le0]);
-  }
 
   struct Cursor {
     int u, j;                  // unit, stage of this wave's run
-    int s, le, q;              // stage inside the visit, live expert, route group
+    int s, le;                 // stage inside the expert, live expert
     int e, n0, n;
     const uint8_t* wp[WT];
-    const uint8_t* bp[NT];
+    const uint8_t* bp;
     const float* sp[WT];
   };
   auto valid = [&](const Cursor& cu) { return w * nsw + cu.j < total; };
   auto aim = [&](Cursor& cu) {
     if (cu.u >= units) return;
     cu.e = uniform(L.expert[cu.le]);
-    cu.n0 = uniform(L.start[cu.le]) + cu.q * 16 * NT;
+    cu.n0 = uniform(L.start[cu.le]);
     cu.n = uniform(L.start[cu.le + 1]) - cu.n0;
     const uint8_t* base = a.w2 + (int64_t)cu.e * a.H * a.I * WB;
 #pragma unroll
@@ -398,17 +366,12 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
       if constexpr (F == MM_FEW_FP8_BLOCK)
         cu.sp[i] = a.s2 + ((int64_t)cu.e * (a.H / 128) + (cu.u * WT + i) / 8) * nst;
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int i = 16 * n + r;
-      cu.bp[n] = reinterpret_cast<const uint8_t*>(a.a) + (int64_t)L.route[cu.n0 + (i < cu.n ? i : 0)] * a.I * 2;
-    }
+    cu.bp = reinterpret_cast<const uint8_t*>(a.a) + (int64_t)L.route[cu.n0 + (r < cu.n ? r : 0)] * a.I * 2;
   };
   auto first = [&](Cursor& cu) {
     cu.j = 0;
     cu.s = f0 % nst;
-    cu.le = le0;
-    cu.q = q0;
+    cu.le = f0 / nst;
     aim(cu);
   };
   auto step = [&](Cursor& cu) {
@@ -417,20 +380,15 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
       first(cu);
     } else if (valid(cu) && ++cu.s == nst) {
       cu.s = 0;
-      ++cu.q;
-      if (uniform(L.start[cu.le]) + cu.q * 16 * NT >= uniform(L.start[cu.le + 1])) ++cu.le, cu.q = 0;
+      ++cu.le;
       aim(cu);
     }
   };
-  auto load = [&](const Cursor& cu, Stage<F, WT, NT, P>& st) {
-    load_weights<F, WT, NT, P>(st, cu.wp, (int64_t)cu.s * (kStage * WB), g);
+  auto load = [&](const Cursor& cu, Stage<F, WT, 1>& st) {
+    load_weights<F, WT, 1>(st, cu.wp, (int64_t)cu.s * (kStage * WB), g);
 #pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            st.b[p][n][j] = *reinterpret_cast<const u32x4*>(cu.bp[n] + (int64_t)p * R * a.I * 2 + (int64_t)cu.s * (kStage * 2) + b_piece<F>(g, j));
+    for (int j = 0; j < 4; ++j)
+      st.b[0][j] = *reinterpret_cast<const u32x4*>(cu.bp + (int64_t)cu.s * (kStage * 2) + b_piece<F>(g, j));
     if constexpr (F == MM_FEW_FP8_BLOCK) {
 #pragma unroll
       for (int i = 0; i < WT; ++i) st.s[i] = cu.sp[i][cu.s];
@@ -441,8 +399,8 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
   ld.u = cu.u = blockIdx.x;
   first(ld);
   first(cu);
-  Stage<F, WT, NT, P> st[D];
-  f32x4 acc[WT][NT];
+  Stage<F, WT, 1> st[D];
+  f32x4 acc[WT];
   clear(acc);
   int side = 0;
 #pragma unroll
@@ -453,26 +411,22 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
   while (cu.u < units) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      if (cu.u < units && valid(cu)) multiply<F, WT, NT, P>(st[d], acc, (cu.n + 15) / 16);
+      if (cu.u < units && valid(cu)) multiply<F, WT, 1>(st[d], acc);
       load(ld, st[d]);
       if (ld.u < units) step(ld);
       if (cu.u < units) {
         const bool last = cu.j + 1 == nsw;
         if (valid(cu) && (last || cu.s + 1 == nst || w * nsw + cu.j + 1 == total)) {
-          // end of this wave's part of a visit: gate * sum into its copy of y
+          // end of this wave's part of an expert: gate * sum into its copy of y
+          if (r < cu.n) {
+            const float gate = L.gate[cu.n0 + r];
+            f32x4* y = ys + side * ylen + ((int64_t)w * a.T + L.token[cu.n0 + r]) * (4 * WT) + g;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int i = 16 * n + r;
-            if (i < cu.n) {
-              const float gate = L.gate[cu.n0 + i];
-              f32x4* y = ys + side * ylen + ((int64_t)w * a.T + L.token[cu.n0 + i]) * (4 * WT) + g;
-#pragma unroll
-              for (int k = 0; k < WT; ++k) {
-                f32x4 v = acc[k][n];
-                if constexpr (F == MM_FEW_FP8)
-                  v *= *reinterpret_cast<const f32x4*>(a.s2 + (int64_t)cu.e * a.H + (cu.u * WT + k) * 16 + 4 * g);
-                y[4 * k] += v * gate;
-              }
+            for (int k = 0; k < WT; ++k) {
+              f32x4 v = acc[k];
+              if constexpr (F == MM_FEW_FP8)
+                v *= *reinterpret_cast<const f32x4*>(a.s2 + (int64_t)cu.e * a.H + (cu.u * WT + k) * 16 + 4 * g);
+              y[4 * k] += v * gate;
             }
           }
           clear(acc);
@@ -491,11 +445,7 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
               yu[(int64_t)k * a.T * 4 * WT + i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             }
             const int64_t at = (int64_t)(i / (4 * WT)) * a.H + cu.u * 16 * WT + (i % (4 * WT)) * 4;
-            if (a.y_f32) {
-              *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + at) = v;
-            } else {
-              *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-            }
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
           }
         }
         step(cu);
@@ -510,8 +460,10 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
 // the weights, fill the vector memory path (64 tokens, e4m3, 32 experts:
 // Linear1 264 us for 0.94 GB of weights).  Here a workgroup takes 256 weight
 // rows of one expert, 32 a wave, and all of the expert's routes; both come by
-// LDS-DMA, 128 bytes of a weight row a stage, two stages ahead.
-// Bound: HBM.
+// LDS-DMA, 128 bytes of a weight row a stage, two stages ahead (one where
+// three stages do not fit LDS).  64 tokens, 7168 x 2048, 32 experts in e4m3:
+// Linear1 191 us for 940 MB (4.9 TB/s), Linear2 111 us for 470 MB and the
+// slots, combine 7 us.  Bound: HBM.
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -525,22 +477,15 @@ struct ExpertRoutes {
   int32_t route[kMaxT];
   int32_t token[kMaxT];
   float gate[kMaxT];
-  int32_t expert, n;
+  int32_t expert, n, twice;
 };
 
 // The `index`-th live expert (n = 0 if there are fewer); as build_lists.
 __device__ void find_expert(const FewArgs& a, ExpertRoutes& X, int index) {
   const int tid = threadIdx.x, Et = a.E + a.S, n = a.T * a.K;
-  for (int e = tid; e < Et; e += kThreads) X.tokens[e] = 0;
-  if (tid < kMaxT) X.route[tid] = 0x7fffffff, X.token[tid] = 0, X.gate[tid] = 0.0f;
+  if (tid < kMaxT) X.route[tid] = 0, X.token[tid] = 0, X.gate[tid] = 0.0f;
   if (tid == 0) X.n = 0, X.expert = 0;
-  __syncthreads();
-  for (int i = tid; i < n; i += kThreads) {
-    const int t = i / a.K, id = a.ids[i];
-    if (id >= 0 && id < a.E && (a.active == nullptr || a.active[t] != 0)) atomicOr(&X.tokens[id], 1ull << t);
-  }
-  if (a.S && tid < a.T && (a.active == nullptr || a.active[tid] != 0)) atomicOr(&X.tokens[a.E], 1ull << tid);
-  __syncthreads();
+  const bool twice = mark_tokens(a, X.tokens, X.twice);
   if (tid < 64) {
     int before = 0;
     for (int e0 = 0; e0 < Et; e0 += 64) {
@@ -559,13 +504,16 @@ __device__ void find_expert(const FewArgs& a, ExpertRoutes& X, int index) {
   const unsigned long long mine = X.tokens[e];
   auto place = [&](int t, int k, float gate) {
     const int p = __popcll(mine & ((1ull << t) - 1));
-    atomicMin(&X.route[p], t * (a.K + a.S) + k);
-    atomicAdd(&X.gate[p], gate);
+    X.route[p] = t * (a.K + a.S) + k;
+    X.gate[p] = gate;
     X.token[p] = t;
   };
   if (e < a.E) {
-    for (int i = tid; i < n; i += kThreads)
-      if (a.ids[i] == e && (mine >> (i / a.K) & 1)) place(i / a.K, i % a.K, a.weights[i]);
+    for (int i = tid; i < n; i += kThreads) {
+      const int t = i / a.K;
+      float gate;
+      if (a.ids[i] == e && (mine >> t & 1) && first_route(a, twice, t, i % a.K, e, gate)) place(t, i % a.K, gate);
+    }
   } else if (tid < a.T && (mine >> tid & 1)) {
     place(tid, a.K, 1.0f);
   }
@@ -651,7 +599,8 @@ __device__ __forceinline__ void few_tile(const FewArgs& a) {
     };
     constexpr int kCopies = kTileRows / 64 + XW;
     f32x4 acc[2][NT];
-    clear(acc);
+    clear(acc[0]);
+    clear(acc[1]);
     auto compute = [&](const uint8_t* ws, const uint8_t* xs, float s0, float s1) {
       f32x4 sum[2][NT];
 #pragma unroll
@@ -781,7 +730,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 // wrote: a valid id that no earlier k of the token names.
 __global__ __launch_bounds__(256) void k_few_combine(FewArgs a) {
   const int t = blockIdx.y, c = ((int)blockIdx.x * 256 + threadIdx.x) * 4, Ks = a.K + a.S;
-  __shared__ int32_t ids[32];
+  __shared__ int32_t ids[kMaxK];
   const bool on = a.active == nullptr || a.active[t] != 0;
   if (threadIdx.x < a.K) ids[threadIdx.x] = a.ids[t * a.K + threadIdx.x];
   __syncthreads();
@@ -805,26 +754,22 @@ __global__ __launch_bounds__(256) void k_few_combine(FewArgs a) {
 
 namespace {
 
-template <int F, int CT, int NT, int P, int D>
+template <int F, int P, int D>
 hipError_t run_l1(const FewArgs& a, int num_cus, hipStream_t s) {
   const int64_t routes = (int64_t)a.T * a.K + (a.S ? a.T : 0);
   const int64_t live = routes < a.E + a.S ? routes : a.E + a.S;
-  const int64_t units = live * (a.I / (16 * CT));
+  const int64_t units = live * (a.I / 16);
   const int grid = (int)(units < num_cus ? units : num_cus);
-  hipLaunchKernelGGL((k_few_l1<F, CT, NT, P, D>), dim3(grid), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((k_few_l1<F, P, D>), dim3(grid), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
-template <int F, int WT, int NT, int P, int D>
+template <int F, int WT, int D>
 hipError_t run_l2(const FewArgs& a, int num_cus, hipStream_t s) {
   const int units = a.H / (16 * WT);
   const size_t lds = (size_t)2 * kWaves * a.T * 4 * WT * 16;
-  if (lds > 32768) {   // beside the lists, more than 64 KiB
-    const hipError_t err = hipFuncSetAttribute((const void*)k_few_l2<F, WT, NT, P, D>,
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (err != hipSuccess) return err;
-  }
-  hipLaunchKernelGGL((k_few_l2<F, WT, NT, P, D>), dim3(units < num_cus ? units : num_cus), dim3(kThreads), lds, s, a);
+  static_assert(2 * kWaves * kStreamT * 4 * 2 * 16 + sizeof(Lists) <= 65536, "LDS without an attribute");
+  hipLaunchKernelGGL((k_few_l2<F, WT, D>), dim3(units < num_cus ? units : num_cus), dim3(kThreads), lds, s, a);
   return hipGetLastError();
 }
 
@@ -841,8 +786,8 @@ template <int F, int P>
 hipError_t run_l1_f(const FewArgs& a, int num_cus, hipStream_t s) {
   // 16 tokens, 32 experts of 7168 x 2048, top-8, us for the whole layer with
   // streaming / tile Linear1: bf16 468 / 519, e4m3 253 / 269; 64 tokens e4m3: 420 / 305
-  if (a.T > 16) return run_tile<F, 1, P>(a, s);
-  return run_l1<F, 1, 1, P, 3>(a, num_cus, s);
+  if (a.T > kStreamT) return run_tile<F, 1, P>(a, s);
+  return run_l1<F, P, 3>(a, num_cus, s);
 }
 template <int F, int P>
 hipError_t run_l2_f(const FewArgs& a, int num_cus, hipStream_t s) {
@@ -856,8 +801,9 @@ hipError_t run_l2_f(const FewArgs& a, int num_cus, hipStream_t s) {
     // 32 columns a unit where that still gives most CUs one: half the control
     // per weight byte (e4m3, one token: 30 against 37 us; bf16, at 5.9 TB/s
     // within a unit, loses by the missing units: 56 against 51 us)
-    if (F != MM_FEW_BF16 && a.H / 32 >= num_cus * 3 / 4) return run_l2<F, 2, 1, P, 3>(a, num_cus, s);
-    return run_l2<F, 1, 1, P, 4>(a, num_cus, s);
+    if constexpr (F != MM_FEW_BF16)
+      if (a.H / 32 >= num_cus * 3 / 4) return run_l2<F, 2, 3>(a, num_cus, s);
+    return run_l2<F, 1, 4>(a, num_cus, s);
   } else {
     return hipErrorInvalidValue;               // float32 y always takes the tiles
   }
@@ -886,7 +832,7 @@ hipError_t run_l2_p(const FewArgs& a, int num_cus, hipStream_t s) {
 // columns.  us for the whole layer, streaming / tiles, e4m3: float32 y 1 token
 // 99 / 82, 4 tokens 214 / 176, 16 tokens 360 / 253; bf16 y 77 / 81, 156 / 172,
 // 231 / 243, 64 tokens 440 / 305.
-bool few_slots(int64_t T, int y_f32) { return y_f32 || T > 16; }
+bool few_slots(int64_t T, int y_f32) { return y_f32 || T > kStreamT; }
 
 hipError_t launch_few_l1(const FewArgs& a, int num_cus, hipStream_t s) {
   return a.y_f32 ? run_l1_p<3>(a, num_cus, s) : run_l1_p<1>(a, num_cus, s);

@@ -286,6 +286,30 @@ def test_few_same_expert_twice():
     within(y, want, err)
 
 
+@pytest.mark.parametrize("T,y_dtype", [(3, "bf16"), (3, "f32"), (40, "f32")])
+def test_few_same_expert_many_times(T, y_dtype):
+    """Several weights of one expert are added in the order of k: large ones that cancel around small ones show it."""
+    E, K = 6, 6
+    ids, wts = few_routes(T, E, K, 3)
+    ids[1] = 2
+    wts[1] = torch.tensor([2.0 ** 20, 1.0 + 2.0 ** -20, -(2.0 ** 20), 0.25, 2.0 ** 21, -(2.0 ** 21)])
+    ids[2] = torch.tensor([1, 4, 1, -1, 4, 1])
+    dev, v1, v2 = few_weights("bf16", E, 256, 128, 4)
+    x = torch.randn(T, 256, generator=gen(5)).to(BF16)
+    one = wts.clone()
+    one[1] = 0
+    for k in range(K):
+        one[1, 0] += wts[1, k]                              # float32, in order
+    want, err = ref.moe(x, v1, v2, torch.where(torch.arange(T)[:, None] == 1, ids.where(torch.arange(K) == 0, -torch.ones_like(ids)), ids),
+                        one, y_bf16=y_dtype == "bf16")
+    first = None
+    for _ in range(4):
+        y, _, _ = moe.moe_few(x.cuda(), *dev, topk_ids=ids.cuda(), topk_weights=wts.cuda(), y_dtype=y_dtype)
+        within(y, want, err)
+        assert first is None or torch.equal(first, y)
+        first = y
+
+
 def test_few_nonfinite_stays_in_its_token():
     T, E = 18, 4
     dev, v1, v2 = few_weights("fp8_block", E, 512, 256, 8)
