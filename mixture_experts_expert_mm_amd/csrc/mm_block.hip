@@ -157,7 +157,8 @@ __device__ __forceinline__ TileAt uniform_tile(const TileAt& t) {
 // Tile `at` of class c in the order (group, 6 M-blocks, N-block, M-block): the
 // 32 tiles of an XCD then read 6 row panels and 5 or 6 weight panels.  A CU's
 // requests wait 500 cycles on average, and how many find L2 decides the rate:
-// 16384 x 4096 x 7168 takes 424 us (504 with all M-blocks first, 437 with 4).
+// 16384 x 4096 x 7168 takes 424 us (482 with 64 M-blocks first), 16384 x 7168 x
+// 2048 270 us (280 with 8, 292 with 64).
 __device__ bool find_tile(const BlockArgs& a, int c, int64_t at, TileAt& o) {
   const int bn = cols_of(c), nb = (a.N + bn - 1) / bn;
   int l = lane_id();
@@ -199,8 +200,9 @@ __device__ bool find_tile(const BlockArgs& a, int c, int64_t at, TileAt& o) {
 // row tile, and its result one 8-byte store.
 // Bound: the copies.  Products alone take 1.03 us a stage, copies that always
 // hit the same lines 1.0 us, the real ones 1.65 us: 64 KiB a stage with a
-// mean latency of 500 cycles.  16384 x 4096 x 7168 runs at 2.27 PFLOP/s; a
-// large e4m3 library product reaches 2.67 here.
+// mean latency of 500 cycles, of which a CU has about 64 lines in flight.
+// 16384 x 4096 x 7168 ran at 2.27 PFLOP/s; a large e4m3 library product reaches
+// 2.67 here.
 // PAIR (small tiles): two groups of 128 a stage, in four slots of LDS, for
 // half as many waits.
 template <int WN, int NT, int MT, bool PAIR, int SR>
@@ -389,8 +391,8 @@ __device__ __forceinline__ void mma_tile(const BlockArgs& a, const TileAt& at, u
 // each class's list (neighbours share an L2), and its workgroups take
 // every n-th tile of it in turn.
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_block_mma(BlockArgs a) {
-  // five separate arrays: the compiler then sees that a stage's reads and the
-  // other stage's copies do not meet, and does not wait for the copies
+  // separate arrays: the compiler then sees that a stage's reads and the other
+  // stage's copies do not meet, and does not wait for the copies
   __shared__ __attribute__((aligned(1024))) uint8_t sa0[kBM * kBlock], sa1[kBM * kBlock], sb0[kBN * kBlock], sb1[kBN * kBlock];
   __shared__ float ssc[2][2][kBM];
   const int x = blockIdx.x % 8, step = gridDim.x / 8;
@@ -491,8 +493,8 @@ __global__ __launch_bounds__(kThreads) void k_block_few(BlockArgs a) {
 // waves.  The first weights are asked for, the rows are quantised into LDS
 // meanwhile (the same codes and scales as k_block_quantize, by the same
 // code), then the waves stream their K-blocks.  Bound: latency: one row x
-// 7168 x 2048 takes 5.x us for 14.7 MB of weights (3 us at the copy rate);
-// a quantising kernel before it added 2 us and a launch.
+// 7168 x 2048 takes 7.1 us for 14.7 MB of weights (3 us at the copy rate);
+// a quantising kernel before it took 2.5 us and a launch more.
 constexpr int kRowThreads = 256, kRowWaves = 4;
 constexpr int64_t kRowBytes = 64 * 1024;        // most codes in LDS
 
@@ -576,9 +578,10 @@ hipError_t launch_block_gemm(const BlockArgs& args, int num_cus, hipStream_t s) 
   if (rest == 0 || rest > kFewRows || a.M > rest) {
     if (rest > 0 && rest <= kFewRows) a.M -= rest;
     // Measured at 4096 x 7168, us with large tiles / small ones / small ones
-    // two groups a stage: 128 rows 60 / 36 / 30, 512 rows 96 / 39 / 32, 1024 rows
-    // (64 large tiles, 512 small ones) 97 / 51 / 60, 2048 rows (128 large tiles)
-    // 97 / 104 / 90; 32 groups of 16 rows (512 half tiles) 184 / 276 / -.
+    // two groups a stage: 128 rows 60 / 36 / 30, 512 rows 81 / 40 / 33, 1024 rows
+    // (64 large tiles, 512 small ones) 83 / 54 / 60, 1500 rows (96 large tiles)
+    // 81 / 84 / -, 2048 rows (128) 83 / 95 / 90; 32 groups of 16 rows (512 half
+    // tiles) 184 / 276 / -.
     const int64_t even = a.M / a.G > 0 ? a.M / a.G : 1;
     const int64_t tiles = (even + kBM - 1) / kBM * a.G * ((a.N + kBN - 1) / kBN);
     const unsigned cus = (unsigned)((num_cus + 7) / 8 * 8);

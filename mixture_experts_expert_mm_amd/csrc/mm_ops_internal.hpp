@@ -25,7 +25,7 @@ struct RouterArgs {
   float scale;
 };
 struct RouterShape {
-  int wide;                  // 0: 16 x 16 a wave; 1: 64 tokens x 64 experts a wave; 2: LDS tiles
+  int wide;                  // 0: 16 x 16 a wave; 1: 64 tokens x 64 experts a wave; 2: tiles of 128 x 256 through LDS; 3: of 256 x 256
   int ks;                    // slices of the hidden dimension over workgroups
   int ep;                    // padded experts of a row of partial scores
 };

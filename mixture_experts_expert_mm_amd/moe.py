@@ -199,6 +199,8 @@ def _stream_of(device, stream):
     """Context in which outputs are allocated and kernels launched: the device of the inputs and, if one is given,
     the stream, so that the allocator knows who uses the buffers."""
     if stream is not None:
+        if getattr(stream, "device", device) != device:
+            raise ValueError(f"stream: one of {device} is needed, got one of {stream.device}")
         return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
     if device.index != torch.cuda.current_device():
         return torch.cuda.device(device)
@@ -288,7 +290,7 @@ def moe_few(x, w1, w2, s1=None, s2=None, *, topk_ids=None, topk_weights=None, ro
             raise ValueError(f"router_weight: [{E}, {H}] is needed")
         K = int(topk)
     else:
-        K = int(topk_ids.shape[1]) if topk_ids.dim() == 2 else 0
+        K = int(topk_ids.shape[1]) if isinstance(topk_ids, torch.Tensor) and topk_ids.dim() == 2 else 0
         _need("topk_ids", topk_ids, torch.int32, (T, K), dev)
         _need("topk_weights", topk_weights, torch.float32, (T, K), dev)
     plan = _few_plan(max(T, 1), H, I, E, K, fmt, y_dtype, activation_clamp, S)
