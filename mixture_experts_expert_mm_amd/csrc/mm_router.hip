@@ -170,7 +170,9 @@ constexpr int kTileE = 256;
 // workgroup (8 waves of 16 * TT x 64), stages of 64 hidden values filled by
 // LDS-DMA: three slots for TT = 4, two stages ahead; two slots for TT = 8.
 // Bound: the copies, of which a CU takes 36 to 40 bytes a ns: 2.8 MB a CU with
-// TT = 4 at 16384 x 256 x 7168, 1.9 MB with 8.
+// TT = 4 at 16384 x 256 x 7168, 1.9 MB with 8 (92 / 71 us: 28 stages of 1.9 us, the
+// rest is the first stage and the writes of 67 MB of partial scores.  Tokens
+// two stages ahead in a third slot: the same time).
 template <int TT>
 __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, uint8_t* w0, uint8_t* x1, uint8_t* w1,
                                             uint8_t* x2, uint8_t* w2) {
@@ -324,18 +326,19 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 // One wave per token.  (Four tokens a wave in turn, the next one's scores
 // asked for meanwhile, took 58 against 42 us at 16384 x 256: a token that needs
 // 64-bit sums then holds up three others.)  Bound: issue, about 500
-// instructions a token, and the latency of the scores.
+// instructions a token, and the latency of the scores: 43 us at 16384 x 256
+// (27 without the turns that select, 29 without the 64-bit sums).
 template <int NV, int KM>
 __global__ __launch_bounds__(256, NV <= 4 ? 4 : 1) void k_router_select(RouterArgs a) {
   const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
   if (t >= a.T) return;
   RouterExperts<NV> ex;
-  RouterToken<NV, KM> tok;
+  RouterToken<NV> tok;
   router_load_token<NV, KM>(a, t, tok);
   router_load_experts<NV, KM>(a, ex);
   int id;
   float w;
-  router_select_token<NV, KM>(a, t, ex, tok, id, w);
+  router_select_token<NV>(a, t, ex, tok, id, w);
   const int l = lane_id();
   if (l < a.K) {
     a.ids[t * a.K + l] = id;
@@ -348,32 +351,42 @@ __global__ __launch_bounds__(256, NV <= 4 ? 4 : 1) void k_router_select(RouterAr
 // kernels, 16 x 16 / 64 x 64 a wave, hidden 7168: 333 tokens x 32 experts
 // 17 / 20, 1000 x 32 22 / 23, 1000 x 64 30 / 27, 4000 x 32 44 / 34).  Beyond, with
 // up to 64 experts, a wave holds 64 x 64 and the waves share the hidden
-// dimension; with more experts the LDS tiles (64 x 64 a wave / tiles: 16384 x
-// 32 81 / 94, 16384 x 64 91 / 95, 2000 x 128 40 / 38, 16384 x 128 144 / 110, 16384 x
-// 256 210 / 92 for the scores alone).
+// dimension; with more experts the LDS tiles (64 x 64 a wave / tiles of 128 x
+// 256: 16384 x 32 81 / 94, 16384 x 64 91 / 95, 2000 x 128 40 / 38, 16384 x 128
+// 144 / 110).  Tiles of 256 x 256 where half of the CUs get one of 24 stages or
+// more (tiles of 128 / 256 rows, hidden 7168: 16384 x 256 126 / 113, 10000 x 256
+// 107 / 95, 16384 x 128 102 / 96, 2000 x 256 39 / 50; hidden 2048: 33000 x 128
+// 122 / 105, 16384 x 160, 8 stages, 52 / 58; hidden 4096: 8192 x 512, 16 stages,
+// 73 / 82).
 RouterShape router_shape(int64_t T, int H, int E) {
   RouterShape s{};
   const int steps = H / kRouterStep;
   s.ep = (E + 15) / 16 * 16;
-  s.wide = T <= 64 || T * E <= 32768 ? 0 : E <= 64 ? 1 : E > 128 && T >= 16384 ? 3 : 2;
-  int64_t tiles = 1, most = steps / (kWaves * 4);
-  if (s.wide == 0) {
-    s.ks = (int)most;
-  } else {
-    if (s.wide == 1) {
-      tiles = (T + 63) / 64;
-      most = steps / (2 * kWaves);
-    } else {
-      const int rows = s.wide == 3 ? 256 : 128;
-      tiles = (T + rows - 1) / rows * ((E + kTileE - 1) / kTileE);
-      most = steps / 8;
-    }
-    const int64_t want = 256 / tiles;
-    s.ks = (int)(want < most ? want : most);
+  if (T <= 64 || T * E <= 32768) {
+    s.wide = 0;
+    s.ks = steps / (kWaves * 4);
+    s.ks = s.ks < 1 ? 1 : s.ks > 8 ? 8 : s.ks;
+    return s;
   }
-  s.ks = s.ks < 1 ? 1 : s.ks > 8 ? 8 : s.ks;
-  if (s.wide >= 2) s.ks = s.ks >= 8 ? 8 : s.ks >= 4 ? 4 : s.ks >= 2 ? 2 : 1;   // whole XCDs to a slice
-  return s;
+  // slices that fill the CUs with `tiles`, of `least` steps at least
+  auto slices = [&](int64_t tiles, int least) {
+    int64_t n = 256 / tiles;
+    n = n < steps / least ? n : steps / least;
+    return (int)(n < 1 ? 1 : n > 8 ? 8 : n);
+  };
+  if (E <= 64) {
+    s.wide = 1;
+    s.ks = slices((T + 63) / 64, 2 * kWaves);
+    return s;
+  }
+  const int64_t cols = (E + kTileE - 1) / kTileE;
+  for (s.wide = 3;; s.wide = 2) {
+    const int rows = s.wide == 3 ? 256 : 128;
+    const int64_t tiles = (T + rows - 1) / rows * cols;
+    const int n = slices(tiles, 8);
+    s.ks = n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;   // whole XCDs to a slice
+    if (s.wide == 2 || (tiles * s.ks >= 128 && steps / s.ks >= 24)) return s;
+  }
 }
 
 hipError_t launch_router_scores(const RouterArgs& a, hipStream_t s) {
@@ -411,6 +424,7 @@ hipError_t launch_router_select(const RouterArgs& a, hipStream_t s) {
   if (a.E <= 64) return run_select<1>(a, s);
   if (a.E <= 128) return run_select<2>(a, s);
   if (a.E <= 256) return run_select<4>(a, s);
+  if (a.E <= 512) return run_select<8>(a, s);
   return run_select<16>(a, s);
 }
 

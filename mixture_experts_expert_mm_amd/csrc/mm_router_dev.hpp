@@ -73,17 +73,19 @@ __device__ __forceinline__ float rank_value(uint32_t k) {
   return k == 1u ? __builtin_nanf("") : __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// KM: most slices of the hidden dimension (2 or 8), all asked for at once.
+// KM: most slices of the hidden dimension (2 or 8).  Up to 32 partial scores a
+// lane are asked for at once (16 experts a lane and 8 slices together did not
+// fit the registers: 8192 x 512 141 against 86 us).
 
 // What does not change from token to token: lane l holds experts l, l + 64, ...
 template <int NV>
 struct RouterExperts {
   float norm[NV], bias[NV];      // |w|; bias
 };
-// One token's partial scores, all asked for at once.
-template <int NV, int KM>
+// One token: |x|^2, the float32 scores.
+template <int NV>
 struct RouterToken {
-  float xx[KM], part[NV][KM];
+  float xx, score[NV];
   int active;
 };
 
@@ -106,16 +108,30 @@ __device__ __forceinline__ void router_load_experts(const RouterArgs& a, RouterE
 }
 
 template <int NV, int KM>
-__device__ __forceinline__ void router_load_token(const RouterArgs& a, int64_t t, RouterToken<NV, KM>& x) {
+__device__ __forceinline__ void router_load_token(const RouterArgs& a, int64_t t, RouterToken<NV>& x) {
+  constexpr int KC = KM * NV <= 32 ? KM : 32 / NV;
   x.active = a.active == nullptr ? 1 : a.active[t];
+  x.xx = 0.0f;
 #pragma unroll
-  for (int k = 0; k < KM; ++k)
-    if (k == 0 || k < a.KS) {
-      x.xx[k] = a.xnorm[(int64_t)k * a.T + t];
+  for (int v = 0; v < NV; ++v) x.score[v] = 0.0f;
+  for (int k0 = 0; k0 < (KC == KM ? 1 : a.KS); k0 += KC) {
+    float xx[KC], part[NV][KC];
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-        x.part[v][k] = a.part[((int64_t)k * a.T + t) * a.Ep + (lane_id() + 64 * v < a.E ? lane_id() + 64 * v : 0)];
-    }
+    for (int k = 0; k < KC; ++k)
+      if (k == 0 || k0 + k < a.KS) {
+        xx[k] = a.xnorm[(int64_t)(k0 + k) * a.T + t];
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          part[v][k] = a.part[((int64_t)(k0 + k) * a.T + t) * a.Ep + (lane_id() + 64 * v < a.E ? lane_id() + 64 * v : 0)];
+      }
+#pragma unroll
+    for (int k = 0; k < KC; ++k)
+      if (k == 0 || k0 + k < a.KS) {
+        x.xx += xx[k];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) x.score[v] += part[v][k];
+      }
+  }
 }
 
 // Lane k returns the k-th expert of token t and its weight (-1 and 0 where
@@ -125,18 +141,15 @@ __device__ __forceinline__ void router_load_token(const RouterArgs& a, int64_t t
 // one, mostly of two): the members of a run get their 64-bit ranks and are put
 // in order among themselves.  Tokens whose float32 sums left their range, and
 // runs past 64 positions, are selected again one expert at a time.
-template <int NV, int KM>
+template <int NV>
 __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t t, const RouterExperts<NV>& ex,
-                                                    const RouterToken<NV, KM>& tok, int& id, float& weight) {
+                                                    const RouterToken<NV>& tok, int& id, float& weight) {
   const int l = lane_id();
   id = -1;
   weight = 0.0f;
   if (tok.active == 0) return;
   const bool sig = a.scoring == MM_ROUTER_SIGMOID, biased = a.bias != nullptr;
-  float xx = tok.xx[0];
-#pragma unroll
-  for (int k = 1; k < KM; ++k)
-    if (k < a.KS) xx += tok.xx[k];
+  const float xx = tok.xx;
   float z[NV], err[NV];        // score argument; bound on the rank's error
   uint32_t key[NV];
   // Every step of a score's float32 sum rounds a partial sum, and the
@@ -151,11 +164,7 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
   for (int v = 0; v < NV; ++v) {
     z[v] = 0.0f, err[v] = 0.0f, key[v] = 0;
     if (l + 64 * v >= a.E) continue;
-    float s = tok.part[v][0];
-#pragma unroll
-    for (int k = 1; k < KM; ++k)
-      if (k < a.KS) s += tok.part[v][k];
-    const float b = ex.bias[v], wn = ex.norm[v];
+    const float s = tok.score[v], b = ex.bias[v], wn = ex.norm[v];
     float d = unit * (0.125f * wn * xnorm + fabsf(s)) + 1e-36f, rank;
     if (sig) {
       z[v] = s;

@@ -61,7 +61,8 @@ def test_router(T, H, E, K, scoring, bias):
 
 
 @pytest.mark.parametrize("T,H,E,K", [(600, 512, 64, 8), (1100, 256, 33, 4), (2500, 2048, 48, 6), (530, 1280, 65, 8),
-                                     (1000, 1024, 300, 10), (2049, 2304, 128, 8), (300, 7168, 256, 8), (33000, 256, 66, 2)])
+                                     (1000, 1024, 300, 10), (2049, 2304, 128, 8), (300, 7168, 256, 8), (33000, 256, 66, 2),
+                                     (10001, 6144, 129, 8), (33100, 1536, 70, 4), (4100, 1024, 500, 9)])
 @pytest.mark.parametrize("scoring,bias", [("softmax", False), ("sigmoid", True)])
 def test_router_many_tokens(T, H, E, K, scoring, bias):
     """The kernels that share a tile among tokens: 64 x 64 up to 64 experts, 128 x 256 beyond, one to eight slices."""
