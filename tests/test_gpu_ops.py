@@ -561,6 +561,17 @@ def test_repeated_calls_are_bitwise_equal():
             assert torch.equal(p, q)
 
 
+def test_stream_of_another_device_is_refused():
+    class Elsewhere:
+        device = torch.device("cuda", 7)
+
+    x = torch.zeros(4, 256, dtype=BF16, device="cuda")
+    with pytest.raises(ValueError, match="stream"):
+        moe.route(x, torch.zeros(8, 256, dtype=BF16, device="cuda"), topk=2, stream=Elsewhere())
+    with pytest.raises(ValueError, match="stream"):
+        moe.block_quantize(x, stream=Elsewhere())
+
+
 def test_streams_and_graphs():
     """Captured and replayed with eager work between, two graphs replayed on two streams at once, and a call on a
     stream other than the current one: all equal the eager results."""
