@@ -116,21 +116,22 @@ __device__ __forceinline__ void group_rows(const BlockArgs& a, int gi, int64_t& 
 
 // How the rows of a group are cut: into blocks of 256 rows, a rest of up to
 // 128 rows being a half block (half the products), listed after the full
-// ones.  kMid: blocks of 128 rows and 64 columns.
-enum Class : int { kFull = 0, kHalf = 1, kMid = 2 };
+// ones.  kMid: blocks of 128 rows and 64 columns; the others as they say.
+enum Class : int { kFull = 0, kHalf = 1, kMid = 2, k64x64 = 3, k64x32 = 4, k32x32 = 5 };
+
+__host__ __device__ __forceinline__ int cols_of(int c) { return c <= kHalf ? kBN : c <= k64x64 ? kMidBN : 32; }
+__host__ __device__ __forceinline__ int most_rows(int c) { return c <= kHalf ? kBM : c == kMid ? kMidBM : c == k32x32 ? 32 : 64; }
 
 // M-blocks of class c in a group of n rows
 __device__ __forceinline__ int64_t blocks_of(int c, int64_t n) {
   const int rest = (int)(n % kBM);
-  if (c == kMid) return (n + kMidBM - 1) / kMidBM;
+  if (c >= kMid) return (n + most_rows(c) - 1) / most_rows(c);
   if (c == kHalf) return rest > 0 && rest <= kBM / 2 ? 1 : 0;
   return n / kBM + (rest > kBM / 2 ? 1 : 0);
 }
 __device__ __forceinline__ int64_t first_block_row(int c, int64_t n, int64_t mb) {
-  return c == kFull ? mb * kBM : c == kMid ? mb * kMidBM : n / kBM * kBM;
+  return c == kHalf ? n / kBM * kBM : mb * most_rows(c);
 }
-__device__ __forceinline__ int cols_of(int c) { return c == kMid ? kMidBN : kBN; }
-__device__ __forceinline__ int most_rows(int c) { return c == kMid ? kMidBM : kBM; }
 
 // M-blocks of class c over all groups (every lane of the wave takes part)
 __device__ int64_t count_blocks(const BlockArgs& a, int c) {
@@ -439,6 +440,136 @@ __global__ __launch_bounds__(kThreads) void k_block_mid(BlockArgs a) {
   }
 }
 
+// Products with few tiles of any size: 32 * MT rows x 32 * NT columns by four
+// waves (2 x 2), two groups of 128 K-values a stage, four stages of LDS.  With
+// one stage ahead, as in the tiles above, a stage takes a microsecond whatever
+// the rows: the latency of a copy.
+template <int MT, int NT>
+__device__ __forceinline__ void ring_tile(const BlockArgs& a, const TileAt& at, uint8_t* s0, uint8_t* s1, uint8_t* s2, uint8_t* s3,
+                                          float* c0, float* c1, float* c2, float* c3) {
+  constexpr int BM = 32 * MT, BN = 32 * NT, kPart = (BM + BN) * kBlock;
+  constexpr int kCopies = 2 * (MT + NT) + 1;      // instructions of a wave and stage
+  const int tid = threadIdx.x;
+  const TileAt t = uniform_tile(at);
+  const int w = uniform(tid / 64), l = tid % 64, r = l % 16, g = l / 16, wm = w % 2, wn = w / 2;
+  const int KB = a.K / kBlock, stages = (KB + 1) / 2, rows = t.rows, cols = a.N - t.n0 < BN ? a.N - t.n0 : BN;
+  // as mma_tile: 8 rows of 128 bytes an instruction, chunks swapped by row, zeros beyond the rows
+  const uint32_t voff = (uint32_t)(l / 8) * a.K + (((l % 8) ^ ((4 * (w % 2) + l / 16) % 8)) * 16);
+  const uint8_t *ab = a.a + t.m0 * a.K, *bb = a.b + ((int64_t)t.group * a.N + t.n0) * a.K;
+  // row scales by the same path: lane i of wave w brings group i % 2 of row 32 * w + i / 2
+  const uint32_t svo = w < MT ? (uint32_t)((32 * w + l / 2) * KB + l % 2) * 4 : 0x7fffff00u;
+  const float* asb = a.as + t.m0 * KB;
+  const int nb = (t.n0 + wn * NT * 16) / kBlock, nblocks = (a.N + kBlock - 1) / kBlock;
+  const float* bsp = a.bs + ((int64_t)t.group * nblocks + (nb < nblocks ? nb : nblocks - 1)) * KB;
+  const int sw = (r / 2) % 8;
+  const int o0 = (g ^ sw) * 16 + r * kBlock, o1 = ((g + 4) ^ sw) * 16 + r * kBlock;
+  auto block = [&](int kb) { return kb < KB ? kb : KB - 1; };   // past the end: the last group again, unused
+  auto copy = [&](int s, uint8_t* to, float* sc) {
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)ab, (short)0, rows * a.K, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)bb, (short)0, cols * a.K, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)asb, (short)0, rows * KB * 4, 0x00020000);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int at = block(2 * s + p) * kBlock;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(to + p * kPart + BM * kBlock + (w + 4 * i) * 1024), 16, voff, (w + 4 * i) * 8 * a.K + at, 0, 0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(to + p * kPart + (w + 4 * i) * 1024), 16, voff, (w + 4 * i) * 8 * a.K + at, 0, 0);
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(sc + w * 64), 4, svo, (s < stages ? s : stages - 1) * 8, 0, 0);
+  };
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto turn = [&]() {
+    // the stage's products stay before the wait: nothing else ties them to it
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) asm volatile("" : "+v"(acc[j][i]));
+    __builtin_amdgcn_sched_barrier(0);
+    constexpr int kLeft = 2 * kCopies;            // the two newest stages' copies may be in flight
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (kLeft & 15) | (kLeft >> 4) << 14);
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  float sb[2] = {bsp[0], bsp[block(1)]};
+  auto stage = [&](int s, const uint8_t* from, const float* sc, uint8_t* to, float* nsc) {
+    const float n0 = bsp[block(2 * s + 2)], n1 = bsp[block(2 * s + 3)];
+    copy(s + 3, to, nsc);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      if (p == 0 || 2 * s + 1 < KB) {
+        u32x4 af[MT][2], bf[NT][2];
+        float sa[MT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint8_t* q = from + p * kPart + BM * kBlock + (wn * NT + j) * 16 * kBlock;
+          bf[j][0] = *reinterpret_cast<const u32x4*>(q + o0);
+          bf[j][1] = *reinterpret_cast<const u32x4*>(q + o1);
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const uint8_t* q = from + p * kPart + (wm * MT + i) * 16 * kBlock;
+          af[i][0] = *reinterpret_cast<const u32x4*>(q + o0);
+          af[i][1] = *reinterpret_cast<const u32x4*>(q + o1);
+          sa[i] = sc[((wm * MT + i) * 16 + r) * 2 + p] * sb[p];
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < MT; ++i) acc[j][i] += mfma128(bf[j][0], bf[j][1], af[i][0], af[i][1]) * sa[i];
+      }
+    turn();
+    sb[0] = n0, sb[1] = n1;
+  };
+  copy(0, s0, c0);
+  copy(1, s1, c1);
+  copy(2, s2, c2);
+  turn();
+  for (int s = 0; s < stages; s += 4) {
+    stage(s, s0, c0, s3, c3);
+    if (s + 1 >= stages) break;
+    stage(s + 1, s1, c1, s0, c0);
+    if (s + 2 >= stages) break;
+    stage(s + 2, s2, c2, s1, c1);
+    if (s + 3 >= stages) break;
+    stage(s + 3, s3, c3, s2, c2);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);              // no copy outlives the tile
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int n = t.n0 + (wn * NT + j) * 16 + 4 * g;
+      const int row = (wm * MT + i) * 16 + r;
+      if (row < rows && n < a.N)
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + (t.m0 + row) * a.N + n) =
+            u32x2{pack_bf16x2(acc[j][i][0], acc[j][i][1]), pack_bf16x2(acc[j][i][2], acc[j][i][3])};
+    }
+  __syncthreads();      // the next tile of this workgroup writes the stages again
+}
+
+template <int MT, int NT>
+__global__ __launch_bounds__(256) void k_block_ring(BlockArgs a) {
+  constexpr int kBytes = (32 * MT + 32 * NT) * kBlock * 2, c = MT == 1 ? k32x32 : NT == 1 ? k64x32 : k64x64;
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[kBytes], s1[kBytes], s2[kBytes], s3[kBytes];
+  __shared__ __attribute__((aligned(1024))) float c0[256], c1[256], c2[256], c3[256];
+  const int x = blockIdx.x % 8, step = gridDim.x / 8;
+  const int64_t total = count_blocks(a, c) * ((a.N + cols_of(c) - 1) / cols_of(c));
+  const int64_t first = total * x / 8, n = total * (x + 1) / 8 - first;
+  for (int64_t k = blockIdx.x / 8; k < n; k += step) {
+    TileAt t;
+    if (!find_tile(a, c, first + k, t)) break;
+    ring_tile<MT, NT>(a, t, s0, s1, s2, s3, c0, c1, c2, c3);
+  }
+}
+
 // Up to 16 rows of one matrix (a.m_first and on): 16 columns a workgroup.
 // Each weight byte goes straight from memory into an operand; the 8 waves
 // share the K-blocks, D of them in flight a wave, and meet in LDS.
@@ -586,7 +717,11 @@ hipError_t launch_block_gemm(const BlockArgs& args, int num_cus, hipStream_t s) 
     const int64_t tiles = (even + kBM - 1) / kBM * a.G * ((a.N + kBN - 1) / kBN);
     const unsigned cus = (unsigned)((num_cus + 7) / 8 * 8);
     const int64_t small = (even + kMidBM - 1) / kMidBM * a.G * ((a.N + kMidBN - 1) / kMidBN);
-    if (tiles < 112 && small <= num_cus) hipLaunchKernelGGL(k_block_mid<true>, dim3(cus), dim3(kThreads), 0, s, a);
+    auto count = [&](int c) { return (even + most_rows(c) - 1) / most_rows(c) * a.G * ((a.N + cols_of(c) - 1) / cols_of(c)); };
+    if (count(k32x32) <= num_cus) hipLaunchKernelGGL((k_block_ring<1, 1>), dim3(cus), dim3(256), 0, s, a);
+    else if (count(k64x32) <= num_cus) hipLaunchKernelGGL((k_block_ring<2, 1>), dim3(cus), dim3(256), 0, s, a);
+    else if (count(k64x64) <= num_cus) hipLaunchKernelGGL((k_block_ring<2, 2>), dim3(cus), dim3(256), 0, s, a);
+    else if (tiles < 112 && small <= num_cus) hipLaunchKernelGGL(k_block_mid<true>, dim3(cus), dim3(kThreads), 0, s, a);
     else if (tiles < 112) hipLaunchKernelGGL(k_block_mid<false>, dim3(3 * cus), dim3(kThreads), 0, s, a);
     else hipLaunchKernelGGL(k_block_mma, dim3(cus), dim3(kThreads), 0, s, a);
     const hipError_t err = hipGetLastError();
