@@ -314,8 +314,7 @@ __device__ __forceinline__ void mma_tile(const BlockArgs& a, const TileAt& at, u
 #pragma unroll
       for (int i = 0; i < MT; ++i) asm volatile("" : "+v"(acc[j][i]));
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's copies have landed
-    __syncthreads();
+    stage_barrier<0>();
     __builtin_amdgcn_sched_barrier(0);
   };
   if constexpr (PAIR) {
@@ -492,12 +491,11 @@ __device__ __forceinline__ void ring_tile(const BlockArgs& a, const TileAt& at, 
 #pragma unroll
       for (int i = 0; i < MT; ++i) asm volatile("" : "+v"(acc[j][i]));
     __builtin_amdgcn_sched_barrier(0);
-    constexpr int kLeft = 2 * kCopies;            // the two newest stages' copies may be in flight
-    __builtin_amdgcn_s_waitcnt(0x0F70 | (kLeft & 15) | (kLeft >> 4) << 14);
-    __syncthreads();
+    stage_barrier<2 * kCopies>();                 // the two newest stages' copies may be in flight
     __builtin_amdgcn_sched_barrier(0);
   };
   float sb[2] = {bsp[0], bsp[block(1)]};
+  __builtin_amdgcn_sched_barrier(0);
   auto stage = [&](int s, const uint8_t* from, const float* sc, uint8_t* to, float* nsc) {
     const float n0 = bsp[block(2 * s + 2)], n1 = bsp[block(2 * s + 3)];
     copy(s + 3, to, nsc);
@@ -532,15 +530,18 @@ __device__ __forceinline__ void ring_tile(const BlockArgs& a, const TileAt& at, 
   copy(1, s1, c1);
   copy(2, s2, c2);
   turn();
-  for (int s = 0; s < stages; s += 4) {
+  // (a break inside the loop would be a path on which the compiler sees a slot
+  // filled one stage ago, and waits for it)
+  int s = 0;
+  for (; s + 3 < stages; s += 4) {
     stage(s, s0, c0, s3, c3);
-    if (s + 1 >= stages) break;
     stage(s + 1, s1, c1, s0, c0);
-    if (s + 2 >= stages) break;
     stage(s + 2, s2, c2, s1, c1);
-    if (s + 3 >= stages) break;
     stage(s + 3, s3, c3, s2, c2);
   }
+  if (s < stages) stage(s, s0, c0, s3, c3);
+  if (s + 1 < stages) stage(s + 1, s1, c1, s0, c0);
+  if (s + 2 < stages) stage(s + 2, s2, c2, s1, c1);
   __builtin_amdgcn_s_waitcnt(0x0F70);              // no copy outlives the tile
 #pragma unroll
   for (int j = 0; j < NT; ++j)

@@ -155,6 +155,15 @@ __device__ __forceinline__ int mx_shared_exp_e4m3(float amax) {
 }
 __device__ __forceinline__ float mx_inv_scale(int x) { return __uint_as_float((uint32_t)(127 - x) << 23); }
 
+// The turn between two stages of LDS-DMA: at most VM of this wave's copies are
+// still in flight, all its LDS reads have returned, then the workgroup
+// barrier.  (__syncthreads waits for every copy in flight.)
+template <int VM>
+__device__ __forceinline__ void stage_barrier() {
+  static_assert(VM < 64, "the wait's field");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
+}
+
 __device__ __forceinline__ float acc_to_f32(float v) { return v; }
 __device__ __forceinline__ float acc_to_f32(int v) { return (float)v; }
 

@@ -642,11 +642,9 @@ __device__ __forceinline__ void few_tile(const FewArgs& a) {
         for (int m = 0; m < NT; ++m) asm volatile("" : "+v"(acc[i][m]));
       __builtin_amdgcn_sched_barrier(0);
       // all copies but the newest stage's (S == 3) have landed
-      __builtin_amdgcn_s_waitcnt(0x0F70 | (S == 3 ? kCopies : 0));
-      __syncthreads();
+      stage_barrier<S == 3 ? kCopies : 0>();
       __builtin_amdgcn_sched_barrier(0);
     };
-    static_assert(kCopies < 16, "the wait's field");
     auto scales = [&](int s, float& s0, float& s1) {
       if constexpr (F == MM_FEW_FP8_BLOCK) s0 = sp0[s < steps ? s : steps - 1], s1 = sp1[s < steps ? s : steps - 1];
     };
@@ -664,13 +662,16 @@ __device__ __forceinline__ void few_tile(const FewArgs& a) {
     if constexpr (S == 3) copy(1, w1, x1);
     turn();
     if constexpr (S == 3) {
-      for (int s = 0; s < steps; s += 3) {
+      // (a break inside the loop would be a path on which the compiler sees a
+      // slot filled one stage ago, and waits for it)
+      int s = 0;
+      for (; s + 2 < steps; s += 3) {
         stage(s, w0, x0, w2, x2);
-        if (s + 1 >= steps) break;
         stage(s + 1, w1, x1, w0, x0);
-        if (s + 2 >= steps) break;
         stage(s + 2, w2, x2, w1, x1);
       }
+      if (s < steps) stage(s, w0, x0, w2, x2);
+      if (s + 1 < steps) stage(s + 1, w1, x1, w0, x0);
     } else {
       for (int s = 0; s < steps; s += 2) {
         stage(s, w0, x0, w1, x1);

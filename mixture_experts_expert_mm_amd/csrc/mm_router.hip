@@ -247,9 +247,7 @@ __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, ui
       for (int j = 0; j < TT; ++j) asm volatile("" : "+v"(acc[i][j]));
     __builtin_amdgcn_sched_barrier(0);
     // all copies but, with three slots, the newest stage's
-    static_assert(TT != 4 || kCopies == 6, "vmcnt(6)");
-    __builtin_amdgcn_s_waitcnt(TT == 4 ? 0x0F76 : 0x0F70);
-    __syncthreads();
+    stage_barrier<TT == 4 ? kCopies : 0>();
     __builtin_amdgcn_sched_barrier(0);
   };
 #pragma unroll
@@ -258,14 +256,23 @@ __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, ui
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) copy(i, s0 + 1, x1, w1);
     turn();
-    for (int s = s0; s < s1; s += 3) {
+    // (a break inside the loop would be a path on which the compiler sees a
+    // slot filled one stage ago, and waits for it)
+    int s = s0;
+    for (; s + 2 < s1; s += 3) {
       compute(x0, w0, s + 2, x2, w2);
       turn();
-      if (s + 1 >= s1) break;
       compute(x1, w1, s + 3, x0, w0);
       turn();
-      if (s + 2 >= s1) break;
       compute(x2, w2, s + 4, x1, w1);
+      turn();
+    }
+    if (s < s1) {
+      compute(x0, w0, s + 2, x2, w2);
+      turn();
+    }
+    if (s + 1 < s1) {
+      compute(x1, w1, s + 3, x0, w0);
       turn();
     }
   } else {
