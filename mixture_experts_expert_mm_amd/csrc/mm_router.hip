@@ -213,8 +213,8 @@ __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, ui
   // squared norms: of the tokens a quarter by each of the four waves that hold them
   const bool do_x = blockIdx.y == 0, do_w = tile == 0 && wt == 0;
   const int sw = (r / 2) % 8;
-  // the copies of stage `next` go out two at a time among the first products
-  auto compute = [&](const uint8_t* xs, const uint8_t* ws, int next, uint8_t* nx, uint8_t* nw) {
+  // the copies of stages nsx (x) and nsw (Wr) go out two at a time among the first products, Wr's before x's
+  auto compute = [&](const uint8_t* xs, const uint8_t* ws, int nsx, uint8_t* nx, int nsw, uint8_t* nw) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int c = ((4 * h + g) ^ sw) * 16 + r * 128;
@@ -226,8 +226,9 @@ __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, ui
 #pragma unroll
       for (int j = 0; j < TT; ++j) {
         if (h == 0 && 2 * j < kCopies) {
-          copy(2 * j, next, nx, nw);
-          if (2 * j + 1 < kCopies) copy(2 * j + 1, next, nx, nw);
+          const int i = (2 * j + kTileT / 64) % kCopies;
+          copy(i, i < kTileT / 64 ? nsx : nsw, nx, nw);
+          copy(i + 1, i < kTileT / 64 ? nsx : nsw, nx, nw);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i][j] = mfma16(wf[i], xf[j], acc[i][j]);
@@ -246,42 +247,69 @@ __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, ui
 #pragma unroll
       for (int j = 0; j < TT; ++j) asm volatile("" : "+v"(acc[i][j]));
     __builtin_amdgcn_sched_barrier(0);
-    // all copies but, with three slots, the newest stage's
-    stage_barrier<TT == 4 ? kCopies : 0>();
+    // all copies but the newest stage's (TT = 8: its x)
+    stage_barrier<TT == 4 ? kCopies : kTileT / 64>();
     __builtin_amdgcn_sched_barrier(0);
   };
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) copy(i, s0, x0, w0);
-  if constexpr (TT == 4) {
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) copy(i, s0 + 1, x1, w1);
-    turn();
+  for (int i = 0; i < (TT == 4 ? kCopies : kTileT / 64); ++i) copy(i, s0 + 1, x1, w1);
+  turn();
+  if constexpr (TT == 4) {
     // (a break inside the loop would be a path on which the compiler sees a
     // slot filled one stage ago, and waits for it)
     int s = s0;
     for (; s + 2 < s1; s += 3) {
-      compute(x0, w0, s + 2, x2, w2);
+      compute(x0, w0, s + 2, x2, s + 2, w2);
       turn();
-      compute(x1, w1, s + 3, x0, w0);
+      compute(x1, w1, s + 3, x0, s + 3, w0);
       turn();
-      compute(x2, w2, s + 4, x1, w1);
+      compute(x2, w2, s + 4, x1, s + 4, w1);
       turn();
     }
     if (s < s1) {
-      compute(x0, w0, s + 2, x2, w2);
+      compute(x0, w0, s + 2, x2, s + 2, w2);
       turn();
     }
     if (s + 1 < s1) {
-      compute(x1, w1, s + 3, x0, w0);
+      compute(x1, w1, s + 3, x0, s + 3, w0);
       turn();
     }
   } else {
-    turn();
-    for (int s = s0; s < s1; s += 2) {
-      compute(x0, w0, s + 1, x1, w1);
+    int s = s0;
+    for (; s + 5 < s1; s += 6) {
+      compute(x0, w0, s + 2, x2, s + 1, w1);
       turn();
-      if (s + 1 >= s1) break;
-      compute(x1, w1, s + 2, x0, w0);
+      compute(x1, w1, s + 3, x0, s + 2, w0);
+      turn();
+      compute(x2, w0, s + 4, x1, s + 3, w1);
+      turn();
+      compute(x0, w1, s + 5, x2, s + 4, w0);
+      turn();
+      compute(x1, w0, s + 6, x0, s + 5, w1);
+      turn();
+      compute(x2, w1, s + 7, x1, s + 6, w0);
+      turn();
+    }
+    if (s < s1) {
+      compute(x0, w0, s + 2, x2, s + 1, w1);
+      turn();
+    }
+    if (s + 1 < s1) {
+      compute(x1, w1, s + 3, x0, s + 2, w0);
+      turn();
+    }
+    if (s + 2 < s1) {
+      compute(x2, w0, s + 4, x1, s + 3, w1);
+      turn();
+    }
+    if (s + 3 < s1) {
+      compute(x0, w1, s + 5, x2, s + 4, w0);
+      turn();
+    }
+    if (s + 4 < s1) {
+      compute(x1, w0, s + 6, x0, s + 5, w1);
       turn();
     }
   }
@@ -326,8 +354,8 @@ __global__ __launch_bounds__(kThreads) void k_router_tile128(RouterArgs a) {
   router_tile<4>(a, x0, w0, x1, w1, x2, w2);
 }
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_router_tile256(RouterArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t x0[256 * 128], x1[256 * 128], w0[kTileE * 128], w1[kTileE * 128];
-  router_tile<8>(a, x0, w0, x1, w1, nullptr, nullptr);
+  __shared__ __attribute__((aligned(1024))) uint8_t x0[256 * 128], x1[256 * 128], x2[256 * 128], w0[kTileE * 128], w1[kTileE * 128];
+  router_tile<8>(a, x0, w0, x1, w1, x2, nullptr);
 }
 
 // One wave per token.  (Four tokens a wave in turn, the next one's scores
