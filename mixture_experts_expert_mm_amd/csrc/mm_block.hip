@@ -97,6 +97,7 @@ constexpr int kBM = 256, kBN = 256;       // the large tile
 constexpr int kMidBM = 128, kMidBN = 64;  // the small tile
 constexpr int kFewRows = 16;              // most rows of a streaming unit
 constexpr int kFewCols = 16;
+constexpr int kRing = 4;                  // stages of the smallest tiles
 constexpr int kGroupM = 6;                // M-blocks that a run of tiles goes through before the next N-block
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -117,10 +118,10 @@ __device__ __forceinline__ void group_rows(const BlockArgs& a, int gi, int64_t& 
 // How the rows of a group are cut: into blocks of 256 rows, a rest of up to
 // 128 rows being a half block (half the products), listed after the full
 // ones.  kMid: blocks of 128 rows and 64 columns; the others as they say.
-enum Class : int { kFull = 0, kHalf = 1, kMid = 2, k64x64 = 3, k64x32 = 4, k32x32 = 5 };
+enum Class : int { kFull = 0, kHalf = 1, kMid = 2, k64x64 = 3, k64x32 = 4, k32x32 = 5, k32x16 = 6 };
 
-__host__ __device__ __forceinline__ int cols_of(int c) { return c <= kHalf ? kBN : c <= k64x64 ? kMidBN : 32; }
-__host__ __device__ __forceinline__ int most_rows(int c) { return c <= kHalf ? kBM : c == kMid ? kMidBM : c == k32x32 ? 32 : 64; }
+__host__ __device__ __forceinline__ int cols_of(int c) { return c <= kHalf ? kBN : c <= k64x64 ? kMidBN : c == k32x16 ? 16 : 32; }
+__host__ __device__ __forceinline__ int most_rows(int c) { return c <= kHalf ? kBM : c == kMid ? kMidBM : c >= k32x32 ? 32 : 64; }
 
 // M-blocks of class c in a group of n rows
 __device__ __forceinline__ int64_t blocks_of(int c, int64_t n) {
@@ -440,14 +441,20 @@ __global__ __launch_bounds__(kThreads) void k_block_mid(BlockArgs a) {
 }
 
 // Products with few tiles of any size: 32 * MT rows x 32 * NT columns by four
-// waves (2 x 2), two groups of 128 K-values a stage, four stages of LDS.  With
-// one stage ahead, as in the tiles above, a stage takes a microsecond whatever
-// the rows: the latency of a copy.
+// waves (2 x 2), two groups of 128 K-values a stage, four stages of LDS.
+// NT = 0: 16 columns; two waves take a stage's first group, two its second.
+// Bound: the stages in turn: 17 rows x 4096 x 7168 takes 12.5 us with weights from
+// HBM (29 MB, 6 us at the copy rate): its copies alone 11.7, its products alone
+// 9.8; with one stage ahead instead of three 24.  Six or eight stages: the same
+// or worse (more to fill first).
 template <int MT, int NT>
-__device__ __forceinline__ void ring_tile(const BlockArgs& a, const TileAt& at, uint8_t* s0, uint8_t* s1, uint8_t* s2, uint8_t* s3,
-                                          float* c0, float* c1, float* c2, float* c3) {
-  constexpr int BM = 32 * MT, BN = 32 * NT, kPart = (BM + BN) * kBlock;
-  constexpr int kCopies = 2 * (MT + NT) + 1;      // instructions of a wave and stage
+__device__ __forceinline__ void ring_tile(const BlockArgs& a, const TileAt& at, uint8_t* const (&slot)[kRing],
+                                          float* const (&scale)[kRing]) {
+  constexpr int D = kRing;
+  constexpr bool SPLIT = NT == 0;
+  constexpr int BM = 32 * MT, BN = SPLIT ? 16 : 32 * NT, kPart = (BM + BN) * kBlock, kGroups = (BM + BN) / 8;
+  constexpr int kCopies = 2 * kGroups / 4 + 1;    // instructions of a wave and stage
+  constexpr int NC = SPLIT ? 1 : NT;              // column tiles of a wave
   const int tid = threadIdx.x;
   const TileAt t = uniform_tile(at);
   const int w = uniform(tid / 64), l = tid % 64, r = l % 16, g = l / 16, wm = w % 2, wn = w / 2;
@@ -458,55 +465,77 @@ __device__ __forceinline__ void ring_tile(const BlockArgs& a, const TileAt& at, 
   // row scales by the same path: lane i of wave w brings group i % 2 of row 32 * w + i / 2
   const uint32_t svo = w < MT ? (uint32_t)((32 * w + l / 2) * KB + l % 2) * 4 : 0x7fffff00u;
   const float* asb = a.as + t.m0 * KB;
-  const int nb = (t.n0 + wn * NT * 16) / kBlock, nblocks = (a.N + kBlock - 1) / kBlock;
-  const float* bsp = a.bs + ((int64_t)t.group * nblocks + (nb < nblocks ? nb : nblocks - 1)) * KB;
+  const int nb = t.n0 / kBlock, nblocks = (a.N + kBlock - 1) / kBlock;   // BN columns lie in one block
+  const float* bsp = a.bs + ((int64_t)t.group * nblocks + nb) * KB;
   const int sw = (r / 2) % 8;
   const int o0 = (g ^ sw) * 16 + r * kBlock, o1 = ((g + 4) ^ sw) * 16 + r * kBlock;
   auto block = [&](int kb) { return kb < KB ? kb : KB - 1; };   // past the end: the last group again, unused
+  // (stages past the end are copied from nothing: without a memory access)
   auto copy = [&](int s, uint8_t* to, float* sc) {
-    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)ab, (short)0, rows * a.K, 0x00020000);
-    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)bb, (short)0, cols * a.K, 0x00020000);
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)asb, (short)0, rows * KB * 4, 0x00020000);
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)ab, (short)0, s < stages ? rows * a.K : 0, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)bb, (short)0, s < stages ? cols * a.K : 0, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)asb, (short)0, s < stages ? rows * KB * 4 : 0, 0x00020000);
+    if constexpr (SPLIT) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int at = block(2 * s + p) * kBlock;
+      for (int i = 0; i < 2 * kGroups / 4; ++i) {
+        const int item = w + 4 * i, p = item / kGroups, grp = item % kGroups;   // rows of a, then of b
+        const bool of_a = grp < BM / 8;
+        const int at = block(2 * s + p) * kBlock + (of_a ? grp : grp - BM / 8) * 8 * a.K;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(of_a ? ra : rb, (lds_ptr_t)(to + p * kPart + grp * 1024), 16, voff, at, 0, 0);
+      }
+    } else {
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(to + p * kPart + BM * kBlock + (w + 4 * i) * 1024), 16, voff, (w + 4 * i) * 8 * a.K + at, 0, 0);
+      for (int p = 0; p < 2; ++p) {
+        const int at = block(2 * s + p) * kBlock;
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(to + p * kPart + (w + 4 * i) * 1024), 16, voff, (w + 4 * i) * 8 * a.K + at, 0, 0);
+        for (int i = 0; i < NT; ++i)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr_t)(to + p * kPart + BM * kBlock + (w + 4 * i) * 1024), 16, voff, (w + 4 * i) * 8 * a.K + at, 0, 0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(to + p * kPart + (w + 4 * i) * 1024), 16, voff, (w + 4 * i) * 8 * a.K + at, 0, 0);
+      }
     }
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(sc + w * 64), 4, svo, (s < stages ? s : stages - 1) * 8, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(sc + w * 64), 4, svo, s * 8, 0, 0);
   };
-  f32x4 acc[NT][MT];
+  f32x4 acc[NC][MT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int j = 0; j < NC; ++j)
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   auto turn = [&]() {
     // the stage's products stay before the wait: nothing else ties them to it
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NC; ++j)
 #pragma unroll
       for (int i = 0; i < MT; ++i) asm volatile("" : "+v"(acc[j][i]));
     __builtin_amdgcn_sched_barrier(0);
-    stage_barrier<2 * kCopies>();                 // the two newest stages' copies may be in flight
+    stage_barrier<(D - 2) * kCopies>();           // all but the next stage's copies may be in flight
     __builtin_amdgcn_sched_barrier(0);
   };
-  float sb[2] = {bsp[0], bsp[block(1)]};
+  // Weight scales by lane, the next CB blocks' asked for CB blocks ahead: a load
+  // that a stage waits for would wait for the copies before it too.
+  constexpr int CB = 8 * D;
+  float cur = bsp[block(l)], nxt = bsp[block(CB + l)];
+  int base = 0;
+  auto refresh = [&](int s) {
+    if (2 * s - base != CB) return;
+    base += CB;
+    cur = nxt;
+    nxt = bsp[block(base + CB + l)];
+  };
   __builtin_amdgcn_sched_barrier(0);
   auto stage = [&](int s, const uint8_t* from, const float* sc, uint8_t* to, float* nsc) {
-    const float n0 = bsp[block(2 * s + 2)], n1 = bsp[block(2 * s + 3)];
-    copy(s + 3, to, nsc);
+    copy(s + D - 1, to, nsc);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int u = 0; u < (SPLIT ? 1 : 2); ++u) {
+      const int p = SPLIT ? wn : u;
       if (p == 0 || 2 * s + 1 < KB) {
-        u32x4 af[MT][2], bf[NT][2];
+        u32x4 af[MT][2], bf[NC][2];
         float sa[MT];
+        const float sb = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(cur), 2 * s + p - base));
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+        for (int j = 0; j < NC; ++j) {
           const uint8_t* q = from + p * kPart + BM * kBlock + (wn * NT + j) * 16 * kBlock;
           bf[j][0] = *reinterpret_cast<const u32x4*>(q + o0);
           bf[j][1] = *reinterpret_cast<const u32x4*>(q + o1);
@@ -516,37 +545,53 @@ __device__ __forceinline__ void ring_tile(const BlockArgs& a, const TileAt& at, 
           const uint8_t* q = from + p * kPart + (wm * MT + i) * 16 * kBlock;
           af[i][0] = *reinterpret_cast<const u32x4*>(q + o0);
           af[i][1] = *reinterpret_cast<const u32x4*>(q + o1);
-          sa[i] = sc[((wm * MT + i) * 16 + r) * 2 + p] * sb[p];
+          sa[i] = sc[((wm * MT + i) * 16 + r) * 2 + p] * sb;
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NC; ++j)
 #pragma unroll
           for (int i = 0; i < MT; ++i) acc[j][i] += mfma128(bf[j][0], bf[j][1], af[i][0], af[i][1]) * sa[i];
       }
+    }
     turn();
-    sb[0] = n0, sb[1] = n1;
   };
-  copy(0, s0, c0);
-  copy(1, s1, c1);
-  copy(2, s2, c2);
+#pragma unroll
+  for (int u = 0; u < D - 1; ++u) copy(u, slot[u], scale[u]);
   turn();
   // (a break inside the loop would be a path on which the compiler sees a slot
   // filled one stage ago, and waits for it)
+  auto at_slot = [&](int s, int u) { stage(s + u, slot[u], scale[u], slot[(u + D - 1) % D], scale[(u + D - 1) % D]); };
   int s = 0;
-  for (; s + 3 < stages; s += 4) {
-    stage(s, s0, c0, s3, c3);
-    stage(s + 1, s1, c1, s0, c0);
-    stage(s + 2, s2, c2, s1, c1);
-    stage(s + 3, s3, c3, s2, c2);
-  }
-  if (s < stages) stage(s, s0, c0, s3, c3);
-  if (s + 1 < stages) stage(s + 1, s1, c1, s0, c0);
-  if (s + 2 < stages) stage(s + 2, s2, c2, s1, c1);
-  __builtin_amdgcn_s_waitcnt(0x0F70);              // no copy outlives the tile
+  for (; s + D <= stages; s += D) {
+    refresh(s);
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+    for (int u = 0; u < D; ++u) at_slot(s, u);
+  }
+  refresh(s);
+#pragma unroll
+  for (int u = 0; u < D - 1; ++u) {
+    if (s + u >= stages) break;
+    at_slot(s, u);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);              // no copy outlives the tile
+  if constexpr (SPLIT) {
+    __syncthreads();                               // nobody reads or fills a stage any more
+    f32x4* half = reinterpret_cast<f32x4*>(slot[0]);
+    if (wn == 1) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) half[(wm * MT + i) * 64 + l] = acc[0][i];
+    }
+    __syncthreads();
+    if (wn == 0) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[0][i] += half[(wm * MT + i) * 64 + l];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
+      if (SPLIT && wn != 0) break;
       const int n = t.n0 + (wn * NT + j) * 16 + 4 * g;
       const int row = (wm * MT + i) * 16 + r;
       if (row < rows && n < a.N)
@@ -558,20 +603,24 @@ __device__ __forceinline__ void ring_tile(const BlockArgs& a, const TileAt& at, 
 
 template <int MT, int NT>
 __global__ __launch_bounds__(256) void k_block_ring(BlockArgs a) {
-  constexpr int kBytes = (32 * MT + 32 * NT) * kBlock * 2, c = MT == 1 ? k32x32 : NT == 1 ? k64x32 : k64x64;
+  constexpr int c = NT == 0 ? k32x16 : MT == 1 ? k32x32 : NT == 1 ? k64x32 : k64x64;
+  constexpr int kBytes = (32 * MT + (NT == 0 ? 16 : 32 * NT)) * kBlock * 2;
+  // separate arrays, as in k_block_mma
   __shared__ __attribute__((aligned(1024))) uint8_t s0[kBytes], s1[kBytes], s2[kBytes], s3[kBytes];
-  __shared__ __attribute__((aligned(1024))) float c0[256], c1[256], c2[256], c3[256];
+  __shared__ float c0[256], c1[256], c2[256], c3[256];   // a float a thread, whatever the rows
+  uint8_t* const slot[kRing] = {s0, s1, s2, s3};
+  float* const scale[kRing] = {c0, c1, c2, c3};
   const int x = blockIdx.x % 8, step = gridDim.x / 8;
   const int64_t total = count_blocks(a, c) * ((a.N + cols_of(c) - 1) / cols_of(c));
   const int64_t first = total * x / 8, n = total * (x + 1) / 8 - first;
   for (int64_t k = blockIdx.x / 8; k < n; k += step) {
     TileAt t;
     if (!find_tile(a, c, first + k, t)) break;
-    ring_tile<MT, NT>(a, t, s0, s1, s2, s3, c0, c1, c2, c3);
+    ring_tile<MT, NT>(a, t, slot, scale);
   }
 }
 
-// Up to 16 rows of one matrix (a.m_first and on): 16 columns a workgroup.
+// The last rows of one matrix, up to 16 (a.m_first and on): 16 columns a workgroup.
 // Each weight byte goes straight from memory into an operand; the 8 waves
 // share the K-blocks, D of them in flight a wave, and meet in LDS.
 __global__ __launch_bounds__(kThreads) void k_block_few(BlockArgs a) {
@@ -621,15 +670,19 @@ __global__ __launch_bounds__(kThreads) void k_block_few(BlockArgs a) {
   }
 }
 
-// A few bf16 rows (a decoded token's projection): 16 columns a workgroup of 4
-// waves.  The first weights are asked for, the rows are quantised into LDS
-// meanwhile (the same codes and scales as k_block_quantize, by the same
-// code), then the waves stream their K-blocks.  Bound: latency: one row x
+// A few rows (a decoded token's projection): 16 columns a workgroup of 4 waves.
+// The first weights are asked for, the rows are brought into LDS meanwhile, from
+// codes or quantised from bf16 (the same codes and scales as k_block_quantize,
+// by the same code), then the waves stream their K-blocks.  Bound: latency: one row x
 // 7168 x 2048 takes 7.1 us for 14.7 MB of weights (3 us at the copy rate);
 // a quantising kernel before it took 2.5 us and a launch more.
 constexpr int kRowThreads = 256, kRowWaves = 4;
-constexpr int64_t kRowBytes = 64 * 1024;        // most codes in LDS
+// Most codes in LDS; us with weights from HBM, these / the smallest tiles: 4 rows
+// x 4096 x 7168 11.5 / 12.0, 8 rows 14.4 / 11.9; 8 rows x 2048 x 4096 7.4 / 7.7, 16
+// rows 9.6 / 7.7.
+constexpr int64_t kRowBytes = 32 * 1024;
 
+template <bool FROM_X>
 __global__ __launch_bounds__(kRowThreads) void k_block_rows(BlockArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   __shared__ f32x4 red[kRowWaves][64];
@@ -653,8 +706,14 @@ __global__ __launch_bounds__(kRowThreads) void k_block_rows(BlockArgs a) {
   };
 #pragma unroll
   for (int d = 0; d < D; ++d) load(d, w + d * kRowWaves);
+  if constexpr (!FROM_X) {
+    const int per = a.K / 16;
+    for (int i = tid; i < M * per; i += kRowThreads)
+      *reinterpret_cast<u32x4*>(codes + i / per * pitch + i % per * 16) = *reinterpret_cast<const u32x4*>(a.a + (int64_t)i * 16);
+    for (int i = tid; i < M * KB; i += kRowThreads) scales[i] = a.as[i];
+  }
   const int per = a.K / 8;
-  for (int i = tid; i < M * per; i += kRowThreads) {   // 16 lanes a group; a whole number of groups a round
+  for (int i = tid; FROM_X && i < M * per; i += kRowThreads) {   // 16 lanes a group; a whole number of groups a round
     const int row = i / per, c = i % per;
     const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.x) + (int64_t)i * 16);
     uint32_t m = amax_bits(v, 0);
@@ -691,46 +750,52 @@ __global__ __launch_bounds__(kRowThreads) void k_block_rows(BlockArgs a) {
   }
 }
 
-bool block_from_x(const BlockArgs& a) { return a.offsets == nullptr && a.M <= 16 && a.M * a.K <= kRowBytes; }
+bool block_in_lds(const BlockArgs& a) { return a.offsets == nullptr && a.M <= 16 && a.M * a.K <= kRowBytes; }
+// bf16 rows are quantised by every workgroup for itself, against a launch more
+// (1 row x 7168 x 2048 7.1 against 9.2 us, 4 rows 9.6 / 9.2, 8 rows 13.1 / 9.2; 2 rows x
+// 4096 x 7168 15.4 / 13.6)
+constexpr int64_t kRowValues = 8 * 1024;
+bool block_from_x(const BlockArgs& a) { return block_in_lds(a) && a.M * a.K <= kRowValues; }
 
 hipError_t launch_block_gemm(const BlockArgs& args, int num_cus, hipStream_t s) {
   BlockArgs a = args;
   const int64_t units = a.N / kFewCols;
-  if (a.x != nullptr) {
+  if (block_in_lds(a)) {
     const size_t lds = (size_t)(a.M * (a.K + 16 + a.K / kBlock * 4));
-    if (lds > 60 * 1024) {   // with the static array, more than 64 KiB
-      const hipError_t err = hipFuncSetAttribute((const void*)k_block_rows, hipFuncAttributeMaxDynamicSharedMemorySize, 72 * 1024);
-      if (err != hipSuccess) return err;
-    }
-    hipLaunchKernelGGL(k_block_rows, dim3((unsigned)units), dim3(kRowThreads), lds, s, a);
+    if (a.x != nullptr) hipLaunchKernelGGL(k_block_rows<true>, dim3((unsigned)units), dim3(kRowThreads), lds, s, a);
+    else hipLaunchKernelGGL(k_block_rows<false>, dim3((unsigned)units), dim3(kRowThreads), lds, s, a);
     return hipGetLastError();
   }
-  // one matrix: up to 16 rows beyond the blocks of 256 are streamed
-  const int64_t rest = a.offsets == nullptr ? a.M % kBM : 0;
-  if (rest == 0 || rest > kFewRows || a.M > rest) {
-    if (rest > 0 && rest <= kFewRows) a.M -= rest;
-    // Measured at 4096 x 7168, us with large tiles / small ones / small ones
-    // two groups a stage: 128 rows 60 / 36 / 30, 512 rows 81 / 40 / 33, 1024 rows
-    // (64 large tiles, 512 small ones) 83 / 54 / 60, 1500 rows (96 large tiles)
-    // 81 / 84 / -, 2048 rows (128) 83 / 95 / 90; 32 groups of 16 rows (512 half
-    // tiles) 184 / 276 / -.
-    const int64_t even = a.M / a.G > 0 ? a.M / a.G : 1;
-    const int64_t tiles = (even + kBM - 1) / kBM * a.G * ((a.N + kBN - 1) / kBN);
-    const unsigned cus = (unsigned)((num_cus + 7) / 8 * 8);
-    const int64_t small = (even + kMidBM - 1) / kMidBM * a.G * ((a.N + kMidBN - 1) / kMidBN);
-    auto count = [&](int c) { return (even + most_rows(c) - 1) / most_rows(c) * a.G * ((a.N + cols_of(c) - 1) / cols_of(c)); };
-    if (count(k32x32) <= num_cus) hipLaunchKernelGGL((k_block_ring<1, 1>), dim3(cus), dim3(256), 0, s, a);
-    else if (count(k64x32) <= num_cus) hipLaunchKernelGGL((k_block_ring<2, 1>), dim3(cus), dim3(256), 0, s, a);
-    else if (count(k64x64) <= num_cus) hipLaunchKernelGGL((k_block_ring<2, 2>), dim3(cus), dim3(256), 0, s, a);
-    else if (tiles < 112 && small <= num_cus) hipLaunchKernelGGL(k_block_mid<true>, dim3(cus), dim3(kThreads), 0, s, a);
-    else if (tiles < 112) hipLaunchKernelGGL(k_block_mid<false>, dim3(3 * cus), dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL(k_block_mma, dim3(cus), dim3(kThreads), 0, s, a);
+  // The smallest tiles that give a CU at most one: us with weights from HBM, 128 x
+  // 64 / 64 x 64, 64 x 32 or 32 x 32 / 32 x 16, 4096 x 7168: 17 rows 34 / 15.3 / 12.5, 64
+  // rows 36 / 15, 128 rows 43 / 21, 256 rows 42 / 27; 2048 x 4096: 17 rows 17.5 / 9.0 /
+  // 7.7, 256 rows 18.6 / 12; 7168 x 2048: 17 rows 12.3 / 6.9 / -, 256 rows 15.5 / 15.3.
+  // Then, at 4096 x 7168, large tiles / 128 x 64 / 128 x 64 with two groups a stage:
+  // 512 rows 81 / 40 / 33, 1024 rows (64 large tiles, 512 small ones) 83 / 54 / 60,
+  // 1500 rows (96 large tiles) 81 / 84 / -, 2048 rows (128) 83 / 95 / 90; 32 groups of
+  // 16 rows (512 half tiles) 184 / 276 / -.
+  const int64_t even = a.M / a.G > 0 ? a.M / a.G : 1;
+  const int64_t tiles = (even + kBM - 1) / kBM * a.G * ((a.N + kBN - 1) / kBN);
+  const unsigned cus = (unsigned)((num_cus + 7) / 8 * 8);
+  auto count = [&](int c) { return (even + most_rows(c) - 1) / most_rows(c) * a.G * ((a.N + cols_of(c) - 1) / cols_of(c)); };
+  if (count(k32x16) <= num_cus) hipLaunchKernelGGL((k_block_ring<1, 0>), dim3(cus), dim3(256), 0, s, a);
+  else if (count(k32x32) <= num_cus) hipLaunchKernelGGL((k_block_ring<1, 1>), dim3(cus), dim3(256), 0, s, a);
+  else if (count(k64x32) <= num_cus) hipLaunchKernelGGL((k_block_ring<2, 1>), dim3(cus), dim3(256), 0, s, a);
+  else if (count(k64x64) <= num_cus) hipLaunchKernelGGL((k_block_ring<2, 2>), dim3(cus), dim3(256), 0, s, a);
+  else if (tiles < 112 && count(kMid) <= num_cus) hipLaunchKernelGGL(k_block_mid<true>, dim3(cus), dim3(kThreads), 0, s, a);
+  else if (tiles < 112) hipLaunchKernelGGL(k_block_mid<false>, dim3(3 * cus), dim3(kThreads), 0, s, a);
+  else {
+    // one matrix: up to 16 rows beyond the blocks of 256 are streamed (4097 rows,
+    // 115 us; 147 with a half tile for the last row)
+    const int64_t rest = a.offsets == nullptr ? a.M % kBM : 0;
+    if (rest <= kFewRows) a.M -= rest;
+    hipLaunchKernelGGL(k_block_mma, dim3(cus), dim3(kThreads), 0, s, a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || a.M == args.M) return err;
     a.m_first = a.M;
     a.M = args.M;
+    hipLaunchKernelGGL(k_block_few, dim3((unsigned)units), dim3(kThreads), 0, s, a);
   }
-  hipLaunchKernelGGL(k_block_few, dim3((unsigned)units), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

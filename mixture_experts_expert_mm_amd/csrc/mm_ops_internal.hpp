@@ -70,7 +70,8 @@ struct BlockArgs {
   int N, K, G;
 };
 hipError_t launch_block_quantize(const void* x, int64_t rows, int cols, uint8_t* q, float* s, hipStream_t st);
-// whether launch_block_gemm quantises a.x on the way (a.a and a.as unused)
+// whether launch_block_gemm holds the rows in LDS, and whether it then quantises a.x on the way (a.a and a.as unused)
+bool block_in_lds(const BlockArgs& a);
 bool block_from_x(const BlockArgs& a);
 hipError_t launch_block_gemm(const BlockArgs& a, int num_cus, hipStream_t s);
 
