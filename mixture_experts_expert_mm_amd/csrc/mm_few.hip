@@ -462,8 +462,8 @@ __global__ __launch_bounds__(kThreads) void k_few_l2(FewArgs a) {
 // rows of one expert, 32 a wave, and all of the expert's routes; both come by
 // LDS-DMA, 128 bytes of a weight row a stage, two stages ahead (one where
 // three stages do not fit LDS).  64 tokens, 7168 x 2048, 32 experts in e4m3:
-// Linear1 191 us for 940 MB (4.9 TB/s), Linear2 111 us for 470 MB and the
-// slots, combine 7 us.  Bound: HBM.
+// Linear1 173 us for 940 MB, Linear2 101 us for 470 MB and the slots, combine 7.5 us.
+// Bound: HBM.  (Waiting for every copy at each stage's barrier: 185, 107, 7.5.)
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -785,8 +785,11 @@ hipError_t run_tile(const FewArgs& a, hipStream_t s) {
 
 template <int F, int P>
 hipError_t run_l1_f(const FewArgs& a, int num_cus, hipStream_t s) {
-  // 16 tokens, 32 experts of 7168 x 2048, top-8, us for the whole layer with
-  // streaming / tile Linear1: bf16 468 / 519, e4m3 253 / 269; 64 tokens e4m3: 420 / 305
+  // us for the whole layer with streaming / tile Linear1, 32 experts of 7168 x 2048,
+  // top-8: 1 token e4m3 77 / 85, 4 tokens 153 / 181, 8 tokens 200 / 208, 16 tokens 237 /
+  // 230, bf16 449 / 447; 16 experts of 4096 x 1408, top-4, bf16: 1 token 50 / 63, 8
+  // tokens 107 / 99, 16 tokens 114 / 113.  One MFMA of routes is the streaming
+  // kernels' limit.
   if (a.T > kStreamT) return run_tile<F, 1, P>(a, s);
   return run_l1<F, P, 3>(a, num_cus, s);
 }
@@ -831,8 +834,8 @@ hipError_t run_l2_p(const FewArgs& a, int num_cus, hipStream_t s) {
 // Linear2 through slots (tiles and a combine), or streaming.  The three parts
 // of A that a float32 y takes cost the streaming kernel a read each per 16
 // columns.  us for the whole layer, streaming / tiles, e4m3: float32 y 1 token
-// 99 / 82, 4 tokens 214 / 176, 16 tokens 360 / 253; bf16 y 77 / 81, 156 / 172,
-// 231 / 243, 64 tokens 440 / 305.
+// 99 / 82, 4 tokens 214 / 172, 16 tokens 360 / 258; bf16 y 77 / 79, 153 / 165,
+// 237 / 246.
 bool few_slots(int64_t T, int y_f32) { return y_f32 || T > kStreamT; }
 
 hipError_t launch_few_l1(const FewArgs& a, int num_cus, hipStream_t s) {

@@ -168,11 +168,11 @@ constexpr int kTileE = 256;
 
 // The same for many tokens and experts: 32 * TT tokens x 256 experts a
 // workgroup (8 waves of 16 * TT x 64), stages of 64 hidden values filled by
-// LDS-DMA: three slots for TT = 4, two stages ahead; two slots for TT = 8.
+// LDS-DMA two stages ahead, in three slots (TT = 8: Wr, which mostly comes from
+// L2, one stage ahead in two; tokens one stage ahead: 70 for 67 us).
 // Bound: the copies, of which a CU takes 36 to 40 bytes a ns: 2.8 MB a CU with
-// TT = 4 at 16384 x 256 x 7168, 1.9 MB with 8 (92 / 71 us: 28 stages of 1.9 us, the
-// rest is the first stage and the writes of 67 MB of partial scores.  Tokens
-// two stages ahead in a third slot: the same time).
+// TT = 4 at 16384 x 256 x 7168, 1.9 MB with 8 (92 / 67 us; the first stage and the
+// writes of 67 MB of partial scores come on top).
 template <int TT>
 __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, uint8_t* w0, uint8_t* x1, uint8_t* w1,
                                             uint8_t* x2, uint8_t* w2) {
