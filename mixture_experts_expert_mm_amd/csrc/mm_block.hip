@@ -118,10 +118,10 @@ __device__ __forceinline__ void group_rows(const BlockArgs& a, int gi, int64_t& 
 // How the rows of a group are cut: into blocks of 256 rows, a rest of up to
 // 128 rows being a half block (half the products), listed after the full
 // ones.  kMid: blocks of 128 rows and 64 columns; the others as they say.
-enum Class : int { kFull = 0, kHalf = 1, kMid = 2, k64x64 = 3, k64x32 = 4, k32x32 = 5, k32x16 = 6 };
+enum Class : int { kFull = 0, kHalf = 1, kMid = 2, k64x64 = 3, k64x32 = 4, k32x32 = 5, k32x16 = 6, k128x128 = 7 };
 
-__host__ __device__ __forceinline__ int cols_of(int c) { return c <= kHalf ? kBN : c <= k64x64 ? kMidBN : c == k32x16 ? 16 : 32; }
-__host__ __device__ __forceinline__ int most_rows(int c) { return c <= kHalf ? kBM : c == kMid ? kMidBM : c >= k32x32 ? 32 : 64; }
+__host__ __device__ __forceinline__ int cols_of(int c) { return c <= kHalf ? kBN : c == k128x128 ? 128 : c <= k64x64 ? kMidBN : c == k32x16 ? 16 : 32; }
+__host__ __device__ __forceinline__ int most_rows(int c) { return c <= kHalf ? kBM : c == kMid || c == k128x128 ? kMidBM : c >= k32x32 ? 32 : 64; }
 
 // M-blocks of class c in a group of n rows
 __device__ __forceinline__ int64_t blocks_of(int c, int64_t n) {
@@ -416,26 +416,27 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
   }
 }
 
-// Products whose large tiles would leave most CUs without one: small tiles,
-// one workgroup a CU with two groups of 128 a stage, or (PAIR false) three
-// with one.
-template <bool PAIR>
+// Products whose large tiles would leave most CUs without one: 128 rows x 32 * NT
+// columns, one workgroup a CU with two groups of 128 a stage, or (PAIR false)
+// three with one.
+template <int NT, bool PAIR>
 __global__ __launch_bounds__(kThreads) void k_block_mid(BlockArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t sa0[kMidBM * kBlock], sa1[kMidBM * kBlock];
-  __shared__ __attribute__((aligned(1024))) uint8_t sb0[kMidBN * kBlock], sb1[kMidBN * kBlock];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb0[32 * NT * kBlock], sb1[32 * NT * kBlock];
   __shared__ float ssc[2][2][kMidBM];
+  constexpr int c = NT == 2 ? kMid : k128x128;
   const int x = blockIdx.x % 8, step = gridDim.x / 8;
-  const int64_t total = count_blocks(a, kMid) * ((a.N + kMidBN - 1) / kMidBN);
+  const int64_t total = count_blocks(a, c) * ((a.N + 32 * NT - 1) / (32 * NT));
   const int64_t first = total * x / 8, n = total * (x + 1) / 8 - first;
   for (int64_t k = blockIdx.x / 8; k < n; k += step) {
     TileAt t;
-    if (!find_tile(a, kMid, first + k, t)) break;
+    if (!find_tile(a, c, first + k, t)) break;
     if constexpr (PAIR) {
       __shared__ __attribute__((aligned(1024))) uint8_t sa2[kMidBM * kBlock], sa3[kMidBM * kBlock];
-      __shared__ __attribute__((aligned(1024))) uint8_t sb2[kMidBN * kBlock], sb3[kMidBN * kBlock];
-      mma_tile<2, 2, 2, true>(a, t, sa0, sa1, sb0, sb1, sa2, sa3, sb2, sb3, ssc);
+      __shared__ __attribute__((aligned(1024))) uint8_t sb2[32 * NT * kBlock], sb3[32 * NT * kBlock];
+      mma_tile<2, NT, 2, true>(a, t, sa0, sa1, sb0, sb1, sa2, sa3, sb2, sb3, ssc);
     } else {
-      mma_tile<2, 2, 2, false>(a, t, sa0, sa1, sb0, sb1, nullptr, nullptr, nullptr, nullptr, ssc);
+      mma_tile<2, NT, 2, false>(a, t, sa0, sa1, sb0, sb1, nullptr, nullptr, nullptr, nullptr, ssc);
     }
   }
 }
@@ -771,9 +772,11 @@ hipError_t launch_block_gemm(const BlockArgs& args, int num_cus, hipStream_t s) 
   // rows 36 / 15, 128 rows 43 / 21, 256 rows 42 / 27; 2048 x 4096: 17 rows 17.5 / 9.0 /
   // 7.7, 256 rows 18.6 / 12; 7168 x 2048: 17 rows 12.3 / 6.9 / -, 256 rows 15.5 / 15.3.
   // Then, at 4096 x 7168, large tiles / 128 x 64 / 128 x 64 with two groups a stage:
-  // 512 rows 81 / 40 / 33, 1024 rows (64 large tiles, 512 small ones) 83 / 54 / 60,
+  // 512 rows 81 / 40 / 33, 1024 rows (64 large tiles, 512 of 128 x 64) 83 / 54 / 60,
   // 1500 rows (96 large tiles) 81 / 84 / -, 2048 rows (128) 83 / 95 / 90; 32 groups of
-  // 16 rows (512 half tiles) 184 / 276 / -.
+  // 16 rows (512 half tiles) 184 / 276 / -.  128 x 64 / 128 x 128 where a CU gets at
+  // most one of these: 1024 x 4096 x 7168 63 / 52, 320 x 7168 x 2048 21 / 18, 2048 x
+  // 2048 x 4096 37 / 30.
   const int64_t even = a.M / a.G > 0 ? a.M / a.G : 1;
   const int64_t tiles = (even + kBM - 1) / kBM * a.G * ((a.N + kBN - 1) / kBN);
   const unsigned cus = (unsigned)((num_cus + 7) / 8 * 8);
@@ -782,8 +785,9 @@ hipError_t launch_block_gemm(const BlockArgs& args, int num_cus, hipStream_t s) 
   else if (count(k32x32) <= num_cus) hipLaunchKernelGGL((k_block_ring<1, 1>), dim3(cus), dim3(256), 0, s, a);
   else if (count(k64x32) <= num_cus) hipLaunchKernelGGL((k_block_ring<2, 1>), dim3(cus), dim3(256), 0, s, a);
   else if (count(k64x64) <= num_cus) hipLaunchKernelGGL((k_block_ring<2, 2>), dim3(cus), dim3(256), 0, s, a);
-  else if (tiles < 112 && count(kMid) <= num_cus) hipLaunchKernelGGL(k_block_mid<true>, dim3(cus), dim3(kThreads), 0, s, a);
-  else if (tiles < 112) hipLaunchKernelGGL(k_block_mid<false>, dim3(3 * cus), dim3(kThreads), 0, s, a);
+  else if (tiles < 112 && count(kMid) <= num_cus) hipLaunchKernelGGL((k_block_mid<2, true>), dim3(cus), dim3(kThreads), 0, s, a);
+  else if (count(k128x128) <= num_cus) hipLaunchKernelGGL((k_block_mid<4, true>), dim3(cus), dim3(kThreads), 0, s, a);
+  else if (tiles < 112) hipLaunchKernelGGL((k_block_mid<2, false>), dim3(3 * cus), dim3(kThreads), 0, s, a);
   else {
     // one matrix: up to 16 rows beyond the blocks of 256 are streamed (4097 rows,
     // 115 us; 147 with a half tile for the last row)

@@ -410,7 +410,7 @@ def test_block_matmul(M, N, K):
 @pytest.mark.parametrize("M,N,K", [(1000, 5120, 384), (900, 6160, 640), (1792, 4096, 128), (1800, 4096, 640), (1900, 4112, 384),
                                    (2048, 3616, 256), (1700, 4224, 896), (4097, 2064, 512), (20, 6416, 4480), (60, 7168, 8320), (40, 4096, 4096),
                                    (100, 7168, 4224), (250, 7168, 4096), (300, 4112, 2176), (9, 4096, 8064), (16, 8192, 2048),
-                                   (272, 4096, 1920), (33, 144, 12416)])
+                                   (272, 4096, 1920), (33, 144, 12416), (700, 4096, 640), (330, 7168, 1152), (1000, 2064, 384)])
 def test_block_matmul_many_tiles(M, N, K):
     """More tiles than compute units, small and large ones, odd and even runs of K-blocks, halves and remainders of rows."""
     test_block_matmul(M, N, K)
