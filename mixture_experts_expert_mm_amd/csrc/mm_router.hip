@@ -399,7 +399,7 @@ RouterShape router_shape(int64_t T, int H, int E) {
   s.ep = (E + 15) / 16 * 16;
   if (T <= 64 || T * E <= 32768) {
     s.wide = 0;
-    s.ks = steps / (kWaves * 4);
+    s.ks = steps / (kWaves * 2);   // two steps a wave, four: 9.4, 10.1 us for both kernels at 1 x 32 x 7168
     s.ks = s.ks < 1 ? 1 : s.ks > 8 ? 8 : s.ks;
     return s;
   }
