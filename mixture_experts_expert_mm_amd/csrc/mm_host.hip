@@ -804,8 +804,10 @@ mm_status mm_router_plan_create(const mm_router_problem* problem, mm_router_plan
   const RouterShape sh = router_shape(p.num_tokens, (int)p.hidden, (int)p.num_experts);
   pl.reserved[0] = sh.ks;
   pl.reserved[1] = sh.ep;
+  pl.reserved[2] = sh.eb;
   pl.workspace_bytes = align_up((int64_t)sh.ks * p.num_tokens * sh.ep * 4, kAlign) +
-                       align_up((int64_t)sh.ks * p.num_tokens * 4, kAlign) + align_up((int64_t)sh.ks * sh.ep * 4, kAlign);
+                       align_up((int64_t)sh.ks * p.num_tokens * 4, kAlign) + align_up((int64_t)sh.ks * sh.ep * 4, kAlign) +
+                       align_up((int64_t)sh.ks * ((p.num_experts + sh.eb - 1) / sh.eb) * p.num_tokens * 4, kAlign);
   pl.checksum = plan_checksum(&pl);
   *plan = pl;
   return MM_OK;
@@ -832,13 +834,16 @@ mm_status mm_router(const mm_router_plan* plan, const void* x, const void* weigh
   a.K = (int)p.num_topk;
   a.KS = (int)plan->reserved[0];
   a.Ep = (int)plan->reserved[1];
+  a.EB = (int)plan->reserved[2];
   a.scoring = p.scoring;
   a.renormalize = p.renormalize;
   a.scale = p.route_scale;
   const int64_t xnorm = align_up((int64_t)a.KS * a.T * a.Ep * 4, kAlign);
   a.part = at<float>(workspace, 0);
   a.xnorm = at<float>(workspace, xnorm);
-  a.wnorm = at<float>(workspace, xnorm + align_up((int64_t)a.KS * a.T * 4, kAlign));
+  const int64_t wnorm = xnorm + align_up((int64_t)a.KS * a.T * 4, kAlign);
+  a.wnorm = at<float>(workspace, wnorm);
+  a.xmost = at<float>(workspace, wnorm + align_up((int64_t)a.KS * a.Ep * 4, kAlign));
   hipStream_t s = static_cast<hipStream_t>(stream);
   MM_TRY(run(MM_K_ROUTER, s, [&] { return launch_router_scores(a, s); }));
   return run(MM_K_ROUTER_SELECT, s, [&] { return launch_router_select(a, s); });

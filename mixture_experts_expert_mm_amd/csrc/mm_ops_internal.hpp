@@ -18,9 +18,10 @@ struct RouterArgs {
   float* weights;            // [T][K]
   float* part;               // ws: [KS][T][Ep] partial scores
   float* xnorm;              // ws: [KS][T] partial |x|^2
+  float* xmost;              // ws: [KS][ceil(E / EB)][T] largest partial sum of a token and EB experts
   float* wnorm;              // ws: [KS][Ep] partial |w|^2
   int64_t T;
-  int H, E, K, Ep, KS;
+  int H, E, K, Ep, KS, EB;
   int scoring, renormalize;
   float scale;
 };
@@ -28,6 +29,7 @@ struct RouterShape {
   int wide;                  // 0: 16 x 16 a wave; 1: 64 tokens x 64 experts a wave; 2: tiles of 128 x 256 through LDS; 3: of 256 x 256
   int ks;                    // slices of the hidden dimension over workgroups
   int ep;                    // padded experts of a row of partial scores
+  int eb;                    // experts of a workgroup
 };
 RouterShape router_shape(int64_t T, int H, int E);
 hipError_t launch_router_scores(const RouterArgs& a, hipStream_t s);

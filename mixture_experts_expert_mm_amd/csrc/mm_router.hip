@@ -8,13 +8,17 @@
 // cut into KS slices so that a single token still occupies many CUs), and
 // k_router_select adds them and selects, one wave per token.
 //
-// The order of two experts is decided by their 64-bit scores.  The float32
-// sum of a score is off by at most about sqrt(steps) * 2^-23 * |x| |w| (every
-// step rounds a partial sum that Cauchy-Schwarz bounds by |x| |w|; the
-// roundings are independent), so the selection carries that bound per
-// expert, and where the best and another expert are closer than their
-// bounds, both are summed again in 64 bits.  About one token in a hundred needs
-// it, for two experts.
+// The order of two experts is decided by their 64-bit scores.  The float32 sum
+// of a score is off by the roundings of its steps: within an MFMA by some
+// 2^-23 of its products (at most |x| |w|), between them by an ulp of the partial
+// sum, independently.  A sum of two values that cancel passes through partial
+// sums far above the score, so the kernels keep the largest one of a token and
+// tile of experts, and the selection carries 2^-23 * (3 |x| |w| + 3 sqrt(steps) *
+// largest) per expert (two outliers that cancel: errors of a third of it; random
+// data: a twentieth).  Where two experts are closer than their bounds, both are
+// summed again in 64 bits: one token in fifty of random data, for two experts.
+#include <type_traits>
+
 #include "mm_router_dev.hpp"
 
 namespace mm {
@@ -40,6 +44,24 @@ __device__ __forceinline__ float sumsq(const u32x4& v, float acc) {
   return acc;
 }
 
+// The largest magnitude of many floats from their bits: the largest positive
+// one in signed order, the largest negative one in unsigned order, half an
+// instruction a value each.
+struct Largest {
+  int32_t pos = 0;
+  uint32_t neg = 0x80000000u;
+  __device__ __forceinline__ void see(const f32x4& v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = v[i];
+      const int32_t b = __builtin_bit_cast(int32_t, f);
+      pos = b > pos ? b : pos;
+      neg = (uint32_t)b > neg ? (uint32_t)b : neg;
+    }
+  }
+  __device__ __forceinline__ float value() const { return fmaxf(__uint_as_float((uint32_t)pos), __uint_as_float(neg & 0x7fffffffu)); }
+};
+
 }  // namespace
 
 // TT x ET tiles of 16 tokens x 16 experts a wave; the 8 waves share the hidden
@@ -50,7 +72,7 @@ template <int TT, int ET>
 __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
   constexpr int KW = kWaves, kSlots = KW / 2;
   __shared__ f32x4 red[kSlots][TT * ET][64];
-  __shared__ float xn[KW][TT * 16], wn[KW][ET * 16];
+  __shared__ float xn[KW][TT * 16], xm[KW][TT * 16], wn[KW][ET * 16];
   const int kw = threadIdx.x / 64, l = threadIdx.x % 64, r = l % 16, g = l / 16;
   const int64_t t0 = (int64_t)blockIdx.x * (16 * TT);
   const int e0 = (int)blockIdx.y * (16 * ET);
@@ -67,8 +89,15 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
   }
   f32x4 acc[TT][ET];
   float xs[TT], ws[ET];
+  Largest most[TT];
 #pragma unroll
   for (int i = 0; i < TT; ++i) xs[i] = 0.0f;
+  auto look = [&]() {
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+#pragma unroll
+      for (int j = 0; j < ET; ++j) most[i].see(acc[i][j]);
+  };
 #pragma unroll
   for (int j = 0; j < ET; ++j) ws[j] = 0.0f;
 #pragma unroll
@@ -88,6 +117,7 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
     for (int i = 0; i < TT; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) xv[i][h] = *reinterpret_cast<const u32x4*>(xp[i] + (int64_t)s * (kRouterStep * 2) + h * 16);
+    look();
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -103,13 +133,16 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
       for (int j = 0; j < ET; ++j) ws[j] = sumsq(wv[j][1], sumsq(wv[j][0], ws[j]));
     }
   }
-  // squared norms: the four lane groups of a row, then the KW waves
+  look();
+  // squared norms and largest partial sums: the four lane groups of a row, then the KW waves
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
-    float v = xs[i];
+    float v = xs[i], m = most[i].value();
     v += __shfl_xor(v, 16, 64);
     v += __shfl_xor(v, 32, 64);
-    if (g == 0) xn[kw][16 * i + r] = v;
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    if (g == 0) xn[kw][16 * i + r] = v, xm[kw][16 * i + r] = m;
   }
 #pragma unroll
   for (int j = 0; j < ET; ++j) {
@@ -147,11 +180,12 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
       }
     }
   }
-  if (blockIdx.y == 0 && (int)threadIdx.x < 16 * TT && t0 + threadIdx.x < a.T) {
-    float v = 0.0f;
+  if ((int)threadIdx.x < 16 * TT && t0 + threadIdx.x < a.T) {
+    float v = 0.0f, m = 0.0f;
 #pragma unroll
-    for (int k = 0; k < KW; ++k) v += xn[k][threadIdx.x];
-    a.xnorm[(int64_t)blockIdx.z * a.T + t0 + threadIdx.x] = v;
+    for (int k = 0; k < KW; ++k) v += xn[k][threadIdx.x], m = fmaxf(m, xm[k][threadIdx.x]);
+    if (blockIdx.y == 0) a.xnorm[(int64_t)blockIdx.z * a.T + t0 + threadIdx.x] = v;
+    a.xmost[((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * a.T + t0 + threadIdx.x] = m;
   }
   if (do_w && (int)threadIdx.x < ET * 16) {
     const int e = (int)blockIdx.y * (16 * ET) + threadIdx.x;
@@ -202,6 +236,7 @@ __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, ui
   };
   f32x4 acc[4][TT];                              // [expert tile][token tile]
   float xs2[TT / 4], ws2[4];
+  Largest most[TT];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     ws2[i] = 0.0f;
@@ -240,12 +275,25 @@ __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, ui
       }
     }
   };
-  auto turn = [&]() {
+  // `look`: every third stage.  What comes and goes between two looks is of the
+  // size of its products, for six steps at most; the bound's products cover it.
+  const std::true_type yes;
+  const std::false_type no;
+  auto turn = [&](auto look) {
     // the stage's products stay before the wait: nothing else ties them to it
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < TT; ++j) asm volatile("" : "+v"(acc[i][j]));
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (decltype(look)::value) {
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most[j].see(acc[i][j]);
+        asm volatile("" : "+v"(most[j].pos), "+v"(most[j].neg));
+      }
+    }
     __builtin_amdgcn_sched_barrier(0);
     // all copies but the newest stage's (TT = 8: its x)
     stage_barrier<TT == 4 ? kCopies : kTileT / 64>();
@@ -255,65 +303,78 @@ __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, ui
   for (int i = 0; i < kCopies; ++i) copy(i, s0, x0, w0);
 #pragma unroll
   for (int i = 0; i < (TT == 4 ? kCopies : kTileT / 64); ++i) copy(i, s0 + 1, x1, w1);
-  turn();
+  turn(no);
   if constexpr (TT == 4) {
     // (a break inside the loop would be a path on which the compiler sees a
     // slot filled one stage ago, and waits for it)
     int s = s0;
     for (; s + 2 < s1; s += 3) {
       compute(x0, w0, s + 2, x2, s + 2, w2);
-      turn();
+      turn(no);
       compute(x1, w1, s + 3, x0, s + 3, w0);
-      turn();
+      turn(no);
       compute(x2, w2, s + 4, x1, s + 4, w1);
-      turn();
+      turn(yes);
     }
     if (s < s1) {
       compute(x0, w0, s + 2, x2, s + 2, w2);
-      turn();
+      turn(yes);
     }
     if (s + 1 < s1) {
       compute(x1, w1, s + 3, x0, s + 3, w0);
-      turn();
+      turn(yes);
     }
   } else {
     int s = s0;
     for (; s + 5 < s1; s += 6) {
       compute(x0, w0, s + 2, x2, s + 1, w1);
-      turn();
+      turn(no);
       compute(x1, w1, s + 3, x0, s + 2, w0);
-      turn();
+      turn(no);
       compute(x2, w0, s + 4, x1, s + 3, w1);
-      turn();
+      turn(yes);
       compute(x0, w1, s + 5, x2, s + 4, w0);
-      turn();
+      turn(no);
       compute(x1, w0, s + 6, x0, s + 5, w1);
-      turn();
+      turn(no);
       compute(x2, w1, s + 7, x1, s + 6, w0);
-      turn();
+      turn(yes);
     }
     if (s < s1) {
       compute(x0, w0, s + 2, x2, s + 1, w1);
-      turn();
+      turn(yes);
     }
     if (s + 1 < s1) {
       compute(x1, w1, s + 3, x0, s + 2, w0);
-      turn();
+      turn(yes);
     }
     if (s + 2 < s1) {
       compute(x2, w0, s + 4, x1, s + 3, w1);
-      turn();
+      turn(yes);
     }
     if (s + 3 < s1) {
       compute(x0, w1, s + 5, x2, s + 4, w0);
-      turn();
+      turn(yes);
     }
     if (s + 4 < s1) {
       compute(x1, w0, s + 6, x0, s + 5, w1);
-      turn();
+      turn(yes);
     }
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);            // no copy outlives the workgroup
+  __syncthreads();                               // the stages are free
+  float* xm = reinterpret_cast<float*>(x0);      // [4][kTileT]: largest partial sums
+#pragma unroll
+  for (int j = 0; j < TT; ++j) {
+    float m = most[j].value();
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    if (g == 0) xm[we * kTileT + (wt * TT + j) * 16 + r] = m;
+  }
+  __syncthreads();
+  if (tid < rows)
+    a.xmost[((int64_t)z * gridDim.y + blockIdx.y) * a.T + t0 + tid] =
+        fmaxf(fmaxf(xm[tid], xm[kTileT + tid]), fmaxf(xm[2 * kTileT + tid], xm[3 * kTileT + tid]));
   float* part = a.part + (int64_t)z * a.T * a.Ep;
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
@@ -397,6 +458,7 @@ RouterShape router_shape(int64_t T, int H, int E) {
   RouterShape s{};
   const int steps = H / kRouterStep;
   s.ep = (E + 15) / 16 * 16;
+  s.eb = 16;
   if (T <= 64 || T * E <= 32768) {
     s.wide = 0;
     s.ks = steps / (kWaves * 2);   // two steps a wave, four: 9.4, 10.1 us for both kernels at 1 x 32 x 7168
@@ -411,9 +473,11 @@ RouterShape router_shape(int64_t T, int H, int E) {
   };
   if (E <= 64) {
     s.wide = 1;
+    s.eb = 64;
     s.ks = slices((T + 63) / 64, 2 * kWaves);
     return s;
   }
+  s.eb = kTileE;
   const int64_t cols = (E + kTileE - 1) / kTileE;
   for (s.wide = 3;; s.wide = 2) {
     const int rows = s.wide == 3 ? 256 : 128;

@@ -82,10 +82,10 @@ template <int NV>
 struct RouterExperts {
   float norm[NV], bias[NV];      // |w|; bias
 };
-// One token: |x|^2, the float32 scores.
+// One token: |x|^2, the float32 scores, the largest partial sums beside them.
 template <int NV>
 struct RouterToken {
-  float xx, score[NV];
+  float xx, score[NV], most[NV];
   int active;
 };
 
@@ -113,23 +113,27 @@ __device__ __forceinline__ void router_load_token(const RouterArgs& a, int64_t t
   x.active = a.active == nullptr ? 1 : a.active[t];
   x.xx = 0.0f;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) x.score[v] = 0.0f;
+  for (int v = 0; v < NV; ++v) x.score[v] = x.most[v] = 0.0f;
+  const int Y = (a.E + a.EB - 1) / a.EB;
   for (int k0 = 0; k0 < (KC == KM ? 1 : a.KS); k0 += KC) {
-    float xx[KC], part[NV][KC];
+    float xx[KC], part[NV][KC], most[NV][KC];
 #pragma unroll
     for (int k = 0; k < KC; ++k)
       if (k == 0 || k0 + k < a.KS) {
         xx[k] = a.xnorm[(int64_t)(k0 + k) * a.T + t];
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-          part[v][k] = a.part[((int64_t)(k0 + k) * a.T + t) * a.Ep + (lane_id() + 64 * v < a.E ? lane_id() + 64 * v : 0)];
+        for (int v = 0; v < NV; ++v) {
+          const int e = lane_id() + 64 * v < a.E ? lane_id() + 64 * v : 0;
+          part[v][k] = a.part[((int64_t)(k0 + k) * a.T + t) * a.Ep + e];
+          most[v][k] = a.xmost[((int64_t)(k0 + k) * Y + e / a.EB) * a.T + t];
+        }
       }
 #pragma unroll
     for (int k = 0; k < KC; ++k)
       if (k == 0 || k0 + k < a.KS) {
         x.xx += xx[k];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) x.score[v] += part[v][k];
+        for (int v = 0; v < NV; ++v) x.score[v] += part[v][k], x.most[v] = fmaxf(x.most[v], most[v][k]);
       }
   }
 }
@@ -137,7 +141,7 @@ __device__ __forceinline__ void router_load_token(const RouterArgs& a, int64_t t
 // Lane k returns the k-th expert of token t and its weight (-1 and 0 where
 // none is left).  The largest float32 ranks are taken in turn; where one is
 // above the next by more than both may be off, their order is that of the
-// 64-bit ranks.  The others form runs of neighbours (one token in a hundred has
+// 64-bit ranks.  The others form runs of neighbours (one token in fifty has
 // one, mostly of two): the members of a run get their 64-bit ranks and are put
 // in order among themselves.  Tokens whose float32 sums left their range, and
 // runs past 64 positions, are selected again one expert at a time.
@@ -152,12 +156,9 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
   const float xx = tok.xx;
   float z[NV], err[NV];        // score argument; bound on the rank's error
   uint32_t key[NV];
-  // Every step of a score's float32 sum rounds a partial sum, and the
-  // roundings are independent: sqrt(steps) * 2^-23 * the partial sums' size,
-  // which is |z| when the products add up and at most |x| |w| (taken at an
-  // eighth: only a sum that cancels down from there comes near it).  The
-  // errors seen are two hundred times smaller.
-  const float unit = 1.1920929e-7f * __builtin_amdgcn_sqrtf((float)(a.H / 32 + a.KS + 8)), xnorm = __builtin_amdgcn_sqrtf(xx);
+  // bounds of the float32 sums (the rule stands at the scores' kernels)
+  const float steps = 3.0f * 1.1920929e-7f * __builtin_amdgcn_sqrtf((float)(a.H / 32 + a.KS + 8));
+  const float products = 3.0f * 1.1920929e-7f * __builtin_amdgcn_sqrtf(xx);
   float most = 0.0f;           // the largest bound of this lane
   bool lost = false;           // some float32 sum left its range
 #pragma unroll
@@ -165,7 +166,7 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
     z[v] = 0.0f, err[v] = 0.0f, key[v] = 0;
     if (l + 64 * v >= a.E) continue;
     const float s = tok.score[v], b = ex.bias[v], wn = ex.norm[v];
-    float d = unit * (0.125f * wn * xnorm + fabsf(s)) + 1e-36f, rank;
+    float d = products * wn + steps * tok.most[v] + 1e-36f, rank;
     if (sig) {
       z[v] = s;
       rank = s;

@@ -121,6 +121,24 @@ def test_router_near_ties_in_sparse_tokens(T, E4):
         check_router(x, w, None, 9, "softmax")
 
 
+@pytest.mark.parametrize("T,H,E,K", [(5, 7168, 32, 8), (200, 7168, 32, 8), (1500, 2048, 48, 8), (2000, 7168, 128, 8),
+                                     (10001, 6144, 129, 8), (600, 16384, 256, 8), (70, 512, 600, 4)])
+@pytest.mark.parametrize("where", ["ends", "half", "beside", "pairs"])
+def test_router_outliers_that_cancel(T, H, E, K, where):
+    """Two large products that cancel: the float32 sum passes through partial sums 2^13 above the scores and loses
+    their low bits, so the order of close experts is in doubt far beyond what the scores themselves say."""
+    log(f"[router cancel] T={T} H={H} E={E} {where}")
+    x, w, _ = router_case(T, H, E, K, "sigmoid", False, 90 + T)
+    n = 1 if where != "pairs" else H // 64
+    first = torch.arange(n) * 32 + 5
+    second = {"ends": torch.tensor([H - 1]), "half": torch.tensor([H // 2]), "beside": torch.tensor([7]),
+              "pairs": H - 1 - first}[where]
+    big = 1024.0 / n ** 0.5
+    x[:, first], x[:, second] = big, -big
+    w[:, first] = w[:, second] = 8.0 / n ** 0.5
+    check_router(x, w, None, K, "sigmoid", renormalize=False)
+
+
 @pytest.mark.parametrize("T,E", [(9, 40), (100, 130), (300, 300)])
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_router_equal_scores(T, E, scoring):
