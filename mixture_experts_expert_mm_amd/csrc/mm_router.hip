@@ -206,7 +206,8 @@ constexpr int kTileE = 256;
 // L2, one stage ahead in two; tokens one stage ahead: 70 for 67 us).
 // Bound: the copies, of which a CU takes 36 to 40 bytes a ns: 2.8 MB a CU with
 // TT = 4 at 16384 x 256 x 7168, 1.9 MB with 8 (92 / 67 us; the first stage and the
-// writes of 67 MB of partial scores come on top).
+// writes of 67 MB of partial scores come on top).  Looking for the largest
+// partial sum costs 5 of 72 us at every third stage, 12 of 79 at each.
 template <int TT>
 __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, uint8_t* w0, uint8_t* x1, uint8_t* w1,
                                             uint8_t* x2, uint8_t* w2) {
@@ -420,9 +421,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 }
 
 // One wave per token.  (Four tokens a wave in turn, the next one's scores
-// asked for meanwhile, took 58 against 42 us at 16384 x 256: a token that needs
+// asked for meanwhile, took 58 against 43 us at 16384 x 256: a token that needs
 // 64-bit sums then holds up three others.)  Bound: issue, about 500
-// instructions a token, and the latency of the scores: 43 us at 16384 x 256
+// instructions a token, and the latency of the scores: 48 us at 16384 x 256
 // (27 without the turns that select, 29 without the 64-bit sums).
 template <int NV, int KM>
 __global__ __launch_bounds__(256, NV <= 4 ? 4 : 1) void k_router_select(RouterArgs a) {
