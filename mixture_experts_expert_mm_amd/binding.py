@@ -22,6 +22,7 @@ KERNEL_IDS = 16
 MM_ROUTER_SOFTMAX, MM_ROUTER_SIGMOID = 0, 1
 SCORING = {"softmax": MM_ROUTER_SOFTMAX, "sigmoid": MM_ROUTER_SIGMOID}
 MM_FEW_BF16, MM_FEW_FP8, MM_FEW_FP8_BLOCK = 0, 1, 2
+OUT_DTYPE = {"bf16": MM_OUT_BF16, "f32": MM_OUT_F32, "fp32": MM_OUT_F32}
 FEW_FORMAT = {"bf16": MM_FEW_BF16, "fp8": MM_FEW_FP8, "fp8_block": MM_FEW_FP8_BLOCK}
 MM_DEVERR_BAD_EXPERT, MM_DEVERR_BARRIER_TIMEOUT, MM_DEVERR_BAD_OFFSETS = 1, 2, 4
 
@@ -294,7 +295,7 @@ def mm_router(plan, x, weight, bias, x_active_mask, topk_ids, topk_weights, work
 def mm_few_plan_create(T, H, I, E, K, weight_format="bf16", y_dtype="bf16", activation_clamp=None,
                        num_shared_experts=0) -> MMFewPlan:
     fmt = FEW_FORMAT[weight_format] if isinstance(weight_format, str) else weight_format
-    yd = (MM_OUT_F32 if y_dtype in ("f32", "fp32") else MM_OUT_BF16) if isinstance(y_dtype, str) else y_dtype
+    yd = OUT_DTYPE.get(y_dtype, -1) if isinstance(y_dtype, str) else y_dtype      # -1: refused by the plan
     prob = MMFewProblem(T, H, I, E, K, fmt, yd, 0 if activation_clamp is None else 1,
                         0.0 if activation_clamp is None else activation_clamp, num_shared_experts, 0)
     plan = MMFewPlan()

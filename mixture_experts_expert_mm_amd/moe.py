@@ -23,6 +23,11 @@ _DT = {"bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn, "int8": torch.int8, "
 MX = ("mxfp8", "mxfp4")
 
 
+def _y_dtype(plan):
+    """The type in which the plan's kernels write y, however the caller spelled it."""
+    return torch.float32 if plan.prob.y_dtype == B.MM_OUT_F32 else torch.bfloat16
+
+
 @dataclasses.dataclass
 class Intermediates:
     expert_counts: torch.Tensor
@@ -107,8 +112,7 @@ class ExpertLayer:
         return torch.empty(nbytes // 4, dtype=torch.float32, device=self.device)
 
     def new_y(self):
-        dt = torch.float32 if self.y_dtype in ("f32", "fp32") else torch.bfloat16
-        return torch.empty((self.T, self.H), dtype=dt, device=self.device)
+        return torch.empty((self.T, self.H), dtype=_y_dtype(self.plan), device=self.device)
 
     # -------------------------------------------------------------- entries
     def forward(self, x, topk_ids, topk_weights, y=None, counts=None, stream=None, active=None):
@@ -161,8 +165,8 @@ class ExpertLayer:
             raise ValueError(f"forward_few takes bf16 or fp8 weights, not {self.usecase}")
         clamp = self.plan.prob.activation_clamp if self.plan.prob.clamp_activation else None
         return moe_few(x, self.w1, self.w2, self.s1, self.s2, topk_ids=topk_ids, topk_weights=topk_weights,
-                       num_shared_experts=self.S, activation_clamp=clamp, y_dtype=self.y_dtype, active=active, y=y,
-                       stream=stream)[0]
+                       num_shared_experts=self.S, activation_clamp=clamp, y_dtype=self.plan.prob.y_dtype,
+                       active=active, y=y, stream=stream)[0]
 
 
 # ------------------------------------------------- operators without a layer
@@ -172,7 +176,6 @@ _few_plan = functools.lru_cache(maxsize=256)(B.mm_few_plan_create)
 _block_plan = functools.lru_cache(maxsize=256)(B.mm_block_plan_create)
 
 FEW_MAX_TOKENS = 64
-_F32 = ("f32", "fp32")
 
 
 def _need(name, t, dtype, shape, device):
@@ -253,7 +256,7 @@ def moe_few(x, w1, w2, s1=None, s2=None, *, topk_ids=None, topk_weights=None, ro
 
     x: bf16 [T,H].  w1 [E+S,2I,H] and w2 [E+S,H,I] are prepared weights (``ExpertLayer.w1``, ``.w2``), bf16, or
     e4m3 with float32 scales in formula order: per output channel (s1 [E+S,2I], s2 [E+S,H]) or per block of 128 x 128
-    (s1 [E+S,2I/128,H/128], s2 [E+S,H/128,I/128]).  Routes: topk_ids and topk_weights, or router_weight (with
+    (s1 [E+S,2I/128,H/128], s2 [E+S,H/128,I/128]).  y_dtype: "bf16" or "f32".  Routes: topk_ids and topk_weights, or router_weight (with
     router_bias, topk, scoring, renormalize and route_scale as in ``route``).  A shared expert is the last of w1, w2."""
     T, H, dev = _rows("x", x)
     if T > FEW_MAX_TOKENS:
@@ -294,7 +297,7 @@ def moe_few(x, w1, w2, s1=None, s2=None, *, topk_ids=None, topk_weights=None, ro
         _need("topk_ids", topk_ids, torch.int32, (T, K), dev)
         _need("topk_weights", topk_weights, torch.float32, (T, K), dev)
     plan = _few_plan(max(T, 1), H, I, E, K, fmt, y_dtype, activation_clamp, S)
-    ydt = torch.float32 if y_dtype in _F32 else torch.bfloat16
+    ydt = _y_dtype(plan)
     if y is not None:
         _need("y", y, ydt, (T, H), dev)
     with _stream_of(dev, stream):

@@ -1,0 +1,57 @@
+"""How the operators' functions read their arguments, without a GPU: the checks, buffers and plans are the real
+ones, the launches are recorded."""
+
+from __future__ import annotations
+
+import contextlib
+
+import pytest
+import torch
+
+from mixture_experts_expert_mm_amd import binding as B
+from mixture_experts_expert_mm_amd import moe
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """Host tensors pass as device ones; the calls that would launch are listed as (name, arguments)."""
+    seen = []
+    monkeypatch.setattr(moe, "_rows", lambda name, x: (*x.shape, x.device))
+    monkeypatch.setattr(moe, "_stream_of", lambda device, stream: contextlib.nullcontext())
+    monkeypatch.setattr(moe, "_raw_stream", lambda device: 0)
+    for name in ("mm_router", "mm_moe_few", "mm_block_quantize", "mm_block_gemm", "mm_block_linear"):
+        monkeypatch.setattr(B, name, lambda *a, name=name: seen.append((name, a)))
+    return seen
+
+
+def few_args(T=3, H=256, I=128, E=4, K=2):
+    x = torch.zeros(T, H, dtype=BF16)
+    w1, w2 = torch.zeros(E, 2 * I, H, dtype=BF16), torch.zeros(E, H, I, dtype=BF16)
+    return (x, w1, w2), dict(topk_ids=torch.zeros(T, K, dtype=torch.int32), topk_weights=torch.zeros(T, K))
+
+
+@pytest.mark.parametrize("y_dtype,want", [("bf16", BF16), ("f32", F32), ("fp32", F32), (B.MM_OUT_F32, F32),
+                                          (B.MM_OUT_BF16, BF16)])
+def test_y_has_the_type_that_the_plan_writes(launches, y_dtype, want):
+    args, routes = few_args()
+    y, _, _ = moe.moe_few(*args, y_dtype=y_dtype, **routes)
+    plan, out = launches[-1][1][0], launches[-1][1][9]
+    assert out is y and y.dtype == want
+    assert plan.prob.y_dtype == (B.MM_OUT_F32 if want == F32 else B.MM_OUT_BF16)
+    other = torch.zeros(3, 256, dtype=BF16 if want == F32 else F32)
+    with pytest.raises(ValueError, match="y:"):
+        moe.moe_few(*args, y_dtype=y_dtype, y=other, **routes)
+    layer = moe.ExpertLayer(3, 256, 128, 4, 2, "bf16", y_dtype, device="cpu")
+    assert layer.new_y().dtype == want
+    layer.w1, layer.w2 = args[1:]
+    assert layer.forward_few(args[0], **routes).dtype == want
+
+
+@pytest.mark.parametrize("y_dtype", ["float32", "bfloat16", "", 2, -1])
+def test_unknown_y_types_are_refused(launches, y_dtype):
+    args, routes = few_args()
+    with pytest.raises(B.MMError):
+        moe.moe_few(*args, y_dtype=y_dtype, **routes)
+    assert not launches
