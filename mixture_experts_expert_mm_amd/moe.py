@@ -204,7 +204,9 @@ def _stream_of(device, stream):
     if stream is not None:
         if getattr(stream, "device", device) != device:
             raise ValueError(f"stream: one of {device} is needed, got one of {stream.device}")
-        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+        if isinstance(stream, int):        # a raw handle; ExternalStream takes 0 for none given
+            stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+        return torch.cuda.stream(stream)
     if device.index != torch.cuda.current_device():
         return torch.cuda.device(device)
     return _HERE
