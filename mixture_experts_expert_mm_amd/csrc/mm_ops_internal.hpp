@@ -24,6 +24,8 @@ struct RouterArgs {
   int H, E, K, Ep, KS, EB;
   int scoring, renormalize;
   float scale;
+  // error of a float32 score in units of 2^-24: of its largest partial sums, of |x| |w| (launch_router_select)
+  float of_sums, of_products;
 };
 struct RouterShape {
   int wide;                  // 0: 16 x 16 a wave; 1: 64 tokens x 64 experts a wave; 2: tiles of 128 x 256 through LDS; 3: of 256 x 256

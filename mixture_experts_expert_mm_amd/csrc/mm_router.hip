@@ -8,15 +8,20 @@
 // cut into KS slices so that a single token still occupies many CUs), and
 // k_router_select adds them and selects, one wave per token.
 //
-// The order of two experts is decided by their 64-bit scores.  The float32 sum
-// of a score is off by the roundings of its steps: within an MFMA by some
-// 2^-23 of its products (at most |x| |w|), between them by an ulp of the partial
-// sum, independently.  A sum of two values that cancel passes through partial
-// sums far above the score, so the kernels keep the largest one of a token and
-// tile of experts, and the selection carries 2^-23 * (3 |x| |w| + 3 sqrt(steps) *
-// largest) per expert (two outliers that cancel: errors of a third of it; random
-// data: a twentieth).  Where two experts are closer than their bounds, both are
-// summed again in 64 bits: one token in fifty of random data, for two experts.
+// The order of two experts is decided by their 64-bit scores, and a float32
+// score carries a bound on its error.  The MFMA takes 8 products at a time: it
+// cuts each below 2^-24 of the power of two of the largest one (7 * 2^-24 of that
+// one at most) and adds the eight to the accumulator with one rounding, of at
+// most 2^-24 of the sum that results.  The roundings need not be independent:
+// where a large partial sum takes in small products of one sign, all go the same
+// way (a value of 1, then eights just below half of its ulp: 446 steps of 2^-23
+// are lost at hidden 7168).  So they are added up.  With m_z the largest partial
+// sum of a token and tile of experts that the kernels saw in slice z: 4 roundings
+// an MFMA of the m_z, and those of the sums over waves and slices.  A partial
+// sum between two looks is off the nearer one by at most half of the products
+// between them: 4 * (MFMAs between looks) / 2 of |x| |w|, beside the 7 of the
+// cut products (launch_router_select).  Where two experts are closer than
+// their bounds, both are summed again in 64 bits.
 #include <type_traits>
 
 #include "mm_router_dev.hpp"
@@ -276,8 +281,7 @@ __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, ui
       }
     }
   };
-  // `look`: every third stage.  What comes and goes between two looks is of the
-  // size of its products, for six steps at most; the bound's products cover it.
+  // `look`: every third stage, six MFMAs
   const std::true_type yes;
   const std::false_type no;
   auto turn = [&](auto look) {
@@ -520,7 +524,18 @@ hipError_t run_select(const RouterArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_router_select(const RouterArgs& a, hipStream_t s) {
+hipError_t launch_router_select(const RouterArgs& args, hipStream_t s) {
+  RouterArgs a = args;
+  const int steps = a.H / kRouterStep;           // of two MFMAs
+  if (a.EB == kTileE) {
+    // a slice is one chain; the slices are added one after the other
+    a.of_sums = (float)(8 * ((steps + a.KS - 1) / a.KS) + a.KS - 1);
+    a.of_products = 8 + 2 * 6;                   // a look every six MFMAs
+  } else {
+    // a slice is eight chains, added in pairs (4 sums of 2 m, 2 of 4 m, one of 8 m)
+    a.of_sums = (float)(8 * kWaves * ((steps + kWaves * a.KS - 1) / (kWaves * a.KS)) + 24 + kWaves * (a.KS - 1));
+    a.of_products = 8 + 2 * 2;                   // a look every two
+  }
   if (a.E <= 64) return run_select<1>(a, s);
   if (a.E <= 128) return run_select<2>(a, s);
   if (a.E <= 256) return run_select<4>(a, s);

@@ -85,7 +85,7 @@ struct RouterExperts {
 // One token: |x|^2, the float32 scores, the largest partial sums beside them.
 template <int NV>
 struct RouterToken {
-  float xx, score[NV], most[NV];
+  float xx, score[NV], most[NV];   // most: summed over the slices
   int active;
 };
 
@@ -103,7 +103,7 @@ __device__ __forceinline__ void router_load_experts(const RouterArgs& a, RouterE
 #pragma unroll
     for (int k = 1; k < KM; ++k)
       if (k < a.KS) s += p[k];
-    x.norm[v] = __builtin_amdgcn_sqrtf(s);
+    x.norm[v] = __builtin_amdgcn_sqrtf(s + 2e-34f);
   }
 }
 
@@ -133,7 +133,7 @@ __device__ __forceinline__ void router_load_token(const RouterArgs& a, int64_t t
       if (k == 0 || k0 + k < a.KS) {
         x.xx += xx[k];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) x.score[v] += part[v][k], x.most[v] = fmaxf(x.most[v], most[v][k]);
+        for (int v = 0; v < NV; ++v) x.score[v] += part[v][k], x.most[v] += most[v][k];
       }
   }
 }
@@ -141,9 +141,9 @@ __device__ __forceinline__ void router_load_token(const RouterArgs& a, int64_t t
 // Lane k returns the k-th expert of token t and its weight (-1 and 0 where
 // none is left).  The largest float32 ranks are taken in turn; where one is
 // above the next by more than both may be off, their order is that of the
-// 64-bit ranks.  The others form runs of neighbours (one token in fifty has
-// one, mostly of two): the members of a run get their 64-bit ranks and are put
-// in order among themselves.  Tokens whose float32 sums left their range, and
+// 64-bit ranks.  The others form runs of neighbours (one token of random data
+// in 20 has one with 128 experts or more, one in 80 with 32; mostly of two): the
+// members of a run get their 64-bit ranks and are put in order among themselves.  Tokens whose float32 sums left their range, and
 // runs past 64 positions, are selected again one expert at a time.
 template <int NV>
 __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t t, const RouterExperts<NV>& ex,
@@ -156,9 +156,11 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
   const float xx = tok.xx;
   float z[NV], err[NV];        // score argument; bound on the rank's error
   uint32_t key[NV];
-  // bounds of the float32 sums (the rule stands at the scores' kernels)
-  const float steps = 3.0f * 1.1920929e-7f * __builtin_amdgcn_sqrtf((float)(a.H / 32 + a.KS + 8));
-  const float products = 3.0f * 1.1920929e-7f * __builtin_amdgcn_sqrtf(xx);
+  // bounds of the float32 sums (the rule stands at the scores' kernels), with a
+  // hundredth for the norms' own roundings; squares below float32's range leave
+  // at most 16384 * 2^-126 = 2e-34 out of a norm
+  const float sums = 1.01f * 5.9604645e-8f * a.of_sums;
+  const float products = 1.01f * 5.9604645e-8f * a.of_products * __builtin_amdgcn_sqrtf(xx + 2e-34f);
   float most = 0.0f;           // the largest bound of this lane
   bool lost = false;           // some float32 sum left its range
 #pragma unroll
@@ -166,7 +168,7 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
     z[v] = 0.0f, err[v] = 0.0f, key[v] = 0;
     if (l + 64 * v >= a.E) continue;
     const float s = tok.score[v], b = ex.bias[v], wn = ex.norm[v];
-    float d = products * wn + steps * tok.most[v] + 1e-36f, rank;
+    float d = products * wn + sums * tok.most[v] + 1e-36f, rank;
     if (sig) {
       z[v] = s;
       rank = s;

@@ -1,0 +1,51 @@
+"""The router's order where float32 sums go wrong in one direction."""
+
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from gpu_helpers import log
+from mixture_experts_expert_mm_amd import moe
+
+pytestmark = pytest.mark.gpu
+
+BF16, F64 = torch.bfloat16, torch.float64
+
+
+def drift_case(H, E, per):
+    """(x [255, H], w [E, H]): past channel 31 every `per` products add up to just below half an ulp of the running
+    sum, which stays near 1, with one sign for expert 6 and the other for expert 4; a float32 sum that rounds as often
+    loses them all.  The token's channel 1 raises expert 4 by 1/255 to 255/255 of a little more than what is lost.
+    The others' scores are 0."""
+    x = torch.zeros(255, H)
+    x[:, 0] = 1.0
+    x[:, 1] = torch.arange(1, 256) * 2.0 ** -10
+    x[:, 32:] = 2.0 ** -12
+    small = float(torch.tensor(0.99).to(BF16)) / per * 2.0 ** -12
+    step = math.ceil((H - 32) / per / 250)             # of 2^-23: the two lose (H - 32) / per in all
+    w = torch.zeros(E, H)
+    w[6, 0] = w[4, 0] = 1.0
+    w[4, 1] = step * 2.0 ** -13
+    w[6, 32:], w[4, 32:] = small, -small
+    return x.to(BF16), w.to(BF16)
+
+
+@pytest.mark.parametrize("H", [1024, 7168, 16384])
+@pytest.mark.parametrize("T,E", [(1, 8), (255, 40), (3000, 40), (2000, 128), (16384, 256), (20000, 66), (33000, 66), (9000, 600)])
+@pytest.mark.parametrize("per", [8, 32])
+def test_router_order_of_sums_that_drift(T, E, H, per):
+    """One slice of the hidden dimension or several, small and large tiles: the same order as in 64 bits."""
+    log(f"[router drift] T={T} H={H} E={E} {per}")
+    x, w = drift_case(H, E, per)
+    z = x.to(F64) @ w.to(F64).t()
+    want = z.sort(dim=1, descending=True, stable=True)[1][:, :2].to(torch.int32)
+    assert 0 < int((want[:, 0] == 6).sum()) < 255
+    at = torch.arange(T) * 97 % 255
+    if T == 1:
+        at = (want[:, 0] == 6).nonzero()[-1]           # the closest one
+    xd = x.cuda()[at.cuda()].contiguous()
+    ids, _ = moe.route(xd, w.cuda(), topk=2)
+    assert torch.equal(ids.cpu(), want[at]), (ids.cpu() != want[at]).any(1).sum()
