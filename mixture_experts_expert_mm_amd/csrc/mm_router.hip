@@ -20,8 +20,10 @@
 // an MFMA of the m_z, and those of the sums over waves and slices.  A partial
 // sum between two looks is off the nearer one by at most half of the products
 // between them: 4 * (MFMAs between looks) / 2 of |x| |w|, beside the 7 of the
-// cut products (launch_router_select).  Where two experts are closer than
-// their bounds, both are summed again in 64 bits.
+// cut products (launch_router_select).  No partial sum is above |x| |w|, which
+// takes the place of the m_z where a NaN or an infinity of another expert of the
+// tile hides them.  Where two experts are closer than their bounds, both are
+// summed again in 64 bits.
 #include <type_traits>
 
 #include "mm_router_dev.hpp"
@@ -49,6 +51,13 @@ __device__ __forceinline__ float sumsq(const u32x4& v, float acc) {
   return acc;
 }
 
+// The larger of two magnitudes by their bits, among which a NaN is the largest:
+// the selection has to learn that it hides the others (fmaxf would drop it).
+__device__ __forceinline__ float larger(float a, float b) {
+  const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  return x > y ? a : b;
+}
+
 // The largest magnitude of many floats from their bits: the largest positive
 // one in signed order, the largest negative one in unsigned order, half an
 // instruction a value each.
@@ -64,7 +73,7 @@ struct Largest {
       neg = (uint32_t)b > neg ? (uint32_t)b : neg;
     }
   }
-  __device__ __forceinline__ float value() const { return fmaxf(__uint_as_float((uint32_t)pos), __uint_as_float(neg & 0x7fffffffu)); }
+  __device__ __forceinline__ float value() const { return larger(__uint_as_float((uint32_t)pos), __uint_as_float(neg & 0x7fffffffu)); }
 };
 
 }  // namespace
@@ -145,8 +154,8 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
     float v = xs[i], m = most[i].value();
     v += __shfl_xor(v, 16, 64);
     v += __shfl_xor(v, 32, 64);
-    m = fmaxf(m, __shfl_xor(m, 16, 64));
-    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    m = larger(m, __shfl_xor(m, 16, 64));
+    m = larger(m, __shfl_xor(m, 32, 64));
     if (g == 0) xn[kw][16 * i + r] = v, xm[kw][16 * i + r] = m;
   }
 #pragma unroll
@@ -188,7 +197,7 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
   if ((int)threadIdx.x < 16 * TT && t0 + threadIdx.x < a.T) {
     float v = 0.0f, m = 0.0f;
 #pragma unroll
-    for (int k = 0; k < KW; ++k) v += xn[k][threadIdx.x], m = fmaxf(m, xm[k][threadIdx.x]);
+    for (int k = 0; k < KW; ++k) v += xn[k][threadIdx.x], m = larger(m, xm[k][threadIdx.x]);
     if (blockIdx.y == 0) a.xnorm[(int64_t)blockIdx.z * a.T + t0 + threadIdx.x] = v;
     a.xmost[((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * a.T + t0 + threadIdx.x] = m;
   }
@@ -372,14 +381,14 @@ __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, ui
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
     float m = most[j].value();
-    m = fmaxf(m, __shfl_xor(m, 16, 64));
-    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    m = larger(m, __shfl_xor(m, 16, 64));
+    m = larger(m, __shfl_xor(m, 32, 64));
     if (g == 0) xm[we * kTileT + (wt * TT + j) * 16 + r] = m;
   }
   __syncthreads();
   if (tid < rows)
     a.xmost[((int64_t)z * gridDim.y + blockIdx.y) * a.T + t0 + tid] =
-        fmaxf(fmaxf(xm[tid], xm[kTileT + tid]), fmaxf(xm[2 * kTileT + tid], xm[3 * kTileT + tid]));
+        larger(larger(xm[tid], xm[kTileT + tid]), larger(xm[2 * kTileT + tid], xm[3 * kTileT + tid]));
   float* part = a.part + (int64_t)z * a.T * a.Ep;
 #pragma unroll
   for (int j = 0; j < TT; ++j) {

@@ -160,7 +160,7 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
   // hundredth for the norms' own roundings; squares below float32's range leave
   // at most 16384 * 2^-126 = 2e-34 out of a norm
   const float sums = 1.01f * 5.9604645e-8f * a.of_sums;
-  const float products = 1.01f * 5.9604645e-8f * a.of_products * __builtin_amdgcn_sqrtf(xx + 2e-34f);
+  const float products = 1.01f * 5.9604645e-8f * a.of_products, xn = __builtin_amdgcn_sqrtf(xx + 2e-34f);
   float most = 0.0f;           // the largest bound of this lane
   bool lost = false;           // some float32 sum left its range
 #pragma unroll
@@ -168,7 +168,8 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
     z[v] = 0.0f, err[v] = 0.0f, key[v] = 0;
     if (l + 64 * v >= a.E) continue;
     const float s = tok.score[v], b = ex.bias[v], wn = ex.norm[v];
-    float d = products * wn + sums * tok.most[v] + 1e-36f, rank;
+    const float norms = xn * wn;
+    float d = products * norms + sums * fminf(tok.most[v], norms) + 1e-36f, rank;    // (a NaN is the larger one)
     if (sig) {
       z[v] = s;
       rank = s;

@@ -1,4 +1,4 @@
-"""The router's order where float32 sums go wrong in one direction."""
+"""The router's order where float32 sums go wrong in one direction, and beside a NaN."""
 
 from __future__ import annotations
 
@@ -7,6 +7,7 @@ import math
 import pytest
 import torch
 
+import ops_reference as ref
 from gpu_helpers import log
 from mixture_experts_expert_mm_amd import moe
 
@@ -49,3 +50,47 @@ def test_router_order_of_sums_that_drift(T, E, H, per):
     xd = x.cuda()[at.cuda()].contiguous()
     ids, _ = moe.route(xd, w.cuda(), topk=2)
     assert torch.equal(ids.cpu(), want[at]), (ids.cpu() != want[at]).any(1).sum()
+
+
+@pytest.mark.parametrize("T,E", [(200, 40), (3000, 40), (2000, 128), (33000, 66), (9000, 600)])
+@pytest.mark.parametrize("sums", [1.0, -1.0])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_router_order_of_sums_that_drift_beside_a_nan(T, E, sums, sign):
+    """The same with sums of either sign, and a NaN in the weights of the expert between the two, which says nothing
+    of them (every other expert is switched off)."""
+    log(f"[router drift nan] T={T} E={E} {sums} {sign}")
+    x, w = drift_case(7168, E, 8)
+    w *= sums
+    z = x.to(F64) @ w[[4, 6]].to(F64).t()
+    want = torch.where(z[:, 1] > z[:, 0], 6, 4).to(torch.int32)
+    w[5, 3], w[5, 6000] = math.copysign(math.nan, sign), math.copysign(math.nan, sign)
+    bias = torch.full((E,), -math.inf)
+    bias[[4, 6]] = 0.0
+    at = torch.arange(T) * 97 % 255
+    ids, _ = moe.route(x.cuda()[at.cuda()].contiguous(), w.cuda(), bias.cuda(), topk=2, scoring="sigmoid")
+    assert torch.equal(ids[:, 0].cpu(), want[at]), (ids[:, 0].cpu() != want[at]).sum()
+
+
+def cancel_case(T, H, E, seed):
+    """Two products of 2^13 that cancel, at both ends of a row: the scores lose their low bits in float32."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, H, generator=g).to(BF16)
+    w = (torch.randn(E, H, generator=g) * H ** -0.5).to(BF16)
+    x[:, 5], x[:, H - 1] = 1024.0, -1024.0
+    w[:, 5] = w[:, H - 1] = 8.0
+    return x, w
+
+
+SIZES = [(5, 7168, 32, 8), (200, 7168, 32, 8), (1500, 2048, 48, 8), (2000, 7168, 128, 8), (600, 16384, 256, 8), (70, 512, 600, 4)]
+
+
+@pytest.mark.parametrize("T,H,E,K", SIZES)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_router_order_beside_a_nan(T, H, E, K, sign):
+    """A NaN in one expert's weights leaves the order of the others as the 64-bit scores have it."""
+    log(f"[router nan] T={T} H={H} E={E}")
+    x, w = cancel_case(T, H, E, 90 + T)
+    w[E // 2, 40] = math.copysign(math.nan, sign)
+    ids, _ = moe.route(x.cuda(), w.cuda(), topk=K, scoring="sigmoid", renormalize=False)
+    want, _, _ = ref.route(x, w, None, K, "sigmoid", False)
+    assert torch.equal(ids.cpu(), want), (ids.cpu() != want).any(1).sum()
