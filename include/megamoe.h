@@ -406,13 +406,15 @@ mm_status mm_read_kernel_clock(const mm_plan* plan, const void* workspace, uint6
  *     weight = score of the selected experts; with renormalize = 1 divided by
  *     (their sum + 1e-20); then times route_scale
  * The K experts of a token come in descending rank, ties to the lower id.
- * Products and weights are float32; where float32 sums leave the order of
- * two experts in doubt, it is decided by their sums in 64 bits.  A rank of
- * -inf (a bias of -inf switches an expert off) is never selected: a slot
- * with no expert left gets id -1 and weight 0, as does every slot of a token
- * whose x_active_mask entry is 0.  A NaN ranks below every number and above
- * -inf; its weight is NaN.  Results do not depend on the other tokens'
- * values.
+ * Sums and weights are float32; where float32 sums leave the order of two
+ * experts in doubt, order and weights come from their sums in 64 bits, so
+ * weights fall wherever score and rank are of one order (to float32 rounding).
+ * A rank of -inf (a bias of -inf switches an expert off) is never selected: a
+ * slot with no expert left gets id -1 and weight 0, as does every slot of a
+ * token whose x_active_mask entry is 0.  A NaN rank is below every number and
+ * above -inf; the weight follows the formula (a NaN score makes its weight NaN,
+ * under softmax every weight of the token).  Results do not depend on the
+ * other tokens' values.
  */
 typedef enum mm_router_scoring { MM_ROUTER_SOFTMAX = 0, MM_ROUTER_SIGMOID = 1 } mm_router_scoring;
 

@@ -287,8 +287,16 @@ __device__ __forceinline__ void router_select_token(const RouterArgs& a, int64_t
       const int p1 = todo != 0 ? __ffsll((unsigned long long)todo) - 1 : p0;
       todo &= todo - 1;
       double d0, d1;
-      router_dot64(a, t, __builtin_amdgcn_readlane(id, p0), __builtin_amdgcn_readlane(id, p1), d0, d1);
+      const int e0 = __builtin_amdgcn_readlane(id, p0), e1 = __builtin_amdgcn_readlane(id, p1);
+      router_dot64(a, t, e0, e1, d0, d1);
       if (l == p0 || l == p1) mine = rank_of(l == p0 ? d0 : d1, id);
+      // the weights from the same sums: they fall in the order that these decide
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const double b = sig ? 0.0 : (double)ex.bias[v];
+        if (l + 64 * v == e0) z[v] = (float)(d0 + b);
+        if (l + 64 * v == e1) z[v] = (float)(d1 + b);
+      }
     }
     // each moves within its run by those that it was wrongly before or behind
     const int run = __popcll((unsigned long long)(~chained & ((2ull << l) - 1)));

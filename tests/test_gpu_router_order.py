@@ -1,4 +1,4 @@
-"""The router's order where float32 sums go wrong in one direction, and beside a NaN."""
+"""The router's order and weights where float32 sums go wrong in one direction, beside a NaN, and in runs."""
 
 from __future__ import annotations
 
@@ -94,3 +94,15 @@ def test_router_order_beside_a_nan(T, H, E, K, sign):
     ids, _ = moe.route(x.cuda(), w.cuda(), topk=K, scoring="sigmoid", renormalize=False)
     want, _, _ = ref.route(x, w, None, K, "sigmoid", False)
     assert torch.equal(ids.cpu(), want), (ids.cpu() != want).any(1).sum()
+
+
+@pytest.mark.parametrize("T,H,E,K", SIZES)
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_router_weights_do_not_rise(T, H, E, K, scoring):
+    """Experts that only their 64-bit sums tell apart get their weights from the same sums.  A weight is rounded by
+    an exponential (2 ulp), a sum and a quotient: two of them are off by 8 * 2^-23 of the value together."""
+    log(f"[router weights] T={T} H={H} E={E} {scoring}")
+    x, w = cancel_case(T, H, E, 190 + T)
+    ids, wts = moe.route(x.cuda(), w.cuda(), topk=K, scoring=scoring, renormalize=False)
+    assert torch.equal(ids.cpu(), ref.route(x, w, None, K, scoring, False)[0])
+    assert bool((wts[:, 1:] <= wts[:, :-1] * (1 + 8 * 2.0 ** -23)).all())
