@@ -15,6 +15,7 @@ import dataclasses
 import functools
 
 import torch
+import torch.autograd.forward_ad as forward_ad
 
 from . import binding as B
 
@@ -187,6 +188,8 @@ def _need(name, t, dtype, shape, device):
                          f"{list(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name}: requires a gradient, which this operator does not compute (call it under no_grad)")
+    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{name}: carries a tangent, which this operator does not compute")
 
 
 def _rows(name, x):

@@ -55,3 +55,23 @@ def test_unknown_y_types_are_refused(launches, y_dtype):
     with pytest.raises(B.MMError):
         moe.moe_few(*args, y_dtype=y_dtype, **routes)
     assert not launches
+
+
+@pytest.mark.parametrize("name", ["x", "w1", "topk_weights"])
+def test_tangents_are_refused(launches, name):
+    """The tangent of forward mode would be dropped in silence, as a gradient would."""
+    import torch.autograd.forward_ad as fw
+
+    (x, w1, w2), routes = few_args()
+    args = dict(x=x, w1=w1, w2=w2, **routes)
+    with fw.dual_level():
+        moe.moe_few(**args)                                  # none carries one
+        n = len(launches)
+        args[name] = fw.make_dual(args[name], torch.ones_like(args[name]))
+        with pytest.raises(ValueError, match=f"{name}: .*tangent"):
+            moe.moe_few(**args)
+        assert len(launches) == n
+        q = torch.zeros(2, 128, dtype=BF16)
+        moe.block_quantize(q)
+        with pytest.raises(ValueError, match="x: .*tangent"):
+            moe.block_quantize(fw.make_dual(q, torch.ones_like(q)))
