@@ -13,6 +13,7 @@ from __future__ import annotations
 import contextlib
 import dataclasses
 import functools
+import operator
 
 import torch
 import torch.autograd.forward_ad as forward_ad
@@ -192,6 +193,13 @@ def _need(name, t, dtype, shape, device):
         raise ValueError(f"{name}: carries a tangent, which this operator does not compute")
 
 
+def _whole(name, n):
+    try:
+        return operator.index(int(n) if isinstance(n, float) and n.is_integer() else n)
+    except TypeError:
+        raise ValueError(f"{name}: a whole number is needed, got {n!r}") from None
+
+
 def _rows(name, x):
     """(rows, columns, device) of a bf16 or e4m3 matrix on a GPU."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
@@ -245,10 +253,11 @@ def route(x, weight, bias=None, *, topk, scoring="softmax", renormalize=True, sc
         _need("active", active, torch.int8, (T,), dev)
     if scoring not in B.SCORING:
         raise ValueError(f"scoring: one of {sorted(B.SCORING)}, got {scoring!r}")
-    plan = _router_plan(max(T, 1), H, E, int(topk), scoring, bool(renormalize), float(scale))
+    K = _whole("topk", topk)
+    plan = _router_plan(max(T, 1), H, E, K, scoring, bool(renormalize), float(scale))
     with _stream_of(dev, stream):
-        ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
-        wts = torch.empty((T, topk), dtype=torch.float32, device=dev)
+        ids = torch.empty((T, K), dtype=torch.int32, device=dev)
+        wts = torch.empty((T, K), dtype=torch.float32, device=dev)
         if T:
             B.mm_router(plan, x, weight, bias, active, ids, wts, _workspace(plan.workspace_bytes, dev), _raw_stream(dev))
     return ids, wts
@@ -266,7 +275,7 @@ def moe_few(x, w1, w2, s1=None, s2=None, *, topk_ids=None, topk_weights=None, ro
     T, H, dev = _rows("x", x)
     if T > FEW_MAX_TOKENS:
         raise ValueError(f"x: at most {FEW_MAX_TOKENS} tokens, got {T} (ExpertLayer.forward takes more)")
-    S = int(num_shared_experts)
+    S = _whole("num_shared_experts", num_shared_experts)
     if not isinstance(w1, torch.Tensor) or w1.dim() != 3 or w1.shape[1] % 2:
         raise ValueError("w1: prepared weights [experts, 2 * intermediate, hidden] are needed")
     Et, I = w1.shape[0], w1.shape[1] // 2
@@ -296,7 +305,7 @@ def moe_few(x, w1, w2, s1=None, s2=None, *, topk_ids=None, topk_weights=None, ro
             raise ValueError("topk: needed with router_weight")
         if not isinstance(router_weight, torch.Tensor) or tuple(router_weight.shape) != (E, H):
             raise ValueError(f"router_weight: [{E}, {H}] is needed")
-        K = int(topk)
+        K = _whole("topk", topk)
     else:
         K = int(topk_ids.shape[1]) if isinstance(topk_ids, torch.Tensor) and topk_ids.dim() == 2 else 0
         _need("topk_ids", topk_ids, torch.int32, (T, K), dev)

@@ -75,3 +75,18 @@ def test_tangents_are_refused(launches, name):
         moe.block_quantize(q)
         with pytest.raises(ValueError, match="x: .*tangent"):
             moe.block_quantize(fw.make_dual(q, torch.ones_like(q)))
+
+
+def test_counts_are_whole_numbers(launches):
+    """A fraction of an expert is refused, not cut off."""
+    (x, w1, w2), routes = few_args()
+    wr = torch.zeros(4, 256, dtype=BF16)
+    for kw in (dict(router_weight=wr, topk=2.5), dict(router_weight=wr, topk="2"), dict(routes, num_shared_experts=0.5)):
+        with pytest.raises(ValueError, match="whole number"):
+            moe.moe_few(x, w1, w2, **kw)
+    with pytest.raises(ValueError, match="topk: .*whole number"):
+        moe.route(x, wr, topk=1.5)
+    assert not launches
+    import numpy as np
+    assert moe.route(x, wr, topk=np.int64(2))[0].shape == moe.route(x, wr, topk=2.0)[0].shape == (3, 2)
+    assert moe.moe_few(x, w1, w2, router_weight=wr, topk=torch.tensor(2))[1].shape == (3, 2)
