@@ -509,7 +509,8 @@ mm_status mm_few_plan_create(const mm_few_problem* problem, mm_few_plan* plan);
  *                  (FP8), [E+S][2I/128][H/128] (FP8_BLOCK), NULL (BF16)
  *   w2             device [E+S][H][I]
  *   w2_scale       device f32 [E+S][H], [E+S][H/128][I/128], or NULL
- *   y              device [T][H] out, bf16 or f32
+ *   y              device [T][H] out, bf16 or f32; may be x, and must not
+ *                  overlap another input
  *   workspace      device, plan.workspace_bytes
  */
 mm_status mm_moe_few(const mm_few_plan* plan, const void* x, const int32_t* topk_ids, const float* topk_weights,
@@ -567,7 +568,8 @@ mm_status mm_block_plan_create(const mm_block_problem* problem, mm_block_plan* p
  *   group_offsets, group_counts  device int32 [G] each (group_offsets may be
  *                  the [G+1] array of mm_dispatch_layout); both NULL if G = 1
  *                  means all M rows
- *   y              device bf16 [M][N] out
+ *   y              device bf16 [M][N] out; must not overlap an input, other
+ *                  than mm_block_linear's x
  */
 mm_status mm_block_gemm(const mm_block_plan* plan, const void* a, const float* a_scale, const void* b,
                         const float* b_scale, const int32_t* group_offsets, const int32_t* group_counts, void* y,

@@ -960,7 +960,10 @@ mm_status mm_block_linear(const mm_block_plan* plan, const void* x, const void* 
   if ((int64_t)workspace_bytes < plan->workspace_bytes) return MM_ERR_WORKSPACE;
   BlockArgs g = block_args(p, b, b_scale, group_offsets, group_counts, y);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (block_from_x(g)) {
+  // quantised on the way, x is read while y is written: not where they overlap
+  const uintptr_t xa = reinterpret_cast<uintptr_t>(x), ya = reinterpret_cast<uintptr_t>(y);
+  const bool apart = xa + p.rows * p.in_features * 2 <= ya || ya + p.rows * p.out_features * 2 <= xa;
+  if (apart && block_from_x(g)) {
     g.x = x;
   } else {
     uint8_t* codes = at<uint8_t>(workspace, 0);

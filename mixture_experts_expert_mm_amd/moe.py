@@ -193,6 +193,15 @@ def _need(name, t, dtype, shape, device):
         raise ValueError(f"{name}: carries a tangent, which this operator does not compute")
 
 
+def _apart(y, *inputs):
+    """y shares no byte with the inputs, which workgroups read while others write y."""
+    lo = y.data_ptr()
+    hi = lo + y.nbytes
+    for t in inputs:
+        if t is not None and t.data_ptr() < hi and lo < t.data_ptr() + t.nbytes:
+            raise ValueError("y: overlaps an input that is read while y is written")
+
+
 def _whole(name, n):
     try:
         return operator.index(int(n) if isinstance(n, float) and n.is_integer() else n)
@@ -271,7 +280,8 @@ def moe_few(x, w1, w2, s1=None, s2=None, *, topk_ids=None, topk_weights=None, ro
     x: bf16 [T,H].  w1 [E+S,2I,H] and w2 [E+S,H,I] are prepared weights (``ExpertLayer.w1``, ``.w2``), bf16, or
     e4m3 with float32 scales in formula order: per output channel (s1 [E+S,2I], s2 [E+S,H]) or per block of 128 x 128
     (s1 [E+S,2I/128,H/128], s2 [E+S,H/128,I/128]).  y_dtype: "bf16" or "f32".  Routes: topk_ids and topk_weights, or router_weight (with
-    router_bias, topk, scoring, renormalize and route_scale as in ``route``).  A shared expert is the last of w1, w2."""
+    router_bias, topk, scoring, renormalize and route_scale as in ``route``).  A shared expert is the last of w1, w2.  y
+    may be x, but must not overlap another input."""
     T, H, dev = _rows("x", x)
     if T > FEW_MAX_TOKENS:
         raise ValueError(f"x: at most {FEW_MAX_TOKENS} tokens, got {T} (ExpertLayer.forward takes more)")
@@ -314,6 +324,7 @@ def moe_few(x, w1, w2, s1=None, s2=None, *, topk_ids=None, topk_weights=None, ro
     ydt = _y_dtype(plan)
     if y is not None:
         _need("y", y, ydt, (T, H), dev)
+        _apart(y, w1, w2, s1, s2, topk_ids, topk_weights, active)      # (x has been read by then)
     with _stream_of(dev, stream):
         if y is None:
             y = torch.empty((T, H), dtype=ydt, device=dev)
@@ -340,7 +351,7 @@ def block_quantize(x, stream=None):
     return q, s
 
 
-def _block_args(M, K, dev, w, ws, offsets, counts, y):
+def _block_args(M, K, dev, rows, w, ws, offsets, counts, y):
     if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
         raise ValueError("w: [out, in] or [groups, out, in] is needed")
     G, N = (1, w.shape[0]) if w.dim() == 2 else (w.shape[0], w.shape[1])
@@ -355,17 +366,19 @@ def _block_args(M, K, dev, w, ws, offsets, counts, y):
         _need("counts", counts, torch.int32, (G,), dev)
     if y is not None:
         _need("y", y, torch.bfloat16, (M, N), dev)
+        _apart(y, *rows, w, ws, offsets, counts)
     return N, _block_plan(max(M, 1), N, K, G)
 
 
 def block_matmul(q, s, w, ws, offsets=None, counts=None, y=None, stream=None):
     """mm_block_gemm: y bf16 [M,N] of e4m3 rows (q [M,K], s [M,K/128]) and weights (w [N,K], ws [ceil(N/128),K/128]),
     or, with w [G,N,K] and ws [G,...], of groups of rows: group g covers rows offsets[g] .. offsets[g] + counts[g]
-    (int32; offsets may have G + 1 entries).  Rows that no group covers are left as they are (in a new y: unset)."""
+    (int32; offsets may have G + 1 entries).  Rows that no group covers are left as they are (in a new y: unset).  y
+    must not overlap an input."""
     M, K, dev = _rows("q", q)
     _need("q", q, torch.float8_e4m3fn, (M, K), dev)
     _need("s", s, torch.float32, (M, K // 128), dev)
-    N, plan = _block_args(M, K, dev, w, ws, offsets, counts, y)
+    N, plan = _block_args(M, K, dev, (q, s), w, ws, offsets, counts, y)
     with _stream_of(dev, stream):
         if y is None:
             y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
@@ -375,10 +388,10 @@ def block_matmul(q, s, w, ws, offsets=None, counts=None, y=None, stream=None):
 
 
 def block_linear(x, w, ws, offsets=None, counts=None, y=None, stream=None):
-    """mm_block_linear: block_matmul of x's (bf16 [M,K]) codes and scales, in one call."""
+    """mm_block_linear: block_matmul of x's (bf16 [M,K]) codes and scales, in one call.  y may overlap x."""
     M, K, dev = _rows("x", x)
     _need("x", x, torch.bfloat16, (M, K), dev)
-    N, plan = _block_args(M, K, dev, w, ws, offsets, counts, y)
+    N, plan = _block_args(M, K, dev, (), w, ws, offsets, counts, y)
     with _stream_of(dev, stream):
         if y is None:
             y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)

@@ -90,3 +90,40 @@ def test_counts_are_whole_numbers(launches):
     import numpy as np
     assert moe.route(x, wr, topk=np.int64(2))[0].shape == moe.route(x, wr, topk=2.0)[0].shape == (3, 2)
     assert moe.moe_few(x, w1, w2, router_weight=wr, topk=torch.tensor(2))[1].shape == (3, 2)
+
+
+def overlapping(y_shape, x_shape, x_dtype, shift):
+    """(y, x): two tensors of one buffer, x beginning `shift` bytes after y."""
+    buf = torch.zeros(1 << 14, dtype=torch.uint8)
+    n, m = 2 * y_shape[0] * y_shape[1], x_shape[0] * x_shape[1] * x_dtype.itemsize
+    return buf[:n].view(BF16).view(y_shape), buf[shift:shift + m].view(x_dtype).view(x_shape)
+
+
+@pytest.mark.parametrize("shift,ok", [(0, False), (512, False), (1008, False), (1024, True), (2048, True)])
+def test_y_apart_from_the_inputs(launches, shift, ok):
+    """Workgroups read the rows while others write y."""
+    w, ws = torch.zeros(128, 128, dtype=torch.float8_e4m3fn), torch.zeros(1, 1)
+    y, x = overlapping((4, 128), (4, 128), BF16, shift)
+    assert moe.block_linear(x, w, ws, y=y) is y              # (reads x first where they overlap)
+    y, q = overlapping((4, 128), (4, 128), torch.float8_e4m3fn, shift)
+    if ok:
+        assert moe.block_matmul(q, torch.zeros(4, 1), w, ws, y=y) is y
+    else:
+        with pytest.raises(ValueError, match="y: .*overlap"):
+            moe.block_matmul(q, torch.zeros(4, 1), w, ws, y=y)
+    (_, w1, w2), routes = few_args(T=2)
+    y, gates = overlapping((2, 256), (2, 2), F32, shift)
+    few = lambda x, y: moe.moe_few(x, w1, w2, y=y, topk_ids=routes["topk_ids"], topk_weights=gates)[0]
+    if ok:
+        assert few(torch.zeros(2, 256, dtype=BF16), y) is y
+    else:
+        with pytest.raises(ValueError, match="y: .*overlap"):
+            few(torch.zeros(2, 256, dtype=BF16), y)
+
+
+def test_the_layer_may_write_over_its_tokens(launches):
+    """Linear1 has read x before Linear2 writes y; the weights stay apart."""
+    (x, w1, w2), routes = few_args(T=2)
+    assert moe.moe_few(x, w1, w2, y=x, **routes)[0] is x
+    with pytest.raises(ValueError, match="y: .*overlap"):
+        moe.moe_few(x, w1, w2, y=w2.view(-1, 256)[:2], **routes)
