@@ -120,7 +120,6 @@ __global__ __launch_bounds__(kThreads) void k_router_scores(RouterArgs a) {
     for (int j = 0; j < ET; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const bool do_x = blockIdx.y == 0, do_w = blockIdx.x == 0;
   const int steps = a.H / kRouterStep, q = (int)blockIdx.z * KW + kw, Q = KW * a.KS;
-#pragma unroll TT == 1 ? 4 : 2
   for (int s = q; s < steps; s += Q) {
     u32x4 xv[TT][2], wv[ET][2];
 #pragma unroll
