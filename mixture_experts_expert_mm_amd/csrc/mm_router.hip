@@ -458,15 +458,17 @@ __global__ __launch_bounds__(256, NV <= 4 ? 4 : 1) void k_router_select(RouterAr
 // With few tokens or few scores in all, the scores are a stream of Wr: 16 x 16
 // tiles over as many workgroups as the hidden dimension gives (us for both
 // kernels, 16 x 16 / 64 x 64 a wave, hidden 7168: 333 tokens x 32 experts
-// 17 / 20, 1000 x 32 22 / 23, 1000 x 64 30 / 27, 4000 x 32 44 / 34).  Beyond, with
-// up to 64 experts, a wave holds 64 x 64 and the waves share the hidden
-// dimension; with more experts the LDS tiles (64 x 64 a wave / tiles of 128 x
-// 256: 16384 x 32 81 / 94, 16384 x 64 91 / 95, 2000 x 128 40 / 38, 16384 x 128
-// 144 / 110).  Tiles of 256 x 256 where half of the CUs get one of 24 stages or
-// more (tiles of 128 / 256 rows, hidden 7168: 16384 x 256 126 / 113, 10000 x 256
-// 107 / 95, 16384 x 128 102 / 96, 2000 x 256 39 / 50; hidden 2048: 33000 x 128
-// 122 / 105, 16384 x 160, 8 stages, 52 / 58; hidden 4096: 8192 x 512, 16 stages,
-// 73 / 82).
+// 18 / 23, 500 x 64 22 / 25, 1000 x 32 24 / 25, 1000 x 64 28 / 25, 4000 x 32
+// 43 / 33).  Beyond, with up to 64 experts, a wave holds 64 x 64 and the waves
+// share the hidden dimension; with more experts the LDS tiles (64 x 64 a wave /
+// tiles of 128 x 256: 16384 x 32 83 / 87, 16384 x 64 93 / 91, 2000 x 128 40 / 37,
+// 16384 x 128 152 / 98).  Tiles of 256 x 256 where those of 128 x 256 fill half of
+// the CUs in one slice and each of theirs gets 24 stages or more (tiles of 128 /
+// 256 rows, hidden 7168: 2000 x 256 44 / 57, 10000 x 256 95 / 98, 16384 x 128
+// 99 / 102, 16384 x 256 117 / 125, 20000 x 256 165 / 160, 33000 x 256 309 / 275,
+// 65536 x 128 334 / 316; hidden 4096: 16384 x 256 84 / 97, 33000 x 256 200 / 184,
+// 8192 x 512 81 / 103; hidden 2048: 33000 x 128 117 / 110, 65536 x 128 169 / 172).
+// The counts are those of a device of 256 CUs.
 RouterShape router_shape(int64_t T, int H, int E) {
   RouterShape s{};
   const int steps = H / kRouterStep;
@@ -497,7 +499,7 @@ RouterShape router_shape(int64_t T, int H, int E) {
     const int64_t tiles = (T + rows - 1) / rows * cols;
     const int n = slices(tiles, 8);
     s.ks = n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;   // whole XCDs to a slice
-    if (s.wide == 2 || (tiles * s.ks >= 128 && steps / s.ks >= 24)) return s;
+    if (s.wide == 2 || ((T + 127) / 128 * cols > 128 && steps / s.ks >= 24)) return s;
   }
 }
 
