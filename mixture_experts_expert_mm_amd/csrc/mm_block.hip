@@ -98,6 +98,7 @@ constexpr int kMidBM = 128, kMidBN = 64;  // the small tile
 constexpr int kFewRows = 16;              // most rows of a streaming unit
 constexpr int kFewCols = 16;
 constexpr int kRing = 4;                  // stages of the smallest tiles
+constexpr int kLargeTiles = 96;           // fewest large tiles of a product that is cut into them
 constexpr int kGroupM = 6;                // M-blocks that a run of tiles goes through before the next N-block
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -771,12 +772,13 @@ hipError_t launch_block_gemm(const BlockArgs& args, int num_cus, hipStream_t s) 
   // 64 / 64 x 64, 64 x 32 or 32 x 32 / 32 x 16, 4096 x 7168: 17 rows 34 / 15.3 / 12.5, 64
   // rows 36 / 15, 128 rows 43 / 21, 256 rows 42 / 27; 2048 x 4096: 17 rows 17.5 / 9.0 /
   // 7.7, 256 rows 18.6 / 12; 7168 x 2048: 17 rows 12.3 / 6.9 / -, 256 rows 15.5 / 15.3.
-  // Then, at 4096 x 7168, large tiles / 128 x 64 / 128 x 64 with two groups a stage:
-  // 512 rows 81 / 40 / 33, 1024 rows (64 large tiles, 512 of 128 x 64) 83 / 54 / 60,
-  // 1500 rows (96 large tiles) 81 / 84 / -, 2048 rows (128) 83 / 95 / 90; 32 groups of
-  // 16 rows (512 half tiles) 184 / 276 / -.  128 x 64 / 128 x 128 where a CU gets at
-  // most one of these: 1024 x 4096 x 7168 63 / 52, 320 x 7168 x 2048 21 / 18, 2048 x
-  // 2048 x 4096 37 / 30.
+  // Then, at 4096 x 7168, 512 rows: large tiles / 128 x 64 / 128 x 64 with two groups a
+  // stage 81 / 40 / 33.  128 x 64 / 128 x 128 where a CU gets at most one of these:
+  // 1024 x 4096 x 7168 63 / 52, 320 x 7168 x 2048 21 / 18, 2048 x 2048 x 4096 37 / 30.
+  // Large tiles from 96 of them on (large / 128 x 64: 4096 x 7168 80 tiles 85 / 89,
+  // 96 tiles 88 / 99, 112 tiles 89 / 101, 128 tiles 89 / 111; 2048 x 4096 72 tiles 50 /
+  // 49, 96 tiles 51 / 50, 104 tiles 51 / 55; 7168 x 2048 84 tiles 32 / 28, 112 tiles 33 /
+  // 33, 140 tiles 33 / 42; 32 groups of 16 rows, 512 half tiles, 182 / 277).
   const int64_t even = a.M / a.G > 0 ? a.M / a.G : 1;
   const int64_t tiles = (even + kBM - 1) / kBM * a.G * ((a.N + kBN - 1) / kBN);
   const unsigned cus = (unsigned)((num_cus + 7) / 8 * 8);
@@ -785,12 +787,14 @@ hipError_t launch_block_gemm(const BlockArgs& args, int num_cus, hipStream_t s) 
   else if (count(k32x32) <= num_cus) hipLaunchKernelGGL((k_block_ring<1, 1>), dim3(cus), dim3(256), 0, s, a);
   else if (count(k64x32) <= num_cus) hipLaunchKernelGGL((k_block_ring<2, 1>), dim3(cus), dim3(256), 0, s, a);
   else if (count(k64x64) <= num_cus) hipLaunchKernelGGL((k_block_ring<2, 2>), dim3(cus), dim3(256), 0, s, a);
-  else if (tiles < 112 && count(kMid) <= num_cus) hipLaunchKernelGGL((k_block_mid<2, true>), dim3(cus), dim3(kThreads), 0, s, a);
+  else if (tiles < kLargeTiles && count(kMid) <= num_cus) hipLaunchKernelGGL((k_block_mid<2, true>), dim3(cus), dim3(kThreads), 0, s, a);
   else if (count(k128x128) <= num_cus) hipLaunchKernelGGL((k_block_mid<4, true>), dim3(cus), dim3(kThreads), 0, s, a);
-  else if (tiles < 112) hipLaunchKernelGGL((k_block_mid<2, false>), dim3(3 * cus), dim3(kThreads), 0, s, a);
+  else if (tiles < kLargeTiles) hipLaunchKernelGGL((k_block_mid<2, false>), dim3(3 * cus), dim3(kThreads), 0, s, a);
   else {
     // one matrix: up to 16 rows beyond the blocks of 256 are streamed (4097 rows,
-    // 115 us; 147 with a half tile for the last row)
+    // 115 us; 147 with a half tile for the last row).  17 to 128 rows beyond, and
+    // those of groups, are a half tile, which copies 48 of a full one's 64 KiB a
+    // stage; where the full tiles fill the CUs' last round it takes one more.
     const int64_t rest = a.offsets == nullptr ? a.M % kBM : 0;
     if (rest <= kFewRows) a.M -= rest;
     hipLaunchKernelGGL(k_block_mma, dim3(cus), dim3(kThreads), 0, s, a);
