@@ -459,8 +459,9 @@ mm_status mm_router(const mm_router_plan* plan, const void* x, const void* weigh
  *     y_t = sum_k G[t,k] * ( SwiGLU( x_t . W1[e] ) . W2[e] ),  e = E[t,k],
  * plus the shared expert's FFN with weight 1 (num_shared_experts = 1, expert
  * index E), from the routes of mm_router or of the caller.  Two or three
- * kernels that read the weights of the experts with a route once; no
- * dispatch, no pool, no grid barrier.
+ * kernels that read the weights of the experts with a route once (W2 twice for
+ * a float32 y and an expert with more than 32 routes); no dispatch, no pool,
+ * no grid barrier.
  * Weight formats: MM_FEW_BF16 and MM_FEW_FP8 (e4m3 with f32 scales per output
  * channel) are the arrays that mm_prepare_weights writes for A16W16 and
  * A8W8_FP8, so a layer holds one copy for both paths; MM_FEW_FP8_BLOCK is
@@ -469,9 +470,9 @@ mm_status mm_router(const mm_router_plan* plan, const void* x, const void* weigh
  * widened exactly, products are exact, sums are float32.  A = SwiGLU(...) is
  * rounded to bf16 when y is bf16 (as A16W16 does) and kept to 24 bits when y
  * is f32.  A token's routes are summed in an order that the routes of the
- * batch alone decide: equal calls give equal bits.  Ids outside [0, E) are skipped (negative: masked) and contribute 0; an id
- * that a token names more than once counts once, with the sum of its weights
- * in the order of k.
+ * batch alone decide: equal calls give equal bits.  Ids outside [0, E) are
+ * skipped (negative: masked) and contribute 0; an id that a token names more
+ * than once counts once, with the sum of its weights in the order of k.
  */
 typedef enum mm_few_format { MM_FEW_BF16 = 0, MM_FEW_FP8 = 1, MM_FEW_FP8_BLOCK = 2 } mm_few_format;
 

@@ -1,12 +1,13 @@
-// The routed-expert layer for at most 64 tokens: kernels that read the live
-// experts' weights once from HBM into MFMA operands.
+// The routed-expert layer for at most 64 tokens: kernels that stream the live
+// experts' weights from HBM into MFMA operands.
 //
 //   Linear1: A[r] = SwiGLU(x_t . W1[e]) for every route r = (t, k), e = id(r)
 //   Linear2: y[t] = sum over t's routes of g_r * (A[r] . W2[e])
 //
 // Weights are the A operand of the 16 x 16 x 32 MFMA (16 weight rows), up to
 // 16 routes of one expert its B operand, so a weight byte is read once
-// whatever the number of tokens.  e4m3 weights are widened exactly to bf16
+// whatever the number of tokens (twice in Linear2 of a float32 y, for an expert
+// with more than 32 routes).  e4m3 weights are widened exactly to bf16
 // (activations are not quantised); float32 accumulators.  A is held in bf16
 // parts: one when y is bf16, whose own rounding is as large; three, the whole
 // float, when y is float32.
@@ -785,11 +786,13 @@ hipError_t run_tile(const FewArgs& a, hipStream_t s) {
 
 template <int F, int P>
 hipError_t run_l1_f(const FewArgs& a, int num_cus, hipStream_t s) {
-  // us for the whole layer with streaming / tile Linear1, 32 experts of 7168 x 2048,
-  // top-8: 1 token e4m3 77 / 85, 4 tokens 153 / 181, 8 tokens 200 / 208, 16 tokens 237 /
-  // 230, bf16 449 / 447; 16 experts of 4096 x 1408, top-4, bf16: 1 token 50 / 63, 8
-  // tokens 107 / 99, 16 tokens 114 / 113.  One MFMA of routes is the streaming
-  // kernels' limit.
+  // us for the whole layer with streaming / tile Linear1 and a bf16 y.  32 experts of
+  // 7168 x 2048, top-8, e4m3: 1 token 77 / 85, 4 tokens 171 / 190, 8 tokens 229 / 230, 16
+  // tokens 264 / 257, bf16 503 / 497; 64 experts of 2048 x 1408, top-6, e4m3: 1 token
+  // 30 / 31, 4 tokens 58 / 52, 8 tokens 80 / 83, 16 tokens 119 / 132, bf16 211 / 234.  16
+  // experts of 4096 x 1408, top-4, favour the tiles in e4m3 from 4 tokens on (51 / 49;
+  // 16 tokens 69 / 59; bf16 123 / 126): several routes an expert, whose rows the
+  // streaming kernel reads again for every 16 columns.  One MFMA of routes is its limit.
   if (a.T > kStreamT) return run_tile<F, 1, P>(a, s);
   return run_l1<F, P, 3>(a, num_cus, s);
 }
@@ -833,9 +836,11 @@ hipError_t run_l2_p(const FewArgs& a, int num_cus, hipStream_t s) {
 
 // Linear2 through slots (tiles and a combine), or streaming.  The three parts
 // of A that a float32 y takes cost the streaming kernel a read each per 16
-// columns.  us for the whole layer, streaming / tiles, e4m3: float32 y 1 token
-// 99 / 82, 4 tokens 214 / 172, 16 tokens 360 / 258; bf16 y 77 / 79, 153 / 165,
-// 237 / 246.
+// columns (us for the whole layer, streaming / tiles, 7168 x 2048 in e4m3: 1 token
+// 99 / 82, 4 tokens 214 / 172, 16 tokens 360 / 258).  With a bf16 y, the sizes above:
+// 1 token 77 / 78, 4 tokens 171 / 187, 16 tokens 264 / 275; smaller matrices with
+// several routes an expert favour the tiles (2048 x 1408, 4 tokens 58 / 49, 16 tokens
+// 119 / 98; 4096 x 1408, 16 tokens 69 / 63), one token does not (30 / 32, 30 / 33).
 bool few_slots(int64_t T, int y_f32) { return y_f32 || T > kStreamT; }
 
 hipError_t launch_few_l1(const FewArgs& a, int num_cus, hipStream_t s) {

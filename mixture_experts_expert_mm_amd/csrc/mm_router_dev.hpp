@@ -1,5 +1,5 @@
-// Selection of one token's experts from its partial scores, by one wave
-// (shared by the router's second kernel and the few-token layer).
+// Selection of one token's experts from its partial scores, by one wave (the
+// router's second kernel).
 #pragma once
 #include "mm_device.hpp"
 #include "mm_ops_internal.hpp"
