@@ -218,8 +218,9 @@ constexpr int kTileE = 256;
 // LDS-DMA two stages ahead, in three slots (TT = 8: Wr, which mostly comes from
 // L2, one stage ahead in two; tokens one stage ahead: 70 for 67 us).
 // Bound: the copies, of which a CU takes 36 to 40 bytes a ns: 2.8 MB a CU with
-// TT = 4 at 16384 x 256 x 7168, 1.9 MB with 8 (92 / 67 us; the first stage and the
-// writes of 67 MB of partial scores come on top).  Looking for the largest
+// TT = 4 at 16384 x 256 x 7168, 1.9 MB with 8, where the 64 tiles take four slices
+// for two and twice the partial scores, 67 MB, are written behind the last
+// stage (69 / 71 us; in one slice, 33000 x 256, 227 / 195).  Looking for the largest
 // partial sum costs 5 of 72 us at every third stage, 12 of 79 at each.
 template <int TT>
 __device__ __forceinline__ void router_tile(const RouterArgs& a, uint8_t* x0, uint8_t* w0, uint8_t* x1, uint8_t* w1,
@@ -435,8 +436,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))
 // One wave per token.  (Four tokens a wave in turn, the next one's scores
 // asked for meanwhile, took 58 against 43 us at 16384 x 256: a token that needs
 // 64-bit sums then holds up three others.)  Bound: issue, about 500
-// instructions a token, and the latency of the scores: 48 us at 16384 x 256
-// (27 without the turns that select, 29 without the 64-bit sums).
+// instructions a token, and the latency of the scores: 50 us at 16384 x 256
+// (20 without the turns that select, 33 without the 64-bit sums of one token in
+// 20).
 template <int NV, int KM>
 __global__ __launch_bounds__(256, NV <= 4 ? 4 : 1) void k_router_select(RouterArgs a) {
   const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
