@@ -579,6 +579,77 @@ mm_status mm_block_linear(const mm_block_plan* plan, const void* x, const void* 
                           const int32_t* group_offsets, const int32_t* group_counts, void* y, void* workspace,
                           uint64_t workspace_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------- sorted tokens
+ * Token rows sorted by expert and back, for expert products of the caller's
+ * own (mm_block_gemm's and mm_int8_gemm's groups, or a library's), with the
+ * gradients of both directions.  Route r = t*K + k is skipped where its id is
+ * outside [0, E) or its token inactive; the kept routes' rows lie in the order
+ * of (expert, route), without padding, and the order is the same in every
+ * call.  R = T*K.
+ *     rows[p] = x[route_of_row[p] / K]        for p < offsets[E]
+ *     rows[p] = 0                              for the rows behind them
+ *     y[t]    = sum_k w[t,k] * rows[row_of_route[t,k]]   (skipped: nothing)
+ * Sums are float32, in the order of k, rounded once.  An id that a token names
+ * twice is two routes.
+ */
+typedef enum mm_element {
+  MM_ELEMENT_BF16 = 0, MM_ELEMENT_F16 = 1, MM_ELEMENT_F32 = 2,
+  MM_ELEMENT_8BIT = 3          /* any byte codes: moved, never summed */
+} mm_element;
+
+typedef struct mm_sort_problem {
+  int64_t num_tokens;    /* T in [1, 2^24], T*K below 2^30 */
+  int64_t hidden;        /* H in [1, 2^20], elements of a row */
+  int64_t num_experts;   /* E in [1, 1024] */
+  int64_t num_topk;      /* K in [1, 64] */
+  int32_t element;       /* mm_element of the rows */
+  int32_t reserved0;     /* must be 0 */
+} mm_sort_problem;
+
+typedef struct mm_sort_plan {
+  mm_sort_problem prob;
+  int64_t workspace_bytes;   /* of mm_sort_tokens; may be 0 */
+  uint64_t checksum;
+  int64_t reserved[4];
+} mm_sort_plan;
+
+mm_status mm_sort_plan_create(const mm_sort_problem* problem, mm_sort_plan* plan);
+
+/*
+ * mm_sort_tokens -- the order, and the rows in it.
+ *   topk_ids       device int32 [T][K]
+ *   x_active_mask  device int8 [T] or NULL
+ *   x              device [T][H], or NULL with rows NULL: the order alone
+ *   counts         device int32 [E] out
+ *   offsets        device int32 [E+1] out: exclusive prefix of counts
+ *   row_of_route   device int32 [T][K] out: -1 for a skipped route
+ *   route_of_row   device int32 [R] out: -1 behind the last row
+ *   rows           device [R][H] out; must not overlap an input
+ *   workspace      device, plan.workspace_bytes (NULL if 0)
+ * mm_sort_rows -- the rows of another x (codes, scales, a gradient) in an
+ * order that mm_sort_tokens has made.
+ * mm_combine_tokens -- y from rows; weights device f32 [T][K], or NULL (all
+ * 1: the gradient of mm_sort_rows, with the rows' gradient in place of rows).
+ * mm_combine_backward -- the gradient of mm_combine_tokens with weights:
+ *     drows[p] = w[t,k] * dy[t]   (0 behind the last row)
+ *     dweights[t,k] = <dy[t], rows[p]> in float32   (0 for a skipped route)
+ * drows may be NULL, and dweights with rows.  (Without weights it is
+ * mm_sort_rows of dy.)
+ * Elements of 8 bits: mm_sort_tokens and mm_sort_rows alone
+ * (MM_ERR_UNSUPPORTED).
+ */
+mm_status mm_sort_tokens(const mm_sort_plan* plan, const int32_t* topk_ids, const int8_t* x_active_mask, const void* x,
+                         int32_t* counts, int32_t* offsets, int32_t* row_of_route, int32_t* route_of_row, void* rows,
+                         void* workspace, uint64_t workspace_bytes, void* stream);
+mm_status mm_sort_rows(const mm_sort_plan* plan, const void* x, const int32_t* offsets, const int32_t* row_of_route,
+                       void* rows, void* stream);
+mm_status mm_combine_tokens(const mm_sort_plan* plan, const void* rows, const int32_t* row_of_route,
+                            const float* weights, void* y, void* stream);
+mm_status mm_combine_backward(const mm_sort_plan* plan, const void* dy, const void* rows, const int32_t* offsets,
+                              const int32_t* row_of_route, const float* weights, void* drows, float* dweights,
+                              void* stream);
+
 /* Kernel timing (diagnostics).  While enabled, every kernel the library
  * launches is bracketed by two HIP events on its stream; mm_trace_collect
  * waits for them and returns, per kernel id, the number of launches and
@@ -589,7 +660,9 @@ typedef enum mm_kernel_id {
   MM_K_MEGA = 9,                 /* the fused persistent kernel of mega_moe */
   MM_K_ROUTER = 10, MM_K_ROUTER_SELECT = 11, MM_K_FEW_L1 = 12, MM_K_FEW_L2 = 13,
   MM_K_BLOCK_QUANTIZE = 14, MM_K_BLOCK_GEMM = 15,
-  MM_K_COUNT_IDS = 16
+                                 /* 16: no kernel */
+  MM_K_SORT_ORDER = 17, MM_K_SORT_ROWS = 18, MM_K_COMBINE_TOKENS = 19, MM_K_COMBINE_BACKWARD = 20,
+  MM_K_COUNT_IDS = 21
 } mm_kernel_id;
 
 mm_status mm_trace_enable(int on);

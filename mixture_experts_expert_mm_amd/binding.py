@@ -18,12 +18,15 @@ from . import _build
 MM_A16W16, MM_A8W8_FP8, MM_A8W8_INT8, MM_MXFP8, MM_MXFP4 = 0, 1, 2, 3, 4
 MM_OUT_BF16, MM_OUT_F32 = 0, 1
 USECASE = {"bf16": MM_A16W16, "fp8": MM_A8W8_FP8, "int8": MM_A8W8_INT8, "mxfp8": MM_MXFP8, "mxfp4": MM_MXFP4}
-KERNEL_IDS = 16
+KERNEL_IDS = 21
 MM_ROUTER_SOFTMAX, MM_ROUTER_SIGMOID = 0, 1
 SCORING = {"softmax": MM_ROUTER_SOFTMAX, "sigmoid": MM_ROUTER_SIGMOID}
 MM_FEW_BF16, MM_FEW_FP8, MM_FEW_FP8_BLOCK = 0, 1, 2
 OUT_DTYPE = {"bf16": MM_OUT_BF16, "f32": MM_OUT_F32, "fp32": MM_OUT_F32}
 FEW_FORMAT = {"bf16": MM_FEW_BF16, "fp8": MM_FEW_FP8, "fp8_block": MM_FEW_FP8_BLOCK}
+MM_ELEMENT_BF16, MM_ELEMENT_F16, MM_ELEMENT_F32, MM_ELEMENT_8BIT = 0, 1, 2, 3
+ELEMENT = {torch.bfloat16: MM_ELEMENT_BF16, torch.float16: MM_ELEMENT_F16, torch.float32: MM_ELEMENT_F32,
+           torch.int8: MM_ELEMENT_8BIT, torch.uint8: MM_ELEMENT_8BIT, torch.float8_e4m3fn: MM_ELEMENT_8BIT}
 MM_DEVERR_BAD_EXPERT, MM_DEVERR_BARRIER_TIMEOUT, MM_DEVERR_BAD_OFFSETS = 1, 2, 4
 
 
@@ -129,12 +132,33 @@ class MMBlockPlan(ctypes.Structure):
     ]
 
 
+class MMSortProblem(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("hidden", ctypes.c_int64),
+        ("num_experts", ctypes.c_int64),
+        ("num_topk", ctypes.c_int64),
+        ("element", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32),
+    ]
+
+
+class MMSortPlan(ctypes.Structure):
+    _fields_ = [
+        ("prob", MMSortProblem),
+        ("workspace_bytes", ctypes.c_int64),
+        ("checksum", ctypes.c_uint64),
+        ("reserved", ctypes.c_int64 * 4),
+    ]
+
+
 EXPORTS = [
     "mm_plan_create", "mm_prepare_weights", "mm_dispatch_layout", "mm_grouped_l1_swiglu",
     "mm_grouped_l2_combine", "mega_moe", "mega_moe_noalloc", "mm_read_device_error", "mm_debug_raw_accumulators",
     "mm_debug_fused_layout", "mm_read_kernel_clock", "mm_trace_enable", "mm_trace_collect", "mm_kernel_name", "mm_status_string",
     "mm_router_plan_create", "mm_router", "mm_few_plan_create", "mm_moe_few", "mm_block_quantize",
     "mm_block_plan_create", "mm_block_gemm", "mm_block_linear",
+    "mm_sort_plan_create", "mm_sort_tokens", "mm_sort_rows", "mm_combine_tokens", "mm_combine_backward",
 ]
 
 _lib = None
@@ -181,6 +205,12 @@ def load() -> ctypes.CDLL:
     lib.mm_block_plan_create.argtypes = [ctypes.POINTER(MMBlockProblem), BP]
     lib.mm_block_gemm.argtypes = [BP, vp, f32p, vp, f32p, i32p, i32p, vp, vp]
     lib.mm_block_linear.argtypes = [BP, vp, vp, f32p, i32p, i32p, vp, vp, u64, vp]
+    SP = ctypes.POINTER(MMSortPlan)
+    lib.mm_sort_plan_create.argtypes = [ctypes.POINTER(MMSortProblem), SP]
+    lib.mm_sort_tokens.argtypes = [SP, i32p, vp, vp, i32p, i32p, i32p, i32p, vp, vp, u64, vp]
+    lib.mm_sort_rows.argtypes = [SP, vp, i32p, i32p, vp, vp]
+    lib.mm_combine_tokens.argtypes = [SP, vp, i32p, f32p, vp, vp]
+    lib.mm_combine_backward.argtypes = [SP, vp, vp, i32p, i32p, f32p, vp, f32p, vp]
     lib.mm_trace_enable.argtypes = [ctypes.c_int]
     lib.mm_trace_collect.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double)]
     lib.mm_kernel_name.argtypes = [ctypes.c_int]
@@ -334,6 +364,37 @@ def mm_block_linear(plan, x, b, b_scale, group_offsets, group_counts, y, workspa
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
+def mm_sort_plan_create(T, H, E, K, element) -> MMSortPlan:
+    prob = MMSortProblem(T, H, E, K, element, 0)
+    plan = MMSortPlan()
+    _check("mm_sort_plan_create", load().mm_sort_plan_create(ctypes.byref(prob), ctypes.byref(plan)))
+    return plan
+
+
+def mm_sort_tokens(plan, topk_ids, x_active_mask, x, counts, offsets, row_of_route, route_of_row, rows, workspace,
+                   stream=None):
+    _check("mm_sort_tokens", load().mm_sort_tokens(
+        ctypes.byref(plan), _ptr(topk_ids), _ptr(x_active_mask), _ptr(x), _ptr(counts), _ptr(offsets),
+        _ptr(row_of_route), _ptr(route_of_row), _ptr(rows), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def mm_sort_rows(plan, x, offsets, row_of_route, rows, stream=None):
+    _check("mm_sort_rows", load().mm_sort_rows(
+        ctypes.byref(plan), _ptr(x), _ptr(offsets), _ptr(row_of_route), _ptr(rows), _stream(stream)))
+
+
+def mm_combine_tokens(plan, rows, row_of_route, weights, y, stream=None):
+    _check("mm_combine_tokens", load().mm_combine_tokens(
+        ctypes.byref(plan), _ptr(rows), _ptr(row_of_route), _ptr(weights), _ptr(y), _stream(stream)))
+
+
+def mm_combine_backward(plan, dy, rows, offsets, row_of_route, weights, drows, dweights, stream=None):
+    _check("mm_combine_backward", load().mm_combine_backward(
+        ctypes.byref(plan), _ptr(dy), _ptr(rows), _ptr(offsets), _ptr(row_of_route), _ptr(weights), _ptr(drows),
+        _ptr(dweights), _stream(stream)))
+
+
 def mm_read_device_error(plan, workspace, stream=None) -> int:
     """The device error word (mm_device_error bits) of the last call on `workspace`."""
     out = ctypes.c_int32(0)
@@ -375,7 +436,8 @@ def mm_trace_collect():
     n = (ctypes.c_int32 * KERNEL_IDS)()
     ms = (ctypes.c_double * KERNEL_IDS)()
     _check("mm_trace_collect", load().mm_trace_collect(n, ms))
-    return {load().mm_kernel_name(i).decode(): (n[i], ms[i]) for i in range(KERNEL_IDS)}
+    names = [load().mm_kernel_name(i).decode() for i in range(KERNEL_IDS)]
+    return {name: (n[i], ms[i]) for i, name in enumerate(names) if name != "unknown"}
 
 
 def mm_kernel_name(i: int) -> str:

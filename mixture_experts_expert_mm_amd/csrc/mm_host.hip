@@ -465,6 +465,31 @@ BlockArgs block_args(const mm_block_problem& p, const void* b, const float* b_sc
   return g;
 }
 
+SortArgs sort_args(const mm_sort_problem& p) {
+  SortArgs a{};
+  a.T = p.num_tokens;
+  a.R = p.num_tokens * p.num_topk;
+  a.row_bytes = p.hidden * (p.element == MM_ELEMENT_F32 ? 4 : p.element == MM_ELEMENT_8BIT ? 1 : 2);
+  a.E = (int)p.num_experts;
+  a.K = (int)p.num_topk;
+  return a;
+}
+
+CombineTokensArgs combine_tokens_args(const mm_sort_problem& p, const void* rows, const int32_t* row_of_route,
+                                      const float* weights) {
+  CombineTokensArgs a{};
+  a.rows = rows;
+  a.row_of_route = row_of_route;
+  a.weights = weights;
+  a.T = p.num_tokens;
+  a.R = p.num_tokens * p.num_topk;
+  a.H = p.hidden;
+  a.E = (int)p.num_experts;
+  a.K = (int)p.num_topk;
+  a.element = p.element;
+  return a;
+}
+
 // ---------------------------------------------------------------- static scratch
 // The workspace of mega_moe_noalloc: a device array of the library itself,
 // one copy per GPU, held until the process ends.  Host code never passes
@@ -975,6 +1000,94 @@ mm_status mm_block_linear(const mm_block_plan* plan, const void* x, const void* 
   return run(MM_K_BLOCK_GEMM, s, [&] { return launch_block_gemm(g, num_cus(), s); });
 }
 
+// --------------------------------------------------------- sorted tokens
+mm_status mm_sort_plan_create(const mm_sort_problem* problem, mm_sort_plan* plan) {
+  if (!problem || !plan) return MM_ERR_INVALID_ARG;
+  const mm_sort_problem p = *problem;
+  if (p.element < MM_ELEMENT_BF16 || p.element > MM_ELEMENT_8BIT) return MM_ERR_UNSUPPORTED;
+  if (p.num_tokens < 1 || p.num_tokens > (1 << 24) || p.hidden < 1 || p.hidden > (1 << 20)) return MM_ERR_INVALID_ARG;
+  if (p.num_experts < 1 || p.num_experts > 1024 || p.num_topk < 1 || p.num_topk > 64) return MM_ERR_INVALID_ARG;
+  if (p.num_tokens * p.num_topk >= (1 << 30) || p.reserved0 != 0) return MM_ERR_INVALID_ARG;
+  mm_sort_plan pl;
+  std::memset(&pl, 0, sizeof(pl));
+  pl.prob = p;
+  const int64_t routes = p.num_tokens * p.num_topk;
+  const int64_t chunk = sort_chunk(routes);
+  pl.workspace_bytes = sort_in_one(routes) ? 0 : align_up((routes + chunk - 1) / chunk * p.num_experts * 4, kAlign);
+  pl.checksum = plan_checksum(&pl);
+  *plan = pl;
+  return MM_OK;
+}
+
+mm_status mm_sort_tokens(const mm_sort_plan* plan, const int32_t* topk_ids, const int8_t* x_active_mask, const void* x,
+                         int32_t* counts, int32_t* offsets, int32_t* row_of_route, int32_t* route_of_row, void* rows,
+                         void* workspace, uint64_t workspace_bytes, void* stream) {
+  MM_TRY(check_plan(plan));
+  if (!ok4(topk_ids) || !ok4(counts) || !ok4(offsets) || !ok4(row_of_route) || !ok4(route_of_row))
+    return MM_ERR_INVALID_ARG;
+  if ((x != nullptr || rows != nullptr) && (!ok16(x) || !ok16(rows))) return MM_ERR_INVALID_ARG;
+  if (plan->workspace_bytes > 0 && !ok16(workspace)) return MM_ERR_INVALID_ARG;
+  if ((int64_t)workspace_bytes < plan->workspace_bytes) return MM_ERR_WORKSPACE;
+  SortArgs a = sort_args(plan->prob);
+  a.ids = topk_ids;
+  a.active = x_active_mask;
+  a.counts = counts;
+  a.offsets = offsets;
+  a.row_of_route = row_of_route;
+  a.route_of_row = route_of_row;
+  a.x = static_cast<const uint8_t*>(x);
+  a.rows = static_cast<uint8_t*>(rows);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (sort_in_one(a.R)) return run(MM_K_SORT_ORDER, s, [&] { return launch_sort_few(a, s); });
+  a.chunk = sort_chunk(a.R);
+  a.chunks = (int)((a.R + a.chunk - 1) / a.chunk);
+  a.hist = at<int32_t>(workspace, 0);
+  MM_TRY(run(MM_K_SORT_ORDER, s, [&] { return launch_sort_order(a, s); }));
+  if (rows == nullptr) return MM_OK;
+  return run(MM_K_SORT_ROWS, s, [&] { return launch_sort_rows(a, s); });
+}
+
+mm_status mm_sort_rows(const mm_sort_plan* plan, const void* x, const int32_t* offsets, const int32_t* row_of_route,
+                       void* rows, void* stream) {
+  MM_TRY(check_plan(plan));
+  if (!ok16(x) || !ok4(offsets) || !ok4(row_of_route) || !ok16(rows)) return MM_ERR_INVALID_ARG;
+  SortArgs a = sort_args(plan->prob);
+  a.offsets = const_cast<int32_t*>(offsets);
+  a.row_of_route = const_cast<int32_t*>(row_of_route);
+  a.x = static_cast<const uint8_t*>(x);
+  a.rows = static_cast<uint8_t*>(rows);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return run(MM_K_SORT_ROWS, s, [&] { return launch_sort_rows(a, s); });
+}
+
+mm_status mm_combine_tokens(const mm_sort_plan* plan, const void* rows, const int32_t* row_of_route,
+                            const float* weights, void* y, void* stream) {
+  MM_TRY(check_plan(plan));
+  if (!ok16(rows) || !ok4(row_of_route) || !aligned(weights, 4) || !ok16(y)) return MM_ERR_INVALID_ARG;
+  if (plan->prob.element == MM_ELEMENT_8BIT) return MM_ERR_UNSUPPORTED;
+  CombineTokensArgs a = combine_tokens_args(plan->prob, rows, row_of_route, weights);
+  a.y = y;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return run(MM_K_COMBINE_TOKENS, s, [&] { return launch_combine_tokens(a, s); });
+}
+
+mm_status mm_combine_backward(const mm_sort_plan* plan, const void* dy, const void* rows, const int32_t* offsets,
+                              const int32_t* row_of_route, const float* weights, void* drows, float* dweights,
+                              void* stream) {
+  MM_TRY(check_plan(plan));
+  if (!ok16(dy) || !ok4(offsets) || !ok4(row_of_route) || !ok4(weights)) return MM_ERR_INVALID_ARG;
+  if ((drows == nullptr && dweights == nullptr) || !aligned(drows, 16) || !aligned(dweights, 4)) return MM_ERR_INVALID_ARG;
+  if (dweights != nullptr && !ok16(rows)) return MM_ERR_INVALID_ARG;
+  if (plan->prob.element == MM_ELEMENT_8BIT) return MM_ERR_UNSUPPORTED;
+  CombineTokensArgs a = combine_tokens_args(plan->prob, rows, row_of_route, weights);
+  a.dy = dy;
+  a.offsets = offsets;
+  a.drows = drows;
+  a.dweights = dweights;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return run(MM_K_COMBINE_BACKWARD, s, [&] { return launch_combine_backward(a, s); });
+}
+
 mm_status mm_trace_enable(int on) {
   std::lock_guard<std::mutex> g(g_trace_mu);
   g_trace_on = on != 0;
@@ -1014,7 +1127,8 @@ const char* mm_kernel_name(int id) {
   static const char* names[] = {"zero",    "count",   "scatter", "gather", "l1_swiglu",
                                 "requant", "l2_gate", "combine", "prepare", "mega",
                                 "router", "router_select", "few_l1", "few_l2",
-                                "block_quantize", "block_gemm"};
+                                "block_quantize", "block_gemm", "unknown",
+                                "sort_order", "sort_rows", "combine_tokens", "combine_backward"};
   if (id < 0 || id >= MM_K_COUNT_IDS) return "unknown";
   return names[id];
 }

@@ -1,5 +1,6 @@
-// Internal interfaces of the router, the few-token layer and the
-// block-scaled product (mm_router.hip, mm_few.hip, mm_block.hip).
+// Internal interfaces of the router, the few-token layer, the block-scaled
+// product and the token sort (mm_router.hip, mm_few.hip, mm_block.hip,
+// mm_sort.hip).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -78,5 +79,41 @@ hipError_t launch_block_quantize(const void* x, int64_t rows, int cols, uint8_t*
 bool block_in_lds(const BlockArgs& a);
 bool block_from_x(const BlockArgs& a);
 hipError_t launch_block_gemm(const BlockArgs& a, int num_cus, hipStream_t s);
+
+// -------------------------------------------------------------- token sort
+struct SortArgs {
+  const int32_t* ids;        // [T][K]
+  const int8_t* active;      // [T] or null
+  int32_t* counts;           // [E]
+  int32_t* offsets;          // [E+1]
+  int32_t* row_of_route;     // [T*K]
+  int32_t* route_of_row;     // [T*K]
+  const uint8_t* x;          // [T][row_bytes], or null
+  uint8_t* rows;             // [T*K][row_bytes], or null
+  int32_t* hist;             // ws: [chunks][E]
+  int64_t T, R, row_bytes;
+  int E, K, chunk, chunks;
+};
+int sort_chunk(int64_t routes);
+// whether launch_sort_few does it all (order and rows); else launch_sort_order, then launch_sort_rows
+bool sort_in_one(int64_t routes);
+hipError_t launch_sort_few(const SortArgs& a, hipStream_t s);
+hipError_t launch_sort_order(const SortArgs& a, hipStream_t s);
+hipError_t launch_sort_rows(const SortArgs& a, hipStream_t s);
+
+struct CombineTokensArgs {
+  const void* rows;          // [T*K][H]
+  const int32_t* row_of_route;
+  const int32_t* offsets;    // [E+1] (backward)
+  const float* weights;      // [T][K], or null (forward: 1)
+  void* y;                   // [T][H] (forward)
+  const void* dy;            // [T][H] (backward)
+  void* drows;               // [T*K][H] or null
+  float* dweights;           // [T][K] or null
+  int64_t T, R, H;
+  int E, K, element;
+};
+hipError_t launch_combine_tokens(const CombineTokensArgs& a, hipStream_t s);
+hipError_t launch_combine_backward(const CombineTokensArgs& a, hipStream_t s);
 
 }  // namespace mm

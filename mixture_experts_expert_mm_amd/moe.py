@@ -4,8 +4,10 @@
 workspace, and calls the C-ABI entry points through ``binding``.  The
 functions ``route``, ``moe_few``, ``block_quantize``, ``block_matmul`` and
 ``block_linear`` hold nothing: each checks its tensors, allocates the
-outputs and a workspace on the calling stream and makes one call.  Nothing
-here computes any part of the expert path.
+outputs and a workspace on the calling stream and makes one call.  So do
+``sort_tokens``, ``sort_rows``, ``combine_tokens`` and ``combine_backward``;
+the first three are differentiable.  Nothing here computes any part of the
+expert path.
 """
 
 from __future__ import annotations
@@ -180,14 +182,15 @@ _block_plan = functools.lru_cache(maxsize=256)(B.mm_block_plan_create)
 FEW_MAX_TOKENS = 64
 
 
-def _need(name, t, dtype, shape, device):
-    """The one check of a tensor argument: a message that says what it has to be."""
+def _need(name, t, dtype, shape, device, grad=False):
+    """The one check of a tensor argument: a message that says what it has to be.  grad: the operator has a gradient
+    with respect to it."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
     if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor {list(shape)} on {device} is needed, got {t.dtype} "
                          f"{list(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
-    if t.requires_grad and torch.is_grad_enabled():
+    if t.requires_grad and not grad and torch.is_grad_enabled():
         raise ValueError(f"{name}: requires a gradient, which this operator does not compute (call it under no_grad)")
     if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
         raise ValueError(f"{name}: carries a tangent, which this operator does not compute")
@@ -398,3 +401,212 @@ def block_linear(x, w, ws, offsets=None, counts=None, y=None, stream=None):
         if M:
             B.mm_block_linear(plan, x, w, ws, offsets, counts, y, _workspace(plan.workspace_bytes, dev), _raw_stream(dev))
     return y
+
+
+# ----------------------------------------------------------- sorted tokens
+
+_sort_plan = functools.lru_cache(maxsize=256)(B.mm_sort_plan_create)
+
+
+@dataclasses.dataclass
+class TokenOrder:
+    """Where the routes' rows lie: experts ascending, an expert's rows in the order of their routes t * K + k.
+
+    counts int32 [E]; offsets int32 [E+1], their exclusive prefix (expert e has the rows offsets[e] .. offsets[e + 1]);
+    row_of_route int32 [T,K], -1 for a skipped route; route_of_row int32 [T*K], -1 behind the last row."""
+    counts: torch.Tensor
+    offsets: torch.Tensor
+    row_of_route: torch.Tensor
+    route_of_row: torch.Tensor
+
+
+def _element(name, x, summed):
+    el = B.ELEMENT.get(x.dtype)
+    if el is None or (summed and el == B.MM_ELEMENT_8BIT):
+        raise ValueError(f"{name}: bf16, float16 or float32" + ("" if summed else ", or 8-bit codes,") +
+                         f" are needed, got {x.dtype}")
+    return el
+
+
+def _order_of(order, device):
+    """(T, E, K) of an order whose tensors are as they have to be."""
+    if not isinstance(order, TokenOrder):
+        raise ValueError(f"order: a TokenOrder is needed, got {type(order).__name__}")
+    if not isinstance(order.row_of_route, torch.Tensor) or order.row_of_route.dim() != 2:
+        raise ValueError("order.row_of_route: a matrix [tokens, topk] is needed")
+    if not isinstance(order.counts, torch.Tensor) or order.counts.dim() != 1:
+        raise ValueError("order.counts: a vector [experts] is needed")
+    (T, K), E, i32 = order.row_of_route.shape, order.counts.shape[0], torch.int32
+    _need("order.counts", order.counts, i32, (E,), device)
+    _need("order.offsets", order.offsets, i32, (E + 1,), device)
+    _need("order.row_of_route", order.row_of_route, i32, (T, K), device)
+    _need("order.route_of_row", order.route_of_row, i32, (T * K,), device)
+    return T, E, K
+
+
+def _records(*tensors):
+    """Whether autograd records this call.  Under capture it may not: the engine ends the process where an eager graph
+    of the same leaves is alive, which cannot be seen from here."""
+    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in tensors):
+        return False
+    _not_captured()
+    return True
+
+
+def _not_captured():
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("autograd under stream capture: call the operators under no_grad and their backward "
+                           "functions instead")
+
+
+def _dense(t):
+    """A gradient as autograd hands it over (expanded, strided, at any address) in the form that kernels take."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
+def _sort_rows(x, order, T, E, K):
+    H = x.shape[1]
+    rows = torch.empty((T * K, H), dtype=x.dtype, device=x.device)
+    if T:
+        plan = _sort_plan(T, H, E, K, B.ELEMENT[x.dtype])
+        B.mm_sort_rows(plan, x, order.offsets, order.row_of_route, rows, _raw_stream(x.device))
+    return rows
+
+
+def _combine(rows, order, weights, T, E, K):
+    H = rows.shape[1]
+    y = torch.empty((T, H), dtype=rows.dtype, device=rows.device)
+    if T:
+        plan = _sort_plan(T, H, E, K, B.ELEMENT[rows.dtype])
+        B.mm_combine_tokens(plan, rows, order.row_of_route, weights, y, _raw_stream(rows.device))
+    return y
+
+
+def _combine_backward(dy, rows, order, weights, T, E, K, of_rows, of_weights):
+    H, dev = dy.shape[1], dy.device
+    drows = torch.empty((T * K, H), dtype=dy.dtype, device=dev) if of_rows else None
+    dweights = torch.empty((T, K), dtype=torch.float32, device=dev) if of_weights else None
+    if T and (of_rows or of_weights):
+        plan = _sort_plan(T, H, E, K, B.ELEMENT[dy.dtype])
+        B.mm_combine_backward(plan, dy, rows if of_weights else None, order.offsets, order.row_of_route, weights, drows,
+                              dweights, _raw_stream(dev))
+    return drows, dweights
+
+
+class _SortFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, make):
+        rows, order, ctx.dims = make(x)
+        ctx.save_for_backward(order.counts, order.offsets, order.row_of_route, order.route_of_row)
+        return rows
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, drows):
+        _not_captured()
+        return _combine(_dense(drows), TokenOrder(*ctx.saved_tensors), None, *ctx.dims), None
+
+
+class _CombineFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, weights, order, dims):
+        ctx.dims = dims
+        ctx.save_for_backward(rows if weights is not None and weights.requires_grad else None, weights, order.counts,
+                              order.offsets, order.row_of_route, order.route_of_row)
+        return _combine(rows, order, weights, *dims)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        _not_captured()
+        rows, weights, *order = ctx.saved_tensors
+        order, dy = TokenOrder(*order), _dense(dy)
+        if weights is None:
+            return _sort_rows(dy, order, *ctx.dims), None, None, None
+        of_rows, of_weights = ctx.needs_input_grad[:2]
+        return *_combine_backward(dy, rows, order, weights, *ctx.dims, of_rows, of_weights), None, None
+
+
+def sort_tokens(x, topk_ids, num_experts, *, active=None, stream=None):
+    """mm_sort_tokens: (rows [T*K,H], TokenOrder) of the tokens x [T,H] (bf16, float16, float32, or 8-bit codes).
+
+    topk_ids: int32 [T,K]; a route with an id outside [0, num_experts), or of a token whose entry of active (int8 [T])
+    is 0, is skipped.  Row p is the token of route ``order.route_of_row[p]``; rows behind the last one are 0.
+    Differentiable with respect to x; the gradient is ``combine_tokens(drows, order)``."""
+    T, H, dev = _rows("x", x)
+    el = _element("x", x, False)
+    _need("x", x, x.dtype, (T, H), dev, grad=el != B.MM_ELEMENT_8BIT)
+    K = int(topk_ids.shape[1]) if isinstance(topk_ids, torch.Tensor) and topk_ids.dim() == 2 else 0
+    _need("topk_ids", topk_ids, torch.int32, (T, K), dev)
+    if active is not None:
+        _need("active", active, torch.int8, (T,), dev)
+    E = _whole("num_experts", num_experts)
+    plan = _sort_plan(max(T, 1), H, E, K, el)
+
+    def make(x):
+        i32 = dict(dtype=torch.int32, device=dev)
+        rows = torch.empty((T * K, H), dtype=x.dtype, device=dev)
+        new = torch.empty if T else torch.zeros
+        order = TokenOrder(new(E, **i32), new(E + 1, **i32), torch.empty((T, K), **i32), torch.empty(T * K, **i32))
+        if T:
+            ws = _workspace(plan.workspace_bytes, dev) if plan.workspace_bytes else None
+            B.mm_sort_tokens(plan, topk_ids, active, x, order.counts, order.offsets, order.row_of_route,
+                             order.route_of_row, rows, ws, _raw_stream(dev))
+        made.append(order)
+        return rows, order, (T, E, K)
+
+    made = []
+    with _stream_of(dev, stream):
+        rows = _SortFunction.apply(x, make) if _records(x) else make(x)[0]
+    return rows, made[0]
+
+
+def sort_rows(x, order, *, stream=None):
+    """mm_sort_rows: the rows [T*K,H] of another x [T,H] (codes, scales, a gradient) in an order that sort_tokens has
+    made.  Differentiable as sort_tokens is."""
+    T, H, dev = _rows("x", x)
+    el = _element("x", x, False)
+    _need("x", x, x.dtype, (T, H), dev, grad=el != B.MM_ELEMENT_8BIT)
+    dims = _order_of(order, dev)
+    if dims[0] != T:
+        raise ValueError(f"order: one of {T} tokens is needed, got one of {dims[0]}")
+    _sort_plan(max(T, 1), H, dims[1], dims[2], el)
+    make = lambda x: (_sort_rows(x, order, *dims), order, dims)
+    with _stream_of(dev, stream):
+        return _SortFunction.apply(x, make) if _records(x) else make(x)[0]
+
+
+def _combine_args(name, rows, order, weights):
+    R, H, dev = _rows(name, rows)
+    el = _element(name, rows, True)
+    dims = T, E, K = _order_of(order, dev)
+    _need(name, rows, rows.dtype, (T * K, H), dev, grad=True)
+    if weights is not None:
+        _need("weights", weights, torch.float32, (T, K), dev, grad=True)
+    _sort_plan(max(T, 1), H, E, K, el)
+    return dims, H, dev
+
+
+def combine_tokens(rows, order, weights=None, *, stream=None):
+    """mm_combine_tokens: y [T,H] = the weighted sum of every token's rows (bf16, float16 or float32 [T*K,H], sorted by
+    ``order``; weights float32 [T,K], None: 1), in float32 in the order of k, rounded once.  Differentiable with respect
+    to rows and weights; the gradients are ``combine_backward(dy, rows, order, weights)``."""
+    dims, _, dev = _combine_args("rows", rows, order, weights)
+    with _stream_of(dev, stream):
+        if _records(rows, weights):
+            return _CombineFunction.apply(rows, weights, order, dims)
+        return _combine(rows, order, weights, *dims)
+
+
+def combine_backward(dy, rows, order, weights, *, stream=None):
+    """mm_combine_backward: (drows [T*K,H], dweights float32 [T,K]) of combine_tokens for y's gradient dy [T,H], as its
+    autograd computes them; for steps that are captured into a graph."""
+    if weights is None:
+        raise ValueError("weights: needed (without weights the gradient is sort_rows(dy, order))")
+    dims, H, dev = _combine_args("rows", rows, order, weights)
+    for name, t in (("rows", rows), ("weights", weights)):
+        _need(name, t, t.dtype, t.shape, dev)
+    _need("dy", dy, rows.dtype, (dims[0], H), dev)
+    with _stream_of(dev, stream):
+        return _combine_backward(dy, rows, order, weights, *dims, True, True)
