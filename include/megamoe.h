@@ -650,6 +650,33 @@ mm_status mm_combine_backward(const mm_sort_plan* plan, const void* dy, const vo
                               const int32_t* row_of_route, const float* weights, void* drows, float* dweights,
                               void* stream);
 
+/*
+ * ------------------------------------------- activation, kept in 8 bits
+ * mm_swiglu -- a = SiLU(h[:, :I]) * h[:, I:], both halves clamped to
+ * [-activation_clamp, activation_clamp] first if clamp_activation is 1 (as in
+ * mm_problem); computed in float32, rounded once.  With codes, also the copy
+ * of h that the gradient takes: each half of a row in groups of 128 values
+ * from its start (the last one may be shorter), scale = max(max|group| / 127,
+ * 1e-8), code = h / scale rounded half to even, both decided in IEEE float32;
+ * h is kept as it was before the clamp.  A group with a NaN or an infinity has
+ * such a scale and reads back as NaN.
+ *   rows, cols   M in [1, 2^24], I in [1, 2^20], M * ceil(I/128) below 2^31
+ *   element      mm_element of h, a, da, dh (not MM_ELEMENT_8BIT)
+ *   h            device [M][2I]
+ *   a            device [M][I] out; must not overlap h
+ *   codes        device int8 [M][2I] out, or NULL: nothing is kept
+ *   scales       device f32 [M][2*ceil(I/128)] out (gate groups, then up
+ *                groups), or NULL with codes
+ * mm_swiglu_backward -- h's gradient dh [M][2I] from a's (da [M][I]) at the
+ * values that codes and scales stand for (code * scale in float32): 0 where
+ * such a value is outside the clamp's interval.
+ */
+mm_status mm_swiglu(int64_t rows, int64_t cols, int32_t element, const void* h, int32_t clamp_activation,
+                    float activation_clamp, void* a, int8_t* codes, float* scales, void* stream);
+mm_status mm_swiglu_backward(int64_t rows, int64_t cols, int32_t element, const void* da, const int8_t* codes,
+                             const float* scales, int32_t clamp_activation, float activation_clamp, void* dh,
+                             void* stream);
+
 /* Kernel timing (diagnostics).  While enabled, every kernel the library
  * launches is bracketed by two HIP events on its stream; mm_trace_collect
  * waits for them and returns, per kernel id, the number of launches and
@@ -662,7 +689,8 @@ typedef enum mm_kernel_id {
   MM_K_BLOCK_QUANTIZE = 14, MM_K_BLOCK_GEMM = 15,
                                  /* 16: no kernel */
   MM_K_SORT_ORDER = 17, MM_K_SORT_ROWS = 18, MM_K_COMBINE_TOKENS = 19, MM_K_COMBINE_BACKWARD = 20,
-  MM_K_COUNT_IDS = 21
+  MM_K_SWIGLU = 21, MM_K_SWIGLU_BACKWARD = 22,
+  MM_K_COUNT_IDS = 23
 } mm_kernel_id;
 
 mm_status mm_trace_enable(int on);

@@ -18,7 +18,7 @@ from . import _build
 MM_A16W16, MM_A8W8_FP8, MM_A8W8_INT8, MM_MXFP8, MM_MXFP4 = 0, 1, 2, 3, 4
 MM_OUT_BF16, MM_OUT_F32 = 0, 1
 USECASE = {"bf16": MM_A16W16, "fp8": MM_A8W8_FP8, "int8": MM_A8W8_INT8, "mxfp8": MM_MXFP8, "mxfp4": MM_MXFP4}
-KERNEL_IDS = 21
+KERNEL_IDS = 23
 MM_ROUTER_SOFTMAX, MM_ROUTER_SIGMOID = 0, 1
 SCORING = {"softmax": MM_ROUTER_SOFTMAX, "sigmoid": MM_ROUTER_SIGMOID}
 MM_FEW_BF16, MM_FEW_FP8, MM_FEW_FP8_BLOCK = 0, 1, 2
@@ -159,6 +159,7 @@ EXPORTS = [
     "mm_router_plan_create", "mm_router", "mm_few_plan_create", "mm_moe_few", "mm_block_quantize",
     "mm_block_plan_create", "mm_block_gemm", "mm_block_linear",
     "mm_sort_plan_create", "mm_sort_tokens", "mm_sort_rows", "mm_combine_tokens", "mm_combine_backward",
+    "mm_swiglu", "mm_swiglu_backward",
 ]
 
 _lib = None
@@ -211,6 +212,9 @@ def load() -> ctypes.CDLL:
     lib.mm_sort_rows.argtypes = [SP, vp, i32p, i32p, vp, vp]
     lib.mm_combine_tokens.argtypes = [SP, vp, i32p, f32p, vp, vp]
     lib.mm_combine_backward.argtypes = [SP, vp, vp, i32p, i32p, f32p, vp, f32p, vp]
+    i32, f32 = ctypes.c_int32, ctypes.c_float
+    lib.mm_swiglu.argtypes = [i64, i64, i32, vp, i32, f32, vp, vp, f32p, vp]
+    lib.mm_swiglu_backward.argtypes = [i64, i64, i32, vp, vp, f32p, i32, f32, vp, vp]
     lib.mm_trace_enable.argtypes = [ctypes.c_int]
     lib.mm_trace_collect.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double)]
     lib.mm_kernel_name.argtypes = [ctypes.c_int]
@@ -393,6 +397,20 @@ def mm_combine_backward(plan, dy, rows, offsets, row_of_route, weights, drows, d
     _check("mm_combine_backward", load().mm_combine_backward(
         ctypes.byref(plan), _ptr(dy), _ptr(rows), _ptr(offsets), _ptr(row_of_route), _ptr(weights), _ptr(drows),
         _ptr(dweights), _stream(stream)))
+
+
+def _clamp(activation_clamp):
+    return (0, 0.0) if activation_clamp is None else (1, activation_clamp)
+
+
+def mm_swiglu(rows, cols, element, h, activation_clamp, a, codes, scales, stream=None):
+    _check("mm_swiglu", load().mm_swiglu(rows, cols, element, _ptr(h), *_clamp(activation_clamp), _ptr(a), _ptr(codes),
+                                         _ptr(scales), _stream(stream)))
+
+
+def mm_swiglu_backward(rows, cols, element, da, codes, scales, activation_clamp, dh, stream=None):
+    _check("mm_swiglu_backward", load().mm_swiglu_backward(
+        rows, cols, element, _ptr(da), _ptr(codes), _ptr(scales), *_clamp(activation_clamp), _ptr(dh), _stream(stream)))
 
 
 def mm_read_device_error(plan, workspace, stream=None) -> int:

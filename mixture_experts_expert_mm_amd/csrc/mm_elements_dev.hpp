@@ -1,0 +1,65 @@
+// Values of the element types (bf16, float16, float32) as float32, and codes
+// of 8 bits with a scale.
+#pragma once
+#include "mm_device.hpp"
+
+namespace mm {
+namespace {
+
+template <int V> struct Bytes;
+template <> struct Bytes<16> { typedef u32x4 type; };
+template <> struct Bytes<8> { typedef u32x2 type; };
+template <> struct Bytes<4> { typedef uint32_t type; };
+template <> struct Bytes<2> { typedef uint16_t type; };
+template <> struct Bytes<1> { typedef uint8_t type; };
+
+// N values of an element type as float32, and back with one rounding
+template <typename E, int N>
+struct Elems {
+  typedef typename Bytes<sizeof(E) * N>::type vec;
+  static __device__ __forceinline__ void load(const void* p, float (&f)[N]) {
+    union { vec v; E e[N]; } u;
+    u.v = *reinterpret_cast<const vec*>(p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = (float)u.e[i];
+  }
+  static __device__ __forceinline__ void store(void* p, const float (&f)[N]) {
+    union { vec v; E e[N]; } u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) u.e[i] = (E)f[i];
+    *reinterpret_cast<vec*>(p) = u.v;
+  }
+};
+
+// Largest magnitude so far, as float bits: integer order is magnitude order,
+// and a NaN is above infinity.
+__device__ __forceinline__ uint32_t amax_of(float v, uint32_t m) {
+  const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+  return b > m ? b : m;
+}
+
+// Scale and code of symmetric 8-bit integers, decided in IEEE float32.  With a
+// NaN or an infinity among the values the scale is one too, codes are 0, and
+// code * scale is NaN.
+__device__ __forceinline__ float int8_scale(uint32_t amax) {
+  const float s = __uint_as_float(amax) / 127.0f;
+  return s < 1e-8f ? 1e-8f : s;        // NaN stays
+}
+__device__ __forceinline__ int int8_code(float v, float s) {
+  const float q = __builtin_rintf(v / s);
+  return q >= -127.0f ? (int)(q > 127.0f ? 127.0f : q) : q < -127.0f ? -127 : 0;
+}
+__device__ __forceinline__ u32x2 int8_codes(const float (&v)[8], float s) {
+  u32x2 o;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= (uint32_t)(int8_code(v[4 * h + i], s) & 0xff) << (8 * i);
+    o[h] = w;
+  }
+  return o;
+}
+
+}  // namespace
+}  // namespace mm

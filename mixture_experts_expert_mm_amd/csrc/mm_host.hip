@@ -490,6 +490,18 @@ CombineTokensArgs combine_tokens_args(const mm_sort_problem& p, const void* rows
   return a;
 }
 
+mm_status swiglu_args(int64_t rows, int64_t cols, int32_t element, int32_t clamp_on, float clamp, SwigluArgs& a) {
+  if (element < MM_ELEMENT_BF16 || element >= MM_ELEMENT_8BIT) return MM_ERR_UNSUPPORTED;
+  if (rows < 1 || rows > (1 << 24) || cols < 1 || cols > (1 << 20)) return MM_ERR_INVALID_ARG;
+  if ((clamp_on != 0 && clamp_on != 1) || (clamp_on && !(clamp >= 0.0f))) return MM_ERR_INVALID_ARG;
+  a.groups = rows * ((cols + 127) / 128);
+  if (a.groups >= ((int64_t)1 << 31)) return MM_ERR_INVALID_ARG;
+  a.I = (int)cols;
+  a.element = element;
+  a.clamp = clamp_on ? clamp : INFINITY;
+  return MM_OK;
+}
+
 // ---------------------------------------------------------------- static scratch
 // The workspace of mega_moe_noalloc: a device array of the library itself,
 // one copy per GPU, held until the process ends.  Host code never passes
@@ -1088,6 +1100,34 @@ mm_status mm_combine_backward(const mm_sort_plan* plan, const void* dy, const vo
   return run(MM_K_COMBINE_BACKWARD, s, [&] { return launch_combine_backward(a, s); });
 }
 
+// ------------------------------------------------ activation, kept in 8 bits
+mm_status mm_swiglu(int64_t rows, int64_t cols, int32_t element, const void* h, int32_t clamp_activation,
+                    float activation_clamp, void* a, int8_t* codes, float* scales, void* stream) {
+  SwigluArgs g{};
+  MM_TRY(swiglu_args(rows, cols, element, clamp_activation, activation_clamp, g));
+  if (!ok16(h) || !ok16(a) || !aligned(codes, 16) || !aligned(scales, 4) || !codes != !scales) return MM_ERR_INVALID_ARG;
+  g.h = h;
+  g.a = a;
+  g.q = codes;
+  g.s = scales;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return run(MM_K_SWIGLU, s, [&] { return launch_swiglu(g, s); });
+}
+
+mm_status mm_swiglu_backward(int64_t rows, int64_t cols, int32_t element, const void* da, const int8_t* codes,
+                             const float* scales, int32_t clamp_activation, float activation_clamp, void* dh,
+                             void* stream) {
+  SwigluArgs g{};
+  MM_TRY(swiglu_args(rows, cols, element, clamp_activation, activation_clamp, g));
+  if (!ok16(da) || !ok16(codes) || !ok4(scales) || !ok16(dh)) return MM_ERR_INVALID_ARG;
+  g.da = da;
+  g.q = const_cast<int8_t*>(codes);
+  g.s = const_cast<float*>(scales);
+  g.dh = dh;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return run(MM_K_SWIGLU_BACKWARD, s, [&] { return launch_swiglu_backward(g, s); });
+}
+
 mm_status mm_trace_enable(int on) {
   std::lock_guard<std::mutex> g(g_trace_mu);
   g_trace_on = on != 0;
@@ -1128,7 +1168,8 @@ const char* mm_kernel_name(int id) {
                                 "requant", "l2_gate", "combine", "prepare", "mega",
                                 "router", "router_select", "few_l1", "few_l2",
                                 "block_quantize", "block_gemm", "unknown",
-                                "sort_order", "sort_rows", "combine_tokens", "combine_backward"};
+                                "sort_order", "sort_rows", "combine_tokens", "combine_backward",
+                                "swiglu", "swiglu_backward"};
   if (id < 0 || id >= MM_K_COUNT_IDS) return "unknown";
   return names[id];
 }

@@ -1,6 +1,6 @@
 // Internal interfaces of the router, the few-token layer, the block-scaled
-// product and the token sort (mm_router.hip, mm_few.hip, mm_block.hip,
-// mm_sort.hip).
+// product, the token sort and the activation (mm_router.hip, mm_few.hip,
+// mm_block.hip, mm_sort.hip, mm_swiglu.hip).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -115,5 +115,20 @@ struct CombineTokensArgs {
 };
 hipError_t launch_combine_tokens(const CombineTokensArgs& a, hipStream_t s);
 hipError_t launch_combine_backward(const CombineTokensArgs& a, hipStream_t s);
+
+// -------------------------------------------------------------- activation
+struct SwigluArgs {
+  const void* h;             // [M][2I]
+  void* a;                   // [M][I]
+  int8_t* q;                 // [M][2I] codes of h, or null
+  float* s;                  // [M][2][ceil(I/128)]
+  const void* da;            // [M][I] (backward)
+  void* dh;                  // [M][2I] (backward)
+  int64_t groups;            // M * ceil(I/128), below 2^31
+  int I, element;
+  float clamp;               // +inf: none
+};
+hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s);
+hipError_t launch_swiglu_backward(const SwigluArgs& a, hipStream_t s);
 
 }  // namespace mm

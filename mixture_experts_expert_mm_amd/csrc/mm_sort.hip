@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "mm_device.hpp"
+#include "mm_elements_dev.hpp"
 #include "mm_ops_internal.hpp"
 
 namespace mm {
@@ -22,13 +23,6 @@ constexpr int kThreads = 256;
 constexpr int kPlaceThreads = 1024;
 constexpr int kMaxTopk = 64;
 constexpr int kMost = 8;             // slots of a token that are in flight together
-
-template <int V> struct Bytes;
-template <> struct Bytes<16> { typedef u32x4 type; };
-template <> struct Bytes<8> { typedef u32x2 type; };
-template <> struct Bytes<4> { typedef uint32_t type; };
-template <> struct Bytes<2> { typedef uint16_t type; };
-template <> struct Bytes<1> { typedef uint8_t type; };
 
 __device__ __forceinline__ int key_of(const SortArgs& a, int64_t r) {
   const int e = a.ids[r];
@@ -254,28 +248,6 @@ __global__ __launch_bounds__(kThreads) void k_sort_rows(SortArgs a) {
       for (int64_t c = s.c; c < chunks; c += s.cx) *reinterpret_cast<vec*>(a.rows + p * a.row_bytes + c * V) = vec{};
   }
 }
-
-namespace {
-
-// N values of an element type as float32, and back with one rounding
-template <typename E, int N>
-struct Elems {
-  typedef typename Bytes<sizeof(E) * N>::type vec;
-  static __device__ __forceinline__ void load(const void* p, float (&f)[N]) {
-    union { vec v; E e[N]; } u;
-    u.v = *reinterpret_cast<const vec*>(p);
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = (float)u.e[i];
-  }
-  static __device__ __forceinline__ void store(void* p, const float (&f)[N]) {
-    union { vec v; E e[N]; } u;
-#pragma unroll
-    for (int i = 0; i < N; ++i) u.e[i] = (E)f[i];
-    *reinterpret_cast<vec*>(p) = u.v;
-  }
-};
-
-}  // namespace
 
 // y[t] = sum_k w[t][k] * rows[row_of_route[t][k]] in float32, in the order of k,
 // eight rows in flight.

@@ -5,9 +5,10 @@ workspace, and calls the C-ABI entry points through ``binding``.  The
 functions ``route``, ``moe_few``, ``block_quantize``, ``block_matmul`` and
 ``block_linear`` hold nothing: each checks its tensors, allocates the
 outputs and a workspace on the calling stream and makes one call.  So do
-``sort_tokens``, ``sort_rows``, ``combine_tokens`` and ``combine_backward``;
-the first three are differentiable.  Nothing here computes any part of the
-expert path.
+``sort_tokens``, ``sort_rows``, ``combine_tokens``, ``combine_backward``,
+``swiglu``, ``swiglu_forward`` and ``swiglu_backward``; sort_tokens, sort_rows,
+combine_tokens and swiglu are differentiable.  Nothing here computes any part
+of the expert path.
 """
 
 from __future__ import annotations
@@ -610,3 +611,86 @@ def combine_backward(dy, rows, order, weights, *, stream=None):
     _need("dy", dy, rows.dtype, (dims[0], H), dev)
     with _stream_of(dev, stream):
         return _combine_backward(dy, rows, order, weights, *dims, True, True)
+
+
+# ------------------------------------------------- activation, kept in 8 bits
+
+def _swiglu_args(h, activation_clamp, grad):
+    M, N, dev = _rows("h", h)
+    el = _element("h", h, True)
+    _need("h", h, h.dtype, (M, N), dev, grad=grad)
+    if N % 2 or N == 0:
+        raise ValueError(f"h: [rows, 2 * intermediate] is needed, got {N} columns")
+    return M, N // 2, dev, el, _clamp_of(activation_clamp)
+
+
+def _clamp_of(activation_clamp):
+    if activation_clamp is None:
+        return None
+    c = float(activation_clamp)
+    if not c >= 0.0:
+        raise ValueError(f"activation_clamp: None or a number from 0 on is needed, got {activation_clamp!r}")
+    return c
+
+
+def _swiglu(h, M, I, el, clamp, keep):
+    dev = h.device
+    a = torch.empty((M, I), dtype=h.dtype, device=dev)
+    q = torch.empty((M, 2 * I), dtype=torch.int8, device=dev) if keep else None
+    s = torch.empty((M, 2 * -(-I // 128)), dtype=torch.float32, device=dev) if keep else None
+    if M:
+        B.mm_swiglu(M, I, el, h, clamp, a, q, s, _raw_stream(dev))
+    return a, q, s
+
+
+def _swiglu_backward(da, q, s, clamp):
+    M, I = da.shape
+    dh = torch.empty((M, 2 * I), dtype=da.dtype, device=da.device)
+    if M:
+        B.mm_swiglu_backward(M, I, B.ELEMENT[da.dtype], da, q, s, clamp, dh, _raw_stream(da.device))
+    return dh
+
+
+class _SwigluFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, M, I, el, clamp):
+        a, q, s = _swiglu(h, M, I, el, clamp, True)
+        ctx.clamp = clamp
+        ctx.save_for_backward(q, s)
+        return a
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, da):
+        _not_captured()
+        return _swiglu_backward(_dense(da), *ctx.saved_tensors, ctx.clamp), None, None, None, None
+
+
+def swiglu(h, *, activation_clamp=None, stream=None):
+    """mm_swiglu: a [M,I] = SiLU(h[:, :I]) * h[:, I:] of h [M,2I] (bf16, float16 or float32), both halves clamped to
+    [-activation_clamp, activation_clamp] first unless that is None.  Differentiable: what it keeps for the backward
+    pass is h in 8 bits, with a float32 scale per 128 values, and the gradient is that at the kept values."""
+    M, I, dev, el, clamp = _swiglu_args(h, activation_clamp, True)
+    with _stream_of(dev, stream):
+        if _records(h):
+            return _SwigluFunction.apply(h, M, I, el, clamp)
+        return _swiglu(h, M, I, el, clamp, False)[0]
+
+
+def swiglu_forward(h, *, activation_clamp=None, stream=None):
+    """(a, codes int8 [M,2I], scales float32 [M,2*ceil(I/128)]): swiglu and the copy of h that swiglu_backward takes."""
+    M, I, dev, el, clamp = _swiglu_args(h, activation_clamp, False)
+    with _stream_of(dev, stream):
+        return _swiglu(h, M, I, el, clamp, True)
+
+
+def swiglu_backward(da, codes, scales, *, activation_clamp=None, stream=None):
+    """mm_swiglu_backward: h's gradient [M,2I] from a's [M,I] and what swiglu_forward kept."""
+    M, I, dev = _rows("da", da)
+    _element("da", da, True)
+    _need("da", da, da.dtype, (M, I), dev)
+    _need("codes", codes, torch.int8, (M, 2 * I), dev)
+    _need("scales", scales, torch.float32, (M, 2 * -(-I // 128)), dev)
+    clamp = _clamp_of(activation_clamp)
+    with _stream_of(dev, stream):
+        return _swiglu_backward(da, codes, scales, clamp)
