@@ -677,6 +677,66 @@ mm_status mm_swiglu_backward(int64_t rows, int64_t cols, int32_t element, const 
                              const float* scales, int32_t clamp_activation, float activation_clamp, void* dh,
                              void* stream);
 
+/*
+ * ------------------------------------------------- 8-bit integer product
+ * mm_int8_quantize -- the A8W8-INT rule for rows of any floating type, of x
+ * or of a weight [N][K]: scale = max(max|row| / 127, 1e-8), code = x / scale
+ * rounded half to even, in [-127, 127], both decided in IEEE float32.  A row
+ * with a NaN or an infinity has such a scale and codes of 0: its products are
+ * NaN.
+ *   rows, cols   in [1, 2^24]; a multiple of 16 up to 131056
+ *   element      mm_element of x (not MM_ELEMENT_8BIT)
+ *   x            device [rows][cols]
+ *   codes        device int8 [rows][cols] out
+ *   scales       device f32 [rows] out
+ */
+mm_status mm_int8_quantize(int64_t rows, int64_t cols, int32_t element, const void* x, int8_t* codes, float* scales,
+                           void* stream);
+
+/*
+ * mm_int8_gemm -- y[m][n] = sum_k a[m][k] * b[n][k] * b_scale[n] * a_scale[m]:
+ * the sum is exact (int32; codes may be -128 too), becomes float32, is scaled
+ * by b_scale, then by a_scale, and is rounded once to y's type.  One matrix, or
+ * groups of rows with a matrix each, as in mm_block_gemm: rows of y that no
+ * group covers are left as they are; the part of a group outside [0, rows) is
+ * ignored; groups must not overlap.
+ * mm_int8_linear -- the same from floating rows: mm_int8_quantize, then the
+ * product, with the same result bit for bit.
+ */
+typedef struct mm_int8_problem {
+  int64_t rows;          /* M in [1, 2^24] */
+  int64_t out_features;  /* N in [1, 2^20] */
+  int64_t in_features;   /* K, multiple of 16 up to 131056 */
+  int64_t num_groups;    /* G in [1, 1024] */
+  int32_t x_element;     /* mm_element of mm_int8_linear's x */
+  int32_t y_element;     /* mm_element of y (neither MM_ELEMENT_8BIT) */
+} mm_int8_problem;
+
+typedef struct mm_int8_plan {
+  mm_int8_problem prob;
+  int64_t workspace_bytes;   /* of mm_int8_linear (codes and scales of the rows) */
+  uint64_t checksum;
+  int64_t reserved[4];
+} mm_int8_plan;
+
+mm_status mm_int8_plan_create(const mm_int8_problem* problem, mm_int8_plan* plan);
+
+/*
+ *   a              device int8 [M][K]
+ *   a_scale        device f32 [M]
+ *   x              device [M][K] of x_element
+ *   b              device int8 [G][N][K]
+ *   b_scale        device f32 [G][N]
+ *   group_offsets, group_counts  as in mm_block_gemm
+ *   y              device [M][N] of y_element out; must not overlap an input
+ */
+mm_status mm_int8_gemm(const mm_int8_plan* plan, const int8_t* a, const float* a_scale, const int8_t* b,
+                       const float* b_scale, const int32_t* group_offsets, const int32_t* group_counts, void* y,
+                       void* stream);
+mm_status mm_int8_linear(const mm_int8_plan* plan, const void* x, const int8_t* b, const float* b_scale,
+                         const int32_t* group_offsets, const int32_t* group_counts, void* y, void* workspace,
+                         uint64_t workspace_bytes, void* stream);
+
 /* Kernel timing (diagnostics).  While enabled, every kernel the library
  * launches is bracketed by two HIP events on its stream; mm_trace_collect
  * waits for them and returns, per kernel id, the number of launches and
@@ -690,7 +750,8 @@ typedef enum mm_kernel_id {
                                  /* 16: no kernel */
   MM_K_SORT_ORDER = 17, MM_K_SORT_ROWS = 18, MM_K_COMBINE_TOKENS = 19, MM_K_COMBINE_BACKWARD = 20,
   MM_K_SWIGLU = 21, MM_K_SWIGLU_BACKWARD = 22,
-  MM_K_COUNT_IDS = 23
+  MM_K_INT8_QUANTIZE = 23, MM_K_INT8_GEMM = 24,
+  MM_K_COUNT_IDS = 25
 } mm_kernel_id;
 
 mm_status mm_trace_enable(int on);

@@ -18,7 +18,7 @@ from . import _build
 MM_A16W16, MM_A8W8_FP8, MM_A8W8_INT8, MM_MXFP8, MM_MXFP4 = 0, 1, 2, 3, 4
 MM_OUT_BF16, MM_OUT_F32 = 0, 1
 USECASE = {"bf16": MM_A16W16, "fp8": MM_A8W8_FP8, "int8": MM_A8W8_INT8, "mxfp8": MM_MXFP8, "mxfp4": MM_MXFP4}
-KERNEL_IDS = 23
+KERNEL_IDS = 25
 MM_ROUTER_SOFTMAX, MM_ROUTER_SIGMOID = 0, 1
 SCORING = {"softmax": MM_ROUTER_SOFTMAX, "sigmoid": MM_ROUTER_SIGMOID}
 MM_FEW_BF16, MM_FEW_FP8, MM_FEW_FP8_BLOCK = 0, 1, 2
@@ -152,6 +152,26 @@ class MMSortPlan(ctypes.Structure):
     ]
 
 
+class MMInt8Problem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("out_features", ctypes.c_int64),
+        ("in_features", ctypes.c_int64),
+        ("num_groups", ctypes.c_int64),
+        ("x_element", ctypes.c_int32),
+        ("y_element", ctypes.c_int32),
+    ]
+
+
+class MMInt8Plan(ctypes.Structure):
+    _fields_ = [
+        ("prob", MMInt8Problem),
+        ("workspace_bytes", ctypes.c_int64),
+        ("checksum", ctypes.c_uint64),
+        ("reserved", ctypes.c_int64 * 4),
+    ]
+
+
 EXPORTS = [
     "mm_plan_create", "mm_prepare_weights", "mm_dispatch_layout", "mm_grouped_l1_swiglu",
     "mm_grouped_l2_combine", "mega_moe", "mega_moe_noalloc", "mm_read_device_error", "mm_debug_raw_accumulators",
@@ -160,6 +180,7 @@ EXPORTS = [
     "mm_block_plan_create", "mm_block_gemm", "mm_block_linear",
     "mm_sort_plan_create", "mm_sort_tokens", "mm_sort_rows", "mm_combine_tokens", "mm_combine_backward",
     "mm_swiglu", "mm_swiglu_backward",
+    "mm_int8_quantize", "mm_int8_plan_create", "mm_int8_gemm", "mm_int8_linear",
 ]
 
 _lib = None
@@ -215,6 +236,11 @@ def load() -> ctypes.CDLL:
     i32, f32 = ctypes.c_int32, ctypes.c_float
     lib.mm_swiglu.argtypes = [i64, i64, i32, vp, i32, f32, vp, vp, f32p, vp]
     lib.mm_swiglu_backward.argtypes = [i64, i64, i32, vp, vp, f32p, i32, f32, vp, vp]
+    IP = ctypes.POINTER(MMInt8Plan)
+    lib.mm_int8_quantize.argtypes = [i64, i64, i32, vp, vp, f32p, vp]
+    lib.mm_int8_plan_create.argtypes = [ctypes.POINTER(MMInt8Problem), IP]
+    lib.mm_int8_gemm.argtypes = [IP, vp, f32p, vp, f32p, i32p, i32p, vp, vp]
+    lib.mm_int8_linear.argtypes = [IP, vp, vp, f32p, i32p, i32p, vp, vp, u64, vp]
     lib.mm_trace_enable.argtypes = [ctypes.c_int]
     lib.mm_trace_collect.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double)]
     lib.mm_kernel_name.argtypes = [ctypes.c_int]
@@ -411,6 +437,30 @@ def mm_swiglu(rows, cols, element, h, activation_clamp, a, codes, scales, stream
 def mm_swiglu_backward(rows, cols, element, da, codes, scales, activation_clamp, dh, stream=None):
     _check("mm_swiglu_backward", load().mm_swiglu_backward(
         rows, cols, element, _ptr(da), _ptr(codes), _ptr(scales), *_clamp(activation_clamp), _ptr(dh), _stream(stream)))
+
+
+def mm_int8_quantize(rows, cols, element, x, codes, scales, stream=None):
+    _check("mm_int8_quantize", load().mm_int8_quantize(rows, cols, element, _ptr(x), _ptr(codes), _ptr(scales),
+                                                       _stream(stream)))
+
+
+def mm_int8_plan_create(M, N, K, G=1, x_element=MM_ELEMENT_BF16, y_element=MM_ELEMENT_BF16) -> MMInt8Plan:
+    prob = MMInt8Problem(M, N, K, G, x_element, y_element)
+    plan = MMInt8Plan()
+    _check("mm_int8_plan_create", load().mm_int8_plan_create(ctypes.byref(prob), ctypes.byref(plan)))
+    return plan
+
+
+def mm_int8_gemm(plan, a, a_scale, b, b_scale, group_offsets, group_counts, y, stream=None):
+    _check("mm_int8_gemm", load().mm_int8_gemm(
+        ctypes.byref(plan), _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(group_offsets), _ptr(group_counts),
+        _ptr(y), _stream(stream)))
+
+
+def mm_int8_linear(plan, x, b, b_scale, group_offsets, group_counts, y, workspace, stream=None):
+    _check("mm_int8_linear", load().mm_int8_linear(
+        ctypes.byref(plan), _ptr(x), _ptr(b), _ptr(b_scale), _ptr(group_offsets), _ptr(group_counts), _ptr(y),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def mm_read_device_error(plan, workspace, stream=None) -> int:

@@ -31,6 +31,30 @@ struct Elems {
   }
 };
 
+// eight neighbours, at an address of their own size
+template <typename E>
+__device__ __forceinline__ void load_elems(const E* p, float (&f)[8]) {
+  if constexpr (sizeof(E) == 2) {
+    Elems<E, 8>::load(p, f);
+  } else {
+    float a[4], b[4];
+    Elems<E, 4>::load(p, a);
+    Elems<E, 4>::load(p + 4, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
+  }
+}
+template <typename E>
+__device__ __forceinline__ void store_elems(E* p, const float (&f)[8]) {
+  if constexpr (sizeof(E) == 2) {
+    Elems<E, 8>::store(p, f);
+  } else {
+    const float a[4] = {f[0], f[1], f[2], f[3]}, b[4] = {f[4], f[5], f[6], f[7]};
+    Elems<E, 4>::store(p, a);
+    Elems<E, 4>::store(p + 4, b);
+  }
+}
+
 // Largest magnitude so far, as float bits: integer order is magnitude order,
 // and a NaN is above infinity.
 __device__ __forceinline__ uint32_t amax_of(float v, uint32_t m) {

@@ -445,8 +445,12 @@ mm_status do_l2(const mm_plan& pl, const int32_t* offsets, const int32_t* counts
 bool ok16(const void* p) { return p && aligned(p, 16); }
 bool ok4(const void* p) { return p && aligned(p, 4); }
 
+// most K-values of an 8-bit integer product: 131056 * 128 * 128 < 2^31
+constexpr int64_t kInt8MaxCols = 131056;
+
 // both group arrays or, for one group, neither
-bool block_groups_ok(const mm_block_problem& p, const int32_t* offsets, const int32_t* counts) {
+template <typename Problem>
+bool block_groups_ok(const Problem& p, const int32_t* offsets, const int32_t* counts) {
   return aligned(offsets, 4) && aligned(counts, 4) && !offsets == !counts && (offsets || p.num_groups == 1);
 }
 
@@ -500,6 +504,23 @@ mm_status swiglu_args(int64_t rows, int64_t cols, int32_t element, int32_t clamp
   a.element = element;
   a.clamp = clamp_on ? clamp : INFINITY;
   return MM_OK;
+}
+
+Int8Args int8_args(const mm_int8_problem& p, const int8_t* b, const float* b_scale, const int32_t* offsets,
+                   const int32_t* counts, void* y) {
+  Int8Args g{};
+  g.b = reinterpret_cast<const uint8_t*>(b);
+  g.bs = b_scale;
+  g.offsets = offsets;
+  g.counts = counts;
+  g.y = y;
+  g.M = p.rows;
+  g.N = (int)p.out_features;
+  g.K = (int)p.in_features;
+  g.G = (int)p.num_groups;
+  g.x_element = p.x_element;
+  g.y_element = p.y_element;
+  return g;
 }
 
 // ---------------------------------------------------------------- static scratch
@@ -1128,6 +1149,70 @@ mm_status mm_swiglu_backward(int64_t rows, int64_t cols, int32_t element, const 
   return run(MM_K_SWIGLU_BACKWARD, s, [&] { return launch_swiglu_backward(g, s); });
 }
 
+// ------------------------------------------------- 8-bit integer product
+mm_status mm_int8_quantize(int64_t rows, int64_t cols, int32_t element, const void* x, int8_t* codes, float* scales,
+                           void* stream) {
+  if (element < MM_ELEMENT_BF16 || element >= MM_ELEMENT_8BIT) return MM_ERR_UNSUPPORTED;
+  if (rows < 1 || rows > (1 << 24) || cols < 16 || cols > kInt8MaxCols || cols % 16) return MM_ERR_INVALID_ARG;
+  if (!ok16(x) || !ok16(codes) || !ok4(scales)) return MM_ERR_INVALID_ARG;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return run(MM_K_INT8_QUANTIZE, s, [&] {
+    return launch_int8_quantize(x, element, rows, (int)cols, reinterpret_cast<uint8_t*>(codes), scales, s);
+  });
+}
+
+mm_status mm_int8_plan_create(const mm_int8_problem* problem, mm_int8_plan* plan) {
+  if (!problem || !plan) return MM_ERR_INVALID_ARG;
+  const mm_int8_problem p = *problem;
+  for (const int32_t e : {p.x_element, p.y_element})
+    if (e < MM_ELEMENT_BF16 || e >= MM_ELEMENT_8BIT) return MM_ERR_UNSUPPORTED;
+  if (p.rows < 1 || p.rows > (1 << 24) || p.out_features < 1 || p.out_features > (1 << 20)) return MM_ERR_INVALID_ARG;
+  if (p.in_features < 16 || p.in_features > kInt8MaxCols || p.in_features % 16) return MM_ERR_INVALID_ARG;
+  if (p.num_groups < 1 || p.num_groups > 1024) return MM_ERR_INVALID_ARG;
+  mm_int8_plan pl;
+  std::memset(&pl, 0, sizeof(pl));
+  pl.prob = p;
+  pl.workspace_bytes = align_up(p.rows * p.in_features, kAlign) + align_up(p.rows * 4, kAlign);
+  pl.checksum = plan_checksum(&pl);
+  *plan = pl;
+  return MM_OK;
+}
+
+mm_status mm_int8_gemm(const mm_int8_plan* plan, const int8_t* a, const float* a_scale, const int8_t* b,
+                       const float* b_scale, const int32_t* group_offsets, const int32_t* group_counts, void* y,
+                       void* stream) {
+  MM_TRY(check_plan(plan));
+  if (!ok16(a) || !ok4(a_scale) || !ok16(b) || !ok4(b_scale) || !ok16(y)) return MM_ERR_INVALID_ARG;
+  if (!block_groups_ok(plan->prob, group_offsets, group_counts)) return MM_ERR_INVALID_ARG;
+  Int8Args g = int8_args(plan->prob, b, b_scale, group_offsets, group_counts, y);
+  g.a = reinterpret_cast<const uint8_t*>(a);
+  g.as = a_scale;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return run(MM_K_INT8_GEMM, s, [&] { return launch_int8_gemm(g, num_cus(), s); });
+}
+
+mm_status mm_int8_linear(const mm_int8_plan* plan, const void* x, const int8_t* b, const float* b_scale,
+                         const int32_t* group_offsets, const int32_t* group_counts, void* y, void* workspace,
+                         uint64_t workspace_bytes, void* stream) {
+  MM_TRY(check_plan(plan));
+  const mm_int8_problem& p = plan->prob;
+  if (!ok16(x) || !ok16(b) || !ok4(b_scale) || !ok16(y) || !ok16(workspace)) return MM_ERR_INVALID_ARG;
+  if (!block_groups_ok(p, group_offsets, group_counts)) return MM_ERR_INVALID_ARG;
+  if ((int64_t)workspace_bytes < plan->workspace_bytes) return MM_ERR_WORKSPACE;
+  Int8Args g = int8_args(p, b, b_scale, group_offsets, group_counts, y);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (int8_from_x(g)) {
+    g.x = x;
+  } else {
+    int8_t* codes = at<int8_t>(workspace, 0);
+    float* scales = at<float>(workspace, align_up(p.rows * p.in_features, kAlign));
+    MM_TRY(mm_int8_quantize(p.rows, p.in_features, p.x_element, x, codes, scales, stream));
+    g.a = reinterpret_cast<const uint8_t*>(codes);
+    g.as = scales;
+  }
+  return run(MM_K_INT8_GEMM, s, [&] { return launch_int8_gemm(g, num_cus(), s); });
+}
+
 mm_status mm_trace_enable(int on) {
   std::lock_guard<std::mutex> g(g_trace_mu);
   g_trace_on = on != 0;
@@ -1169,7 +1254,7 @@ const char* mm_kernel_name(int id) {
                                 "router", "router_select", "few_l1", "few_l2",
                                 "block_quantize", "block_gemm", "unknown",
                                 "sort_order", "sort_rows", "combine_tokens", "combine_backward",
-                                "swiglu", "swiglu_backward"};
+                                "swiglu", "swiglu_backward", "int8_quantize", "int8_gemm"};
   if (id < 0 || id >= MM_K_COUNT_IDS) return "unknown";
   return names[id];
 }

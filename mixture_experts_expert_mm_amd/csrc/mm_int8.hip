@@ -1,0 +1,507 @@
+// Products of 8-bit integers with a float32 scale per row of x and per row
+// (output channel) of w, dense or over groups of rows:
+//
+//   y[m][n] = float(sum_k q[m][k] * w[n][k]) * ws[n] * s[m]
+//
+// and the quantiser of the rows:
+//   s[m] = max(max_k|x[m][k]| / 127, 1e-8),  q = round-half-even(x / s), in [-127, 127].
+//
+// The sums are exact (int32, K up to 131056), so tiles, slices of K and the
+// number of rows have no part in a result.
+#include <type_traits>
+
+#include "mm_device.hpp"
+#include "mm_elements_dev.hpp"
+#include "mm_ops_internal.hpp"
+#include "mm_tiles_dev.hpp"
+
+namespace mm {
+
+namespace {
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+constexpr int kStep = 128;           // K-values (bytes) of a row that a part of a stage holds
+constexpr int kFewRows = 16;         // most rows of a streaming unit
+constexpr int kFewCols = 16;
+constexpr uint32_t kOutside = 0x7fffff00u;   // an offset beyond every descriptor: arrives as zeros
+
+// 16 x 16 outputs, 64 K-values: each lane supplies 16 bytes of its A row and B
+// column (lane % 16); element i of lane l is C[4 * (l / 16) + i][l % 16].
+__device__ __forceinline__ void mfma64(i32x4& c, const u32x4& a, const u32x4& b) {
+  c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+// four neighbouring columns n .. n + 3 of a row of y
+template <typename E>
+__device__ __forceinline__ void put4(const Int8Args& a, int64_t row, int n, const float (&v)[4]) {
+  E* y = static_cast<E*>(a.y) + row * a.N + n;
+  if (a.N % 4 == 0) {
+    if (n < a.N) Elems<E, 4>::store(y, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.N) y[i] = (E)v[i];
+  }
+}
+
+__device__ __forceinline__ void scales4(const Int8Args& a, int group, int n, float (&v)[4]) {
+  const float* p = a.bs + (int64_t)group * a.N;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = p[n + i < a.N ? n + i : a.N - 1];
+}
+
+// One tile: WM x WN waves of 16 * MT rows x 16 * NT columns; D stages of LDS,
+// each P parts of 128 K-values, filled by LDS-DMA D - 1 stages ahead.  Weights
+// are the MFMA's A operand, so a lane's four sums are four columns of one row.
+// SPREAD: copies that go out between two column tiles' products (0: all of a
+// stage's before its first product).
+template <typename E, int WM, int WN, int MT, int NT, int D, int P, int SPREAD>
+__device__ __forceinline__ void int8_tile(const Int8Args& a, const TileAt& at, uint8_t* const (&slot)[D]) {
+  constexpr int W = WM * WN, BM = 16 * MT * WM, BN = 16 * NT * WN, kPart = (BM + BN) * kStep;
+  constexpr int kGroups = (BM + BN) / 8, kOfA = BM / 8, kCopies = P * kGroups / W;
+  static_assert(kOfA % W == 0 && kGroups % W == 0 && W % 2 == 0, "a wave's copies are of one operand each");
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));   // nothing derived from it is kept across tiles
+  const TileAt t = uniform_tile(at);
+  const int w = uniform(tid / 64), l = tid % 64, r = l % 16, g = l / 16, wm = w % WM, wn = w / WM;
+  const int KB = (a.K + kStep - 1) / kStep, stages = (KB + P - 1) / P;
+  const int rows = t.rows, cols = a.N - t.n0 < BN ? a.N - t.n0 : BN;
+  // One instruction moves 8 rows of 128 bytes, lane i to byte 16 * i; the chunk
+  // at place p of row x is p ^ (x / 2 % 8), so that 16 rows read at one chunk
+  // hit 16 different bank groups.  Rows past the last one, chunks past K and
+  // stages past the end are beyond the descriptor: zeros without an access.
+  const int chunk = (l % 8) ^ ((4 * (w % 2) + l / 16) % 8);
+  const uint32_t voff = (uint32_t)(l / 8) * a.K + chunk * 16;
+  const uint32_t vlast = chunk * 16 < a.K - (KB - 1) * kStep ? voff : kOutside;
+  const uint8_t *ab = a.a + t.m0 * a.K, *bb = a.b + ((int64_t)t.group * a.N + t.n0) * a.K;
+  auto copy = [&](int i, int s, uint8_t* to) {
+    const int item = W * i, p = item / kGroups, grp = item % kGroups;      // (compile-time), + w
+    const bool of_a = grp < kOfA;
+    const int kb = s * P + p;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(of_a ? ab : bb), (short)0, kb < KB ? (of_a ? rows : cols) * a.K : 0, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(to + p * kPart + (grp + w) * 1024), 16,
+                                             kb + 1 < KB ? voff : vlast, ((of_a ? grp : grp - kOfA) + w) * 8 * a.K + kb * kStep, 0, 0);
+  };
+  const int sw = (r / 2) % 8;
+  const int o0 = (g ^ sw) * 16 + r * kStep, o1 = ((g + 4) ^ sw) * 16 + r * kStep;
+  i32x4 acc[NT][MT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
+  auto turn = [&]() {
+    // the stage's products stay before the wait: nothing else ties them to it
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) asm volatile("" : "+v"(acc[j][i]));
+    __builtin_amdgcn_sched_barrier(0);
+    stage_barrier<(D - 2) * kCopies>();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto stage = [&](int s, const uint8_t* from, uint8_t* to) {
+    int next = 0;
+    if constexpr (SPREAD == 0) {
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) copy(i, s + D - 1, to);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if (P > 1 && s * P + p >= KB) break;
+      const uint8_t *sa = from + p * kPart, *sb = sa + BM * kStep;
+      u32x4 af[MT][2], b[2][2];
+      auto weights = [&](int j) {
+        b[j % 2][0] = *reinterpret_cast<const u32x4*>(sb + (wn * NT + j) * 16 * kStep + o0);
+        b[j % 2][1] = *reinterpret_cast<const u32x4*>(sb + (wn * NT + j) * 16 * kStep + o1);
+      };
+      weights(0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        af[i][0] = *reinterpret_cast<const u32x4*>(sa + (wm * MT + i) * 16 * kStep + o0);
+        af[i][1] = *reinterpret_cast<const u32x4*>(sa + (wm * MT + i) * 16 * kStep + o1);
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        if (j + 1 < NT) weights(j + 1);
+        if constexpr (SPREAD > 0) {
+#pragma unroll
+          for (int c = 0; c < SPREAD; ++c)
+            if (next < kCopies) copy(next++, s + D - 1, to);
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          mfma64(acc[j][i], b[j % 2][0], af[i][0]);
+          mfma64(acc[j][i], b[j % 2][1], af[i][1]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    turn();
+  };
+#pragma unroll
+  for (int u = 0; u < D - 1; ++u)
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) copy(i, u, slot[u]);
+  turn();
+  // (a break inside the loop would be a path on which the compiler sees a slot
+  // filled one stage ago, and waits for it)
+  int s = 0;
+  for (; s + D <= stages; s += D) {
+#pragma unroll
+    for (int u = 0; u < D; ++u) stage(s + u, slot[u], slot[(u + D - 1) % D]);
+  }
+#pragma unroll
+  for (int u = 0; u < D - 1; ++u) {
+    if (s + u >= stages) break;
+    stage(s + u, slot[u], slot[(u + D - 1) % D]);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);              // no copy outlives the tile
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int row = (wm * MT + i) * 16 + r;
+    if (row >= rows) continue;
+    const float sa = a.as[t.m0 + row];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int n = t.n0 + (wn * NT + j) * 16 + 4 * g;
+      float ws[4], v[4];
+      scales4(a, t.group, n, ws);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = (float)acc[j][i][k] * ws[k] * sa;
+      put4<E>(a, t.m0 + row, n, v);
+    }
+  }
+  __syncthreads();      // the next tile of this workgroup writes the stages again
+}
+
+}  // namespace
+
+// Products with many rows: 256 x 256 tiles, and 128 x 256 for a group's rest.
+// One workgroup a CU; XCD x takes an eighth of each class's list (neighbours
+// share an L2), and its workgroups take every n-th tile of it in turn.
+template <typename E>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_mma(Int8Args a) {
+  // separate arrays: the compiler then sees that a stage's reads and the other
+  // stage's copies do not meet, and does not wait for the copies
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[(kBM + kBN) * kStep], s1[(kBM + kBN) * kStep];
+  uint8_t* const slot[2] = {s0, s1};
+  const int x = blockIdx.x % 8, step = gridDim.x / 8;
+  int64_t n[2], first[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int64_t total = count_blocks(a, c) * ((a.N + kBN - 1) / kBN);
+    first[c] = total * x / 8;
+    n[c] = total * (x + 1) / 8 - first[c];
+  }
+  for (int64_t k = blockIdx.x / 8; k < n[0] + n[1]; k += step) {
+    TileAt t;
+    if (k < n[0]) {
+      if (!find_tile(a, kFull, first[0] + k, t)) break;
+      int8_tile<E, 4, 2, 4, 8, 2, 1, 2>(a, t, slot);
+    } else {
+      if (!find_tile(a, kHalf, first[1] + k - n[0], t)) break;
+      int8_tile<E, 4, 2, 2, 8, 2, 1, 2>(a, t, slot);
+    }
+  }
+}
+
+// Products whose large tiles would leave most CUs without one: tiles of class c.
+template <typename E, int C, int WM, int WN, int MT, int NT, int D>
+__global__ __launch_bounds__(64 * WM * WN) void k_int8_ring(Int8Args a) {
+  constexpr int kBytes = 16 * (MT * WM + NT * WN) * kStep * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[kBytes], s1[kBytes], s2[D > 2 ? kBytes : 16], s3[D > 2 ? kBytes : 16];
+  const int x = blockIdx.x % 8, step = gridDim.x / 8;
+  const int64_t total = count_blocks(a, C) * ((a.N + cols_of(C) - 1) / cols_of(C));
+  const int64_t first = total * x / 8, n = total * (x + 1) / 8 - first;
+  for (int64_t k = blockIdx.x / 8; k < n; k += step) {
+    TileAt t;
+    if (!find_tile(a, C, first + k, t)) break;
+    if constexpr (D == 4) {
+      uint8_t* const slot[4] = {s0, s1, s2, s3};
+      int8_tile<E, WM, WN, MT, NT, 4, 2, 0>(a, t, slot);
+    } else {
+      uint8_t* const slot[2] = {s0, s1};
+      int8_tile<E, WM, WN, MT, NT, 2, 2, 2>(a, t, slot);
+    }
+  }
+}
+
+namespace {
+
+constexpr int kRowThreads = 256, kRowWaves = 4, kDeep = 4;
+
+// The weights of 16 columns from memory, `kDeep` steps of 128 K-values in
+// flight a wave, the four waves taking every fourth step; rows from `x` with a
+// pitch.  Returns a wave's sums.
+template <typename Rows>
+__device__ __forceinline__ i32x4 stream_columns(const Int8Args& a, int n0, int w, int l, const Rows& rows) {
+  const int r = l % 16, g = l / 16, KB = (a.K + kStep - 1) / kStep;
+  const uint8_t* bp = a.b + (int64_t)(n0 + r < a.N ? n0 + r : a.N - 1) * a.K;
+  u32x4 b[kDeep][2];
+  // past the end: the last step again, unused (a load under a condition would
+  // make the compiler wait for all of them); past K inside the last step: the
+  // row's first values, which meet zeros
+  auto load = [&](int d, int kb) {
+    kb = kb < KB ? kb : KB - 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = kb * kStep + g * 32 + h * 16;
+      b[d][h] = *reinterpret_cast<const u32x4*>(bp + (k < a.K ? k : 0));
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < kDeep; ++d) load(d, w + d * kRowWaves);
+  rows.bring();
+  i32x4 acc = {0, 0, 0, 0};
+  for (int k0 = w; k0 < KB; k0 += kDeep * kRowWaves) {
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const int kb = k0 + d * kRowWaves;
+      if (kb < KB) {
+        mfma64(acc, b[d][0], rows.at(kb * kStep + g * 32));
+        mfma64(acc, b[d][1], rows.at(kb * kStep + g * 32 + 16));
+      }
+      load(d, kb + kDeep * kRowWaves);
+    }
+  }
+  return acc;
+}
+
+// sums of the four waves, scaled and written
+template <typename E>
+__device__ __forceinline__ void finish_columns(const Int8Args& a, const i32x4& acc, int n0, int64_t m0, int rows, float sa,
+                                               i32x4 (*red)[64]) {
+  const int tid = threadIdx.x, w = tid / 64, l = tid % 64, r = l % 16, g = l / 16;
+  red[w][l] = acc;
+  __syncthreads();
+  if (tid >= 64 || r >= rows) return;
+  const i32x4 sum = red[0][l] + red[1][l] + red[2][l] + red[3][l];
+  float ws[4], v[4];
+  scales4(a, 0, n0 + 4 * g, ws);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = (float)sum[k] * ws[k] * sa;
+  put4<E>(a, m0 + r, n0 + 4 * g, v);
+}
+
+// rows of codes in memory
+struct RowsOfCodes {
+  const uint8_t* p;
+  int K;
+  __device__ void bring() const {}
+  __device__ u32x4 at(int k) const {
+    return k < K ? *reinterpret_cast<const u32x4*>(p + k) : u32x4{0u, 0u, 0u, 0u};
+  }
+};
+
+}  // namespace
+
+// The last rows of one matrix, up to 16 (a.m_first and on): 16 columns a
+// workgroup, weights straight from memory into the operands.
+template <typename E>
+__global__ __launch_bounds__(kRowThreads) void k_int8_few(Int8Args a) {
+  __shared__ i32x4 red[kRowWaves][64];
+  const int l = threadIdx.x % 64, w = uniform(threadIdx.x / 64), n0 = (int)blockIdx.x * kFewCols;
+  const int rows = (int)(a.M - a.m_first);
+  const int64_t row = a.m_first + (l % 16 < rows ? l % 16 : 0);
+  const i32x4 acc = stream_columns(a, n0, w, l, RowsOfCodes{a.a + row * a.K, a.K});
+  finish_columns<E>(a, acc, n0, a.m_first, rows, a.as[row], red);
+}
+
+namespace {
+
+// most values of the rows that every workgroup quantises for itself
+constexpr int kRowValues = 8 * 1024;
+
+// Rows of x, quantised into LDS by the whole workgroup: values in registers, a
+// maximum per row, then the codes.
+template <typename X>
+struct RowsOfX {
+  const Int8Args& a;
+  uint8_t* codes;              // [M][pitch], zeros from K to the step's end
+  float* scale;                // [M]
+  uint32_t* amax;              // [M]
+  int pitch, row;
+  __device__ void bring() const {
+    constexpr int kTurns = kRowValues / 8 / kRowThreads;
+    const int tid = threadIdx.x, M = (int)a.M, per = a.K / 8, pad = (pitch - a.K) / 8;
+    const X* x = static_cast<const X*>(a.x);
+    float v[kTurns][8];
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) {
+      const int i = tid + u * kRowThreads;
+      if (i < M * per) load_elems(x + (int64_t)i * 8, v[u]);
+    }
+    if (tid < M) amax[tid] = 0;
+    for (int i = tid; i < M * pad; i += kRowThreads)
+      *reinterpret_cast<u32x2*>(codes + i / pad * pitch + a.K + i % pad * 8) = u32x2{0u, 0u};
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) {
+      const int i = tid + u * kRowThreads;
+      if (i - tid % 64 >= M * per) break;            // (the same in all lanes of a wave)
+      uint32_t m = 0;
+      const int mine = i < M * per ? i / per : -1;
+      if (mine >= 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = amax_of(v[u][j], m);
+      }
+      const int first = uniform(mine);
+      if (ballot(mine == first || mine < 0) == ~0ull) {
+        m = wave_max(m);
+        if (tid % 64 == 0) atomicMax(&amax[first], m);
+      } else if (mine >= 0) {
+        atomicMax(&amax[mine], m);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) {
+      const int i = tid + u * kRowThreads;
+      if (i >= M * per) break;
+      *reinterpret_cast<u32x2*>(codes + i / per * pitch + i % per * 8) = int8_codes(v[u], int8_scale(amax[i / per]));
+    }
+    if (tid < M) scale[tid] = int8_scale(amax[tid]);
+    __syncthreads();
+  }
+  __device__ u32x4 at(int k) const { return *reinterpret_cast<const u32x4*>(codes + row * pitch + k); }
+};
+
+}  // namespace
+
+// A few floating rows (a decoded token's projection): 16 columns a workgroup;
+// the first weights are asked for, the rows are quantised into LDS meanwhile.
+template <typename E, typename X>
+__global__ __launch_bounds__(kRowThreads) void k_int8_rows(Int8Args a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  __shared__ i32x4 red[kRowWaves][64];
+  __shared__ float scale[kFewRows];
+  __shared__ uint32_t amax[kFewRows];
+  const int l = threadIdx.x % 64, w = uniform(threadIdx.x / 64), n0 = (int)blockIdx.x * kFewCols, M = (int)a.M;
+  const int pitch = (a.K + kStep - 1) / kStep * kStep + 16;      // rows of one column of chunks in different banks
+  const int row = l % 16 < M ? l % 16 : 0;
+  const i32x4 acc = stream_columns(a, n0, w, l, RowsOfX<X>{a, dyn, scale, amax, pitch, row});
+  finish_columns<E>(a, acc, n0, 0, M, scale[row], red);
+}
+
+// Codes and scales of rows: PER threads a row, its values in registers while
+// they fit.  Bound: HBM.
+template <typename X, int PER>
+__global__ __launch_bounds__(kRowThreads) void k_int8_quantize(const X* x, int64_t rows, int K, uint8_t* q, float* s) {
+  constexpr int kHeld = 8;                  // chunks of 8 values that a thread holds
+  __shared__ uint32_t red[kRowWaves];
+  const int sub = threadIdx.x / PER, at = threadIdx.x % PER, per = K / 8;
+  for (int64_t m0 = (int64_t)blockIdx.x * (kRowThreads / PER); m0 < rows; m0 += (int64_t)gridDim.x * (kRowThreads / PER)) {
+    const int64_t m = m0 + sub;
+    const bool live = m < rows;
+    const X* p = x + m * K;
+    float v[kHeld][8];
+    uint32_t big = 0;
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+      if (live && at + u * PER < per) load_elems(p + (at + u * PER) * 8, v[u]);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+      if (live && at + u * PER < per) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) big = amax_of(v[u][j], big);
+      }
+    for (int c = at + kHeld * PER; live && c < per; c += PER) {
+      float f[8];
+      load_elems(p + c * 8, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) big = amax_of(f[j], big);
+    }
+    big = wave_max(big);
+    if constexpr (PER > 64) {
+      __syncthreads();                      // (the last row's maximum has been read)
+      if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = big;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kRowWaves; ++i) big = red[i] > big ? red[i] : big;
+    }
+    const float sc = int8_scale(big);
+    if (live && at == 0) s[m] = sc;
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+      if (live && at + u * PER < per) *reinterpret_cast<u32x2*>(q + m * K + (at + u * PER) * 8) = int8_codes(v[u], sc);
+    for (int c = at + kHeld * PER; live && c < per; c += PER) {
+      float f[8];
+      load_elems(p + c * 8, f);
+      *reinterpret_cast<u32x2*>(q + m * K + c * 8) = int8_codes(f, sc);
+    }
+  }
+}
+
+namespace {
+
+template <typename F>
+hipError_t for_type(int element, const F& f) {
+  return element == MM_ELEMENT_BF16 ? f(__bf16{}) : element == MM_ELEMENT_F16 ? f(_Float16{}) : f(float{});
+}
+
+template <typename E>
+hipError_t gemm(const Int8Args& args, int num_cus, hipStream_t s) {
+  Int8Args a = args;
+  const unsigned units = (unsigned)((a.N + kFewCols - 1) / kFewCols);
+  if (a.x != nullptr) {
+    const size_t lds = (size_t)a.M * ((a.K + kStep - 1) / kStep * kStep + 16);
+    return for_type(a.x_element, [&](auto x) {
+      hipLaunchKernelGGL((k_int8_rows<E, decltype(x)>), dim3(units), dim3(kRowThreads), lds, s, a);
+      return hipGetLastError();
+    });
+  }
+  const int64_t even = a.M / a.G > 0 ? a.M / a.G : 1;
+  const unsigned cus = (unsigned)((num_cus + 7) / 8 * 8);
+  auto count = [&](int c) { return (even + most_rows(c) - 1) / most_rows(c) * a.G * ((a.N + cols_of(c) - 1) / cols_of(c)); };
+  if (a.offsets == nullptr && a.M <= kFewRows) {
+    a.m_first = 0;
+    hipLaunchKernelGGL(k_int8_few<E>, dim3(units), dim3(kRowThreads), 0, s, a);
+  } else if (count(k32x32) <= num_cus) {
+    hipLaunchKernelGGL((k_int8_ring<E, k32x32, 2, 2, 1, 1, 4>), dim3(cus), dim3(256), 0, s, a);
+  } else if (count(k64x32) <= num_cus) {
+    hipLaunchKernelGGL((k_int8_ring<E, k64x32, 2, 2, 2, 1, 4>), dim3(cus), dim3(256), 0, s, a);
+  } else if (count(k64x64) <= num_cus) {
+    hipLaunchKernelGGL((k_int8_ring<E, k64x64, 2, 2, 2, 2, 4>), dim3(cus), dim3(256), 0, s, a);
+  } else if (count(k128x128) <= num_cus) {
+    hipLaunchKernelGGL((k_int8_ring<E, k128x128, 4, 2, 2, 4, 2>), dim3(cus), dim3(512), 0, s, a);
+  } else {
+    // one matrix: up to 16 rows beyond the blocks of 256 are streamed
+    const int64_t rest = a.offsets == nullptr ? a.M % kBM : 0;
+    if (rest <= kFewRows) a.M -= rest;
+    hipLaunchKernelGGL(k_int8_mma<E>, dim3(cus), dim3(512), 0, s, a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess || a.M == args.M) return err;
+    a.m_first = a.M;
+    a.M = args.M;
+    hipLaunchKernelGGL(k_int8_few<E>, dim3(units), dim3(kRowThreads), 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool int8_from_x(const Int8Args& a) { return a.offsets == nullptr && a.M <= kFewRows && a.M * a.K <= kRowValues; }
+
+hipError_t launch_int8_gemm(const Int8Args& a, int num_cus, hipStream_t s) {
+  return for_type(a.y_element, [&](auto e) { return gemm<decltype(e)>(a, num_cus, s); });
+}
+
+hipError_t launch_int8_quantize(const void* x, int element, int64_t rows, int cols, uint8_t* q, float* s, hipStream_t st) {
+  return for_type(element, [&](auto e) {
+    typedef decltype(e) X;
+    if (cols <= 4096) {
+      const int64_t n = (rows + 3) / 4;
+      hipLaunchKernelGGL((k_int8_quantize<X, 64>), dim3((unsigned)(n < (1 << 20) ? n : (1 << 20))), dim3(kRowThreads), 0, st,
+                         static_cast<const X*>(x), rows, cols, q, s);
+    } else {
+      hipLaunchKernelGGL((k_int8_quantize<X, kRowThreads>), dim3((unsigned)(rows < (1 << 20) ? rows : (1 << 20))),
+                         dim3(kRowThreads), 0, st, static_cast<const X*>(x), rows, cols, q, s);
+    }
+    return hipGetLastError();
+  });
+}
+
+}  // namespace mm

@@ -1,6 +1,7 @@
 // Internal interfaces of the router, the few-token layer, the block-scaled
-// product, the token sort and the activation (mm_router.hip, mm_few.hip,
-// mm_block.hip, mm_sort.hip, mm_swiglu.hip).
+// product, the token sort, the activation and the 8-bit integer product
+// (mm_router.hip, mm_few.hip, mm_block.hip, mm_sort.hip, mm_swiglu.hip,
+// mm_int8.hip).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -130,5 +131,25 @@ struct SwigluArgs {
 };
 hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s);
 hipError_t launch_swiglu_backward(const SwigluArgs& a, hipStream_t s);
+
+// ------------------------------------------------- 8-bit integer product
+struct Int8Args {
+  const uint8_t* a;          // int8 [M][K]
+  const float* as;           // [M]
+  const void* x;             // [M][K] (quantised on the way), or null
+  const uint8_t* b;          // int8 [G][N][K]
+  const float* bs;           // [G][N]
+  const int32_t* offsets;    // as in BlockArgs
+  const int32_t* counts;
+  void* y;                   // [M][N]
+  int64_t M;
+  int64_t m_first;           // first row of the streaming units
+  int N, K, G;
+  int x_element, y_element;
+};
+hipError_t launch_int8_quantize(const void* x, int element, int64_t rows, int cols, uint8_t* q, float* s, hipStream_t st);
+// whether launch_int8_gemm may quantise a.x on the way (a.a and a.as unused)
+bool int8_from_x(const Int8Args& a);
+hipError_t launch_int8_gemm(const Int8Args& a, int num_cus, hipStream_t s);
 
 }  // namespace mm

@@ -42,15 +42,7 @@ template <typename E, bool WIDE>
 __device__ __forceinline__ void load8(const E* p, int lane, int n, float (&v)[kPer]) {
   if constexpr (WIDE) {
     if (lane * kPer < n) {
-      if constexpr (sizeof(E) == 2) {
-        Elems<E, 8>::load(p + lane * kPer, v);
-      } else {
-        float a[4], b[4];
-        Elems<E, 4>::load(p + lane * kPer, a);
-        Elems<E, 4>::load(p + lane * kPer + 4, b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-      }
+      load_elems(p + lane * kPer, v);
       return;
     }
 #pragma unroll
@@ -64,14 +56,7 @@ __device__ __forceinline__ void load8(const E* p, int lane, int n, float (&v)[kP
 template <typename E, bool WIDE>
 __device__ __forceinline__ void store8(E* p, int lane, int n, const float (&v)[kPer]) {
   if constexpr (WIDE) {
-    if (lane * kPer >= n) return;
-    if constexpr (sizeof(E) == 2) {
-      Elems<E, 8>::store(p + lane * kPer, v);
-    } else {
-      const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
-      Elems<E, 4>::store(p + lane * kPer, a);
-      Elems<E, 4>::store(p + lane * kPer + 4, b);
-    }
+    if (lane * kPer < n) store_elems(p + lane * kPer, v);
   } else {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)

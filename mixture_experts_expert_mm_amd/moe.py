@@ -6,9 +6,9 @@ functions ``route``, ``moe_few``, ``block_quantize``, ``block_matmul`` and
 ``block_linear`` hold nothing: each checks its tensors, allocates the
 outputs and a workspace on the calling stream and makes one call.  So do
 ``sort_tokens``, ``sort_rows``, ``combine_tokens``, ``combine_backward``,
-``swiglu``, ``swiglu_forward`` and ``swiglu_backward``; sort_tokens, sort_rows,
-combine_tokens and swiglu are differentiable.  Nothing here computes any part
-of the expert path.
+``swiglu``, ``swiglu_forward``, ``swiglu_backward``, ``int8_quantize``,
+``int8_matmul`` and ``int8_linear``; sort_tokens, sort_rows, combine_tokens and
+swiglu are differentiable.  Nothing here computes any part of the expert path.
 """
 
 from __future__ import annotations
@@ -355,6 +355,15 @@ def block_quantize(x, stream=None):
     return q, s
 
 
+def _group_args(G, offsets, counts, dev):
+    if (offsets is None) != (counts is None) or (offsets is None and G > 1):
+        raise ValueError("offsets, counts: both are needed, or neither with one matrix")
+    if offsets is not None:
+        n = offsets.shape[0] if isinstance(offsets, torch.Tensor) and offsets.dim() == 1 else -1
+        _need("offsets", offsets, torch.int32, (n if n == G + 1 else G,), dev)
+        _need("counts", counts, torch.int32, (G,), dev)
+
+
 def _block_args(M, K, dev, rows, w, ws, offsets, counts, y):
     if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
         raise ValueError("w: [out, in] or [groups, out, in] is needed")
@@ -362,12 +371,7 @@ def _block_args(M, K, dev, rows, w, ws, offsets, counts, y):
     lead = () if w.dim() == 2 else (G,)
     _need("w", w, torch.float8_e4m3fn, lead + (N, K), dev)
     _need("ws", ws, torch.float32, lead + (-(-N // 128), K // 128), dev)
-    if (offsets is None) != (counts is None) or (offsets is None and G > 1):
-        raise ValueError("offsets, counts: both are needed, or neither with one matrix")
-    if offsets is not None:
-        n = offsets.shape[0] if isinstance(offsets, torch.Tensor) and offsets.dim() == 1 else -1
-        _need("offsets", offsets, torch.int32, (n if n == G + 1 else G,), dev)
-        _need("counts", counts, torch.int32, (G,), dev)
+    _group_args(G, offsets, counts, dev)
     if y is not None:
         _need("y", y, torch.bfloat16, (M, N), dev)
         _apart(y, *rows, w, ws, offsets, counts)
@@ -694,3 +698,72 @@ def swiglu_backward(da, codes, scales, *, activation_clamp=None, stream=None):
     clamp = _clamp_of(activation_clamp)
     with _stream_of(dev, stream):
         return _swiglu_backward(da, codes, scales, clamp)
+
+
+# ------------------------------------------------- 8-bit integer product
+
+_int8_plan = functools.lru_cache(maxsize=256)(B.mm_int8_plan_create)
+_Y_TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+def int8_quantize(x, stream=None):
+    """mm_int8_quantize: (codes int8 [M,K], scales float32 [M]) of rows of x, tokens or a weight's output channels
+    (bf16, float16 or float32; K a multiple of 16)."""
+    M, K, dev = _rows("x", x)
+    el = _element("x", x, True)
+    _need("x", x, x.dtype, (M, K), dev)
+    if K % 16 or K == 0:
+        raise ValueError(f"x: the columns have to be a multiple of 16, got {K}")
+    with _stream_of(dev, stream):
+        q = torch.empty((M, K), dtype=torch.int8, device=dev)
+        s = torch.empty(M, dtype=torch.float32, device=dev)
+        if M:
+            B.mm_int8_quantize(M, K, el, x, q, s, _raw_stream(dev))
+    return q, s
+
+
+def _int8_args(M, K, dev, x_element, rows, w, ws, offsets, counts, y_dtype, y):
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
+        raise ValueError("w: [out, in] or [groups, out, in] is needed")
+    G, N = (1, w.shape[0]) if w.dim() == 2 else (w.shape[0], w.shape[1])
+    lead = () if w.dim() == 2 else (G,)
+    _need("w", w, torch.int8, lead + (N, K), dev)
+    _need("ws", ws, torch.float32, lead + (N,), dev)
+    _group_args(G, offsets, counts, dev)
+    if y_dtype not in _Y_TYPES:
+        raise ValueError(f"y_dtype: one of {sorted(_Y_TYPES)} is needed, got {y_dtype!r}")
+    dt = _Y_TYPES[y_dtype]
+    if y is not None:
+        _need("y", y, dt, (M, N), dev)
+        _apart(y, *rows, w, ws, offsets, counts)
+    return N, dt, _int8_plan(max(M, 1), N, K, G, x_element, B.ELEMENT[dt])
+
+
+def int8_matmul(q, s, w, ws, offsets=None, counts=None, *, y_dtype="bf16", y=None, stream=None):
+    """mm_int8_gemm: y [M,N] of int8 rows (q [M,K], s float32 [M]) and weights (w int8 [N,K], ws float32 [N]), or, with
+    w [G,N,K] and ws [G,N], of groups of rows as in ``block_matmul``; sort_tokens' order has their offsets and counts.
+    y_dtype: "bf16", "f16" or "f32".  Sums are exact.  y must not overlap an input."""
+    M, K, dev = _rows("q", q)
+    _need("q", q, torch.int8, (M, K), dev)
+    _need("s", s, torch.float32, (M,), dev)
+    N, dt, plan = _int8_args(M, K, dev, B.MM_ELEMENT_BF16, (q, s), w, ws, offsets, counts, y_dtype, y)
+    with _stream_of(dev, stream):
+        if y is None:
+            y = torch.empty((M, N), dtype=dt, device=dev)
+        if M:
+            B.mm_int8_gemm(plan, q, s, w, ws, offsets, counts, y, _raw_stream(dev))
+    return y
+
+
+def int8_linear(x, w, ws, offsets=None, counts=None, *, y_dtype="bf16", y=None, stream=None):
+    """mm_int8_linear: int8_matmul of x's (bf16, float16 or float32 [M,K]) codes and scales, in one call."""
+    M, K, dev = _rows("x", x)
+    el = _element("x", x, True)
+    _need("x", x, x.dtype, (M, K), dev)
+    N, dt, plan = _int8_args(M, K, dev, el, (x,), w, ws, offsets, counts, y_dtype, y)
+    with _stream_of(dev, stream):
+        if y is None:
+            y = torch.empty((M, N), dtype=dt, device=dev)
+        if M:
+            B.mm_int8_linear(plan, x, w, ws, offsets, counts, y, _workspace(plan.workspace_bytes, dev), _raw_stream(dev))
+    return y
