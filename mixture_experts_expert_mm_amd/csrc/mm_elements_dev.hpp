@@ -17,18 +17,21 @@ template <> struct Bytes<1> { typedef uint8_t type; };
 template <typename E, int N>
 struct Elems {
   typedef typename Bytes<sizeof(E) * N>::type vec;
-  static __device__ __forceinline__ void load(const void* p, float (&f)[N]) {
-    union { vec v; E e[N]; } u;
-    u.v = *reinterpret_cast<const vec*>(p);
+  union Both { vec v; E e[N]; };
+  static __device__ __forceinline__ void unpack(const vec& v, float (&f)[N]) {
+    Both u;
+    u.v = v;
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = (float)u.e[i];
   }
-  static __device__ __forceinline__ void store(void* p, const float (&f)[N]) {
-    union { vec v; E e[N]; } u;
+  static __device__ __forceinline__ vec pack(const float (&f)[N]) {
+    Both u;
 #pragma unroll
     for (int i = 0; i < N; ++i) u.e[i] = (E)f[i];
-    *reinterpret_cast<vec*>(p) = u.v;
+    return u.v;
   }
+  static __device__ __forceinline__ void load(const void* p, float (&f)[N]) { unpack(*reinterpret_cast<const vec*>(p), f); }
+  static __device__ __forceinline__ void store(void* p, const float (&f)[N]) { *reinterpret_cast<vec*>(p) = pack(f); }
 };
 
 // eight neighbours, at an address of their own size
@@ -73,14 +76,34 @@ __device__ __forceinline__ int int8_code(float v, float s) {
   const float q = __builtin_rintf(v / s);
   return q >= -127.0f ? (int)(q > 127.0f ? 127.0f : q) : q < -127.0f ? -127 : 0;
 }
+
+// Eight codes at once, the same ones: a product with the reciprocal is within
+// 2^-15 of the quotient (three roundings of at most 127 * 2^-24 and one more of
+// the quotient's own), so it rounds to the same integer unless it is that near
+// to the middle between two; only then are the quotients taken.  (Eight IEEE
+// divisions are 80 instructions; 64 Ki rows of 2 x 2048 bf16 values 320 -> 215 us.)
+// t + 1.5 * 2^23 has the rounded integer in its low bits.
 __device__ __forceinline__ u32x2 int8_codes(const float (&v)[8], float s) {
+  constexpr float kShift = 12582912.0f;
+  const float r = 1.0f / s;
+  uint32_t bits[8];
+  float most = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = v[i] * r, u = t + kShift;
+    bits[i] = __float_as_uint(u);
+    most = fmaxf(most, fabsf(t - (u - kShift)));
+  }
+  if (most > 0.5f - 0x1p-14f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bits[i] = (uint32_t)int8_code(v[i], s);
+  }
   u32x2 o;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w |= (uint32_t)(int8_code(v[4 * h + i], s) & 0xff) << (8 * i);
-    o[h] = w;
+    const uint32_t lo = __builtin_amdgcn_perm(bits[4 * h + 1], bits[4 * h], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(bits[4 * h + 3], bits[4 * h + 2], 0x04000c0cu);
+    o[h] = s < INFINITY ? lo | hi : 0u;      // (no codes beside a scale that is no number)
   }
   return o;
 }

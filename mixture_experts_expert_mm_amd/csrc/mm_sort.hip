@@ -21,14 +21,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPlaceThreads = 1024;
+constexpr int kMaxThreads = 512;     // of k_combine_backward
 constexpr int kMaxTopk = 64;
 constexpr int kMost = 8;             // slots of a token that are in flight together
+constexpr int64_t kFewRoutes = 8192; // most routes of the single launch
 
 __device__ __forceinline__ int key_of(const SortArgs& a, int64_t r) {
   const int e = a.ids[r];
-  if ((uint32_t)e >= (uint32_t)a.E) return a.E;
-  if (a.active != nullptr && a.active[(uint32_t)r / (uint32_t)a.K] == 0) return a.E;   // (routes are below 2^30)
-  return e;
+  const bool on = a.active == nullptr || a.active[(uint32_t)r / (uint32_t)a.K] != 0;   // (routes are below 2^30)
+  return on && (uint32_t)e < (uint32_t)a.E ? e : a.E;
 }
 
 // Exclusive prefix of v over the workgroup's threads; `all` gets the sum.
@@ -70,62 +71,100 @@ __device__ void write_offsets(const SortArgs& a, const int32_t* tot, int32_t* pa
   }
 }
 
-// How a workgroup's threads share rows: `cx` of them (a power of two) go
-// along a row, the others take further tokens.
+// How a workgroup's threads share narrow rows: `cx` of them (a power of two)
+// go along a row, the others take further tokens.
 struct Split {
   int cx, c, ty, sub;
 };
 __device__ __forceinline__ Split split_of(int64_t chunks) {
   int cx = 1;
-  while (cx < kThreads && cx < chunks) cx <<= 1;
+  while (cx < 64 && cx < chunks) cx <<= 1;
   return Split{cx, (int)threadIdx.x & (cx - 1), kThreads / cx, (int)threadIdx.x / cx};
 }
+
+// A value of an array that no kernel writes while this one runs.  UNIFORM: the
+// same address in all lanes, through the scalar unit.
+template <bool UNIFORM, typename T>
+__device__ __forceinline__ T slot(const T* p) {
+  if constexpr (UNIFORM) return *(const __attribute__((address_space(4))) T*)reinterpret_cast<uintptr_t>(p);
+  return *p;
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// f(t, c): every vector c of every token t, by the whole grid.  WIDE (rows of 64
+// vectors and more): a wave takes 64 neighbours of one token.
+template <bool WIDE, typename F>
+__device__ __forceinline__ void for_vectors(int64_t tokens, int64_t chunks, const F& f) {
+  if constexpr (WIDE) {
+    const uint32_t per = (uint32_t)((chunks + 63) / 64);          // (a tensor has fewer than 2^32 such pieces)
+    const uint32_t total = (uint32_t)tokens * per, step = gridDim.x * (kThreads / 64);
+    for (uint32_t u = blockIdx.x * (kThreads / 64) + (uint32_t)uniform(threadIdx.x / 64); u < total; u += step) {
+      const int64_t c = (int64_t)(u % per) * 64 + threadIdx.x % 64;
+      if (c < chunks) f((int64_t)(u / per), c);
+    }
+  } else {
+    const Split s = split_of(chunks);
+    for (int64_t t = (int64_t)blockIdx.x * s.ty + s.sub; t < tokens; t += (int64_t)gridDim.x * s.ty)
+      for (int64_t c = s.c; c < chunks; c += s.cx) f(t, c);
+  }
+}
+
+// what is read or written once
+template <typename V>
+__device__ __forceinline__ V stream_in(const V* p) { return __builtin_nontemporal_load(p); }
+template <typename V>
+__device__ __forceinline__ void stream_out(void* p, const V& v) { __builtin_nontemporal_store(v, static_cast<V*>(p)); }
 
 }  // namespace
 
 // A few routes: each workgroup finds the places of one token's routes by
-// counting the routes before them, so that one launch does it all.
+// counting the routes before them, so that one launch does it all; one
+// workgroup more counts the experts' routes.
 template <int V>
 __global__ __launch_bounds__(kThreads) void k_sort_few(SortArgs a) {
   typedef typename Bytes<V>::type vec;
-  __shared__ int32_t hist[1025], part[kThreads / 64], cnt[kThreads / 64][kMost], place[kMaxTopk];
-  __shared__ uint8_t skip[kMaxTopk];
+  constexpr int kWaves = kThreads / 64;
+  __shared__ int32_t cnt[kWaves][kMost], place[kMaxTopk];
   const int tid = threadIdx.x, w = tid / 64, R = (int)a.R;
   const int64_t t = blockIdx.x;
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
+  // the order of (key, route): routes are below 2^13 (kFewRoutes), keys at most 2^10
+  auto rank_of = [&](int r) { return (uint32_t)key_of(a, r) << 13 | (uint32_t)r; };
+  if (t == a.T) {
+    __shared__ int32_t hist[1025], part[kWaves];
+    if (blockIdx.y > 0) return;
     for (int e = tid; e <= a.E; e += kThreads) hist[e] = 0;
     __syncthreads();
     for (int r = tid; r < R; r += kThreads) atomicAdd(&hist[key_of(a, r)], 1);
     __syncthreads();
     write_offsets<kThreads>(a, hist, part);
+    return;
   }
   for (int k0 = 0; k0 < a.K; k0 += kMost) {
     const int r0 = (int)t * a.K + k0;
-    int key[kMost], before[kMost];
+    uint32_t mine[kMost];
+    int before[kMost];
 #pragma unroll
-    for (int i = 0; i < kMost; ++i) key[i] = k0 + i < a.K ? key_of(a, r0 + i) : -1, before[i] = 0;
-    for (int r = tid; r < R; r += kThreads) {
-      const int e = key_of(a, r);
+    for (int i = 0; i < kMost; ++i) mine[i] = k0 + i < a.K ? rank_of(r0 + i) : 0, before[i] = 0;
+    for (int j = 0; j < R; j += kThreads) {
+      const uint32_t other = j + tid < R ? rank_of(j + tid) : ~0u;
 #pragma unroll
-      for (int i = 0; i < kMost; ++i) before[i] += e < key[i] || (e == key[i] && r < r0 + i) ? 1 : 0;
+      for (int i = 0; i < kMost; ++i) before[i] += __popcll(ballot(other < mine[i]));
     }
+    if (tid % 64 == 0) {
 #pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-      const int n = wave_sum(before[i]);
-      if (tid % 64 == 0) cnt[w][i] = n;
+      for (int i = 0; i < kMost; ++i) cnt[w][i] = before[i];
     }
     __syncthreads();
     if (tid < kMost && k0 + tid < a.K) {
-      int n = 0, mine = 0;
+      int n = 0;
 #pragma unroll
-      for (int i = 0; i < kThreads / 64; ++i) n += cnt[i][tid];
-#pragma unroll
-      for (int i = 0; i < kMost; ++i) mine = i == tid ? key[i] : mine;
-      place[k0 + tid] = n;
-      skip[k0 + tid] = mine == a.E;
+      for (int i = 0; i < kWaves; ++i) n += cnt[i][tid];
+      const bool skip = key_of(a, r0 + tid) == a.E;
+      place[k0 + tid] = skip ? ~n : n;
       if (blockIdx.y == 0) {
-        a.row_of_route[r0 + tid] = mine == a.E ? -1 : n;
-        a.route_of_row[n] = mine == a.E ? -1 : r0 + tid;
+        a.row_of_route[r0 + tid] = skip ? -1 : n;
+        a.route_of_row[n] = skip ? -1 : r0 + tid;
       }
     }
     __syncthreads();
@@ -134,9 +173,10 @@ __global__ __launch_bounds__(kThreads) void k_sort_few(SortArgs a) {
   const int64_t chunks = a.row_bytes / V;
   for (int64_t c = (int64_t)blockIdx.y * kThreads + tid; c < chunks; c += (int64_t)gridDim.y * kThreads) {
     const vec v = *reinterpret_cast<const vec*>(a.x + t * a.row_bytes + c * V);
-    const vec zero = {};
-    for (int k = 0; k < a.K; ++k)
-      *reinterpret_cast<vec*>(a.rows + (int64_t)place[k] * a.row_bytes + c * V) = skip[k] ? zero : v;
+    for (int k = 0; k < a.K; ++k) {
+      const int p = place[k];
+      *reinterpret_cast<vec*>(a.rows + (int64_t)(p < 0 ? ~p : p) * a.row_bytes + c * V) = p < 0 ? vec{} : v;
+    }
   }
 }
 
@@ -227,147 +267,145 @@ __global__ __launch_bounds__(kPlaceThreads) void k_sort_place(SortArgs a) {
   }
 }
 
-// rows[row_of_route[t][k]] = x[t]; the workgroup of token t also clears those of
-// the rows t * K .. t * K + K - 1 that no route fills.
-template <int V>
+// rows[row_of_route[t][k]] = x[t]; who brings token t also clears those of the
+// rows t * K .. t * K + K - 1 that no route fills.
+template <int V, bool WIDE>
 __global__ __launch_bounds__(kThreads) void k_sort_rows(SortArgs a) {
   typedef typename Bytes<V>::type vec;
-  const int64_t chunks = a.row_bytes / V;
-  const Split s = split_of(chunks);
-  const int64_t kept = a.offsets[a.E];
-  for (int64_t t = (int64_t)blockIdx.x * s.ty + s.sub; t < a.T; t += (int64_t)gridDim.x * s.ty) {
-    const int32_t* to = a.row_of_route + t * a.K;
-    for (int64_t c = s.c; c < chunks; c += s.cx) {
-      const vec v = *reinterpret_cast<const vec*>(a.x + t * a.row_bytes + c * V);
-      for (int k = 0; k < a.K; ++k) {
-        const int64_t p = to[k];
-        if (p >= 0 && p < a.R) *reinterpret_cast<vec*>(a.rows + p * a.row_bytes + c * V) = v;
-      }
+  const int64_t kept = slot<true>(a.offsets + a.E);
+  for_vectors<WIDE>(a.T, a.row_bytes / V, [&](int64_t t, int64_t c) {
+    const vec v = *reinterpret_cast<const vec*>(a.x + t * a.row_bytes + c * V);
+    for (int k = 0; k < a.K; ++k) {
+      const int64_t p = slot<WIDE>(a.row_of_route + t * a.K + k);
+      if (p >= 0 && p < a.R) stream_out(a.rows + p * a.row_bytes + c * V, v);
     }
     for (int64_t p = t * a.K > kept ? t * a.K : kept; p < (t + 1) * a.K; ++p)
-      for (int64_t c = s.c; c < chunks; c += s.cx) *reinterpret_cast<vec*>(a.rows + p * a.row_bytes + c * V) = vec{};
+      stream_out(a.rows + p * a.row_bytes + c * V, vec{});
+  });
+}
+
+namespace {
+
+// Slots k0 .. k0 + SLOTS - 1 of token t: their rows, -1 for one that is skipped or
+// past K, and their weights.  No load is under a condition: the compiler would
+// wait for the loads in flight at each.
+template <int SLOTS, bool UNIFORM>
+__device__ __forceinline__ void load_slots(const CombineTokensArgs& a, int64_t t, int k0, int64_t (&p)[SLOTS], float (&w)[SLOTS]) {
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) {
+    const int64_t at = t * a.K + (k0 + i < a.K ? k0 + i : k0);
+    p[i] = slot<UNIFORM>(a.row_of_route + at);
+    w[i] = slot<UNIFORM>(a.weights != nullptr ? a.weights + at : reinterpret_cast<const float*>(a.row_of_route + at));
+  }
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) {
+    if (a.weights == nullptr) w[i] = 1.0f;
+    if (k0 + i >= a.K || p[i] >= a.R) p[i] = -1;
   }
 }
+
+}  // namespace
 
 // y[t] = sum_k w[t][k] * rows[row_of_route[t][k]] in float32, in the order of k,
-// eight rows in flight.
-template <typename E, int N>
+// SLOTS rows in flight.  A skipped slot reads row 0 and adds nothing, whatever
+// its weight.
+template <typename E, int N, int SLOTS, bool WIDE>
 __global__ __launch_bounds__(kThreads) void k_combine_tokens(CombineTokensArgs a) {
   typedef Elems<E, N> el;
-  const int64_t chunks = a.H / N;
-  const Split s = split_of(chunks);
   const E* rows = static_cast<const E*>(a.rows);
-  for (int64_t t = (int64_t)blockIdx.x * s.ty + s.sub; t < a.T; t += (int64_t)gridDim.x * s.ty) {
-    int32_t p[kMost];
-    float w[kMost];
-    auto slots = [&](int k0) {
+  for_vectors<WIDE>(a.T, a.H / N, [&](int64_t t, int64_t c) {
+    float acc[N] = {};
+    for (int k0 = 0; k0 < a.K; k0 += SLOTS) {
+      int64_t p[SLOTS];
+      float w[SLOTS];
+      typename el::vec v[SLOTS];
+      load_slots<SLOTS, WIDE>(a, t, k0, p, w);
 #pragma unroll
-      for (int i = 0; i < kMost; ++i) {
-        const bool in = k0 + i < a.K;
-        p[i] = in ? a.row_of_route[t * a.K + k0 + i] : -1;
-        w[i] = in && a.weights != nullptr ? a.weights[t * a.K + k0 + i] : 1.0f;
-        if (p[i] >= a.R) p[i] = -1;
+      for (int i = 0; i < SLOTS; ++i) v[i] = stream_in(reinterpret_cast<const typename el::vec*>(rows + (p[i] < 0 ? 0 : p[i]) * a.H + c * N));
+#pragma unroll
+      for (int i = 0; i < SLOTS; ++i) {
+        float f[N];
+        el::unpack(v[i], f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = p[i] < 0 ? acc[j] : fmaf(w[i], f[j], acc[j]);
       }
-    };
-    if (a.K <= kMost) slots(0);
-    for (int64_t c = s.c; c < chunks; c += s.cx) {
-      float acc[N] = {};
-      for (int k0 = 0; k0 < a.K; k0 += kMost) {
-        if (a.K > kMost) slots(k0);
-        float v[kMost][N];
-#pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-#pragma unroll
-          for (int j = 0; j < N; ++j) v[i][j] = 0.0f;
-          if (p[i] >= 0) el::load(rows + p[i] * a.H + c * N, v[i]);
-        }
-        // a skipped slot adds nothing, whatever its weight
-#pragma unroll
-        for (int i = 0; i < kMost; ++i)
-#pragma unroll
-          for (int j = 0; j < N; ++j) acc[j] = p[i] >= 0 ? fmaf(w[i], v[i][j], acc[j]) : acc[j];
-      }
-      el::store(static_cast<E*>(a.y) + t * a.H + c * N, acc);
     }
-  }
+    el::store(static_cast<E*>(a.y) + t * a.H + c * N, acc);
+  });
 }
 
-// drows[p] = w * dy[t] and dw = <dy[t], rows[p]> for the token's rows p, eight
-// slots at a time; 64 or 256 threads a token.  The sums' order is fixed.
-template <typename E, int N, int PER>
-__global__ __launch_bounds__(kThreads) void k_combine_backward(CombineTokensArgs a) {
+// drows[p] = w * dy[t] and dw = <dy[t], rows[p]> for the token's rows p, SLOTS at
+// a time.  A token has a wave, or (WIDE) a workgroup whose size the launch fits
+// to the row.  The sums' order is fixed.
+template <typename E, int N, int SLOTS, bool WIDE>
+__global__ __launch_bounds__(kMaxThreads) void k_combine_backward(CombineTokensArgs a) {
   typedef Elems<E, N> el;
-  constexpr int kTokens = kThreads / PER;
-  __shared__ float red[kThreads / 64][kMost];
+  typedef typename el::vec vec;
+  __shared__ float red[kMaxThreads / 64][SLOTS];
   const int64_t chunks = a.H / N;
-  const int sub = threadIdx.x / PER, at = threadIdx.x % PER, w = threadIdx.x / 64, l = threadIdx.x % 64;
+  const int waves = blockDim.x / 64, w = uniform(threadIdx.x / 64), l = threadIdx.x % 64;
+  const int at = WIDE ? threadIdx.x : l, per = WIDE ? blockDim.x : 64;
   const E *rows = static_cast<const E*>(a.rows), *dy = static_cast<const E*>(a.dy);
   E* drows = static_cast<E*>(a.drows);
-  const int64_t kept = a.offsets[a.E];
-  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < a.T; t0 += (int64_t)gridDim.x * kTokens) {
-    const int64_t t = t0 + sub;
-    const bool live = t < a.T;
-    const int32_t* from = a.row_of_route + t * a.K;
-    for (int k0 = 0; k0 < a.K; k0 += kMost) {
-      int32_t p[kMost];
-      float wt[kMost], dot[kMost];
+  const int64_t kept = slot<true>(a.offsets + a.E);
+  const int64_t step = WIDE ? gridDim.x : (int64_t)gridDim.x * waves;
+  for (int64_t t = WIDE ? blockIdx.x : (int64_t)blockIdx.x * waves + w; t < a.T; t += step) {
+    for (int k0 = 0; k0 < a.K; k0 += SLOTS) {
+      int64_t p[SLOTS];
+      float wt[SLOTS], dot[SLOTS];
+      load_slots<SLOTS, true>(a, t, k0, p, wt);
 #pragma unroll
-      for (int i = 0; i < kMost; ++i) {
-        const int32_t q = live && k0 + i < a.K ? from[k0 + i] : -1;
-        p[i] = q < a.R ? q : -1;
-        wt[i] = p[i] >= 0 ? a.weights[t * a.K + k0 + i] : 0.0f;
-        dot[i] = 0.0f;
-      }
-      for (int64_t c = at; live && c < chunks; c += PER) {
+      for (int i = 0; i < SLOTS; ++i) dot[i] = 0.0f;
+      for (int64_t c = at; c < chunks; c += per) {
         float d[N];
-        el::load(dy + t * a.H + c * N, d);
+        vec v[SLOTS];
+        const vec raw = *reinterpret_cast<const vec*>(dy + t * a.H + c * N);
+        if (a.dweights != nullptr) {
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-          if (p[i] < 0) continue;
-          if (a.dweights != nullptr) {
-            float v[N];
-            el::load(rows + p[i] * a.H + c * N, v);
+          for (int i = 0; i < SLOTS; ++i) v[i] = stream_in(reinterpret_cast<const vec*>(rows + (p[i] < 0 ? 0 : p[i]) * a.H + c * N));
+        }
+        el::unpack(raw, d);
+        if (drows != nullptr) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) dot[i] = fmaf(d[j], v[j], dot[i]);
-          }
-          if (drows != nullptr) {
+          for (int i = 0; i < SLOTS; ++i) {
             float o[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) o[j] = wt[i] * d[j];
-            el::store(drows + p[i] * a.H + c * N, o);
+            if (p[i] >= 0) stream_out(drows + p[i] * a.H + c * N, el::pack(o));
+          }
+        }
+        if (a.dweights != nullptr) {
+#pragma unroll
+          for (int i = 0; i < SLOTS; ++i) {
+            float f[N];
+            el::unpack(v[i], f);
+#pragma unroll
+            for (int j = 0; j < N; ++j) dot[i] = fmaf(d[j], f[j], dot[i]);
           }
         }
       }
       if (a.dweights != nullptr) {
+        float mine = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) dot[i] = wave_sum(dot[i]);
-        if constexpr (PER > 64) {
-          __syncthreads();             // (the last slots' sums have been read)
-          if (l == 0) {
-#pragma unroll
-            for (int i = 0; i < kMost; ++i) red[w][i] = dot[i];
-          }
-          __syncthreads();
-          if (at < kMost && live && k0 + at < a.K) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < PER / 64; ++i) sum += red[i][at];
-            a.dweights[t * a.K + k0 + at] = sum;
-          }
-        } else {
-          float mine = dot[0];
-#pragma unroll
-          for (int i = 1; i < kMost; ++i) mine = l == i ? dot[i] : mine;
-          if (l < kMost && live && k0 + l < a.K) a.dweights[t * a.K + k0 + l] = mine;
+        for (int i = 0; i < SLOTS; ++i) {
+          const float sum = p[i] < 0 ? 0.0f : wave_sum(dot[i]);
+          mine = l == i ? sum : mine;
         }
+        if constexpr (WIDE) {
+          __syncthreads();             // (the last slots' sums have been read)
+          if (l < SLOTS) red[w][l] = mine;
+          __syncthreads();
+          if (w == 0 && l < SLOTS) {
+            mine = 0.0f;
+            for (int i = 0; i < waves; ++i) mine += red[i][l];
+          }
+        }
+        if ((!WIDE || w == 0) && l < SLOTS && k0 + l < a.K) a.dweights[t * a.K + k0 + l] = mine;
       }
     }
-    if (drows != nullptr && live) {
+    if (drows != nullptr) {
       for (int64_t q = t * a.K > kept ? t * a.K : kept; q < (t + 1) * a.K; ++q)
-        for (int64_t c = at; c < chunks; c += PER) {
-          const float zero[N] = {};
-          el::store(drows + q * a.H + c * N, zero);
-        }
+        for (int64_t c = at; c < chunks; c += per) stream_out(drows + q * a.H + c * N, vec{});
     }
   }
 }
@@ -380,62 +418,81 @@ int vector_bytes(int64_t row_bytes) {
   return (int)(v < 16 ? v : 16);
 }
 
-int64_t tokens_a_group(int64_t chunks) {
+// workgroups of for_vectors
+bool is_wide(int64_t chunks) { return chunks >= 64; }
+unsigned vector_grid(int64_t tokens, int64_t chunks) {
   int64_t cx = 1;
-  while (cx < kThreads && cx < chunks) cx <<= 1;
-  return kThreads / cx;
+  while (cx < 64 && cx < chunks) cx <<= 1;
+  const int64_t pieces = is_wide(chunks) ? tokens * ((chunks + 63) / 64) * 64 : tokens * cx;
+  const int64_t n = (pieces + kThreads - 1) / kThreads;
+  return (unsigned)(n < (1 << 20) ? n : (1 << 20));
 }
-
-unsigned grid_of(int64_t groups) { return (unsigned)(groups < (1 << 20) ? groups : (1 << 20)); }
 
 template <int V>
 hipError_t sort_rows(const SortArgs& a, hipStream_t s) {
-  const int64_t ty = tokens_a_group(a.row_bytes / V);
-  hipLaunchKernelGGL(k_sort_rows<V>, dim3(grid_of((a.T + ty - 1) / ty)), dim3(kThreads), 0, s, a);
+  const int64_t chunks = a.row_bytes / V;
+  const dim3 grid(vector_grid(a.T, chunks));
+  if (is_wide(chunks)) hipLaunchKernelGGL((k_sort_rows<V, true>), grid, dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_sort_rows<V, false>), grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();
+}
+
+// a workgroup brings 256 vectors of a row at a time; few tokens' rows are shared by several, up to 1024 in all
+unsigned slices_of(int64_t chunks, int64_t tokens) {
+  const int64_t turns = (chunks + kThreads - 1) / kThreads, most = 1024 / tokens > 1 ? 1024 / tokens : 1;
+  return (unsigned)(turns < most ? turns : most);
 }
 
 template <int V>
 hipError_t sort_few(const SortArgs& a, hipStream_t s) {
-  // a workgroup brings 4 KiB of a row at a time; up to 1024 of them
-  const int64_t turns = a.rows == nullptr ? 1 : (a.row_bytes / V + kThreads - 1) / kThreads;
-  const int64_t most = 1024 / a.T > 1 ? 1024 / a.T : 1;
-  hipLaunchKernelGGL(k_sort_few<V>, dim3((unsigned)a.T, (unsigned)(turns < most ? turns : most)), dim3(kThreads), 0, s, a);
+  const unsigned slices = a.rows == nullptr ? 1 : slices_of(a.row_bytes / V, a.T);
+  hipLaunchKernelGGL(k_sort_few<V>, dim3((unsigned)(a.T + 1), slices), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
-template <typename E, int N>
+template <typename E, int N, int SLOTS>
 hipError_t combine(const CombineTokensArgs& a, hipStream_t s) {
-  const int64_t ty = tokens_a_group(a.H / N);
-  hipLaunchKernelGGL((k_combine_tokens<E, N>), dim3(grid_of((a.T + ty - 1) / ty)), dim3(kThreads), 0, s, a);
+  const int64_t chunks = a.H / N;
+  const dim3 grid(vector_grid(a.T, chunks));
+  if (is_wide(chunks)) hipLaunchKernelGGL((k_combine_tokens<E, N, SLOTS, true>), grid, dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_combine_tokens<E, N, SLOTS, false>), grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
-template <typename E, int N>
+template <typename E, int N, int SLOTS>
 hipError_t combine_backward(const CombineTokensArgs& a, hipStream_t s) {
-  if (a.H / N <= 64)
-    hipLaunchKernelGGL((k_combine_backward<E, N, 64>), dim3(grid_of((a.T + 3) / 4)), dim3(kThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_combine_backward<E, N, kThreads>), dim3(grid_of(a.T)), dim3(kThreads), 0, s, a);
+  const int64_t chunks = a.H / N, most = 1 << 20;
+  if (chunks <= 64) {
+    const int64_t n = (a.T + 3) / 4;
+    hipLaunchKernelGGL((k_combine_backward<E, N, SLOTS, false>), dim3((unsigned)(n < most ? n : most)), dim3(256), 0, s, a);
+  } else {
+    // the fewest turns along a row, and for them the fewest waves
+    const int64_t turns = (chunks + kMaxThreads - 1) / kMaxThreads, threads = ((chunks + turns - 1) / turns + 63) / 64 * 64;
+    hipLaunchKernelGGL((k_combine_backward<E, N, SLOTS, true>), dim3((unsigned)(a.T < most ? a.T : most)), dim3((unsigned)threads), 0, s, a);
+  }
   return hipGetLastError();
 }
 
-// f(E, N) for the element type and the widest vector that divides a row
+// f(E, N, SLOTS) for the element type, the widest vector that divides a row and
+// the slots of a token that are in flight together
 template <typename F>
-hipError_t for_elements(int element, int64_t H, const F& f) {
-  const int v = vector_bytes(H * (element == MM_ELEMENT_F32 ? 4 : 2));
-  if (element == MM_ELEMENT_F32) {
-    if (v == 16) return f(float{}, std::integral_constant<int, 4>{});
-    if (v == 8) return f(float{}, std::integral_constant<int, 2>{});
-    return f(float{}, std::integral_constant<int, 1>{});
+hipError_t for_elements(const CombineTokensArgs& a, const F& f) {
+  const int v = vector_bytes(a.H * (a.element == MM_ELEMENT_F32 ? 4 : 2));
+  auto slots = [&](auto e, auto n) {
+    return a.K > 4 ? f(e, n, std::integral_constant<int, kMost>{}) : f(e, n, std::integral_constant<int, 4>{});
+  };
+  if (a.element == MM_ELEMENT_F32) {
+    if (v == 16) return slots(float{}, std::integral_constant<int, 4>{});
+    if (v == 8) return slots(float{}, std::integral_constant<int, 2>{});
+    return slots(float{}, std::integral_constant<int, 1>{});
   }
   auto half = [&](auto e) {
-    if (v == 16) return f(e, std::integral_constant<int, 8>{});
-    if (v == 8) return f(e, std::integral_constant<int, 4>{});
-    if (v == 4) return f(e, std::integral_constant<int, 2>{});
-    return f(e, std::integral_constant<int, 1>{});
+    if (v == 16) return slots(e, std::integral_constant<int, 8>{});
+    if (v == 8) return slots(e, std::integral_constant<int, 4>{});
+    if (v == 4) return slots(e, std::integral_constant<int, 2>{});
+    return slots(e, std::integral_constant<int, 1>{});
   };
-  return element == MM_ELEMENT_BF16 ? half(__bf16{}) : half(_Float16{});
+  return a.element == MM_ELEMENT_BF16 ? half(__bf16{}) : half(_Float16{});
 }
 
 }  // namespace
@@ -446,7 +503,7 @@ int sort_chunk(int64_t routes) {
   return (int)((even + kPlaceThreads - 1) / kPlaceThreads * kPlaceThreads);
 }
 
-bool sort_in_one(int64_t routes) { return routes <= 8192; }
+bool sort_in_one(int64_t routes) { return routes <= kFewRoutes; }
 
 hipError_t launch_sort_order(const SortArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(k_sort_count, dim3((unsigned)a.chunks), dim3(kThreads), 0, s, a);
@@ -478,11 +535,11 @@ hipError_t launch_sort_rows(const SortArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_combine_tokens(const CombineTokensArgs& a, hipStream_t s) {
-  return for_elements(a.element, a.H, [&](auto e, auto n) { return combine<decltype(e), n.value>(a, s); });
+  return for_elements(a, [&](auto e, auto n, auto k) { return combine<decltype(e), n.value, k.value>(a, s); });
 }
 
 hipError_t launch_combine_backward(const CombineTokensArgs& a, hipStream_t s) {
-  return for_elements(a.element, a.H, [&](auto e, auto n) { return combine_backward<decltype(e), n.value>(a, s); });
+  return for_elements(a, [&](auto e, auto n, auto k) { return combine_backward<decltype(e), n.value, k.value>(a, s); });
 }
 
 }  // namespace mm

@@ -550,10 +550,12 @@ def sort_tokens(x, topk_ids, num_experts, *, active=None, stream=None):
     plan = _sort_plan(max(T, 1), H, E, K, el)
 
     def make(x):
-        i32 = dict(dtype=torch.int32, device=dev)
-        rows = torch.empty((T * K, H), dtype=x.dtype, device=dev)
-        new = torch.empty if T else torch.zeros
-        order = TokenOrder(new(E, **i32), new(E + 1, **i32), torch.empty((T, K), **i32), torch.empty(T * K, **i32))
+        R = T * K
+        rows = torch.empty((R, H), dtype=x.dtype, device=dev)
+        # one allocation for the four
+        counts, offsets, row, route = (torch.empty if T else torch.zeros)(
+            2 * (E + R) + 1, dtype=torch.int32, device=dev).split((E, E + 1, R, R))
+        order = TokenOrder(counts, offsets, row.view(T, K), route)
         if T:
             ws = _workspace(plan.workspace_bytes, dev) if plan.workspace_bytes else None
             B.mm_sort_tokens(plan, topk_ids, active, x, order.counts, order.offsets, order.row_of_route,
