@@ -726,7 +726,7 @@ mm_status mm_int8_plan_create(const mm_int8_problem* problem, mm_int8_plan* plan
  *   a_scale        device f32 [M]
  *   x              device [M][K] of x_element
  *   b              device int8 [G][N][K]
- *   b_scale        device f32 [G][N]
+ *   b_scale        device f32 [G][N] (4-byte aligned will do unless N % 4 is 0)
  *   group_offsets, group_counts  as in mm_block_gemm
  *   y              device [M][N] of y_element out; must not overlap an input
  */

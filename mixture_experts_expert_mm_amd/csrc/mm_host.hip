@@ -506,6 +506,11 @@ mm_status swiglu_args(int64_t rows, int64_t cols, int32_t element, int32_t clamp
   return MM_OK;
 }
 
+// read four at a time where a group's row of them is whole vectors
+bool int8_scale_ok(const mm_int8_problem& p, const float* b_scale) {
+  return b_scale && aligned(b_scale, p.out_features % 4 == 0 ? 16 : 4);
+}
+
 Int8Args int8_args(const mm_int8_problem& p, const int8_t* b, const float* b_scale, const int32_t* offsets,
                    const int32_t* counts, void* y) {
   Int8Args g{};
@@ -1182,7 +1187,7 @@ mm_status mm_int8_gemm(const mm_int8_plan* plan, const int8_t* a, const float* a
                        const float* b_scale, const int32_t* group_offsets, const int32_t* group_counts, void* y,
                        void* stream) {
   MM_TRY(check_plan(plan));
-  if (!ok16(a) || !ok4(a_scale) || !ok16(b) || !ok4(b_scale) || !ok16(y)) return MM_ERR_INVALID_ARG;
+  if (!ok16(a) || !ok4(a_scale) || !ok16(b) || !int8_scale_ok(plan->prob, b_scale) || !ok16(y)) return MM_ERR_INVALID_ARG;
   if (!block_groups_ok(plan->prob, group_offsets, group_counts)) return MM_ERR_INVALID_ARG;
   Int8Args g = int8_args(plan->prob, b, b_scale, group_offsets, group_counts, y);
   g.a = reinterpret_cast<const uint8_t*>(a);
@@ -1196,7 +1201,7 @@ mm_status mm_int8_linear(const mm_int8_plan* plan, const void* x, const int8_t* 
                          uint64_t workspace_bytes, void* stream) {
   MM_TRY(check_plan(plan));
   const mm_int8_problem& p = plan->prob;
-  if (!ok16(x) || !ok16(b) || !ok4(b_scale) || !ok16(y) || !ok16(workspace)) return MM_ERR_INVALID_ARG;
+  if (!ok16(x) || !ok16(b) || !int8_scale_ok(p, b_scale) || !ok16(y) || !ok16(workspace)) return MM_ERR_INVALID_ARG;
   if (!block_groups_ok(p, group_offsets, group_counts)) return MM_ERR_INVALID_ARG;
   if ((int64_t)workspace_bytes < plan->workspace_bytes) return MM_ERR_WORKSPACE;
   Int8Args g = int8_args(p, b, b_scale, group_offsets, group_counts, y);

@@ -32,23 +32,32 @@ __device__ __forceinline__ void mfma64(i32x4& c, const u32x4& a, const u32x4& b)
   c = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
 
-// four neighbouring columns n .. n + 3 of a row of y
+// four neighbouring columns n .. n + 3 of a row of y [..][N]
 template <typename E>
-__device__ __forceinline__ void put4(const Int8Args& a, int64_t row, int n, const float (&v)[4]) {
-  E* y = static_cast<E*>(a.y) + row * a.N + n;
-  if (a.N % 4 == 0) {
-    if (n < a.N) Elems<E, 4>::store(y, v);
+__device__ __forceinline__ void put4(void* y, int N, int64_t row, int n, const float (&v)[4]) {
+  E* p = static_cast<E*>(y) + row * N + n;
+  if (N % 4 == 0) {
+    if (n < N) Elems<E, 4>::store(p, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (n + i < a.N) y[i] = (E)v[i];
+      if (n + i < N) p[i] = (E)v[i];
   }
 }
 
-__device__ __forceinline__ void scales4(const Int8Args& a, int group, int n, float (&v)[4]) {
-  const float* p = a.bs + (int64_t)group * a.N;
+// their scales, from a group's row (16-byte aligned where N % 4 is 0)
+__device__ __forceinline__ void scales4(const float* p, int N, int n, float (&v)[4]) {
+  if (N % 4 == 0) {
+    Elems<float, 4>::load(p + (n < N ? n : 0), v);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = p[n + i < a.N ? n + i : a.N - 1];
+    for (int i = 0; i < 4; ++i) v[i] = p[n + i < N ? n + i : N - 1];
+  }
+}
+
+__device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<const uint8_t*>((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
 }
 
 // One tile: WM x WN waves of 16 * MT rows x 16 * NT columns; D stages of LDS,
@@ -63,26 +72,30 @@ __device__ __forceinline__ void int8_tile(const Int8Args& a, const TileAt& at, u
   static_assert(kOfA % W == 0 && kGroups % W == 0 && W % 2 == 0, "a wave's copies are of one operand each");
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));   // nothing derived from it is kept across tiles
+  // (the arguments' fields in registers: a tile of this size outgrows what the
+  // compiler follows through the reference)
+  const int K = uniform(a.K), N = uniform(a.N);
   const TileAt t = uniform_tile(at);
   const int w = uniform(tid / 64), l = tid % 64, r = l % 16, g = l / 16, wm = w % WM, wn = w / WM;
-  const int KB = (a.K + kStep - 1) / kStep, stages = (KB + P - 1) / P;
-  const int rows = t.rows, cols = a.N - t.n0 < BN ? a.N - t.n0 : BN;
+  const int KB = (K + kStep - 1) / kStep, stages = (KB + P - 1) / P;
+  const int rows = t.rows, cols = N - t.n0 < BN ? N - t.n0 : BN;
   // One instruction moves 8 rows of 128 bytes, lane i to byte 16 * i; the chunk
   // at place p of row x is p ^ (x / 2 % 8), so that 16 rows read at one chunk
   // hit 16 different bank groups.  Rows past the last one, chunks past K and
   // stages past the end are beyond the descriptor: zeros without an access.
   const int chunk = (l % 8) ^ ((4 * (w % 2) + l / 16) % 8);
-  const uint32_t voff = (uint32_t)(l / 8) * a.K + chunk * 16;
-  const uint32_t vlast = chunk * 16 < a.K - (KB - 1) * kStep ? voff : kOutside;
-  const uint8_t *ab = a.a + t.m0 * a.K, *bb = a.b + ((int64_t)t.group * a.N + t.n0) * a.K;
-  auto copy = [&](int i, int s, uint8_t* to) {
+  const uint32_t voff = (uint32_t)(l / 8) * K + chunk * 16;
+  const uint32_t vlast = chunk * 16 < K - (KB - 1) * kStep ? voff : kOutside;
+  const uint8_t* ab = uniform_ptr(a.a + t.m0 * K);
+  const uint8_t* bb = uniform_ptr(a.b + ((int64_t)t.group * N + t.n0) * K);
+  auto copy = [&](int i, int s, uint8_t* to) __attribute__((always_inline)) {
     const int item = W * i, p = item / kGroups, grp = item % kGroups;      // (compile-time), + w
     const bool of_a = grp < kOfA;
     const int kb = s * P + p;
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(of_a ? ab : bb), (short)0, kb < KB ? (of_a ? rows : cols) * a.K : 0, 0x00020000);
+        (void*)(of_a ? ab : bb), (short)0, kb < KB ? (of_a ? rows : cols) * K : 0, 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(to + p * kPart + (grp + w) * 1024), 16,
-                                             kb + 1 < KB ? voff : vlast, ((of_a ? grp : grp - kOfA) + w) * 8 * a.K + kb * kStep, 0, 0);
+                                             kb + 1 < KB ? voff : vlast, ((of_a ? grp : grp - kOfA) + w) * 8 * K + kb * kStep, 0, 0);
   };
   const int sw = (r / 2) % 8;
   const int o0 = (g ^ sw) * 16 + r * kStep, o1 = ((g + 4) ^ sw) * 16 + r * kStep;
@@ -91,7 +104,7 @@ __device__ __forceinline__ void int8_tile(const Int8Args& a, const TileAt& at, u
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[j][i] = i32x4{0, 0, 0, 0};
-  auto turn = [&]() {
+  auto turn = [&]() __attribute__((always_inline)) {
     // the stage's products stay before the wait: nothing else ties them to it
 #pragma unroll
     for (int j = 0; j < NT; ++j)
@@ -101,7 +114,7 @@ __device__ __forceinline__ void int8_tile(const Int8Args& a, const TileAt& at, u
     stage_barrier<(D - 2) * kCopies>();
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto stage = [&](int s, const uint8_t* from, uint8_t* to) {
+  auto stage = [&](int s, const uint8_t* from, uint8_t* to) __attribute__((always_inline)) {
     int next = 0;
     if constexpr (SPREAD == 0) {
 #pragma unroll
@@ -112,30 +125,31 @@ __device__ __forceinline__ void int8_tile(const Int8Args& a, const TileAt& at, u
     for (int p = 0; p < P; ++p) {
       if (P > 1 && s * P + p >= KB) break;
       const uint8_t *sa = from + p * kPart, *sb = sa + BM * kStep;
-      u32x4 af[MT][2], b[2][2];
-      auto weights = [&](int j) {
-        b[j % 2][0] = *reinterpret_cast<const u32x4*>(sb + (wn * NT + j) * 16 * kStep + o0);
-        b[j % 2][1] = *reinterpret_cast<const u32x4*>(sb + (wn * NT + j) * 16 * kStep + o1);
+      // The first 64 K-values of all columns, then the other 64: one half's rows
+      // are in registers while the other half's arrive, a few before each column.
+      u32x4 af[2][MT], b[2];
+      auto rows_of = [&](int h, int i) __attribute__((always_inline)) { af[h][i] = *reinterpret_cast<const u32x4*>(sa + (wm * MT + i) * 16 * kStep + (h ? o1 : o0)); };
+      auto cols_of_half = [&](int at) __attribute__((always_inline)) {
+        b[at % 2] = *reinterpret_cast<const u32x4*>(sb + (wn * NT + at % NT) * 16 * kStep + (at / NT ? o1 : o0));
       };
-      weights(0);
+      cols_of_half(0);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        af[i][0] = *reinterpret_cast<const u32x4*>(sa + (wm * MT + i) * 16 * kStep + o0);
-        af[i][1] = *reinterpret_cast<const u32x4*>(sa + (wm * MT + i) * 16 * kStep + o1);
-      }
+      for (int i = 0; i < MT; ++i) rows_of(0, i);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        if (j + 1 < NT) weights(j + 1);
+      for (int at = 0; at < 2 * NT; ++at) {
+        const int h = at / NT, j = at % NT;
+        if (at + 1 < 2 * NT) cols_of_half(at + 1);
+        if (h == 0) {
+#pragma unroll
+          for (int i = j * MT / NT; i < (j + 1) * MT / NT; ++i) rows_of(1, i);
+        }
         if constexpr (SPREAD > 0) {
 #pragma unroll
           for (int c = 0; c < SPREAD; ++c)
             if (next < kCopies) copy(next++, s + D - 1, to);
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          mfma64(acc[j][i], b[j % 2][0], af[i][0]);
-          mfma64(acc[j][i], b[j % 2][1], af[i][1]);
-        }
+        for (int i = 0; i < MT; ++i) mfma64(acc[j][i], b[at % 2], af[h][i]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -159,19 +173,23 @@ __device__ __forceinline__ void int8_tile(const Int8Args& a, const TileAt& at, u
     stage(s + u, slot[u], slot[(u + D - 1) % D]);
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);              // no copy outlives the tile
+  void* const y = a.y;
+  const float *as = a.as + t.m0, *bs = a.bs + (int64_t)t.group * N;
+  // all scales before the first store: a load behind stores waits for them too
+  float ws[NT][4], sa[MT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) scales4(bs, N, t.n0 + (wn * NT + j) * 16 + 4 * g, ws[j]);
+#pragma unroll
+  for (int i = 0; i < MT; ++i) sa[i] = as[(wm * MT + i) * 16 + r < rows ? (wm * MT + i) * 16 + r : 0];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int row = (wm * MT + i) * 16 + r;
-    if (row >= rows) continue;
-    const float sa = a.as[t.m0 + row];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int n = t.n0 + (wn * NT + j) * 16 + 4 * g;
-      float ws[4], v[4];
-      scales4(a, t.group, n, ws);
+      float v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = (float)acc[j][i][k] * ws[k] * sa;
-      put4<E>(a, t.m0 + row, n, v);
+      for (int k = 0; k < 4; ++k) v[k] = (float)acc[j][i][k] * ws[j][k] * sa[i];
+      if (row < rows) put4<E>(y, N, t.m0 + row, t.n0 + (wn * NT + j) * 16 + 4 * g, v);
     }
   }
   __syncthreads();      // the next tile of this workgroup writes the stages again
@@ -200,10 +218,10 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     TileAt t;
     if (k < n[0]) {
       if (!find_tile(a, kFull, first[0] + k, t)) break;
-      int8_tile<E, 4, 2, 4, 8, 2, 1, 2>(a, t, slot);
+      int8_tile<E, 4, 2, 4, 8, 2, 1, 1>(a, t, slot);
     } else {
       if (!find_tile(a, kHalf, first[1] + k - n[0], t)) break;
-      int8_tile<E, 4, 2, 2, 8, 2, 1, 2>(a, t, slot);
+      int8_tile<E, 4, 2, 2, 8, 2, 1, 1>(a, t, slot);
     }
   }
 }
@@ -280,10 +298,10 @@ __device__ __forceinline__ void finish_columns(const Int8Args& a, const i32x4& a
   if (tid >= 64 || r >= rows) return;
   const i32x4 sum = red[0][l] + red[1][l] + red[2][l] + red[3][l];
   float ws[4], v[4];
-  scales4(a, 0, n0 + 4 * g, ws);
+  scales4(a.bs, a.N, n0 + 4 * g, ws);
 #pragma unroll
   for (int k = 0; k < 4; ++k) v[k] = (float)sum[k] * ws[k] * sa;
-  put4<E>(a, m0 + r, n0 + 4 * g, v);
+  put4<E>(a.y, a.N, m0 + r, n0 + 4 * g, v);
 }
 
 // rows of codes in memory
