@@ -714,7 +714,8 @@ typedef struct mm_int8_problem {
 
 typedef struct mm_int8_plan {
   mm_int8_problem prob;
-  int64_t workspace_bytes;   /* of mm_int8_linear (codes and scales of the rows) */
+  int64_t workspace_bytes;   /* of mm_int8_linear with group arrays (codes and scales of the rows) */
+  int64_t dense_workspace_bytes; /* without them; 0 where the product quantises the rows itself */
   uint64_t checksum;
   int64_t reserved[4];
 } mm_int8_plan;
@@ -729,6 +730,7 @@ mm_status mm_int8_plan_create(const mm_int8_problem* problem, mm_int8_plan* plan
  *   b_scale        device f32 [G][N] (4-byte aligned will do unless N % 4 is 0)
  *   group_offsets, group_counts  as in mm_block_gemm
  *   y              device [M][N] of y_element out; must not overlap an input
+ *   workspace      device, as the plan says (NULL if 0)
  */
 mm_status mm_int8_gemm(const mm_int8_plan* plan, const int8_t* a, const float* a_scale, const int8_t* b,
                        const float* b_scale, const int32_t* group_offsets, const int32_t* group_counts, void* y,

@@ -167,6 +167,7 @@ class MMInt8Plan(ctypes.Structure):
     _fields_ = [
         ("prob", MMInt8Problem),
         ("workspace_bytes", ctypes.c_int64),
+        ("dense_workspace_bytes", ctypes.c_int64),
         ("checksum", ctypes.c_uint64),
         ("reserved", ctypes.c_int64 * 4),
     ]
@@ -460,7 +461,7 @@ def mm_int8_gemm(plan, a, a_scale, b, b_scale, group_offsets, group_counts, y, s
 def mm_int8_linear(plan, x, b, b_scale, group_offsets, group_counts, y, workspace, stream=None):
     _check("mm_int8_linear", load().mm_int8_linear(
         ctypes.byref(plan), _ptr(x), _ptr(b), _ptr(b_scale), _ptr(group_offsets), _ptr(group_counts), _ptr(y),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def mm_read_device_error(plan, workspace, stream=None) -> int:

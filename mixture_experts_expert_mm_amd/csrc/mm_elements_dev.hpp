@@ -58,6 +58,24 @@ __device__ __forceinline__ void store_elems(E* p, const float (&f)[8]) {
   }
 }
 
+// eight neighbours as they are in memory
+template <typename E>
+struct Raw8 {
+  u32x4 v[sizeof(E) / 2];
+  __device__ __forceinline__ void load(const E* p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(E) / 2; ++i) v[i] = reinterpret_cast<const u32x4*>(p)[i];
+  }
+  __device__ __forceinline__ void unpack(float (&f)[8]) const {
+    if constexpr (sizeof(E) == 2) {
+      Elems<E, 8>::unpack(v[0], f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i / 4][i % 4]);
+    }
+  }
+};
+
 // Largest magnitude so far, as float bits: integer order is magnitude order,
 // and a NaN is above infinity.
 __device__ __forceinline__ uint32_t amax_of(float v, uint32_t m) {

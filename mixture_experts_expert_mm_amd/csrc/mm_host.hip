@@ -1178,6 +1178,7 @@ mm_status mm_int8_plan_create(const mm_int8_problem* problem, mm_int8_plan* plan
   std::memset(&pl, 0, sizeof(pl));
   pl.prob = p;
   pl.workspace_bytes = align_up(p.rows * p.in_features, kAlign) + align_up(p.rows * 4, kAlign);
+  pl.dense_workspace_bytes = int8_from_x(int8_args(p, nullptr, nullptr, nullptr, nullptr, nullptr)) ? 0 : pl.workspace_bytes;
   pl.checksum = plan_checksum(&pl);
   *plan = pl;
   return MM_OK;
@@ -1201,9 +1202,11 @@ mm_status mm_int8_linear(const mm_int8_plan* plan, const void* x, const int8_t* 
                          uint64_t workspace_bytes, void* stream) {
   MM_TRY(check_plan(plan));
   const mm_int8_problem& p = plan->prob;
-  if (!ok16(x) || !ok16(b) || !int8_scale_ok(p, b_scale) || !ok16(y) || !ok16(workspace)) return MM_ERR_INVALID_ARG;
+  if (!ok16(x) || !ok16(b) || !int8_scale_ok(p, b_scale) || !ok16(y)) return MM_ERR_INVALID_ARG;
   if (!block_groups_ok(p, group_offsets, group_counts)) return MM_ERR_INVALID_ARG;
-  if ((int64_t)workspace_bytes < plan->workspace_bytes) return MM_ERR_WORKSPACE;
+  const int64_t need = group_offsets ? plan->workspace_bytes : plan->dense_workspace_bytes;
+  if (need > 0 && !ok16(workspace)) return MM_ERR_INVALID_ARG;
+  if ((int64_t)workspace_bytes < need) return MM_ERR_WORKSPACE;
   Int8Args g = int8_args(p, b, b_scale, group_offsets, group_counts, y);
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (int8_from_x(g)) {

@@ -24,6 +24,10 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 constexpr int kStep = 128;           // K-values (bytes) of a row that a part of a stage holds
 constexpr int kFewRows = 16;         // most rows of a streaming unit
 constexpr int kFewCols = 16;
+// Most rows of a product that are streamed; us, streamed / tiles of 32 x 32: 1 row x 4096 x 7168 8.4 / 10.1, 7168 x 2048
+// 6.9 / 6.0, 16384 x 4096 17.5 / 18.7; 8 rows x 4096 x 7168 9.7 / 10.3; 16 rows 11.2 / 10.3, 7168 x 2048 9.1 / 6.2
+constexpr int kStreamRows = 8;
+constexpr int kQuantThreads = 512;
 constexpr uint32_t kOutside = 0x7fffff00u;   // an offset beyond every descriptor: arrives as zeros
 
 // 16 x 16 outputs, 64 K-values: each lane supplies 16 bytes of its A row and B
@@ -249,16 +253,16 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_ring(Int8Args a) {
 
 namespace {
 
-constexpr int kRowThreads = 256, kRowWaves = 4, kDeep = 4;
+constexpr int kDeep = 4;
 
 // The weights of 16 columns from memory, `kDeep` steps of 128 K-values in
-// flight a wave, the four waves taking every fourth step; rows from `x` with a
-// pitch.  Returns a wave's sums.
-template <typename Rows>
+// flight a wave, the W waves taking steps in turn.  Returns a wave's sums.
+template <int W, typename Rows>
 __device__ __forceinline__ i32x4 stream_columns(const Int8Args& a, int n0, int w, int l, const Rows& rows) {
-  const int r = l % 16, g = l / 16, KB = (a.K + kStep - 1) / kStep;
-  const uint8_t* bp = a.b + (int64_t)(n0 + r < a.N ? n0 + r : a.N - 1) * a.K;
+  const int r = l % 16, g = l / 16, K = a.K, KB = (K + kStep - 1) / kStep;
+  const uint8_t* bp = a.b + (int64_t)(n0 + r < a.N ? n0 + r : a.N - 1) * K;
   u32x4 b[kDeep][2];
+  typename Rows::Ahead x[kDeep][2];
   // past the end: the last step again, unused (a load under a condition would
   // make the compiler wait for all of them); past K inside the last step: the
   // row's first values, which meet zeros
@@ -267,36 +271,42 @@ __device__ __forceinline__ i32x4 stream_columns(const Int8Args& a, int n0, int w
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int k = kb * kStep + g * 32 + h * 16;
-      b[d][h] = *reinterpret_cast<const u32x4*>(bp + (k < a.K ? k : 0));
+      b[d][h] = *reinterpret_cast<const u32x4*>(bp + (k < K ? k : 0));
+      rows.ask(x[d][h], k < K ? k : 0);
     }
   };
 #pragma unroll
-  for (int d = 0; d < kDeep; ++d) load(d, w + d * kRowWaves);
+  for (int d = 0; d < kDeep; ++d) load(d, w + d * W);
   rows.bring();
   i32x4 acc = {0, 0, 0, 0};
-  for (int k0 = w; k0 < KB; k0 += kDeep * kRowWaves) {
+  for (int k0 = w; k0 < KB; k0 += kDeep * W) {
 #pragma unroll
     for (int d = 0; d < kDeep; ++d) {
-      const int kb = k0 + d * kRowWaves;
+      const int kb = k0 + d * W;
       if (kb < KB) {
-        mfma64(acc, b[d][0], rows.at(kb * kStep + g * 32));
-        mfma64(acc, b[d][1], rows.at(kb * kStep + g * 32 + 16));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = kb * kStep + g * 32 + h * 16;
+          mfma64(acc, b[d][h], rows.at(x[d][h], k, k < K));
+        }
       }
-      load(d, kb + kDeep * kRowWaves);
+      load(d, kb + kDeep * W);
     }
   }
   return acc;
 }
 
-// sums of the four waves, scaled and written
-template <typename E>
+// sums of the waves, scaled and written
+template <typename E, int W>
 __device__ __forceinline__ void finish_columns(const Int8Args& a, const i32x4& acc, int n0, int64_t m0, int rows, float sa,
                                                i32x4 (*red)[64]) {
   const int tid = threadIdx.x, w = tid / 64, l = tid % 64, r = l % 16, g = l / 16;
   red[w][l] = acc;
   __syncthreads();
   if (tid >= 64 || r >= rows) return;
-  const i32x4 sum = red[0][l] + red[1][l] + red[2][l] + red[3][l];
+  i32x4 sum = red[0][l];
+#pragma unroll
+  for (int i = 1; i < W; ++i) sum += red[i][l];
   float ws[4], v[4];
   scales4(a.bs, a.N, n0 + 4 * g, ws);
 #pragma unroll
@@ -304,28 +314,28 @@ __device__ __forceinline__ void finish_columns(const Int8Args& a, const i32x4& a
   put4<E>(a.y, a.N, m0 + r, n0 + 4 * g, v);
 }
 
-// rows of codes in memory
+// rows of codes in memory, asked for with the weights of their step
 struct RowsOfCodes {
+  typedef u32x4 Ahead;
   const uint8_t* p;
-  int K;
   __device__ void bring() const {}
-  __device__ u32x4 at(int k) const {
-    return k < K ? *reinterpret_cast<const u32x4*>(p + k) : u32x4{0u, 0u, 0u, 0u};
-  }
+  __device__ void ask(u32x4& x, int k) const { x = *reinterpret_cast<const u32x4*>(p + k); }
+  __device__ u32x4 at(const u32x4& x, int, bool in) const { return in ? x : u32x4{0u, 0u, 0u, 0u}; }
 };
 
 }  // namespace
 
-// The last rows of one matrix, up to 16 (a.m_first and on): 16 columns a
-// workgroup, weights straight from memory into the operands.
+// Up to 16 rows of one matrix (a.m_first and on): 16 columns a workgroup, weights
+// straight from memory into the operands.
 template <typename E>
-__global__ __launch_bounds__(kRowThreads) void k_int8_few(Int8Args a) {
-  __shared__ i32x4 red[kRowWaves][64];
+__global__ __launch_bounds__(256) void k_int8_few(Int8Args a) {
+  constexpr int W = 4;
+  __shared__ i32x4 red[W][64];
   const int l = threadIdx.x % 64, w = uniform(threadIdx.x / 64), n0 = (int)blockIdx.x * kFewCols;
   const int rows = (int)(a.M - a.m_first);
   const int64_t row = a.m_first + (l % 16 < rows ? l % 16 : 0);
-  const i32x4 acc = stream_columns(a, n0, w, l, RowsOfCodes{a.a + row * a.K, a.K});
-  finish_columns<E>(a, acc, n0, a.m_first, rows, a.as[row], red);
+  const i32x4 acc = stream_columns<W>(a, n0, w, l, RowsOfCodes{a.a + row * a.K});
+  finish_columns<E, W>(a, acc, n0, a.m_first, rows, a.as[row], red);
 }
 
 namespace {
@@ -335,30 +345,31 @@ constexpr int kRowValues = 8 * 1024;
 
 // Rows of x, quantised into LDS by the whole workgroup: values in registers, a
 // maximum per row, then the codes.
-template <typename X>
+template <typename X, int THREADS>
 struct RowsOfX {
+  struct Ahead {};
   const Int8Args& a;
   uint8_t* codes;              // [M][pitch], zeros from K to the step's end
   float* scale;                // [M]
   uint32_t* amax;              // [M]
   int pitch, row;
   __device__ void bring() const {
-    constexpr int kTurns = kRowValues / 8 / kRowThreads;
+    constexpr int kTurns = kRowValues / 8 / THREADS;
     const int tid = threadIdx.x, M = (int)a.M, per = a.K / 8, pad = (pitch - a.K) / 8;
     const X* x = static_cast<const X*>(a.x);
     float v[kTurns][8];
 #pragma unroll
     for (int u = 0; u < kTurns; ++u) {
-      const int i = tid + u * kRowThreads;
+      const int i = tid + u * THREADS;
       if (i < M * per) load_elems(x + (int64_t)i * 8, v[u]);
     }
     if (tid < M) amax[tid] = 0;
-    for (int i = tid; i < M * pad; i += kRowThreads)
+    for (int i = tid; i < M * pad; i += THREADS)
       *reinterpret_cast<u32x2*>(codes + i / pad * pitch + a.K + i % pad * 8) = u32x2{0u, 0u};
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kTurns; ++u) {
-      const int i = tid + u * kRowThreads;
+      const int i = tid + u * THREADS;
       if (i - tid % 64 >= M * per) break;            // (the same in all lanes of a wave)
       uint32_t m = 0;
       const int mine = i < M * per ? i / per : -1;
@@ -377,75 +388,80 @@ struct RowsOfX {
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kTurns; ++u) {
-      const int i = tid + u * kRowThreads;
+      const int i = tid + u * THREADS;
       if (i >= M * per) break;
       *reinterpret_cast<u32x2*>(codes + i / per * pitch + i % per * 8) = int8_codes(v[u], int8_scale(amax[i / per]));
     }
     if (tid < M) scale[tid] = int8_scale(amax[tid]);
     __syncthreads();
   }
-  __device__ u32x4 at(int k) const { return *reinterpret_cast<const u32x4*>(codes + row * pitch + k); }
+  __device__ void ask(Ahead&, int) const {}
+  __device__ u32x4 at(const Ahead&, int k, bool) const { return *reinterpret_cast<const u32x4*>(codes + row * pitch + k); }
 };
 
 }  // namespace
 
 // A few floating rows (a decoded token's projection): 16 columns a workgroup;
 // the first weights are asked for, the rows are quantised into LDS meanwhile.
-template <typename E, typename X>
-__global__ __launch_bounds__(kRowThreads) void k_int8_rows(Int8Args a) {
+template <typename E, typename X, int W>
+__global__ __launch_bounds__(64 * W) void k_int8_rows(Int8Args a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
-  __shared__ i32x4 red[kRowWaves][64];
+  __shared__ i32x4 red[W][64];
   __shared__ float scale[kFewRows];
   __shared__ uint32_t amax[kFewRows];
   const int l = threadIdx.x % 64, w = uniform(threadIdx.x / 64), n0 = (int)blockIdx.x * kFewCols, M = (int)a.M;
   const int pitch = (a.K + kStep - 1) / kStep * kStep + 16;      // rows of one column of chunks in different banks
   const int row = l % 16 < M ? l % 16 : 0;
-  const i32x4 acc = stream_columns(a, n0, w, l, RowsOfX<X>{a, dyn, scale, amax, pitch, row});
-  finish_columns<E>(a, acc, n0, 0, M, scale[row], red);
+  const i32x4 acc = stream_columns<W>(a, n0, w, l, RowsOfX<X, 64 * W>{a, dyn, scale, amax, pitch, row});
+  finish_columns<E, W>(a, acc, n0, 0, M, scale[row], red);
 }
 
-// Codes and scales of rows: PER threads a row, its values in registers while
-// they fit.  Bound: HBM.
-template <typename X, int PER>
-__global__ __launch_bounds__(kRowThreads) void k_int8_quantize(const X* x, int64_t rows, int K, uint8_t* q, float* s) {
-  constexpr int kHeld = 8;                  // chunks of 8 values that a thread holds
-  __shared__ uint32_t red[kRowWaves];
-  const int sub = threadIdx.x / PER, at = threadIdx.x % PER, per = K / 8;
-  for (int64_t m0 = (int64_t)blockIdx.x * (kRowThreads / PER); m0 < rows; m0 += (int64_t)gridDim.x * (kRowThreads / PER)) {
-    const int64_t m = m0 + sub;
-    const bool live = m < rows;
+// Codes and scales of rows: a wave a row (GROUP false), or a workgroup whose size
+// the launch fits to the row; TURNS chunks of 8 values a thread in registers, as
+// they are in memory; longer rows are read twice.  Bound: HBM.
+template <typename X, bool GROUP, int TURNS>
+__global__ __launch_bounds__(kQuantThreads) void k_int8_quantize(const X* x, int64_t rows, int K, uint8_t* q, float* s) {
+  __shared__ uint32_t red[kQuantThreads / 64];
+  const int waves = blockDim.x / 64, w = threadIdx.x / 64, per = K / 8;
+  const int at = GROUP ? threadIdx.x : threadIdx.x % 64, step = GROUP ? blockDim.x : 64, rows_at_once = GROUP ? 1 : waves;
+  for (int64_t m0 = (int64_t)blockIdx.x * rows_at_once; m0 < rows; m0 += (int64_t)gridDim.x * rows_at_once) {
+    int64_t m = GROUP ? m0 : m0 + w;
+    m = m < rows ? m : rows - 1;             // (past the end: the last row again)
     const X* p = x + m * K;
-    float v[kHeld][8];
+    Raw8<X> v[TURNS];
     uint32_t big = 0;
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u)
-      if (live && at + u * PER < per) load_elems(p + (at + u * PER) * 8, v[u]);
+    for (int u = 0; u < TURNS; ++u) v[u].load(p + (at + u * step < per ? at + u * step : 0) * 8);
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u)
-      if (live && at + u * PER < per) {
+    for (int u = 0; u < TURNS; ++u) {
+      float f[8];
+      v[u].unpack(f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) big = amax_of(v[u][j], big);
-      }
-    for (int c = at + kHeld * PER; live && c < per; c += PER) {
+      for (int j = 0; j < 8; ++j) big = amax_of(f[j], big);
+    }
+    for (int c = at + TURNS * step; c < per; c += step) {
       float f[8];
       load_elems(p + c * 8, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) big = amax_of(f[j], big);
     }
     big = wave_max(big);
-    if constexpr (PER > 64) {
+    if constexpr (GROUP) {
       __syncthreads();                      // (the last row's maximum has been read)
-      if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = big;
+      if (threadIdx.x % 64 == 0) red[w] = big;
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kRowWaves; ++i) big = red[i] > big ? red[i] : big;
+      for (int i = 0; i < waves; ++i) big = red[i] > big ? red[i] : big;
     }
     const float sc = int8_scale(big);
-    if (live && at == 0) s[m] = sc;
+    if (at == 0) s[m] = sc;
 #pragma unroll
-    for (int u = 0; u < kHeld; ++u)
-      if (live && at + u * PER < per) *reinterpret_cast<u32x2*>(q + m * K + (at + u * PER) * 8) = int8_codes(v[u], sc);
-    for (int c = at + kHeld * PER; live && c < per; c += PER) {
+    for (int u = 0; u < TURNS; ++u) {
+      float f[8];
+      v[u].unpack(f);
+      const u32x2 o = int8_codes(f, sc);
+      if (at + u * step < per) *reinterpret_cast<u32x2*>(q + m * K + (at + u * step) * 8) = o;
+    }
+    for (int c = at + TURNS * step; c < per; c += step) {
       float f[8];
       load_elems(p + c * 8, f);
       *reinterpret_cast<u32x2*>(q + m * K + c * 8) = int8_codes(f, sc);
@@ -467,16 +483,19 @@ hipError_t gemm(const Int8Args& args, int num_cus, hipStream_t s) {
   if (a.x != nullptr) {
     const size_t lds = (size_t)a.M * ((a.K + kStep - 1) / kStep * kStep + 16);
     return for_type(a.x_element, [&](auto x) {
-      hipLaunchKernelGGL((k_int8_rows<E, decltype(x)>), dim3(units), dim3(kRowThreads), lds, s, a);
+      // eight waves where each then has all its steps in flight (1 row, us, four / eight waves: 7168 x 2048 7.7 / 9.7,
+      // 16384 x 4096 18.4 / 21.0, 4096 x 7168 13.8 / 12.1)
+      if (a.K <= 32 * kStep) hipLaunchKernelGGL((k_int8_rows<E, decltype(x), 4>), dim3(units), dim3(256), lds, s, a);
+      else hipLaunchKernelGGL((k_int8_rows<E, decltype(x), 8>), dim3(units), dim3(512), lds, s, a);
       return hipGetLastError();
     });
   }
   const int64_t even = a.M / a.G > 0 ? a.M / a.G : 1;
   const unsigned cus = (unsigned)((num_cus + 7) / 8 * 8);
   auto count = [&](int c) { return (even + most_rows(c) - 1) / most_rows(c) * a.G * ((a.N + cols_of(c) - 1) / cols_of(c)); };
-  if (a.offsets == nullptr && a.M <= kFewRows) {
+  if (a.offsets == nullptr && a.M <= kStreamRows) {
     a.m_first = 0;
-    hipLaunchKernelGGL(k_int8_few<E>, dim3(units), dim3(kRowThreads), 0, s, a);
+    hipLaunchKernelGGL(k_int8_few<E>, dim3(units), dim3(256), 0, s, a);
   } else if (count(k32x32) <= num_cus) {
     hipLaunchKernelGGL((k_int8_ring<E, k32x32, 2, 2, 1, 1, 4>), dim3(cus), dim3(256), 0, s, a);
   } else if (count(k64x32) <= num_cus) {
@@ -494,7 +513,7 @@ hipError_t gemm(const Int8Args& args, int num_cus, hipStream_t s) {
     if (err != hipSuccess || a.M == args.M) return err;
     a.m_first = a.M;
     a.M = args.M;
-    hipLaunchKernelGGL(k_int8_few<E>, dim3(units), dim3(kRowThreads), 0, s, a);
+    hipLaunchKernelGGL(k_int8_few<E>, dim3(units), dim3(256), 0, s, a);
   }
   return hipGetLastError();
 }
@@ -510,15 +529,21 @@ hipError_t launch_int8_gemm(const Int8Args& a, int num_cus, hipStream_t s) {
 hipError_t launch_int8_quantize(const void* x, int element, int64_t rows, int cols, uint8_t* q, float* s, hipStream_t st) {
   return for_type(element, [&](auto e) {
     typedef decltype(e) X;
-    if (cols <= 4096) {
-      const int64_t n = (rows + 3) / 4;
-      hipLaunchKernelGGL((k_int8_quantize<X, 64>), dim3((unsigned)(n < (1 << 20) ? n : (1 << 20))), dim3(kRowThreads), 0, st,
+    const int chunks = cols / 8;
+    auto run = [&](auto group, auto turns, int threads) {
+      const int64_t n = decltype(group)::value ? rows : (rows + 3) / 4;
+      hipLaunchKernelGGL((k_int8_quantize<X, decltype(group)::value, decltype(turns)::value>),
+                         dim3((unsigned)(n < (1 << 20) ? n : (1 << 20))), dim3((unsigned)threads), 0, st,
                          static_cast<const X*>(x), rows, cols, q, s);
-    } else {
-      hipLaunchKernelGGL((k_int8_quantize<X, kRowThreads>), dim3((unsigned)(rows < (1 << 20) ? rows : (1 << 20))),
-                         dim3(kRowThreads), 0, st, static_cast<const X*>(x), rows, cols, q, s);
-    }
-    return hipGetLastError();
+      return hipGetLastError();
+    };
+    typedef std::integral_constant<int, 2> Two;
+    typedef std::integral_constant<int, 4> Four;
+    // a wave a row up to 2048 columns; beyond, two chunks a thread while a workgroup has enough of them
+    if (chunks <= 2 * 64) return run(std::false_type{}, Two{}, 256);
+    if (chunks <= 4 * 64) return run(std::false_type{}, Four{}, 256);
+    if (chunks <= 2 * kQuantThreads) return run(std::true_type{}, Two{}, (chunks + 127) / 128 * 64);
+    return run(std::true_type{}, Four{}, kQuantThreads);
   });
 }
 

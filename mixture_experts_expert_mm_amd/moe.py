@@ -554,7 +554,7 @@ def sort_tokens(x, topk_ids, num_experts, *, active=None, stream=None):
         rows = torch.empty((R, H), dtype=x.dtype, device=dev)
         # one allocation for the four
         counts, offsets, row, route = (torch.empty if T else torch.zeros)(
-            2 * (E + R) + 1, dtype=torch.int32, device=dev).split((E, E + 1, R, R))
+            2 * (E + R) + 1, dtype=torch.int32, device=dev).split_with_sizes((E, E + 1, R, R))
         order = TokenOrder(counts, offsets, row.view(T, K), route)
         if T:
             ws = _workspace(plan.workspace_bytes, dev) if plan.workspace_bytes else None
@@ -767,5 +767,6 @@ def int8_linear(x, w, ws, offsets=None, counts=None, *, y_dtype="bf16", y=None, 
         if y is None:
             y = torch.empty((M, N), dtype=dt, device=dev)
         if M:
-            B.mm_int8_linear(plan, x, w, ws, offsets, counts, y, _workspace(plan.workspace_bytes, dev), _raw_stream(dev))
+            n = plan.dense_workspace_bytes if offsets is None else plan.workspace_bytes
+            B.mm_int8_linear(plan, x, w, ws, offsets, counts, y, _workspace(n, dev) if n else None, _raw_stream(dev))
     return y

@@ -33,8 +33,11 @@ def test_plan_refuses(dims):
 
 
 def test_plan():
-    assert ctypes.sizeof(B.MMInt8Problem) == 40 and ctypes.sizeof(B.MMInt8Plan) == 40 + 8 + 8 + 32
-    assert B.mm_int8_plan_create(5, 1, 131056).workspace_bytes >= 5 * 131060
+    assert ctypes.sizeof(B.MMInt8Problem) == 40 and ctypes.sizeof(B.MMInt8Plan) == 40 + 16 + 8 + 32
+    p = B.mm_int8_plan_create(5, 1, 131056)
+    assert p.workspace_bytes >= 5 * 131060 and p.dense_workspace_bytes == p.workspace_bytes
+    p = B.mm_int8_plan_create(2, 64, 4096)                         # few rows: quantised inside the product, unless in groups
+    assert p.workspace_bytes >= 2 * 4100 and p.dense_workspace_bytes == 0
     for kw in (dict(x_element=3), dict(y_element=3), dict(x_element=-1), dict(y_element=4)):
         with pytest.raises(B.MMError) as ei:
             B.mm_int8_plan_create(4, 16, 16, **kw)
@@ -55,7 +58,7 @@ def test_entry_points_validate_before_any_hip_call(lib):
         assert call(lib.mm_int8_quantize, args, i, v) == 1
     for v in (-1, 3):
         assert call(lib.mm_int8_quantize, args, 2, v) == 2
-    p, gp = B.mm_int8_plan_create(4, 10, 32), B.mm_int8_plan_create(4, 10, 32, 3)
+    p, gp = B.mm_int8_plan_create(40, 10, 32), B.mm_int8_plan_create(40, 10, 32, 3)
     bad = B.MMInt8Plan.from_buffer_copy(p)
     bad.prob.rows = 5
     args = [P(p), GOOD, GOOD, GOOD, GOOD, None, None, GOOD, None]
@@ -66,6 +69,8 @@ def test_entry_points_validate_before_any_hip_call(lib):
         assert call(lib.mm_int8_gemm, args, i, GOOD) == 1
     for v in (P(bad), P(gp), None):                                # (several groups need their rows)
         assert call(lib.mm_int8_gemm, args, 0, v) == 1
+    wide = B.mm_int8_plan_create(40, 12, 32)                       # scales of whole vectors are read as such
+    assert call(lib.mm_int8_gemm, [P(wide)] + args[1:], 4, GOOD + 4) == 1
     args = [P(p), GOOD, GOOD, GOOD, None, None, GOOD, GOOD, 1 << 40, None]
     for i in (1, 2, 3, 6, 7):
         assert call(lib.mm_int8_linear, args, i, None) == 1
@@ -95,8 +100,12 @@ def test_what_is_launched(launches):
         assert y.shape == (5, 7) and y.dtype == dt and launches[-1][1][0].prob.y_element == B.ELEMENT[dt]
     y = torch.zeros(5, 7, dtype=torch.bfloat16)
     assert moe.int8_linear(x, w, ws, y=y) is y
-    plan = launches[-1][1][0]
-    assert plan.prob.x_element == B.MM_ELEMENT_F16 and launches[-1][1][7].numel() == plan.workspace_bytes
+    assert launches[-1][1][0].prob.x_element == B.MM_ELEMENT_F16 and launches[-1][1][7] is None
+    one = torch.zeros(1, dtype=torch.int32)
+    for big, groups in ((torch.zeros(50, 48), ()), (x.float(), (one, one))):
+        moe.int8_linear(big, w[None] if groups else w, ws[None] if groups else ws, *groups)
+        plan = launches[-1][1][0]
+        assert plan.prob.x_element == B.MM_ELEMENT_F32 and launches[-1][1][7].numel() == plan.workspace_bytes
 
 
 def test_refusals(launches):
