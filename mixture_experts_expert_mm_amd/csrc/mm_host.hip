@@ -1051,7 +1051,7 @@ mm_status mm_sort_plan_create(const mm_sort_problem* problem, mm_sort_plan* plan
   pl.prob = p;
   const int64_t routes = p.num_tokens * p.num_topk;
   const int64_t chunk = sort_chunk(routes);
-  pl.workspace_bytes = sort_in_one(routes) ? 0 : align_up((routes + chunk - 1) / chunk * p.num_experts * 4, kAlign);
+  pl.workspace_bytes = sort_in_one(routes, p.num_topk) ? 0 : align_up((routes + chunk - 1) / chunk * p.num_experts * 4, kAlign);
   pl.checksum = plan_checksum(&pl);
   *plan = pl;
   return MM_OK;
@@ -1076,7 +1076,7 @@ mm_status mm_sort_tokens(const mm_sort_plan* plan, const int32_t* topk_ids, cons
   a.x = static_cast<const uint8_t*>(x);
   a.rows = static_cast<uint8_t*>(rows);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (sort_in_one(a.R)) return run(MM_K_SORT_ORDER, s, [&] { return launch_sort_few(a, s); });
+  if (sort_in_one(a.R, a.K)) return run(MM_K_SORT_ORDER, s, [&] { return launch_sort_few(a, s); });
   a.chunk = sort_chunk(a.R);
   a.chunks = (int)((a.R + a.chunk - 1) / a.chunk);
   a.hist = at<int32_t>(workspace, 0);

@@ -490,6 +490,14 @@ hipError_t gemm(const Int8Args& args, int num_cus, hipStream_t s) {
       return hipGetLastError();
     });
   }
+  // The smallest tiles that give a CU at most one, then those of 128 x 128 for up
+  // to two rounds, then the large ones.  us with weights from HBM, 32 x 32 / 64 x 32 /
+  // 64 x 64 / 128 x 64 / 128 x 128 / large, 4096 x 7168: 64 rows 11 / 15 / 20 / 25 / 30 /
+  // 49, 128 rows 20 / 15 / 20 / 28 / 34 / 53, 256 rows 36 / 27 / 21 / 28 / 34 / 73, 512 rows
+  // 72 / 54 / 41 / 38 / 46 / 90, 1024 rows - / - / 83 / 74 / 50 / 92, 1280 rows (320 tiles of
+  // 128 x 128) 79 / 93, 2048 rows (512) 94 / 96, 2560 rows (640) 117 / 97; 2048 to 7168: 64
+  // rows 10 / 7.7 / 9.9 / 11 / 13 / 20, 256 rows 29 / 23 / 18 / 12 / 15 / 31, 512 rows - / - / 32 /
+  // 21 / 16 / 32, 1024 rows (448) 29 / 33, 1536 rows (672) 43 / 34.
   const int64_t even = a.M / a.G > 0 ? a.M / a.G : 1;
   const unsigned cus = (unsigned)((num_cus + 7) / 8 * 8);
   auto count = [&](int c) { return (even + most_rows(c) - 1) / most_rows(c) * a.G * ((a.N + cols_of(c) - 1) / cols_of(c)); };
@@ -502,7 +510,9 @@ hipError_t gemm(const Int8Args& args, int num_cus, hipStream_t s) {
     hipLaunchKernelGGL((k_int8_ring<E, k64x32, 2, 2, 2, 1, 4>), dim3(cus), dim3(256), 0, s, a);
   } else if (count(k64x64) <= num_cus) {
     hipLaunchKernelGGL((k_int8_ring<E, k64x64, 2, 2, 2, 2, 4>), dim3(cus), dim3(256), 0, s, a);
-  } else if (count(k128x128) <= num_cus) {
+  } else if (count(kMid) <= num_cus) {
+    hipLaunchKernelGGL((k_int8_ring<E, kMid, 4, 2, 2, 2, 2>), dim3(cus), dim3(512), 0, s, a);
+  } else if (count(k128x128) <= 2 * num_cus) {
     hipLaunchKernelGGL((k_int8_ring<E, k128x128, 4, 2, 2, 4, 2>), dim3(cus), dim3(512), 0, s, a);
   } else {
     // one matrix: up to 16 rows beyond the blocks of 256 are streamed

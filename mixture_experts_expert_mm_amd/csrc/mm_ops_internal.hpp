@@ -97,7 +97,7 @@ struct SortArgs {
 };
 int sort_chunk(int64_t routes);
 // whether launch_sort_few does it all (order and rows); else launch_sort_order, then launch_sort_rows
-bool sort_in_one(int64_t routes);
+bool sort_in_one(int64_t routes, int64_t topk);
 hipError_t launch_sort_few(const SortArgs& a, hipStream_t s);
 hipError_t launch_sort_order(const SortArgs& a, hipStream_t s);
 hipError_t launch_sort_rows(const SortArgs& a, hipStream_t s);

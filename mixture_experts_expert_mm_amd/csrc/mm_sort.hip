@@ -24,7 +24,11 @@ constexpr int kPlaceThreads = 1024;
 constexpr int kMaxThreads = 512;     // of k_combine_backward
 constexpr int kMaxTopk = 64;
 constexpr int kMost = 8;             // slots of a token that are in flight together
-constexpr int64_t kFewRoutes = 8192; // most routes of the single launch
+// Most routes of the single launch, where every workgroup reads all of them once
+// for each eight slots of its token.  us, one launch / three, rows of 7168 bf16,
+// top-8: 1 token 4.0 / 10, 64 tokens 5.4 / 12, 256 tokens 11 / 16, 512 tokens 20 / 22,
+// 1024 tokens 36 / 34; top-4 of 4096: 2048 tokens 28 / 23; top-64 of 1024: 128 tokens 85 / 21.
+constexpr int64_t kFewRoutes = 4096;
 
 __device__ __forceinline__ int key_of(const SortArgs& a, int64_t r) {
   const int e = a.ids[r];
@@ -503,7 +507,7 @@ int sort_chunk(int64_t routes) {
   return (int)((even + kPlaceThreads - 1) / kPlaceThreads * kPlaceThreads);
 }
 
-bool sort_in_one(int64_t routes) { return routes <= kFewRoutes; }
+bool sort_in_one(int64_t routes, int64_t topk) { return routes * ((topk + kMost - 1) / kMost) <= kFewRoutes; }
 
 hipError_t launch_sort_order(const SortArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(k_sort_count, dim3((unsigned)a.chunks), dim3(kThreads), 0, s, a);

@@ -42,12 +42,15 @@ def within(y, want, err, what=""):
     assert y.shape == want.shape and bool((over <= 0).all()), (what, float(over.max()), (over > 0).nonzero()[:4])
 
 
-# every kernel (up to 16 rows; tiles of 32 x 32, 64 x 32, 64 x 64, 128 x 128, 256 x 256 with a rest of 1, 16, 17, 128, 129
-# and 255 rows), K of less than a step, with a last step of every length, an even and an odd number of steps
+# every kernel (up to 8 rows; tiles of 32 x 32, 64 x 32, 64 x 64, 128 x 64, 128 x 128 for one round and two, 256 x 256 with a
+# rest of 1, 16, 17, 128, 129 and 255 rows), K of less than a step, with a last step of every length, an even and an odd
+# number of steps
 SHAPES = [(1, 1, 16), (1, 7168, 2048), (3, 5, 48), (16, 40, 144), (16, 1000, 7168), (17, 16, 128), (17, 33, 272), (31, 1001, 400),
           (64, 512, 1008), (65, 130, 640), (100, 4096, 272), (200, 1026, 896), (129, 4100, 1152), (300, 2048, 64), (512, 2052, 2064),
           (1100, 4096, 336), (2049, 2052, 400), (2064, 1999, 1280), (2065, 2048, 144), (2176, 2050, 640), (2177, 2048, 656),
-          (2303, 2111, 128), (4097, 1024, 1408), (40, 150, 8192), (24, 3, 131056)]
+          (2303, 2111, 128), (4097, 1024, 1408), (40, 150, 8192), (24, 3, 131056),
+          (2049, 4100, 400), (2064, 4099, 272), (2065, 4096, 144), (2176, 4098, 640), (2177, 4096, 656), (2303, 4223, 128), (2304, 4352, 48),
+          (600, 3500, 272), (1000, 2100, 528)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -121,7 +124,8 @@ def groups_of(G, M, seed, kind):
 
 
 @pytest.mark.parametrize("G,M,N,K", [(2, 9, 40, 144), (5, 100, 130, 272), (32, 64, 256, 640), (3, 700, 516, 1008), (8, 1500, 2049, 400),
-                                     (70, 3000, 256, 256), (4, 5000, 1024, 912), (300, 40, 64, 128), (33, 9000, 512, 384)])
+                                     (70, 3000, 256, 256), (4, 5000, 1024, 912), (300, 40, 64, 128), (33, 9000, 512, 384),
+                                     (40, 6000, 1024, 272), (9, 20000, 641, 144)])
 @pytest.mark.parametrize("kind", ["dense", "gaps"])
 def test_groups(G, M, N, K, kind):
     log(f"[int8 groups] G={G} M={M} N={N} K={K} {kind}")

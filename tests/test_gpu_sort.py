@@ -55,11 +55,11 @@ def within(y, want, err):
     assert bool((over <= 0).all()), (float(over.max()), float(want.abs().max()))
 
 
-# around the limit of the single launch (8192 routes), of a chunk (1024) and of a turn; E around the waves' and
+# around the limit of the single launch (4096 routes for each eight slots), of a chunk (1024) and of a turn; E around the waves' and
 # workgroups' sizes
 SHAPES = [(1, 8, 1, 1), (1, 7168, 32, 8), (3, 1, 5, 5), (17, 33, 8, 4), (64, 520, 1024, 64), (129, 6, 257, 3),
           (1024, 16, 64, 8), (1025, 16, 64, 8), (8193, 4, 255, 1), (2731, 3, 1000, 3), (20011, 2, 16, 5), (700, 1, 1024, 64),
-          (5000, 256, 256, 8), (40000, 8, 3, 2)]
+          (5000, 256, 256, 8), (40000, 8, 3, 2), (512, 520, 40, 8), (513, 520, 40, 8), (227, 64, 99, 9), (228, 64, 99, 9)]
 
 
 @pytest.mark.parametrize("T,H,E,K", SHAPES)
