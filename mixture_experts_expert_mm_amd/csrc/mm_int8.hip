@@ -22,7 +22,7 @@ namespace {
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr int kStep = 128;           // K-values (bytes) of a row that a part of a stage holds
-constexpr int kFewRows = 16;         // most rows of a streaming unit
+constexpr int kFewRows = 16;         // most rows that are streamed together
 constexpr int kFewCols = 16;
 // Most rows of a product that are streamed; us, streamed / tiles of 32 x 32: 1 row x 4096 x 7168 8.4 / 10.1, 7168 x 2048
 // 6.9 / 6.0, 16384 x 4096 17.5 / 18.7; 8 rows x 4096 x 7168 9.7 / 10.3; 16 rows 11.2 / 10.3, 7168 x 2048 9.1 / 6.2
@@ -201,35 +201,6 @@ __device__ __forceinline__ void int8_tile(const Int8Args& a, const TileAt& at, u
 
 }  // namespace
 
-// Products with many rows: 256 x 256 tiles, and 128 x 256 for a group's rest.
-// One workgroup a CU; XCD x takes an eighth of each class's list (neighbours
-// share an L2), and its workgroups take every n-th tile of it in turn.
-template <typename E>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_mma(Int8Args a) {
-  // separate arrays: the compiler then sees that a stage's reads and the other
-  // stage's copies do not meet, and does not wait for the copies
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[(kBM + kBN) * kStep], s1[(kBM + kBN) * kStep];
-  uint8_t* const slot[2] = {s0, s1};
-  const int x = blockIdx.x % 8, step = gridDim.x / 8;
-  int64_t n[2], first[2];
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int64_t total = count_blocks(a, c) * ((a.N + kBN - 1) / kBN);
-    first[c] = total * x / 8;
-    n[c] = total * (x + 1) / 8 - first[c];
-  }
-  for (int64_t k = blockIdx.x / 8; k < n[0] + n[1]; k += step) {
-    TileAt t;
-    if (k < n[0]) {
-      if (!find_tile(a, kFull, first[0] + k, t)) break;
-      int8_tile<E, 4, 2, 4, 8, 2, 1, 1>(a, t, slot);
-    } else {
-      if (!find_tile(a, kHalf, first[1] + k - n[0], t)) break;
-      int8_tile<E, 4, 2, 2, 8, 2, 1, 1>(a, t, slot);
-    }
-  }
-}
-
 // Products whose large tiles would leave most CUs without one: tiles of class c.
 template <typename E, int C, int WM, int WN, int MT, int NT, int D>
 __global__ __launch_bounds__(64 * WM * WN) void k_int8_ring(Int8Args a) {
@@ -303,15 +274,17 @@ __device__ __forceinline__ void finish_columns(const Int8Args& a, const i32x4& a
   const int tid = threadIdx.x, w = tid / 64, l = tid % 64, r = l % 16, g = l / 16;
   red[w][l] = acc;
   __syncthreads();
-  if (tid >= 64 || r >= rows) return;
-  i32x4 sum = red[0][l];
+  if (tid < 64 && r < rows) {
+    i32x4 sum = red[0][l];
 #pragma unroll
-  for (int i = 1; i < W; ++i) sum += red[i][l];
-  float ws[4], v[4];
-  scales4(a.bs, a.N, n0 + 4 * g, ws);
+    for (int i = 1; i < W; ++i) sum += red[i][l];
+    float ws[4], v[4];
+    scales4(a.bs, a.N, n0 + 4 * g, ws);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) v[k] = (float)sum[k] * ws[k] * sa;
-  put4<E>(a.y, a.N, m0 + r, n0 + 4 * g, v);
+    for (int k = 0; k < 4; ++k) v[k] = (float)sum[k] * ws[k] * sa;
+    put4<E>(a.y, a.N, m0 + r, n0 + 4 * g, v);
+  }
+  __syncthreads();      // the next columns write `red` again
 }
 
 // rows of codes in memory, asked for with the weights of their step
@@ -323,19 +296,56 @@ struct RowsOfCodes {
   __device__ u32x4 at(const u32x4& x, int, bool in) const { return in ? x : u32x4{0u, 0u, 0u, 0u}; }
 };
 
+// The rows behind a.M, up to 16 (a.tail): 16 columns a workgroup at a time, weights
+// straight from memory into the operands.
+template <typename E, int W>
+__device__ __forceinline__ void stream_tail(const Int8Args& a, i32x4 (*red)[64]) {
+  const int l = threadIdx.x % 64, w = uniform(threadIdx.x / 64), units = (a.N + kFewCols - 1) / kFewCols;
+  const int64_t row = a.M + (l % 16 < a.tail ? l % 16 : 0);
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const i32x4 acc = stream_columns<W>(a, u * kFewCols, w, l, RowsOfCodes{a.a + row * a.K});
+    finish_columns<E, W>(a, acc, u * kFewCols, a.M, a.tail, a.as[row], red);
+  }
+}
+
 }  // namespace
 
-// Up to 16 rows of one matrix (a.m_first and on): 16 columns a workgroup, weights
-// straight from memory into the operands.
+// A few rows of codes.
 template <typename E>
 __global__ __launch_bounds__(256) void k_int8_few(Int8Args a) {
-  constexpr int W = 4;
-  __shared__ i32x4 red[W][64];
-  const int l = threadIdx.x % 64, w = uniform(threadIdx.x / 64), n0 = (int)blockIdx.x * kFewCols;
-  const int rows = (int)(a.M - a.m_first);
-  const int64_t row = a.m_first + (l % 16 < rows ? l % 16 : 0);
-  const i32x4 acc = stream_columns<W>(a, n0, w, l, RowsOfCodes{a.a + row * a.K});
-  finish_columns<E, W>(a, acc, n0, a.m_first, rows, a.as[row], red);
+  __shared__ i32x4 red[4][64];
+  stream_tail<E, 4>(a, red);
+}
+
+// Products with many rows: 256 x 256 tiles, and 128 x 256 for a group's rest; up
+// to 16 rows behind the tiles of one matrix are streamed by who is done.
+// One workgroup a CU; XCD x takes an eighth of each class's list (neighbours
+// share an L2), and its workgroups take every n-th tile of it in turn.
+template <typename E>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_int8_mma(Int8Args a) {
+  // separate arrays: the compiler then sees that a stage's reads and the other
+  // stage's copies do not meet, and does not wait for the copies
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[(kBM + kBN) * kStep], s1[(kBM + kBN) * kStep];
+  uint8_t* const slot[2] = {s0, s1};
+  const int x = blockIdx.x % 8, step = gridDim.x / 8;
+  int64_t n[2], first[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int64_t total = count_blocks(a, c) * ((a.N + kBN - 1) / kBN);
+    first[c] = total * x / 8;
+    n[c] = total * (x + 1) / 8 - first[c];
+  }
+  for (int64_t k = blockIdx.x / 8; k < n[0] + n[1]; k += step) {
+    TileAt t;
+    if (k < n[0]) {
+      if (!find_tile(a, kFull, first[0] + k, t)) break;
+      int8_tile<E, 4, 2, 4, 8, 2, 1, 1>(a, t, slot);
+    } else {
+      if (!find_tile(a, kHalf, first[1] + k - n[0], t)) break;
+      int8_tile<E, 4, 2, 2, 8, 2, 1, 1>(a, t, slot);
+    }
+  }
+  if (a.tail > 0) stream_tail<E, 8>(a, reinterpret_cast<i32x4(*)[64]>(s0));
 }
 
 namespace {
@@ -502,7 +512,8 @@ hipError_t gemm(const Int8Args& args, int num_cus, hipStream_t s) {
   const unsigned cus = (unsigned)((num_cus + 7) / 8 * 8);
   auto count = [&](int c) { return (even + most_rows(c) - 1) / most_rows(c) * a.G * ((a.N + cols_of(c) - 1) / cols_of(c)); };
   if (a.offsets == nullptr && a.M <= kStreamRows) {
-    a.m_first = 0;
+    a.tail = (int)a.M;
+    a.M = 0;
     hipLaunchKernelGGL(k_int8_few<E>, dim3(units), dim3(256), 0, s, a);
   } else if (count(k32x32) <= num_cus) {
     hipLaunchKernelGGL((k_int8_ring<E, k32x32, 2, 2, 1, 1, 4>), dim3(cus), dim3(256), 0, s, a);
@@ -515,15 +526,15 @@ hipError_t gemm(const Int8Args& args, int num_cus, hipStream_t s) {
   } else if (count(k128x128) <= 2 * num_cus) {
     hipLaunchKernelGGL((k_int8_ring<E, k128x128, 4, 2, 2, 4, 2>), dim3(cus), dim3(512), 0, s, a);
   } else {
-    // one matrix: up to 16 rows beyond the blocks of 256 are streamed
+    // one matrix: up to 16 rows beyond the blocks of 256 are streamed, in place of a
+    // round more (16388 x 4096 x 2048: 2.6 us for the last four rows; 4097 x 4096 x 7168,
+    // whose tiles all end together: 8.5)
     const int64_t rest = a.offsets == nullptr ? a.M % kBM : 0;
-    if (rest <= kFewRows) a.M -= rest;
+    if (rest <= kFewRows) {
+      a.tail = (int)rest;
+      a.M -= rest;
+    }
     hipLaunchKernelGGL(k_int8_mma<E>, dim3(cus), dim3(512), 0, s, a);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess || a.M == args.M) return err;
-    a.m_first = a.M;
-    a.M = args.M;
-    hipLaunchKernelGGL(k_int8_few<E>, dim3(units), dim3(256), 0, s, a);
   }
   return hipGetLastError();
 }

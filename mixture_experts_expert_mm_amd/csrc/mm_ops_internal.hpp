@@ -143,7 +143,7 @@ struct Int8Args {
   const int32_t* counts;
   void* y;                   // [M][N]
   int64_t M;
-  int64_t m_first;           // first row of the streaming units
+  int tail;                  // rows behind the M ones, streamed
   int N, K, G;
   int x_element, y_element;
 };
