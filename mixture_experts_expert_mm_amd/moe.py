@@ -499,38 +499,58 @@ def _combine_backward(dy, rows, order, weights, T, E, K, of_rows, of_weights):
     return drows, dweights
 
 
+def _once(backward):
+    """once_differentiable, whose wrapping costs more than a launch, where the backward pass is recorded itself."""
+    recorded = torch.autograd.function.once_differentiable(backward)
+    return lambda ctx, *grads: recorded(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+
+
+def _keep_order(ctx, order):
+    # as attributes: each saved tensor costs to unpack; what is written over is found all the same
+    ctx.order = order
+    ctx.versions = order.row_of_route._version, order.offsets._version
+
+
+def _kept_order(ctx):
+    order = ctx.order
+    if ctx.versions != (order.row_of_route._version, order.offsets._version):
+        raise RuntimeError("order: was modified in place before the backward pass")
+    return order
+
+
 class _SortFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, make):
         rows, order, ctx.dims = make(x)
-        ctx.save_for_backward(order.counts, order.offsets, order.row_of_route, order.route_of_row)
+        _keep_order(ctx, order)
         return rows
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, drows):
         _not_captured()
-        return _combine(_dense(drows), TokenOrder(*ctx.saved_tensors), None, *ctx.dims), None
+        return _combine(_dense(drows), _kept_order(ctx), None, *ctx.dims), None
 
 
 class _CombineFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, weights, order, dims):
         ctx.dims = dims
-        ctx.save_for_backward(rows if weights is not None and weights.requires_grad else None, weights, order.counts,
-                              order.offsets, order.row_of_route, order.route_of_row)
+        _keep_order(ctx, order)
+        if weights is not None:
+            ctx.save_for_backward(rows if weights.requires_grad else None, weights)
         return _combine(rows, order, weights, *dims)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, dy):
         _not_captured()
-        rows, weights, *order = ctx.saved_tensors
-        order, dy = TokenOrder(*order), _dense(dy)
-        if weights is None:
+        order, dy = _kept_order(ctx), _dense(dy)
+        of_rows, of_weights, _, _ = ctx.needs_input_grad
+        saved = ctx.saved_tensors
+        if not saved:
             return _sort_rows(dy, order, *ctx.dims), None, None, None
-        of_rows, of_weights = ctx.needs_input_grad[:2]
-        return *_combine_backward(dy, rows, order, weights, *ctx.dims, of_rows, of_weights), None, None
+        return *_combine_backward(dy, saved[0], order, saved[1], *ctx.dims, of_rows, of_weights), None, None
 
 
 def sort_tokens(x, topk_ids, num_experts, *, active=None, stream=None):
@@ -666,7 +686,7 @@ class _SwigluFunction(torch.autograd.Function):
         return a
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, da):
         _not_captured()
         return _swiglu_backward(_dense(da), *ctx.saved_tensors, ctx.clamp), None, None, None, None

@@ -267,3 +267,26 @@ def test_capture_with_autograd_is_refused():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, moe.combine_tokens(rows, order, w).detach())
+
+
+def test_backward_twice_and_orders_written_over():
+    """A graph may be kept and gone through again, not differentiated twice; an order may not change in between."""
+    ids, _ = routes(40, 5, 3, 7)
+    x = torch.randn(40, 16, device="cuda", requires_grad=True)
+    w = torch.rand(40, 3, device="cuda", requires_grad=True)
+    rows, order = moe.sort_tokens(x, ids.cuda(), 5)
+    y = moe.combine_tokens(rows, order, w)
+    dy = torch.randn_like(y)
+    one = torch.autograd.grad(y, (x, w), dy, retain_graph=True)
+    two = torch.autograd.grad(y, (x, w), dy, retain_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+    three = torch.autograd.grad(y, (x, w), dy, create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(one, three))
+    with pytest.raises(RuntimeError, match="once_differentiable|does not require grad"):
+        torch.autograd.grad(three[1].sum(), x)
+    for t in (order.row_of_route, order.offsets):
+        rows, order = moe.sort_tokens(x, ids.cuda(), 5)
+        y = moe.combine_tokens(rows, order, w)
+        {True: order.row_of_route, False: order.offsets}[t.dim() == 2].zero_()
+        with pytest.raises(RuntimeError, match="modified in place"):
+            torch.autograd.grad(y, (x, w), dy)
