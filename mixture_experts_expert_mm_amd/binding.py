@@ -260,18 +260,16 @@ def status_string(status: int) -> str:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream
 
 

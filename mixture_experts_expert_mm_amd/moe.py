@@ -186,6 +186,9 @@ FEW_MAX_TOKENS = 64
 def _need(name, t, dtype, shape, device, grad=False):
     """The one check of a tensor argument: a message that says what it has to be.  grad: the operator has a gradient
     with respect to it."""
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()
+            and forward_ad._current_level < 0 and (grad or not t.requires_grad)):
+        return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
     if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
@@ -219,7 +222,8 @@ def _rows(name, x):
         raise ValueError(f"{name}: a matrix is needed")
     if not x.is_cuda:
         raise ValueError(f"{name}: a tensor on a GPU is needed, got one on {x.device}")
-    return *x.shape, x.device
+    rows, columns = x.shape
+    return rows, columns, x.device
 
 
 def _stream_of(device, stream):
@@ -434,25 +438,25 @@ def _element(name, x, summed):
 
 
 def _order_of(order, device):
-    """(T, E, K) of an order whose tensors are as they have to be."""
+    """(T, E, K) of an order, of which what kernels read (offsets, row_of_route) is as it has to be."""
     if not isinstance(order, TokenOrder):
         raise ValueError(f"order: a TokenOrder is needed, got {type(order).__name__}")
-    if not isinstance(order.row_of_route, torch.Tensor) or order.row_of_route.dim() != 2:
+    row, offsets = order.row_of_route, order.offsets
+    if not isinstance(row, torch.Tensor) or row.dim() != 2:
         raise ValueError("order.row_of_route: a matrix [tokens, topk] is needed")
-    if not isinstance(order.counts, torch.Tensor) or order.counts.dim() != 1:
-        raise ValueError("order.counts: a vector [experts] is needed")
-    (T, K), E, i32 = order.row_of_route.shape, order.counts.shape[0], torch.int32
-    _need("order.counts", order.counts, i32, (E,), device)
-    _need("order.offsets", order.offsets, i32, (E + 1,), device)
-    _need("order.row_of_route", order.row_of_route, i32, (T, K), device)
-    _need("order.route_of_row", order.route_of_row, i32, (T * K,), device)
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
+        raise ValueError("order.offsets: a vector [experts + 1] is needed")
+    T, K = row.shape
+    E = offsets.shape[0] - 1
+    _need("order.offsets", offsets, torch.int32, (E + 1,), device)
+    _need("order.row_of_route", row, torch.int32, (T, K), device)
     return T, E, K
 
 
-def _records(*tensors):
+def _records(a, b=None):
     """Whether autograd records this call.  Under capture it may not: the engine ends the process where an eager graph
     of the same leaves is alive, which cannot be seen from here."""
-    if not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in tensors):
+    if not (a.requires_grad or (b is not None and b.requires_grad)) or not torch.is_grad_enabled():
         return False
     _not_captured()
     return True
@@ -466,7 +470,8 @@ def _not_captured():
 
 def _dense(t):
     """A gradient as autograd hands it over (expanded, strided, at any address) in the form that kernels take."""
-    t = t.contiguous()
+    if not t.is_contiguous():
+        t = t.contiguous()
     return t.clone() if t.data_ptr() % 16 else t
 
 
@@ -520,16 +525,22 @@ def _kept_order(ctx):
 
 class _SortFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, make):
-        rows, order, ctx.dims = make(x)
-        _keep_order(ctx, order)
+    def forward(ctx, x, args, made):
+        """made: an order to sort by, or nothing yet, which args then make."""
+        ctx.dims = args[-3:]
+        if made:
+            rows = _sort_rows(x, made[0], *ctx.dims)
+        else:
+            rows, order = _sort_tokens(x, *args)
+            made.append(order)
+        _keep_order(ctx, made[0])
         return rows
 
     @staticmethod
     @_once
     def backward(ctx, drows):
         _not_captured()
-        return _combine(_dense(drows), _kept_order(ctx), None, *ctx.dims), None
+        return _combine(_dense(drows), _kept_order(ctx), None, *ctx.dims), None, None
 
 
 class _CombineFunction(torch.autograd.Function):
@@ -553,6 +564,18 @@ class _CombineFunction(torch.autograd.Function):
         return *_combine_backward(dy, saved[0], order, saved[1], *ctx.dims, of_rows, of_weights), None, None
 
 
+def _sort_tokens(x, topk_ids, active, plan, T, E, K):
+    R, dev = T * K, x.device
+    rows = torch.empty((R, x.shape[1]), dtype=x.dtype, device=dev)
+    # one allocation for the four
+    counts, offsets, row, route = (torch.empty if T else torch.zeros)(
+        2 * (E + R) + 1, dtype=torch.int32, device=dev).split_with_sizes((E, E + 1, R, R))
+    if T:
+        ws = _workspace(plan.workspace_bytes, dev) if plan.workspace_bytes else None
+        B.mm_sort_tokens(plan, topk_ids, active, x, counts, offsets, row, route, rows, ws, _raw_stream(dev))
+    return rows, TokenOrder(counts, offsets, row.view(T, K), route)
+
+
 def sort_tokens(x, topk_ids, num_experts, *, active=None, stream=None):
     """mm_sort_tokens: (rows [T*K,H], TokenOrder) of the tokens x [T,H] (bf16, float16, float32, or 8-bit codes).
 
@@ -561,32 +584,18 @@ def sort_tokens(x, topk_ids, num_experts, *, active=None, stream=None):
     Differentiable with respect to x; the gradient is ``combine_tokens(drows, order)``."""
     T, H, dev = _rows("x", x)
     el = _element("x", x, False)
-    _need("x", x, x.dtype, (T, H), dev, grad=el != B.MM_ELEMENT_8BIT)
-    K = int(topk_ids.shape[1]) if isinstance(topk_ids, torch.Tensor) and topk_ids.dim() == 2 else 0
+    _need("x", x, x.dtype, (T, H), dev, el != B.MM_ELEMENT_8BIT)
+    K = topk_ids.shape[1] if isinstance(topk_ids, torch.Tensor) and topk_ids.dim() == 2 else 0
     _need("topk_ids", topk_ids, torch.int32, (T, K), dev)
     if active is not None:
         _need("active", active, torch.int8, (T,), dev)
-    E = _whole("num_experts", num_experts)
-    plan = _sort_plan(max(T, 1), H, E, K, el)
-
-    def make(x):
-        R = T * K
-        rows = torch.empty((R, H), dtype=x.dtype, device=dev)
-        # one allocation for the four
-        counts, offsets, row, route = (torch.empty if T else torch.zeros)(
-            2 * (E + R) + 1, dtype=torch.int32, device=dev).split_with_sizes((E, E + 1, R, R))
-        order = TokenOrder(counts, offsets, row.view(T, K), route)
-        if T:
-            ws = _workspace(plan.workspace_bytes, dev) if plan.workspace_bytes else None
-            B.mm_sort_tokens(plan, topk_ids, active, x, order.counts, order.offsets, order.row_of_route,
-                             order.route_of_row, rows, ws, _raw_stream(dev))
-        made.append(order)
-        return rows, order, (T, E, K)
-
-    made = []
+    E = num_experts if type(num_experts) is int else _whole("num_experts", num_experts)
+    plan = _sort_plan(T or 1, H, E, K, el)
     with _stream_of(dev, stream):
-        rows = _SortFunction.apply(x, make) if _records(x) else make(x)[0]
-    return rows, made[0]
+        if _records(x):
+            made = []
+            return _SortFunction.apply(x, (topk_ids, active, plan, T, E, K), made), made[0]
+        return _sort_tokens(x, topk_ids, active, plan, T, E, K)
 
 
 def sort_rows(x, order, *, stream=None):
@@ -599,9 +608,8 @@ def sort_rows(x, order, *, stream=None):
     if dims[0] != T:
         raise ValueError(f"order: one of {T} tokens is needed, got one of {dims[0]}")
     _sort_plan(max(T, 1), H, dims[1], dims[2], el)
-    make = lambda x: (_sort_rows(x, order, *dims), order, dims)
     with _stream_of(dev, stream):
-        return _SortFunction.apply(x, make) if _records(x) else make(x)[0]
+        return _SortFunction.apply(x, dims, [order]) if _records(x) else _sort_rows(x, order, *dims)
 
 
 def _combine_args(name, rows, order, weights):

@@ -135,10 +135,11 @@ def test_refusals(launches):
         ("weights", lambda: moe.combine_tokens(rows, order, w[:, :1])),
         ("weights", lambda: moe.combine_backward(x, rows, order, None)),
         ("dy", lambda: moe.combine_backward(x.half(), rows, order, w)), ("dy", lambda: moe.combine_backward(x[:2], rows, order, w)),
-        ("order.offsets", lambda: moe.sort_rows(x, moe.TokenOrder(order.counts, order.counts, order.row_of_route, order.route_of_row))),
+        ("order.offsets", lambda: moe.sort_rows(x, moe.TokenOrder(order.counts, None, order.row_of_route, order.route_of_row))),
+        ("order.offsets", lambda: moe.sort_rows(x, moe.TokenOrder(order.counts, order.offsets.long(), order.row_of_route, order.route_of_row))),
         ("order.row_of_route", lambda: moe.sort_rows(x, moe.TokenOrder(order.counts, order.offsets, order.row_of_route.view(-1), order.route_of_row))),
-        ("order.route_of_row", lambda: moe.combine_tokens(rows, moe.TokenOrder(order.counts, order.offsets, order.row_of_route, order.route_of_row[1:]))),
-        ("order.counts", lambda: moe.combine_tokens(rows, moe.TokenOrder(None, order.offsets, order.row_of_route, order.route_of_row))),
+        ("order.row_of_route", lambda: moe.combine_tokens(rows, moe.TokenOrder(order.counts, order.offsets, order.row_of_route.float(), order.route_of_row))),
+        ("order.row_of_route", lambda: moe.combine_tokens(rows, moe.TokenOrder(order.counts, order.offsets, order.row_of_route.t(), order.route_of_row))),
         ("rows: .*gradient", lambda: moe.combine_backward(x, rows.clone().requires_grad_(), order, w)),
         ("weights: .*gradient", lambda: moe.combine_backward(x, rows, order, w.clone().requires_grad_())),
     ]
