@@ -272,12 +272,14 @@ __global__ __launch_bounds__(kPlaceThreads) void k_sort_place(SortArgs a) {
 }
 
 // rows[row_of_route[t][k]] = x[t]; who brings token t also clears those of the
-// rows t * K .. t * K + K - 1 that no route fills.
+// rows t * K .. t * K + K - 1 that no route fills.  WIDE: a workgroup a token, or
+// several where there are few (16384 tokens of 7168 bf16 to 8 experts each: a
+// wave per 64 vectors instead, as k_combine_tokens has it, 2% more).
 template <int V, bool WIDE>
 __global__ __launch_bounds__(kThreads) void k_sort_rows(SortArgs a) {
   typedef typename Bytes<V>::type vec;
-  const int64_t kept = slot<true>(a.offsets + a.E);
-  for_vectors<WIDE>(a.T, a.row_bytes / V, [&](int64_t t, int64_t c) {
+  const int64_t kept = slot<true>(a.offsets + a.E), chunks = a.row_bytes / V;
+  auto one = [&](int64_t t, int64_t c) {
     const vec v = *reinterpret_cast<const vec*>(a.x + t * a.row_bytes + c * V);
     for (int k = 0; k < a.K; ++k) {
       const int64_t p = slot<WIDE>(a.row_of_route + t * a.K + k);
@@ -285,7 +287,13 @@ __global__ __launch_bounds__(kThreads) void k_sort_rows(SortArgs a) {
     }
     for (int64_t p = t * a.K > kept ? t * a.K : kept; p < (t + 1) * a.K; ++p)
       stream_out(a.rows + p * a.row_bytes + c * V, vec{});
-  });
+  };
+  if constexpr (WIDE) {
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x)
+      for (int64_t c = (int64_t)blockIdx.y * kThreads + threadIdx.x; c < chunks; c += (int64_t)gridDim.y * kThreads) one(t, c);
+  } else {
+    for_vectors<false>(a.T, chunks, one);
+  }
 }
 
 namespace {
@@ -432,19 +440,20 @@ unsigned vector_grid(int64_t tokens, int64_t chunks) {
   return (unsigned)(n < (1 << 20) ? n : (1 << 20));
 }
 
-template <int V>
-hipError_t sort_rows(const SortArgs& a, hipStream_t s) {
-  const int64_t chunks = a.row_bytes / V;
-  const dim3 grid(vector_grid(a.T, chunks));
-  if (is_wide(chunks)) hipLaunchKernelGGL((k_sort_rows<V, true>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((k_sort_rows<V, false>), grid, dim3(kThreads), 0, s, a);
-  return hipGetLastError();
-}
-
 // a workgroup brings 256 vectors of a row at a time; few tokens' rows are shared by several, up to 1024 in all
 unsigned slices_of(int64_t chunks, int64_t tokens) {
   const int64_t turns = (chunks + kThreads - 1) / kThreads, most = 1024 / tokens > 1 ? 1024 / tokens : 1;
   return (unsigned)(turns < most ? turns : most);
+}
+
+template <int V>
+hipError_t sort_rows(const SortArgs& a, hipStream_t s) {
+  const int64_t chunks = a.row_bytes / V, most = 1 << 20;
+  if (is_wide(chunks))
+    hipLaunchKernelGGL((k_sort_rows<V, true>), dim3((unsigned)(a.T < most ? a.T : most), slices_of(chunks, a.T)), dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_sort_rows<V, false>), dim3(vector_grid(a.T, chunks)), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
 }
 
 template <int V>
