@@ -98,8 +98,9 @@ __device__ __forceinline__ int int8_code(float v, float s) {
 // Eight codes at once, the same ones: a product with the reciprocal is within
 // 2^-15 of the quotient (three roundings of at most 127 * 2^-24 and one more of
 // the quotient's own), so it rounds to the same integer unless it is that near
-// to the middle between two; only then are the quotients taken.  (Eight IEEE
-// divisions are 80 instructions; 64 Ki rows of 2 x 2048 bf16 values 320 -> 215 us.)
+// to the middle between two; only then are the quotients taken.  (Sixteen IEEE
+// divisions a lane: 320 us for the copy of 65536 x 4096 bf16 values with its
+// activation; this way 280.)
 // t + 1.5 * 2^23 has the rounded integer in its low bits.
 __device__ __forceinline__ u32x2 int8_codes(const float (&v)[8], float s) {
   constexpr float kShift = 12582912.0f;

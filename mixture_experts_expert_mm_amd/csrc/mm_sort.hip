@@ -8,7 +8,10 @@
 // The order is a stable counting sort, so every result has one value.
 //
 // Bound: HBM for the rows (a token's row is read once and written K times, or
-// the other way round); launches for a few tokens.
+// the other way round); launches for a few tokens.  At 16384 tokens of 7168 bf16
+// with 8 of 256 experts each: the order 15 us, rows written 431 us (4.9 TB/s, as a
+// copy), read and summed 360 (5.8), read and written with both gradients 809
+// (5.0); one token 4.4.
 #include <type_traits>
 
 #include "mm_device.hpp"
@@ -320,7 +323,9 @@ __device__ __forceinline__ void load_slots(const CombineTokensArgs& a, int64_t t
 
 // y[t] = sum_k w[t][k] * rows[row_of_route[t][k]] in float32, in the order of k,
 // SLOTS rows in flight.  A skipped slot reads row 0 and adds nothing, whatever
-// its weight.
+// its weight.  WIDE: a wave takes 64 neighbouring vectors of a token, its rows'
+// places and weights come through the scalar unit (a workgroup a token, places by
+// lane, 478 us in place of 344 at 16384 x 8 rows of 7168 bf16).
 template <typename E, int N, int SLOTS, bool WIDE>
 __global__ __launch_bounds__(kThreads) void k_combine_tokens(CombineTokensArgs a) {
   typedef Elems<E, N> el;

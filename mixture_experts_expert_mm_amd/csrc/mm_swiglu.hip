@@ -7,7 +7,8 @@
 //   backward at h~ = q * s:  dg = da * u * sig * (1 + g * (1 - sig)) where |g~| <= c,
 //                            du = da * g * sig                       where |u~| <= c
 //
-// Bound: HBM; every value is read and written once.
+// Bound: HBM; every value is read and written once.  65536 rows of 2 x 2048 bf16,
+// forward with the copy and backward: 408 us for 2.15 GB (5.3 TB/s; a copy 4.9).
 #include <type_traits>
 
 #include "mm_device.hpp"
