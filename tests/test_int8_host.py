@@ -76,7 +76,7 @@ def test_entry_points_validate_before_any_hip_call(lib):
         assert call(lib.mm_int8_linear, args, i, None) == 1
         assert call(lib.mm_int8_linear, args, i, GOOD + 2) == 1
     assert call(lib.mm_int8_linear, args, 4, GOOD) == 1 and call(lib.mm_int8_linear, args, 8, 16) == 3
-    assert [B.mm_kernel_name(i) for i in (23, 24, 25)] == ["int8_quantize", "int8_gemm", "unknown"]
+    assert [B.mm_kernel_name(i) for i in (23, 24)] == ["int8_quantize", "int8_gemm"]
 
 
 @pytest.fixture
