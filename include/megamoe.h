@@ -662,6 +662,10 @@ mm_status mm_combine_backward(const mm_sort_plan* plan, const void* dy, const vo
  * such a scale and reads back as NaN.
  *   rows, cols   M in [1, 2^24], I in [1, 2^20], M * ceil(I/128) below 2^31
  *   element      mm_element of h, a, da, dh (not MM_ELEMENT_8BIT)
+ *   gate_up_group  0: h is [gate columns | up columns]; else they alternate in
+ *                groups of so many (a multiple of 8 that divides I), as they do
+ *                behind a prepared W1 (mm_plan.gate_up_group).  codes and dh lie
+ *                as h does; scales, and what a group is, do not depend on it
  *   h            device [M][2I]
  *   a            device [M][I] out; must not overlap h
  *   codes        device int8 [M][2I] out, or NULL: nothing is kept
@@ -671,11 +675,11 @@ mm_status mm_combine_backward(const mm_sort_plan* plan, const void* dy, const vo
  * values that codes and scales stand for (code * scale in float32): 0 where
  * such a value is outside the clamp's interval.
  */
-mm_status mm_swiglu(int64_t rows, int64_t cols, int32_t element, const void* h, int32_t clamp_activation,
-                    float activation_clamp, void* a, int8_t* codes, float* scales, void* stream);
-mm_status mm_swiglu_backward(int64_t rows, int64_t cols, int32_t element, const void* da, const int8_t* codes,
-                             const float* scales, int32_t clamp_activation, float activation_clamp, void* dh,
-                             void* stream);
+mm_status mm_swiglu(int64_t rows, int64_t cols, int32_t element, int32_t gate_up_group, const void* h,
+                    int32_t clamp_activation, float activation_clamp, void* a, int8_t* codes, float* scales, void* stream);
+mm_status mm_swiglu_backward(int64_t rows, int64_t cols, int32_t element, int32_t gate_up_group, const void* da,
+                             const int8_t* codes, const float* scales, int32_t clamp_activation, float activation_clamp,
+                             void* dh, void* stream);
 
 /*
  * ------------------------------------------------- 8-bit integer product

@@ -235,8 +235,8 @@ def load() -> ctypes.CDLL:
     lib.mm_combine_tokens.argtypes = [SP, vp, i32p, f32p, vp, vp]
     lib.mm_combine_backward.argtypes = [SP, vp, vp, i32p, i32p, f32p, vp, f32p, vp]
     i32, f32 = ctypes.c_int32, ctypes.c_float
-    lib.mm_swiglu.argtypes = [i64, i64, i32, vp, i32, f32, vp, vp, f32p, vp]
-    lib.mm_swiglu_backward.argtypes = [i64, i64, i32, vp, vp, f32p, i32, f32, vp, vp]
+    lib.mm_swiglu.argtypes = [i64, i64, i32, i32, vp, i32, f32, vp, vp, f32p, vp]
+    lib.mm_swiglu_backward.argtypes = [i64, i64, i32, i32, vp, vp, f32p, i32, f32, vp, vp]
     IP = ctypes.POINTER(MMInt8Plan)
     lib.mm_int8_quantize.argtypes = [i64, i64, i32, vp, vp, f32p, vp]
     lib.mm_int8_plan_create.argtypes = [ctypes.POINTER(MMInt8Problem), IP]
@@ -428,14 +428,15 @@ def _clamp(activation_clamp):
     return (0, 0.0) if activation_clamp is None else (1, activation_clamp)
 
 
-def mm_swiglu(rows, cols, element, h, activation_clamp, a, codes, scales, stream=None):
-    _check("mm_swiglu", load().mm_swiglu(rows, cols, element, _ptr(h), *_clamp(activation_clamp), _ptr(a), _ptr(codes),
-                                         _ptr(scales), _stream(stream)))
+def mm_swiglu(rows, cols, element, gate_up_group, h, activation_clamp, a, codes, scales, stream=None):
+    _check("mm_swiglu", load().mm_swiglu(rows, cols, element, gate_up_group, _ptr(h), *_clamp(activation_clamp), _ptr(a),
+                                         _ptr(codes), _ptr(scales), _stream(stream)))
 
 
-def mm_swiglu_backward(rows, cols, element, da, codes, scales, activation_clamp, dh, stream=None):
+def mm_swiglu_backward(rows, cols, element, gate_up_group, da, codes, scales, activation_clamp, dh, stream=None):
     _check("mm_swiglu_backward", load().mm_swiglu_backward(
-        rows, cols, element, _ptr(da), _ptr(codes), _ptr(scales), *_clamp(activation_clamp), _ptr(dh), _stream(stream)))
+        rows, cols, element, gate_up_group, _ptr(da), _ptr(codes), _ptr(scales), *_clamp(activation_clamp), _ptr(dh),
+        _stream(stream)))
 
 
 def mm_int8_quantize(rows, cols, element, x, codes, scales, stream=None):

@@ -494,14 +494,17 @@ CombineTokensArgs combine_tokens_args(const mm_sort_problem& p, const void* rows
   return a;
 }
 
-mm_status swiglu_args(int64_t rows, int64_t cols, int32_t element, int32_t clamp_on, float clamp, SwigluArgs& a) {
+mm_status swiglu_args(int64_t rows, int64_t cols, int32_t element, int32_t turn, int32_t clamp_on, float clamp,
+                      SwigluArgs& a) {
   if (element < MM_ELEMENT_BF16 || element >= MM_ELEMENT_8BIT) return MM_ERR_UNSUPPORTED;
   if (rows < 1 || rows > (1 << 24) || cols < 1 || cols > (1 << 20)) return MM_ERR_INVALID_ARG;
   if ((clamp_on != 0 && clamp_on != 1) || (clamp_on && !(clamp >= 0.0f))) return MM_ERR_INVALID_ARG;
+  if (turn < 0 || (turn > 0 && (turn % 8 || cols % turn))) return MM_ERR_INVALID_ARG;
   a.groups = rows * ((cols + 127) / 128);
   if (a.groups >= ((int64_t)1 << 31)) return MM_ERR_INVALID_ARG;
   a.I = (int)cols;
   a.element = element;
+  a.turn = turn;
   a.clamp = clamp_on ? clamp : INFINITY;
   return MM_OK;
 }
@@ -1127,10 +1130,10 @@ mm_status mm_combine_backward(const mm_sort_plan* plan, const void* dy, const vo
 }
 
 // ------------------------------------------------ activation, kept in 8 bits
-mm_status mm_swiglu(int64_t rows, int64_t cols, int32_t element, const void* h, int32_t clamp_activation,
-                    float activation_clamp, void* a, int8_t* codes, float* scales, void* stream) {
+mm_status mm_swiglu(int64_t rows, int64_t cols, int32_t element, int32_t gate_up_group, const void* h,
+                    int32_t clamp_activation, float activation_clamp, void* a, int8_t* codes, float* scales, void* stream) {
   SwigluArgs g{};
-  MM_TRY(swiglu_args(rows, cols, element, clamp_activation, activation_clamp, g));
+  MM_TRY(swiglu_args(rows, cols, element, gate_up_group, clamp_activation, activation_clamp, g));
   if (!ok16(h) || !ok16(a) || !aligned(codes, 16) || !aligned(scales, 4) || !codes != !scales) return MM_ERR_INVALID_ARG;
   g.h = h;
   g.a = a;
@@ -1140,11 +1143,11 @@ mm_status mm_swiglu(int64_t rows, int64_t cols, int32_t element, const void* h, 
   return run(MM_K_SWIGLU, s, [&] { return launch_swiglu(g, s); });
 }
 
-mm_status mm_swiglu_backward(int64_t rows, int64_t cols, int32_t element, const void* da, const int8_t* codes,
-                             const float* scales, int32_t clamp_activation, float activation_clamp, void* dh,
-                             void* stream) {
+mm_status mm_swiglu_backward(int64_t rows, int64_t cols, int32_t element, int32_t gate_up_group, const void* da,
+                             const int8_t* codes, const float* scales, int32_t clamp_activation, float activation_clamp,
+                             void* dh, void* stream) {
   SwigluArgs g{};
-  MM_TRY(swiglu_args(rows, cols, element, clamp_activation, activation_clamp, g));
+  MM_TRY(swiglu_args(rows, cols, element, gate_up_group, clamp_activation, activation_clamp, g));
   if (!ok16(da) || !ok16(codes) || !ok4(scales) || !ok16(dh)) return MM_ERR_INVALID_ARG;
   g.da = da;
   g.q = const_cast<int8_t*>(codes);

@@ -127,6 +127,7 @@ struct SwigluArgs {
   void* dh;                  // [M][2I] (backward)
   int64_t groups;            // M * ceil(I/128), below 2^31
   int I, element;
+  int turn;                  // 0: gate columns, then up columns; else in turns of so many (a multiple of 8 that divides I)
   float clamp;               // +inf: none
 };
 hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s);

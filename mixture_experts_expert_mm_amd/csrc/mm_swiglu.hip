@@ -7,6 +7,9 @@
 //   backward at h~ = q * s:  dg = da * u * sig * (1 + g * (1 - sig)) where |g~| <= c,
 //                            du = da * g * sig                       where |u~| <= c
 //
+// h's columns are [g | u], or gate and up columns in turns of `turn` (as the rows
+// of a prepared W1 lie); the groups are of neighbouring gates, or ups, either way.
+//
 // Bound: HBM; every value is read and written once.  65536 rows of 2 x 2048 bf16,
 // forward with the copy and backward: 408 us for 2.15 GB (5.3 TB/s; a copy 4.9).
 #include <type_traits>
@@ -38,6 +41,21 @@ __device__ __forceinline__ float sigmoid(float z) {
 // (WIDE: I % 8 == 0); else every 16th.
 template <bool WIDE>
 __device__ __forceinline__ int place(int lane, int i) { return WIDE ? lane * kPer + i : i * kLanes + lane; }
+
+// Where a group's gates lie in h; its up values are ups_from behind them.  For a
+// lane of the TURN form (always WIDE): its place less what load8 and the like add.
+// A form of its own: the branch costs the other 1 % (65536 rows: 439 against 436 us).
+template <bool TURN>
+__device__ __forceinline__ int64_t gate_at(const SwigluArgs& a, uint32_t row, uint32_t grp, int lane) {
+  const int64_t base = (int64_t)row * 2 * a.I;
+  if constexpr (TURN) {
+    const uint32_t mine = grp * kGroup + lane * kPer, t = (uint32_t)a.turn;
+    return base + mine + mine / t * t - lane * kPer;
+  }
+  return base + grp * kGroup;
+}
+template <bool TURN>
+__device__ __forceinline__ int ups_from(const SwigluArgs& a) { return TURN ? a.turn : a.I; }
 
 template <typename E, bool WIDE>
 __device__ __forceinline__ void load8(const E* p, int lane, int n, float (&v)[kPer]) {
@@ -103,7 +121,7 @@ __device__ __forceinline__ void kept8(const int8_t* q, float s, int lane, int n,
 }  // namespace
 
 // 16 lanes take a group of the gate and the same group of the up half.
-template <typename E, bool WIDE, bool KEEP>
+template <typename E, bool WIDE, bool TURN, bool KEEP>
 __global__ __launch_bounds__(kThreads) void k_swiglu(SwigluArgs a) {
   const int lane = threadIdx.x % kLanes;
   const uint32_t per_row = (uint32_t)((a.I + kGroup - 1) / kGroup), total = (uint32_t)a.groups;
@@ -112,12 +130,12 @@ __global__ __launch_bounds__(kThreads) void k_swiglu(SwigluArgs a) {
   for (uint32_t at = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes; at < total; at += gridDim.x * (kThreads / kLanes)) {
     const uint32_t row = at / per_row, grp = at % per_row;
     const int n = a.I - (int)grp * kGroup;               // values from here to the row's end
-    const int64_t first = (int64_t)row * 2 * a.I + grp * kGroup;
+    const int64_t gate = gate_at<TURN>(a, row, grp, lane), up = gate + ups_from<TURN>(a);
     float g[kPer], u[kPer], o[kPer];
-    load8<E, WIDE>(h + first, lane, n, g);
-    load8<E, WIDE>(h + first + a.I, lane, n, u);
+    load8<E, WIDE>(h + gate, lane, n, g);
+    load8<E, WIDE>(h + up, lane, n, u);
     if constexpr (KEEP) {
-      const float sg = keep8<WIDE>(g, a.q + first, lane, n), su = keep8<WIDE>(u, a.q + first + a.I, lane, n);
+      const float sg = keep8<WIDE>(g, a.q + gate, lane, n), su = keep8<WIDE>(u, a.q + up, lane, n);
       float* s = a.s + (int64_t)row * 2 * per_row + grp;
       if (lane == 0) s[0] = sg;
       if (lane == 1) s[per_row] = su;
@@ -131,7 +149,7 @@ __global__ __launch_bounds__(kThreads) void k_swiglu(SwigluArgs a) {
   }
 }
 
-template <typename E, bool WIDE>
+template <typename E, bool WIDE, bool TURN>
 __global__ __launch_bounds__(kThreads) void k_swiglu_backward(SwigluArgs a) {
   const int lane = threadIdx.x % kLanes;
   const uint32_t per_row = (uint32_t)((a.I + kGroup - 1) / kGroup), total = (uint32_t)a.groups;
@@ -140,12 +158,12 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_backward(SwigluArgs a) {
   for (uint32_t at = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes; at < total; at += gridDim.x * (kThreads / kLanes)) {
     const uint32_t row = at / per_row, grp = at % per_row;
     const int n = a.I - (int)grp * kGroup;
-    const int64_t first = (int64_t)row * 2 * a.I + grp * kGroup;
+    const int64_t gate = gate_at<TURN>(a, row, grp, lane), up = gate + ups_from<TURN>(a);
     const float* s = a.s + (int64_t)row * 2 * per_row + grp;
     float g[kPer], u[kPer], d[kPer];
     load8<E, WIDE>(da + (int64_t)row * a.I + grp * kGroup, lane, n, d);
-    kept8<WIDE>(a.q + first, s[0], lane, n, g);
-    kept8<WIDE>(a.q + first + a.I, s[per_row], lane, n, u);
+    kept8<WIDE>(a.q + gate, s[0], lane, n, g);
+    kept8<WIDE>(a.q + up, s[per_row], lane, n, u);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const float gc = clamped(g[i], a.clamp), uc = clamped(u[i], a.clamp), sig = sigmoid<E>(gc);
@@ -154,8 +172,8 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_backward(SwigluArgs a) {
       g[i] = gout ? 0.0f : d[i] * uc * sig * (1.0f + gc * (1.0f - sig));
       u[i] = uout ? 0.0f : d[i] * gc * sig;
     }
-    store8<E, WIDE>(dh + first, lane, n, g);
-    store8<E, WIDE>(dh + first + a.I, lane, n, u);
+    store8<E, WIDE>(dh + gate, lane, n, g);
+    store8<E, WIDE>(dh + up, lane, n, u);
   }
 }
 
@@ -164,7 +182,8 @@ namespace {
 template <typename F>
 hipError_t for_type(const SwigluArgs& a, const F& f) {
   auto wide = [&](auto e) {
-    return a.I % kPer == 0 ? f(e, std::true_type{}) : f(e, std::false_type{});
+    if (a.turn) return f(e, std::true_type{}, std::true_type{});        // of 8s, so I is too
+    return a.I % kPer == 0 ? f(e, std::true_type{}, std::false_type{}) : f(e, std::false_type{}, std::false_type{});
   };
   return a.element == MM_ELEMENT_BF16 ? wide(__bf16{}) : a.element == MM_ELEMENT_F16 ? wide(_Float16{}) : wide(float{});
 }
@@ -177,18 +196,19 @@ unsigned grid_of(int64_t groups) {
 }  // namespace
 
 hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s) {
-  return for_type(a, [&](auto e, auto w) {
+  return for_type(a, [&](auto e, auto w, auto t) {
     typedef decltype(e) E;
-    constexpr bool W = decltype(w)::value;
-    if (a.q != nullptr) hipLaunchKernelGGL((k_swiglu<E, W, true>), dim3(grid_of(a.groups)), dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((k_swiglu<E, W, false>), dim3(grid_of(a.groups)), dim3(kThreads), 0, s, a);
+    constexpr bool W = decltype(w)::value, T = decltype(t)::value;
+    if (a.q != nullptr) hipLaunchKernelGGL((k_swiglu<E, W, T, true>), dim3(grid_of(a.groups)), dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((k_swiglu<E, W, T, false>), dim3(grid_of(a.groups)), dim3(kThreads), 0, s, a);
     return hipGetLastError();
   });
 }
 
 hipError_t launch_swiglu_backward(const SwigluArgs& a, hipStream_t s) {
-  return for_type(a, [&](auto e, auto w) {
-    hipLaunchKernelGGL((k_swiglu_backward<decltype(e), decltype(w)::value>), dim3(grid_of(a.groups)), dim3(kThreads), 0, s, a);
+  return for_type(a, [&](auto e, auto w, auto t) {
+    hipLaunchKernelGGL((k_swiglu_backward<decltype(e), decltype(w)::value, decltype(t)::value>), dim3(grid_of(a.groups)),
+                       dim3(kThreads), 0, s, a);
     return hipGetLastError();
   });
 }

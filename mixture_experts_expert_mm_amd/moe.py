@@ -649,13 +649,20 @@ def combine_backward(dy, rows, order, weights, *, stream=None):
 
 # ------------------------------------------------- activation, kept in 8 bits
 
-def _swiglu_args(h, activation_clamp, grad):
+def _swiglu_args(h, activation_clamp, gate_up_group, grad):
     M, N, dev = _rows("h", h)
     el = _element("h", h, True)
-    _need("h", h, h.dtype, (M, N), dev, grad=grad)
+    _need("h", h, h.dtype, (M, N), dev, grad)
     if N % 2 or N == 0:
         raise ValueError(f"h: [rows, 2 * intermediate] is needed, got {N} columns")
-    return M, N // 2, dev, el, _clamp_of(activation_clamp)
+    return M, N // 2, dev, el, _turn_of(gate_up_group, N // 2), _clamp_of(activation_clamp)
+
+
+def _turn_of(gate_up_group, I):
+    g = gate_up_group if type(gate_up_group) is int else _whole("gate_up_group", gate_up_group)
+    if g < 0 or (g and (g % 8 or I % g)):
+        raise ValueError(f"gate_up_group: 0, or a multiple of 8 that divides {I}, is needed, got {gate_up_group!r}")
+    return g
 
 
 def _clamp_of(activation_clamp):
@@ -667,29 +674,29 @@ def _clamp_of(activation_clamp):
     return c
 
 
-def _swiglu(h, M, I, el, clamp, keep):
+def _swiglu(h, M, I, el, turn, clamp, keep):
     dev = h.device
     a = torch.empty((M, I), dtype=h.dtype, device=dev)
     q = torch.empty((M, 2 * I), dtype=torch.int8, device=dev) if keep else None
     s = torch.empty((M, 2 * -(-I // 128)), dtype=torch.float32, device=dev) if keep else None
     if M:
-        B.mm_swiglu(M, I, el, h, clamp, a, q, s, _raw_stream(dev))
+        B.mm_swiglu(M, I, el, turn, h, clamp, a, q, s, _raw_stream(dev))
     return a, q, s
 
 
-def _swiglu_backward(da, q, s, clamp):
+def _swiglu_backward(da, q, s, turn, clamp):
     M, I = da.shape
     dh = torch.empty((M, 2 * I), dtype=da.dtype, device=da.device)
     if M:
-        B.mm_swiglu_backward(M, I, B.ELEMENT[da.dtype], da, q, s, clamp, dh, _raw_stream(da.device))
+        B.mm_swiglu_backward(M, I, B.ELEMENT[da.dtype], turn, da, q, s, clamp, dh, _raw_stream(da.device))
     return dh
 
 
 class _SwigluFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, h, M, I, el, clamp):
-        a, q, s = _swiglu(h, M, I, el, clamp, True)
-        ctx.clamp = clamp
+    def forward(ctx, h, M, I, el, turn, clamp):
+        a, q, s = _swiglu(h, M, I, el, turn, clamp, True)
+        ctx.how = turn, clamp
         ctx.save_for_backward(q, s)
         return a
 
@@ -697,37 +704,40 @@ class _SwigluFunction(torch.autograd.Function):
     @_once
     def backward(ctx, da):
         _not_captured()
-        return _swiglu_backward(_dense(da), *ctx.saved_tensors, ctx.clamp), None, None, None, None
+        return _swiglu_backward(_dense(da), *ctx.saved_tensors, *ctx.how), None, None, None, None, None
 
 
-def swiglu(h, *, activation_clamp=None, stream=None):
-    """mm_swiglu: a [M,I] = SiLU(h[:, :I]) * h[:, I:] of h [M,2I] (bf16, float16 or float32), both halves clamped to
-    [-activation_clamp, activation_clamp] first unless that is None.  Differentiable: what it keeps for the backward
-    pass is h in 8 bits, with a float32 scale per 128 values, and the gradient is that at the kept values."""
-    M, I, dev, el, clamp = _swiglu_args(h, activation_clamp, True)
+def swiglu(h, *, activation_clamp=None, gate_up_group=0, stream=None):
+    """mm_swiglu: a [M,I] = SiLU(gate) * up of h [M,2I] (bf16, float16 or float32), gate and up clamped to
+    [-activation_clamp, activation_clamp] first unless that is None.  gate_up_group: 0 where h is [gate | up]; behind the
+    rows of ``ExpertLayer.w1`` gate and up columns alternate in groups of ``layer.plan.gate_up_group``.  Differentiable:
+    what it keeps for the backward pass is h in 8 bits, with a float32 scale per 128 gate or up values, and the gradient
+    is that at the kept values."""
+    M, I, dev, el, turn, clamp = _swiglu_args(h, activation_clamp, gate_up_group, True)
     with _stream_of(dev, stream):
         if _records(h):
-            return _SwigluFunction.apply(h, M, I, el, clamp)
-        return _swiglu(h, M, I, el, clamp, False)[0]
+            return _SwigluFunction.apply(h, M, I, el, turn, clamp)
+        return _swiglu(h, M, I, el, turn, clamp, False)[0]
 
 
-def swiglu_forward(h, *, activation_clamp=None, stream=None):
-    """(a, codes int8 [M,2I], scales float32 [M,2*ceil(I/128)]): swiglu and the copy of h that swiglu_backward takes."""
-    M, I, dev, el, clamp = _swiglu_args(h, activation_clamp, False)
+def swiglu_forward(h, *, activation_clamp=None, gate_up_group=0, stream=None):
+    """(a, codes int8 [M,2I], scales float32 [M,2*ceil(I/128)]): swiglu and the copy of h that swiglu_backward takes
+    (codes lie as h does; scales of the gates come first)."""
+    M, I, dev, el, turn, clamp = _swiglu_args(h, activation_clamp, gate_up_group, False)
     with _stream_of(dev, stream):
-        return _swiglu(h, M, I, el, clamp, True)
+        return _swiglu(h, M, I, el, turn, clamp, True)
 
 
-def swiglu_backward(da, codes, scales, *, activation_clamp=None, stream=None):
+def swiglu_backward(da, codes, scales, *, activation_clamp=None, gate_up_group=0, stream=None):
     """mm_swiglu_backward: h's gradient [M,2I] from a's [M,I] and what swiglu_forward kept."""
     M, I, dev = _rows("da", da)
     _element("da", da, True)
     _need("da", da, da.dtype, (M, I), dev)
     _need("codes", codes, torch.int8, (M, 2 * I), dev)
     _need("scales", scales, torch.float32, (M, 2 * -(-I // 128)), dev)
-    clamp = _clamp_of(activation_clamp)
+    turn, clamp = _turn_of(gate_up_group, I), _clamp_of(activation_clamp)
     with _stream_of(dev, stream):
-        return _swiglu_backward(da, codes, scales, clamp)
+        return _swiglu_backward(da, codes, scales, turn, clamp)
 
 
 # ------------------------------------------------- 8-bit integer product

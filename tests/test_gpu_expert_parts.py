@@ -82,6 +82,12 @@ def test_serving(T, H, I, E, K):
     assert torch.equal(h2[:n], h[:n])
     layer = moe.ExpertLayer(T, H, I, E, K, "int8")
     layer.load_weights(w1.transpose(1, 2).contiguous(), w2.transpose(1, 2).contiguous(), s1, s2)
+    # the parts on the layer's own weights: gate and up columns alternate, and so do their scales
+    turn = layer.plan.gate_up_group
+    s1_turned = layer.s1.view(E, 2, I // turn, turn).transpose(1, 2).reshape(E, 2 * I).contiguous()
+    a2 = moe.swiglu(moe.int8_linear(rows, layer.w1, s1_turned, o.offsets, o.counts), gate_up_group=turn)
+    assert torch.equal(a2[:n], a[:n])
+    assert torch.equal(moe.combine_tokens(moe.int8_linear(a2, layer.w2, layer.s2, o.offsets, o.counts), o, gates), y)
     whole, counts = layer.forward(x.cuda(), ids, gates, active=active.cuda())
     assert torch.equal(counts, o.counts)
     # The layer quantises its float32 SwiGLU(h); the parts round h and a to bf16 first.  With |silu'| <= 1.1 and

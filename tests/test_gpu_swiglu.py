@@ -142,3 +142,28 @@ def test_gradient_shapes_streams_and_graphs():
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(out, want))
         assert torch.equal(dh, moe.swiglu_backward(db, *want[1:]))
+
+
+def alternate(t, I, g):
+    """Columns [gate | up] of t in turns of g."""
+    return t.view(t.shape[0], 2, I // g, g).transpose(1, 2).reshape(t.shape).contiguous()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("M,I,g", [(1, 32, 32), (5, 128, 32), (3, 8, 8), (40, 200, 40), (333, 1408, 32), (17, 2048, 32), (9, 264, 8),
+                                   (4, 264, 264), (700, 96, 24)])
+@pytest.mark.parametrize("clamp", [None, 1.5])
+def test_alternating_columns(M, I, g, dtype, clamp):
+    """The same values, codes, scales and gradients wherever the columns lie."""
+    h, da = inputs(M, I, dtype, 7)
+    a, q, s = moe.swiglu_forward(h.cuda(), activation_clamp=clamp)
+    dh = moe.swiglu_backward(da.cuda(), q, s, activation_clamp=clamp)
+    turned = alternate(h, I, g).cuda()
+    b, p, r = moe.swiglu_forward(turned, activation_clamp=clamp, gate_up_group=g)
+    assert torch.equal(a, b) and torch.equal(s, r) and torch.equal(alternate(q, I, g), p)
+    assert torch.equal(moe.swiglu(turned, activation_clamp=clamp, gate_up_group=g), a)
+    d = moe.swiglu_backward(da.cuda(), p, r, activation_clamp=clamp, gate_up_group=g)
+    assert torch.equal(alternate(dh, I, g), d)
+    hr = turned.requires_grad_()
+    moe.swiglu(hr, activation_clamp=clamp, gate_up_group=g).backward(da.cuda())
+    assert torch.equal(hr.grad, d)

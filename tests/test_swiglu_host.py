@@ -24,8 +24,8 @@ def lib():
 
 
 def test_entry_points_validate_before_any_hip_call(lib):
-    fwd = [4, 8, 0, GOOD, 0, 0.0, GOOD, GOOD, GOOD, None]
-    bwd = [4, 8, 0, GOOD, GOOD, GOOD, 0, 0.0, GOOD, None]
+    fwd = [4, 8, 0, 0, GOOD, 0, 0.0, GOOD, GOOD, GOOD, None]
+    bwd = [4, 8, 0, 0, GOOD, GOOD, GOOD, 0, 0.0, GOOD, None]
 
     def call(fn, args, *changes):
         a = list(args)
@@ -39,14 +39,16 @@ def test_entry_points_validate_before_any_hip_call(lib):
         assert call(fn, args, (0, 1 << 24), (1, 1 << 14)) == 1                 # 2^31 groups
         for v in (-1, 3, 4):
             assert call(fn, args, (2, v)) == 2
+        for cols, v in ((8, -8), (8, 4), (8, 16), (40, 32), (24, 12)):             # groups of gate and up columns
+            assert call(fn, args, (1, cols), (3, v)) == 1
     for on, c in ((2, 0.0), (1, -1.0), (1, float("nan"))):
-        assert call(lib.mm_swiglu, fwd, (4, on), (5, c)) == 1
-        assert call(lib.mm_swiglu_backward, bwd, (6, on), (7, c)) == 1
-    for i in (3, 6):
+        assert call(lib.mm_swiglu, fwd, (5, on), (6, c)) == 1
+        assert call(lib.mm_swiglu_backward, bwd, (7, on), (8, c)) == 1
+    for i in (4, 7):
         assert call(lib.mm_swiglu, fwd, (i, None)) == 1 and call(lib.mm_swiglu, fwd, (i, GOOD + 8)) == 1
-    for i, v in ((7, None), (8, None), (7, GOOD + 8), (8, GOOD + 2)):          # codes and scales: both or neither
+    for i, v in ((8, None), (9, None), (8, GOOD + 8), (9, GOOD + 2)):          # codes and scales: both or neither
         assert call(lib.mm_swiglu, fwd, (i, v)) == 1
-    for i in (3, 4, 5, 8):
+    for i in (4, 5, 6, 9):
         assert call(lib.mm_swiglu_backward, bwd, (i, None)) == 1
         assert call(lib.mm_swiglu_backward, bwd, (i, GOOD + 2)) == 1
     assert [B.mm_kernel_name(i) for i in (21, 22)] == ["swiglu", "swiglu_backward"]
@@ -67,14 +69,14 @@ def launches(monkeypatch):
 
 def test_what_is_launched(launches):
     h = torch.zeros(3, 520, dtype=torch.bfloat16)
-    assert moe.swiglu(h).shape == (3, 260) and launches[-1][1][6] is None      # nothing is kept
+    assert moe.swiglu(h).shape == (3, 260) and launches[-1][1][7] is None      # nothing is kept
     a, q, s = moe.swiglu_forward(h, activation_clamp=2)
-    assert q.shape == h.shape and q.dtype == torch.int8 and s.shape == (3, 6) and launches[-1][1][4] == 2.0
+    assert q.shape == h.shape and q.dtype == torch.int8 and s.shape == (3, 6) and launches[-1][1][5] == 2.0
     moe.swiglu(h.clone().requires_grad_())
-    assert launches[-1][1][6] is not None
+    assert launches[-1][1][7] is not None
     with torch.no_grad():
         moe.swiglu(h.clone().requires_grad_())
-    assert launches[-1][1][6] is None
+    assert launches[-1][1][7] is None
     assert moe.swiglu_backward(a, q, s).shape == h.shape
     n = len(launches)
     assert moe.swiglu(h[:0]).shape == (0, 260) and len(launches) == n
@@ -90,6 +92,9 @@ def test_refusals(launches):
         ("activation_clamp", lambda: moe.swiglu(h, activation_clamp=-1.0)),
         ("activation_clamp", lambda: moe.swiglu(h, activation_clamp=float("nan"))),
         ("activation_clamp", lambda: moe.swiglu_backward(da, q, s, activation_clamp=-2)),
+        ("gate_up_group", lambda: moe.swiglu(h, gate_up_group=12)), ("gate_up_group", lambda: moe.swiglu(h, gate_up_group=32)),
+        ("gate_up_group", lambda: moe.swiglu(h, gate_up_group=-8)), ("gate_up_group", lambda: moe.swiglu(h, gate_up_group=1.5)),
+        ("gate_up_group", lambda: moe.swiglu_backward(da, q, s, gate_up_group=8)),
         ("da", lambda: moe.swiglu_backward(da.double(), q, s)), ("codes", lambda: moe.swiglu_backward(da, q[:2], s)),
         ("codes", lambda: moe.swiglu_backward(da, h, s)), ("scales", lambda: moe.swiglu_backward(da, q, s[:, :5])),
         ("scales", lambda: moe.swiglu_backward(da, q, s.half())), ("da", lambda: moe.swiglu_backward(da.t(), q, s)),
