@@ -475,32 +475,32 @@ def _dense(t):
     return t.clone() if t.data_ptr() % 16 else t
 
 
-def _sort_rows(x, order, T, E, K):
+def _sort_rows(x, offsets, row_of_route, T, E, K):
     H = x.shape[1]
     rows = torch.empty((T * K, H), dtype=x.dtype, device=x.device)
     if T:
         plan = _sort_plan(T, H, E, K, B.ELEMENT[x.dtype])
-        B.mm_sort_rows(plan, x, order.offsets, order.row_of_route, rows, _raw_stream(x.device))
+        B.mm_sort_rows(plan, x, offsets, row_of_route, rows, _raw_stream(x.device))
     return rows
 
 
-def _combine(rows, order, weights, T, E, K):
+def _combine(rows, row_of_route, weights, T, E, K):
     H = rows.shape[1]
     y = torch.empty((T, H), dtype=rows.dtype, device=rows.device)
     if T:
         plan = _sort_plan(T, H, E, K, B.ELEMENT[rows.dtype])
-        B.mm_combine_tokens(plan, rows, order.row_of_route, weights, y, _raw_stream(rows.device))
+        B.mm_combine_tokens(plan, rows, row_of_route, weights, y, _raw_stream(rows.device))
     return y
 
 
-def _combine_backward(dy, rows, order, weights, T, E, K, of_rows, of_weights):
+def _combine_backward(dy, rows, offsets, row_of_route, weights, T, E, K, of_rows, of_weights):
     H, dev = dy.shape[1], dy.device
     drows = torch.empty((T * K, H), dtype=dy.dtype, device=dev) if of_rows else None
     dweights = torch.empty((T, K), dtype=torch.float32, device=dev) if of_weights else None
     if T and (of_rows or of_weights):
         plan = _sort_plan(T, H, E, K, B.ELEMENT[dy.dtype])
-        B.mm_combine_backward(plan, dy, rows if of_weights else None, order.offsets, order.row_of_route, weights, drows,
-                              dweights, _raw_stream(dev))
+        B.mm_combine_backward(plan, dy, rows if of_weights else None, offsets, row_of_route, weights, drows, dweights,
+                              _raw_stream(dev))
     return drows, dweights
 
 
@@ -510,17 +510,26 @@ def _once(backward):
     return lambda ctx, *grads: recorded(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
 
 
-def _keep_order(ctx, order):
-    # as attributes: each saved tensor costs to unpack; what is written over is found all the same
-    ctx.order = order
-    ctx.versions = order.row_of_route._version, order.offsets._version
+def _keep(ctx, **tensors):
+    """Saves tensors for the backward pass: they themselves, since the caller's TokenOrder may hold others by then."""
+    ctx.kept = [(name, t.dtype, t.shape) for name, t in tensors.items()]
+    # (an order may come from inference mode, whose tensors autograd does not save)
+    ctx.save_for_backward(*(t.clone() if t.is_inference() else t for t in tensors.values()))
 
 
-def _kept_order(ctx):
-    order = ctx.order
-    if ctx.versions != (order.row_of_route._version, order.offsets._version):
-        raise RuntimeError("order: was modified in place before the backward pass")
-    return order
+def _kept(ctx, device):
+    """What _keep saved, looked at again: data exchanged under a tensor, or by a hook of saved tensors, is not noticed by
+    autograd, and the kernels would read past its end."""
+    try:
+        tensors = ctx.saved_tensors
+    except RuntimeError as e:
+        if "inplace operation" not in str(e):
+            raise
+        names = ", ".join(name for name, _, _ in ctx.kept)
+        raise RuntimeError(f"{names}: one of them was modified in place before the backward pass") from e
+    for t, (name, dtype, shape) in zip(tensors, ctx.kept):
+        _need(name, t, dtype, shape, device, grad=True)
+    return tensors
 
 
 class _SortFunction(torch.autograd.Function):
@@ -529,39 +538,41 @@ class _SortFunction(torch.autograd.Function):
         """made: an order to sort by, or nothing yet, which args then make."""
         ctx.dims = args[-3:]
         if made:
-            rows = _sort_rows(x, made[0], *ctx.dims)
+            rows = _sort_rows(x, made[0].offsets, made[0].row_of_route, *ctx.dims)
         else:
             rows, order = _sort_tokens(x, *args)
             made.append(order)
-        _keep_order(ctx, made[0])
+        _keep(ctx, row_of_route=made[0].row_of_route)
         return rows
 
     @staticmethod
     @_once
     def backward(ctx, drows):
         _not_captured()
-        return _combine(_dense(drows), _kept_order(ctx), None, *ctx.dims), None, None
+        return _combine(_dense(drows), *_kept(ctx, drows.device), None, *ctx.dims), None, None
 
 
 class _CombineFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, weights, order, dims):
         ctx.dims = dims
-        _keep_order(ctx, order)
-        if weights is not None:
-            ctx.save_for_backward(rows if weights.requires_grad else None, weights)
-        return _combine(rows, order, weights, *dims)
+        of_weights = {} if weights is None else dict(weights=weights)
+        if weights is not None and weights.requires_grad:
+            of_weights["rows"] = rows
+        _keep(ctx, offsets=order.offsets, row_of_route=order.row_of_route, **of_weights)
+        return _combine(rows, order.row_of_route, weights, *dims)
 
     @staticmethod
     @_once
     def backward(ctx, dy):
         _not_captured()
-        order, dy = _kept_order(ctx), _dense(dy)
+        dy = _dense(dy)
         of_rows, of_weights, _, _ = ctx.needs_input_grad
-        saved = ctx.saved_tensors
+        offsets, row, *saved = _kept(ctx, dy.device)
         if not saved:
-            return _sort_rows(dy, order, *ctx.dims), None, None, None
-        return *_combine_backward(dy, saved[0], order, saved[1], *ctx.dims, of_rows, of_weights), None, None
+            return _sort_rows(dy, offsets, row, *ctx.dims), None, None, None
+        weights, rows = saved if of_weights else (saved[0], None)
+        return *_combine_backward(dy, rows, offsets, row, weights, *ctx.dims, of_rows, of_weights), None, None
 
 
 def _sort_tokens(x, topk_ids, active, plan, T, E, K):
@@ -609,7 +620,9 @@ def sort_rows(x, order, *, stream=None):
         raise ValueError(f"order: one of {T} tokens is needed, got one of {dims[0]}")
     _sort_plan(max(T, 1), H, dims[1], dims[2], el)
     with _stream_of(dev, stream):
-        return _SortFunction.apply(x, dims, [order]) if _records(x) else _sort_rows(x, order, *dims)
+        if _records(x):
+            return _SortFunction.apply(x, dims, [order])
+        return _sort_rows(x, order.offsets, order.row_of_route, *dims)
 
 
 def _combine_args(name, rows, order, weights):
@@ -631,7 +644,7 @@ def combine_tokens(rows, order, weights=None, *, stream=None):
     with _stream_of(dev, stream):
         if _records(rows, weights):
             return _CombineFunction.apply(rows, weights, order, dims)
-        return _combine(rows, order, weights, *dims)
+        return _combine(rows, order.row_of_route, weights, *dims)
 
 
 def combine_backward(dy, rows, order, weights, *, stream=None):
@@ -644,7 +657,7 @@ def combine_backward(dy, rows, order, weights, *, stream=None):
         _need(name, t, t.dtype, t.shape, dev)
     _need("dy", dy, rows.dtype, (dims[0], H), dev)
     with _stream_of(dev, stream):
-        return _combine_backward(dy, rows, order, weights, *dims, True, True)
+        return _combine_backward(dy, rows, order.offsets, order.row_of_route, weights, *dims, True, True)
 
 
 # ------------------------------------------------- activation, kept in 8 bits
@@ -697,14 +710,14 @@ class _SwigluFunction(torch.autograd.Function):
     def forward(ctx, h, M, I, el, turn, clamp):
         a, q, s = _swiglu(h, M, I, el, turn, clamp, True)
         ctx.how = turn, clamp
-        ctx.save_for_backward(q, s)
+        _keep(ctx, codes=q, scales=s)
         return a
 
     @staticmethod
     @_once
     def backward(ctx, da):
         _not_captured()
-        return _swiglu_backward(_dense(da), *ctx.saved_tensors, *ctx.how), None, None, None, None, None
+        return _swiglu_backward(_dense(da), *_kept(ctx, da.device), *ctx.how), None, None, None, None, None
 
 
 def swiglu(h, *, activation_clamp=None, gate_up_group=0, stream=None):
