@@ -578,9 +578,10 @@ class _CombineFunction(torch.autograd.Function):
 def _sort_tokens(x, topk_ids, active, plan, T, E, K):
     R, dev = T * K, x.device
     rows = torch.empty((R, x.shape[1]), dtype=x.dtype, device=dev)
-    # one allocation for the four
-    counts, offsets, row, route = (torch.empty if T else torch.zeros)(
-        2 * (E + R) + 1, dtype=torch.int32, device=dev).split_with_sizes((E, E + 1, R, R))
+    # one allocation for the four, each with a version of its own: what a program writes into one (counts of several
+    # batches summed up, say) is no change of another, which the backward pass reads
+    buffer = (torch.empty if T else torch.zeros)(2 * (E + R) + 1, dtype=torch.int32, device=dev)
+    counts, offsets, row, route = torch.unsafe_split_with_sizes(buffer, (E, E + 1, R, R))
     if T:
         ws = _workspace(plan.workspace_bytes, dev) if plan.workspace_bytes else None
         B.mm_sort_tokens(plan, topk_ids, active, x, counts, offsets, row, route, rows, ws, _raw_stream(dev))
