@@ -183,17 +183,24 @@ _block_plan = functools.lru_cache(maxsize=256)(B.mm_block_plan_create)
 FEW_MAX_TOKENS = 64
 
 
-def _need(name, t, dtype, shape, device, grad=False):
+_VEC = 16
+
+
+def _need(name, t, dtype, shape, device, grad=False, at=1):
     """The one check of a tensor argument: a message that says what it has to be.  grad: the operator has a gradient
-    with respect to it."""
+    with respect to it.  at: the number of bytes of which its address is a multiple (_VEC where it is read or written in
+    whole vectors)."""
     if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()
-            and forward_ad._current_level < 0 and (grad or not t.requires_grad)):
+            and (at == 1 or t.data_ptr() % at == 0) and forward_ad._current_level < 0 and (grad or not t.requires_grad)):
         return
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: a tensor is needed, got {type(t).__name__}")
     if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor {list(shape)} on {device} is needed, got {t.dtype} "
                          f"{list(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
+    if t.data_ptr() % at:
+        raise ValueError(f"{name}: its address has to be a multiple of {at} bytes, which a part of another tensor may not "
+                         f"begin at (clone it)")
     if t.requires_grad and not grad and torch.is_grad_enabled():
         raise ValueError(f"{name}: requires a gradient, which this operator does not compute (call it under no_grad)")
     if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
@@ -262,8 +269,8 @@ def route(x, weight, bias=None, *, topk, scoring="softmax", renormalize=True, sc
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight: a matrix [experts, hidden] is needed")
     E = weight.shape[0]
-    _need("x", x, torch.bfloat16, (T, H), dev)
-    _need("weight", weight, torch.bfloat16, (E, H), dev)
+    _need("x", x, torch.bfloat16, (T, H), dev, at=_VEC)
+    _need("weight", weight, torch.bfloat16, (E, H), dev, at=_VEC)
     if bias is not None:
         _need("bias", bias, torch.float32, (E,), dev)
     if active is not None:
@@ -304,15 +311,15 @@ def moe_few(x, w1, w2, s1=None, s2=None, *, topk_ids=None, topk_weights=None, ro
         fmt = "fp8_block" if isinstance(s1, torch.Tensor) and s1.dim() == 3 else "fp8"
     else:
         raise ValueError(f"w1: bf16 or float8_e4m3fn weights are needed, got {w1.dtype}")
-    _need("x", x, torch.bfloat16, (T, H), dev)
-    _need("w1", w1, w1.dtype, (Et, 2 * I, H), dev)
-    _need("w2", w2, w1.dtype, (Et, H, I), dev)
+    _need("x", x, torch.bfloat16, (T, H), dev, at=_VEC)
+    _need("w1", w1, w1.dtype, (Et, 2 * I, H), dev, at=_VEC)
+    _need("w2", w2, w1.dtype, (Et, H, I), dev, at=_VEC)
     if fmt == "bf16":
         if s1 is not None or s2 is not None:
             raise ValueError("s1, s2: bf16 weights have no scales")
     else:
-        _need("s1", s1, torch.float32, (Et, 2 * I) if fmt == "fp8" else (Et, 2 * I // 128, H // 128), dev)
-        _need("s2", s2, torch.float32, (Et, H) if fmt == "fp8" else (Et, H // 128, I // 128), dev)
+        _need("s1", s1, torch.float32, (Et, 2 * I) if fmt == "fp8" else (Et, 2 * I // 128, H // 128), dev, at=_VEC)
+        _need("s2", s2, torch.float32, (Et, H) if fmt == "fp8" else (Et, H // 128, I // 128), dev, at=_VEC)
     if active is not None:
         _need("active", active, torch.int8, (T,), dev)
     routed = router_weight is not None
@@ -331,7 +338,7 @@ def moe_few(x, w1, w2, s1=None, s2=None, *, topk_ids=None, topk_weights=None, ro
     plan = _few_plan(max(T, 1), H, I, E, K, fmt, y_dtype, activation_clamp, S)
     ydt = _y_dtype(plan)
     if y is not None:
-        _need("y", y, ydt, (T, H), dev)
+        _need("y", y, ydt, (T, H), dev, at=_VEC)
         _apart(y, w1, w2, s1, s2, topk_ids, topk_weights, active)      # (x has been read by then)
     with _stream_of(dev, stream):
         if y is None:
@@ -348,7 +355,7 @@ def moe_few(x, w1, w2, s1=None, s2=None, *, topk_ids=None, topk_weights=None, ro
 def block_quantize(x, stream=None):
     """mm_block_quantize: (codes float8_e4m3fn [M,K], scales float32 [M,K/128]) of bf16 rows."""
     M, K, dev = _rows("x", x)
-    _need("x", x, torch.bfloat16, (M, K), dev)
+    _need("x", x, torch.bfloat16, (M, K), dev, at=_VEC)
     if K % 128 or K == 0:
         raise ValueError(f"x: the columns have to be a multiple of 128, got {K}")
     with _stream_of(dev, stream):
@@ -373,11 +380,11 @@ def _block_args(M, K, dev, rows, w, ws, offsets, counts, y):
         raise ValueError("w: [out, in] or [groups, out, in] is needed")
     G, N = (1, w.shape[0]) if w.dim() == 2 else (w.shape[0], w.shape[1])
     lead = () if w.dim() == 2 else (G,)
-    _need("w", w, torch.float8_e4m3fn, lead + (N, K), dev)
+    _need("w", w, torch.float8_e4m3fn, lead + (N, K), dev, at=_VEC)
     _need("ws", ws, torch.float32, lead + (-(-N // 128), K // 128), dev)
     _group_args(G, offsets, counts, dev)
     if y is not None:
-        _need("y", y, torch.bfloat16, (M, N), dev)
+        _need("y", y, torch.bfloat16, (M, N), dev, at=_VEC)
         _apart(y, *rows, w, ws, offsets, counts)
     return N, _block_plan(max(M, 1), N, K, G)
 
@@ -388,7 +395,7 @@ def block_matmul(q, s, w, ws, offsets=None, counts=None, y=None, stream=None):
     (int32; offsets may have G + 1 entries).  Rows that no group covers are left as they are (in a new y: unset).  y
     must not overlap an input."""
     M, K, dev = _rows("q", q)
-    _need("q", q, torch.float8_e4m3fn, (M, K), dev)
+    _need("q", q, torch.float8_e4m3fn, (M, K), dev, at=_VEC)
     _need("s", s, torch.float32, (M, K // 128), dev)
     N, plan = _block_args(M, K, dev, (q, s), w, ws, offsets, counts, y)
     with _stream_of(dev, stream):
@@ -402,7 +409,7 @@ def block_matmul(q, s, w, ws, offsets=None, counts=None, y=None, stream=None):
 def block_linear(x, w, ws, offsets=None, counts=None, y=None, stream=None):
     """mm_block_linear: block_matmul of x's (bf16 [M,K]) codes and scales, in one call.  y may overlap x."""
     M, K, dev = _rows("x", x)
-    _need("x", x, torch.bfloat16, (M, K), dev)
+    _need("x", x, torch.bfloat16, (M, K), dev, at=_VEC)
     N, plan = _block_args(M, K, dev, (), w, ws, offsets, counts, y)
     with _stream_of(dev, stream):
         if y is None:
@@ -472,7 +479,7 @@ def _dense(t):
     """A gradient as autograd hands it over (expanded, strided, at any address) in the form that kernels take."""
     if not t.is_contiguous():
         t = t.contiguous()
-    return t.clone() if t.data_ptr() % 16 else t
+    return t.clone() if t.data_ptr() % _VEC else t
 
 
 def _sort_rows(x, offsets, row_of_route, T, E, K):
@@ -596,7 +603,7 @@ def sort_tokens(x, topk_ids, num_experts, *, active=None, stream=None):
     Differentiable with respect to x; the gradient is ``combine_tokens(drows, order)``."""
     T, H, dev = _rows("x", x)
     el = _element("x", x, False)
-    _need("x", x, x.dtype, (T, H), dev, el != B.MM_ELEMENT_8BIT)
+    _need("x", x, x.dtype, (T, H), dev, el != B.MM_ELEMENT_8BIT, _VEC)
     K = topk_ids.shape[1] if isinstance(topk_ids, torch.Tensor) and topk_ids.dim() == 2 else 0
     _need("topk_ids", topk_ids, torch.int32, (T, K), dev)
     if active is not None:
@@ -615,7 +622,7 @@ def sort_rows(x, order, *, stream=None):
     made.  Differentiable as sort_tokens is."""
     T, H, dev = _rows("x", x)
     el = _element("x", x, False)
-    _need("x", x, x.dtype, (T, H), dev, grad=el != B.MM_ELEMENT_8BIT)
+    _need("x", x, x.dtype, (T, H), dev, el != B.MM_ELEMENT_8BIT, _VEC)
     dims = _order_of(order, dev)
     if dims[0] != T:
         raise ValueError(f"order: one of {T} tokens is needed, got one of {dims[0]}")
@@ -630,7 +637,7 @@ def _combine_args(name, rows, order, weights):
     R, H, dev = _rows(name, rows)
     el = _element(name, rows, True)
     dims = T, E, K = _order_of(order, dev)
-    _need(name, rows, rows.dtype, (T * K, H), dev, grad=True)
+    _need(name, rows, rows.dtype, (T * K, H), dev, True, _VEC)
     if weights is not None:
         _need("weights", weights, torch.float32, (T, K), dev, grad=True)
     _sort_plan(max(T, 1), H, E, K, el)
@@ -656,7 +663,7 @@ def combine_backward(dy, rows, order, weights, *, stream=None):
     dims, H, dev = _combine_args("rows", rows, order, weights)
     for name, t in (("rows", rows), ("weights", weights)):
         _need(name, t, t.dtype, t.shape, dev)
-    _need("dy", dy, rows.dtype, (dims[0], H), dev)
+    _need("dy", dy, rows.dtype, (dims[0], H), dev, at=_VEC)
     with _stream_of(dev, stream):
         return _combine_backward(dy, rows, order.offsets, order.row_of_route, weights, *dims, True, True)
 
@@ -666,7 +673,7 @@ def combine_backward(dy, rows, order, weights, *, stream=None):
 def _swiglu_args(h, activation_clamp, gate_up_group, grad):
     M, N, dev = _rows("h", h)
     el = _element("h", h, True)
-    _need("h", h, h.dtype, (M, N), dev, grad)
+    _need("h", h, h.dtype, (M, N), dev, grad, _VEC)
     if N % 2 or N == 0:
         raise ValueError(f"h: [rows, 2 * intermediate] is needed, got {N} columns")
     return M, N // 2, dev, el, _turn_of(gate_up_group, N // 2), _clamp_of(activation_clamp)
@@ -746,8 +753,8 @@ def swiglu_backward(da, codes, scales, *, activation_clamp=None, gate_up_group=0
     """mm_swiglu_backward: h's gradient [M,2I] from a's [M,I] and what swiglu_forward kept."""
     M, I, dev = _rows("da", da)
     _element("da", da, True)
-    _need("da", da, da.dtype, (M, I), dev)
-    _need("codes", codes, torch.int8, (M, 2 * I), dev)
+    _need("da", da, da.dtype, (M, I), dev, at=_VEC)
+    _need("codes", codes, torch.int8, (M, 2 * I), dev, at=_VEC)
     _need("scales", scales, torch.float32, (M, 2 * -(-I // 128)), dev)
     turn, clamp = _turn_of(gate_up_group, I), _clamp_of(activation_clamp)
     with _stream_of(dev, stream):
@@ -765,7 +772,7 @@ def int8_quantize(x, stream=None):
     (bf16, float16 or float32; K a multiple of 16)."""
     M, K, dev = _rows("x", x)
     el = _element("x", x, True)
-    _need("x", x, x.dtype, (M, K), dev)
+    _need("x", x, x.dtype, (M, K), dev, at=_VEC)
     if K % 16 or K == 0:
         raise ValueError(f"x: the columns have to be a multiple of 16, got {K}")
     with _stream_of(dev, stream):
@@ -781,14 +788,14 @@ def _int8_args(M, K, dev, x_element, rows, w, ws, offsets, counts, y_dtype, y):
         raise ValueError("w: [out, in] or [groups, out, in] is needed")
     G, N = (1, w.shape[0]) if w.dim() == 2 else (w.shape[0], w.shape[1])
     lead = () if w.dim() == 2 else (G,)
-    _need("w", w, torch.int8, lead + (N, K), dev)
-    _need("ws", ws, torch.float32, lead + (N,), dev)
+    _need("w", w, torch.int8, lead + (N, K), dev, at=_VEC)
+    _need("ws", ws, torch.float32, lead + (N,), dev, at=1 if N % 4 else _VEC)
     _group_args(G, offsets, counts, dev)
     if y_dtype not in _Y_TYPES:
         raise ValueError(f"y_dtype: one of {sorted(_Y_TYPES)} is needed, got {y_dtype!r}")
     dt = _Y_TYPES[y_dtype]
     if y is not None:
-        _need("y", y, dt, (M, N), dev)
+        _need("y", y, dt, (M, N), dev, at=_VEC)
         _apart(y, *rows, w, ws, offsets, counts)
     return N, dt, _int8_plan(max(M, 1), N, K, G, x_element, B.ELEMENT[dt])
 
@@ -798,7 +805,7 @@ def int8_matmul(q, s, w, ws, offsets=None, counts=None, *, y_dtype="bf16", y=Non
     w [G,N,K] and ws [G,N], of groups of rows as in ``block_matmul``; sort_tokens' order has their offsets and counts.
     y_dtype: "bf16", "f16" or "f32".  Sums are exact.  y must not overlap an input."""
     M, K, dev = _rows("q", q)
-    _need("q", q, torch.int8, (M, K), dev)
+    _need("q", q, torch.int8, (M, K), dev, at=_VEC)
     _need("s", s, torch.float32, (M,), dev)
     N, dt, plan = _int8_args(M, K, dev, B.MM_ELEMENT_BF16, (q, s), w, ws, offsets, counts, y_dtype, y)
     with _stream_of(dev, stream):
@@ -813,7 +820,7 @@ def int8_linear(x, w, ws, offsets=None, counts=None, *, y_dtype="bf16", y=None, 
     """mm_int8_linear: int8_matmul of x's (bf16, float16 or float32 [M,K]) codes and scales, in one call."""
     M, K, dev = _rows("x", x)
     el = _element("x", x, True)
-    _need("x", x, x.dtype, (M, K), dev)
+    _need("x", x, x.dtype, (M, K), dev, at=_VEC)
     N, dt, plan = _int8_args(M, K, dev, el, (x,), w, ws, offsets, counts, y_dtype, y)
     with _stream_of(dev, stream):
         if y is None:
