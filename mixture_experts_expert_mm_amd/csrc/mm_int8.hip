@@ -321,8 +321,9 @@ __global__ __launch_bounds__(256) void k_int8_few(Int8Args a) {
   stream_tail<E, 4>(a, red);
 }
 
-// Products with many rows: 256 x 256 tiles, and 128 x 256 for a group's rest; up
-// to 16 rows behind the tiles of one matrix are streamed by who is done.
+// Products with many rows, or too many columns for small tiles: 256 x 256 tiles, and
+// 128 x 256 for a group's rest; up to 16 rows behind the tiles of one matrix (which
+// may have no tile) are streamed by who is done.
 // One workgroup a CU; XCD x takes an eighth of each class's list (neighbours
 // share an L2), and its workgroups take every n-th tile of it in turn.
 template <typename E>
@@ -535,7 +536,9 @@ hipError_t gemm(const Int8Args& args, int num_cus, hipStream_t s) {
   } else {
     // one matrix: up to 16 rows beyond the blocks of 256 are streamed, in place of a
     // round more (16388 x 4096 x 2048: 2.6 us for the last four rows; 4097 x 4096 x 7168,
-    // whose tiles all end together: 8.5)
+    // whose tiles all end together: 8.5).  9 to 16 rows of more columns than 128 x 128
+    // tiles take in two rounds (65536 on 256 CUs) come here too: all of them are such
+    // rows, and there is no tile
     const int64_t rest = a.offsets == nullptr ? a.M % kBM : 0;
     if (rest <= kFewRows) {
       a.tail = (int)rest;
