@@ -517,14 +517,13 @@ def _once(backward):
     return lambda ctx, *grads: recorded(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
 
 
-def _keep(ctx, **tensors):
+def _keep(ctx, *tensors):
     """Saves tensors for the backward pass: they themselves, since the caller's TokenOrder may hold others by then."""
-    ctx.kept = [(name, t.dtype, t.shape) for name, t in tensors.items()]
-    # (an order may come from inference mode, whose tensors autograd does not save)
-    ctx.save_for_backward(*(t.clone() if t.is_inference() else t for t in tensors.values()))
+    ctx.save_for_backward(*tensors)
+    ctx.kept = [(t.dtype, t.nbytes, True, t.get_device()) for t in tensors]
 
 
-def _kept(ctx, device):
+def _kept(ctx, *names):
     """What _keep saved, looked at again: data exchanged under a tensor, or by a hook of saved tensors, is not noticed by
     autograd, and the kernels would read past its end."""
     try:
@@ -532,11 +531,16 @@ def _kept(ctx, device):
     except RuntimeError as e:
         if "inplace operation" not in str(e):
             raise
-        names = ", ".join(name for name, _, _ in ctx.kept)
-        raise RuntimeError(f"{names}: one of them was modified in place before the backward pass") from e
-    for t, (name, dtype, shape) in zip(tensors, ctx.kept):
-        _need(name, t, dtype, shape, device, grad=True)
+        raise RuntimeError(f"{', '.join(names)}: one of them was modified in place before the backward pass") from e
+    if [(t.dtype, t.nbytes, t.is_contiguous(), t.get_device()) for t in tensors] != ctx.kept:
+        what = ", ".join(f"{n} {t.dtype} {list(t.shape)} on {t.device}" for n, t in zip(names, tensors))
+        raise RuntimeError(f"{what}: what the forward call was given is needed, but one of them was exchanged")
     return tensors
+
+
+def _savable(t):
+    """t, or a copy of one that was made in inference mode, which autograd does not save."""
+    return t.clone() if t.is_inference() else t
 
 
 class _SortFunction(torch.autograd.Function):
@@ -549,24 +553,22 @@ class _SortFunction(torch.autograd.Function):
         else:
             rows, order = _sort_tokens(x, *args)
             made.append(order)
-        _keep(ctx, row_of_route=made[0].row_of_route)
+        _keep(ctx, _savable(made[0].row_of_route))
         return rows
 
     @staticmethod
     @_once
     def backward(ctx, drows):
         _not_captured()
-        return _combine(_dense(drows), *_kept(ctx, drows.device), None, *ctx.dims), None, None
+        return _combine(_dense(drows), *_kept(ctx, "row_of_route"), None, *ctx.dims), None, None
 
 
 class _CombineFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, weights, order, dims):
         ctx.dims = dims
-        of_weights = {} if weights is None else dict(weights=weights)
-        if weights is not None and weights.requires_grad:
-            of_weights["rows"] = rows
-        _keep(ctx, offsets=order.offsets, row_of_route=order.row_of_route, **of_weights)
+        kept = () if weights is None else (weights, rows) if weights.requires_grad else (weights,)
+        _keep(ctx, _savable(order.offsets), _savable(order.row_of_route), *kept)
         return _combine(rows, order.row_of_route, weights, *dims)
 
     @staticmethod
@@ -575,7 +577,7 @@ class _CombineFunction(torch.autograd.Function):
         _not_captured()
         dy = _dense(dy)
         of_rows, of_weights, _, _ = ctx.needs_input_grad
-        offsets, row, *saved = _kept(ctx, dy.device)
+        offsets, row, *saved = _kept(ctx, "offsets", "row_of_route", "weights", "rows")
         if not saved:
             return _sort_rows(dy, offsets, row, *ctx.dims), None, None, None
         weights, rows = saved if of_weights else (saved[0], None)
@@ -718,14 +720,14 @@ class _SwigluFunction(torch.autograd.Function):
     def forward(ctx, h, M, I, el, turn, clamp):
         a, q, s = _swiglu(h, M, I, el, turn, clamp, True)
         ctx.how = turn, clamp
-        _keep(ctx, codes=q, scales=s)
+        _keep(ctx, q, s)
         return a
 
     @staticmethod
     @_once
     def backward(ctx, da):
         _not_captured()
-        return _swiglu_backward(_dense(da), *_kept(ctx, da.device), *ctx.how), None, None, None, None, None
+        return _swiglu_backward(_dense(da), *_kept(ctx, "codes", "scales"), *ctx.how), None, None, None, None, None
 
 
 def swiglu(h, *, activation_clamp=None, gate_up_group=0, stream=None):
