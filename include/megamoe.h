@@ -654,7 +654,8 @@ mm_status mm_combine_backward(const mm_sort_plan* plan, const void* dy, const vo
  * ------------------------------------------- activation, kept in 8 bits
  * mm_swiglu -- a = SiLU(h[:, :I]) * h[:, I:], both halves clamped to
  * [-activation_clamp, activation_clamp] first if clamp_activation is 1 (as in
- * mm_problem); computed in float32, rounded once.  With codes, also the copy
+ * mm_problem); computed in float32, rounded once (a sigmoid below 2^-126, that
+ * of a gate below -87.3, may count as 0).  With codes, also the copy
  * of h that the gradient takes: each half of a row in groups of 128 values
  * from its start (the last one may be shorter), scale = max(max|group| / 127,
  * 1e-8), code = h / scale rounded half to even, both decided in IEEE float32;

@@ -28,9 +28,11 @@ constexpr int kGroup = 128, kLanes = 16, kPer = kGroup / kLanes;   // a group's 
 // NaN stays, as it does in the formula
 __device__ __forceinline__ float clamped(float v, float c) { return v > c ? c : v < -c ? -c : v; }
 
-// 1 / (1 + e^-z).  The 16-bit types take the fast exponential and reciprocal
-// (relative error below 2^-16 up to |z| = 88, against a rounding of 2^-8 or
-// 2^-11); float32 the accurate ones.
+// 1 / (1 + e^-z).  The 16-bit types take the fast exponential and reciprocal:
+// relative error below 2^-16 from z = -87.3 on, against a rounding of 2^-8 or 2^-11;
+// below, where the value is under 2^-126, the reciprocal gives 0 (off by at most
+// 2^-126, before the factors of gate and up).  float32 takes the accurate ones: 0
+// only where e^-z is beyond float32, below z = -88.7.
 template <typename E>
 __device__ __forceinline__ float sigmoid(float z) {
   if constexpr (sizeof(E) == 4) return 1.0f / (1.0f + expf(-z));
