@@ -24,8 +24,11 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 constexpr int kStep = 128;           // K-values (bytes) of a row that a part of a stage holds
 constexpr int kFewRows = 16;         // most rows that are streamed together
 constexpr int kFewCols = 16;
-// Most rows of a product that are streamed; us, streamed / tiles of 32 x 32: 1 row x 4096 x 7168 8.4 / 10.1, 7168 x 2048
-// 6.9 / 6.0, 16384 x 4096 17.5 / 18.7; 8 rows x 4096 x 7168 9.7 / 10.3; 16 rows 11.2 / 10.3, 7168 x 2048 9.1 / 6.2
+// Most rows of a product that are streamed; us one behind the other, weights from HBM, streamed / tiles of 32 x 32:
+// 4096 x 7168: 1 row 10.3 / 11.5, 4 rows 10.6 / 11.6, 8 rows 11.0 / 11.6 (another run: 16 rows 11.2 / 10.3, where 1 row
+// took 8.4 / 10.1).  The rule goes by the rows alone, which suits that shape: the tiles are faster from one row on where
+// K is short (7168 x 2048: 7.1 / 6.3, 8 rows 8.2 / 6.4), and from four on at 16384 x 4096 (18.6 / 19.2, 4 rows 19.6 / 19.2,
+// 8 rows 21.1 / 19.2).
 constexpr int kStreamRows = 8;
 constexpr int kQuantThreads = 512;
 constexpr uint32_t kOutside = 0x7fffff00u;   // an offset beyond every descriptor: arrives as zeros
@@ -516,6 +519,10 @@ hipError_t gemm(const Int8Args& args, int num_cus, hipStream_t s) {
   // 128 x 128) 79 / 93, 2048 rows (512) 94 / 96, 2560 rows (640) 117 / 97; 2048 to 7168: 64
   // rows 10 / 7.7 / 9.9 / 11 / 13 / 20, 256 rows 29 / 23 / 18 / 12 / 15 / 31, 512 rows - / - / 32 /
   // 21 / 16 / 32, 1024 rows (448) 29 / 33, 1536 rows (672) 43 / 34.
+  // Groups count as evenly filled, the empty ones too (which have rows is known on the
+  // device alone): right for a prefill; a decoded batch over few of many groups gets
+  // larger tiles than its rows fill (8 rows to 8 of 32 groups, 4096 x 7168, 83 us; to 8
+  // of 8 55; 48 for the weights at a copy's rate).
   const int64_t even = a.M / a.G > 0 ? a.M / a.G : 1;
   const unsigned cus = (unsigned)((num_cus + 7) / 8 * 8);
   auto count = [&](int c) { return (even + most_rows(c) - 1) / most_rows(c) * a.G * ((a.N + cols_of(c) - 1) / cols_of(c)); };
@@ -536,7 +543,7 @@ hipError_t gemm(const Int8Args& args, int num_cus, hipStream_t s) {
   } else {
     // one matrix: up to 16 rows beyond the blocks of 256 are streamed, in place of a
     // round more (16388 x 4096 x 2048: 2.6 us for the last four rows; 4097 x 4096 x 7168,
-    // whose tiles all end together: 8.5).  9 to 16 rows of more columns than 128 x 128
+    // whose tiles all end together: 4.6).  9 to 16 rows of more columns than 128 x 128
     // tiles take in two rounds (65536 on 256 CUs) come here too: all of them are such
     // rows, and there is no tile
     const int64_t rest = a.offsets == nullptr ? a.M % kBM : 0;

@@ -10,8 +10,8 @@
 // Bound: HBM for the rows (a token's row is read once and written K times, or
 // the other way round); launches for a few tokens.  At 16384 tokens of 7168 bf16
 // with 8 of 256 experts each: the order 15 us, rows written 431 us (4.9 TB/s, as a
-// copy), read and summed 360 (5.8), read and written with both gradients 809
-// (5.0); one token 4.4.
+// copy), read and summed 362 (5.8), read and written with both gradients 804
+// (4.9 to 5.0 for 3.99 GB); one token 4.2.
 #include <type_traits>
 
 #include "mm_device.hpp"
@@ -31,6 +31,10 @@ constexpr int kMost = 8;             // slots of a token that are in flight toge
 // for each eight slots of its token.  us, one launch / three, rows of 7168 bf16,
 // top-8: 1 token 4.0 / 10, 64 tokens 5.4 / 12, 256 tokens 11 / 16, 512 tokens 20 / 22,
 // 1024 tokens 36 / 34; top-4 of 4096: 2048 tokens 28 / 23; top-64 of 1024: 128 tokens 85 / 21.
+// The bound leaves the number of workgroups out; within it that cost 1 us at
+// most where measured (one behind the other, rows of 7168 bf16): top-1 1024 tokens 8.3 / 14, 2048 tokens 15 / 20,
+// 4096 tokens 31 / 30; top-2 1024 tokens 11 / 17, 2048 tokens 21 / 25; top-4 1024 tokens 19 / 23;
+// top-8 512 tokens 20 / 23.
 constexpr int64_t kFewRoutes = 4096;
 
 __device__ __forceinline__ int key_of(const SortArgs& a, int64_t r) {

@@ -10,8 +10,10 @@
 // h's columns are [g | u], or gate and up columns in turns of `turn` (as the rows
 // of a prepared W1 lie); the groups are of neighbouring gates, or ups, either way.
 //
-// Bound: HBM; every value is read and written once.  65536 rows of 2 x 2048 bf16,
-// forward with the copy and backward: 408 us for 2.15 GB (5.3 TB/s; a copy 4.9).
+// Bound: HBM; every value is read and written once.  65536 rows of 2 x 2048 bf16, one
+// launch behind the other on the same buffers: forward with the copy 231 us (1.08
+// GB, 4.7 TB/s), backward 191 (5.7; a copy 4.9); with other inputs in turn, traced one
+// by one, 235 to 289 and 180 to 204.
 #include <type_traits>
 
 #include "mm_device.hpp"
@@ -46,7 +48,10 @@ __device__ __forceinline__ int place(int lane, int i) { return WIDE ? lane * kPe
 
 // Where a group's gates lie in h; its up values are ups_from behind them.  For a
 // lane of the TURN form (always WIDE): its place less what load8 and the like add.
-// A form of its own: the branch costs the other 1 % (65536 rows: 439 against 436 us).
+// A form of its own: with halves as one turn of I, the same code for both, halves
+// take longer on the same buffers (forward with the copy and backward, us, this /
+// that: 65536 rows of 2048 231 + 191 / 243 + 193, 8192 rows 32.3 + 25.0 / 33.1 + 25.2,
+// 1333 rows of 1408 float16 6.5 + 4.8 / 6.7 + 4.9; in two turns each, 1 % apart).
 template <bool TURN>
 __device__ __forceinline__ int64_t gate_at(const SwigluArgs& a, uint32_t row, uint32_t grp, int lane) {
   const int64_t base = (int64_t)row * 2 * a.I;
