@@ -9,9 +9,10 @@
 //
 // Bound: HBM for the rows (a token's row is read once and written K times, or
 // the other way round); launches for a few tokens.  At 16384 tokens of 7168 bf16
-// with 8 of 256 experts each: the order 15 us, rows written 431 us (4.9 TB/s, as a
-// copy), read and summed 362 (5.8), read and written with both gradients 804
-// (4.9 to 5.0 for 3.99 GB); one token 4.2.
+// with 8 of 256 experts each: the order 15 us, rows written 427 to 431 us (4.9 TB/s,
+// as a copy), read and summed 344 to 362 (5.8 to 6.1), read and written with both
+// gradients 775 to 809 (4.9 to 5.1 for 3.99 GB): medians of several runs, which differ
+// by where the buffers lie (single launches from 372, 334 and 662); one token 4.3.
 #include <type_traits>
 
 #include "mm_device.hpp"
